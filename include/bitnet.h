@@ -35,7 +35,8 @@
  *     128 (one i2_s block) wherever packed weights are involved.
  *   - Each call runs on the device that is current on the calling thread; that device must
  *     be an sm_103 GPU (GB300), else BITNET_EUNSUPPORTED.
- *   - Inputs must be finite; NaN/Inf activations are outside the contract.
+ *   - Inputs must be finite; NaN/Inf activations are outside the contract (the bitnet_kv4 calls
+ *     say what they make of them).
  */
 #ifndef BITNET_GB300_H
 #define BITNET_GB300_H
@@ -372,10 +373,113 @@ BITNET_API int bitnet_sweep_plan_run(bitnet_sweep_plan plan, void *stream);
 BITNET_API int bitnet_sweep_plan_destroy(bitnet_sweep_plan plan);
 
 /*
+ * The 4-bit key/value cache -- what stands between the q/k/v projections of a decoder layer and
+ * its output projection ("bitnet.rs" "Forward Pass", causal attention with shared key/value
+ * heads): keys and values are quantised to 4 bits as they are written, and attention reads the
+ * codes. The format and the rounding are this library's own; the pages have none.
+ *
+ * A vector (the key or the value of one token and one key/value head, D = head_dim numbers) is
+ * held as D codes, a step and a base, and stands for step * code + base:
+ *   lo, hi = min and max of the x, each clamped to [-61440, 61440]
+ *   base = fp16(lo), step = fp16((hi - lo) / 15)   (fp32 subtract and divide, one rounding each)
+ *   code = clamp(rne((x - base) / step), 0, 15)    (the exact quotient rounded once, ties to even)
+ * with code 0 where step is 0. A vector with a NaN is held as NaN (it reads back as NaN, and
+ * attention is NaN for the queries that see the token, for no other).
+ *
+ * Pages of BITNET_KV4_PAGE = 64 tokens. A page holds, for each key/value head in turn, one block
+ * of 64 * D + 512 bytes; W = D / 8 is the number of 32-bit words of a vector:
+ *   64 key rows of W words    token t of the page in row rho(t) = (t & ~7) | (t & 3) << 1 | (t >> 2) & 1;
+ *                             nibble n of word w (bits 4n+3:4n) is the code of dimension w + W * n
+ *   64 value rows of W words  token t in row t, the same nibbles; with D = 128 the two halves of
+ *                             the row are exchanged where t & 2
+ *   64 x 4 fp16               row rho(t): key step, key base, value step, value base
+ * Pages need no initialisation: only the places of cached tokens are used.
+ */
+#define BITNET_KV4_PAGE 64
+
+typedef struct bitnet_kv4_cache {
+  void *pages;         /* n_pages * kv_heads * (64 * head_dim + 512) bytes (device), 16-byte aligned */
+  int64_t n_pages;     /* 1 .. 2^31 - 1                                                              */
+  int32_t kv_heads;    /* 1 .. 1024                                                                  */
+  int32_t head_dim;    /* 64 or 128                                                                  */
+} bitnet_kv4_cache;
+
+/*
+ * A batch of sequences. Its tokens are the last tokens of their sequences: token i of the n new
+ * ones of a sequence with kv_len cached tokens (the new ones among them) has position
+ * kv_len - n + i. Position j of sequence b lies in page page_table[b][j / 64], place j % 64. The
+ * arrays are read on the device; the sizes below bound them. A sequence whose entries break a
+ * bound (cu_q outside 0..total_q or falling, more than max_q tokens, kv_len outside 0..max_kv, a
+ * page id outside 0..n_pages - 1) makes the call record BITNET_ERANGE in the device error word;
+ * nothing outside the arrays is read or written, and that sequence's results are not valid.
+ */
+typedef struct bitnet_kv4_batch {
+  const int32_t *cu_q;       /* batch + 1: where each sequence's tokens begin in the packed rows   */
+  const int32_t *kv_len;     /* batch: cached tokens of each sequence                              */
+  const int32_t *page_table; /* batch x max_pages: page ids                                        */
+  int64_t batch;             /* 1 .. 65535                                                         */
+  int64_t max_pages;         /* 1 .. 2^24: entries of a page_table row                             */
+  int64_t total_q;           /* 0 .. 2^31 - 1: packed rows (0: the call does nothing)              */
+  int64_t max_q;             /* 1 .. 2^31 - 1: no sequence has more tokens in the batch            */
+  int64_t max_kv;            /* 0 .. 64 * max_pages: no sequence has more cached tokens            */
+} bitnet_kv4_batch;
+
+/* Bytes of the pages of a cache; BITNET_EINVAL for sizes outside the ranges above. */
+BITNET_API int64_t bitnet_kv4_cache_bytes(int64_t n_pages, int64_t kv_heads, int64_t head_dim);
+
+/*
+ * bitnet_kv4_append -- quantise the batch's keys and values and write them to their places.
+ *   k, v : total_q rows of kv_heads x head_dim, fp32 or bf16 (dtype) (device, read); row r begins
+ *          at k + r * k_stride (elements), its heads lie one after another
+ *   Tokens with a negative position (more new tokens than kv_len) have no place: they are not
+ *   written, and BITNET_ERANGE is recorded.
+ *   k and v 16-byte aligned, strides >= kv_heads * head_dim and multiples of 16 bytes. Sequences
+ *   of one call must not share the places that they write.
+ */
+BITNET_API int bitnet_kv4_append(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch, const void *k,
+                                 const void *v, int dtype, int64_t k_stride, int64_t v_stride, void *stream);
+
+/*
+ * bitnet_kv4_read -- read the batch's tokens back: out = step * code + base, one rounding to fp32,
+ * then one to bf16 where dtype asks for it. A batch whose cu_q are the running sums of kv_len reads
+ * whole sequences. Layout and alignment of k and v (device, written) as in bitnet_kv4_append; rows
+ * with a negative position are not written, and BITNET_ERANGE is recorded.
+ */
+BITNET_API int bitnet_kv4_read(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch, void *k, void *v,
+                               int dtype, int64_t k_stride, int64_t v_stride, void *stream);
+
+/*
+ * bitnet_kv4_attention -- causal attention of the batch's queries over the cache.
+ *   A query at position p sees position j where j <= p and (window == 0 or j > p - window or
+ *   j < sinks):  out = sum_j softmax_j(scale * q . k_j) v_j, zeros where it sees nothing. Query
+ *   head h reads key/value head h / (q_heads / kv_heads).
+ *   q      : total_q rows of q_heads x head_dim, fp32 or bf16 (dtype) (device, read); row r begins
+ *            at q + r * q_stride (elements). A query is used as fp16 at a power-of-two scale of its
+ *            own: bf16 values keep their bits (those below 2^-28 of the row's largest may not),
+ *            fp32 values round to 11 bits.
+ *   out    : total_q rows of q_heads x head_dim, bf16 (device, written), row stride out_stride. The
+ *            sums are held in fp32; softmax weights enter the product with the values as fp16.
+ *   q_heads: a multiple of kv_heads, at most 128 * kv_heads
+ *   window : 0 for all positions, else 1 .. 2^31 - 1; sinks: 0 .. 2^31 - 1 (unused with window 0)
+ *   workspace : device, 256-byte aligned, at least bitnet_kv4_attention_workspace_size bytes (for
+ *            the same cache, batch sizes and q_heads; it may be NULL where that is 0). Needs no
+ *            initialisation; calls that may run at the same time need one each.
+ *   q and out 16-byte aligned, strides >= q_heads * head_dim and multiples of 16 bytes; scale finite.
+ * The results of a call are the same bits each time it is made with the same arguments.
+ */
+BITNET_API int64_t bitnet_kv4_attention_workspace_size(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch,
+                                                       int64_t q_heads);
+BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch, const void *q,
+                                    int dtype, int64_t q_heads, int64_t q_stride, float scale, int64_t window,
+                                    int64_t sinks, void *out, int64_t out_stride, void *workspace,
+                                    int64_t workspace_bytes, void *stream);
+
+/*
  * bitnet_last_device_error -- read and clear the device-side error word of the current
  * device. Kernels that wait on an mbarrier give up after a bounded number of polls and
  * record BITNET_ETIMEOUT there instead of hanging; bitnet_quant_weight records BITNET_ERANGE
- * for weights outside its range. Synchronises the device.
+ * for weights outside its range, the bitnet_kv4 calls for batches that break their bounds.
+ * Synchronises the device.
  * Returns BITNET_OK, BITNET_ETIMEOUT, BITNET_ERANGE or BITNET_ECUDA.
  */
 BITNET_API int bitnet_last_device_error(void);

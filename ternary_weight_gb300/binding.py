@@ -56,6 +56,12 @@ SIGNATURES = {
     "bitnet_sweep_plan_create": ([_P, ctypes.c_int, ctypes.c_int, _P], ctypes.c_int),
     "bitnet_sweep_plan_run": ([_P, _P], ctypes.c_int),
     "bitnet_sweep_plan_destroy": ([_P], ctypes.c_int),
+    "bitnet_kv4_cache_bytes": ([_I64, _I64, _I64], _I64),
+    "bitnet_kv4_append": ([_P, _P, _P, _P, ctypes.c_int, _I64, _I64, _P], ctypes.c_int),
+    "bitnet_kv4_read": ([_P, _P, _P, _P, ctypes.c_int, _I64, _I64, _P], ctypes.c_int),
+    "bitnet_kv4_attention_workspace_size": ([_P, _P, _I64], _I64),
+    "bitnet_kv4_attention": (
+        [_P, _P, _P, ctypes.c_int, _I64, _I64, ctypes.c_float, _I64, _I64, _P, _I64, _P, _I64, _P], ctypes.c_int),
     "bitnet_w2a8_ffn": (
         [_P, ctypes.c_int, _I64, _I64, _I64, _P, ctypes.c_float, _P, ctypes.c_float, _P, ctypes.c_float, _P,
          ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _I64, _P], ctypes.c_int),
@@ -421,3 +427,169 @@ class SweepPlan:
             self.close()
         except Exception:
             pass
+
+
+KV4_PAGE = 64
+
+
+class _KV4CacheDesc(ctypes.Structure):
+    """ctypes mirror of bitnet_kv4_cache (include/bitnet.h)."""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class _KV4BatchDesc(ctypes.Structure):
+    """ctypes mirror of bitnet_kv4_batch (include/bitnet.h)."""
+    _fields_ = [("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("total_q", ctypes.c_int64),
+                ("max_q", ctypes.c_int64), ("max_kv", ctypes.c_int64)]
+
+
+def kv4_cache_bytes(n_pages, kv_heads, head_dim) -> int:
+    n = lib().bitnet_kv4_cache_bytes(n_pages, kv_heads, head_dim)
+    if n < 0:
+        raise BitnetError(int(n), "bitnet_kv4_cache_bytes")
+    return int(n)
+
+
+class KV4Cache:
+    """A pool of pages of the 4-bit key/value cache: n_pages pages of 64 tokens for kv_heads heads
+    of head_dim (64 or 128) numbers. ``pages``, a flat uint8 CUDA tensor of kv4_cache_bytes bytes,
+    is allocated here (uninitialised; no page needs to be cleared) if not given."""
+
+    def __init__(self, n_pages, kv_heads, head_dim, pages=None, device="cuda"):
+        import torch
+
+        need = kv4_cache_bytes(n_pages, kv_heads, head_dim)
+        if pages is None:
+            pages = torch.empty(need, dtype=torch.uint8, device=device)
+        if pages.dtype != torch.uint8 or pages.numel() != need:
+            raise ValueError("pages must be %d bytes of uint8" % need)
+        _require_cuda(pages)
+        self.pages, self.n_pages, self.kv_heads, self.head_dim = pages, n_pages, kv_heads, head_dim
+        self._desc = _KV4CacheDesc(pages.data_ptr(), n_pages, kv_heads, head_dim)
+        self._ref = ctypes.c_void_p(ctypes.addressof(self._desc))
+
+
+class KV4Batch:
+    """The sequences of a call: ``cu_q`` (batch + 1), ``kv_len`` (batch) and ``page_table`` (batch x
+    max_pages), int32 CUDA tensors that are read when the call runs (so a program may update them
+    in place between calls, also between replays of a captured graph), and the sizes that bound
+    them: total_q packed rows, at most max_q new and max_kv cached tokens a sequence."""
+
+    def __init__(self, cu_q, kv_len, page_table, total_q, max_q, max_kv=None):
+        import torch
+
+        n = kv_len.numel()
+        if any(t.dtype != torch.int32 for t in (cu_q, kv_len, page_table)):
+            raise ValueError("cu_q, kv_len and page_table must be int32")
+        if cu_q.shape != (n + 1,) or kv_len.shape != (n,) or page_table.dim() != 2 or page_table.shape[0] != n:
+            raise ValueError("cu_q must have batch + 1 entries, kv_len batch, and page_table batch rows")
+        _require_cuda(cu_q, kv_len, page_table)
+        if max_kv is None:
+            max_kv = page_table.shape[1] * KV4_PAGE
+        self.cu_q, self.kv_len, self.page_table = cu_q, kv_len, page_table
+        self.total_q, self.max_q, self.max_kv = int(total_q), int(max_q), int(max_kv)
+        self._desc = _KV4BatchDesc(cu_q.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), n, page_table.shape[1],
+                                   self.total_q, self.max_q, self.max_kv)
+        self._ref = ctypes.c_void_p(ctypes.addressof(self._desc))
+        self._ws = {}  # attention workspace bytes by cache and query heads
+
+
+def _kv4_rows(t, rows, heads, dim):
+    """Checks a rows x heads x dim tensor whose heads lie one after another; its row stride."""
+    if t.shape != (rows, heads, dim):
+        raise ValueError("expected a %d x %d x %d tensor" % (rows, heads, dim))
+    s = t.stride()
+    if not t.is_cuda or (rows and (s[2] != 1 or (heads > 1 and s[1] != dim))):
+        raise ValueError("rows must be CUDA tensors whose heads lie one after another")
+    return s[0] if rows > 1 else heads * dim
+
+
+def _on_stream(stream):
+    """Allocations made for a call on a given stream belong to that stream."""
+    import contextlib
+
+    import torch
+
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def kv4_append(cache, batch, k, v, stream=None):
+    """Quantise the batch's keys and values (total_q x kv_heads x head_dim, fp32 or bf16 CUDA; rows may
+    be strided, e.g. slices of a fused q/k/v row) to 4 bits and write them to their places."""
+    dt = _act_dtype(k)
+    if v.dtype != k.dtype:
+        raise ValueError("k and v must have the same dtype")
+    ks = _kv4_rows(k, batch.total_q, cache.kv_heads, cache.head_dim)
+    vs = _kv4_rows(v, batch.total_q, cache.kv_heads, cache.head_dim)
+    if not batch.total_q:
+        return
+    _check(lib().bitnet_kv4_append(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs, _stream(stream)),
+           "bitnet_kv4_append")
+
+
+def kv4_read(cache, batch, dtype=None, k=None, v=None, stream=None):
+    """Read the batch's tokens back from the cache as (k, v), each total_q x kv_heads x head_dim of
+    ``dtype`` (fp32 or bf16, default bf16; or that of the given k and v, which are written)."""
+    import torch
+
+    shape = (batch.total_q, cache.kv_heads, cache.head_dim)
+    if k is None or v is None:
+        with _on_stream(stream):
+            like = k if k is not None else v
+            dtype = like.dtype if like is not None else dtype if dtype is not None else torch.bfloat16
+            k = torch.empty(shape, dtype=dtype, device=cache.pages.device) if k is None else k
+            v = torch.empty(shape, dtype=dtype, device=cache.pages.device) if v is None else v
+    dt = _act_dtype(k)
+    if v.dtype != k.dtype or (dtype is not None and dtype != k.dtype):
+        raise ValueError("k and v must have the same dtype, the one asked for")
+    ks, vs = _kv4_rows(k, *shape), _kv4_rows(v, *shape)
+    if batch.total_q:
+        _check(lib().bitnet_kv4_read(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs, _stream(stream)),
+               "bitnet_kv4_read")
+    return k, v
+
+
+def kv4_attention_workspace_size(cache, batch, q_heads) -> int:
+    n = lib().bitnet_kv4_attention_workspace_size(cache._ref, batch._ref, q_heads)
+    if n < 0:
+        raise BitnetError(int(n), "bitnet_kv4_attention_workspace_size")
+    return int(n)
+
+
+def kv4_attention(cache, batch, q, scale, window=0, sinks=0, out=None, workspace=None, stream=None):
+    """Causal attention of the batch's queries (total_q x q_heads x head_dim, fp32 or bf16 CUDA, rows may
+    be strided) over the cache: a query at position p sees position j where j <= p and (window == 0
+    or j > p - window or j < sinks). Returns total_q x q_heads x head_dim bf16 (``out`` if given).
+    ``workspace``: a uint8 CUDA tensor of at least kv4_attention_workspace_size bytes, allocated
+    here if not given."""
+    import torch
+
+    dt = _act_dtype(q)
+    if q.dim() != 3:
+        raise ValueError("q must be total_q x q_heads x head_dim")
+    heads = q.shape[1]
+    qs = _kv4_rows(q, batch.total_q, heads, cache.head_dim)
+    key = (heads, cache.kv_heads, cache.head_dim)
+    need = batch._ws.get(key)
+    if need is None:
+        need = batch._ws[key] = kv4_attention_workspace_size(cache, batch, heads)
+    if out is None or (workspace is None and need):
+        with _on_stream(stream):
+            if out is None:
+                out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            if workspace is None and need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if out.dtype != torch.bfloat16:
+        raise ValueError("out must be bfloat16")
+    os_ = _kv4_rows(out, batch.total_q, heads, cache.head_dim)
+    _require_cuda(workspace)
+    if batch.total_q:
+        ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None \
+            else (None, 0)
+        _check(lib().bitnet_kv4_attention(cache._ref, batch._ref, q.data_ptr(), dt, heads, qs, float(scale),
+                                          int(window), int(sinks), out.data_ptr(), os_, ws_ptr, ws_bytes,
+                                          _stream(stream)),
+               "bitnet_kv4_attention")
+    return out

@@ -9,6 +9,7 @@
 #include "bitnet.h"
 #include "bitnet_dev.cuh"
 #include "gemm_pair.h"
+#include "kv4.cuh"
 
 #include <cmath>
 #include <new>
@@ -451,6 +452,108 @@ BITNET_API int bitnet_sweep_plan_destroy(bitnet_sweep_plan plan) {
   return e1 == cudaSuccess && e2 == cudaSuccess ? BITNET_OK : BITNET_ECUDA;
 }
 
+// ---- the 4-bit key/value cache ----
+namespace {
+constexpr int64_t kKvMaxHeads = 1024, kKvMaxBatch = 65535, kKvMaxPages = 1 << 24, kKvMaxShare = 128;
+
+bool valid_kv4_sizes(int64_t n_pages, int64_t kv_heads, int64_t head_dim) {
+  return n_pages >= 1 && n_pages <= INT32_MAX && kv_heads >= 1 && kv_heads <= kKvMaxHeads &&
+         (head_dim == 64 || head_dim == 128);
+}
+// the checks that every call makes of its cache and batch; fills *out
+int check_kv4(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* b, Kv4* out) {
+  if (!cache || !b || !cache->pages || !b->cu_q || !b->kv_len || !b->page_table) return BITNET_EINVAL;
+  if (!valid_kv4_sizes(cache->n_pages, cache->kv_heads, cache->head_dim)) return BITNET_EINVAL;
+  if (b->batch < 1 || b->batch > kKvMaxBatch || b->max_pages < 1 || b->max_pages > kKvMaxPages || b->total_q < 0 ||
+      b->total_q > INT32_MAX || b->max_q < 1 || b->max_q > INT32_MAX || b->max_kv < 0 ||
+      b->max_kv > b->max_pages * kKvPage)
+    return BITNET_EINVAL;
+  // rows x heads of a call fit the grids (2^31 blocks of at least 16 vectors)
+  if (b->total_q > (int64_t(1) << 33) / cache->kv_heads) return BITNET_EINVAL;
+  if (!aligned(cache->pages, 16) || !aligned(b->cu_q, 4) || !aligned(b->kv_len, 4) || !aligned(b->page_table, 4))
+    return BITNET_EALIGN;
+  *out = Kv4{static_cast<uint8_t*>(cache->pages), (int)cache->n_pages, cache->kv_heads, b->cu_q, b->kv_len,
+             b->page_table, b->max_pages, (int)b->batch, (int)b->total_q, (int)b->max_q, (int)b->max_kv};
+  return BITNET_OK;
+}
+// a row stride in elements: at least `least`, and a multiple of 16 bytes
+int check_stride(int64_t stride, int64_t least, int64_t elem_bytes) {
+  if (stride < least || stride > (int64_t(1) << 40)) return BITNET_EINVAL;
+  return stride * elem_bytes % 16 == 0 ? BITNET_OK : BITNET_EALIGN;
+}
+int check_kv4_rows(const Kv4& c, int dim, const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride) {
+  if (!k || !v || (dtype != BITNET_F32 && dtype != BITNET_BF16)) return BITNET_EINVAL;
+  const int64_t eb = dtype == BITNET_BF16 ? 2 : 4;
+  if (int st = check_stride(k_stride, (int64_t)c.kv_heads * dim, eb)) return st;
+  if (int st = check_stride(v_stride, (int64_t)c.kv_heads * dim, eb)) return st;
+  return aligned(k, 16) && aligned(v, 16) ? BITNET_OK : BITNET_EALIGN;
+}
+bool valid_q_heads(int64_t q_heads, int64_t kv_heads) {
+  return q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads / kv_heads <= kKvMaxShare;
+}
+}  // namespace
+
+BITNET_API int64_t bitnet_kv4_cache_bytes(int64_t n_pages, int64_t kv_heads, int64_t head_dim) {
+  if (!valid_kv4_sizes(n_pages, kv_heads, head_dim)) return BITNET_EINVAL;
+  return n_pages * kv_heads * kv4_block_bytes((int)head_dim);
+}
+
+BITNET_API int bitnet_kv4_append(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* batch, const void* k,
+                                 const void* v, int dtype, int64_t k_stride, int64_t v_stride, void* stream) {
+  Kv4 c{};
+  if (int st = check_kv4(cache, batch, &c)) return st;
+  if (int st = check_kv4_rows(c, cache->head_dim, k, v, dtype, k_stride, v_stride)) return st;
+  if (c.total_q == 0) return BITNET_OK;
+  int sms = 0;
+  if (int st = check_device(&sms)) return st;
+  return status_of(launch_kv4_append(c, cache->head_dim, k, v, dtype == BITNET_BF16, k_stride, v_stride,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+BITNET_API int bitnet_kv4_read(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* batch, void* k, void* v,
+                               int dtype, int64_t k_stride, int64_t v_stride, void* stream) {
+  Kv4 c{};
+  if (int st = check_kv4(cache, batch, &c)) return st;
+  if (int st = check_kv4_rows(c, cache->head_dim, k, v, dtype, k_stride, v_stride)) return st;
+  if (c.total_q == 0) return BITNET_OK;
+  int sms = 0;
+  if (int st = check_device(&sms)) return st;
+  return status_of(launch_kv4_read(c, cache->head_dim, k, v, dtype == BITNET_BF16, k_stride, v_stride,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+BITNET_API int64_t bitnet_kv4_attention_workspace_size(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* batch,
+                                                       int64_t q_heads) {
+  Kv4 c{};
+  if (int st = check_kv4(cache, batch, &c)) return st;
+  if (!valid_q_heads(q_heads, c.kv_heads)) return BITNET_EINVAL;
+  return kv4_attention_ws_bytes(c, cache->head_dim, (int)q_heads);
+}
+
+BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* batch, const void* q,
+                                    int dtype, int64_t q_heads, int64_t q_stride, float scale, int64_t window,
+                                    int64_t sinks, void* out, int64_t out_stride, void* workspace,
+                                    int64_t workspace_bytes, void* stream) {
+  Kv4 c{};
+  if (int st = check_kv4(cache, batch, &c)) return st;
+  if (!q || !out || (dtype != BITNET_F32 && dtype != BITNET_BF16)) return BITNET_EINVAL;
+  if (!valid_q_heads(q_heads, c.kv_heads) || !std::isfinite(scale)) return BITNET_EINVAL;
+  if (window < 0 || window > INT32_MAX || sinks < 0 || sinks > INT32_MAX) return BITNET_EINVAL;
+  const int64_t row = q_heads * cache->head_dim;
+  if (int st = check_stride(q_stride, row, dtype == BITNET_BF16 ? 2 : 4)) return st;
+  if (int st = check_stride(out_stride, row, 2)) return st;
+  const int64_t need = kv4_attention_ws_bytes(c, cache->head_dim, (int)q_heads);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return BITNET_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || (workspace && !aligned(workspace, 256))) return BITNET_EALIGN;
+  if (c.total_q == 0) return BITNET_OK;
+  int sms = 0;
+  if (int st = check_device(&sms)) return st;
+  const Kv4Attn a{q, static_cast<uint16_t*>(out), q_stride, out_stride, (int)q_heads, (int)(q_heads / c.kv_heads),
+                  scale, window ? (int)window : INT32_MAX, window ? (int)sinks : 0};
+  return status_of(launch_kv4_attention(c, cache->head_dim, a, dtype == BITNET_BF16, workspace, sms,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
 BITNET_API int bitnet_selftest_wait_timeout(const void* src, int64_t bytes, int32_t max_polls, uint32_t* report,
                                             void* stream) {
   if (!src || !report || !selftest_bytes_ok(bytes) || max_polls < 1 || max_polls > (1 << 20)) return BITNET_EINVAL;
@@ -470,7 +573,8 @@ BITNET_API int bitnet_last_device_error(void) {
                                     read_clear_device_error_gemv_group, read_clear_device_error_smallm,
                                     read_clear_device_error_quant_weight, read_clear_device_error_sweep,
                                     read_clear_device_error_gemv_ring, read_clear_device_error_selftest,
-                                    read_clear_device_error_prefill, read_clear_device_error_pair};
+                                    read_clear_device_error_prefill, read_clear_device_error_pair,
+                                    read_clear_device_error_kv4_cache, read_clear_device_error_kv4_attn};
   for (auto rd : readers) {
     int v = 0;
     if (rd(&v) != cudaSuccess) return BITNET_ECUDA;
