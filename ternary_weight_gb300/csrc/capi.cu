@@ -574,7 +574,8 @@ BITNET_API int bitnet_last_device_error(void) {
                                     read_clear_device_error_quant_weight, read_clear_device_error_sweep,
                                     read_clear_device_error_gemv_ring, read_clear_device_error_selftest,
                                     read_clear_device_error_prefill, read_clear_device_error_pair,
-                                    read_clear_device_error_kv4_cache, read_clear_device_error_kv4_attn};
+                                    read_clear_device_error_kv4_cache, read_clear_device_error_kv4_attn,
+                                    read_clear_device_error_kv4_decode};
   for (auto rd : readers) {
     int v = 0;
     if (rd(&v) != cudaSuccess) return BITNET_ECUDA;

@@ -10,7 +10,7 @@ namespace {
 constexpr int WARPS = 4;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * WARPS) kv4_attn_simple_kernel(Kv4 c, Kv4Attn a) {
+__global__ void __launch_bounds__(32 * WARPS) kv4_attn_simple_kernel(Kv4 c, Kv4Attn a, int done_rows) {
   constexpr int W = D / 8;
   __shared__ float qs[WARPS][D];
   __shared__ float ps[WARPS][32];
@@ -23,6 +23,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv4_attn_simple_kernel(Kv4 c, Kv4A
   const int b = kv4_find(c, (int)row);
   if (b < 0) return;
   const Kv4Seq s = kv4_sequence(c, b, &bad);
+  if ((int64_t)s.n * a.share <= done_rows) return;
   const int i = (int)row - s.q0;
   const int p = i < s.n ? s.len - s.n + i : -1;
   for (int d = lane; d < D; d += 32) {
@@ -86,16 +87,34 @@ __global__ void __launch_bounds__(32 * WARPS) kv4_attn_simple_kernel(Kv4 c, Kv4A
 
 }  // namespace
 
-int64_t kv4_attention_ws_bytes(const Kv4&, int, int) { return 0; }
+// The rows that the few-row kernel takes of a sequence, 0 if it is not needed: it is where a sequence
+// may have so few; a batch of equal, longer sequences has none.
+static int decode_rows(const Kv4& c, int share) {
+  const int64_t all = (int64_t)c.max_q * share;
+  if (all > kKvDecodeRows && (c.batch == 1 || (int64_t)c.batch * c.max_q == c.total_q)) return 0;
+  const int64_t rows = all <= kKvDecodeRows ? all : share;  // with longer sequences beside: single tokens
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kKvDecodeRows ? kKvDecodeRows : 0;
+}
 
-cudaError_t launch_kv4_attention(const Kv4& c, int dim, const Kv4Attn& a, bool bf16, void*, int, cudaStream_t st) {
+int64_t kv4_attention_ws_bytes(const Kv4& c, int dim, int q_heads) {
+  const int rows = decode_rows(c, q_heads / c.kv_heads);
+  return rows ? kv4_decode_ws_bytes(c, dim, rows) : 0;
+}
+
+cudaError_t launch_kv4_attention(const Kv4& c, int dim, const Kv4Attn& a, bool bf16, void* workspace, int num_sms,
+                                 cudaStream_t st) {
+  const int rows = decode_rows(c, a.share);
+  if (rows) {
+    if (cudaError_t e = launch_kv4_decode(c, dim, a, bf16, rows, workspace, num_sms, st)) return e;
+    if ((int64_t)c.max_q * a.share <= rows) return cudaSuccess;
+  }
   const unsigned grid = (unsigned)(((int64_t)c.total_q * a.q_heads + WARPS - 1) / WARPS);
   if (dim == 128)
-    bf16 ? kv4_attn_simple_kernel<128, true><<<grid, 32 * WARPS, 0, st>>>(c, a)
-         : kv4_attn_simple_kernel<128, false><<<grid, 32 * WARPS, 0, st>>>(c, a);
+    bf16 ? kv4_attn_simple_kernel<128, true><<<grid, 32 * WARPS, 0, st>>>(c, a, rows)
+         : kv4_attn_simple_kernel<128, false><<<grid, 32 * WARPS, 0, st>>>(c, a, rows);
   else
-    bf16 ? kv4_attn_simple_kernel<64, true><<<grid, 32 * WARPS, 0, st>>>(c, a)
-         : kv4_attn_simple_kernel<64, false><<<grid, 32 * WARPS, 0, st>>>(c, a);
+    bf16 ? kv4_attn_simple_kernel<64, true><<<grid, 32 * WARPS, 0, st>>>(c, a, rows)
+         : kv4_attn_simple_kernel<64, false><<<grid, 32 * WARPS, 0, st>>>(c, a, rows);
   return cudaGetLastError();
 }
 

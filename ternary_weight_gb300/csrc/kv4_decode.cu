@@ -1,0 +1,694 @@
+// kv4_decode.cu -- attention over the 4-bit key/value cache for a few query rows a sequence: single
+// tokens and drafted ones, n * share <= 8 NT rows (share = query heads of one key/value head).
+//
+// Bound by the bytes of the cache. Every warp is its own pipeline: it fetches whole page blocks (one
+// head's 64 tokens, one bulk copy of 64 D + 512 contiguous bytes) into a ring of its own in shared
+// memory and never waits for another warp.
+//
+// Arithmetic, for one block and the rows r of a sequence:
+//   raw[t][r] = sum_d code_k[t][d] q'[r][d]     tokens x rows, m16n8k16 with the codes as the A operand
+//   s = scale (step_k raw + base_k sum(q))      the raw dot and its correction, fp32
+//   p = 2^(s log2 e - m), l = sum p             running maximum m and sum l, fp32
+//   O[d][r] += sum_t code_v[t][d] w[t][r]       dims x rows, w = p step_v / vref as fp16
+//   bsum[r] += p base_v                         out = (vref O + bsum) / l
+// A code enters as the fp16 subnormal c * 2^-24 (its nibble masked out of the word) or c * 2^-20 (the
+// nibble above, not shifted): products and fp32 sums of subnormals are exact in the matrix unit, and
+// the factors go into q' (whose dims of odd nibbles are scaled by 2^-4) and into the last scaling of
+// O. So a word of 8 codes costs 5 instructions for keys; for values, pairs of tokens are joined byte
+// by byte first (0.75 instructions a code). q' is q at a power-of-two scale of its own row, as fp16.
+// w is fp16: vref, a power of two above every step_v met so far by the warp, keeps it below 1, so
+// the rounding is 2^-11 of a weight and at most 2^-25 of the largest for the small ones.
+// The scores' fragment (tokens x rows) becomes the second product's B fragment by an 8 x 8 transpose
+// in registers.
+//
+// Split: the pages that the batch sees, in the order sequence, head, page, are cut into equal runs,
+// one a warp, whatever the lengths are (a ragged batch keeps every SM busy to the end; 64 sequences
+// of 17 to 8175 tokens). A (sequence, head) unit that lies in one run is finished by its warp; one
+// that is cut leaves a partial (m, l, unscaled sum) for each run, and a second kernel joins them in
+// order, so results do not depend on timing.
+#include "kv4.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace bitnet {
+namespace {
+
+constexpr int WARPS = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int W = D / 8;             // words of a vector
+  static constexpr int KS = D / 16;           // k steps of the scores; m tiles of the values
+  static constexpr int BLK = 64 * D + 512;    // bytes of a block
+  static constexpr int ROWS = 8 * NT;
+  static constexpr bool QS = NT > 2;          // query fragments in shared memory (registers are full)
+  static constexpr int BLOCKS = NT == 1 ? 3 : 2;  // resident blocks of an SM
+  static constexpr int STAGES = BLOCKS == 3 || QS ? 2 : 3;
+  static constexpr int QBYTES = QS ? ROWS * D * 2 : 0;
+  static constexpr int PBYTES = kKvPage * 16;  // the page's parameters as fp32
+  static constexpr int WARP_BYTES = STAGES * BLK + PBYTES + QBYTES;
+  static constexpr int SMEM = WARPS * WARP_BYTES;
+  static constexpr int PART = ROWS * (D + 2);  // floats of a partial: ROWS x D sums, then m, then l
+};
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// plain shared-memory loads: the compiler may move them past one another, not past the barriers
+template <typename T>
+__device__ __forceinline__ T lds(const uint8_t* p) {
+  return *reinterpret_cast<const T*>(p);
+}
+
+// The pages that the rows of a sequence see: page i of np is page i of the sequence, or i + skip from
+// i = ns on (what lies between the sinks and the window of the first row). np = 0: no row of this
+// kernel's, or nothing cached.
+struct Span {
+  int np, ns, skip;
+};
+__device__ __forceinline__ Span span_of(const Kv4& c, const Kv4Attn& a, const Kv4Seq& s, int max_rows) {
+  Span p{0, 0, 0};
+  if (s.n < 1 || (int64_t)s.n * a.share > max_rows || s.len < 1) return p;
+  const int low = (int)max((int64_t)0, (int64_t)s.len - s.n - a.window + 1);
+  const int low_page = low / kKvPage, sink_pages = (min(a.sinks, low) + kKvPage - 1) / kKvPage;
+  p.ns = min(sink_pages, low_page);
+  p.skip = low_page - p.ns;
+  p.np = p.ns + (s.len + kKvPage - 1) / kKvPage - low_page;
+  return p;
+}
+
+// A place in the order sequence, head, page.
+struct Cursor {
+  int b, h, i;
+  Kv4Seq s;
+  Span p;
+};
+__device__ __forceinline__ void next_sequence(Cursor& k, const Kv4& c, const Kv4Attn& a, int max_rows, bool* bad) {
+  do {
+    ++k.b;
+    if (k.b >= c.batch) return;
+    k.s = kv4_sequence(c, k.b, bad);
+    k.p = span_of(c, a, k.s, max_rows);
+  } while (k.p.np == 0);
+}
+
+// where the runs' results go in the workspace: for each unit the first and the last run that hold a
+// part of it, then two partials for each run (a run's first and last unit may be cut)
+struct Work {
+  int2* runs;     // batch x kv_heads
+  float* parts;   // n_runs x 2 x PART
+};
+
+template <int D, int NT, bool BF16>
+__global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_kernel(Kv4 c, Kv4Attn a, Work ws) {
+  using S = Shape<D, NT>;
+  constexpr int W = S::W, KS = S::KS, BLK = S::BLK, STAGES = S::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[WARPS][STAGES];
+  __shared__ int start_b[WARPS];
+  __shared__ int64_t scan[WARPS], start_at[WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q4 = lane & 3;
+  bool bad = false;
+  pdl_launch_dependents();
+  if (lane == 0)
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
+  fence_mbar_init();
+
+  // the runs: pages of all sequences before each thread's share of them, then of each run's start
+  const int per = (c.batch + 32 * WARPS - 1) / (32 * WARPS);
+  const int b0 = min((int)threadIdx.x * per, c.batch), b1 = min(b0 + per, c.batch);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += span_of(c, a, kv4_sequence(c, b, &bad), S::ROWS).np;
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) scan[warp] = upto;
+  if (threadIdx.x < WARPS) start_b[threadIdx.x] = c.batch;
+  __syncthreads();
+  int64_t before = upto - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    if (i < warp) before += scan[i];
+    total += scan[i];
+  }
+  const int64_t pages = total * c.kv_heads, n_runs = min(pages, (int64_t)gridDim.x * WARPS);
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    if ((int64_t)blockIdx.x * WARPS + i >= n_runs) break;
+    const int64_t x = pages * ((int64_t)blockIdx.x * WARPS + i) / n_runs;
+    int64_t at = before * c.kv_heads;
+    if (x < at || x >= at + mine * c.kv_heads) continue;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t here = (int64_t)span_of(c, a, kv4_sequence(c, b, &bad), S::ROWS).np * c.kv_heads;
+      if (x < at + here) {
+        start_b[i] = b;
+        start_at[i] = x - at;
+        break;
+      }
+      at += here;
+    }
+  }
+  __syncthreads();
+  const int64_t run = (int64_t)blockIdx.x * WARPS + warp;
+  if (run >= n_runs) {
+    if (bad) record_device_error(kErrRange);
+    return;
+  }
+  int64_t left = pages * (run + 1) / n_runs - pages * run / n_runs;  // pages of this run to finish, at least 1
+
+  uint8_t* const ring = smem + warp * S::WARP_BYTES;
+  float4* const par = reinterpret_cast<float4*>(ring + STAGES * BLK);
+  uint8_t* const qs = ring + STAGES * BLK + S::PBYTES;
+  Cursor use;  // the page being used
+  use.b = start_b[warp] - 1;
+  next_sequence(use, c, a, S::ROWS, &bad);
+  use.h = (int)(start_at[warp] / use.p.np);
+  use.i = (int)(start_at[warp] % use.p.np);
+  Cursor get = use;  // the page to fetch next
+  int64_t to_get = left;
+  int ids = 0, ids_from = -64;  // page ids ids_from .. + 31 of the unit, one a lane
+  bool abort = false;
+
+  auto fetch = [&](int stage) {
+    if (to_get == 0) return;
+    if (get.i < ids_from || get.i >= ids_from + 32) {
+      ids_from = get.i;
+      const int i = min(get.i + lane, get.p.np - 1);
+      ids = c.page_table[(int64_t)get.b * c.max_pages + (i < get.p.ns ? i : i + get.p.skip)];
+      if (ids < 0 || ids >= c.n_pages) bad = true, ids = 0;
+    }
+    const int id = __shfl_sync(0xffffffffu, ids, get.i - ids_from);
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[warp][stage], BLK);
+      bulk_copy_g2s(ring + stage * BLK, c.pages + ((int64_t)id * c.kv_heads + get.h) * BLK, BLK, &full[warp][stage]);
+    }
+    --to_get;
+    if (++get.i == get.p.np) {
+      get.i = 0;
+      if (++get.h == c.kv_heads) {
+        get.h = 0;
+        ids_from = -64;
+        if (to_get) next_sequence(get, c, a, S::ROWS, &bad);
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) fetch(i);
+
+  uint32_t qf[S::QS ? 1 : NT][S::QS ? 1 : KS][2];
+  float c1[NT][2], c0[NT][2], m[NT][2], l[NT][2], bs[NT][2];
+  int pos[NT][2];
+  float O[NT][KS][4];
+  float vref = 0.0f;
+  bool begun = use.i == 0;  // this run holds the unit's first page
+  bool fresh = true;
+  int stage = 0;
+  uint32_t parity = 0;
+
+  while (left > 0) {
+    if (fresh) {  // a new unit: its queries
+      fresh = false;
+      vref = 5.9604644775390625e-8f;  // 2^-24: no step is smaller, but 0
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = 8 * nt + g, i = r / a.share;
+        float x[D / 4];
+        constexpr int V = W / 4;  // consecutive words, so dimensions, of this lane
+        if (i < use.s.n) {
+          const int64_t at = (int64_t)(use.s.q0 + i) * a.q_stride + (int64_t)(use.h * a.share + r % a.share) * D + V * q4;
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int v = 0; v < V; v += 2) {
+              if constexpr (BF16) {
+                const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at + W * n + v);
+                x[n * V + v] = __uint_as_float(u << 16);
+                x[n * V + v + 1] = __uint_as_float(u & 0xffff0000u);
+              } else {
+                const float2 u = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + W * n + v);
+                x[n * V + v] = u.x;
+                x[n * V + v + 1] = u.y;
+              }
+            }
+        } else {
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) x[e] = 0.0f;
+        }
+        float mx = 0.0f;
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e) mx = fmaxf(mx, fabsf(x[e]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // q' = q 2^(13 - e), 2^e <= max |q| < 2^(e + 1): fp16 with 2^-28 of the maximum still a normal
+        // number, also where it is scaled by 2^-4. Not below e = -100, and not for infinities.
+        int e = (int)(__float_as_uint(mx) >> 23) - 127;
+        e = e == 128 ? 13 : max(e, -100);
+        const float up = __int_as_float((13 - e + 127) << 23), down = __int_as_float((e - 13 + 127) << 23);
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < D / 4; ++k) {
+          x[k] = __half2float(__float2half_rn(x[k] * up));
+          sum += x[k];
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int v = s >> 1, n = (s & 1) * 2;  // word v of the lane; nibbles n, n + 4 and n + 1, n + 5
+          const uint32_t f0 = pack_half2(x[n * V + v], x[(n + 4) * V + v]);
+          const uint32_t f1 = pack_half2(x[(n + 1) * V + v] * 0.0625f, x[(n + 5) * V + v] * 0.0625f);
+          if constexpr (S::QS)
+            *reinterpret_cast<uint2*>(qs + ((nt * KS + s) * 32 + lane) * 8) = make_uint2(f0, f1);
+          else
+            qf[nt][s][0] = f0, qf[nt][s][1] = f1;
+        }
+        const float f = a.scale * kLog2e * down;
+        const float k1 = f * 16777216.0f, k0 = f * sum;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int col = 2 * q4 + j;
+          c1[nt][j] = __shfl_sync(0xffffffffu, k1, 4 * col);
+          c0[nt][j] = __shfl_sync(0xffffffffu, k0, 4 * col);
+          pos[nt][j] = use.s.len - use.s.n + (8 * nt + col) / a.share;
+          m[nt][j] = kNegInf;
+          l[nt][j] = bs[nt][j] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) O[nt][k][j] = 0.0f;
+      }
+      __syncwarp();
+    }
+
+    if (!mbar_wait_warp(&full[warp][stage], parity, &abort)) break;
+    const uint8_t* const blk = ring + stage * BLK;
+    const int first = (use.i < use.p.ns ? use.i : use.i + use.p.skip) * kKvPage;  // the page's first position
+    const int first_low = (int)max((int64_t)0, (int64_t)use.s.len - use.s.n - a.window + 1);
+    const int last_low = (int)max((int64_t)0, (int64_t)use.s.len - a.window);
+    // whether every row sees the whole page
+    const bool whole = first + kKvPage <= use.s.len - use.s.n + 1 &&
+                       (first >= last_low || first + kKvPage <= a.sinks);
+
+    // the parameters of two tokens a lane, as fp32: key step and base, value step and base
+    float vmax = 0.0f;
+    float4 two[2];
+    {
+      const uint4 u = lds<uint4>(blk + kKvPage * D + lane * 16);
+      const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 pk = __half22float2(*reinterpret_cast<const __half2*>(&raw[2 * e]));
+        const float2 pv = __half22float2(*reinterpret_cast<const __half2*>(&raw[2 * e + 1]));
+        // a value vector of NaN acts through its score, so that a weight of 0 never meets a NaN
+        const float z = (pv.x - pv.x) + (pv.y - pv.y);
+        bool none = z != 0.0f;
+        if (!whole) {  // nor what lies where no row of the unit looks
+          const int j = first + kv4_rho_inv(2 * lane + e);
+          none |= j >= use.s.len || (j < first_low && j >= a.sinks);
+        }
+        two[e] = make_float4(pk.x, pk.y + z, none ? 0.0f : pv.x, none ? 0.0f : pv.y);
+        vmax = fmaxf(vmax, two[e].z);
+      }
+      vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+      if (vmax >= vref) {
+        const float now = __uint_as_float((__float_as_uint(vmax) & 0x7f800000u) + 0x00800000u), f = vref / now;
+        vref = now;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) O[nt][k][j] *= f;
+      }
+      const float inv = __uint_as_float(0x7f000000u - __float_as_uint(vref));  // 1 / vref, a power of two
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        two[e].z *= inv;
+        par[2 * lane + e] = two[e];
+      }
+      __syncwarp();
+    }
+
+    // scores
+    float s[NT][4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[nt][i][j] = 0.0f;
+      uint32_t k0[W / 4], k1[W / 4];  // rows g and g + 8 of the tile
+      const uint8_t* const at = blk + (16 * i + g) * (D / 2) + q4 * W;
+      if constexpr (D == 128) {
+        const uint4 u = lds<uint4>(at), v = lds<uint4>(at + 8 * (D / 2));
+        k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
+        k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
+      } else {
+        const uint2 u = lds<uint2>(at), v = lds<uint2>(at + 8 * (D / 2));
+        k0[0] = u.x, k0[1] = u.y;
+        k1[0] = v.x, k1[1] = v.y;
+      }
+#pragma unroll
+      for (int st = 0; st < KS; ++st) {
+        const int v = st >> 1;
+        const uint32_t x = st & 1 ? k0[v] >> 8 : k0[v], y = st & 1 ? k1[v] >> 8 : k1[v];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint2 f;
+          if constexpr (S::QS)
+            f = lds<uint2>(qs + ((nt * KS + st) * 32 + lane) * 8);
+          else
+            f = make_uint2(qf[nt][st][0], qf[nt][st][1]);
+          mma16816(s[nt][i], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // rows g and g + 8: the correction
+        const float2 k = *reinterpret_cast<const float2*>(&par[16 * i + 8 * e + g]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            s[nt][i][2 * e + j] = fmaf(k.x, s[nt][i][2 * e + j] * c1[nt][j], k.y * c0[nt][j]);
+      }
+    }
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = first + kv4_rho_inv(16 * i + 8 * e + g);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j2 = 0; j2 < 2; ++j2) {
+              const int p = pos[nt][j2];
+              if (j > p || (p - j >= a.window && j >= a.sinks)) s[nt][i][2 * e + j2] = kNegInf;
+            }
+        }
+    }
+    // running maxima
+    float mn[NT][2];
+    bool grows = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float v = m[nt][j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v = fmaxf(v, fmaxf(s[nt][i][j], s[nt][i][2 + j]));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        mn[nt][j] = v;
+        grows |= v > m[nt][j];
+      }
+    if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float al[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          al[j] = mn[nt][j] == kNegInf ? 1.0f : exp2_approx(m[nt][j] - mn[nt][j]);
+          m[nt][j] = mn[nt][j];
+          l[nt][j] *= al[j];
+          bs[nt][j] *= al[j];
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) O[nt][k][j] *= al[j & 1];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t wf[NT][2], wl[NT][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 v = reinterpret_cast<const float2*>(&par[16 * i + 8 * e + g])[1];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float mref = m[nt][j] == kNegInf ? 0.0f : m[nt][j];
+            const float p = exp2_approx(s[nt][i][2 * e + j] - mref);
+            l[nt][j] += p;
+            bs[nt][j] = fmaf(p, v.y, bs[nt][j]);
+            w[j] = p * v.x;
+          }
+          const uint32_t hi = pack_half2(w[0], w[1]);
+          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          wf[nt][e] = transpose8x8(hi);
+          wl[nt][e] = transpose8x8(pack_half2(w[0] - back.x, w[1] - back.y));
+        }
+      }
+      // values: tokens 16 i + q4 (+ 4, + 8, + 12), the words of dimension rows g
+      const uint8_t* const at = blk + kKvPage * (D / 2) + (16 * i + q4) * (D / 2);
+      uint32_t v[4][W / 8];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if constexpr (D == 128) {
+          const uint2 u = lds<uint2>(at + t * 4 * (D / 2) + ((8 * g) ^ ((q4 & 2) << 4)));
+          v[t][0] = u.x, v[t][1] = u.y;
+        } else {
+          v[t][0] = lds<uint32_t>(at + t * 4 * (D / 2) + 4 * g);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int x = k >> 2, by = k & 3;  // word, byte
+        const uint32_t sel = 0x4400u + 0x1111u * by;
+        const uint32_t a01 = __byte_perm(v[0][x], v[1][x], sel), a23 = __byte_perm(v[2][x], v[3][x], sel);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(O[nt][k], a01 & 0x000f000fu, a01 & 0x00f000f0u, a23 & 0x000f000fu, a23 & 0x00f000f0u, wf[nt][0],
+                   wf[nt][1]);
+          mma16816(O[nt][k], a01 & 0x000f000fu, a01 & 0x00f000f0u, a23 & 0x000f000fu, a23 & 0x00f000f0u, wl[nt][0],
+                   wl[nt][1]);
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the block: its place may be written again
+    fetch(stage);
+    if (++stage == STAGES) stage = 0, parity ^= 1u;
+    --left;
+    ++use.i;
+
+    if (use.i == use.p.np || left == 0) {  // the unit ends, or this run's part of it
+      const bool ends = use.i == use.p.np, alone = begun && ends;
+      const int rows = use.s.n * a.share;
+      const int64_t unit = (int64_t)use.b * c.kv_heads + use.h;
+      float* part = ws.parts + (2 * run + (begun ? 1 : 0)) * S::PART;
+      if (lane == 0) {
+        if (begun) ws.runs[unit].x = (int)run;
+        if (ends) ws.runs[unit].y = (int)run;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float sl = l[nt][j], sb = bs[nt][j];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            sl += __shfl_xor_sync(0xffffffffu, sl, o);
+            sb += __shfl_xor_sync(0xffffffffu, sb, o);
+          }
+          const int r = 8 * nt + 2 * q4 + j;
+          if (r >= rows) continue;
+          const float lo = vref * 16777216.0f, hi = vref * 1048576.0f;
+          const float norm = alone ? (sl == 0.0f ? 0.0f : 1.0f / sl) : 1.0f;
+          uint16_t* out = a.out + (int64_t)(use.s.q0 + r / a.share) * a.out_stride +
+                          (int64_t)(use.h * a.share + r % a.share) * D;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {  // nibble n: dimension W n + word
+            float y[W / 8];
+#pragma unroll
+            for (int x = 0; x < W / 8; ++x)
+              y[x] = fmaf(O[nt][4 * x + (n >> 1)][(n & 1) * 2 + j], n & 1 ? hi : lo, sb) * norm;
+            const int d = W * n + (W / 8) * g;
+            if constexpr (D == 128) {
+              if (alone)
+                *reinterpret_cast<__nv_bfloat162*>(out + d) = __floats2bfloat162_rn(y[0], y[1]);
+              else
+                *reinterpret_cast<float2*>(part + r * D + d) = make_float2(y[0], y[1]);
+            } else {
+              if (alone)
+                reinterpret_cast<__nv_bfloat16*>(out)[d] = __float2bfloat16_rn(y[0]);
+              else
+                part[r * D + d] = y[0];
+            }
+          }
+          if (!alone && g == 0) {
+            part[S::ROWS * D + r] = m[nt][j];
+            part[S::ROWS * (D + 1) + r] = sl;
+          }
+        }
+      fresh = true;
+      begun = true;
+      if (ends && left > 0) {
+        use.i = 0;
+        if (++use.h == c.kv_heads) {
+          use.h = 0;
+          next_sequence(use, c, a, S::ROWS, &bad);
+        }
+      }
+    }
+  }
+  if (abort && lane == 0) {  // copies in flight land before the block ends
+    bool given_up = false;
+    for (int i = 0; i < STAGES && to_get + i < left; ++i) {
+      mbar_wait(&full[warp][stage], parity, &given_up);
+      if (++stage == STAGES) stage = 0, parity ^= 1u;
+    }
+  }
+  if (bad) record_device_error(kErrRange);
+}
+
+// Joins the partials of one row of a unit, in the order of the runs; zeros for a row of a sequence
+// that has nothing cached. A unit finished by one run is left alone.
+constexpr int JOIN_WARPS = 8;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Attn a, Work ws) {
+  constexpr int PART = ROWS * (D + 2), E = D / 32;
+  __shared__ float part_m[JOIN_WARPS], part_l[JOIN_WARPS], part_o[JOIN_WARPS][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int unit = blockIdx.x, r = blockIdx.y, b = unit / c.kv_heads, h = unit % c.kv_heads;
+  bool bad = false;
+  const Kv4Seq s = kv4_sequence(c, b, &bad);
+  pdl_wait();
+  const int64_t rows = (int64_t)s.n * a.share;
+  if (rows > ROWS || r >= rows) return;
+  uint16_t* out = a.out + (int64_t)(s.q0 + r / a.share) * a.out_stride + (int64_t)(h * a.share + r % a.share) * D;
+  if (s.len < 1) {
+    for (int d = threadIdx.x; d < D; d += 32 * JOIN_WARPS) out[d] = 0;
+    if (bad && threadIdx.x == 0) record_device_error(kErrRange);
+    return;
+  }
+  const int2 runs = ws.runs[unit];
+  if (runs.x == runs.y) return;
+  float m = kNegInf, l = 0.0f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 4
+  for (int i = runs.x + warp; i <= runs.y; i += JOIN_WARPS) {
+    const float* part = ws.parts + (2 * (int64_t)i + (i == runs.x ? 1 : 0)) * PART;
+    const float pm = part[ROWS * D + r], pl = part[ROWS * (D + 1) + r];
+    float po[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) po[e] = part[r * D + E * lane + e];
+    const float mn = fmaxf(m, pm), ref = mn == kNegInf ? 0.0f : mn;
+    const float f = exp2_approx(m - ref), pf = exp2_approx(pm - ref);
+    m = mn;
+    l = l * f + pl * pf;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * f + po[e] * pf;
+  }
+  if (lane == 0) part_m[warp] = m, part_l[warp] = l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) part_o[warp][E * lane + e] = o[e];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float mx = kNegInf;
+    for (int i = 0; i < JOIN_WARPS; ++i) mx = fmaxf(mx, part_m[i]);
+    if (mx == kNegInf) mx = 0.0f;
+    float sl = 0.0f, so = 0.0f;
+    for (int i = 0; i < JOIN_WARPS; ++i) {
+      const float f = exp2_approx(part_m[i] - mx);
+      sl = fmaf(part_l[i], f, sl);
+      so = fmaf(part_o[i][threadIdx.x], f, so);
+    }
+    reinterpret_cast<__nv_bfloat16*>(out)[threadIdx.x] = __float2bfloat16_rn(sl == 0.0f ? 0.0f : so / sl);
+  }
+}
+
+// runs of a call: a warp each of `blocks` blocks an SM, fewer where there are not as many pages to see
+int64_t runs_of(const Kv4& c, int resident) {
+  const int64_t pages = (int64_t)c.batch * c.kv_heads * ((c.max_kv + kKvPage - 1) / kKvPage);
+  const int64_t blocks = (pages + WARPS - 1) / WARPS;
+  return WARPS * (blocks < 1 ? 1 : blocks < resident ? blocks : resident);
+}
+
+template <int D, int NT, bool BF16>
+cudaError_t launch(const Kv4& c, const Kv4Attn& a, void* workspace, int num_sms, cudaStream_t st) {
+  using S = Shape<D, NT>;
+  Work ws;
+  ws.runs = static_cast<int2*>(workspace);
+  ws.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                      ((int64_t)c.batch * c.kv_heads * 8 + 255) / 256 * 256);
+  cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       S::SMEM);
+  if (e != cudaSuccess) return e;
+  kv4_decode_kernel<D, NT, BF16><<<(unsigned)(runs_of(c, S::BLOCKS * num_sms) / WARPS), 32 * WARPS, S::SMEM, st>>>(c, a, ws);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  const int64_t rows = (int64_t)c.max_q * a.share;
+  cfg.gridDim = dim3((unsigned)(c.batch * c.kv_heads), (unsigned)(rows < S::ROWS ? rows : S::ROWS));
+  cfg.blockDim = dim3(32 * JOIN_WARPS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, S::ROWS>, c, a, ws);
+}
+template <int D, bool BF16>
+cudaError_t launch_rows(const Kv4& c, const Kv4Attn& a, int rows, void* ws, int num_sms, cudaStream_t st) {
+  if (rows <= 8) return launch<D, 1, BF16>(c, a, ws, num_sms, st);
+  if (rows <= 16) return launch<D, 2, BF16>(c, a, ws, num_sms, st);
+  return launch<D, 4, BF16>(c, a, ws, num_sms, st);
+}
+
+}  // namespace
+
+int64_t kv4_decode_ws_bytes(const Kv4& c, int dim, int rows) {
+  // as for the largest GPU of this kind (160 SMs), so that the size does not depend on the device
+  return ((int64_t)c.batch * c.kv_heads * 8 + 255) / 256 * 256 + runs_of(c, 3 * 160) * 2 * rows * (dim + 2) * 4;
+}
+
+cudaError_t launch_kv4_decode(const Kv4& c, int dim, const Kv4Attn& a, bool bf16, int rows, void* ws, int num_sms,
+                              cudaStream_t st) {
+  if (num_sms > 160) num_sms = 160;
+  if (dim == 128)
+    return bf16 ? launch_rows<128, true>(c, a, rows, ws, num_sms, st) : launch_rows<128, false>(c, a, rows, ws, num_sms, st);
+  return bf16 ? launch_rows<64, true>(c, a, rows, ws, num_sms, st) : launch_rows<64, false>(c, a, rows, ws, num_sms, st);
+}
+
+cudaError_t read_clear_device_error_kv4_decode(int* value) {
+  int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_device_error, sizeof(int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
+}
+
+}  // namespace bitnet
