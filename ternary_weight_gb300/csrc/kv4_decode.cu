@@ -192,6 +192,11 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
   next_sequence(use, c, a, S::ROWS, &bad);
   use.h = (int)(start_at[warp] / use.p.np);
   use.i = (int)(start_at[warp] % use.p.np);
+  // a block whose runs all lie inside one unit joins its warps' partials in shared memory first
+  const int64_t unit_at = pages * run / n_runs - use.i;
+  const bool inside = unit_at < pages * ((int64_t)blockIdx.x * WARPS) / n_runs &&
+                      unit_at + use.p.np > pages * ((int64_t)blockIdx.x * WARPS + WARPS) / n_runs;
+  const int rows = use.s.n * a.share;  // of the first unit: all there is where it is used
   Cursor get = use;  // the page to fetch next
   int64_t to_get = left;
   int ids = 0, ids_from = -64;  // page ids ids_from .. + 31 of the unit, one a lane
@@ -506,9 +511,9 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
 
     if (use.i == use.p.np || left == 0) {  // the unit ends, or this run's part of it
       const bool ends = use.i == use.p.np, alone = begun && ends;
-      const int rows = use.s.n * a.share;
+      const int unit_rows = use.s.n * a.share;
       const int64_t unit = (int64_t)use.b * c.kv_heads + use.h;
-      float* part = ws.parts + (2 * run + (begun ? 1 : 0)) * S::PART;
+      float* part = inside ? reinterpret_cast<float*>(ring) : ws.parts + (2 * run + (begun ? 1 : 0)) * S::PART;
       if (lane == 0) {
         if (begun) ws.runs[unit].x = (int)run;
         if (ends) ws.runs[unit].y = (int)run;
@@ -524,7 +529,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
             sb += __shfl_xor_sync(0xffffffffu, sb, o);
           }
           const int r = 8 * nt + 2 * q4 + j;
-          if (r >= rows) continue;
+          if (r >= unit_rows) continue;
           const float lo = vref * 16777216.0f, hi = vref * 1048576.0f;
           const float norm = alone ? (sl == 0.0f ? 0.0f : 1.0f / sl) : 1.0f;
           uint16_t* out = a.out + (int64_t)(use.s.q0 + r / a.share) * a.out_stride +
@@ -571,6 +576,33 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       if (++stage == STAGES) stage = 0, parity ^= 1u;
     }
   }
+  if (inside) {
+    __syncthreads();
+    const auto parts = [&](int i) { return reinterpret_cast<const float*>(smem + i * S::WARP_BYTES); };
+    float* part = ws.parts + 2 * (int64_t)blockIdx.x * WARPS * S::PART;
+    for (int r = threadIdx.x / 32; r < rows; r += WARPS) {
+      float mx = kNegInf, f[WARPS], sl = 0.0f;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) mx = fmaxf(mx, parts(i)[S::ROWS * D + r]);
+      const float ref = mx == kNegInf ? 0.0f : mx;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) {
+        f[i] = exp2_approx(parts(i)[S::ROWS * D + r] - ref);
+        sl = fmaf(parts(i)[S::ROWS * (D + 1) + r], f[i], sl);
+      }
+#pragma unroll
+      for (int d = 0; d < D; d += 32) {
+        float o = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) o = fmaf(parts(i)[r * D + d + lane], f[i], o);
+        part[r * D + d + lane] = o;
+      }
+      if (lane == 0) {
+        part[S::ROWS * D + r] = mx;
+        part[S::ROWS * (D + 1) + r] = sl;
+      }
+    }
+  }
   if (bad) record_device_error(kErrRange);
 }
 
@@ -599,8 +631,15 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Att
   float m = kNegInf, l = 0.0f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  // runs of the blocks that lie inside the unit left one partial a block, with their first run
+  const int in0 = runs.x / WARPS * WARPS + WARPS, in1 = runs.y / WARPS * WARPS;
+  const int head = in0 - runs.x, blocks = in0 < in1 ? (in1 - in0) / WARPS : 0;
+  const int count = in0 < in1 ? head + blocks + runs.y - in1 + 1 : runs.y - runs.x + 1;
 #pragma unroll 4
-  for (int i = runs.x + warp; i <= runs.y; i += JOIN_WARPS) {
+  for (int k = warp; k < count; k += JOIN_WARPS) {
+    const int i = k < head || blocks == 0 ? runs.x + k
+                  : k < head + blocks     ? in0 + (k - head) * WARPS
+                                          : in1 + (k - head - blocks);
     const float* part = ws.parts + (2 * (int64_t)i + (i == runs.x ? 1 : 0)) * PART;
     const float pm = part[ROWS * D + r], pl = part[ROWS * (D + 1) + r];
     float po[E];
