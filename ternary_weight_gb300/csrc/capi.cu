@@ -470,6 +470,8 @@ int check_kv4(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* b, Kv4* out
     return BITNET_EINVAL;
   // rows x heads of a call fit the grids (2^31 blocks of at least 16 vectors)
   if (b->total_q > (int64_t(1) << 33) / cache->kv_heads) return BITNET_EINVAL;
+  // and a warp's share of the pages its counters
+  if ((b->max_kv + kKvPage - 1) / kKvPage > (int64_t(1) << 40) / (b->batch * cache->kv_heads)) return BITNET_EINVAL;
   if (!aligned(cache->pages, 16) || !aligned(b->cu_q, 4) || !aligned(b->kv_len, 4) || !aligned(b->page_table, 4))
     return BITNET_EALIGN;
   *out = Kv4{static_cast<uint8_t*>(cache->pages), (int)cache->n_pages, cache->kv_heads, b->cu_q, b->kv_len,

@@ -78,6 +78,27 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// two fp32 lanes an instruction
+__device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // plain shared-memory loads: the compiler may move them past one another, not past the barriers
 template <typename T>
 __device__ __forceinline__ T lds(const uint8_t* p) {
@@ -182,7 +203,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
     if (bad) record_device_error(kErrRange);
     return;
   }
-  int64_t left = pages * (run + 1) / n_runs - pages * run / n_runs;  // pages of this run to finish, at least 1
+  int left = (int)(pages * (run + 1) / n_runs - pages * run / n_runs);  // pages of this run to finish, at least 1
 
   uint8_t* const ring = smem + warp * S::WARP_BYTES;
   float4* const par = reinterpret_cast<float4*>(ring + STAGES * BLK);
@@ -198,7 +219,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
                       unit_at + use.p.np > pages * ((int64_t)blockIdx.x * WARPS + WARPS) / n_runs;
   const int rows = use.s.n * a.share;  // of the first unit: all there is where it is used
   Cursor get = use;  // the page to fetch next
-  int64_t to_get = left;
+  int to_get = left;
   int ids = 0, ids_from = -64;  // page ids ids_from .. + 31 of the unit, one a lane
   bool abort = false;
 
@@ -229,19 +250,19 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
   for (int i = 0; i < STAGES; ++i) fetch(i);
 
   uint32_t qf[S::QS ? 1 : NT][S::QS ? 1 : KS][2];
-  float c1[NT][2], c0[NT][2], m[NT][2], l[NT][2], bs[NT][2];
+  // per row (column of the fragments): u = step raw + base qs is the score up to the factor c1 >= 0,
+  // m its running maximum
+  float c1[NT][2], qs2[NT][2], m[NT][2], bs[NT][2];
+  uint64_t l[NT];
   int pos[NT][2];
   float O[NT][KS][4];
-  float vref = 0.0f;
   bool begun = use.i == 0;  // this run holds the unit's first page
-  bool fresh = true;
   int stage = 0;
   uint32_t parity = 0;
 
   while (left > 0) {
-    if (fresh) {  // a new unit: its queries
-      fresh = false;
-      vref = 5.9604644775390625e-8f;  // 2^-24: no step is smaller, but 0
+    float vref = 5.9604644775390625e-8f;  // 2^-24: no step is smaller, but 0
+    {  // a new unit: its queries
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + g, i = r / a.share;
@@ -276,7 +297,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
         // number, also where it is scaled by 2^-4. Not below e = -100, and not for infinities.
         int e = (int)(__float_as_uint(mx) >> 23) - 127;
         e = e == 128 ? 13 : max(e, -100);
-        const float up = __int_as_float((13 - e + 127) << 23), down = __int_as_float((e - 13 + 127) << 23);
+        const float up = __int_as_float((13 - e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f), down = __int_as_float((e - 13 + 127) << 23);
         float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < D / 4; ++k) {
@@ -295,17 +316,19 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           else
             qf[nt][s][0] = f0, qf[nt][s][1] = f1;
         }
-        const float f = a.scale * kLog2e * down;
-        const float k1 = f * 16777216.0f, k0 = f * sum;
+        // c1 of 0 would make NaN of a masked score
+        const float k1 = fmaxf(fabsf(a.scale) * kLog2e * down * 16777216.0f, 1.17549435e-38f);
+        const float k0 = sum * 5.9604644775390625e-8f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int col = 2 * q4 + j;
           c1[nt][j] = __shfl_sync(0xffffffffu, k1, 4 * col);
-          c0[nt][j] = __shfl_sync(0xffffffffu, k0, 4 * col);
+          qs2[nt][j] = __shfl_sync(0xffffffffu, k0, 4 * col);
           pos[nt][j] = use.s.len - use.s.n + (8 * nt + col) / a.share;
           m[nt][j] = kNegInf;
-          l[nt][j] = bs[nt][j] = 0.0f;
+          bs[nt][j] = 0.0f;
         }
+        l[nt] = 0;
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -314,11 +337,16 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       __syncwarp();
     }
 
-    if (!mbar_wait_warp(&full[warp][stage], parity, &abort)) break;
-    const uint8_t* const blk = ring + stage * BLK;
-    const int first = (use.i < use.p.ns ? use.i : use.i + use.p.skip) * kKvPage;  // the page's first position
+    // the pages of the unit that are this run's
     const int first_low = (int)max((int64_t)0, (int64_t)use.s.len - use.s.n - a.window + 1);
     const int last_low = (int)max((int64_t)0, (int64_t)use.s.len - a.window);
+    const int until = min(use.p.np, use.i + left);
+    for (; use.i < until; ++use.i, --left) {
+    if (__any_sync(0xffffffffu, !mbar_try_wait(smem_u32(&full[warp][stage]), parity)) &&
+        !mbar_wait_warp(&full[warp][stage], parity, &abort))
+      break;
+    const uint8_t* const blk = ring + stage * BLK;
+    const int first = (use.i < use.p.ns ? use.i : use.i + use.p.skip) * kKvPage;  // the page's first position
     // whether every row sees the whole page
     const bool whole = first + kKvPage <= use.s.len - use.s.n + 1 &&
                        (first >= last_low || first + kKvPage <= a.sinks);
@@ -403,7 +431,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            s[nt][i][2 * e + j] = fmaf(k.x, s[nt][i][2 * e + j] * c1[nt][j], k.y * c0[nt][j]);
+            s[nt][i][2 * e + j] = fmaf(k.x, s[nt][i][2 * e + j], k.y * qs2[nt][j]);
       }
     }
     if (!whole) {
@@ -443,16 +471,22 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
         float al[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          al[j] = mn[nt][j] == kNegInf ? 1.0f : exp2_approx(m[nt][j] - mn[nt][j]);
+          al[j] = mn[nt][j] == kNegInf ? 1.0f : exp2_approx(c1[nt][j] * (m[nt][j] - mn[nt][j]));
           m[nt][j] = mn[nt][j];
-          l[nt][j] *= al[j];
           bs[nt][j] *= al[j];
         }
+        l[nt] = fma2(l[nt], f2pack(al[0], al[1]), 0);
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int j = 0; j < 4; ++j) O[nt][k][j] *= al[j & 1];
       }
+    }
+    uint64_t c1p[NT], off[NT];  // weight = 2^(c1 u + off)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      c1p[nt] = f2pack(c1[nt][0], c1[nt][1]);
+      off[nt] = f2pack(m[nt][0] == kNegInf ? 0.0f : -c1[nt][0] * m[nt][0], m[nt][1] == kNegInf ? 0.0f : -c1[nt][1] * m[nt][1]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -462,15 +496,12 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
         const float2 v = reinterpret_cast<const float2*>(&par[16 * i + 8 * e + g])[1];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float w[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float mref = m[nt][j] == kNegInf ? 0.0f : m[nt][j];
-            const float p = exp2_approx(s[nt][i][2 * e + j] - mref);
-            l[nt][j] += p;
-            bs[nt][j] = fmaf(p, v.y, bs[nt][j]);
-            w[j] = p * v.x;
-          }
+          const float2 t = f2unpack(fma2(f2pack(s[nt][i][2 * e], s[nt][i][2 * e + 1]), c1p[nt], off[nt]));
+          const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
+          l[nt] = add2(l[nt], f2pack(p0, p1));
+          bs[nt][0] = fmaf(p0, v.y, bs[nt][0]);
+          bs[nt][1] = fmaf(p1, v.y, bs[nt][1]);
+          const float w[2] = {p0 * v.x, p1 * v.x};
           const uint32_t hi = pack_half2(w[0], w[1]);
           const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
           wf[nt][e] = transpose8x8(hi);
@@ -506,10 +537,10 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
     __syncwarp();  // every lane has read the block: its place may be written again
     fetch(stage);
     if (++stage == STAGES) stage = 0, parity ^= 1u;
-    --left;
-    ++use.i;
+    }
+    if (use.i < until) break;  // gave up waiting
 
-    if (use.i == use.p.np || left == 0) {  // the unit ends, or this run's part of it
+    {  // the unit ends, or this run's part of it
       const bool ends = use.i == use.p.np, alone = begun && ends;
       const int unit_rows = use.s.n * a.share;
       const int64_t unit = (int64_t)use.b * c.kv_heads + use.h;
@@ -522,7 +553,8 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float sl = l[nt][j], sb = bs[nt][j];
+          const float2 ls = f2unpack(l[nt]);
+          float sl = j ? ls.y : ls.x, sb = bs[nt][j];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             sl += __shfl_xor_sync(0xffffffffu, sl, o);
@@ -554,11 +586,10 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
             }
           }
           if (!alone && g == 0) {
-            part[S::ROWS * D + r] = m[nt][j];
+            part[S::ROWS * D + r] = m[nt][j] * c1[nt][j];
             part[S::ROWS * (D + 1) + r] = sl;
           }
         }
-      fresh = true;
       begun = true;
       if (ends && left > 0) {
         use.i = 0;
