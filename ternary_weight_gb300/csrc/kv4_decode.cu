@@ -36,6 +36,7 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kBigStep = 0.015625f;  // 2^-6
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <int D, int NT>
@@ -57,11 +58,18 @@ struct Shape {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 
+// ZERO: the sum begins at 0 (d is not read)
+template <bool ZERO>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (ZERO)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -386,6 +394,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         two[e].z *= inv;
+        if (two[e].z >= kBigStep) two[e].w = __fdividef(two[e].w, two[e].z);
         par[2 * lane + e] = two[e];
       }
       __syncwarp();
@@ -395,10 +404,6 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
     float s[NT][4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][i][j] = 0.0f;
       uint32_t k0[W / 4], k1[W / 4];  // rows g and g + 8 of the tile
       const uint8_t* const at = blk + (16 * i + g) * (D / 2) + q4 * W;
       if constexpr (D == 128) {
@@ -421,7 +426,10 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
             f = lds<uint2>(qs + ((nt * KS + st) * 32 + lane) * 8);
           else
             f = make_uint2(qf[nt][st][0], qf[nt][st][1]);
-          mma16816(s[nt][i], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
+          if (st == 0)
+            mma16816<true>(s[nt][i], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
+          else
+            mma16816<false>(s[nt][i], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
         }
       }
 #pragma unroll
@@ -490,7 +498,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t wf[NT][2], wl[NT][2];
+      uint32_t wf[NT][2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float2 v = reinterpret_cast<const float2*>(&par[16 * i + 8 * e + g])[1];
@@ -499,13 +507,11 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           const float2 t = f2unpack(fma2(f2pack(s[nt][i][2 * e], s[nt][i][2 * e + 1]), c1p[nt], off[nt]));
           const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
           l[nt] = add2(l[nt], f2pack(p0, p1));
-          bs[nt][0] = fmaf(p0, v.y, bs[nt][0]);
-          bs[nt][1] = fmaf(p1, v.y, bs[nt][1]);
-          const float w[2] = {p0 * v.x, p1 * v.x};
-          const uint32_t hi = pack_half2(w[0], w[1]);
-          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          wf[nt][e] = transpose8x8(hi);
-          wl[nt][e] = transpose8x8(pack_half2(w[0] - back.x, w[1] - back.y));
+          const uint32_t w = pack_half2(p0 * v.x, p1 * v.x);
+          const float2 wr = __half22float2(*reinterpret_cast<const __half2*>(&w));
+          bs[nt][0] = fmaf(v.x >= kBigStep ? wr.x : p0, v.y, bs[nt][0]);
+          bs[nt][1] = fmaf(v.x >= kBigStep ? wr.y : p1, v.y, bs[nt][1]);
+          wf[nt][e] = transpose8x8(w);
         }
       }
       // values: tokens 16 i + q4 (+ 4, + 8, + 12), the words of dimension rows g
@@ -526,12 +532,9 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
         const uint32_t sel = 0x4400u + 0x1111u * by;
         const uint32_t a01 = __byte_perm(v[0][x], v[1][x], sel), a23 = __byte_perm(v[2][x], v[3][x], sel);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(O[nt][k], a01 & 0x000f000fu, a01 & 0x00f000f0u, a23 & 0x000f000fu, a23 & 0x00f000f0u, wf[nt][0],
-                   wf[nt][1]);
-          mma16816(O[nt][k], a01 & 0x000f000fu, a01 & 0x00f000f0u, a23 & 0x000f000fu, a23 & 0x00f000f0u, wl[nt][0],
-                   wl[nt][1]);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816<false>(O[nt][k], a01 & 0x000f000fu, a01 & 0x00f000f0u, a23 & 0x000f000fu, a23 & 0x00f000f0u,
+                          wf[nt][0], wf[nt][1]);
       }
     }
     __syncwarp();  // every lane has read the block: its place may be written again
