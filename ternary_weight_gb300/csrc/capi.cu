@@ -551,8 +551,8 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache* cache, const bitnet_
   int sms = 0;
   if (int st = check_device(&sms)) return st;
   const Kv4Attn a{q, static_cast<uint16_t*>(out), q_stride, out_stride, (int)q_heads, (int)(q_heads / c.kv_heads),
-                  scale, window ? (int)window : INT32_MAX, window ? (int)sinks : 0};
-  return status_of(launch_kv4_attention(c, cache->head_dim, a, dtype == BITNET_BF16, workspace, sms,
+                  scale, window ? (int)window : INT32_MAX, window ? (int)sinks : 0, dtype == BITNET_BF16};
+  return status_of(launch_kv4_attention(c, cache->head_dim, a, workspace, sms,
                                         static_cast<cudaStream_t>(stream)));
 }
 

@@ -95,16 +95,17 @@ struct Kv4Attn {
   int q_heads, share;  // share = q_heads / kv_heads
   float scale;
   int window, sinks;   // window 0x7fffffff: all positions
+  bool bf16;           // of q
 };
 int64_t kv4_attention_ws_bytes(const Kv4& c, int dim, int q_heads);
-cudaError_t launch_kv4_attention(const Kv4& c, int dim, const Kv4Attn& a, bool bf16, void* workspace, int num_sms,
+cudaError_t launch_kv4_attention(const Kv4& c, int dim, const Kv4Attn& a, void* workspace, int num_sms,
                                  cudaStream_t stream);
 cudaError_t read_clear_device_error_kv4_attn(int* value);
 
 // A few rows a sequence (kv4_decode.cu): sequences with n * share <= rows, rows = 8, 16 or 32.
 constexpr int kKvDecodeRows = 32;
 int64_t kv4_decode_ws_bytes(const Kv4& c, int dim, int rows);
-cudaError_t launch_kv4_decode(const Kv4& c, int dim, const Kv4Attn& a, bool bf16, int rows, void* ws, int num_sms,
+cudaError_t launch_kv4_decode(const Kv4& c, int dim, const Kv4Attn& a, int rows, void* ws, int num_sms,
                               cudaStream_t stream);
 cudaError_t read_clear_device_error_kv4_decode(int* value);
 

@@ -101,19 +101,19 @@ int64_t kv4_attention_ws_bytes(const Kv4& c, int dim, int q_heads) {
   return rows ? kv4_decode_ws_bytes(c, dim, rows) : 0;
 }
 
-cudaError_t launch_kv4_attention(const Kv4& c, int dim, const Kv4Attn& a, bool bf16, void* workspace, int num_sms,
+cudaError_t launch_kv4_attention(const Kv4& c, int dim, const Kv4Attn& a, void* workspace, int num_sms,
                                  cudaStream_t st) {
   const int rows = decode_rows(c, a.share);
   if (rows) {
-    if (cudaError_t e = launch_kv4_decode(c, dim, a, bf16, rows, workspace, num_sms, st)) return e;
+    if (cudaError_t e = launch_kv4_decode(c, dim, a, rows, workspace, num_sms, st)) return e;
     if ((int64_t)c.max_q * a.share <= rows) return cudaSuccess;
   }
   const unsigned grid = (unsigned)(((int64_t)c.total_q * a.q_heads + WARPS - 1) / WARPS);
   if (dim == 128)
-    bf16 ? kv4_attn_simple_kernel<128, true><<<grid, 32 * WARPS, 0, st>>>(c, a, rows)
+    a.bf16 ? kv4_attn_simple_kernel<128, true><<<grid, 32 * WARPS, 0, st>>>(c, a, rows)
          : kv4_attn_simple_kernel<128, false><<<grid, 32 * WARPS, 0, st>>>(c, a, rows);
   else
-    bf16 ? kv4_attn_simple_kernel<64, true><<<grid, 32 * WARPS, 0, st>>>(c, a, rows)
+    a.bf16 ? kv4_attn_simple_kernel<64, true><<<grid, 32 * WARPS, 0, st>>>(c, a, rows)
          : kv4_attn_simple_kernel<64, false><<<grid, 32 * WARPS, 0, st>>>(c, a, rows);
   return cudaGetLastError();
 }

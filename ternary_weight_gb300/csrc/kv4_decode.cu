@@ -113,6 +113,35 @@ __device__ __forceinline__ T lds(const uint8_t* p) {
   return *reinterpret_cast<const T*>(p);
 }
 
+// V consecutive numbers of the queries from element `at` on
+template <int V>
+__device__ __forceinline__ void load_q(const Kv4Attn& a, int64_t at, float* x) {
+  if (a.bf16) {
+    uint32_t u[V / 2];
+    const uint16_t* p = static_cast<const uint16_t*>(a.q) + at;
+    if constexpr (V == 4) {
+      const uint2 t = *reinterpret_cast<const uint2*>(p);
+      u[0] = t.x, u[1] = t.y;
+    } else {
+      u[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      x[2 * k] = __uint_as_float(u[k] << 16);
+      x[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+  } else {
+    const float* p = static_cast<const float*>(a.q) + at;
+    if constexpr (V == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(p);
+      x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+    } else {
+      const float2 t = *reinterpret_cast<const float2*>(p);
+      x[0] = t.x, x[1] = t.y;
+    }
+  }
+}
+
 // The pages that the rows of a sequence see: page i of np is page i of the sequence, or i + skip from
 // i = ns on (what lies between the sinks and the window of the first row). np = 0: no row of this
 // kernel's, or nothing cached.
@@ -130,21 +159,6 @@ __device__ __forceinline__ Span span_of(const Kv4& c, const Kv4Attn& a, const Kv
   return p;
 }
 
-// A place in the order sequence, head, page.
-struct Cursor {
-  int b, h, i;
-  Kv4Seq s;
-  Span p;
-};
-__device__ __forceinline__ void next_sequence(Cursor& k, const Kv4& c, const Kv4Attn& a, int max_rows, bool* bad) {
-  do {
-    ++k.b;
-    if (k.b >= c.batch) return;
-    k.s = kv4_sequence(c, k.b, bad);
-    k.p = span_of(c, a, k.s, max_rows);
-  } while (k.p.np == 0);
-}
-
 // where the runs' results go in the workspace: for each unit the first and the last run that hold a
 // part of it, then two partials for each run (a run's first and last unit may be cut)
 struct Work {
@@ -152,87 +166,164 @@ struct Work {
   float* parts;   // n_runs x 2 x PART
 };
 
-template <int D, int NT, bool BF16>
+// A unit (sequence b, head h) and the pages [i, until) of it that a run holds; weight is what the run
+// holds beyond them.
+struct Unit {
+  int b, h, i, until, weight;
+  Kv4Seq s;
+  Span p;
+};
+// Beginning a unit costs about what a page does (its queries' latency, its results): it counts as
+// kUnitCost pages when the runs are cut.
+constexpr int kUnitCost = 2;
+
+// the next unit of a run; false at the run's end
+__device__ __forceinline__ bool next_unit(Unit& u, const Kv4& c, const Kv4Attn& a, int max_rows, bool* bad) {
+  if (u.until < u.p.np || u.weight <= kUnitCost) return false;
+  if (++u.h == c.kv_heads) {
+    u.h = 0;
+    do {
+      if (++u.b >= c.batch) return false;
+      u.s = kv4_sequence(c, u.b, bad);
+      u.p = span_of(c, a, u.s, max_rows);
+    } while (u.p.np == 0);
+  }
+  u.weight -= kUnitCost;
+  u.i = 0;
+  u.until = min(u.p.np, u.weight);
+  u.weight -= u.until;
+  return true;
+}
+
+// SPLIT: units are cut into runs of all warps of the grid, and what they leave is joined by a second
+// kernel. Otherwise a block takes one unit, its warps a part each, and joins them itself.
+template <int D, int NT, bool SPLIT>
 __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_kernel(Kv4 c, Kv4Attn a, Work ws) {
   using S = Shape<D, NT>;
   constexpr int W = S::W, KS = S::KS, BLK = S::BLK, STAGES = S::STAGES;
+  constexpr int V = W / 4;  // consecutive words, so dimensions, of a lane's queries and keys
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[WARPS][STAGES];
-  __shared__ int start_b[WARPS];
-  __shared__ int64_t scan[WARPS], start_at[WARPS];
+  __shared__ int64_t scan[WARPS];
+  __shared__ Unit starts[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q4 = lane & 3;
   bool bad = false;
-  pdl_launch_dependents();
+  if (SPLIT) pdl_launch_dependents();
   if (lane == 0)
     for (int i = 0; i < STAGES; ++i) mbar_init(&full[warp][i], 1);
   fence_mbar_init();
 
-  // the runs: pages of all sequences before each thread's share of them, then of each run's start
-  const int per = (c.batch + 32 * WARPS - 1) / (32 * WARPS);
-  const int b0 = min((int)threadIdx.x * per, c.batch), b1 = min(b0 + per, c.batch);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += span_of(c, a, kv4_sequence(c, b, &bad), S::ROWS).np;
-  int64_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) scan[warp] = upto;
-  if (threadIdx.x < WARPS) start_b[threadIdx.x] = c.batch;
-  __syncthreads();
-  int64_t before = upto - mine, total = 0;
-#pragma unroll
-  for (int i = 0; i < WARPS; ++i) {
-    if (i < warp) before += scan[i];
-    total += scan[i];
-  }
-  const int64_t pages = total * c.kv_heads, n_runs = min(pages, (int64_t)gridDim.x * WARPS);
-#pragma unroll
-  for (int i = 0; i < WARPS; ++i) {
-    if ((int64_t)blockIdx.x * WARPS + i >= n_runs) break;
-    const int64_t x = pages * ((int64_t)blockIdx.x * WARPS + i) / n_runs;
-    int64_t at = before * c.kv_heads;
-    if (x < at || x >= at + mine * c.kv_heads) continue;
+  Unit use;           // the unit being used
+  bool inside;        // the block's warps join their partials in shared memory
+  int64_t run = 0;
+  if constexpr (SPLIT) {
+    // weights of the sequences before each thread's share of them, then each run's start
+    const int per = (c.batch + 32 * WARPS - 1) / (32 * WARPS);
+    const int b0 = min((int)threadIdx.x * per, c.batch), b1 = min(b0 + per, c.batch);
+    int64_t mine = 0;
+    Kv4Seq s{0, 0, 0};
+    Span p{0, 0, 0};
     for (int b = b0; b < b1; ++b) {
-      const int64_t here = (int64_t)span_of(c, a, kv4_sequence(c, b, &bad), S::ROWS).np * c.kv_heads;
-      if (x < at + here) {
-        start_b[i] = b;
-        start_at[i] = x - at;
-        break;
-      }
-      at += here;
+      s = kv4_sequence(c, b, &bad);
+      p = span_of(c, a, s, S::ROWS);
+      if (p.np) mine += (int64_t)(p.np + kUnitCost) * c.kv_heads;
     }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    int64_t before = upto - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+      if (i < warp) before += scan[i];
+      total += scan[i];
+    }
+    // run r begins at r * size + min(r, rest)
+    const int64_t n_runs = min(total, (int64_t)gridDim.x * WARPS);
+    const int64_t run0 = (int64_t)blockIdx.x * WARPS;
+    if (run0 >= n_runs) {  // the whole block
+      if (bad) record_device_error(kErrRange);
+      return;
+    }
+    const int64_t size = total <= INT32_MAX ? (uint32_t)total / (uint32_t)n_runs : total / n_runs;
+    const int64_t rest = total - size * n_runs;
+    const auto begin = [&](int64_t r) { return r * size + min(r, rest); };
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+      const int64_t x = begin(run0 + i);
+      if (run0 + i >= n_runs || x < before || x >= before + mine) continue;
+      int64_t at = before;
+      for (int b = b0; b < b1; ++b) {
+        if (per > 1) {
+          s = kv4_sequence(c, b, &bad);
+          p = span_of(c, a, s, S::ROWS);
+        }
+        if (p.np == 0) continue;
+        const int unit = p.np + kUnitCost;
+        const int64_t here = (int64_t)unit * c.kv_heads;
+        if (x < at + here) {
+          const int h = here <= INT32_MAX ? (uint32_t)(x - at) / (uint32_t)unit : (int)((x - at) / unit);
+          starts[i] = Unit{b, h, (int)(x - at - (int64_t)h * unit), 0, (int)(begin(run0 + i + 1) - x), s, p};
+          break;
+        }
+        at += here;
+      }
+    }
+    __syncthreads();
+    run = run0 + warp;
+    if (run >= n_runs) {
+      if (bad) record_device_error(kErrRange);
+      return;
+    }
+    use = starts[warp];
+    // from a place in the unit's weight to its pages
+    const int64_t unit_at = begin(run) - use.i;
+    const int skip = max(0, kUnitCost - use.i);  // what the run pays of the unit's cost
+    use.i = max(0, use.i - kUnitCost);
+    use.weight -= skip;
+    use.until = max(use.i, min(use.p.np, use.i + use.weight));
+    use.weight -= use.until - use.i;
+    inside = begin(run0) - unit_at > kUnitCost && begin(run0 + WARPS) - unit_at - kUnitCost < use.p.np;
+    if (use.until == use.i) {  // it ends within the unit's cost
+      if (bad) record_device_error(kErrRange);
+      return;
+    }
+  } else {
+    use.b = blockIdx.x / c.kv_heads;
+    use.h = blockIdx.x - use.b * c.kv_heads;
+    use.s = kv4_sequence(c, use.b, &bad);
+    use.p = span_of(c, a, use.s, S::ROWS);
+    if (use.p.np == 0) {  // nothing cached: zeros
+      if ((int64_t)use.s.n * a.share <= S::ROWS && use.s.len < 1)
+        for (int r = warp; r < use.s.n * a.share; r += WARPS)
+          for (int d = lane; d < D; d += 32)
+            a.out[(int64_t)(use.s.q0 + r / a.share) * a.out_stride + (int64_t)(use.h * a.share + r % a.share) * D + d] = 0;
+      if (bad) record_device_error(kErrRange);
+      return;
+    }
+    use.i = (int)((int64_t)use.p.np * warp / WARPS);
+    use.until = (int)((int64_t)use.p.np * (warp + 1) / WARPS);
+    use.weight = 0;
+    inside = true;
   }
-  __syncthreads();
-  const int64_t run = (int64_t)blockIdx.x * WARPS + warp;
-  if (run >= n_runs) {
-    if (bad) record_device_error(kErrRange);
-    return;
-  }
-  int left = (int)(pages * (run + 1) / n_runs - pages * run / n_runs);  // pages of this run to finish, at least 1
+  const int rows = use.s.n * a.share;  // of the first unit: the only one where they are joined here
 
   uint8_t* const ring = smem + warp * S::WARP_BYTES;
   float4* const par = reinterpret_cast<float4*>(ring + STAGES * BLK);
   uint8_t* const qs = ring + STAGES * BLK + S::PBYTES;
-  Cursor use;  // the page being used
-  use.b = start_b[warp] - 1;
-  next_sequence(use, c, a, S::ROWS, &bad);
-  use.h = (int)(start_at[warp] / use.p.np);
-  use.i = (int)(start_at[warp] % use.p.np);
-  // a block whose runs all lie inside one unit joins its warps' partials in shared memory first
-  const int64_t unit_at = pages * run / n_runs - use.i;
-  const bool inside = unit_at < pages * ((int64_t)blockIdx.x * WARPS) / n_runs &&
-                      unit_at + use.p.np > pages * ((int64_t)blockIdx.x * WARPS + WARPS) / n_runs;
-  const int rows = use.s.n * a.share;  // of the first unit: all there is where it is used
-  Cursor get = use;  // the page to fetch next
-  int to_get = left;
-  int ids = 0, ids_from = -64;  // page ids ids_from .. + 31 of the unit, one a lane
+  Unit get = use;                    // the unit whose page is fetched next
+  bool more = use.i < use.until;     // there is a page to fetch
+  int ids = 0, ids_from = -64;       // page ids ids_from .. + 31 of the unit, one a lane
+  int in_flight = 0;
   bool abort = false;
 
   auto fetch = [&](int stage) {
-    if (to_get == 0) return;
+    if (!more) return;
     if (get.i < ids_from || get.i >= ids_from + 32) {
       ids_from = get.i;
       const int i = min(get.i + lane, get.p.np - 1);
@@ -244,18 +335,21 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       mbar_arrive_expect_tx(&full[warp][stage], BLK);
       bulk_copy_g2s(ring + stage * BLK, c.pages + ((int64_t)id * c.kv_heads + get.h) * BLK, BLK, &full[warp][stage]);
     }
-    --to_get;
-    if (++get.i == get.p.np) {
-      get.i = 0;
-      if (++get.h == c.kv_heads) {
-        get.h = 0;
-        ids_from = -64;
-        if (to_get) next_sequence(get, c, a, S::ROWS, &bad);
+    ++in_flight;
+    if (++get.i == get.until) {
+      const int b = get.b;
+      more = next_unit(get, c, a, S::ROWS, &bad);
+      if (get.b != b) ids_from = -64;
+      if (more) {  // its queries are wanted soon
+        const int bytes = a.share * D * (a.bf16 ? 2 : 4);
+        for (int i = 0; i < get.s.n; ++i) {
+          const char* q = static_cast<const char*>(a.q) +
+                          ((get.s.q0 + i) * a.q_stride + (int64_t)get.h * a.share * D) * (a.bf16 ? 2 : 4);
+          for (int o = 128 * lane; o < bytes; o += 128 * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + o));
+        }
       }
     }
   };
-#pragma unroll
-  for (int i = 0; i < STAGES; ++i) fetch(i);
 
   uint32_t qf[S::QS ? 1 : NT][S::QS ? 1 : KS][2];
   // per row (column of the fragments): u = step raw + base qs is the score up to the factor c1 >= 0,
@@ -264,37 +358,30 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
   uint64_t l[NT];
   int pos[NT][2];
   float O[NT][KS][4];
-  bool begun = use.i == 0;  // this run holds the unit's first page
   int stage = 0;
   uint32_t parity = 0;
+  bool started = false;
 
-  while (left > 0) {
+  while (use.i < use.until) {
+    const bool begun = use.i == 0;  // this run holds the unit's first page
     float vref = 5.9604644775390625e-8f;  // 2^-24: no step is smaller, but 0
     {  // a new unit: its queries
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + g, i = r / a.share;
         float x[D / 4];
-        constexpr int V = W / 4;  // consecutive words, so dimensions, of this lane
         if (i < use.s.n) {
           const int64_t at = (int64_t)(use.s.q0 + i) * a.q_stride + (int64_t)(use.h * a.share + r % a.share) * D + V * q4;
 #pragma unroll
-          for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int v = 0; v < V; v += 2) {
-              if constexpr (BF16) {
-                const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at + W * n + v);
-                x[n * V + v] = __uint_as_float(u << 16);
-                x[n * V + v + 1] = __uint_as_float(u & 0xffff0000u);
-              } else {
-                const float2 u = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + W * n + v);
-                x[n * V + v] = u.x;
-                x[n * V + v + 1] = u.y;
-              }
-            }
+          for (int n = 0; n < 8; ++n) load_q<V>(a, at + W * n, &x[n * V]);
         } else {
 #pragma unroll
           for (int e = 0; e < D / 4; ++e) x[e] = 0.0f;
+        }
+        if (!started) {  // behind the first queries: the copies fill the memory's queues
+          started = true;
+#pragma unroll
+          for (int k = 0; k < STAGES; ++k) fetch(k);
         }
         float mx = 0.0f;
 #pragma unroll
@@ -345,210 +432,209 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       __syncwarp();
     }
 
-    // the pages of the unit that are this run's
     const int first_low = (int)max((int64_t)0, (int64_t)use.s.len - use.s.n - a.window + 1);
     const int last_low = (int)max((int64_t)0, (int64_t)use.s.len - a.window);
-    const int until = min(use.p.np, use.i + left);
-    for (; use.i < until; ++use.i, --left) {
-    if (__any_sync(0xffffffffu, !mbar_try_wait(smem_u32(&full[warp][stage]), parity)) &&
-        !mbar_wait_warp(&full[warp][stage], parity, &abort))
-      break;
-    const uint8_t* const blk = ring + stage * BLK;
-    const int first = (use.i < use.p.ns ? use.i : use.i + use.p.skip) * kKvPage;  // the page's first position
-    // whether every row sees the whole page
-    const bool whole = first + kKvPage <= use.s.len - use.s.n + 1 &&
-                       (first >= last_low || first + kKvPage <= a.sinks);
+    for (; use.i < use.until; ++use.i) {
+      if (__any_sync(0xffffffffu, !mbar_try_wait(smem_u32(&full[warp][stage]), parity)) &&
+          !mbar_wait_warp(&full[warp][stage], parity, &abort))
+        break;
+      const uint8_t* const blk = ring + stage * BLK;
+      const int first = (use.i < use.p.ns ? use.i : use.i + use.p.skip) * kKvPage;  // the page's first position
+      // whether every row sees the whole page
+      const bool whole = first + kKvPage <= use.s.len - use.s.n + 1 &&
+                         (first >= last_low || first + kKvPage <= a.sinks);
 
-    // the parameters of two tokens a lane, as fp32: key step and base, value step and base
-    float vmax = 0.0f;
-    float4 two[2];
-    {
-      const uint4 u = lds<uint4>(blk + kKvPage * D + lane * 16);
-      const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 pk = __half22float2(*reinterpret_cast<const __half2*>(&raw[2 * e]));
-        const float2 pv = __half22float2(*reinterpret_cast<const __half2*>(&raw[2 * e + 1]));
-        // a value vector of NaN acts through its score, so that a weight of 0 never meets a NaN
-        const float z = (pv.x - pv.x) + (pv.y - pv.y);
-        bool none = z != 0.0f;
-        if (!whole) {  // nor what lies where no row of the unit looks
-          const int j = first + kv4_rho_inv(2 * lane + e);
-          none |= j >= use.s.len || (j < first_low && j >= a.sinks);
-        }
-        two[e] = make_float4(pk.x, pk.y + z, none ? 0.0f : pv.x, none ? 0.0f : pv.y);
-        vmax = fmaxf(vmax, two[e].z);
-      }
-      vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
-      if (vmax >= vref) {
-        const float now = __uint_as_float((__float_as_uint(vmax) & 0x7f800000u) + 0x00800000u), f = vref / now;
-        vref = now;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) O[nt][k][j] *= f;
-      }
-      const float inv = __uint_as_float(0x7f000000u - __float_as_uint(vref));  // 1 / vref, a power of two
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        two[e].z *= inv;
-        if (two[e].z >= kBigStep) two[e].w = __fdividef(two[e].w, two[e].z);
-        par[2 * lane + e] = two[e];
-      }
-      __syncwarp();
-    }
-
-    // scores
-    float s[NT][4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t k0[W / 4], k1[W / 4];  // rows g and g + 8 of the tile
-      const uint8_t* const at = blk + (16 * i + g) * (D / 2) + q4 * W;
-      if constexpr (D == 128) {
-        const uint4 u = lds<uint4>(at), v = lds<uint4>(at + 8 * (D / 2));
-        k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
-        k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
-      } else {
-        const uint2 u = lds<uint2>(at), v = lds<uint2>(at + 8 * (D / 2));
-        k0[0] = u.x, k0[1] = u.y;
-        k1[0] = v.x, k1[1] = v.y;
-      }
-#pragma unroll
-      for (int st = 0; st < KS; ++st) {
-        const int v = st >> 1;
-        const uint32_t x = st & 1 ? k0[v] >> 8 : k0[v], y = st & 1 ? k1[v] >> 8 : k1[v];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          uint2 f;
-          if constexpr (S::QS)
-            f = lds<uint2>(qs + ((nt * KS + st) * 32 + lane) * 8);
-          else
-            f = make_uint2(qf[nt][st][0], qf[nt][st][1]);
-          if (st == 0)
-            mma16816<true>(s[nt][i], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
-          else
-            mma16816<false>(s[nt][i], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {  // rows g and g + 8: the correction
-        const float2 k = *reinterpret_cast<const float2*>(&par[16 * i + 8 * e + g]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            s[nt][i][2 * e + j] = fmaf(k.x, s[nt][i][2 * e + j], k.y * qs2[nt][j]);
-      }
-    }
-    if (!whole) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
+      // the parameters of two tokens a lane, as fp32: key step and base, value step and base
+      float vmax = 0.0f;
+      float4 two[2];
+      {
+        const uint4 u = lds<uint4>(blk + kKvPage * D + lane * 16);
+        const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int j = first + kv4_rho_inv(16 * i + 8 * e + g);
+          const float2 pk = __half22float2(*reinterpret_cast<const __half2*>(&raw[2 * e]));
+          const float2 pv = __half22float2(*reinterpret_cast<const __half2*>(&raw[2 * e + 1]));
+          // a value vector of NaN acts through its score, so that a weight of 0 never meets a NaN
+          const float z = (pv.x - pv.x) + (pv.y - pv.y);
+          bool none = z != 0.0f;
+          if (!whole) {  // nor what lies where no row of the unit looks
+            const int j = first + kv4_rho_inv(2 * lane + e);
+            none |= j >= use.s.len || (j < first_low && j >= a.sinks);
+          }
+          two[e] = make_float4(pk.x, pk.y + z, none ? 0.0f : pv.x, none ? 0.0f : pv.y);
+          vmax = fmaxf(vmax, two[e].z);
+        }
+        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+        if (vmax >= vref) {
+          const float now = __uint_as_float((__float_as_uint(vmax) & 0x7f800000u) + 0x00800000u), f = vref / now;
+          vref = now;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j2 = 0; j2 < 2; ++j2) {
-              const int p = pos[nt][j2];
-              if (j > p || (p - j >= a.window && j >= a.sinks)) s[nt][i][2 * e + j2] = kNegInf;
-            }
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) O[nt][k][j] *= f;
         }
-    }
-    // running maxima
-    float mn[NT][2];
-    bool grows = false;
+        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(vref));  // 1 / vref, a power of two
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float v = m[nt][j];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v = fmaxf(v, fmaxf(s[nt][i][j], s[nt][i][2 + j]));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        mn[nt][j] = v;
-        grows |= v > m[nt][j];
+        for (int e = 0; e < 2; ++e) {
+          two[e].z *= inv;
+          if (two[e].z >= kBigStep) two[e].w = __fdividef(two[e].w, two[e].z);
+          par[2 * lane + e] = two[e];
+        }
+        __syncwarp();
       }
-    if (__any_sync(0xffffffffu, grows)) {
+
+      // scores
+      float s[NT][4][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float al[2];
+      for (int i = 0; i < 4; ++i) {
+        uint32_t k0[W / 4], k1[W / 4];  // rows g and g + 8 of the tile
+        const uint8_t* const at = blk + (16 * i + g) * (D / 2) + q4 * W;
+        if constexpr (D == 128) {
+          const uint4 u = lds<uint4>(at), v = lds<uint4>(at + 8 * (D / 2));
+          k0[0] = u.x, k0[1] = u.y, k0[2] = u.z, k0[3] = u.w;
+          k1[0] = v.x, k1[1] = v.y, k1[2] = v.z, k1[3] = v.w;
+        } else {
+          const uint2 u = lds<uint2>(at), v = lds<uint2>(at + 8 * (D / 2));
+          k0[0] = u.x, k0[1] = u.y;
+          k1[0] = v.x, k1[1] = v.y;
+        }
+#pragma unroll
+        for (int st = 0; st < KS; ++st) {
+          const int v = st >> 1;
+          const uint32_t x = st & 1 ? k0[v] >> 8 : k0[v], y = st & 1 ? k1[v] >> 8 : k1[v];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint2 f;
+            if constexpr (S::QS)
+              f = lds<uint2>(qs + ((nt * KS + st) * 32 + lane) * 8);
+            else
+              f = make_uint2(qf[nt][st][0], qf[nt][st][1]);
+            if (st == 0)
+              mma16816<true>(s[nt][i], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
+            else
+              mma16816<false>(s[nt][i], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // rows g and g + 8: the correction
+          const float2 k = *reinterpret_cast<const float2*>(&par[16 * i + 8 * e + g]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              s[nt][i][2 * e + j] = fmaf(k.x, s[nt][i][2 * e + j], k.y * qs2[nt][j]);
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = first + kv4_rho_inv(16 * i + 8 * e + g);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j2 = 0; j2 < 2; ++j2) {
+                const int p = pos[nt][j2];
+                if (j > p || (p - j >= a.window && j >= a.sinks)) s[nt][i][2 * e + j2] = kNegInf;
+              }
+          }
+      }
+      // running maxima
+      float mn[NT][2];
+      bool grows = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          al[j] = mn[nt][j] == kNegInf ? 1.0f : exp2_approx(c1[nt][j] * (m[nt][j] - mn[nt][j]));
-          m[nt][j] = mn[nt][j];
-          bs[nt][j] *= al[j];
+          float v = m[nt][j];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v = fmaxf(v, fmaxf(s[nt][i][j], s[nt][i][2 + j]));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          mn[nt][j] = v;
+          grows |= v > m[nt][j];
         }
-        l[nt] = fma2(l[nt], f2pack(al[0], al[1]), 0);
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) O[nt][k][j] *= al[j & 1];
-      }
-    }
-    uint64_t c1p[NT], off[NT];  // weight = 2^(c1 u + off)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      c1p[nt] = f2pack(c1[nt][0], c1[nt][1]);
-      off[nt] = f2pack(m[nt][0] == kNegInf ? 0.0f : -c1[nt][0] * m[nt][0], m[nt][1] == kNegInf ? 0.0f : -c1[nt][1] * m[nt][1]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t wf[NT][2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 v = reinterpret_cast<const float2*>(&par[16 * i + 8 * e + g])[1];
+      if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float2 t = f2unpack(fma2(f2pack(s[nt][i][2 * e], s[nt][i][2 * e + 1]), c1p[nt], off[nt]));
-          const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
-          l[nt] = add2(l[nt], f2pack(p0, p1));
-          const uint32_t w = pack_half2(p0 * v.x, p1 * v.x);
-          const float2 wr = __half22float2(*reinterpret_cast<const __half2*>(&w));
-          bs[nt][0] = fmaf(v.x >= kBigStep ? wr.x : p0, v.y, bs[nt][0]);
-          bs[nt][1] = fmaf(v.x >= kBigStep ? wr.y : p1, v.y, bs[nt][1]);
-          wf[nt][e] = transpose8x8(w);
+          float al[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            al[j] = mn[nt][j] == kNegInf ? 1.0f : exp2_approx(c1[nt][j] * (m[nt][j] - mn[nt][j]));
+            m[nt][j] = mn[nt][j];
+            bs[nt][j] *= al[j];
+          }
+          l[nt] = fma2(l[nt], f2pack(al[0], al[1]), 0);
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) O[nt][k][j] *= al[j & 1];
         }
       }
-      // values: tokens 16 i + q4 (+ 4, + 8, + 12), the words of dimension rows g
-      const uint8_t* const at = blk + kKvPage * (D / 2) + (16 * i + q4) * (D / 2);
-      uint32_t v[4][W / 8];
+      uint64_t c1p[NT], off[NT];  // weight = 2^(c1 u + off)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if constexpr (D == 128) {
-          const uint2 u = lds<uint2>(at + t * 4 * (D / 2) + ((8 * g) ^ ((q4 & 2) << 4)));
-          v[t][0] = u.x, v[t][1] = u.y;
-        } else {
-          v[t][0] = lds<uint32_t>(at + t * 4 * (D / 2) + 4 * g);
+      for (int nt = 0; nt < NT; ++nt) {
+        c1p[nt] = f2pack(c1[nt][0], c1[nt][1]);
+        off[nt] = f2pack(m[nt][0] == kNegInf ? 0.0f : -c1[nt][0] * m[nt][0], m[nt][1] == kNegInf ? 0.0f : -c1[nt][1] * m[nt][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t wf[NT][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 v = reinterpret_cast<const float2*>(&par[16 * i + 8 * e + g])[1];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 t = f2unpack(fma2(f2pack(s[nt][i][2 * e], s[nt][i][2 * e + 1]), c1p[nt], off[nt]));
+            const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
+            l[nt] = add2(l[nt], f2pack(p0, p1));
+            const uint32_t w = pack_half2(p0 * v.x, p1 * v.x);
+            const float2 wr = __half22float2(*reinterpret_cast<const __half2*>(&w));
+            bs[nt][0] = fmaf(v.x >= kBigStep ? wr.x : p0, v.y, bs[nt][0]);
+            bs[nt][1] = fmaf(v.x >= kBigStep ? wr.y : p1, v.y, bs[nt][1]);
+            wf[nt][e] = transpose8x8(w);
+          }
+        }
+        // values: tokens 16 i + q4 (+ 4, + 8, + 12), the words of dimension rows g
+        const uint8_t* const at = blk + kKvPage * (D / 2) + (16 * i + q4) * (D / 2);
+        uint32_t v[4][W / 8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          if constexpr (D == 128) {
+            const uint2 u = lds<uint2>(at + t * 4 * (D / 2) + ((8 * g) ^ ((q4 & 2) << 4)));
+            v[t][0] = u.x, v[t][1] = u.y;
+          } else {
+            v[t][0] = lds<uint32_t>(at + t * 4 * (D / 2) + 4 * g);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int x = k >> 2, by = k & 3;  // word, byte
+          const uint32_t sel = 0x4400u + 0x1111u * by;
+          const uint32_t a01 = __byte_perm(v[0][x], v[1][x], sel), a23 = __byte_perm(v[2][x], v[3][x], sel);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816<false>(O[nt][k], a01 & 0x000f000fu, a01 & 0x00f000f0u, a23 & 0x000f000fu, a23 & 0x00f000f0u,
+                            wf[nt][0], wf[nt][1]);
         }
       }
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int x = k >> 2, by = k & 3;  // word, byte
-        const uint32_t sel = 0x4400u + 0x1111u * by;
-        const uint32_t a01 = __byte_perm(v[0][x], v[1][x], sel), a23 = __byte_perm(v[2][x], v[3][x], sel);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma16816<false>(O[nt][k], a01 & 0x000f000fu, a01 & 0x00f000f0u, a23 & 0x000f000fu, a23 & 0x00f000f0u,
-                          wf[nt][0], wf[nt][1]);
-      }
+      __syncwarp();  // every lane has read the block: its place may be written again
+      --in_flight;
+      fetch(stage);
+      if (++stage == STAGES) stage = 0, parity ^= 1u;
     }
-    __syncwarp();  // every lane has read the block: its place may be written again
-    fetch(stage);
-    if (++stage == STAGES) stage = 0, parity ^= 1u;
-    }
-    if (use.i < until) break;  // gave up waiting
+    if (abort) break;
 
     {  // the unit ends, or this run's part of it
-      const bool ends = use.i == use.p.np, alone = begun && ends;
+      const bool ends = use.i == use.p.np, alone = SPLIT && begun && ends;
       const int unit_rows = use.s.n * a.share;
       const int64_t unit = (int64_t)use.b * c.kv_heads + use.h;
       float* part = inside ? reinterpret_cast<float*>(ring) : ws.parts + (2 * run + (begun ? 1 : 0)) * S::PART;
-      if (lane == 0) {
+      if (SPLIT && lane == 0) {
         if (begun) ws.runs[unit].x = (int)run;
         if (ends) ws.runs[unit].y = (int)run;
       }
@@ -593,19 +679,12 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
             part[S::ROWS * (D + 1) + r] = sl;
           }
         }
-      begun = true;
-      if (ends && left > 0) {
-        use.i = 0;
-        if (++use.h == c.kv_heads) {
-          use.h = 0;
-          next_sequence(use, c, a, S::ROWS, &bad);
-        }
-      }
     }
+    if (!next_unit(use, c, a, S::ROWS, &bad)) break;
   }
   if (abort && lane == 0) {  // copies in flight land before the block ends
     bool given_up = false;
-    for (int i = 0; i < STAGES && to_get + i < left; ++i) {
+    for (; in_flight > 0; --in_flight) {
       mbar_wait(&full[warp][stage], parity, &given_up);
       if (++stage == STAGES) stage = 0, parity ^= 1u;
     }
@@ -613,25 +692,37 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
   if (inside) {
     __syncthreads();
     const auto parts = [&](int i) { return reinterpret_cast<const float*>(smem + i * S::WARP_BYTES); };
-    float* part = ws.parts + 2 * (int64_t)blockIdx.x * WARPS * S::PART;
-    for (int r = threadIdx.x / 32; r < rows; r += WARPS) {
+    float* part = SPLIT ? ws.parts + 2 * (int64_t)blockIdx.x * WARPS * S::PART : nullptr;
+    for (int r = warp; r < rows; r += WARPS) {
       float mx = kNegInf, f[WARPS], sl = 0.0f;
-#pragma unroll
-      for (int i = 0; i < WARPS; ++i) mx = fmaxf(mx, parts(i)[S::ROWS * D + r]);
-      const float ref = mx == kNegInf ? 0.0f : mx;
+      bool has[WARPS];  // a warp of a unit with fewer pages than warps has no part
 #pragma unroll
       for (int i = 0; i < WARPS; ++i) {
-        f[i] = exp2_approx(parts(i)[S::ROWS * D + r] - ref);
-        sl = fmaf(parts(i)[S::ROWS * (D + 1) + r], f[i], sl);
+        has[i] = SPLIT || (int64_t)use.p.np * (i + 1) / WARPS > (int64_t)use.p.np * i / WARPS;
+        if (has[i]) mx = fmaxf(mx, parts(i)[S::ROWS * D + r]);
       }
+      const float ref = mx == kNegInf ? 0.0f : mx;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i)
+        if (has[i]) {
+          f[i] = exp2_approx(parts(i)[S::ROWS * D + r] - ref);
+          sl = fmaf(parts(i)[S::ROWS * (D + 1) + r], f[i], sl);
+        }
+      const float norm = sl == 0.0f ? 0.0f : 1.0f / sl;
+      uint16_t* out = a.out + (int64_t)(use.s.q0 + r / a.share) * a.out_stride +
+                      (int64_t)(use.h * a.share + r % a.share) * D;
 #pragma unroll
       for (int d = 0; d < D; d += 32) {
         float o = 0.0f;
 #pragma unroll
-        for (int i = 0; i < WARPS; ++i) o = fmaf(parts(i)[r * D + d + lane], f[i], o);
-        part[r * D + d + lane] = o;
+        for (int i = 0; i < WARPS; ++i)
+          if (has[i]) o = fmaf(parts(i)[r * D + d + lane], f[i], o);
+        if (SPLIT)
+          part[r * D + d + lane] = o;
+        else
+          reinterpret_cast<__nv_bfloat16*>(out)[d + lane] = __float2bfloat16_rn(o * norm);
       }
-      if (lane == 0) {
+      if (SPLIT && lane == 0) {
         part[S::ROWS * D + r] = mx;
         part[S::ROWS * (D + 1) + r] = sl;
       }
@@ -704,24 +795,40 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Att
   }
 }
 
-// runs of a call: a warp each of `blocks` blocks an SM, fewer where there are not as many pages to see
+// the most pages that a sequence can show the rows of a call
+int64_t most_pages(const Kv4& c) { return ((int64_t)c.max_kv + kKvPage - 1) / kKvPage; }
+// runs of a call: a warp each of `resident` blocks, fewer where there are not as many pages to see
 int64_t runs_of(const Kv4& c, int resident) {
-  const int64_t pages = (int64_t)c.batch * c.kv_heads * ((c.max_kv + kKvPage - 1) / kKvPage);
-  const int64_t blocks = (pages + WARPS - 1) / WARPS;
+  const int64_t weight = (int64_t)c.batch * c.kv_heads * (most_pages(c) + kUnitCost);
+  const int64_t blocks = (weight + WARPS - 1) / WARPS;
   return WARPS * (blocks < 1 ? 1 : blocks < resident ? blocks : resident);
 }
+// Whether units are cut. A block for each unit needs no search for the runs and no second kernel, but
+// lasts as long as the longest: measured, cut and uncut, us (20 and 5 heads x 128, one query a
+// sequence): 1 x 512 tokens 9.0, 6.4; 1 x 1024 9.3, 8.4; 1 x 4096 10.4, 23.3; 64 x 1024 21.4, 16.8;
+// 64 x 2048 29.2, 26.8; 64 x 4096 42.2, 45.5; 256 x 2048 78.4, 68.6.
+bool cuts(const Kv4& c) {
+  const int64_t uncut = 16 + (int64_t)c.batch * c.kv_heads / 20;
+  return most_pages(c) > (uncut < 64 ? uncut : 64);
+}
 
-template <int D, int NT, bool BF16>
+template <int D, int NT>
 cudaError_t launch(const Kv4& c, const Kv4Attn& a, void* workspace, int num_sms, cudaStream_t st) {
   using S = Shape<D, NT>;
-  Work ws;
+  Work ws{};
+  cudaError_t e;
+  if (!cuts(c)) {
+    e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    kv4_decode_kernel<D, NT, false><<<(unsigned)(c.batch * c.kv_heads), 32 * WARPS, S::SMEM, st>>>(c, a, ws);
+    return cudaGetLastError();
+  }
   ws.runs = static_cast<int2*>(workspace);
   ws.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                       ((int64_t)c.batch * c.kv_heads * 8 + 255) / 256 * 256);
-  cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       S::SMEM);
+  e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
-  kv4_decode_kernel<D, NT, BF16><<<(unsigned)(runs_of(c, S::BLOCKS * num_sms) / WARPS), 32 * WARPS, S::SMEM, st>>>(c, a, ws);
+  kv4_decode_kernel<D, NT, true><<<(unsigned)(runs_of(c, S::BLOCKS * num_sms) / WARPS), 32 * WARPS, S::SMEM, st>>>(c, a, ws);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const int64_t rows = (int64_t)c.max_q * a.share;
@@ -735,26 +842,25 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, void* workspace, int num_sms,
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, S::ROWS>, c, a, ws);
 }
-template <int D, bool BF16>
+template <int D>
 cudaError_t launch_rows(const Kv4& c, const Kv4Attn& a, int rows, void* ws, int num_sms, cudaStream_t st) {
-  if (rows <= 8) return launch<D, 1, BF16>(c, a, ws, num_sms, st);
-  if (rows <= 16) return launch<D, 2, BF16>(c, a, ws, num_sms, st);
-  return launch<D, 4, BF16>(c, a, ws, num_sms, st);
+  if (rows <= 8) return launch<D, 1>(c, a, ws, num_sms, st);
+  if (rows <= 16) return launch<D, 2>(c, a, ws, num_sms, st);
+  return launch<D, 4>(c, a, ws, num_sms, st);
 }
 
 }  // namespace
 
 int64_t kv4_decode_ws_bytes(const Kv4& c, int dim, int rows) {
+  if (!cuts(c)) return 0;
   // as for the largest GPU of this kind (160 SMs), so that the size does not depend on the device
   return ((int64_t)c.batch * c.kv_heads * 8 + 255) / 256 * 256 + runs_of(c, 3 * 160) * 2 * rows * (dim + 2) * 4;
 }
 
-cudaError_t launch_kv4_decode(const Kv4& c, int dim, const Kv4Attn& a, bool bf16, int rows, void* ws, int num_sms,
+cudaError_t launch_kv4_decode(const Kv4& c, int dim, const Kv4Attn& a, int rows, void* ws, int num_sms,
                               cudaStream_t st) {
   if (num_sms > 160) num_sms = 160;
-  if (dim == 128)
-    return bf16 ? launch_rows<128, true>(c, a, rows, ws, num_sms, st) : launch_rows<128, false>(c, a, rows, ws, num_sms, st);
-  return bf16 ? launch_rows<64, true>(c, a, rows, ws, num_sms, st) : launch_rows<64, false>(c, a, rows, ws, num_sms, st);
+  return dim == 128 ? launch_rows<128>(c, a, rows, ws, num_sms, st) : launch_rows<64>(c, a, rows, ws, num_sms, st);
 }
 
 cudaError_t read_clear_device_error_kv4_decode(int* value) {
