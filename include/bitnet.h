@@ -460,7 +460,7 @@ BITNET_API int bitnet_kv4_read(const bitnet_kv4_cache *cache, const bitnet_kv4_b
  *            fp32 values round to 11 bits.
  *   out    : total_q rows of q_heads x head_dim, bf16 (device, written), row stride out_stride. The
  *            sums are held in fp32; softmax weights enter the product with the values as fp16.
- *   q_heads: a multiple of kv_heads, at most 128 * kv_heads
+ *   q_heads: a multiple of kv_heads, at most 128 * kv_heads, and total_q * q_heads / kv_heads < 2^31 - 4096
  *   window : 0 for all positions, else 1 .. 2^31 - 1; sinks: 0 .. 2^31 - 1 (unused with window 0)
  *   workspace : device, 256-byte aligned, at least bitnet_kv4_attention_workspace_size bytes (for
  *            the same cache, batch sizes and q_heads; it may be NULL where that is 0). Needs no

@@ -493,6 +493,10 @@ int check_kv4_rows(const Kv4& c, int dim, const void* k, const void* v, int dtyp
 bool valid_q_heads(int64_t q_heads, int64_t kv_heads) {
   return q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads / kv_heads <= kKvMaxShare;
 }
+// rows of a key/value head are counted in 32 bits
+bool valid_q_rows(const Kv4& c, int64_t q_heads) {
+  return (int64_t)c.total_q * (q_heads / c.kv_heads) <= INT32_MAX - 4096;
+}
 }  // namespace
 
 BITNET_API int64_t bitnet_kv4_cache_bytes(int64_t n_pages, int64_t kv_heads, int64_t head_dim) {
@@ -528,7 +532,7 @@ BITNET_API int64_t bitnet_kv4_attention_workspace_size(const bitnet_kv4_cache* c
                                                        int64_t q_heads) {
   Kv4 c{};
   if (int st = check_kv4(cache, batch, &c)) return st;
-  if (!valid_q_heads(q_heads, c.kv_heads)) return BITNET_EINVAL;
+  if (!valid_q_heads(q_heads, c.kv_heads) || !valid_q_rows(c, q_heads)) return BITNET_EINVAL;
   return kv4_attention_ws_bytes(c, cache->head_dim, (int)q_heads);
 }
 
@@ -544,6 +548,7 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache* cache, const bitnet_
   const int64_t row = q_heads * cache->head_dim;
   if (int st = check_stride(q_stride, row, dtype == BITNET_BF16 ? 2 : 4)) return st;
   if (int st = check_stride(out_stride, row, 2)) return st;
+  if (!valid_q_rows(c, q_heads)) return BITNET_EINVAL;
   const int64_t need = kv4_attention_ws_bytes(c, cache->head_dim, (int)q_heads);
   if (need > 0 && (!workspace || workspace_bytes < need)) return BITNET_EINVAL;
   if (!aligned(q, 16) || !aligned(out, 16) || (workspace && !aligned(workspace, 256))) return BITNET_EALIGN;
@@ -576,8 +581,8 @@ BITNET_API int bitnet_last_device_error(void) {
                                     read_clear_device_error_quant_weight, read_clear_device_error_sweep,
                                     read_clear_device_error_gemv_ring, read_clear_device_error_selftest,
                                     read_clear_device_error_prefill, read_clear_device_error_pair,
-                                    read_clear_device_error_kv4_cache, read_clear_device_error_kv4_attn,
-                                    read_clear_device_error_kv4_decode};
+                                    read_clear_device_error_kv4_cache, read_clear_device_error_kv4_decode,
+                                    read_clear_device_error_kv4_prompt};
   for (auto rd : readers) {
     int v = 0;
     if (rd(&v) != cudaSuccess) return BITNET_ECUDA;

@@ -100,7 +100,6 @@ struct Kv4Attn {
 int64_t kv4_attention_ws_bytes(const Kv4& c, int dim, int q_heads);
 cudaError_t launch_kv4_attention(const Kv4& c, int dim, const Kv4Attn& a, void* workspace, int num_sms,
                                  cudaStream_t stream);
-cudaError_t read_clear_device_error_kv4_attn(int* value);
 
 // A few rows a sequence (kv4_decode.cu): sequences with n * share <= rows, rows = 8, 16 or 32.
 constexpr int kKvDecodeRows = 32;
@@ -108,5 +107,9 @@ int64_t kv4_decode_ws_bytes(const Kv4& c, int dim, int rows);
 cudaError_t launch_kv4_decode(const Kv4& c, int dim, const Kv4Attn& a, int rows, void* ws, int num_sms,
                               cudaStream_t stream);
 cudaError_t read_clear_device_error_kv4_decode(int* value);
+// Many rows (kv4_prompt.cu): sequences with n * share > done_rows.
+int64_t kv4_prompt_ws_bytes(const Kv4& c, int dim, int share);
+cudaError_t launch_kv4_prompt(const Kv4& c, int dim, const Kv4Attn& a, int done_rows, void* ws, cudaStream_t stream);
+cudaError_t read_clear_device_error_kv4_prompt(int* value);
 
 }  // namespace bitnet

@@ -1,0 +1,672 @@
+// kv4_prompt.cu -- attention over the 4-bit key/value cache for many query rows a sequence (prompts
+// and their chunks), on the 5th-generation tensor cores.
+//
+// A block takes 256 query rows of one sequence and key/value head (tokens x shared heads, so that the
+// heads that share keys and values share their expansion too) as two tiles of 128, and walks over the
+// cache 128 tokens (two pages) at a time:
+//   S_t = Q_t K^T     128 x 128, K = D: both operands in shared memory (128-byte swizzle, K-major)
+//   P_t = 2^(c1 S - c1 m)  in registers, written over S_t in tensor memory as fp16
+//   O_t += P_t V      128 x D, K = 128: P from tensor memory, V^T in shared memory
+// Bound by the tensor cores (4 D flops a pair), then by the exponentials.
+//
+// Operands are fp16 and sums fp32: q at a power-of-two scale of its row, k and v as step * code + base
+// rounded to fp16 (2^-11 of the number itself, less than the 4-bit step by far), p up to 2^8.
+// The codes are expanded once for both tiles: a code masked into the mantissa of 1024.0 (or 16 of it)
+// becomes an exact fp16 by one multiply-add, the number by another. Word w of a key goes to columns
+// 8 w .. 8 w + 7 in nibble order 0 4 1 5 2 6 3 7; the queries are stored in the same order. Values are
+// transposed on the way: a lane takes one word of 8 tokens, pairs them byte by byte, and stores 8
+// tokens of a dimension as 16 bytes.
+//
+// Roles (17 warps): 0-3 and 4-7 softmax of the two tiles, one row a thread; 8-11 keys; 12-15 values;
+// 16 issues the MMAs in the order  PV_A(j) S_A(j+1) PV_B(j) S_B(j+1): one tile's softmax has the time
+// of the other's two products. The running maximum is moved (and O rescaled) only where a row's has
+// grown by more than 2^8.
+//
+// Where the query tiles are fewer than the SMs, the cache positions are cut into `splits` parts whose
+// results a second kernel joins in order.
+#include "kv4.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace bitnet {
+namespace {
+
+constexpr int THREADS = 544;
+constexpr int ROWS = 256;   // query rows of a block
+constexpr int TOK = 128;    // cache tokens of a step
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kSlack = 8.0f;  // log2 of how far a weight may exceed 1 before the maximum moves
+
+template <int D>
+struct Prompt {
+  static constexpr int W = D / 8;
+  static constexpr int BLK = 64 * D + 512;
+  static constexpr int Q_TILE = 128 * D * 2, K_STAGE = TOK * D * 2, V_STAGE = D * TOK * 2;
+  static constexpr int SMEM = 2 * Q_TILE + 2 * K_STAGE + 2 * V_STAGE + 1024;
+  static constexpr uint32_t IDESC_S = make_idesc_f16_f32(128, TOK), IDESC_O = make_idesc_f16_f32(128, D);
+};
+// tensor memory columns: scores (and weights over them) and outputs of the two tiles
+constexpr uint32_t TM_S = 0, TM_O = 256;
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// the codes in nibbles 0 and 4 of x, or 1 and 5, as exact fp16
+__device__ __forceinline__ uint32_t codes_even(uint32_t x) {
+  return hsub2((x & 0x000f000fu) | 0x64006400u, 0x64006400u);  // 1024 + c
+}
+__device__ __forceinline__ uint32_t codes_odd(uint32_t x) {
+  return hfma2((x & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd400d400u);  // (1024 + 16 c) / 16 - 64
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// byte offset of 16-byte chunk c (0..7) of row r in a 128-byte-swizzled K-major tile
+__device__ __forceinline__ uint32_t sw128(int r, int c) {
+  return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// What a block works on: query rows row0 .. row0 + rows of one sequence and head, and the pages that
+// any of them sees, page i being page i of the sequence, or i + skip from i = ns on.
+struct Item {
+  int b, h, row0, rows;
+  int np, ns, skip;
+  Kv4Seq s;
+};
+// a page's first position; past every query where there is no such page
+__device__ __forceinline__ int page_first(const Item& it, int i) {
+  return i >= it.np ? INT32_MAX - 2 * TOK : (i < it.ns ? i : i + it.skip) * kKvPage;
+}
+
+// Partials of a split call: for each item and part ROWS x D sums, ROWS maxima (log2), ROWS sums; and
+// for each item what it is.
+struct Parts {
+  float* sums;
+  int4* info;  // first packed row of the sequence, first query row, query rows (0: none), head
+  int splits;
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a, int done_rows, Parts parts) {
+  using P = Prompt<D>;
+  constexpr int W = P::W;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], q_full, all_done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int warp_sum[THREADS / 32];
+  __shared__ Item item_s;
+  __shared__ float row_c1[ROWS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  const uint32_t q_s = base, k_s = q_s + 2 * P::Q_TILE, v_s = k_s + 2 * P::K_STAGE;
+  bool bad = false;
+  pdl_launch_dependents();
+
+  // ---- which item: item x of a head is the x-th tile of all sequences, each one's last (longest) first
+  const int x = blockIdx.x / c.kv_heads, split = blockIdx.y;
+  {
+    const int per = (c.batch + THREADS - 1) / THREADS;
+    const int b0 = min((int)threadIdx.x * per, c.batch), b1 = min(b0 + per, c.batch);
+    const auto tiles_of = [&](const Kv4Seq& s) {
+      const int64_t r = (int64_t)s.n * a.share;
+      return r <= done_rows ? 0 : (int)((r + ROWS - 1) / ROWS);
+    };
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += tiles_of(kv4_sequence(c, b, &bad));
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    if (threadIdx.x == 0) {
+      item_s.rows = 0;
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&k_full[i], 4);
+        mbar_init(&v_full[i], 4);
+        mbar_init(&k_empty[i], 1);
+        mbar_init(&v_empty[i], 1);
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], 4);
+        mbar_init(&pv_done[i], 1);
+      }
+      mbar_init(&q_full, 8);
+      mbar_init(&all_done, 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+    int at = upto - mine;
+    for (int i = 0; i < warp; ++i) at += warp_sum[i];
+    if (x >= at && x < at + mine) {
+      for (int b = b0; b < b1; ++b) {
+        const Kv4Seq s = kv4_sequence(c, b, &bad);
+        const int t = tiles_of(s);
+        if (x < at + t) {
+          Item it;
+          it.b = b;
+          it.h = blockIdx.x % c.kv_heads;
+          it.s = s;
+          it.row0 = (t - 1 - (x - at)) * ROWS;
+          it.rows = min(ROWS, s.n * a.share - it.row0);
+          const int pos0 = s.len - s.n + it.row0 / a.share, pos1 = s.len - s.n + (it.row0 + it.rows - 1) / a.share;
+          const int low = (int)max((int64_t)0, (int64_t)pos0 - a.window + 1);
+          const int low_page = low / kKvPage, sink_pages = (min(a.sinks, low) + kKvPage - 1) / kKvPage;
+          it.ns = min(sink_pages, low_page);
+          it.skip = low_page - it.ns;
+          it.np = pos1 < 0 ? 0 : it.ns + pos1 / kKvPage + 1 - low_page;
+          item_s = it;
+          break;
+        }
+        at += t;
+      }
+    }
+  }
+  __syncthreads();
+  const Item it = item_s;
+  if (parts.splits > 1 && split == 0 && threadIdx.x == 0)
+    parts.info[blockIdx.x] = make_int4(it.s.q0, it.row0, it.rows, it.h);
+  if (it.rows == 0) {  // fewer items than the grid was made for
+    if (bad) record_device_error(kErrRange);
+    return;
+  }
+  if (warp == 16) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int all = (it.np + 1) / 2;  // steps of the item, then of this part of it
+  const int j0 = (int)((int64_t)all * split / parts.splits), j1 = (int)((int64_t)all * (split + 1) / parts.splits);
+  const int steps = j1 - j0;
+  bool abort = false;
+
+  if (warp < 8) {
+    // ================================ softmax ================================
+    const int tile = warp >> 2, quarter = warp & 3;
+    {  // the queries of both tiles, 32 rows a warp: W lanes a row, lane w the numbers w + W n
+      constexpr int RPI = 32 / W;  // rows at a time
+      const int w = lane % W;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32 / RPI; i0 += 4) {
+        float q[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = warp * 32 + (i0 + i) * RPI + lane / W, gr = it.row0 + r;
+          const int64_t at = (int64_t)(it.s.q0 + gr / a.share) * a.q_stride + (int64_t)(it.h * a.share + gr % a.share) * D + w;
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+            q[i][n] = r >= it.rows ? 0.0f
+                      : a.bf16     ? __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(a.q) + at + W * n) << 16)
+                                   : __ldg(static_cast<const float*>(a.q) + at + W * n);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = warp * 32 + (i0 + i) * RPI + lane / W;
+          float mx = 0.0f;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) mx = fmaxf(mx, fabsf(q[i][n]));
+#pragma unroll
+          for (int o = W / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          // q' = q 2^(13 - e), 2^e <= max |q| < 2^(e + 1); not below e = -100, and not for infinities
+          int e = (int)(__float_as_uint(mx) >> 23) - 127;
+          e = e == 128 ? 13 : max(e, -100);
+          const float up = __int_as_float((13 - e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
+          uint32_t f[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) f[n] = pack_half2(q[i][n] * up, q[i][n + 4] * up);
+          sts128(q_s + (r >> 7) * P::Q_TILE + (w >> 3) * (128 * 128) + sw128(r & 127, w & 7), f[0], f[1], f[2], f[3]);
+          // a factor of 0 would make NaN of a masked score
+          if (w == 0) row_c1[r] = fmaxf(fabsf(a.scale) * kLog2e * __int_as_float((e - 13 + 127) << 23), 1.17549435e-38f);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full);
+      mbar_wait_warp(&q_full, 0, &abort);
+    }
+    const int r = tile * 128 + quarter * 32 + lane, gr = it.row0 + r;
+    const bool there = r < it.rows;
+    const float c1 = row_c1[r];
+    const int pos = there ? it.s.len - it.s.n + gr / a.share : -1;
+    // of the warp's rows: the first position, and the last window's beginning (rows past the end follow the last)
+    const int last = min(it.rows, tile * 128 + quarter * 32 + 32) - 1;
+    const int pos_first = it.s.len - it.s.n + (it.row0 + tile * 128 + quarter * 32) / a.share;
+    const int64_t low_last = (int64_t)it.s.len - it.s.n + (it.row0 + max(last, 0)) / a.share - a.window + 1;
+    const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + TM_S + (uint32_t)(tile * 128);
+    const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + TM_O + (uint32_t)(tile * D);
+    float m = kNegInf, l = 0.0f;
+    for (int j = 0; j < steps; ++j) {
+      int hi[2], lo[2], sk[2];  // of the step's pages: columns x <= hi with x >= lo or x < sk are seen
+      bool whole = true;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int first = page_first(it, 2 * (j0 + j) + p);
+        hi[p] = pos - first;
+        lo[p] = (int)max((int64_t)INT32_MIN, (int64_t)hi[p] - a.window + 1);
+        sk[p] = max(a.sinks - first, 0);
+        whole &= first + kKvPage - 1 <= pos_first && (first >= low_last || first + kKvPage <= a.sinks);
+      }
+      if (!mbar_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort)) break;
+      tc_fence_after();
+      float mx = m;
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(ts + 32 * ch, v);
+        tmem_ld_wait();
+        if (whole) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
+        } else {
+          const int p = ch >> 1, x0 = 32 * (ch & 1);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (x0 + k <= hi[p] && (x0 + k >= lo[p] || x0 + k < sk[p])) mx = fmaxf(mx, __uint_as_float(v[k]));
+        }
+      }
+      // a row's first scores, or scores far above the maximum in use: move it
+      const bool far = mx > m && (m == kNegInf || c1 * (mx - m) > kSlack);
+      if (__any_sync(0xffffffffu, far)) {
+        const float f = m == kNegInf ? (mx == kNegInf ? 1.0f : 0.0f) : exp2_approx(c1 * (m - mx));
+        m = mx;
+        l *= f;
+        if (j > 0) {  // the scores of this step were computed after the last step's product with V
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(to + 32 * ch, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+            tmem_st_x32(to + 32 * ch, v);
+          }
+        }
+      }
+      const float off = m == kNegInf ? 0.0f : -c1 * m;
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t v[32], w[16];
+        tmem_ld_32x32b_x32(ts + 32 * ch, v);
+        tmem_ld_wait();
+        if (!whole) {
+          const int p = ch >> 1, x0 = 32 * (ch & 1);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!(x0 + k <= hi[p] && (x0 + k >= lo[p] || x0 + k < sk[p]))) v[k] = __float_as_uint(kNegInf);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float p0 = exp2_approx(fmaf(__uint_as_float(v[2 * k]), c1, off));
+          const float p1 = exp2_approx(fmaf(__uint_as_float(v[2 * k + 1]), c1, off));
+          l += p0 + p1;
+          w[k] = pack_half2(p0, p1);
+        }
+        tmem_st_x16(ts + 16 * ch, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[tile]);
+    }
+    if (steps > 0) mbar_wait_warp(&pv_done[tile], (uint32_t)(steps - 1) & 1u, &abort);
+    tc_fence_after();
+    {
+      const float norm = parts.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+      uint16_t* out = a.out + (int64_t)(it.s.q0 + gr / a.share) * a.out_stride + (int64_t)(it.h * a.share + gr % a.share) * D;
+      float* part = parts.splits > 1 ? parts.sums + ((int64_t)blockIdx.x * parts.splits + split) * (ROWS * (D + 2)) : nullptr;
+#pragma unroll
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t v[32];
+        if (steps > 0 && !abort) {
+          tmem_ld_32x32b_x32(to + 32 * ch, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0;
+        }
+        if (!there) continue;
+        if (part) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(part + r * D + 32 * ch + 4 * k) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * i]) * norm,
+                                                             __uint_as_float(v[8 * k + 2 * i + 1]) * norm);
+              y[i] = *reinterpret_cast<const uint32_t*>(&t);
+            }
+            *reinterpret_cast<uint4*>(out + 32 * ch + 8 * k) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      if (part && there) {
+        part[ROWS * D + r] = m * c1;
+        part[ROWS * (D + 1) + r] = l;
+      }
+    }
+    tc_fence_before();
+  } else if (warp < 16) {
+    // ================================ expansion ================================
+    const int ew = warp & 3;
+    const bool values = warp >= 12;
+    // a page's block of the item's head; the last page's again where there is no such page
+    const auto block = [&](int i) -> const uint8_t* { return kv4_block(c, it.b, [&] { const int k = min(i, it.np - 1); return k < it.ns ? k : k + it.skip; }(), it.h, P::BLK, &bad); };
+    if (!values) {
+      // 8 rows of all chunks (D = 128), or 16 of both (D = 64), a time: lane & 7 is the row of eight
+      constexpr int GROUPS = D == 128 ? 16 : 8, IT = GROUPS / 4;
+      const int row8 = lane & 7, chunk = D == 128 ? lane >> 3 : (lane >> 3) & 1, half = D == 128 ? 0 : lane >> 4;
+      uint4 code[IT];
+      uint2 par[IT];
+      const auto load = [&](int j) {
+        const uint8_t* blk[2] = {block(2 * (j0 + j)), block(2 * (j0 + j) + 1)};
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int row = D == 128 ? (ew + 4 * i) * 8 + row8 : (ew + 4 * i) * 16 + half * 8 + row8;  // of 128
+          const uint8_t* p = blk[row >> 6];
+          code[i] = __ldg(reinterpret_cast<const uint4*>(p + (row & 63) * (D / 2) + 16 * chunk));
+          par[i] = __ldg(reinterpret_cast<const uint2*>(p + kKvPage * D + (row & 63) * 8));
+        }
+      };
+      if (steps > 0) load(0);
+      for (int j = 0; j < steps; ++j) {
+        const int st = j & 1;
+        if (j >= 2 && !mbar_wait_warp(&k_empty[st], (uint32_t)(j / 2 - 1) & 1u, &abort)) break;
+        const uint32_t dst = k_s + st * P::K_STAGE;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int row = D == 128 ? (ew + 4 * i) * 8 + row8 : (ew + 4 * i) * 16 + half * 8 + row8;
+          const int t = (row & 64) + kv4_rho_inv(row & 63);
+          const uint32_t step = __byte_perm(par[i].x, 0, 0x1010);
+          uint32_t bs = __byte_perm(par[i].x, 0, 0x3232);
+          // a value vector of NaN acts through its key, so that a weight of 0 never meets a NaN
+          const uint32_t z = hsub2(par[i].y, par[i].y);
+          bs = hadd2(bs, hadd2(__byte_perm(z, 0, 0x1010), __byte_perm(z, 0, 0x3232)));
+          const uint32_t wd[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t up = wd[k] >> 8;
+            const int w = 4 * chunk + k;
+            sts128(dst + (w >> 3) * (TOK * 128) + sw128(t, w & 7), hfma2(codes_even(wd[k]), step, bs),
+                   hfma2(codes_odd(wd[k]), step, bs), hfma2(codes_even(up), step, bs), hfma2(codes_odd(up), step, bs));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[st]);
+        if (j + 1 < steps) load(j + 1);
+      }
+    } else {
+      // 8 tokens a lane, word w of each; 16 (D = 128) or 32 tokens a time
+      constexpr int TPI = 8 * (32 / W), IT = TOK / TPI / 4;
+      const int w = lane % W, grp = lane / W;
+      uint32_t code[IT][8], par[IT][8];
+      const auto load = [&](int j) {
+        const uint8_t* blk[2] = {block(2 * (j0 + j)), block(2 * (j0 + j) + 1)};
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int t0 = (ew + 4 * i) * TPI + 8 * grp;  // of 128; a multiple of 8
+          const uint8_t* p = blk[t0 >> 6];
+          const int first = page_first(it, 2 * (j0 + j) + (t0 >> 6)) + (t0 & 63);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int t = (t0 & 63) + k;
+            code[i][k] = __ldg(reinterpret_cast<const uint32_t*>(p + kKvPage * (D / 2) + t * (D / 2)) +
+                               (D == 128 && (k & 2) ? w ^ (W / 2) : w));
+            const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p + kKvPage * D + kv4_rho(t) * 8 + 4));
+            par[i][k] = first + k < it.s.len ? v : 0;  // no value where nothing is cached
+          }
+        }
+      };
+      if (steps > 0) load(0);
+      for (int j = 0; j < steps; ++j) {
+        const int st = j & 1;
+        if (j >= 2 && !mbar_wait_warp(&v_empty[st], (uint32_t)(j / 2 - 1) & 1u, &abort)) break;
+        const uint32_t dst = v_s + st * P::V_STAGE;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int t0 = (ew + 4 * i) * TPI + 8 * grp;
+          uint32_t step[4], bs[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            step[k] = __byte_perm(par[i][2 * k], par[i][2 * k + 1], 0x5410);
+            bs[k] = __byte_perm(par[i][2 * k], par[i][2 * k + 1], 0x7632);
+            const uint32_t z = hadd2(hsub2(step[k], step[k]), hsub2(bs[k], bs[k]));
+            uint32_t ok;  // all ones where finite
+            asm("set.eq.u32.f16x2 %0, %1, %2;" : "=r"(ok) : "r"(z), "r"(0u));
+            step[k] &= ok;
+            bs[k] &= ok;
+          }
+#pragma unroll
+          for (int by = 0; by < 4; ++by) {
+            uint32_t e[4], o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t u = __byte_perm(code[i][2 * k], code[i][2 * k + 1], 0x4400 + 0x1111 * by);
+              e[k] = hfma2(codes_even(u), step[k], bs[k]);
+              o[k] = hfma2(codes_odd(u), step[k], bs[k]);
+            }
+            const uint32_t at = dst + (t0 >> 6) * (D * 128);
+            const int d = w + W * 2 * by, ch = (t0 & 63) >> 3;
+            sts128(at + sw128(d, ch), e[0], e[1], e[2], e[3]);
+            sts128(at + sw128(d + W, ch), o[0], o[1], o[2], o[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[st]);
+        if (j + 1 < steps) load(j + 1);
+      }
+    }
+  } else if (lane == 0 && steps > 0) {
+    // ================================ MMA issue ================================
+    const uint64_t qd = make_sw128_kmajor_desc(q_s), kd = make_sw128_kmajor_desc(k_s), vd = make_sw128_kmajor_desc(v_s);
+    const auto scores = [&](int t, int j) {
+      const uint64_t ad = qd + (uint64_t)(t * (P::Q_TILE >> 4)), bd = kd + (uint64_t)((j & 1) * (P::K_STAGE >> 4));
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const uint64_t o = (uint64_t)((s >> 2) * ((128 * 128) >> 4) + (s & 3) * 2);
+        mma_f16_ss(tmem + TM_S + t * 128, ad + o, bd + o, P::IDESC_S, s > 0);
+      }
+      mma_commit(&s_full[t]);
+    };
+    const auto values = [&](int t, int j) {
+      const uint64_t bd = vd + (uint64_t)((j & 1) * (P::V_STAGE >> 4));
+#pragma unroll
+      for (int s = 0; s < TOK / 16; ++s)
+        mma_f16_ts(tmem + TM_O + t * D, tmem + TM_S + t * 128 + 8 * s,
+                   bd + (uint64_t)((s >> 2) * ((D * 128) >> 4) + (s & 3) * 2), P::IDESC_O, j > 0 || s > 0);
+      mma_commit(&pv_done[t]);
+    };
+    bool ok = mbar_wait(&q_full, 0, &abort) && mbar_wait(&k_full[0], 0, &abort);
+    if (ok) {
+      tc_fence_after();
+      scores(0, 0);
+      scores(1, 0);
+      mma_commit(&k_empty[0]);
+    }
+    for (int j = 0; ok && j < steps; ++j) {
+      ok = mbar_wait(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
+      for (int t = 0; ok && t < 2; ++t) {
+        ok = mbar_wait(&p_full[t], (uint32_t)j & 1u, &abort);
+        if (!ok) break;
+        tc_fence_after();
+        values(t, j);
+        if (t == 1) mma_commit(&v_empty[j & 1]);
+        if (j + 1 < steps) {
+          // the scores go where the weights lie that this product still reads
+          ok = (t || mbar_wait(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
+               mbar_wait(&pv_done[t], (uint32_t)j & 1u, &abort);
+          if (!ok) break;
+          tc_fence_after();
+          scores(t, j + 1);
+          if (t == 1) mma_commit(&k_empty[(j + 1) & 1]);
+        }
+      }
+    }
+    if (!ok) {  // what was issued ends before the tensor memory is given back
+      bool given_up = false;
+      mma_commit(&all_done);
+      mbar_wait(&all_done, 0, &given_up);
+    }
+  }
+  if (bad) record_device_error(kErrRange);
+  __syncwarp();
+  __syncthreads();
+  if (warp == 16) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of a split item, a warp a row.
+constexpr int JOIN_WARPS = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_prompt_join_kernel(Kv4Attn a, Parts parts) {
+  constexpr int E = D / 32;
+  pdl_wait();
+  const int4 info = parts.info[blockIdx.x];
+  const int r = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= info.z) return;
+  const float* part = parts.sums + (int64_t)blockIdx.x * parts.splits * (ROWS * (D + 2));
+  float mx = kNegInf;
+  for (int s = 0; s < parts.splits; ++s) mx = fmaxf(mx, part[(int64_t)s * (ROWS * (D + 2)) + ROWS * D + r]);
+  if (mx == kNegInf) mx = 0.0f;
+  float l = 0.0f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  for (int s = 0; s < parts.splits; ++s) {
+    const float* p = part + (int64_t)s * (ROWS * (D + 2));
+    const float f = exp2_approx(p[ROWS * D + r] - mx);
+    l = fmaf(p[ROWS * (D + 1) + r], f, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(p[r * D + E * lane + e], f, o[e]);
+  }
+  const float norm = l == 0.0f ? 0.0f : 1.0f / l;
+  const int gr = info.y + r;
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(info.x + gr / a.share) * a.out_stride +
+                       (int64_t)(info.w * a.share + gr % a.share) * D;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[E * lane + e] = __float2bfloat16_rn(o[e] * norm);
+}
+
+// items of a call, at most: tiles of all sequences for each head
+int64_t items_of(const Kv4& c, int share) {
+  const int64_t rows = (int64_t)c.total_q * share;
+  const int64_t tiles = rows / ROWS + c.batch;
+  return c.kv_heads * (c.batch == 1 ? (rows + ROWS - 1) / ROWS : tiles);
+}
+// Parts of an item: enough for every SM to have one, each of at least 4 steps.
+int splits_of(const Kv4& c, int share, int window) {
+  (void)window;
+  const int64_t items = items_of(c, share), steps = ((int64_t)c.max_kv + TOK - 1) / TOK;
+  int64_t s = 152 / (items < 1 ? 1 : items);
+  if (s > steps / 4) s = steps / 4;
+  return s < 1 ? 1 : (int)s;
+}
+
+template <int D>
+cudaError_t launch(const Kv4& c, const Kv4Attn& a, int done_rows, void* ws, cudaStream_t st) {
+  using P = Prompt<D>;
+  const int64_t items = items_of(c, a.share);
+  Parts parts{};
+  parts.splits = splits_of(c, a.share, a.window);
+  if (parts.splits > 1) {
+    parts.info = static_cast<int4*>(ws);
+    parts.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (items * 16 + 255) / 256 * 256);
+  }
+  cudaError_t e = cudaFuncSetAttribute(kv4_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
+  if (e != cudaSuccess) return e;
+  kv4_prompt_kernel<D><<<dim3((unsigned)items, (unsigned)parts.splits), THREADS, P::SMEM, st>>>(c, a, done_rows, parts);
+  if ((e = cudaGetLastError()) != cudaSuccess || parts.splits == 1) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)items, ROWS / JOIN_WARPS);
+  cfg.blockDim = dim3(32 * JOIN_WARPS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_prompt_join_kernel<D>, a, parts);
+}
+
+}  // namespace
+
+int64_t kv4_prompt_ws_bytes(const Kv4& c, int dim, int share) {
+  const int64_t items = items_of(c, share);
+  const int splits = splits_of(c, share, 0);
+  return splits == 1 ? 0 : (items * 16 + 255) / 256 * 256 + items * splits * ROWS * (dim + 2) * 4;
+}
+
+cudaError_t launch_kv4_prompt(const Kv4& c, int dim, const Kv4Attn& a, int done_rows, void* ws, cudaStream_t st) {
+  return dim == 128 ? launch<128>(c, a, done_rows, ws, st) : launch<64>(c, a, done_rows, ws, st);
+}
+
+cudaError_t read_clear_device_error_kv4_prompt(int* value) {
+  int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_device_error, sizeof(int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
+}
+
+}  // namespace bitnet
