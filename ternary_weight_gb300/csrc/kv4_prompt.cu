@@ -17,8 +17,8 @@
 // transposed on the way: a lane takes one word of 8 tokens, pairs them byte by byte, and stores 8
 // tokens of a dimension as 16 bytes.
 //
-// Roles (17 warps): 0-3 and 4-7 softmax of the two tiles, one row a thread; 8-11 keys; 12-15 values;
-// 16 issues the MMAs in the order  PV_A(j) S_A(j+1) PV_B(j) S_B(j+1): one tile's softmax has the time
+// Roles (16 warps): 0-3 and 4-7 softmax of the two tiles, one row a thread; 8-11 keys; 12-14 values;
+// 15 issues the MMAs in the order  PV_A(j) S_A(j+1) PV_B(j) S_B(j+1): one tile's softmax has the time
 // of the other's two products. The running maximum is moved (and O rescaled) only where a row's has
 // grown by more than 2^8.
 //
@@ -32,7 +32,7 @@
 namespace bitnet {
 namespace {
 
-constexpr int THREADS = 544;
+constexpr int THREADS = 512;
 constexpr int ROWS = 256;   // query rows of a block
 constexpr int TOK = 128;    // cache tokens of a step
 constexpr float kLog2e = 1.4426950408889634f;
@@ -61,6 +61,26 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
@@ -98,14 +118,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -180,7 +192,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       item_s.rows = 0;
       for (int i = 0; i < 2; ++i) {
         mbar_init(&k_full[i], 4);
-        mbar_init(&v_full[i], 4);
+        mbar_init(&v_full[i], 3);
         mbar_init(&k_empty[i], 1);
         mbar_init(&v_empty[i], 1);
         mbar_init(&s_full[i], 1);
@@ -226,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     if (bad) record_device_error(kErrRange);
     return;
   }
-  if (warp == 16) {
+  if (warp == 15) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
@@ -242,38 +254,61 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
   if (warp < 8) {
     // ================================ softmax ================================
     const int tile = warp >> 2, quarter = warp & 3;
-    {  // the queries of both tiles, 32 rows a warp: W lanes a row, lane w the numbers w + W n
+    {  // the queries of both tiles, 32 rows a warp: W lanes a row, 8 dimensions a lane
       constexpr int RPI = 32 / W;  // rows at a time
-      const int w = lane % W;
+      const int w = lane % W;      // dimensions 8 w .. 8 w + 7: nibble n = w / (W / 8) of words 8 w % W ..
+      const int n = w / (W / 8), word0 = 8 * w % W;
 #pragma unroll 1
-      for (int i0 = 0; i0 < 32 / RPI; i0 += 4) {
-        float q[4][8];
+      for (int i0 = 0; i0 < 32 / RPI; i0 += 8) {
+        float q[8][8];
+        int64_t at[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = warp * 32 + (i0 + i) * RPI + lane / W, gr = it.row0 + r;
-          const int64_t at = (int64_t)(it.s.q0 + gr / a.share) * a.q_stride + (int64_t)(it.h * a.share + gr % a.share) * D + w;
+        for (int i = 0; i < 8; ++i) {  // rows past the end read the last one
+          const int r = min(warp * 32 + (i0 + i) * RPI + lane / W, it.rows - 1), gr = it.row0 + r;
+          at[i] = (int64_t)(it.s.q0 + gr / a.share) * a.q_stride + (int64_t)(it.h * a.share + gr % a.share) * D + 8 * w;
+        }
+        if (a.bf16) {
+          uint4 u[8];
 #pragma unroll
-          for (int n = 0; n < 8; ++n)
-            q[i][n] = r >= it.rows ? 0.0f
-                      : a.bf16     ? __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(a.q) + at + W * n) << 16)
-                                   : __ldg(static_cast<const float*>(a.q) + at + W * n);
+          for (int i = 0; i < 8; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at[i]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[i][2 * k] = __uint_as_float(x[k] << 16), q[i][2 * k + 1] = __uint_as_float(x[k] & 0xffff0000u);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at[i]);
+            const float4 x = __ldg(p), y = __ldg(p + 1);
+            q[i][0] = x.x, q[i][1] = x.y, q[i][2] = x.z, q[i][3] = x.w;
+            q[i][4] = y.x, q[i][5] = y.y, q[i][6] = y.z, q[i][7] = y.w;
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const int r = warp * 32 + (i0 + i) * RPI + lane / W;
           float mx = 0.0f;
 #pragma unroll
-          for (int n = 0; n < 8; ++n) mx = fmaxf(mx, fabsf(q[i][n]));
+          for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(q[i][k]));
 #pragma unroll
           for (int o = W / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
           // q' = q 2^(13 - e), 2^e <= max |q| < 2^(e + 1); not below e = -100, and not for infinities
           int e = (int)(__float_as_uint(mx) >> 23) - 127;
           e = e == 128 ? 13 : max(e, -100);
           const float up = __int_as_float((13 - e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
-          uint32_t f[4];
+          // nibbles n and n + 4 of a word lie side by side: half of the lane's numbers go to the lane
+          // that has the other nibble, half of that one's come here
+          const bool high = n >= 4;
 #pragma unroll
-          for (int n = 0; n < 4; ++n) f[n] = pack_half2(q[i][n] * up, q[i][n + 4] * up);
-          sts128(q_s + (r >> 7) * P::Q_TILE + (w >> 3) * (128 * 128) + sw128(r & 127, w & 7), f[0], f[1], f[2], f[3]);
+          for (int k = 0; k < 4; ++k) {
+            const float mine = high ? q[i][4 + k] : q[i][k], give = high ? q[i][k] : q[i][4 + k];
+            const float got = __shfl_xor_sync(0xffffffffu, give, W / 2);
+            const uint32_t f = pack_half2((high ? got : mine) * up, (high ? mine : got) * up);
+            const int word = word0 + k + (high ? 4 : 0);
+            st_shared_u32(q_s + (r >> 7) * P::Q_TILE + (word >> 3) * (128 * 128) + sw128(r & 127, word & 7) + 4 * (n & 3), f);
+          }
           // a factor of 0 would make NaN of a masked score
           if (w == 0) row_c1[r] = fmaxf(fabsf(a.scale) * kLog2e * __int_as_float((e - 13 + 127) << 23), 1.17549435e-38f);
         }
@@ -307,22 +342,22 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       }
       if (!mbar_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort)) break;
       tc_fence_after();
-      float mx = m;
+      float mx4[4] = {m, m, m, m};
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(ts + 32 * ch, v);
+      for (int p = 0; p < 2; ++p) {  // a page's columns
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(ts + 64 * p, v[0]);
+        tmem_ld_32x32b_x32(ts + 64 * p + 32, v[1]);
         tmem_ld_wait();
-        if (whole) {
+        if (!whole) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
-        } else {
-          const int p = ch >> 1, x0 = 32 * (ch & 1);
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (x0 + k <= hi[p] && (x0 + k >= lo[p] || x0 + k < sk[p])) mx = fmaxf(mx, __uint_as_float(v[k]));
+          for (int k = 0; k < 64; ++k)
+            if (!(k <= hi[p] && (k >= lo[p] || k < sk[p]))) v[k >> 5][k & 31] = __float_as_uint(kNegInf);
         }
+#pragma unroll
+        for (int k = 0; k < 64; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(v[k >> 5][k & 31]));
       }
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       // a row's first scores, or scores far above the maximum in use: move it
       const bool far = mx > m && (m == kNegInf || c1 * (mx - m) > kSlack);
       if (__any_sync(0xffffffffu, far)) {
@@ -342,26 +377,31 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         }
       }
       const float off = m == kNegInf ? 0.0f : -c1 * m;
+      const uint64_t c2 = f2pack(c1, c1), off2 = f2pack(off, off);
+      uint64_t l2[2] = {0, 0};
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t v[32], w[16];
-        tmem_ld_32x32b_x32(ts + 32 * ch, v);
+      for (int p = 0; p < 2; ++p) {
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(ts + 64 * p, v[0]);
+        tmem_ld_32x32b_x32(ts + 64 * p + 32, v[1]);
         tmem_ld_wait();
         if (!whole) {
-          const int p = ch >> 1, x0 = 32 * (ch & 1);
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (!(x0 + k <= hi[p] && (x0 + k >= lo[p] || x0 + k < sk[p]))) v[k] = __float_as_uint(kNegInf);
+          for (int k = 0; k < 64; ++k)
+            if (!(k <= hi[p] && (k >= lo[p] || k < sk[p]))) v[k >> 5][k & 31] = __float_as_uint(kNegInf);
         }
+        uint32_t w[32];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float p0 = exp2_approx(fmaf(__uint_as_float(v[2 * k]), c1, off));
-          const float p1 = exp2_approx(fmaf(__uint_as_float(v[2 * k + 1]), c1, off));
-          l += p0 + p1;
+        for (int k = 0; k < 32; ++k) {
+          const float2 t = f2unpack(fma2(f2pack(__uint_as_float(v[k >> 4][2 * (k & 15)]), __uint_as_float(v[k >> 4][2 * (k & 15) + 1])), c2, off2));
+          const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
+          l2[k & 1] = add2(l2[k & 1], f2pack(p0, p1));
           w[k] = pack_half2(p0, p1);
         }
-        tmem_st_x16(ts + 16 * ch, w);
+        tmem_st_x32(ts + 32 * p, w);
       }
+      const float2 la = f2unpack(add2(l2[0], l2[1]));
+      l += la.x + la.y;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -408,12 +448,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       }
     }
     tc_fence_before();
-  } else if (warp < 16) {
+  } else if (warp < 15) {
     // ================================ expansion ================================
     const int ew = warp & 3;
     const bool values = warp >= 12;
-    // a page's block of the item's head; the last page's again where there is no such page
-    const auto block = [&](int i) -> const uint8_t* { return kv4_block(c, it.b, [&] { const int k = min(i, it.np - 1); return k < it.ns ? k : k + it.skip; }(), it.h, P::BLK, &bad); };
+    // a page's id (the last page's again where there is no such page), asked for a step before its codes
+    const auto page_id = [&](int i) {
+      const int k = min(i, it.np - 1);
+      return __ldg(c.page_table + (int64_t)it.b * c.max_pages + (k < it.ns ? k : k + it.skip));
+    };
+    const auto block = [&](int id) -> const uint8_t* {
+      if (id < 0 || id >= c.n_pages) bad = true, id = 0;
+      return c.pages + ((int64_t)id * c.kv_heads + it.h) * P::BLK;
+    };
+    int id0 = 0, id1 = 0;
+    if (steps > 0) id0 = page_id(2 * j0), id1 = page_id(2 * j0 + 1);
     if (!values) {
       // 8 rows of all chunks (D = 128), or 16 of both (D = 64), a time: lane & 7 is the row of eight
       constexpr int GROUPS = D == 128 ? 16 : 8, IT = GROUPS / 4;
@@ -421,7 +470,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       uint4 code[IT];
       uint2 par[IT];
       const auto load = [&](int j) {
-        const uint8_t* blk[2] = {block(2 * (j0 + j)), block(2 * (j0 + j) + 1)};
+        const uint8_t* blk[2] = {block(id0), block(id1)};
+        id0 = page_id(2 * (j0 + j) + 2), id1 = page_id(2 * (j0 + j) + 3);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const int row = D == 128 ? (ew + 4 * i) * 8 + row8 : (ew + 4 * i) * 16 + half * 8 + row8;  // of 128
@@ -459,15 +509,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         if (j + 1 < steps) load(j + 1);
       }
     } else {
-      // 8 tokens a lane, word w of each; 16 (D = 128) or 32 tokens a time
-      constexpr int TPI = 8 * (32 / W), IT = TOK / TPI / 4;
+      // 8 tokens a lane, word w of each; 16 (D = 128) or 32 tokens a time, in turn over three warps
+      constexpr int TPI = 8 * (32 / W), GROUPS = TOK / TPI, IT = (GROUPS + 2) / 3;
       const int w = lane % W, grp = lane / W;
       uint32_t code[IT][8], par[IT][8];
       const auto load = [&](int j) {
-        const uint8_t* blk[2] = {block(2 * (j0 + j)), block(2 * (j0 + j) + 1)};
+        const uint8_t* blk[2] = {block(id0), block(id1)};
+        id0 = page_id(2 * (j0 + j) + 2), id1 = page_id(2 * (j0 + j) + 3);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-          const int t0 = (ew + 4 * i) * TPI + 8 * grp;  // of 128; a multiple of 8
+          if (ew + 3 * i >= GROUPS) break;
+          const int t0 = (ew + 3 * i) * TPI + 8 * grp;  // of 128; a multiple of 8
           const uint8_t* p = blk[t0 >> 6];
           const int first = page_first(it, 2 * (j0 + j) + (t0 >> 6)) + (t0 & 63);
 #pragma unroll
@@ -487,7 +539,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         const uint32_t dst = v_s + st * P::V_STAGE;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-          const int t0 = (ew + 4 * i) * TPI + 8 * grp;
+          if (ew + 3 * i >= GROUPS) break;
+          const int t0 = (ew + 3 * i) * TPI + 8 * grp;
           uint32_t step[4], bs[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -575,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
   if (bad) record_device_error(kErrRange);
   __syncwarp();
   __syncthreads();
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == 15) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of a split item, a warp a row.
