@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
-      mbar_wait_warp(&q_full, 0, &abort);
+      kv4_wait_warp(&q_full, 0, &abort);
     }
     const int r = tile * 128 + quarter * 32 + lane, gr = it.row0 + r;
     const bool there = r < it.rows;
@@ -340,20 +340,29 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         sk[p] = max(a.sinks - first, 0);
         whole &= first + kKvPage - 1 <= pos_first && (first >= low_last || first + kKvPage <= a.sinks);
       }
-      if (!mbar_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort)) break;
+      if (!kv4_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort)) break;
       tc_fence_after();
-      float mx4[4] = {m, m, m, m};
+      if (!whole) {  // what a row does not see becomes -inf in place, 32 columns at a time
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          const int x0 = 32 * (ch & 1), h = hi[ch >> 1] - x0, b = lo[ch >> 1] - x0, k0 = sk[ch >> 1] - x0;
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(ts + 32 * ch, v);
+          tmem_ld_wait();
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {  // a page's columns
+          for (int k = 0; k < 32; ++k)
+            if (k > h || (k < b && k >= k0)) v[k] = __float_as_uint(kNegInf);
+          tmem_st_x32(ts + 32 * ch, v);
+        }
+        tmem_st_wait();
+      }
+      float mx4[4] = {m, m, m, m};
+#pragma unroll 1
+      for (int p = 0; p < 2; ++p) {
         uint32_t v[2][32];
         tmem_ld_32x32b_x32(ts + 64 * p, v[0]);
         tmem_ld_32x32b_x32(ts + 64 * p + 32, v[1]);
         tmem_ld_wait();
-        if (!whole) {
-#pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (!(k <= hi[p] && (k >= lo[p] || k < sk[p]))) v[k >> 5][k & 31] = __float_as_uint(kNegInf);
-        }
 #pragma unroll
         for (int k = 0; k < 64; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(v[k >> 5][k & 31]));
       }
@@ -365,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         m = mx;
         l *= f;
         if (j > 0) {  // the scores of this step were computed after the last step's product with V
-#pragma unroll
+#pragma unroll 1
           for (int ch = 0; ch < D / 32; ++ch) {
             uint32_t v[32];
             tmem_ld_32x32b_x32(to + 32 * ch, v);
@@ -379,17 +388,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       const float off = m == kNegInf ? 0.0f : -c1 * m;
       const uint64_t c2 = f2pack(c1, c1), off2 = f2pack(off, off);
       uint64_t l2[2] = {0, 0};
-#pragma unroll
+#pragma unroll 1
       for (int p = 0; p < 2; ++p) {
         uint32_t v[2][32];
         tmem_ld_32x32b_x32(ts + 64 * p, v[0]);
         tmem_ld_32x32b_x32(ts + 64 * p + 32, v[1]);
         tmem_ld_wait();
-        if (!whole) {
-#pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (!(k <= hi[p] && (k >= lo[p] || k < sk[p]))) v[k >> 5][k & 31] = __float_as_uint(kNegInf);
-        }
         uint32_t w[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
@@ -407,13 +411,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[tile]);
     }
-    if (steps > 0) mbar_wait_warp(&pv_done[tile], (uint32_t)(steps - 1) & 1u, &abort);
+    if (steps > 0) kv4_wait_warp(&pv_done[tile], (uint32_t)(steps - 1) & 1u, &abort);
     tc_fence_after();
     {
       const float norm = parts.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
       uint16_t* out = a.out + (int64_t)(it.s.q0 + gr / a.share) * a.out_stride + (int64_t)(it.h * a.share + gr % a.share) * D;
       float* part = parts.splits > 1 ? parts.sums + ((int64_t)blockIdx.x * parts.splits + split) * (ROWS * (D + 2)) : nullptr;
-#pragma unroll
+#pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t v[32];
         if (steps > 0 && !abort) {
@@ -450,45 +454,44 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     tc_fence_before();
   } else if (warp < 15) {
     // ================================ expansion ================================
-    const int ew = warp & 3;
-    const bool values = warp >= 12;
-    // a page's id (the last page's again where there is no such page), asked for a step before its codes
+    const int pages = 2 * steps;
+    // a page's id (the last page's again where there is no such page), asked for ahead of its codes
     const auto page_id = [&](int i) {
-      const int k = min(i, it.np - 1);
+      const int k = min(2 * j0 + i, it.np - 1);
       return __ldg(c.page_table + (int64_t)it.b * c.max_pages + (k < it.ns ? k : k + it.skip));
     };
     const auto block = [&](int id) -> const uint8_t* {
       if (id < 0 || id >= c.n_pages) bad = true, id = 0;
       return c.pages + ((int64_t)id * c.kv_heads + it.h) * P::BLK;
     };
-    int id0 = 0, id1 = 0;
-    if (steps > 0) id0 = page_id(2 * j0), id1 = page_id(2 * j0 + 1);
-    if (!values) {
-      // 8 rows of all chunks (D = 128), or 16 of both (D = 64), a time: lane & 7 is the row of eight
-      constexpr int GROUPS = D == 128 ? 16 : 8, IT = GROUPS / 4;
-      const int row8 = lane & 7, chunk = D == 128 ? lane >> 3 : (lane >> 3) & 1, half = D == 128 ? 0 : lane >> 4;
-      uint4 code[IT];
-      uint2 par[IT];
-      const auto load = [&](int j) {
-        const uint8_t* blk[2] = {block(id0), block(id1)};
-        id0 = page_id(2 * (j0 + j) + 2), id1 = page_id(2 * (j0 + j) + 3);
+    if (pages > 0 && warp < 12) {
+      // keys, a page at a time: 8 rows of all chunks (D = 128), or 16 of both (D = 64), a warp and unit;
+      // lane & 7 is the row of eight, so that 8 lanes store to 8 rows
+      constexpr int U = D == 128 ? 2 : 1;
+      const int ew = warp - 8, row8 = lane & 7, chunk = D == 128 ? lane >> 3 : (lane >> 3) & 1;
+      const int row0 = D == 128 ? ew * 8 + row8 : ew * 16 + (lane >> 4) * 8 + row8;  // and + 32 in the second unit
+      uint4 code[U], code_n[U];
+      uint2 par[U], par_n[U];
+      const auto load = [&](int id, uint4(&cd)[U], uint2(&pr)[U]) {
+        const uint8_t* p = block(id);
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          const int row = D == 128 ? (ew + 4 * i) * 8 + row8 : (ew + 4 * i) * 16 + half * 8 + row8;  // of 128
-          const uint8_t* p = blk[row >> 6];
-          code[i] = __ldg(reinterpret_cast<const uint4*>(p + (row & 63) * (D / 2) + 16 * chunk));
-          par[i] = __ldg(reinterpret_cast<const uint2*>(p + kKvPage * D + (row & 63) * 8));
+        for (int i = 0; i < U; ++i) {
+          cd[i] = __ldg(reinterpret_cast<const uint4*>(p + (row0 + 32 * i) * (D / 2) + 16 * chunk));
+          pr[i] = __ldg(reinterpret_cast<const uint2*>(p + kKvPage * D + (row0 + 32 * i) * 8));
         }
       };
-      if (steps > 0) load(0);
-      for (int j = 0; j < steps; ++j) {
-        const int st = j & 1;
-        if (j >= 2 && !mbar_wait_warp(&k_empty[st], (uint32_t)(j / 2 - 1) & 1u, &abort)) break;
+      load(page_id(0), code, par);
+      int id = page_id(1);
+#pragma unroll 1
+      for (int pg = 0; pg < pages; ++pg) {
+        load(id, code_n, par_n);
+        id = page_id(pg + 2);
+        const int st = (pg >> 1) & 1;
+        if (pg >= 4 && !(pg & 1) && !kv4_wait_warp(&k_empty[st], (uint32_t)((pg >> 2) - 1) & 1u, &abort)) break;
         const uint32_t dst = k_s + st * P::K_STAGE;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          const int row = D == 128 ? (ew + 4 * i) * 8 + row8 : (ew + 4 * i) * 16 + half * 8 + row8;
-          const int t = (row & 64) + kv4_rho_inv(row & 63);
+        for (int i = 0; i < U; ++i) {
+          const int t = 64 * (pg & 1) + kv4_rho_inv(row0 + 32 * i);
           const uint32_t step = __byte_perm(par[i].x, 0, 0x1010);
           uint32_t bs = __byte_perm(par[i].x, 0, 0x3232);
           // a value vector of NaN acts through its key, so that a weight of 0 never meets a NaN
@@ -502,75 +505,77 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
             sts128(dst + (w >> 3) * (TOK * 128) + sw128(t, w & 7), hfma2(codes_even(wd[k]), step, bs),
                    hfma2(codes_odd(wd[k]), step, bs), hfma2(codes_even(up), step, bs), hfma2(codes_odd(up), step, bs));
           }
+          code[i] = code_n[i];
+          par[i] = par_n[i];
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[st]);
-        if (j + 1 < steps) load(j + 1);
+        if (pg & 1) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[st]);
+        }
       }
-    } else {
-      // 8 tokens a lane, word w of each; 16 (D = 128) or 32 tokens a time, in turn over three warps
-      constexpr int TPI = 8 * (32 / W), GROUPS = TOK / TPI, IT = (GROUPS + 2) / 3;
-      const int w = lane % W, grp = lane / W;
-      uint32_t code[IT][8], par[IT][8];
-      const auto load = [&](int j) {
-        const uint8_t* blk[2] = {block(id0), block(id1)};
-        id0 = page_id(2 * (j0 + j) + 2), id1 = page_id(2 * (j0 + j) + 3);
+    } else if (pages > 0) {
+      // values: word w of 8 tokens a lane, 16 (D = 128) or 32 tokens a unit; the units of all pages go to
+      // the three warps in turn
+      constexpr int TPU = 8 * (32 / W), UPP = kKvPage / TPU;  // tokens of a unit, units of a page
+      const int w = lane % W, grp = lane / W, units = UPP * pages;
+      uint32_t code[8], par[8], code_n[8], par_n[8];
+      const auto load = [&](int u, int id, uint32_t(&cd)[8], uint32_t(&pr)[8]) {
+        const int t0 = (u % UPP) * TPU + 8 * grp, first = page_first(it, 2 * j0 + u / UPP) + t0;
+        const uint8_t* p = block(id) + kKvPage * (D / 2) + t0 * (D / 2);
+        const uint8_t* q = block(id) + kKvPage * D + t0 * 8 + 4;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          if (ew + 3 * i >= GROUPS) break;
-          const int t0 = (ew + 3 * i) * TPI + 8 * grp;  // of 128; a multiple of 8
-          const uint8_t* p = blk[t0 >> 6];
-          const int first = page_first(it, 2 * (j0 + j) + (t0 >> 6)) + (t0 & 63);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int t = (t0 & 63) + k;
-            code[i][k] = __ldg(reinterpret_cast<const uint32_t*>(p + kKvPage * (D / 2) + t * (D / 2)) +
-                               (D == 128 && (k & 2) ? w ^ (W / 2) : w));
-            const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p + kKvPage * D + kv4_rho(t) * 8 + 4));
-            par[i][k] = first + k < it.s.len ? v : 0;  // no value where nothing is cached
-          }
+        for (int k = 0; k < 8; ++k) {
+          cd[k] = __ldg(reinterpret_cast<const uint32_t*>(p + k * (D / 2)) + (D == 128 && (k & 2) ? w ^ (W / 2) : w));
+          const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(q + kv4_rho(k) * 8));
+          pr[k] = first + k < it.s.len ? v : 0;  // no value where nothing is cached
         }
       };
-      if (steps > 0) load(0);
-      for (int j = 0; j < steps; ++j) {
-        const int st = j & 1;
-        if (j >= 2 && !mbar_wait_warp(&v_empty[st], (uint32_t)(j / 2 - 1) & 1u, &abort)) break;
-        const uint32_t dst = v_s + st * P::V_STAGE;
+      int u = warp - 12;
+      load(u, page_id(u / UPP), code, par);
+      int id = page_id((u + 3) / UPP), done = -1;  // the last step whose place was waited for
+#pragma unroll 1
+      for (; u < units; u += 3) {
+        load(min(u + 3, units - 1), id, code_n, par_n);
+        id = page_id((u + 6) / UPP);
+        const int j = u / (2 * UPP), st = j & 1;
+        if (j != done) {
+          done = j;
+          if (j >= 2 && !kv4_wait_warp(&v_empty[st], (uint32_t)(j / 2 - 1) & 1u, &abort)) break;
+        }
+        const uint32_t at = v_s + st * P::V_STAGE + ((u / UPP) & 1) * (D * 128);
+        const int ch = ((u % UPP) * TPU >> 3) + grp;
+        uint32_t step[4], bs[4];
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          if (ew + 3 * i >= GROUPS) break;
-          const int t0 = (ew + 3 * i) * TPI + 8 * grp;
-          uint32_t step[4], bs[4];
+        for (int k = 0; k < 4; ++k) {
+          step[k] = __byte_perm(par[2 * k], par[2 * k + 1], 0x5410);
+          bs[k] = __byte_perm(par[2 * k], par[2 * k + 1], 0x7632);
+          const uint32_t z = hadd2(hsub2(step[k], step[k]), hsub2(bs[k], bs[k]));
+          uint32_t ok;  // all ones where finite
+          asm("set.eq.u32.f16x2 %0, %1, %2;" : "=r"(ok) : "r"(z), "r"(0u));
+          step[k] &= ok;
+          bs[k] &= ok;
+        }
+#pragma unroll
+        for (int by = 0; by < 4; ++by) {
+          uint32_t e[4], o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            step[k] = __byte_perm(par[i][2 * k], par[i][2 * k + 1], 0x5410);
-            bs[k] = __byte_perm(par[i][2 * k], par[i][2 * k + 1], 0x7632);
-            const uint32_t z = hadd2(hsub2(step[k], step[k]), hsub2(bs[k], bs[k]));
-            uint32_t ok;  // all ones where finite
-            asm("set.eq.u32.f16x2 %0, %1, %2;" : "=r"(ok) : "r"(z), "r"(0u));
-            step[k] &= ok;
-            bs[k] &= ok;
+            const uint32_t x = __byte_perm(code[2 * k], code[2 * k + 1], 0x4400 + 0x1111 * by);
+            e[k] = hfma2(codes_even(x), step[k], bs[k]);
+            o[k] = hfma2(codes_odd(x), step[k], bs[k]);
           }
-#pragma unroll
-          for (int by = 0; by < 4; ++by) {
-            uint32_t e[4], o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t u = __byte_perm(code[i][2 * k], code[i][2 * k + 1], 0x4400 + 0x1111 * by);
-              e[k] = hfma2(codes_even(u), step[k], bs[k]);
-              o[k] = hfma2(codes_odd(u), step[k], bs[k]);
-            }
-            const uint32_t at = dst + (t0 >> 6) * (D * 128);
-            const int d = w + W * 2 * by, ch = (t0 & 63) >> 3;
-            sts128(at + sw128(d, ch), e[0], e[1], e[2], e[3]);
-            sts128(at + sw128(d + W, ch), o[0], o[1], o[2], o[3]);
-          }
+          const int d = w + W * 2 * by;
+          sts128(at + sw128(d, ch), e[0], e[1], e[2], e[3]);
+          sts128(at + sw128(d + W, ch), o[0], o[1], o[2], o[3]);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_full[st]);
-        if (j + 1 < steps) load(j + 1);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) code[k] = code_n[k], par[k] = par_n[k];
+        if (u + 3 >= 2 * UPP * (j + 1)) {  // this warp's last unit of the step
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_full[st]);
+        }
       }
     }
   } else if (lane == 0 && steps > 0) {
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
                    bd + (uint64_t)((s >> 2) * ((D * 128) >> 4) + (s & 3) * 2), P::IDESC_O, j > 0 || s > 0);
       mma_commit(&pv_done[t]);
     };
-    bool ok = mbar_wait(&q_full, 0, &abort) && mbar_wait(&k_full[0], 0, &abort);
+    bool ok = kv4_wait(&q_full, 0, &abort) && kv4_wait(&k_full[0], 0, &abort);
     if (ok) {
       tc_fence_after();
       scores(0, 0);
@@ -601,17 +606,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       mma_commit(&k_empty[0]);
     }
     for (int j = 0; ok && j < steps; ++j) {
-      ok = mbar_wait(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
+      ok = kv4_wait(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
       for (int t = 0; ok && t < 2; ++t) {
-        ok = mbar_wait(&p_full[t], (uint32_t)j & 1u, &abort);
+        ok = kv4_wait(&p_full[t], (uint32_t)j & 1u, &abort);
         if (!ok) break;
         tc_fence_after();
         values(t, j);
         if (t == 1) mma_commit(&v_empty[j & 1]);
         if (j + 1 < steps) {
           // the scores go where the weights lie that this product still reads
-          ok = (t || mbar_wait(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
-               mbar_wait(&pv_done[t], (uint32_t)j & 1u, &abort);
+          ok = (t || kv4_wait(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
+               kv4_wait(&pv_done[t], (uint32_t)j & 1u, &abort);
           if (!ok) break;
           tc_fence_after();
           scores(t, j + 1);
@@ -622,7 +627,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     if (!ok) {  // what was issued ends before the tensor memory is given back
       bool given_up = false;
       mma_commit(&all_done);
-      mbar_wait(&all_done, 0, &given_up);
+      kv4_wait(&all_done, 0, &given_up);
     }
   }
   if (bad) record_device_error(kErrRange);
