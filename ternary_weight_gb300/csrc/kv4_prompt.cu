@@ -17,8 +17,8 @@
 // transposed on the way: a lane takes one word of 8 tokens, pairs them byte by byte, and stores 8
 // tokens of a dimension as 16 bytes.
 //
-// Roles (16 warps): 0-3 and 4-7 softmax of the two tiles, one row a thread; 8-11 keys; 12-14 values;
-// 15 issues the MMAs in the order  PV_A(j) S_A(j+1) PV_B(j) S_B(j+1): one tile's softmax has the time
+// Roles (24 warps): 0-7 and 8-15 softmax of the two tiles, half a row (one page's columns) a thread;
+// 16-19 keys; 20-22 values; 23 issues the MMAs in the order  PV_A(j) S_A(j+1) PV_B(j) S_B(j+1): one tile's softmax has the time
 // of the other's two products. The running maximum is moved (and O rescaled) only where a row's has
 // grown by more than 2^8.
 //
@@ -32,7 +32,7 @@
 namespace bitnet {
 namespace {
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 768;
 constexpr int ROWS = 256;   // query rows of a block
 constexpr int TOK = 128;    // cache tokens of a step
 constexpr float kLog2e = 1.4426950408889634f;
@@ -120,6 +120,14 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -133,10 +141,14 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// x / d for x < 512, 1 <= d <= 128, with m = ceil(65536 / d)
+__device__ __forceinline__ int small_div(int x, uint32_t m) { return (int)(((uint32_t)x * m) >> 16); }
+
 // What a block works on: query rows row0 .. row0 + rows of one sequence and head, and the pages that
 // any of them sees, page i being page i of the sequence, or i + skip from i = ns on.
 struct Item {
   int b, h, row0, rows;
+  int tok0, head0;  // token and shared head of row0
   int np, ns, skip;
   Kv4Seq s;
 };
@@ -145,7 +157,7 @@ __device__ __forceinline__ int page_first(const Item& it, int i) {
   return i >= it.np ? INT32_MAX - 2 * TOK : (i < it.ns ? i : i + it.skip) * kKvPage;
 }
 
-// Partials of a split call: for each item and part ROWS x D sums, ROWS maxima (log2), ROWS sums; and
+// Partials of a split call: for each item (tile x heads + head) and part ROWS x D sums, ROWS maxima (log2), ROWS sums; and
 // for each item what it is.
 struct Parts {
   float* sums;
@@ -154,7 +166,7 @@ struct Parts {
 };
 
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a, int done_rows, Parts parts) {
+__global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a, int done_rows, uint32_t share_m, Parts parts) {
   using P = Prompt<D>;
   constexpr int W = P::W;
   extern __shared__ uint8_t smem_raw[];
@@ -163,7 +175,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
   __shared__ uint32_t tmem_slot;
   __shared__ int warp_sum[THREADS / 32];
   __shared__ Item item_s;
-  __shared__ float row_c1[ROWS];
+  __shared__ float row_c1[ROWS], row_x[2][2][ROWS];  // the halves' maxima (then sums), by step parity
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t q_s = base, k_s = q_s + 2 * P::Q_TILE, v_s = k_s + 2 * P::K_STAGE;
@@ -172,6 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
 
   // ---- which item: item x of a head is the x-th tile of all sequences, each one's last (longest) first
   const int x = blockIdx.x / c.kv_heads, split = blockIdx.y;
+  const int64_t item_no = blockIdx.x;
   {
     const int per = (c.batch + THREADS - 1) / THREADS;
     const int b0 = min((int)threadIdx.x * per, c.batch), b1 = min(b0 + per, c.batch);
@@ -196,10 +209,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         mbar_init(&k_empty[i], 1);
         mbar_init(&v_empty[i], 1);
         mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[i], 4);
+        mbar_init(&p_full[i], 8);
         mbar_init(&pv_done[i], 1);
       }
-      mbar_init(&q_full, 8);
+      mbar_init(&q_full, 16);
       mbar_init(&all_done, 1);
       fence_mbar_init();
     }
@@ -213,11 +226,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         if (x < at + t) {
           Item it;
           it.b = b;
-          it.h = blockIdx.x % c.kv_heads;
+          it.h = blockIdx.x - x * c.kv_heads;
           it.s = s;
           it.row0 = (t - 1 - (x - at)) * ROWS;
           it.rows = min(ROWS, s.n * a.share - it.row0);
-          const int pos0 = s.len - s.n + it.row0 / a.share, pos1 = s.len - s.n + (it.row0 + it.rows - 1) / a.share;
+          it.tok0 = it.row0 / a.share;
+          it.head0 = it.row0 - it.tok0 * a.share;
+          const int pos0 = s.len - s.n + it.tok0, pos1 = pos0 + small_div(it.head0 + it.rows - 1, share_m);
           const int low = (int)max((int64_t)0, (int64_t)pos0 - a.window + 1);
           const int low_page = low / kKvPage, sink_pages = (min(a.sinks, low) + kKvPage - 1) / kKvPage;
           it.ns = min(sink_pages, low_page);
@@ -233,12 +248,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
   __syncthreads();
   const Item it = item_s;
   if (parts.splits > 1 && split == 0 && threadIdx.x == 0)
-    parts.info[blockIdx.x] = make_int4(it.s.q0, it.row0, it.rows, it.h);
+    parts.info[item_no] = make_int4(it.s.q0, it.row0, it.rows, it.h);
   if (it.rows == 0) {  // fewer items than the grid was made for
     if (bad) record_device_error(kErrRange);
     return;
   }
-  if (warp == 15) {
+  if (warp == 23) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
@@ -251,35 +266,39 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
   const int steps = j1 - j0;
   bool abort = false;
 
-  if (warp < 8) {
+  if (warp < 16) {
     // ================================ softmax ================================
-    const int tile = warp >> 2, quarter = warp & 3;
-    {  // the queries of both tiles, 32 rows a warp: W lanes a row, 8 dimensions a lane
-      constexpr int RPI = 32 / W;  // rows at a time
+    const int tile = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    // token (from the item's first) and head of a row of the item
+    const auto token_of = [&](int r) { return small_div(it.head0 + r, share_m); };
+    {  // the queries of both tiles, 16 rows a warp: W lanes a row, 8 dimensions a lane
+      constexpr int RPI = 32 / W, BATCH = 4;  // rows at a time; of loads in flight
       const int w = lane % W;      // dimensions 8 w .. 8 w + 7: nibble n = w / (W / 8) of words 8 w % W ..
       const int n = w / (W / 8), word0 = 8 * w % W;
+      const bool high = n >= 4;
 #pragma unroll 1
-      for (int i0 = 0; i0 < 32 / RPI; i0 += 8) {
-        float q[8][8];
-        int64_t at[8];
+      for (int i0 = 0; i0 < 16; i0 += BATCH * RPI) {
+        const int r0 = warp * 16 + i0 + lane / W;
+        float q[BATCH][8], mx[BATCH], up[BATCH];
+        int64_t at[BATCH];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {  // rows past the end read the last one
-          const int r = min(warp * 32 + (i0 + i) * RPI + lane / W, it.rows - 1), gr = it.row0 + r;
-          at[i] = (int64_t)(it.s.q0 + gr / a.share) * a.q_stride + (int64_t)(it.h * a.share + gr % a.share) * D + 8 * w;
+        for (int i = 0; i < BATCH; ++i) {  // rows past the end read the last one
+          const int r = min(r0 + i * RPI, it.rows - 1), t = token_of(r);
+          at[i] = (int64_t)(it.s.q0 + it.tok0 + t) * a.q_stride + (int64_t)(it.h * a.share + it.head0 + r - t * a.share) * D + 8 * w;
         }
         if (a.bf16) {
-          uint4 u[8];
+          uint4 u[BATCH];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at[i]));
+          for (int i = 0; i < BATCH; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at[i]));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < BATCH; ++i) {
             const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) q[i][2 * k] = __uint_as_float(x[k] << 16), q[i][2 * k + 1] = __uint_as_float(x[k] & 0xffff0000u);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < BATCH; ++i) {
             const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at[i]);
             const float4 x = __ldg(p), y = __ldg(p + 1);
             q[i][0] = x.x, q[i][1] = x.y, q[i][2] = x.z, q[i][3] = x.w;
@@ -287,30 +306,40 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
           }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = warp * 32 + (i0 + i) * RPI + lane / W;
-          float mx = 0.0f;
+        for (int i = 0; i < BATCH; ++i) {
+          mx[i] = 0.0f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(q[i][k]));
+          for (int k = 0; k < 8; ++k) mx[i] = fmaxf(mx[i], fabsf(q[i][k]));
+        }
 #pragma unroll
-          for (int o = W / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int o = W / 2; o; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
           // q' = q 2^(13 - e), 2^e <= max |q| < 2^(e + 1); not below e = -100, and not for infinities
-          int e = (int)(__float_as_uint(mx) >> 23) - 127;
+          int e = (int)(__float_as_uint(mx[i]) >> 23) - 127;
           e = e == 128 ? 13 : max(e, -100);
-          const float up = __int_as_float((13 - e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
-          // nibbles n and n + 4 of a word lie side by side: half of the lane's numbers go to the lane
-          // that has the other nibble, half of that one's come here
-          const bool high = n >= 4;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float mine = high ? q[i][4 + k] : q[i][k], give = high ? q[i][k] : q[i][4 + k];
-            const float got = __shfl_xor_sync(0xffffffffu, give, W / 2);
-            const uint32_t f = pack_half2((high ? got : mine) * up, (high ? mine : got) * up);
-            const int word = word0 + k + (high ? 4 : 0);
-            st_shared_u32(q_s + (r >> 7) * P::Q_TILE + (word >> 3) * (128 * 128) + sw128(r & 127, word & 7) + 4 * (n & 3), f);
-          }
+          up[i] = __int_as_float((13 - e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
           // a factor of 0 would make NaN of a masked score
-          if (w == 0) row_c1[r] = fmaxf(fabsf(a.scale) * kLog2e * __int_as_float((e - 13 + 127) << 23), 1.17549435e-38f);
+          if (w == 0)
+            row_c1[r0 + i * RPI] = fmaxf(fabsf(a.scale) * kLog2e * __int_as_float((e - 13 + 127) << 23), 1.17549435e-38f);
+        }
+        // nibbles n and n + 4 of a word lie side by side: half of the lane's numbers go to the lane that
+        // has the other nibble, half of that one's come here
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int word = word0 + k + (high ? 4 : 0);
+          float got[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) got[i] = __shfl_xor_sync(0xffffffffu, high ? q[i][k] : q[i][4 + k], W / 2);
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const float mine = high ? q[i][4 + k] : q[i][k];
+            const int r = r0 + i * RPI;
+            st_shared_u32(q_s + (r >> 7) * P::Q_TILE + (word >> 3) * (128 * 128) + sw128(r & 127, word & 7) + 4 * (n & 3),
+                          pack_half2((high ? got[i] : mine) * up[i], (high ? mine : got[i]) * up[i]));
+          }
         }
       }
       fence_proxy_async_smem();
@@ -318,34 +347,32 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       if (lane == 0) mbar_arrive(&q_full);
       kv4_wait_warp(&q_full, 0, &abort);
     }
-    const int r = tile * 128 + quarter * 32 + lane, gr = it.row0 + r;
+    const int w0 = tile * 128 + quarter * 32, r = w0 + lane;  // the warp's first row, the thread's row
     const bool there = r < it.rows;
     const float c1 = row_c1[r];
-    const int pos = there ? it.s.len - it.s.n + gr / a.share : -1;
+    const int pos0 = it.s.len - it.s.n + it.tok0;
+    const int pos = there ? pos0 + token_of(r) : -1;
     // of the warp's rows: the first position, and the last window's beginning (rows past the end follow the last)
-    const int last = min(it.rows, tile * 128 + quarter * 32 + 32) - 1;
-    const int pos_first = it.s.len - it.s.n + (it.row0 + tile * 128 + quarter * 32) / a.share;
-    const int64_t low_last = (int64_t)it.s.len - it.s.n + (it.row0 + max(last, 0)) / a.share - a.window + 1;
-    const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + TM_S + (uint32_t)(tile * 128);
-    const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + TM_O + (uint32_t)(tile * D);
+    const int pos_first = pos0 + token_of(w0);
+    const int64_t low_last = (int64_t)pos0 + token_of(max(min(it.rows, w0 + 32) - 1, 0)) - a.window + 1;
+    const uint32_t lane0 = (uint32_t)(quarter * 32) << 16;
+    // this page's scores; the weights lie over the first half of them
+    const uint32_t ts = tmem + lane0 + TM_S + (uint32_t)(tile * 128 + half * 64);
+    const uint32_t to = tmem + lane0 + TM_O + (uint32_t)(tile * D + half * (D / 2));
+    const int pair = 1 + tile * 4 + quarter;  // barrier of the two warps that share rows
     float m = kNegInf, l = 0.0f;
     for (int j = 0; j < steps; ++j) {
-      int hi[2], lo[2], sk[2];  // of the step's pages: columns x <= hi with x >= lo or x < sk are seen
-      bool whole = true;
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int first = page_first(it, 2 * (j0 + j) + p);
-        hi[p] = pos - first;
-        lo[p] = (int)max((int64_t)INT32_MIN, (int64_t)hi[p] - a.window + 1);
-        sk[p] = max(a.sinks - first, 0);
-        whole &= first + kKvPage - 1 <= pos_first && (first >= low_last || first + kKvPage <= a.sinks);
-      }
-      if (!kv4_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort)) break;
+      const int first = page_first(it, 2 * (j0 + j) + half);
+      const bool whole = first + kKvPage - 1 <= pos_first && (first >= low_last || first + kKvPage <= a.sinks);
+      // (no way out of the loop when a wait gives up: the pair's barriers have to match)
+      kv4_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort);
       tc_fence_after();
       if (!whole) {  // what a row does not see becomes -inf in place, 32 columns at a time
+        const int hi = pos - first;  // columns x <= hi with x >= lo or x < sk are seen
+        const int lo = (int)max((int64_t)INT32_MIN, (int64_t)hi - a.window + 1), sk = max(a.sinks - first, 0);
 #pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          const int x0 = 32 * (ch & 1), h = hi[ch >> 1] - x0, b = lo[ch >> 1] - x0, k0 = sk[ch >> 1] - x0;
+        for (int ch = 0; ch < 2; ++ch) {
+          const int h = hi - 32 * ch, b = max(lo, INT32_MIN + 64) - 32 * ch, k0 = sk - 32 * ch;
           uint32_t v[32];
           tmem_ld_32x32b_x32(ts + 32 * ch, v);
           tmem_ld_wait();
@@ -356,17 +383,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         }
         tmem_st_wait();
       }
-      float mx4[4] = {m, m, m, m};
+      float mx4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll 1
-      for (int p = 0; p < 2; ++p) {
-        uint32_t v[2][32];
-        tmem_ld_32x32b_x32(ts + 64 * p, v[0]);
-        tmem_ld_32x32b_x32(ts + 64 * p + 32, v[1]);
+      for (int ch = 0; ch < 2; ++ch) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(ts + 32 * ch, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 64; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(v[k >> 5][k & 31]));
+        for (int k = 0; k < 32; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(v[k]));
       }
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      // the other page's maximum, from the other warp of these rows
+      float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      row_x[j & 1][half][r] = mx;
+      named_bar_sync(pair, 64);
+      mx = fmaxf(m, fmaxf(mx, row_x[j & 1][half ^ 1][r]));
       // a row's first scores, or scores far above the maximum in use: move it
       const bool far = mx > m && (m == kNegInf || c1 * (mx - m) > kSlack);
       if (__any_sync(0xffffffffu, far)) {
@@ -375,7 +405,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         l *= f;
         if (j > 0) {  // the scores of this step were computed after the last step's product with V
 #pragma unroll 1
-          for (int ch = 0; ch < D / 32; ++ch) {
+          for (int ch = 0; ch < D / 64; ++ch) {
             uint32_t v[32];
             tmem_ld_32x32b_x32(to + 32 * ch, v);
             tmem_ld_wait();
@@ -389,20 +419,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       const uint64_t c2 = f2pack(c1, c1), off2 = f2pack(off, off);
       uint64_t l2[2] = {0, 0};
 #pragma unroll 1
-      for (int p = 0; p < 2; ++p) {
-        uint32_t v[2][32];
-        tmem_ld_32x32b_x32(ts + 64 * p, v[0]);
-        tmem_ld_32x32b_x32(ts + 64 * p + 32, v[1]);
+      for (int ch = 0; ch < 2; ++ch) {
+        uint32_t v[32], w[16];
+        tmem_ld_32x32b_x32(ts + 32 * ch, v);
         tmem_ld_wait();
-        uint32_t w[32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float2 t = f2unpack(fma2(f2pack(__uint_as_float(v[k >> 4][2 * (k & 15)]), __uint_as_float(v[k >> 4][2 * (k & 15) + 1])), c2, off2));
+        for (int k = 0; k < 16; ++k) {
+          const float2 t = f2unpack(fma2(f2pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, off2));
           const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
           l2[k & 1] = add2(l2[k & 1], f2pack(p0, p1));
           w[k] = pack_half2(p0, p1);
         }
-        tmem_st_x32(ts + 32 * p, w);
+        tmem_st_x16(ts + 16 * ch, w);
       }
       const float2 la = f2unpack(add2(l2[0], l2[1]));
       l += la.x + la.y;
@@ -413,46 +441,65 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     }
     if (steps > 0) kv4_wait_warp(&pv_done[tile], (uint32_t)(steps - 1) & 1u, &abort);
     tc_fence_after();
-    {
-      const float norm = parts.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-      uint16_t* out = a.out + (int64_t)(it.s.q0 + gr / a.share) * a.out_stride + (int64_t)(it.h * a.share + gr % a.share) * D;
-      float* part = parts.splits > 1 ? parts.sums + ((int64_t)blockIdx.x * parts.splits + split) * (ROWS * (D + 2)) : nullptr;
+    row_x[steps & 1][half][r] = l;
+    named_bar_sync(pair, 64);
+    l = half ? row_x[steps & 1][0][r] + l : l + row_x[steps & 1][1][r];
+    const float norm = parts.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+    float* part = parts.splits > 1 ? parts.sums + (item_no * parts.splits + split) * (ROWS * (D + 2)) : nullptr;
+    // rows go out through this tile's query operand, which no product reads any more: 16-byte chunk c of
+    // row r at (c ^ (r & 7)), so that a row leaves in one piece
+    const uint32_t stage = q_s + tile * P::Q_TILE + quarter * (32 * D * 2);
 #pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t v[32];
-        if (steps > 0 && !abort) {
-          tmem_ld_32x32b_x32(to + 32 * ch, v);
-          tmem_ld_wait();
-        } else {
+    for (int ch = 0; ch < D / 64; ++ch) {
+      uint32_t v[32];
+      if (steps > 0 && !abort) {
+        tmem_ld_32x32b_x32(to + 32 * ch, v);
+        tmem_ld_wait();
+      } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = 0;
-        }
-        if (!there) continue;
-        if (part) {
+        for (int k = 0; k < 32; ++k) v[k] = 0;
+      }
+      const int d = half * (D / 2) + 32 * ch;
+      if (part) {
+        if (there) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(part + r * D + 32 * ch + 4 * k) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        } else {
+            *reinterpret_cast<uint4*>(part + r * D + d + 4 * k) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+      } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t y[4];
+        for (int k = 0; k < 4; ++k) {
+          uint32_t y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * i]) * norm,
-                                                             __uint_as_float(v[8 * k + 2 * i + 1]) * norm);
-              y[i] = *reinterpret_cast<const uint32_t*>(&t);
-            }
-            *reinterpret_cast<uint4*>(out + 32 * ch + 8 * k) = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * i]) * norm,
+                                                           __uint_as_float(v[8 * k + 2 * i + 1]) * norm);
+            y[i] = *reinterpret_cast<const uint32_t*>(&t);
           }
+          sts128(stage + lane * (D * 2) + (((d / 8 + k) ^ (lane & 7)) << 4), y[0], y[1], y[2], y[3]);
         }
       }
-      if (part && there) {
+    }
+    if (part) {
+      if (there && half == 0) {
         part[ROWS * D + r] = m * c1;
         part[ROWS * (D + 1) + r] = l;
       }
+    } else {
+      named_bar_sync(pair, 64);
+      constexpr int C = D / 8, RPI = 32 / C;  // chunks of a row, rows at a time
+      const int ck = lane % C;
+#pragma unroll
+      for (int i = 0; i < 16; i += RPI) {  // 16 of the rows each
+        const int rr = half * 16 + i + lane / C, row = w0 + rr, t = token_of(row);
+        if (row < it.rows)
+          *reinterpret_cast<uint4*>(a.out + (int64_t)(it.s.q0 + it.tok0 + t) * a.out_stride +
+                                    (int64_t)(it.h * a.share + it.head0 + row - t * a.share) * D + 8 * ck) =
+              lds128(stage + rr * (D * 2) + ((ck ^ (rr & 7)) << 4));
+      }
     }
     tc_fence_before();
-  } else if (warp < 15) {
+  } else if (warp < 23) {
     // ================================ expansion ================================
     const int pages = 2 * steps;
     // a page's id (the last page's again where there is no such page), asked for ahead of its codes
@@ -464,11 +511,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       if (id < 0 || id >= c.n_pages) bad = true, id = 0;
       return c.pages + ((int64_t)id * c.kv_heads + it.h) * P::BLK;
     };
-    if (pages > 0 && warp < 12) {
+    if (pages > 0 && warp < 20) {
       // keys, a page at a time: 8 rows of all chunks (D = 128), or 16 of both (D = 64), a warp and unit;
       // lane & 7 is the row of eight, so that 8 lanes store to 8 rows
       constexpr int U = D == 128 ? 2 : 1;
-      const int ew = warp - 8, row8 = lane & 7, chunk = D == 128 ? lane >> 3 : (lane >> 3) & 1;
+      const int ew = warp - 16, row8 = lane & 7, chunk = D == 128 ? lane >> 3 : (lane >> 3) & 1;
       const int row0 = D == 128 ? ew * 8 + row8 : ew * 16 + (lane >> 4) * 8 + row8;  // and + 32 in the second unit
       uint4 code[U], code_n[U];
       uint2 par[U], par_n[U];
@@ -531,7 +578,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
           pr[k] = first + k < it.s.len ? v : 0;  // no value where nothing is cached
         }
       };
-      int u = warp - 12;
+      int u = warp - 20;
       load(u, page_id(u / UPP), code, par);
       int id = page_id((u + 3) / UPP), done = -1;  // the last step whose place was waited for
 #pragma unroll 1
@@ -594,7 +641,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       const uint64_t bd = vd + (uint64_t)((j & 1) * (P::V_STAGE >> 4));
 #pragma unroll
       for (int s = 0; s < TOK / 16; ++s)
-        mma_f16_ts(tmem + TM_O + t * D, tmem + TM_S + t * 128 + 8 * s,
+        mma_f16_ts(tmem + TM_O + t * D, tmem + TM_S + t * 128 + (s >> 2) * 64 + (s & 3) * 8,
                    bd + (uint64_t)((s >> 2) * ((D * 128) >> 4) + (s & 3) * 2), P::IDESC_O, j > 0 || s > 0);
       mma_commit(&pv_done[t]);
     };
@@ -633,7 +680,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
   if (bad) record_device_error(kErrRange);
   __syncwarp();
   __syncthreads();
-  if (warp == 15) tmem_dealloc(tmem, 512);
+  if (warp == 23) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of a split item, a warp a row.
@@ -667,16 +714,16 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_prompt_join_kernel(Kv4Att
   for (int e = 0; e < E; ++e) out[E * lane + e] = __float2bfloat16_rn(o[e] * norm);
 }
 
-// items of a call, at most: tiles of all sequences for each head
-int64_t items_of(const Kv4& c, int share) {
+// tiles of a call's sequences, at most
+int64_t tiles_of(const Kv4& c, int share) {
   const int64_t rows = (int64_t)c.total_q * share;
   const int64_t tiles = rows / ROWS + c.batch;
-  return c.kv_heads * (c.batch == 1 ? (rows + ROWS - 1) / ROWS : tiles);
+  return c.batch == 1 ? (rows + ROWS - 1) / ROWS : tiles;
 }
 // Parts of an item: enough for every SM to have one, each of at least 4 steps.
 int splits_of(const Kv4& c, int share, int window) {
   (void)window;
-  const int64_t items = items_of(c, share), steps = ((int64_t)c.max_kv + TOK - 1) / TOK;
+  const int64_t items = tiles_of(c, share) * c.kv_heads, steps = ((int64_t)c.max_kv + TOK - 1) / TOK;
   int64_t s = 152 / (items < 1 ? 1 : items);
   if (s > steps / 4) s = steps / 4;
   return s < 1 ? 1 : (int)s;
@@ -685,7 +732,7 @@ int splits_of(const Kv4& c, int share, int window) {
 template <int D>
 cudaError_t launch(const Kv4& c, const Kv4Attn& a, int done_rows, void* ws, cudaStream_t st) {
   using P = Prompt<D>;
-  const int64_t items = items_of(c, a.share);
+  const int64_t items = tiles_of(c, a.share) * c.kv_heads;
   Parts parts{};
   parts.splits = splits_of(c, a.share, a.window);
   if (parts.splits > 1) {
@@ -694,7 +741,9 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, int done_rows, void* ws, cuda
   }
   cudaError_t e = cudaFuncSetAttribute(kv4_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
   if (e != cudaSuccess) return e;
-  kv4_prompt_kernel<D><<<dim3((unsigned)items, (unsigned)parts.splits), THREADS, P::SMEM, st>>>(c, a, done_rows, parts);
+  if (items > INT32_MAX) return cudaErrorInvalidValue;
+  kv4_prompt_kernel<D><<<dim3((unsigned)items, (unsigned)parts.splits), THREADS, P::SMEM, st>>>(
+      c, a, done_rows, (65536u + a.share - 1) / a.share, parts);
   if ((e = cudaGetLastError()) != cudaSuccess || parts.splits == 1) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)items, ROWS / JOIN_WARPS);
@@ -711,7 +760,7 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, int done_rows, void* ws, cuda
 }  // namespace
 
 int64_t kv4_prompt_ws_bytes(const Kv4& c, int dim, int share) {
-  const int64_t items = items_of(c, share);
+  const int64_t items = tiles_of(c, share) * c.kv_heads;
   const int splits = splits_of(c, share, 0);
   return splits == 1 ? 0 : (items * 16 + 255) / 256 * 256 + items * splits * ROWS * (dim + 2) * 4;
 }
