@@ -111,13 +111,36 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 __device__ __forceinline__ uint32_t sw128(int r, int c) {
   return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+// descriptors by their low words: the high one is the same for every operand here
+__device__ __forceinline__ void mma_f16_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 ad, {%1, %3};\n\t"
+      "mov.b64 bd, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 bd, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -625,55 +648,67 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         }
       }
     }
-  } else if (lane == 0 && steps > 0) {
+  } else if (steps > 0) {
     // ================================ MMA issue ================================
+    // The whole warp goes through the waits, so that descriptors stay in uniform registers, and one
+    // elected lane issues.
+    const bool leader = elect_one();
     const uint64_t qd = make_sw128_kmajor_desc(q_s), kd = make_sw128_kmajor_desc(k_s), vd = make_sw128_kmajor_desc(v_s);
+    const uint32_t hi = (uint32_t)(qd >> 32), q_lo = (uint32_t)qd, k_lo = (uint32_t)kd, v_lo = (uint32_t)vd;
     const auto scores = [&](int t, int j) {
-      const uint64_t ad = qd + (uint64_t)(t * (P::Q_TILE >> 4)), bd = kd + (uint64_t)((j & 1) * (P::K_STAGE >> 4));
+      const uint32_t ad = q_lo + (uint32_t)(t * (P::Q_TILE >> 4)), bd = k_lo + (uint32_t)((j & 1) * (P::K_STAGE >> 4));
+      const uint32_t d = tmem + TM_S + (uint32_t)(t * 128);
+      if (leader) {
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const uint64_t o = (uint64_t)((s >> 2) * ((128 * 128) >> 4) + (s & 3) * 2);
-        mma_f16_ss(tmem + TM_S + t * 128, ad + o, bd + o, P::IDESC_S, s > 0);
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t o = (uint32_t)((s >> 2) * ((128 * 128) >> 4) + (s & 3) * 2);
+          mma_f16_ss_lo(d, ad + o, bd + o, hi, P::IDESC_S, s > 0);
+        }
+        mma_commit(&s_full[t]);
+        if (t == 1) mma_commit(&k_empty[j & 1]);
       }
-      mma_commit(&s_full[t]);
+      __syncwarp();
     };
     const auto values = [&](int t, int j) {
-      const uint64_t bd = vd + (uint64_t)((j & 1) * (P::V_STAGE >> 4));
+      const uint32_t bd = v_lo + (uint32_t)((j & 1) * (P::V_STAGE >> 4));
+      const uint32_t d = tmem + TM_O + (uint32_t)(t * D), p = tmem + TM_S + (uint32_t)(t * 128);
+      if (leader) {
 #pragma unroll
-      for (int s = 0; s < TOK / 16; ++s)
-        mma_f16_ts(tmem + TM_O + t * D, tmem + TM_S + t * 128 + (s >> 2) * 64 + (s & 3) * 8,
-                   bd + (uint64_t)((s >> 2) * ((D * 128) >> 4) + (s & 3) * 2), P::IDESC_O, j > 0 || s > 0);
-      mma_commit(&pv_done[t]);
+        for (int s = 0; s < TOK / 16; ++s)
+          mma_f16_ts_lo(d, p + (s >> 2) * 64 + (s & 3) * 8, bd + (uint32_t)((s >> 2) * ((D * 128) >> 4) + (s & 3) * 2), hi,
+                        P::IDESC_O, j > 0 || s > 0);
+        mma_commit(&pv_done[t]);
+        if (t == 1) mma_commit(&v_empty[j & 1]);
+      }
+      __syncwarp();
     };
-    bool ok = kv4_wait(&q_full, 0, &abort) && kv4_wait(&k_full[0], 0, &abort);
+    bool ok = kv4_wait_warp(&q_full, 0, &abort) && kv4_wait_warp(&k_full[0], 0, &abort);
     if (ok) {
       tc_fence_after();
       scores(0, 0);
       scores(1, 0);
-      mma_commit(&k_empty[0]);
     }
     for (int j = 0; ok && j < steps; ++j) {
-      ok = kv4_wait(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
-      for (int t = 0; ok && t < 2; ++t) {
-        ok = kv4_wait(&p_full[t], (uint32_t)j & 1u, &abort);
+      ok = kv4_wait_warp(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        ok = ok && kv4_wait_warp(&p_full[t], (uint32_t)j & 1u, &abort);
         if (!ok) break;
         tc_fence_after();
         values(t, j);
-        if (t == 1) mma_commit(&v_empty[j & 1]);
         if (j + 1 < steps) {
           // the scores go where the weights lie that this product still reads
-          ok = (t || kv4_wait(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
-               kv4_wait(&pv_done[t], (uint32_t)j & 1u, &abort);
+          ok = (t || kv4_wait_warp(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
+               kv4_wait_warp(&pv_done[t], (uint32_t)j & 1u, &abort);
           if (!ok) break;
           tc_fence_after();
           scores(t, j + 1);
-          if (t == 1) mma_commit(&k_empty[(j + 1) & 1]);
         }
       }
     }
     if (!ok) {  // what was issued ends before the tensor memory is given back
       bool given_up = false;
-      mma_commit(&all_done);
+      if (leader) mma_commit(&all_done);
       kv4_wait(&all_done, 0, &given_up);
     }
   }
