@@ -81,33 +81,6 @@ __device__ __forceinline__ uint8_t* kv4_block(const Kv4& c, int b, int page, int
   return c.pages + ((int64_t)id * c.kv_heads + h) * block_bytes;
 }
 
-// Bounded waits that leave the issue slots to the block's other warps: each poll may suspend the thread
-// for up to 2 us. 2^22 polls are far above any legal wait, whether they suspend or not.
-__device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity, bool* abort) {
-  if (*abort) return false;
-  const uint32_t a = smem_u32(bar);
-  for (uint32_t i = 0; i < (1u << 22); ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(a), "r"(parity), "r"(2000u)
-        : "memory");
-    if (ok) return true;
-  }
-  record_device_error(kErrTimeout);
-  *abort = true;
-  return false;
-}
-// by all lanes of a warp, with one outcome for all
-__device__ __forceinline__ bool kv4_wait_warp(uint64_t* bar, uint32_t parity, bool* abort) {
-  const bool ok = __all_sync(0xffffffffu, kv4_wait(bar, parity, abort));
-  if (!ok) *abort = true;
-  return ok;
-}
-
 cudaError_t launch_kv4_append(const Kv4& c, int dim, const void* k, const void* v, bool bf16, int64_t k_stride,
                               int64_t v_stride, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4& c, int dim, void* k, void* v, bool bf16, int64_t k_stride, int64_t v_stride,

@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
-      kv4_wait_warp(&q_full, 0, &abort);
+      mbar_wait_warp(&q_full, 0, &abort);
     }
     const int w0 = tile * 128 + quarter * 32, r = w0 + lane;  // the warp's first row, the thread's row
     const bool there = r < it.rows;
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       const int first = page_first(it, 2 * (j0 + j) + half);
       const bool whole = first + kKvPage - 1 <= pos_first && (first >= low_last || first + kKvPage <= a.sinks);
       // (no way out of the loop when a wait gives up: the pair's barriers have to match)
-      kv4_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort);
+      mbar_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort);
       tc_fence_after();
       if (!whole) {  // what a row does not see becomes -inf in place, 32 columns at a time
         const int hi = pos - first;  // columns x <= hi with x >= lo or x < sk are seen
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[tile]);
     }
-    if (steps > 0) kv4_wait_warp(&pv_done[tile], (uint32_t)(steps - 1) & 1u, &abort);
+    if (steps > 0) mbar_wait_warp(&pv_done[tile], (uint32_t)(steps - 1) & 1u, &abort);
     tc_fence_after();
     row_x[steps & 1][half][r] = l;
     named_bar_sync(pair, 64);
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         load(id, code_n, par_n);
         id = page_id(pg + 2);
         const int st = (pg >> 1) & 1;
-        if (pg >= 4 && !(pg & 1) && !kv4_wait_warp(&k_empty[st], (uint32_t)((pg >> 2) - 1) & 1u, &abort)) break;
+        if (pg >= 4 && !(pg & 1) && !mbar_wait_warp(&k_empty[st], (uint32_t)((pg >> 2) - 1) & 1u, &abort)) break;
         const uint32_t dst = k_s + st * P::K_STAGE;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         const int j = u / (2 * UPP), st = j & 1;
         if (j != done) {
           done = j;
-          if (j >= 2 && !kv4_wait_warp(&v_empty[st], (uint32_t)(j / 2 - 1) & 1u, &abort)) break;
+          if (j >= 2 && !mbar_wait_warp(&v_empty[st], (uint32_t)(j / 2 - 1) & 1u, &abort)) break;
         }
         const uint32_t at = v_s + st * P::V_STAGE + ((u / UPP) & 1) * (D * 128);
         const int ch = ((u % UPP) * TPU >> 3) + grp;
@@ -682,24 +682,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       }
       __syncwarp();
     };
-    bool ok = kv4_wait_warp(&q_full, 0, &abort) && kv4_wait_warp(&k_full[0], 0, &abort);
+    bool ok = mbar_wait_warp(&q_full, 0, &abort) && mbar_wait_warp(&k_full[0], 0, &abort);
     if (ok) {
       tc_fence_after();
       scores(0, 0);
       scores(1, 0);
     }
     for (int j = 0; ok && j < steps; ++j) {
-      ok = kv4_wait_warp(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
+      ok = mbar_wait_warp(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        ok = ok && kv4_wait_warp(&p_full[t], (uint32_t)j & 1u, &abort);
+        ok = ok && mbar_wait_warp(&p_full[t], (uint32_t)j & 1u, &abort);
         if (!ok) break;
         tc_fence_after();
         values(t, j);
         if (j + 1 < steps) {
           // the scores go where the weights lie that this product still reads
-          ok = (t || kv4_wait_warp(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
-               kv4_wait_warp(&pv_done[t], (uint32_t)j & 1u, &abort);
+          ok = (t || mbar_wait_warp(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
+               mbar_wait_warp(&pv_done[t], (uint32_t)j & 1u, &abort);
           if (!ok) break;
           tc_fence_after();
           scores(t, j + 1);
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     if (!ok) {  // what was issued ends before the tensor memory is given back
       bool given_up = false;
       if (leader) mma_commit(&all_done);
-      kv4_wait(&all_done, 0, &given_up);
+      mbar_wait(&all_done, 0, &given_up);
     }
   }
   if (bad) record_device_error(kErrRange);
