@@ -1,9 +1,6 @@
 // kv4_cache.cu -- writing the 4-bit key/value cache and reading it back.
 //
-// Both kernels move each vector once: W = D / 8 neighbouring lanes hold one vector, lane w the
-// word w (dimensions w + W n, n = 0..7), so a nibble is one load or store of W neighbouring
-// elements. Work items are numbered (row, head, key or value) over the packed rows, so the grid
-// holds no idle blocks for short sequences of a ragged batch.
+// Both kernels move each vector once and are bound by bytes.
 //
 // Quantisation is exact: the code is the correctly rounded quotient (x - base) / step although only
 // fp32 is used. t = (x - base) * (1 / step) is within 3 roundings, 16 * 3 * 2^-24 < 2^-18, of the
@@ -46,149 +43,241 @@ __device__ __noinline__ float border_code(float x, float base, float step, float
   return above ? n + 1.0f : n;
 }
 
-// Where a work item's vector lies: row, head and kind of the packed arrays, sequence and position in
-// the cache. pos < 0: the item has no place (past the end, or a token that the cache cannot hold).
-struct Place {
-  int64_t row;
-  int b, pos, h, is_v;
-  bool bad;
-};
-__device__ __forceinline__ Place place_of(const Kv4& c, int64_t item) {
-  const uint32_t per = 2 * c.kv_heads;
-  Place p{0, 0, -1, 0, 0, false};
-  if (item >= (int64_t)c.total_q * per) return p;
-  p.row = item / per;
-  const uint32_t hv = (uint32_t)(item - p.row * per);
-  p.h = hv >> 1;
-  p.is_v = hv & 1;
-  p.b = kv4_find(c, (int)p.row);
-  if (p.b < 0) return p;
-  const Kv4Seq s = kv4_sequence(c, p.b, &p.bad);
-  const int i = (int)p.row - s.q0;
-  p.pos = i < s.n ? s.len - s.n + i : -1;
-  p.bad |= p.pos < 0;
-  return p;
+// A block takes `rows` consecutive packed rows, all heads. The rows' places (page id and place in it,
+// negative where a row has none) are looked up once, a thread a row; then W lanes take a vector, four
+// vectors in flight. Lane w of a vector loads or stores dimensions 8 w .. 8 w + 7 in 16-byte pieces;
+// between that and its words (dimensions w + W n) lies a transpose of 8 x 8 nibbles over 8 lanes.
+constexpr int MAX_ROWS = 32, BATCH = 4;
+
+__device__ __forceinline__ void row_places(const Kv4& c, int row0, int rows, int2* place, bool* bad) {
+  const int i = threadIdx.x;
+  if (i >= rows) return;
+  int2 p = make_int2(-1, 0);
+  const int b = kv4_find(c, row0 + i);
+  if (b >= 0) {
+    bool wrong = false;
+    const Kv4Seq s = kv4_sequence(c, b, &wrong);
+    const int k = row0 + i - s.q0, pos = k < s.n ? s.len - s.n + k : -1;
+    if (pos >= 0 && !wrong) {
+      p.x = c.page_table[(int64_t)b * c.max_pages + pos / kKvPage];
+      p.y = pos % kKvPage;
+    }
+    if (p.x < 0 || p.x >= c.n_pages) *bad = true, p.x = -1;
+  }
+  place[i] = p;
+}
+// nibble j of lane i of each group of 8 lanes <-> nibble i of lane j; lanes i and i ^ 1 are `gap` apart
+__device__ __forceinline__ uint32_t transpose_nibbles(uint32_t x, int lane, int gap) {
+  const int i = lane / gap;
+  uint32_t y = __shfl_xor_sync(0xffffffffu, x, 4 * gap);
+  x = i & 4 ? (x & 0xffff0000u) | (y >> 16) : (x & 0xffffu) | (y << 16);
+  y = __shfl_xor_sync(0xffffffffu, x, 2 * gap);
+  x = i & 2 ? (x & 0xff00ff00u) | ((y >> 8) & 0x00ff00ffu) : (x & 0x00ff00ffu) | ((y << 8) & 0xff00ff00u);
+  y = __shfl_xor_sync(0xffffffffu, x, gap);
+  return i & 1 ? (x & 0xf0f0f0f0u) | ((y >> 4) & 0x0f0f0f0fu) : (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
+}
+// Lane w has the codes of dimensions 8 w + k in nibble k; the word that it then holds. D = 128: lanes of
+// like parity hold nibbles n = w / 2 of words 8 (w & 1) + k, so lane w gets word 8 (w & 1) + w / 2.
+template <int D>
+__device__ __forceinline__ int word_of(int w) {
+  return D == 128 ? 8 * (w & 1) + (w >> 1) : w;
+}
+template <int D>
+__device__ __forceinline__ uint32_t exchange(uint32_t x, int lane) {
+  return transpose_nibbles(x, D == 128 ? lane & 15 : lane & 7, D == 128 ? 2 : 1);
 }
 
 template <typename T>
-__device__ __forceinline__ float load1(const T* p);
+struct Eight {  // 8 numbers as they are loaded
+  uint4 a;
+  __device__ __forceinline__ void load(const T* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[2 * k] = __uint_as_float(u[k] << 16), x[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(T* p, const float (&x)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+      u[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
 template <>
-__device__ __forceinline__ float load1<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float load1<__nv_bfloat16>(const __nv_bfloat16* p) {
-  return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+
+// vector e of a block: row, head, key or value (e < 2^16, m = ceil(2^32 / per))
+struct Vec {
+  int row, h, is_v;
+};
+__device__ __forceinline__ Vec vec_of(uint32_t e, uint32_t per, uint32_t m) {
+  const uint32_t r = per == 1 ? e : __umulhi(e, m), hv = e - r * per;
+  return Vec{(int)r, (int)(hv >> 1), (int)(hv & 1)};
+}
+template <int D>
+__device__ __forceinline__ uint32_t* word_at(uint8_t* blk, int t, int is_v, int word) {
+  uint32_t* rows = reinterpret_cast<uint32_t*>(blk);
+  constexpr int W = D / 8;
+  return rows + (is_v ? (kKvPage + t) * W + (D == 128 && (t & 2) ? word ^ (W / 2) : word) : kv4_rho(t) * W + word);
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) kv4_append_kernel(Kv4 c, const T* __restrict__ k, const T* __restrict__ v,
-                                                             int64_t k_stride, int64_t v_stride) {
-  constexpr int W = D / 8, VPB = THREADS / W;
-  const int w = threadIdx.x % W;
-  const Place p = place_of(c, (int64_t)blockIdx.x * VPB + threadIdx.x / W);  // the same for a vector's W lanes
-  bool bad = p.bad;
-  float x[8];
-  if (p.pos >= 0) {
-    const T* row = (p.is_v ? v + p.row * v_stride : k + p.row * k_stride) + (int64_t)p.h * D + w;
+                                                             int64_t k_stride, int64_t v_stride, int max_rows, uint32_t m) {
+  constexpr int W = D / 8, WORKERS = THREADS / W;
+  __shared__ int2 place[MAX_ROWS];
+  const int w = threadIdx.x % W, lane = threadIdx.x & 31;
+  const int row0 = blockIdx.x * max_rows, rows = min(max_rows, c.total_q - row0);
+  const uint32_t per = 2 * c.kv_heads, count = rows * per;
+  bool bad = false;
+  for (uint32_t e0 = 0; e0 < count; e0 += WORKERS * BATCH) {  // the same for the whole block
+    Eight<T> in[BATCH];
+    const uint32_t first = e0 + threadIdx.x / W;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) x[n] = load1(row + W * n);
-  } else {
-#pragma unroll
-    for (int n = 0; n < 8; ++n) x[n] = 0.0f;
-  }
-  float lo = kKvMax, hi = -kKvMax;
-#pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    x[n] = max_nan(min_nan(x[n], kKvMax), -kKvMax);
-    lo = min_nan(lo, x[n]);
-    hi = max_nan(hi, x[n]);
-  }
-#pragma unroll
-  for (int o = W / 2; o >= 1; o >>= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const __half base_h = __float2half_rn(lo), step_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-  const float base = __half2float(base_h), step = __half2float(step_h);
-  uint32_t word = 0;
-  if (step > 0.0f) {
-    const float inv = __frcp_rn(step);
-    float t[8];
-    bool near = false;
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      t[n] = fminf(fmaxf(__fmul_rn(__fsub_rn(x[n], base), inv), 0.0f), 15.0f);
-      const float m = __fadd_rn(t[n], kMagic);
-      near |= fabsf(t[n] - __fsub_rn(m, kMagic)) > 0.5f - 7.62939453125e-6f;
-      word |= (__float_as_uint(m) & 15u) << (4 * n);
+    for (int i = 0; i < BATCH; ++i) {
+      const Vec q = vec_of(min(first + i * WORKERS, count - 1), per, m);
+      in[i].load((q.is_v ? v + (row0 + q.row) * v_stride : k + (row0 + q.row) * k_stride) + (int64_t)q.h * D + 8 * w);
     }
-    if (near) {
-      word = 0;
+    if (e0 == 0) {  // the numbers are on their way
+      row_places(c, row0, rows, place, &bad);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const uint32_t e = first + i * WORKERS;
+      if (e0 + i * WORKERS >= count) break;  // the whole block
+      float x[8];
+      in[i].get(x);
+      float lo = kKvMax, hi = -kKvMax;
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        float r = __fsub_rn(__fadd_rn(t[n], kMagic), kMagic);
-        if (fabsf(t[n] - r) > 0.5f - 7.62939453125e-6f)
-          r = border_code(x[n], base, step, fminf(floorf(t[n]), 14.0f));
-        word |= (uint32_t)r << (4 * n);
+        x[n] = max_nan(min_nan(x[n], kKvMax), -kKvMax);
+        lo = min_nan(lo, x[n]);
+        hi = max_nan(hi, x[n]);
+      }
+#pragma unroll
+      for (int o = W / 2; o >= 1; o >>= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      const __half base_h = __float2half_rn(lo), step_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
+      const float base = __half2float(base_h), step = __half2float(step_h);
+      uint32_t word = 0;
+      if (step > 0.0f) {
+        const float inv = __frcp_rn(step);
+        float t[8];
+        bool near = false;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          t[n] = fminf(fmaxf(__fmul_rn(__fsub_rn(x[n], base), inv), 0.0f), 15.0f);
+          const float r = __fadd_rn(t[n], kMagic);
+          near |= fabsf(t[n] - __fsub_rn(r, kMagic)) > 0.5f - 7.62939453125e-6f;
+          word |= (__float_as_uint(r) & 15u) << (4 * n);
+        }
+        if (near) {
+          word = 0;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            float r = __fsub_rn(__fadd_rn(t[n], kMagic), kMagic);
+            if (fabsf(t[n] - r) > 0.5f - 7.62939453125e-6f)
+              r = border_code(x[n], base, step, fminf(floorf(t[n]), 14.0f));
+            word |= (uint32_t)r << (4 * n);
+          }
+        }
+      }
+      word = exchange<D>(word, lane);
+      if (e < count) {
+        const Vec q = vec_of(e, per, m);
+        const int2 p = place[q.row];
+        if (p.x >= 0) {
+          uint8_t* blk = c.pages + ((int64_t)p.x * c.kv_heads + q.h) * kv4_block_bytes(D);
+          *word_at<D>(blk, p.y, q.is_v, word_of<D>(w)) = word;
+          if (w == 0)
+            reinterpret_cast<__half2*>(blk + kKvPage * D)[2 * kv4_rho(p.y) + q.is_v] = __halves2half2(step_h, base_h);
+        }
       }
     }
   }
-  if (p.pos >= 0) {
-    const int t = p.pos % kKvPage;
-    uint8_t* blk = kv4_block(c, p.b, p.pos / kKvPage, p.h, kv4_block_bytes(D), &bad);
-    if (!bad) {
-      uint32_t* rows = reinterpret_cast<uint32_t*>(blk);
-      if (p.is_v)
-        rows[(kKvPage + t) * W + (D == 128 && (t & 2) ? w ^ (W / 2) : w)] = word;
-      else
-        rows[kv4_rho(t) * W + w] = word;
-      if (w == 0)
-        reinterpret_cast<__half2*>(blk + kKvPage * D)[2 * kv4_rho(t) + p.is_v] = __halves2half2(step_h, base_h);
+  if (bad) record_device_error(kErrRange);
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS) kv4_read_kernel(Kv4 c, T* __restrict__ k, T* __restrict__ v,
+                                                           int64_t k_stride, int64_t v_stride, int max_rows, uint32_t m) {
+  constexpr int W = D / 8, WORKERS = THREADS / W;
+  __shared__ int2 place[MAX_ROWS];
+  const int w = threadIdx.x % W, lane = threadIdx.x & 31;
+  const int row0 = blockIdx.x * max_rows, rows = min(max_rows, c.total_q - row0);
+  const uint32_t per = 2 * c.kv_heads, count = rows * per;
+  bool bad = false;
+  row_places(c, row0, rows, place, &bad);
+  __syncthreads();
+  for (uint32_t e0 = 0; e0 < count; e0 += WORKERS * BATCH) {
+    uint32_t word[BATCH];
+    __half2 par[BATCH];
+    const uint32_t first = e0 + threadIdx.x / W;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const Vec q = vec_of(min(first + i * WORKERS, count - 1), per, m);
+      const int2 p = place[q.row];
+      uint8_t* blk = c.pages + ((int64_t)max(p.x, 0) * c.kv_heads + q.h) * kv4_block_bytes(D);
+      word[i] = *word_at<D>(blk, p.y, q.is_v, word_of<D>(w));
+      par[i] = reinterpret_cast<const __half2*>(blk + kKvPage * D)[2 * kv4_rho(p.y) + q.is_v];
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const uint32_t e = first + i * WORKERS;
+      if (e0 + i * WORKERS >= count) break;
+      const uint32_t x = exchange<D>(word[i], lane);
+      const float step = __low2float(par[i]), base = __high2float(par[i]);
+      float y[8];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) y[n] = __fmaf_rn(step, (float)((x >> (4 * n)) & 15u), base);
+      if (e < count) {
+        const Vec q = vec_of(e, per, m);
+        if (place[q.row].x >= 0)
+          Eight<T>::store((q.is_v ? v + (row0 + q.row) * v_stride : k + (row0 + q.row) * k_stride) + (int64_t)q.h * D + 8 * w, y);
+      }
     }
   }
   if (bad) record_device_error(kErrRange);
 }
 
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-template <int D, typename T>
-__global__ void __launch_bounds__(THREADS) kv4_read_kernel(Kv4 c, T* __restrict__ k, T* __restrict__ v,
-                                                           int64_t k_stride, int64_t v_stride) {
-  constexpr int W = D / 8, VPB = THREADS / W;
-  const int w = threadIdx.x % W;
-  const Place p = place_of(c, (int64_t)blockIdx.x * VPB + threadIdx.x / W);
-  bool bad = p.bad;
-  if (p.pos >= 0) {
-    const int t = p.pos % kKvPage;
-    const uint8_t* blk = kv4_block(c, p.b, p.pos / kKvPage, p.h, kv4_block_bytes(D), &bad);
-    const uint32_t* rows = reinterpret_cast<const uint32_t*>(blk);
-    const uint32_t word = p.is_v ? rows[(kKvPage + t) * W + (D == 128 && (t & 2) ? w ^ (W / 2) : w)]
-                                 : rows[kv4_rho(t) * W + w];
-    const __half2 par = reinterpret_cast<const __half2*>(blk + kKvPage * D)[2 * kv4_rho(t) + p.is_v];
-    const float step = __low2float(par), base = __high2float(par);
-    T* row = (p.is_v ? v + p.row * v_stride : k + p.row * k_stride) + (int64_t)p.h * D + w;
-#pragma unroll
-    for (int n = 0; n < 8; ++n) store1(row + W * n, __fmaf_rn(step, (float)((word >> (4 * n)) & 15u), base));
-  }
-  if (bad) record_device_error(kErrRange);
+// rows of a block: few enough that all SMs have several blocks
+int block_rows(const Kv4& c) {
+  const int r = c.total_q / 608;
+  return r < 1 ? 1 : r > MAX_ROWS ? MAX_ROWS : r;
 }
-
-template <int D>
-int64_t blocks_of(const Kv4& c) {
-  constexpr int VPB = THREADS / (D / 8);
-  return ((int64_t)c.total_q * 2 * c.kv_heads + VPB - 1) / VPB;
-}
+uint32_t per_magic(const Kv4& c) { return (uint32_t)(((uint64_t(1) << 32) + 2 * c.kv_heads - 1) / (2 * c.kv_heads)); }
 
 template <int D, typename T>
 cudaError_t append(const Kv4& c, const void* k, const void* v, int64_t k_stride, int64_t v_stride, cudaStream_t st) {
-  kv4_append_kernel<D, T><<<(unsigned)blocks_of<D>(c), THREADS, 0, st>>>(
-      c, static_cast<const T*>(k), static_cast<const T*>(v), k_stride, v_stride);
+  const int rows = block_rows(c);
+  kv4_append_kernel<D, T><<<(unsigned)((c.total_q + (int64_t)rows - 1) / rows), THREADS, 0, st>>>(
+      c, static_cast<const T*>(k), static_cast<const T*>(v), k_stride, v_stride, rows, per_magic(c));
   return cudaGetLastError();
 }
 template <int D, typename T>
 cudaError_t read(const Kv4& c, void* k, void* v, int64_t k_stride, int64_t v_stride, cudaStream_t st) {
-  kv4_read_kernel<D, T><<<(unsigned)blocks_of<D>(c), THREADS, 0, st>>>(c, static_cast<T*>(k), static_cast<T*>(v),
-                                                                      k_stride, v_stride);
+  const int rows = block_rows(c);
+  kv4_read_kernel<D, T><<<(unsigned)((c.total_q + (int64_t)rows - 1) / rows), THREADS, 0, st>>>(
+      c, static_cast<T*>(k), static_cast<T*>(v), k_stride, v_stride, rows, per_magic(c));
   return cudaGetLastError();
 }
 
