@@ -15,8 +15,9 @@
 namespace bitnet {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int WORK = 256, THREADS = WORK + 32;
 constexpr float kKvMax = 61440.0f;
+constexpr float kNear = 0.5f - 7.62939453125e-6f;  // 2^-17 below a half
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: x + kMagic holds rne(x) in its low bits
 
 // NaN-keeping minimum and maximum (fminf and fmaxf drop a NaN)
@@ -28,6 +29,16 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -43,15 +54,16 @@ __device__ __noinline__ float border_code(float x, float base, float step, float
   return above ? n + 1.0f : n;
 }
 
-// A block takes `rows` consecutive packed rows, all heads. The rows' places (page id and place in it,
-// negative where a row has none) are looked up once, a thread a row; then W lanes take a vector, four
-// vectors in flight. Lane w of a vector loads or stores dimensions 8 w .. 8 w + 7 in 16-byte pieces;
-// between that and its words (dimensions w + W n) lies a transpose of 8 x 8 nibbles over 8 lanes.
-constexpr int MAX_ROWS = 32, BATCH = 4;
+// A block takes chunks of `rows` consecutive packed rows, all heads, one after another. Eight warps move
+// the vectors: W lanes take the key and the value of one row and head, lane w dimensions 8 w .. 8 w + 7
+// in 16-byte pieces; between that and the words (dimensions w + W n) lies a transpose of 8 x 8 nibbles
+// over 8 lanes. A ninth warp looks up the next chunk's places meanwhile (page id, and place in the page;
+// negative where a row has none): three dependent loads a row.
+constexpr int MAX_ROWS = 16, BATCH = 2, READ_BATCH = 4;
 
-__device__ __forceinline__ void row_places(const Kv4& c, int row0, int rows, int2* place, bool* bad) {
-  const int i = threadIdx.x;
-  if (i >= rows) return;
+__device__ __forceinline__ void row_places(const Kv4& c, int row0, int max_rows, int2* place, bool* bad) {
+  const int i = threadIdx.x - WORK;
+  if (i < 0 || i >= max_rows || row0 + i >= c.total_q) return;
   int2 p = make_int2(-1, 0);
   const int b = kv4_find(c, row0 + i);
   if (b >= 0) {
@@ -122,94 +134,124 @@ struct Eight<float> {
   }
 };
 
-// vector e of a block: row, head, key or value (e < 2^16, m = ceil(2^32 / per))
-struct Vec {
-  int row, h, is_v;
-};
-__device__ __forceinline__ Vec vec_of(uint32_t e, uint32_t per, uint32_t m) {
-  const uint32_t r = per == 1 ? e : __umulhi(e, m), hv = e - r * per;
-  return Vec{(int)r, (int)(hv >> 1), (int)(hv & 1)};
+template <int D>
+__device__ __forceinline__ uint32_t* key_word(uint8_t* blk, int t, int word) {
+  return reinterpret_cast<uint32_t*>(blk) + kv4_rho(t) * (D / 8) + word;
 }
 template <int D>
-__device__ __forceinline__ uint32_t* word_at(uint8_t* blk, int t, int is_v, int word) {
-  uint32_t* rows = reinterpret_cast<uint32_t*>(blk);
+__device__ __forceinline__ uint32_t* value_word(uint8_t* blk, int t, int word) {
   constexpr int W = D / 8;
-  return rows + (is_v ? (kKvPage + t) * W + (D == 128 && (t & 2) ? word ^ (W / 2) : word) : kv4_rho(t) * W + word);
+  return reinterpret_cast<uint32_t*>(blk) + (kKvPage + t) * W + (D == 128 && (t & 2) ? word ^ (W / 2) : word);
+}
+// step and base of token t: keys', then values'
+template <int D>
+__device__ __forceinline__ uint2* params(uint8_t* blk, int t) {
+  return reinterpret_cast<uint2*>(blk + kKvPage * D) + kv4_rho(t);
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(THREADS) kv4_append_kernel(Kv4 c, const T* __restrict__ k, const T* __restrict__ v,
-                                                             int64_t k_stride, int64_t v_stride, int max_rows, uint32_t m) {
-  constexpr int W = D / 8, WORKERS = THREADS / W;
-  __shared__ int2 place[MAX_ROWS];
-  const int w = threadIdx.x % W, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.x * max_rows, rows = min(max_rows, c.total_q - row0);
-  const uint32_t per = 2 * c.kv_heads, count = rows * per;
-  bool bad = false;
-  for (uint32_t e0 = 0; e0 < count; e0 += WORKERS * BATCH) {  // the same for the whole block
-    Eight<T> in[BATCH];
-    const uint32_t first = e0 + threadIdx.x / W;
+// Quantises a vector, 8 numbers a lane of W: the lane's codes (number k in nibble k) and the parameters.
+template <int W>
+__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* par) {
+  float lo = min_nan(min3_nan(x[0], x[1], x[2]), min3_nan(x[3], x[4], min3_nan(x[5], x[6], x[7])));
+  float hi = max_nan(max3_nan(x[0], x[1], x[2]), max3_nan(x[3], x[4], max3_nan(x[5], x[6], x[7])));
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const Vec q = vec_of(min(first + i * WORKERS, count - 1), per, m);
-      in[i].load((q.is_v ? v + (row0 + q.row) * v_stride : k + (row0 + q.row) * k_stride) + (int64_t)q.h * D + 8 * w);
-    }
-    if (e0 == 0) {  // the numbers are on their way
-      row_places(c, row0, rows, place, &bad);
-      __syncthreads();
-    }
+  for (int o = W / 2; o >= 1; o >>= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  // (a number beyond +-61440 needs no clamp of its own: its code is clamped below)
+  const float lo_c = max_nan(min_nan(lo, kKvMax), -kKvMax), hi_c = max_nan(min_nan(hi, kKvMax), -kKvMax);
+  const __half base_h = __float2half_rn(lo_c), step_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi_c, lo_c), 15.0f));
+  const float base = __half2float(base_h), step = __half2float(step_h);
+  *par = (uint32_t)__half_as_ushort(step_h) | (uint32_t)__half_as_ushort(base_h) << 16;
+  uint32_t word = 0;
+  if (step > 0.0f) {
+    const float inv = __frcp_rn(step);
+    // quotients outside (-0.49, 15.49) need the clamp: where the fp16 base or step is far off the ends
+    const bool clamp = !(__fmul_rn(__fsub_rn(lo, base), inv) > -0.49f && __fmul_rn(__fsub_rn(hi, base), inv) < 15.49f);
+    float t[8];
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const uint32_t e = first + i * WORKERS;
-      if (e0 + i * WORKERS >= count) break;  // the whole block
-      float x[8];
-      in[i].get(x);
-      float lo = kKvMax, hi = -kKvMax;
+    for (int n = 0; n < 8; ++n) t[n] = __fmul_rn(__fsub_rn(x[n], base), inv);
+    if (clamp) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) t[n] = fminf(fmaxf(t[n], 0.0f), 15.0f);
+    }
+    float off = 0.0f;  // the largest distance from an integer
+#pragma unroll
+    for (int n = 7; n >= 0; --n) {
+      const float r = __fadd_rn(t[n], kMagic);
+      off = fmaxf(off, fabsf(t[n] - __fsub_rn(r, kMagic)));
+      word = word * 16u + __float_as_uint(r);
+    }
+    word -= 0x4b400000u * 0x11111111u;  // the eight kMagic
+    if (off > kNear) {
+      word = 0;
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        x[n] = max_nan(min_nan(x[n], kKvMax), -kKvMax);
-        lo = min_nan(lo, x[n]);
-        hi = max_nan(hi, x[n]);
+        float r = __fsub_rn(__fadd_rn(t[n], kMagic), kMagic);
+        if (fabsf(t[n] - r) > kNear) r = border_code(x[n], base, step, floorf(t[n]));
+        word |= (uint32_t)r << (4 * n);
       }
+    }
+  }
+  return word;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS, 3) kv4_append_kernel(Kv4 c, const T* __restrict__ k, const T* __restrict__ v,
+                                                                int64_t k_stride, int64_t v_stride, int max_rows,
+                                                                uint32_t m) {
+  constexpr int W = D / 8, WORKERS = WORK / W;
+  __shared__ int2 place[2][MAX_ROWS];
+  const int w = threadIdx.x % W, lane = threadIdx.x & 31, first = threadIdx.x / W;
+  const int stride = gridDim.x * max_rows;
+  bool bad = false;
+  int buf = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * max_rows; row0 < c.total_q; row0 += stride, buf ^= 1) {
+    const int rows = (int)min((int64_t)max_rows, c.total_q - row0);
+    const int count = rows * c.kv_heads;  // pairs of a key and a value
+    const auto pair_of = [&](int e, int* row, int* h) {
+      e = min(e, count - 1);
+      *row = c.kv_heads == 1 ? e : (int)__umulhi((uint32_t)e, m);
+      *h = e - *row * c.kv_heads;
+    };
+    Eight<T> in[BATCH][2];
+    const auto load = [&](int e0) {
 #pragma unroll
-      for (int o = W / 2; o >= 1; o >>= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      for (int i = 0; i < BATCH; ++i) {
+        int row, h;
+        pair_of(e0 + first + i * WORKERS, &row, &h);
+        in[i][0].load(k + (row0 + row) * k_stride + (int64_t)h * D + 8 * w);
+        in[i][1].load(v + (row0 + row) * v_stride + (int64_t)h * D + 8 * w);
       }
-      const __half base_h = __float2half_rn(lo), step_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-      const float base = __half2float(base_h), step = __half2float(step_h);
-      uint32_t word = 0;
-      if (step > 0.0f) {
-        const float inv = __frcp_rn(step);
-        float t[8];
-        bool near = false;
+    };
+    if (threadIdx.x < WORK) load(0);  // on their way while the places are looked up
+    if (row0 == (int64_t)blockIdx.x * max_rows) row_places(c, (int)row0, max_rows, place[0], &bad);
+    __syncthreads();
+    if (threadIdx.x >= WORK) {
+      if (row0 + stride < c.total_q) row_places(c, (int)(row0 + stride), max_rows, place[buf ^ 1], &bad);
+      continue;
+    }
+    for (int e0 = 0; e0 < count; e0 += WORKERS * BATCH) {
+      if (e0) load(e0);
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          t[n] = fminf(fmaxf(__fmul_rn(__fsub_rn(x[n], base), inv), 0.0f), 15.0f);
-          const float r = __fadd_rn(t[n], kMagic);
-          near |= fabsf(t[n] - __fsub_rn(r, kMagic)) > 0.5f - 7.62939453125e-6f;
-          word |= (__float_as_uint(r) & 15u) << (4 * n);
-        }
-        if (near) {
-          word = 0;
-#pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            float r = __fsub_rn(__fadd_rn(t[n], kMagic), kMagic);
-            if (fabsf(t[n] - r) > 0.5f - 7.62939453125e-6f)
-              r = border_code(x[n], base, step, fminf(floorf(t[n]), 14.0f));
-            word |= (uint32_t)r << (4 * n);
-          }
-        }
-      }
-      word = exchange<D>(word, lane);
-      if (e < count) {
-        const Vec q = vec_of(e, per, m);
-        const int2 p = place[q.row];
-        if (p.x >= 0) {
-          uint8_t* blk = c.pages + ((int64_t)p.x * c.kv_heads + q.h) * kv4_block_bytes(D);
-          *word_at<D>(blk, p.y, q.is_v, word_of<D>(w)) = word;
-          if (w == 0)
-            reinterpret_cast<__half2*>(blk + kKvPage * D)[2 * kv4_rho(p.y) + q.is_v] = __halves2half2(step_h, base_h);
+      for (int i = 0; i < BATCH; ++i) {
+        const int e = e0 + first + i * WORKERS;
+        if (e0 + i * WORKERS >= count) break;  // all the workers
+        float x[8];
+        uint2 par;
+        in[i][0].get(x);
+        const uint32_t kw = exchange<D>(quantise<W>(x, &par.x), lane);
+        in[i][1].get(x);
+        const uint32_t vw = exchange<D>(quantise<W>(x, &par.y), lane);
+        int row, h;
+        pair_of(e, &row, &h);
+        const int2 p = place[buf][row];
+        if (e < count && p.x >= 0) {
+          uint8_t* blk = c.pages + ((int64_t)p.x * c.kv_heads + h) * kv4_block_bytes(D);
+          *key_word<D>(blk, p.y, word_of<D>(w)) = kw;
+          *value_word<D>(blk, p.y, word_of<D>(w)) = vw;
+          if (w == 0) *params<D>(blk, p.y) = par;
         }
       }
     }
@@ -218,66 +260,87 @@ __global__ void __launch_bounds__(THREADS) kv4_append_kernel(Kv4 c, const T* __r
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(THREADS) kv4_read_kernel(Kv4 c, T* __restrict__ k, T* __restrict__ v,
-                                                           int64_t k_stride, int64_t v_stride, int max_rows, uint32_t m) {
-  constexpr int W = D / 8, WORKERS = THREADS / W;
-  __shared__ int2 place[MAX_ROWS];
-  const int w = threadIdx.x % W, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.x * max_rows, rows = min(max_rows, c.total_q - row0);
-  const uint32_t per = 2 * c.kv_heads, count = rows * per;
+__global__ void __launch_bounds__(THREADS, 3) kv4_read_kernel(Kv4 c, T* __restrict__ k, T* __restrict__ v,
+                                                              int64_t k_stride, int64_t v_stride, int max_rows,
+                                                              uint32_t m) {
+  constexpr int W = D / 8, WORKERS = WORK / W;
+  __shared__ int2 place[2][MAX_ROWS];
+  const int w = threadIdx.x % W, lane = threadIdx.x & 31, first = threadIdx.x / W;
+  const int stride = gridDim.x * max_rows;
   bool bad = false;
-  row_places(c, row0, rows, place, &bad);
-  __syncthreads();
-  for (uint32_t e0 = 0; e0 < count; e0 += WORKERS * BATCH) {
-    uint32_t word[BATCH];
-    __half2 par[BATCH];
-    const uint32_t first = e0 + threadIdx.x / W;
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const Vec q = vec_of(min(first + i * WORKERS, count - 1), per, m);
-      const int2 p = place[q.row];
-      uint8_t* blk = c.pages + ((int64_t)max(p.x, 0) * c.kv_heads + q.h) * kv4_block_bytes(D);
-      word[i] = *word_at<D>(blk, p.y, q.is_v, word_of<D>(w));
-      par[i] = reinterpret_cast<const __half2*>(blk + kKvPage * D)[2 * kv4_rho(p.y) + q.is_v];
+  int buf = 0;
+  row_places(c, blockIdx.x * max_rows, max_rows, place[0], &bad);
+  for (int64_t row0 = (int64_t)blockIdx.x * max_rows; row0 < c.total_q; row0 += stride, buf ^= 1) {
+    const int rows = (int)min((int64_t)max_rows, c.total_q - row0);
+    const int count = rows * c.kv_heads;
+    __syncthreads();
+    if (threadIdx.x >= WORK) {
+      if (row0 + stride < c.total_q) row_places(c, (int)(row0 + stride), max_rows, place[buf ^ 1], &bad);
+      continue;
     }
+    for (int e0 = 0; e0 < count; e0 += WORKERS * READ_BATCH) {
+      uint32_t kw[READ_BATCH], vw[READ_BATCH];
+      uint2 par[READ_BATCH];
+      int row[READ_BATCH], h[READ_BATCH];
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const uint32_t e = first + i * WORKERS;
-      if (e0 + i * WORKERS >= count) break;
-      const uint32_t x = exchange<D>(word[i], lane);
-      const float step = __low2float(par[i]), base = __high2float(par[i]);
-      float y[8];
+      for (int i = 0; i < READ_BATCH; ++i) {
+        const int e = min(e0 + first + i * WORKERS, count - 1);
+        row[i] = c.kv_heads == 1 ? e : (int)__umulhi((uint32_t)e, m);
+        h[i] = e - row[i] * c.kv_heads;
+        const int2 p = place[buf][row[i]];
+        if (p.x < 0) row[i] = -1;
+        uint8_t* blk = c.pages + ((int64_t)max(p.x, 0) * c.kv_heads + h[i]) * kv4_block_bytes(D);
+        kw[i] = *key_word<D>(blk, p.y, word_of<D>(w));
+        vw[i] = *value_word<D>(blk, p.y, word_of<D>(w));
+        par[i] = *params<D>(blk, p.y);
+      }
 #pragma unroll
-      for (int n = 0; n < 8; ++n) y[n] = __fmaf_rn(step, (float)((x >> (4 * n)) & 15u), base);
-      if (e < count) {
-        const Vec q = vec_of(e, per, m);
-        if (place[q.row].x >= 0)
-          Eight<T>::store((q.is_v ? v + (row0 + q.row) * v_stride : k + (row0 + q.row) * k_stride) + (int64_t)q.h * D + 8 * w, y);
+      for (int i = 0; i < READ_BATCH; ++i) {
+        if (e0 + i * WORKERS >= count) break;
+        const bool there = e0 + first + i * WORKERS < count && row[i] >= 0;
+        const auto give = [&](uint32_t word, uint32_t pr, T* to) {
+          const uint32_t x = exchange<D>(word, lane), even = x & 0x0f0f0f0fu, odd = (x >> 4) & 0x0f0f0f0fu;
+          const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&pr));
+          float y[8];
+#pragma unroll
+          for (int n = 0; n < 8; ++n)  // 2^23 + code, exactly
+            y[n] = __fmaf_rn(sb.x, __uint_as_float(__byte_perm(n & 1 ? odd : even, 0x4b000000u, 0x7650 | (n >> 1))) - 8388608.0f, sb.y);
+          if (there) Eight<T>::store(to, y);
+        };
+        const int64_t at = row0 + row[i];
+        give(kw[i], par[i].x, k + at * k_stride + (int64_t)h[i] * D + 8 * w);
+        give(vw[i], par[i].y, v + at * v_stride + (int64_t)h[i] * D + 8 * w);
       }
     }
   }
   if (bad) record_device_error(kErrRange);
 }
 
-// rows of a block: few enough that all SMs have several blocks
-int block_rows(const Kv4& c) {
-  const int r = c.total_q / 608;
+// rows of a chunk: few enough that all SMs have several blocks
+int chunk_rows(const Kv4& c) {
+  const int r = c.total_q / (3 * 152);
   return r < 1 ? 1 : r > MAX_ROWS ? MAX_ROWS : r;
 }
-uint32_t per_magic(const Kv4& c) { return (uint32_t)(((uint64_t(1) << 32) + 2 * c.kv_heads - 1) / (2 * c.kv_heads)); }
+// blocks: three an SM (what fits), each with as many chunks as the next
+unsigned blocks(const Kv4& c, int rows) {
+  const int64_t chunks = (c.total_q + (int64_t)rows - 1) / rows;
+  return (unsigned)(chunks < 3 * 152 ? chunks : 3 * 152);
+}
+// e / kv_heads = umulhi(e, m) for e < 2^14 and at most 1024 heads
+uint32_t heads_magic(const Kv4& c) { return (uint32_t)(((uint64_t(1) << 32) + c.kv_heads - 1) / c.kv_heads); }
 
 template <int D, typename T>
 cudaError_t append(const Kv4& c, const void* k, const void* v, int64_t k_stride, int64_t v_stride, cudaStream_t st) {
-  const int rows = block_rows(c);
-  kv4_append_kernel<D, T><<<(unsigned)((c.total_q + (int64_t)rows - 1) / rows), THREADS, 0, st>>>(
-      c, static_cast<const T*>(k), static_cast<const T*>(v), k_stride, v_stride, rows, per_magic(c));
+  const int rows = chunk_rows(c);
+  kv4_append_kernel<D, T><<<blocks(c, rows), THREADS, 0, st>>>(c, static_cast<const T*>(k), static_cast<const T*>(v),
+                                                               k_stride, v_stride, rows, heads_magic(c));
   return cudaGetLastError();
 }
 template <int D, typename T>
 cudaError_t read(const Kv4& c, void* k, void* v, int64_t k_stride, int64_t v_stride, cudaStream_t st) {
-  const int rows = block_rows(c);
-  kv4_read_kernel<D, T><<<(unsigned)((c.total_q + (int64_t)rows - 1) / rows), THREADS, 0, st>>>(
-      c, static_cast<T*>(k), static_cast<T*>(v), k_stride, v_stride, rows, per_magic(c));
+  const int rows = chunk_rows(c);
+  kv4_read_kernel<D, T><<<blocks(c, rows), THREADS, 0, st>>>(c, static_cast<T*>(k), static_cast<T*>(v), k_stride,
+                                                             v_stride, rows, heads_magic(c));
   return cudaGetLastError();
 }
 
