@@ -434,8 +434,8 @@ BITNET_API int64_t bitnet_kv4_cache_bytes(int64_t n_pages, int64_t kv_heads, int
  *          at k + r * k_stride (elements), its heads lie one after another
  *   Tokens with a negative position (more new tokens than kv_len) have no place: they are not
  *   written, and BITNET_ERANGE is recorded.
- *   k and v 16-byte aligned, strides >= kv_heads * head_dim and multiples of 16 bytes. Sequences
- *   of one call must not share the places that they write.
+ *   k and v 16-byte aligned, strides >= kv_heads * head_dim, at most 2^26, and multiples of 16
+ *   bytes. Sequences of one call must not share the places that they write.
  */
 BITNET_API int bitnet_kv4_append(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch, const void *k,
                                  const void *v, int dtype, int64_t k_stride, int64_t v_stride, void *stream);
@@ -465,7 +465,8 @@ BITNET_API int bitnet_kv4_read(const bitnet_kv4_cache *cache, const bitnet_kv4_b
  *   workspace : device, 256-byte aligned, at least bitnet_kv4_attention_workspace_size bytes (for
  *            the same cache, batch sizes and q_heads; it may be NULL where that is 0). Needs no
  *            initialisation; calls that may run at the same time need one each.
- *   q and out 16-byte aligned, strides >= q_heads * head_dim and multiples of 16 bytes; scale finite.
+ *   q and out 16-byte aligned, strides >= q_heads * head_dim, at most 2^26, and multiples of 16 bytes;
+ *   scale finite.
  * The results of a call are the same bits each time it is made with the same arguments.
  */
 BITNET_API int64_t bitnet_kv4_attention_workspace_size(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch,

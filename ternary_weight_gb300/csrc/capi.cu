@@ -478,9 +478,10 @@ int check_kv4(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* b, Kv4* out
              b->page_table, b->max_pages, (int)b->batch, (int)b->total_q, (int)b->max_q, (int)b->max_kv};
   return BITNET_OK;
 }
-// a row stride in elements: at least `least`, and a multiple of 16 bytes
+// a row stride in elements: at least `least`, at most 2^26 (16 rows' offsets are 32-bit), and a multiple
+// of 16 bytes
 int check_stride(int64_t stride, int64_t least, int64_t elem_bytes) {
-  if (stride < least || stride > (int64_t(1) << 40)) return BITNET_EINVAL;
+  if (stride < least || stride > (int64_t(1) << 26)) return BITNET_EINVAL;
   return stride * elem_bytes % 16 == 0 ? BITNET_OK : BITNET_EALIGN;
 }
 int check_kv4_rows(const Kv4& c, int dim, const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride) {

@@ -61,23 +61,47 @@ __device__ __noinline__ float border_code(float x, float base, float step, float
 // negative where a row has none): three dependent loads a row.
 constexpr int MAX_ROWS = 16, BATCH = 2, READ_BATCH = 4;
 
-__device__ __forceinline__ void row_places(const Kv4& c, int row0, int max_rows, int2* place, bool* bad) {
+// Where a row's vectors lie: its page (null where it has no place) and its token there.
+struct Place {
+  uint8_t* page;
+  int t, unused;
+};
+template <int D>
+__device__ __forceinline__ void row_places(const Kv4& c, int row0, int max_rows, Place* place, bool* bad) {
   const int i = threadIdx.x - WORK;
   if (i < 0 || i >= max_rows || row0 + i >= c.total_q) return;
-  int2 p = make_int2(-1, 0);
+  Place p{nullptr, 0, 0};
   const int b = kv4_find(c, row0 + i);
   if (b >= 0) {
     bool wrong = false;
     const Kv4Seq s = kv4_sequence(c, b, &wrong);
     const int k = row0 + i - s.q0, pos = k < s.n ? s.len - s.n + k : -1;
     if (pos >= 0 && !wrong) {
-      p.x = c.page_table[(int64_t)b * c.max_pages + pos / kKvPage];
-      p.y = pos % kKvPage;
+      wrong = true;
+      const int id = c.page_table[(int64_t)b * c.max_pages + pos / kKvPage];
+      if (id >= 0 && id < c.n_pages) {
+        wrong = false;
+        p.page = c.pages + (int64_t)id * c.kv_heads * kv4_block_bytes(D);
+        p.t = pos % kKvPage;
+      }
     }
-    if (p.x < 0 || p.x >= c.n_pages) *bad = true, p.x = -1;
+    if (p.page == nullptr) *bad = true;
   }
   place[i] = p;
 }
+// The pairs (row, head) of a worker: `WORKERS` pairs on is dr rows and dh heads.
+struct Pair {
+  int row, h;
+  __device__ __forceinline__ void next(int dr, int dh, int heads) {
+    row += dr;
+    h += dh;
+    if (h >= heads) h -= heads, ++row;
+  }
+};
+struct Steps {
+  int dr, dh;      // WORKERS / heads, WORKERS % heads
+  uint32_t magic;  // worker / heads = umulhi(worker, magic)
+};
 // nibble j of lane i of each group of 8 lanes <-> nibble i of lane j; lanes i and i ^ 1 are `gap` apart
 __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t x, int lane, int gap) {
   const int i = lane / gap;
@@ -200,58 +224,57 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* par)
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS, 3) kv4_append_kernel(Kv4 c, const T* __restrict__ k, const T* __restrict__ v,
                                                                 int64_t k_stride, int64_t v_stride, int max_rows,
-                                                                uint32_t m) {
-  constexpr int W = D / 8, WORKERS = WORK / W;
-  __shared__ int2 place[2][MAX_ROWS];
-  const int w = threadIdx.x % W, lane = threadIdx.x & 31, first = threadIdx.x / W;
-  const int stride = gridDim.x * max_rows;
+                                                                Steps steps) {
+  constexpr int W = D / 8, WORKERS = WORK / W, BLK = (int)kv4_block_bytes(D);
+  __shared__ Place place[2][MAX_ROWS];
+  const int w = threadIdx.x % W, lane = threadIdx.x & 31, worker = threadIdx.x / W;
+  const int stride = gridDim.x * max_rows, heads = c.kv_heads;
+  Pair first;
+  first.row = heads == 1 ? worker : (int)__umulhi((uint32_t)worker, steps.magic);
+  first.h = worker - first.row * heads;
   bool bad = false;
   int buf = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * max_rows; row0 < c.total_q; row0 += stride, buf ^= 1) {
     const int rows = (int)min((int64_t)max_rows, c.total_q - row0);
-    const int count = rows * c.kv_heads;  // pairs of a key and a value
-    const auto pair_of = [&](int e, int* row, int* h) {
-      e = min(e, count - 1);
-      *row = c.kv_heads == 1 ? e : (int)__umulhi((uint32_t)e, m);
-      *h = e - *row * c.kv_heads;
-    };
+    const T *const kc = k + row0 * k_stride + 8 * w, *const vc = v + row0 * v_stride + 8 * w;
     Eight<T> in[BATCH][2];
-    const auto load = [&](int e0) {
+    Pair at[BATCH], p = first;
+    const auto load = [&]() {
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        int row, h;
-        pair_of(e0 + first + i * WORKERS, &row, &h);
-        in[i][0].load(k + (row0 + row) * k_stride + (int64_t)h * D + 8 * w);
-        in[i][1].load(v + (row0 + row) * v_stride + (int64_t)h * D + 8 * w);
+        at[i] = p;
+        p.next(steps.dr, steps.dh, heads);
+        if (at[i].row < rows) {
+          in[i][0].load(kc + (at[i].row * (int)k_stride + at[i].h * D));
+          in[i][1].load(vc + (at[i].row * (int)v_stride + at[i].h * D));
+        }
       }
     };
-    if (threadIdx.x < WORK) load(0);  // on their way while the places are looked up
-    if (row0 == (int64_t)blockIdx.x * max_rows) row_places(c, (int)row0, max_rows, place[0], &bad);
+    if (threadIdx.x < WORK) load();  // on their way while the places are looked up
+    if (row0 == (int64_t)blockIdx.x * max_rows) row_places<D>(c, (int)row0, max_rows, place[0], &bad);
     __syncthreads();
     if (threadIdx.x >= WORK) {
-      if (row0 + stride < c.total_q) row_places(c, (int)(row0 + stride), max_rows, place[buf ^ 1], &bad);
+      if (row0 + stride < c.total_q) row_places<D>(c, (int)(row0 + stride), max_rows, place[buf ^ 1], &bad);
       continue;
     }
-    for (int e0 = 0; e0 < count; e0 += WORKERS * BATCH) {
-      if (e0) load(e0);
+    for (int e = 0; e < rows * heads; e += WORKERS * BATCH) {
+      if (e) load();
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const int e = e0 + first + i * WORKERS;
-        if (e0 + i * WORKERS >= count) break;  // all the workers
+        if (e + i * WORKERS >= rows * heads) break;
+        const bool there = at[i].row < rows;
         float x[8];
         uint2 par;
         in[i][0].get(x);
         const uint32_t kw = exchange<D>(quantise<W>(x, &par.x), lane);
         in[i][1].get(x);
         const uint32_t vw = exchange<D>(quantise<W>(x, &par.y), lane);
-        int row, h;
-        pair_of(e, &row, &h);
-        const int2 p = place[buf][row];
-        if (e < count && p.x >= 0) {
-          uint8_t* blk = c.pages + ((int64_t)p.x * c.kv_heads + h) * kv4_block_bytes(D);
-          *key_word<D>(blk, p.y, word_of<D>(w)) = kw;
-          *value_word<D>(blk, p.y, word_of<D>(w)) = vw;
-          if (w == 0) *params<D>(blk, p.y) = par;
+        const Place pl = place[buf][there ? at[i].row : 0];
+        if (there && pl.page) {
+          uint8_t* blk = pl.page + at[i].h * BLK;
+          *key_word<D>(blk, pl.t, word_of<D>(w)) = kw;
+          *value_word<D>(blk, pl.t, word_of<D>(w)) = vw;
+          if (w == 0) *params<D>(blk, pl.t) = par;
         }
       }
     }
@@ -262,42 +285,51 @@ __global__ void __launch_bounds__(THREADS, 3) kv4_append_kernel(Kv4 c, const T* 
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS, 3) kv4_read_kernel(Kv4 c, T* __restrict__ k, T* __restrict__ v,
                                                               int64_t k_stride, int64_t v_stride, int max_rows,
-                                                              uint32_t m) {
-  constexpr int W = D / 8, WORKERS = WORK / W;
-  __shared__ int2 place[2][MAX_ROWS];
-  const int w = threadIdx.x % W, lane = threadIdx.x & 31, first = threadIdx.x / W;
-  const int stride = gridDim.x * max_rows;
+                                                              Steps steps) {
+  constexpr int W = D / 8, WORKERS = WORK / W, BLK = (int)kv4_block_bytes(D);
+  __shared__ Place place[2][MAX_ROWS];
+  const int w = threadIdx.x % W, lane = threadIdx.x & 31, worker = threadIdx.x / W;
+  const int stride = gridDim.x * max_rows, heads = c.kv_heads;
+  Pair first;
+  first.row = heads == 1 ? worker : (int)__umulhi((uint32_t)worker, steps.magic);
+  first.h = worker - first.row * heads;
   bool bad = false;
   int buf = 0;
-  row_places(c, blockIdx.x * max_rows, max_rows, place[0], &bad);
+  row_places<D>(c, blockIdx.x * max_rows, max_rows, place[0], &bad);
   for (int64_t row0 = (int64_t)blockIdx.x * max_rows; row0 < c.total_q; row0 += stride, buf ^= 1) {
     const int rows = (int)min((int64_t)max_rows, c.total_q - row0);
-    const int count = rows * c.kv_heads;
     __syncthreads();
     if (threadIdx.x >= WORK) {
-      if (row0 + stride < c.total_q) row_places(c, (int)(row0 + stride), max_rows, place[buf ^ 1], &bad);
+      if (row0 + stride < c.total_q) row_places<D>(c, (int)(row0 + stride), max_rows, place[buf ^ 1], &bad);
       continue;
     }
-    for (int e0 = 0; e0 < count; e0 += WORKERS * READ_BATCH) {
+    T *const kc = k + row0 * k_stride + 8 * w, *const vc = v + row0 * v_stride + 8 * w;
+    Pair p = first;
+    for (int e = 0; e < rows * heads; e += WORKERS * READ_BATCH) {
       uint32_t kw[READ_BATCH], vw[READ_BATCH];
       uint2 par[READ_BATCH];
-      int row[READ_BATCH], h[READ_BATCH];
+      Pair at[READ_BATCH];
 #pragma unroll
       for (int i = 0; i < READ_BATCH; ++i) {
-        const int e = min(e0 + first + i * WORKERS, count - 1);
-        row[i] = c.kv_heads == 1 ? e : (int)__umulhi((uint32_t)e, m);
-        h[i] = e - row[i] * c.kv_heads;
-        const int2 p = place[buf][row[i]];
-        if (p.x < 0) row[i] = -1;
-        uint8_t* blk = c.pages + ((int64_t)max(p.x, 0) * c.kv_heads + h[i]) * kv4_block_bytes(D);
-        kw[i] = *key_word<D>(blk, p.y, word_of<D>(w));
-        vw[i] = *value_word<D>(blk, p.y, word_of<D>(w));
-        par[i] = *params<D>(blk, p.y);
+        at[i] = p;
+        p.next(steps.dr, steps.dh, heads);
+        kw[i] = vw[i] = 0;
+        par[i] = make_uint2(0, 0);
+        if (at[i].row >= rows) continue;
+        const Place pl = place[buf][at[i].row];
+        if (pl.page) {
+          uint8_t* blk = pl.page + at[i].h * BLK;
+          kw[i] = *key_word<D>(blk, pl.t, word_of<D>(w));
+          vw[i] = *value_word<D>(blk, pl.t, word_of<D>(w));
+          par[i] = *params<D>(blk, pl.t);
+        } else {
+          at[i].row = rows;  // nothing is written
+        }
       }
 #pragma unroll
       for (int i = 0; i < READ_BATCH; ++i) {
-        if (e0 + i * WORKERS >= count) break;
-        const bool there = e0 + first + i * WORKERS < count && row[i] >= 0;
+        if (e + i * WORKERS >= rows * heads) break;
+        const bool there = at[i].row < rows;
         const auto give = [&](uint32_t word, uint32_t pr, T* to) {
           const uint32_t x = exchange<D>(word, lane), even = x & 0x0f0f0f0fu, odd = (x >> 4) & 0x0f0f0f0fu;
           const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&pr));
@@ -307,9 +339,8 @@ __global__ void __launch_bounds__(THREADS, 3) kv4_read_kernel(Kv4 c, T* __restri
             y[n] = __fmaf_rn(sb.x, __uint_as_float(__byte_perm(n & 1 ? odd : even, 0x4b000000u, 0x7650 | (n >> 1))) - 8388608.0f, sb.y);
           if (there) Eight<T>::store(to, y);
         };
-        const int64_t at = row0 + row[i];
-        give(kw[i], par[i].x, k + at * k_stride + (int64_t)h[i] * D + 8 * w);
-        give(vw[i], par[i].y, v + at * v_stride + (int64_t)h[i] * D + 8 * w);
+        give(kw[i], par[i].x, kc + (at[i].row * (int)k_stride + at[i].h * D));
+        give(vw[i], par[i].y, vc + (at[i].row * (int)v_stride + at[i].h * D));
       }
     }
   }
@@ -326,21 +357,25 @@ unsigned blocks(const Kv4& c, int rows) {
   const int64_t chunks = (c.total_q + (int64_t)rows - 1) / rows;
   return (unsigned)(chunks < 3 * 152 ? chunks : 3 * 152);
 }
-// e / kv_heads = umulhi(e, m) for e < 2^14 and at most 1024 heads
-uint32_t heads_magic(const Kv4& c) { return (uint32_t)(((uint64_t(1) << 32) + c.kv_heads - 1) / c.kv_heads); }
+template <int D>
+Steps steps_of(const Kv4& c) {
+  constexpr int workers = WORK / (D / 8);
+  return Steps{workers / c.kv_heads, workers % c.kv_heads,
+               (uint32_t)(((uint64_t(1) << 32) + c.kv_heads - 1) / c.kv_heads)};
+}
 
 template <int D, typename T>
 cudaError_t append(const Kv4& c, const void* k, const void* v, int64_t k_stride, int64_t v_stride, cudaStream_t st) {
   const int rows = chunk_rows(c);
   kv4_append_kernel<D, T><<<blocks(c, rows), THREADS, 0, st>>>(c, static_cast<const T*>(k), static_cast<const T*>(v),
-                                                               k_stride, v_stride, rows, heads_magic(c));
+                                                               k_stride, v_stride, rows, steps_of<D>(c));
   return cudaGetLastError();
 }
 template <int D, typename T>
 cudaError_t read(const Kv4& c, void* k, void* v, int64_t k_stride, int64_t v_stride, cudaStream_t st) {
   const int rows = chunk_rows(c);
   kv4_read_kernel<D, T><<<blocks(c, rows), THREADS, 0, st>>>(c, static_cast<T*>(k), static_cast<T*>(v), k_stride,
-                                                             v_stride, rows, heads_magic(c));
+                                                             v_stride, rows, steps_of<D>(c));
   return cudaGetLastError();
 }
 
