@@ -3,10 +3,9 @@
 // Both kernels move each vector once and are bound by bytes.
 //
 // Quantisation is exact: the code is the correctly rounded quotient (x - base) / step although only
-// fp32 is used. t = (x - base) * (1 / step) is within 3 roundings, 16 * 3 * 2^-24 < 2^-18, of the
-// quotient where it matters (below 16); unless t lies within 2^-17 of a half integer its rounding
-// is the quotient's. Near one, x is compared with the border step * (n + 1/2) + base itself: the
-// product is exact in fp32 (5 + 11 bits), and the sum's rounding error is known exactly.
+// fp32 is used. An approximate quotient decides unless it lies near a half integer (within several times
+// its error); there x is compared with the border step * (n + 1/2) + base itself: the product is exact
+// in fp32 (5 + 11 bits), and the sum's rounding error is known exactly.
 #include "kv4.cuh"
 
 #include <cuda_bf16.h>
@@ -17,7 +16,8 @@ namespace {
 
 constexpr int WORK = 256, THREADS = WORK + 32;
 constexpr float kKvMax = 61440.0f;
-constexpr float kNear = 0.5f - 7.62939453125e-6f;  // 2^-17 below a half
+constexpr float kNear = 0.5f - 7.62939453125e-6f;       // 2^-17 below a half
+constexpr float kNearPlain = 0.5f - 1.52587890625e-5f;  // 2^-16
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: x + kMagic holds rne(x) in its low bits
 
 // NaN-keeping minimum and maximum (fminf and fmaxf drop a NaN)
@@ -40,6 +40,28 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// two fp32 lanes an instruction
+__device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // rne((x - base) / step) where the quotient lies next to n + 1/2
@@ -173,6 +195,20 @@ __device__ __forceinline__ uint2* params(uint8_t* blk, int t) {
   return reinterpret_cast<uint2*>(blk + kKvPage * D) + kv4_rho(t);
 }
 
+// The codes one by one, with every care: the clamp, and the borders.
+__device__ __noinline__ uint32_t careful_codes(const float (&x)[8], float base, float step) {
+  const float inv = __frcp_rn(step);
+  uint32_t word = 0;
+#pragma unroll 1
+  for (int n = 7; n >= 0; --n) {
+    const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[n], base), inv), 0.0f), 15.0f);
+    float r = __fsub_rn(__fadd_rn(t, kMagic), kMagic);
+    if (fabsf(t - r) > kNear) r = border_code(x[n], base, step, floorf(t));
+    word = word << 4 | (uint32_t)r;
+  }
+  return word;
+}
+
 // Quantises a vector, 8 numbers a lane of W: the lane's codes (number k in nibble k) and the parameters.
 template <int W>
 __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* par) {
@@ -183,41 +219,34 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* par)
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
-  // (a number beyond +-61440 needs no clamp of its own: its code is clamped below)
-  const float lo_c = max_nan(min_nan(lo, kKvMax), -kKvMax), hi_c = max_nan(min_nan(hi, kKvMax), -kKvMax);
-  const __half base_h = __float2half_rn(lo_c), step_h = __float2half_rn(__fdiv_rn(__fsub_rn(hi_c, lo_c), 15.0f));
-  const float base = __half2float(base_h), step = __half2float(step_h);
-  *par = (uint32_t)__half_as_ushort(step_h) | (uint32_t)__half_as_ushort(base_h) << 16;
+  // (a number beyond +-61440 needs no clamp of its own: its code is clamped)
+  const float range = __fsub_rn(max_nan(min_nan(hi, kKvMax), -kKvMax), max_nan(min_nan(lo, kKvMax), -kKvMax));
+  // range / 15, correctly rounded: one correction by the exact remainder (Markstein)
+  float q = __fmul_rn(range, 1.0f / 15.0f);
+  q = __fmaf_rn(__fmaf_rn(q, -15.0f, range), 1.0f / 15.0f, q);
+  const __half2 sb = __halves2half2(__float2half_rn(q), __float2half_rn(max_nan(min_nan(lo, kKvMax), -kKvMax)));
+  const float step = __low2float(sb), base = __high2float(sb);
+  *par = *reinterpret_cast<const uint32_t*>(&sb);
+  // t = x inv - base inv: within 2^-23 (2 |x inv| + 2 |base inv|) < 2^-16 of the quotient where the base
+  // is less than 16 steps off zero; else, and where a quotient may need the clamp or lies near a border,
+  // the careful way
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+  const float off = -base * inv;
+  float near = 0.0f;  // the largest distance from an integer
   uint32_t word = 0;
-  if (step > 0.0f) {
-    const float inv = __frcp_rn(step);
-    // quotients outside (-0.49, 15.49) need the clamp: where the fp16 base or step is far off the ends
-    const bool clamp = !(__fmul_rn(__fsub_rn(lo, base), inv) > -0.49f && __fmul_rn(__fsub_rn(hi, base), inv) < 15.49f);
-    float t[8];
+  const uint64_t inv2 = f2pack(inv, inv), off2 = f2pack(off, off), magic2 = f2pack(kMagic, kMagic),
+                 minus2 = f2pack(-kMagic, -kMagic), neg2 = f2pack(-1.0f, -1.0f);
 #pragma unroll
-    for (int n = 0; n < 8; ++n) t[n] = __fmul_rn(__fsub_rn(x[n], base), inv);
-    if (clamp) {
-#pragma unroll
-      for (int n = 0; n < 8; ++n) t[n] = fminf(fmaxf(t[n], 0.0f), 15.0f);
-    }
-    float off = 0.0f;  // the largest distance from an integer
-#pragma unroll
-    for (int n = 7; n >= 0; --n) {
-      const float r = __fadd_rn(t[n], kMagic);
-      off = fmaxf(off, fabsf(t[n] - __fsub_rn(r, kMagic)));
-      word = word * 16u + __float_as_uint(r);
-    }
-    word -= 0x4b400000u * 0x11111111u;  // the eight kMagic
-    if (off > kNear) {
-      word = 0;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        float r = __fsub_rn(__fadd_rn(t[n], kMagic), kMagic);
-        if (fabsf(t[n] - r) > kNear) r = border_code(x[n], base, step, floorf(t[n]));
-        word |= (uint32_t)r << (4 * n);
-      }
-    }
+  for (int n = 6; n >= 0; n -= 2) {
+    const uint64_t t = fma2(f2pack(x[n], x[n + 1]), inv2, off2), r = add2(t, magic2);
+    const float2 d = f2unpack(fma2(add2(r, minus2), neg2, t)), c = f2unpack(r);
+    near = fmaxf(near, fmaxf(fabsf(d.x), fabsf(d.y)));
+    word = (word * 16u + __float_as_uint(c.y)) * 16u + __float_as_uint(c.x);
   }
+  word -= 0x4b400000u * 0x11111111u;  // the eight kMagic
+  const bool plain = near < kNearPlain && fabsf(off) < 16.0f && fmaf(lo, inv, off) > -0.49f && fmaf(hi, inv, off) < 15.49f;
+  if (!plain) word = step > 0.0f ? careful_codes(x, base, step) : 0;
   return word;
 }
 
