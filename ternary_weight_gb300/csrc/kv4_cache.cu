@@ -124,25 +124,31 @@ struct Steps {
   int dr, dh;      // WORKERS / heads, WORKERS % heads
   uint32_t magic;  // worker / heads = umulhi(worker, magic)
 };
-// nibble j of lane i of each group of 8 lanes <-> nibble i of lane j; lanes i and i ^ 1 are `gap` apart
-__device__ __forceinline__ uint32_t transpose_nibbles(uint32_t x, int lane, int gap) {
-  const int i = lane / gap;
-  uint32_t y = __shfl_xor_sync(0xffffffffu, x, 4 * gap);
-  x = i & 4 ? (x & 0xffff0000u) | (y >> 16) : (x & 0xffffu) | (y << 16);
-  y = __shfl_xor_sync(0xffffffffu, x, 2 * gap);
-  x = i & 2 ? (x & 0xff00ff00u) | ((y >> 8) & 0x00ff00ffu) : (x & 0x00ff00ffu) | ((y << 8) & 0xff00ff00u);
-  y = __shfl_xor_sync(0xffffffffu, x, gap);
-  return i & 1 ? (x & 0xf0f0f0f0u) | ((y >> 4) & 0x0f0f0f0fu) : (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
-}
-// Lane w has the codes of dimensions 8 w + k in nibble k; the word that it then holds. D = 128: lanes of
-// like parity hold nibbles n = w / 2 of words 8 (w & 1) + k, so lane w gets word 8 (w & 1) + w / 2.
+// The transpose: nibble j of lane i of 8 lanes <-> nibble i of lane j, lanes i and i ^ 1 `gap` apart, in
+// three exchanges (halves, bytes, nibbles). Lane w has the codes of dimensions 8 w + k in nibble k. With
+// D = 128 lanes of like parity hold nibbles n = w / 2 of words 8 (w & 1) + k, so gap is 2 and lane w ends
+// with word 8 (w & 1) + w / 2; with D = 64 gap is 1 and lane w ends with word w.
+template <int D>
+struct Exchange {
+  uint32_t halves, bytes, shift, keep;  // byte selectors, rotation and mask of the lane
+  __device__ __forceinline__ explicit Exchange(int w) {
+    const int i = D == 128 ? w >> 1 : w;
+    halves = i & 4 ? 0x3276 : 0x5410;
+    bytes = i & 2 ? 0x3715 : 0x6240;
+    shift = i & 1 ? 28 : 4;
+    keep = i & 1 ? 0xf0f0f0f0u : 0x0f0f0f0fu;
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+    constexpr int gap = D == 128 ? 2 : 1;
+    x = __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 4 * gap), halves);
+    x = __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 2 * gap), bytes);
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, gap);
+    return (x & keep) | (__funnelshift_l(y, y, shift) & ~keep);
+  }
+};
 template <int D>
 __device__ __forceinline__ int word_of(int w) {
   return D == 128 ? 8 * (w & 1) + (w >> 1) : w;
-}
-template <int D>
-__device__ __forceinline__ uint32_t exchange(uint32_t x, int lane) {
-  return transpose_nibbles(x, D == 128 ? lane & 15 : lane & 7, D == 128 ? 2 : 1);
 }
 
 template <typename T>
@@ -256,7 +262,8 @@ __global__ void __launch_bounds__(THREADS, 3) kv4_append_kernel(Kv4 c, const T* 
                                                                 Steps steps) {
   constexpr int W = D / 8, WORKERS = WORK / W, BLK = (int)kv4_block_bytes(D);
   __shared__ Place place[2][MAX_ROWS];
-  const int w = threadIdx.x % W, lane = threadIdx.x & 31, worker = threadIdx.x / W;
+  const int w = threadIdx.x % W, worker = threadIdx.x / W;
+  const Exchange<D> ex(w);
   const int stride = gridDim.x * max_rows, heads = c.kv_heads;
   Pair first;
   first.row = heads == 1 ? worker : (int)__umulhi((uint32_t)worker, steps.magic);
@@ -295,9 +302,9 @@ __global__ void __launch_bounds__(THREADS, 3) kv4_append_kernel(Kv4 c, const T* 
         float x[8];
         uint2 par;
         in[i][0].get(x);
-        const uint32_t kw = exchange<D>(quantise<W>(x, &par.x), lane);
+        const uint32_t kw = ex(quantise<W>(x, &par.x));
         in[i][1].get(x);
-        const uint32_t vw = exchange<D>(quantise<W>(x, &par.y), lane);
+        const uint32_t vw = ex(quantise<W>(x, &par.y));
         const Place pl = place[buf][there ? at[i].row : 0];
         if (there && pl.page) {
           uint8_t* blk = pl.page + at[i].h * BLK;
@@ -317,7 +324,8 @@ __global__ void __launch_bounds__(THREADS, 3) kv4_read_kernel(Kv4 c, T* __restri
                                                               Steps steps) {
   constexpr int W = D / 8, WORKERS = WORK / W, BLK = (int)kv4_block_bytes(D);
   __shared__ Place place[2][MAX_ROWS];
-  const int w = threadIdx.x % W, lane = threadIdx.x & 31, worker = threadIdx.x / W;
+  const int w = threadIdx.x % W, worker = threadIdx.x / W;
+  const Exchange<D> ex(w);
   const int stride = gridDim.x * max_rows, heads = c.kv_heads;
   Pair first;
   first.row = heads == 1 ? worker : (int)__umulhi((uint32_t)worker, steps.magic);
@@ -360,12 +368,17 @@ __global__ void __launch_bounds__(THREADS, 3) kv4_read_kernel(Kv4 c, T* __restri
         if (e + i * WORKERS >= rows * heads) break;
         const bool there = at[i].row < rows;
         const auto give = [&](uint32_t word, uint32_t pr, T* to) {
-          const uint32_t x = exchange<D>(word, lane), even = x & 0x0f0f0f0fu, odd = (x >> 4) & 0x0f0f0f0fu;
+          const uint32_t x = ex(word), even = x & 0x0f0f0f0fu, odd = (x >> 4) & 0x0f0f0f0fu;
           const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&pr));
           float y[8];
 #pragma unroll
-          for (int n = 0; n < 8; ++n)  // 2^23 + code, exactly
-            y[n] = __fmaf_rn(sb.x, __uint_as_float(__byte_perm(n & 1 ? odd : even, 0x4b000000u, 0x7650 | (n >> 1))) - 8388608.0f, sb.y);
+          for (int n = 0; n < 8; n += 2) {  // 2^23 + code, exactly
+            const uint32_t c0 = __byte_perm(even, 0x4b000000u, 0x7650 | (n >> 1)), c1 = __byte_perm(odd, 0x4b000000u, 0x7650 | (n >> 1));
+            const uint64_t code = add2(f2pack(__uint_as_float(c0), __uint_as_float(c1)), f2pack(-8388608.0f, -8388608.0f));
+            const float2 t = f2unpack(fma2(code, f2pack(sb.x, sb.x), f2pack(sb.y, sb.y)));
+            y[n] = t.x;
+            y[n + 1] = t.y;
+          }
           if (there) Eight<T>::store(to, y);
         };
         give(kw[i], par[i].x, kc + (at[i].row * (int)k_stride + at[i].h * D));
