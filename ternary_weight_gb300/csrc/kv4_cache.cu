@@ -257,7 +257,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* par)
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(THREADS, 3) kv4_append_kernel(Kv4 c, const T* __restrict__ k, const T* __restrict__ v,
+__global__ void __launch_bounds__(THREADS, 4) kv4_append_kernel(Kv4 c, const T* __restrict__ k, const T* __restrict__ v,
                                                                 int64_t k_stride, int64_t v_stride, int max_rows,
                                                                 Steps steps) {
   constexpr int W = D / 8, WORKERS = WORK / W, BLK = (int)kv4_block_bytes(D);
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 3) kv4_append_kernel(Kv4 c, const T* 
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(THREADS, 3) kv4_read_kernel(Kv4 c, T* __restrict__ k, T* __restrict__ v,
+__global__ void __launch_bounds__(THREADS, 4) kv4_read_kernel(Kv4 c, T* __restrict__ k, T* __restrict__ v,
                                                               int64_t k_stride, int64_t v_stride, int max_rows,
                                                               Steps steps) {
   constexpr int W = D / 8, WORKERS = WORK / W, BLK = (int)kv4_block_bytes(D);
@@ -391,13 +391,13 @@ __global__ void __launch_bounds__(THREADS, 3) kv4_read_kernel(Kv4 c, T* __restri
 
 // rows of a chunk: few enough that all SMs have several blocks
 int chunk_rows(const Kv4& c) {
-  const int r = c.total_q / (3 * 152);
+  const int r = c.total_q / (4 * 152);
   return r < 1 ? 1 : r > MAX_ROWS ? MAX_ROWS : r;
 }
-// blocks: three an SM (what fits), each with as many chunks as the next
+// blocks: four an SM (what fits), each with as many chunks as the next
 unsigned blocks(const Kv4& c, int rows) {
   const int64_t chunks = (c.total_q + (int64_t)rows - 1) / rows;
-  return (unsigned)(chunks < 3 * 152 ? chunks : 3 * 152);
+  return (unsigned)(chunks < 4 * 152 ? chunks : 4 * 152);
 }
 template <int D>
 Steps steps_of(const Kv4& c) {
