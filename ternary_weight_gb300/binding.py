@@ -467,6 +467,7 @@ class KV4Cache:
             raise ValueError("pages must be %d bytes of uint8" % need)
         _require_cuda(pages)
         self.pages, self.n_pages, self.kv_heads, self.head_dim = pages, n_pages, kv_heads, head_dim
+        self.device = pages.device
         self._desc = _KV4CacheDesc(pages.data_ptr(), n_pages, kv_heads, head_dim)
         self._ref = ctypes.c_void_p(ctypes.addressof(self._desc))
 
@@ -496,6 +497,23 @@ class KV4Batch:
         self._ws = {}  # attention workspace bytes by cache and query heads
 
 
+# A decode step makes these calls for every layer, and their kernels take a few microseconds: the helpers
+# below look everything up once and touch each tensor's properties once.
+_kv4_torch = None  # (torch, its dtypes -> BITNET dtypes, torch.bfloat16, raw current stream by device index)
+
+
+def _kv4_setup():
+    global _kv4_torch
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        def raw(index):
+            return torch.cuda.current_stream(index).cuda_stream
+    _kv4_torch = torch, {torch.float32: BITNET_F32, torch.bfloat16: BITNET_BF16}, torch.bfloat16, raw
+    return _kv4_torch
+
+
 def _kv4_rows(t, rows, heads, dim):
     """Checks a rows x heads x dim tensor whose heads lie one after another; its row stride."""
     if t.shape != (rows, heads, dim):
@@ -506,48 +524,56 @@ def _kv4_rows(t, rows, heads, dim):
     return s[0] if rows > 1 else heads * dim
 
 
-def _on_stream(stream):
-    """Allocations made for a call on a given stream belong to that stream."""
-    import contextlib
-
-    import torch
-
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _kv4_empty(torch, shape, dtype, device, stream):
+    """An output of a call on `stream` belongs to that stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def kv4_append(cache, batch, k, v, stream=None):
     """Quantise the batch's keys and values (total_q x kv_heads x head_dim, fp32 or bf16 CUDA; rows may
     be strided, e.g. slices of a fused q/k/v row) to 4 bits and write them to their places."""
-    dt = _act_dtype(k)
-    if v.dtype != k.dtype:
-        raise ValueError("k and v must have the same dtype")
-    ks = _kv4_rows(k, batch.total_q, cache.kv_heads, cache.head_dim)
-    vs = _kv4_rows(v, batch.total_q, cache.kv_heads, cache.head_dim)
-    if not batch.total_q:
-        return
-    _check(lib().bitnet_kv4_append(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs, _stream(stream)),
-           "bitnet_kv4_append")
+    _, dtypes, _, raw = _kv4_torch or _kv4_setup()
+    dt = dtypes.get(k.dtype)
+    if dt is None or v.dtype != k.dtype:
+        raise ValueError("k and v must both be float32 or bfloat16")
+    rows, heads, dim = batch.total_q, cache.kv_heads, cache.head_dim
+    ks, vs = _kv4_rows(k, rows, heads, dim), _kv4_rows(v, rows, heads, dim)
+    if rows:
+        st = lib().bitnet_kv4_append(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs,
+                                     raw(k.get_device()) if stream is None else stream.cuda_stream)
+        if st:
+            raise BitnetError(st, "bitnet_kv4_append")
 
 
 def kv4_read(cache, batch, dtype=None, k=None, v=None, stream=None):
     """Read the batch's tokens back from the cache as (k, v), each total_q x kv_heads x head_dim of
     ``dtype`` (fp32 or bf16, default bf16; or that of the given k and v, which are written)."""
-    import torch
-
-    shape = (batch.total_q, cache.kv_heads, cache.head_dim)
+    torch, dtypes, bf16, raw = _kv4_torch or _kv4_setup()
+    rows, heads, dim = batch.total_q, cache.kv_heads, cache.head_dim
+    ks = vs = heads * dim
     if k is None or v is None:
-        with _on_stream(stream):
-            like = k if k is not None else v
-            dtype = like.dtype if like is not None else dtype if dtype is not None else torch.bfloat16
-            k = torch.empty(shape, dtype=dtype, device=cache.pages.device) if k is None else k
-            v = torch.empty(shape, dtype=dtype, device=cache.pages.device) if v is None else v
-    dt = _act_dtype(k)
-    if v.dtype != k.dtype or (dtype is not None and dtype != k.dtype):
-        raise ValueError("k and v must have the same dtype, the one asked for")
-    ks, vs = _kv4_rows(k, *shape), _kv4_rows(v, *shape)
-    if batch.total_q:
-        _check(lib().bitnet_kv4_read(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs, _stream(stream)),
-               "bitnet_kv4_read")
+        given = k if k is not None else v
+        if dtype is None:
+            dtype = bf16 if given is None else given.dtype
+    if k is None:
+        k = _kv4_empty(torch, (rows, heads, dim), dtype, cache.device, stream)
+    else:
+        ks = _kv4_rows(k, rows, heads, dim)
+    if v is None:
+        v = _kv4_empty(torch, (rows, heads, dim), dtype, cache.device, stream)
+    else:
+        vs = _kv4_rows(v, rows, heads, dim)
+    dt = dtypes.get(k.dtype)
+    if dt is None or v.dtype != k.dtype or (dtype is not None and dtype != k.dtype):
+        raise ValueError("k and v must both be float32 or bfloat16, as asked for")
+    if rows:
+        st = lib().bitnet_kv4_read(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs,
+                                   raw(cache.device.index) if stream is None else stream.cuda_stream)
+        if st:
+            raise BitnetError(st, "bitnet_kv4_read")
     return k, v
 
 
@@ -564,32 +590,33 @@ def kv4_attention(cache, batch, q, scale, window=0, sinks=0, out=None, workspace
     or j > p - window or j < sinks). Returns total_q x q_heads x head_dim bf16 (``out`` if given).
     ``workspace``: a uint8 CUDA tensor of at least kv4_attention_workspace_size bytes, allocated
     here if not given."""
-    import torch
-
-    dt = _act_dtype(q)
-    if q.dim() != 3:
-        raise ValueError("q must be total_q x q_heads x head_dim")
-    heads = q.shape[1]
-    qs = _kv4_rows(q, batch.total_q, heads, cache.head_dim)
-    key = (heads, cache.kv_heads, cache.head_dim)
+    torch, dtypes, bf16, raw = _kv4_torch or _kv4_setup()
+    dt = dtypes.get(q.dtype)
+    if dt is None or q.dim() != 3:
+        raise ValueError("q must be total_q x q_heads x head_dim, float32 or bfloat16")
+    rows, heads, dim = batch.total_q, q.shape[1], cache.head_dim
+    qs = _kv4_rows(q, rows, heads, dim)
+    key = (heads, cache.kv_heads, dim)
     need = batch._ws.get(key)
     if need is None:
         need = batch._ws[key] = kv4_attention_workspace_size(cache, batch, heads)
-    if out is None or (workspace is None and need):
-        with _on_stream(stream):
-            if out is None:
-                out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-            if workspace is None and need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if out.dtype != torch.bfloat16:
+    if out is None:
+        out, os_ = _kv4_empty(torch, (rows, heads, dim), bf16, cache.device, stream), heads * dim
+    elif out.dtype != bf16:
         raise ValueError("out must be bfloat16")
-    os_ = _kv4_rows(out, batch.total_q, heads, cache.head_dim)
-    _require_cuda(workspace)
-    if batch.total_q:
-        ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None \
-            else (None, 0)
-        _check(lib().bitnet_kv4_attention(cache._ref, batch._ref, q.data_ptr(), dt, heads, qs, float(scale),
-                                          int(window), int(sinks), out.data_ptr(), os_, ws_ptr, ws_bytes,
-                                          _stream(stream)),
-               "bitnet_kv4_attention")
+    else:
+        os_ = _kv4_rows(out, rows, heads, dim)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        _require_cuda(workspace)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace, ws_bytes = _kv4_empty(torch, need, torch.uint8, cache.device, stream), need
+        ws_ptr = workspace.data_ptr()
+    if rows:
+        st = lib().bitnet_kv4_attention(cache._ref, batch._ref, q.data_ptr(), dt, heads, qs, scale, window, sinks,
+                                        out.data_ptr(), os_, ws_ptr, ws_bytes,
+                                        raw(q.get_device()) if stream is None else stream.cuda_stream)
+        if st:
+            raise BitnetError(st, "bitnet_kv4_attention")
     return out
