@@ -22,6 +22,9 @@
 // of the other's two products. The running maximum is moved (and O rescaled) only where a row's has
 // grown by more than 2^8.
 //
+// With at most 128 rows both slots hold the same queries and take the steps in turn, so that the two
+// chains still overlap; their results are joined at the end as those of two halves of the cache.
+//
 // Where the query tiles are fewer than the SMs, the cache positions are cut into `splits` parts whose
 // results a second kernel joins in order.
 #include "kv4.cuh"
@@ -47,8 +50,16 @@ struct Prompt {
   static constexpr int SMEM = 2 * Q_TILE + 2 * K_STAGE + 2 * V_STAGE + 1024;
   static constexpr uint32_t IDESC_S = make_idesc_f16_f32(128, TOK), IDESC_O = make_idesc_f16_f32(128, D);
 };
-// tensor memory columns: scores (and weights over them) and outputs of the two tiles
+// Tensor memory columns of the two slots: scores (128 each), outputs (D each), weights (64 each). With
+// D = 128 that is more than there is, and a half of the weights lies over the first half of its scores:
+// the next scores then have to wait for the product that reads the weights. With D = 64 the weights have
+// columns of their own, and the next scores only wait for the last ones to be read.
 constexpr uint32_t TM_S = 0, TM_O = 256;
+template <int D>
+struct Weights {
+  static constexpr bool APART = D == 64;
+  static constexpr uint32_t AT = APART ? 384 : TM_S, SLOT = APART ? 64 : 128, HALF = APART ? 32 : 64;
+};
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
@@ -143,13 +154,17 @@ __device__ __forceinline__ void mma_f16_ts_lo(uint32_t d_tmem, uint32_t a_tmem, 
       "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
@@ -287,6 +302,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
   const int all = (it.np + 1) / 2;  // steps of the item, then of this part of it
   const int j0 = (int)((int64_t)all * split / parts.splits), j1 = (int)((int64_t)all * (split + 1) / parts.splits);
   const int steps = j1 - j0;
+  const bool twin = it.rows <= 128;  // one tile of rows, in both slots
   bool abort = false;
 
   if (warp < 16) {
@@ -370,7 +386,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       if (lane == 0) mbar_arrive(&q_full);
       mbar_wait_warp(&q_full, 0, &abort);
     }
-    const int w0 = tile * 128 + quarter * 32, r = w0 + lane;  // the warp's first row, the thread's row
+    const int w0 = (twin ? 0 : tile * 128) + quarter * 32, r = w0 + lane;  // the warp's first row, the thread's row
+    const int mine = twin ? (steps + 1 - tile) / 2 : steps;                // steps of this slot
     const bool there = r < it.rows;
     const float c1 = row_c1[r];
     const int pos0 = it.s.len - it.s.n + it.tok0;
@@ -379,13 +396,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     const int pos_first = pos0 + token_of(w0);
     const int64_t low_last = (int64_t)pos0 + token_of(max(min(it.rows, w0 + 32) - 1, 0)) - a.window + 1;
     const uint32_t lane0 = (uint32_t)(quarter * 32) << 16;
-    // this page's scores; the weights lie over the first half of them
+    // this page's scores and weights
+    using WT = Weights<D>;
+    const uint32_t tp = tmem + lane0 + WT::AT + (uint32_t)tile * WT::SLOT + (uint32_t)half * WT::HALF;
     const uint32_t ts = tmem + lane0 + TM_S + (uint32_t)(tile * 128 + half * 64);
     const uint32_t to = tmem + lane0 + TM_O + (uint32_t)(tile * D + half * (D / 2));
+    const int xr = tile * 128 + quarter * 32 + lane;  // the thread's place in row_x
     const int pair = 1 + tile * 4 + quarter;  // barrier of the two warps that share rows
     float m = kNegInf, l = 0.0f;
-    for (int j = 0; j < steps; ++j) {
-      const int first = page_first(it, 2 * (j0 + j) + half);
+    for (int j = 0; j < mine; ++j) {
+      const int first = page_first(it, 2 * (j0 + (twin ? 2 * j + tile : j)) + half);
       const bool whole = first + kKvPage - 1 <= pos_first && (first >= low_last || first + kKvPage <= a.sinks);
       // (no way out of the loop when a wait gives up: the pair's barriers have to match)
       mbar_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort);
@@ -406,27 +426,33 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         }
         tmem_st_wait();
       }
+      // 16 columns at a time, the next ones on their way
+      uint32_t v[2][16];
       float mx4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll 1
-      for (int ch = 0; ch < 2; ++ch) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(ts + 32 * ch, v);
-        tmem_ld_wait();
+      tmem_ld_x16(ts, v[0]);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(v[k]));
+      for (int ch = 0; ch < 4; ++ch) {
+        tmem_ld_wait();
+        tmem_ld_x16(ts + 16 * ((ch + 1) & 3), v[(ch + 1) & 1]);  // at last the first ones again
+#pragma unroll
+        for (int k = 0; k < 16; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(v[ch & 1][k]));
       }
       // the other page's maximum, from the other warp of these rows
       float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      row_x[j & 1][half][r] = mx;
+      row_x[j & 1][half][xr] = mx;
       named_bar_sync(pair, 64);
-      mx = fmaxf(m, fmaxf(mx, row_x[j & 1][half ^ 1][r]));
+      mx = fmaxf(m, fmaxf(mx, row_x[j & 1][half ^ 1][xr]));
       // a row's first scores, or scores far above the maximum in use: move it
       const bool far = mx > m && (m == kNegInf || c1 * (mx - m) > kSlack);
       if (__any_sync(0xffffffffu, far)) {
         const float f = m == kNegInf ? (mx == kNegInf ? 1.0f : 0.0f) : exp2_approx(c1 * (m - mx));
         m = mx;
         l *= f;
-        if (j > 0) {  // the scores of this step were computed after the last step's product with V
+        if (j > 0) {  // after the last step's product with V
+          if (WT::APART) {
+            mbar_wait_warp(&pv_done[tile], (uint32_t)(j - 1) & 1u, &abort);
+            tc_fence_after();
+          }
 #pragma unroll 1
           for (int ch = 0; ch < D / 64; ++ch) {
             uint32_t v[32];
@@ -438,22 +464,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
           }
         }
       }
+      if (WT::APART && j > 0) mbar_wait_warp(&pv_done[tile], (uint32_t)(j - 1) & 1u, &abort);  // its weights are read
       const float off = m == kNegInf ? 0.0f : -c1 * m;
       const uint64_t c2 = f2pack(c1, c1), off2 = f2pack(off, off);
       uint64_t l2[2] = {0, 0};
-#pragma unroll 1
-      for (int ch = 0; ch < 2; ++ch) {
-        uint32_t v[32], w[16];
-        tmem_ld_32x32b_x32(ts + 32 * ch, v);
-        tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 t = f2unpack(fma2(f2pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, off2));
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t w[8];
+        tmem_ld_wait();
+        if (ch < 3) tmem_ld_x16(ts + 16 * (ch + 1), v[(ch + 1) & 1]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t(&u)[16] = v[ch & 1];
+          const float2 t = f2unpack(fma2(f2pack(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])), c2, off2));
           const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
           l2[k & 1] = add2(l2[k & 1], f2pack(p0, p1));
           w[k] = pack_half2(p0, p1);
         }
-        tmem_st_x16(ts + 16 * ch, w);
+        tmem_st_x8(tp + 8 * ch, w);
       }
       const float2 la = f2unpack(add2(l2[0], l2[1]));
       l += la.x + la.y;
@@ -462,25 +490,69 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[tile]);
     }
-    if (steps > 0) mbar_wait_warp(&pv_done[tile], (uint32_t)(steps - 1) & 1u, &abort);
+    if (mine > 0) mbar_wait_warp(&pv_done[tile], (uint32_t)(mine - 1) & 1u, &abort);
     tc_fence_after();
-    row_x[steps & 1][half][r] = l;
+    row_x[mine & 1][half][xr] = l;
     named_bar_sync(pair, 64);
-    l = half ? row_x[steps & 1][0][r] + l : l + row_x[steps & 1][1][r];
+    l = half ? row_x[mine & 1][0][xr] + l : l + row_x[mine & 1][1][xr];
+    // twins: slot 1 leaves its sums where the keys were (128 rows x D fp32, 16-byte chunk c of row r at
+    // c ^ (r & 7)) and its maximum and sum of weights in row_x; slot 0 takes them in
+    float f0 = 1.0f, f1 = 0.0f;
+    const uint32_t twin_s = k_s + (uint32_t)(quarter * 32 + lane) * (D * 4);
+    if (twin) {
+      named_bar_sync(9, 512);  // every product is done
+      if (tile == 1) {
+        if (half == 0) row_x[0][0][xr] = m, row_x[0][1][xr] = l;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 64; ++ch) {
+          uint32_t v[32];
+          if (mine > 0 && !abort) {
+            tmem_ld_32x32b_x32(to + 32 * ch, v);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            sts128(twin_s + (((half * (D / 8) + 8 * ch + k) ^ (lane & 7)) << 4), v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+      }
+      named_bar_sync(9, 512);
+      if (tile == 0) {
+        const float m1 = row_x[0][0][xr + 128], l1 = row_x[0][1][xr + 128], mx = fmaxf(m, m1);
+        const float ref = mx == kNegInf ? 0.0f : mx;
+        f0 = exp2_approx(c1 * (m - ref));
+        f1 = exp2_approx(c1 * (m1 - ref));
+        m = mx;
+        l = l * f0 + l1 * f1;
+      }
+    }
     const float norm = parts.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
     float* part = parts.splits > 1 ? parts.sums + (item_no * parts.splits + split) * (ROWS * (D + 2)) : nullptr;
     // rows go out through this tile's query operand, which no product reads any more: 16-byte chunk c of
     // row r at (c ^ (r & 7)), so that a row leaves in one piece
     const uint32_t stage = q_s + tile * P::Q_TILE + quarter * (32 * D * 2);
+    const bool gives = !twin || tile == 0;
 #pragma unroll 1
-    for (int ch = 0; ch < D / 64; ++ch) {
+    for (int ch = 0; ch < D / 64 && gives; ++ch) {
       uint32_t v[32];
-      if (steps > 0 && !abort) {
+      if (mine > 0 && !abort) {
         tmem_ld_32x32b_x32(to + 32 * ch, v);
         tmem_ld_wait();
       } else {
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = 0;
+      }
+      if (twin) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint4 o = lds128(twin_s + (((half * (D / 8) + 8 * ch + k) ^ (lane & 7)) << 4));
+          v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * f0 + __uint_as_float(o.x) * f1);
+          v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * f0 + __uint_as_float(o.y) * f1);
+          v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * f0 + __uint_as_float(o.z) * f1);
+          v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * f0 + __uint_as_float(o.w) * f1);
+        }
       }
       const int d = half * (D / 2) + 32 * ch;
       if (part) {
@@ -503,7 +575,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         }
       }
     }
-    if (part) {
+    if (!gives) {
+    } else if (part) {
       if (there && half == 0) {
         part[ROWS * D + r] = m * c1;
         part[ROWS * (D + 1) + r] = l;
@@ -591,14 +664,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       const int w = lane % W, grp = lane / W, units = UPP * pages;
       uint32_t code[8], par[8], code_n[8], par_n[8];
       const auto load = [&](int u, int id, uint32_t(&cd)[8], uint32_t(&pr)[8]) {
-        const int t0 = (u % UPP) * TPU + 8 * grp, first = page_first(it, 2 * j0 + u / UPP) + t0;
+        const int t0 = (u % UPP) * TPU + 8 * grp;
         const uint8_t* p = block(id) + kKvPage * (D / 2) + t0 * (D / 2);
-        const uint8_t* q = block(id) + kKvPage * D + t0 * 8 + 4;
+        const uint8_t* q = p + kKvPage * (D / 2) - t0 * (D / 2) + t0 * 8 + 4;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           cd[k] = __ldg(reinterpret_cast<const uint32_t*>(p + k * (D / 2)) + (D == 128 && (k & 2) ? w ^ (W / 2) : w));
-          const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(q + kv4_rho(k) * 8));
-          pr[k] = first + k < it.s.len ? v : 0;  // no value where nothing is cached
+          pr[k] = __ldg(reinterpret_cast<const uint32_t*>(q + kv4_rho(k) * 8));
         }
       };
       int u = warp - 20;
@@ -615,6 +687,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         }
         const uint32_t at = v_s + st * P::V_STAGE + ((u / UPP) & 1) * (D * 128);
         const int ch = ((u % UPP) * TPU >> 3) + grp;
+        const int left = it.s.len - page_first(it, 2 * j0 + u / UPP) - ((u % UPP) * TPU + 8 * grp);
         uint32_t step[4], bs[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -623,6 +696,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
           const uint32_t z = hadd2(hsub2(step[k], step[k]), hsub2(bs[k], bs[k]));
           uint32_t ok;  // all ones where finite
           asm("set.eq.u32.f16x2 %0, %1, %2;" : "=r"(ok) : "r"(z), "r"(0u));
+          if (left < 2 * k + 2) ok &= left < 2 * k + 1 ? 0u : 0xffffu;  // no value where nothing is cached
           step[k] &= ok;
           bs[k] &= ok;
         }
@@ -655,8 +729,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     const bool leader = elect_one();
     const uint64_t qd = make_sw128_kmajor_desc(q_s), kd = make_sw128_kmajor_desc(k_s), vd = make_sw128_kmajor_desc(v_s);
     const uint32_t hi = (uint32_t)(qd >> 32), q_lo = (uint32_t)qd, k_lo = (uint32_t)kd, v_lo = (uint32_t)vd;
-    const auto scores = [&](int t, int j) {
-      const uint32_t ad = q_lo + (uint32_t)(t * (P::Q_TILE >> 4)), bd = k_lo + (uint32_t)((j & 1) * (P::K_STAGE >> 4));
+    const auto scores = [&](int t, int j, bool frees) {
+      const uint32_t ad = q_lo + (uint32_t)(twin ? 0 : t * (P::Q_TILE >> 4)), bd = k_lo + (uint32_t)((j & 1) * (P::K_STAGE >> 4));
       const uint32_t d = tmem + TM_S + (uint32_t)(t * 128);
       if (leader) {
 #pragma unroll
@@ -665,44 +739,79 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
           mma_f16_ss_lo(d, ad + o, bd + o, hi, P::IDESC_S, s > 0);
         }
         mma_commit(&s_full[t]);
-        if (t == 1) mma_commit(&k_empty[j & 1]);
+        if (frees) mma_commit(&k_empty[j & 1]);
       }
       __syncwarp();
     };
-    const auto values = [&](int t, int j) {
+    const auto values = [&](int t, int j, bool more, bool frees) {
       const uint32_t bd = v_lo + (uint32_t)((j & 1) * (P::V_STAGE >> 4));
-      const uint32_t d = tmem + TM_O + (uint32_t)(t * D), p = tmem + TM_S + (uint32_t)(t * 128);
+      const uint32_t d = tmem + TM_O + (uint32_t)(t * D), p = tmem + Weights<D>::AT + (uint32_t)t * Weights<D>::SLOT;
       if (leader) {
 #pragma unroll
         for (int s = 0; s < TOK / 16; ++s)
-          mma_f16_ts_lo(d, p + (s >> 2) * 64 + (s & 3) * 8, bd + (uint32_t)((s >> 2) * ((D * 128) >> 4) + (s & 3) * 2), hi,
-                        P::IDESC_O, j > 0 || s > 0);
+          mma_f16_ts_lo(d, p + (s >> 2) * Weights<D>::HALF + (s & 3) * 8, bd + (uint32_t)((s >> 2) * ((D * 128) >> 4) + (s & 3) * 2), hi,
+                        P::IDESC_O, more || s > 0);
         mma_commit(&pv_done[t]);
-        if (t == 1) mma_commit(&v_empty[j & 1]);
+        if (frees) mma_commit(&v_empty[j & 1]);
       }
       __syncwarp();
     };
     bool ok = mbar_wait_warp(&q_full, 0, &abort) && mbar_wait_warp(&k_full[0], 0, &abort);
     if (ok) {
       tc_fence_after();
-      scores(0, 0);
-      scores(1, 0);
+      scores(0, 0, twin);
+      if (!twin) scores(1, 0, true);
     }
-    for (int j = 0; ok && j < steps; ++j) {
-      ok = mbar_wait_warp(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        ok = ok && mbar_wait_warp(&p_full[t], (uint32_t)j & 1u, &abort);
+    if (twin) {
+      if (ok && steps > 1) {
+        ok = mbar_wait_warp(&k_full[1], 0, &abort);
+        tc_fence_after();
+        if (ok) scores(1, 1, true);
+      }
+      for (int j = 0; ok && j < steps; ++j) {  // slot j & 1, its (j / 2)-th step
+        const int t = j & 1;
+        const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+        ok = mbar_wait_warp(&v_full[t], ph, &abort) && mbar_wait_warp(&p_full[t], ph, &abort);
         if (!ok) break;
         tc_fence_after();
-        values(t, j);
-        if (j + 1 < steps) {
-          // the scores go where the weights lie that this product still reads
-          ok = (t || mbar_wait_warp(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
-               mbar_wait_warp(&pv_done[t], (uint32_t)j & 1u, &abort);
+        const bool next = j + 2 < steps;
+        if (Weights<D>::APART && next) {
+          ok = mbar_wait_warp(&k_full[t], ph ^ 1u, &abort);
           if (!ok) break;
           tc_fence_after();
-          scores(t, j + 1);
+          scores(t, j + 2, true);
+        }
+        values(t, j, j > 1, true);
+        if (!Weights<D>::APART && next) {
+          ok = mbar_wait_warp(&k_full[t], ph ^ 1u, &abort) && mbar_wait_warp(&pv_done[t], ph, &abort);
+          if (!ok) break;
+          tc_fence_after();
+          scores(t, j + 2, true);
+        }
+      }
+    } else {
+      for (int j = 0; ok && j < steps; ++j) {
+        ok = mbar_wait_warp(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          ok = ok && mbar_wait_warp(&p_full[t], (uint32_t)j & 1u, &abort);
+          if (!ok) break;
+          tc_fence_after();
+          const bool next = j + 1 < steps;
+          if (Weights<D>::APART && next) {
+            ok = t || mbar_wait_warp(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort);
+            if (!ok) break;
+            tc_fence_after();
+            scores(t, j + 1, t == 1);
+          }
+          values(t, j, j > 0, t == 1);
+          if (!Weights<D>::APART && next) {
+            ok = (t || mbar_wait_warp(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
+                 mbar_wait_warp(&pv_done[t], (uint32_t)j & 1u, &abort);
+            if (!ok) break;
+            tc_fence_after();
+            scores(t, j + 1, t == 1);
+          }
         }
       }
     }
@@ -755,11 +864,12 @@ int64_t tiles_of(const Kv4& c, int share) {
   const int64_t tiles = rows / ROWS + c.batch;
   return c.batch == 1 ? (rows + ROWS - 1) / ROWS : tiles;
 }
-// Parts of an item: enough for every SM to have one, each of at least 4 steps.
-int splits_of(const Kv4& c, int share, int window) {
-  (void)window;
+// Parts of an item: where there are fewer items than SMs, enough for two blocks each SM (the lengths
+// differ), each of at least 4 steps.
+int splits_of(const Kv4& c, int share) {
   const int64_t items = tiles_of(c, share) * c.kv_heads, steps = ((int64_t)c.max_kv + TOK - 1) / TOK;
-  int64_t s = 152 / (items < 1 ? 1 : items);
+  if (items >= 152) return 1;
+  int64_t s = (2 * 152 + items - 1) / items;
   if (s > steps / 4) s = steps / 4;
   return s < 1 ? 1 : (int)s;
 }
@@ -769,7 +879,7 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, int done_rows, void* ws, cuda
   using P = Prompt<D>;
   const int64_t items = tiles_of(c, a.share) * c.kv_heads;
   Parts parts{};
-  parts.splits = splits_of(c, a.share, a.window);
+  parts.splits = splits_of(c, a.share);
   if (parts.splits > 1) {
     parts.info = static_cast<int4*>(ws);
     parts.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (items * 16 + 255) / 256 * 256);
@@ -796,7 +906,7 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, int done_rows, void* ws, cuda
 
 int64_t kv4_prompt_ws_bytes(const Kv4& c, int dim, int share) {
   const int64_t items = tiles_of(c, share) * c.kv_heads;
-  const int splits = splits_of(c, share, 0);
+  const int splits = splits_of(c, share);
   return splits == 1 ? 0 : (items * 16 + 255) / 256 * 256 + items * splits * ROWS * (dim + 2) * 4;
 }
 
