@@ -18,7 +18,7 @@
 // tokens of a dimension as 16 bytes.
 //
 // Roles (24 warps): 0-7 and 8-15 softmax of the two tiles, half a row (one page's columns) a thread;
-// 16-19 keys; 20-22 values; 23 issues the MMAs in the order  PV_A(j) S_A(j+1) PV_B(j) S_B(j+1): one tile's softmax has the time
+// 16-18 keys; 19-22 values; 23 issues the MMAs in the order  PV_A(j) S_A(j+1) PV_B(j) S_B(j+1): one tile's softmax has the time
 // of the other's two products. The running maximum is moved (and O rescaled) only where a row's has
 // grown by more than 2^8.
 //
@@ -179,6 +179,36 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Bounded waits of few instructions: the roles share their schedulers, so every instruction of a wait
+// costs. One that gives up records it, and the later ones of the warp then poll once only; all roles keep
+// going through their steps (their loops are bounded, what they touch stays in bounds, and the pairs'
+// barriers match), with results that do not count.
+struct Waits {
+  uint32_t polls = kMaxPolls;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 0;\n\t"
+        "POLL:\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 q, n, %3;\n\t"
+        "@q bra POLL;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(polls)
+        : "memory");
+    if (!ok) {
+      if (polls > 1) record_device_error(kErrTimeout);
+      polls = 1;
+    }
+  }
+  __device__ __forceinline__ bool gave_up() const { return polls == 1; }
+};
+
 // x / d for x < 512, 1 <= d <= 128, with m = ceil(65536 / d)
 __device__ __forceinline__ int small_div(int x, uint32_t m) { return (int)(((uint32_t)x * m) >> 16); }
 
@@ -242,8 +272,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     if (threadIdx.x == 0) {
       item_s.rows = 0;
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&k_full[i], 4);
-        mbar_init(&v_full[i], 3);
+        mbar_init(&k_full[i], 3);
+        mbar_init(&v_full[i], 4);
         mbar_init(&k_empty[i], 1);
         mbar_init(&v_empty[i], 1);
         mbar_init(&s_full[i], 1);
@@ -303,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
   const int j0 = (int)((int64_t)all * split / parts.splits), j1 = (int)((int64_t)all * (split + 1) / parts.splits);
   const int steps = j1 - j0;
   const bool twin = it.rows <= 128;  // one tile of rows, in both slots
-  bool abort = false;
+  Waits wait;
 
   if (warp < 16) {
     // ================================ softmax ================================
@@ -384,7 +414,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
-      mbar_wait_warp(&q_full, 0, &abort);
+      wait(&q_full, 0);
+      __syncwarp();
     }
     const int w0 = (twin ? 0 : tile * 128) + quarter * 32, r = w0 + lane;  // the warp's first row, the thread's row
     const int mine = twin ? (steps + 1 - tile) / 2 : steps;                // steps of this slot
@@ -407,8 +438,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     for (int j = 0; j < mine; ++j) {
       const int first = page_first(it, 2 * (j0 + (twin ? 2 * j + tile : j)) + half);
       const bool whole = first + kKvPage - 1 <= pos_first && (first >= low_last || first + kKvPage <= a.sinks);
-      // (no way out of the loop when a wait gives up: the pair's barriers have to match)
-      mbar_wait_warp(&s_full[tile], (uint32_t)j & 1u, &abort);
+      wait(&s_full[tile], (uint32_t)j & 1u);
+      __syncwarp();
       tc_fence_after();
       if (!whole) {  // what a row does not see becomes -inf in place, 32 columns at a time
         const int hi = pos - first;  // columns x <= hi with x >= lo or x < sk are seen
@@ -450,7 +481,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         l *= f;
         if (j > 0) {  // after the last step's product with V
           if (WT::APART) {
-            mbar_wait_warp(&pv_done[tile], (uint32_t)(j - 1) & 1u, &abort);
+            wait(&pv_done[tile], (uint32_t)(j - 1) & 1u);
+            __syncwarp();
             tc_fence_after();
           }
 #pragma unroll 1
@@ -464,7 +496,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
           }
         }
       }
-      if (WT::APART && j > 0) mbar_wait_warp(&pv_done[tile], (uint32_t)(j - 1) & 1u, &abort);  // its weights are read
+      if (WT::APART && j > 0) {  // its weights are read
+        wait(&pv_done[tile], (uint32_t)(j - 1) & 1u);
+        __syncwarp();
+      }
       const float off = m == kNegInf ? 0.0f : -c1 * m;
       const uint64_t c2 = f2pack(c1, c1), off2 = f2pack(off, off);
       uint64_t l2[2] = {0, 0};
@@ -490,7 +525,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[tile]);
     }
-    if (mine > 0) mbar_wait_warp(&pv_done[tile], (uint32_t)(mine - 1) & 1u, &abort);
+    if (mine > 0) wait(&pv_done[tile], (uint32_t)(mine - 1) & 1u);
+    __syncwarp();
     tc_fence_after();
     row_x[mine & 1][half][xr] = l;
     named_bar_sync(pair, 64);
@@ -506,7 +542,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
 #pragma unroll 1
         for (int ch = 0; ch < D / 64; ++ch) {
           uint32_t v[32];
-          if (mine > 0 && !abort) {
+          if (mine > 0) {
             tmem_ld_32x32b_x32(to + 32 * ch, v);
             tmem_ld_wait();
           } else {
@@ -537,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
 #pragma unroll 1
     for (int ch = 0; ch < D / 64 && gives; ++ch) {
       uint32_t v[32];
-      if (mine > 0 && !abort) {
+      if (mine > 0) {
         tmem_ld_32x32b_x32(to + 32 * ch, v);
         tmem_ld_wait();
       } else {
@@ -607,50 +643,56 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       if (id < 0 || id >= c.n_pages) bad = true, id = 0;
       return c.pages + ((int64_t)id * c.kv_heads + it.h) * P::BLK;
     };
-    if (pages > 0 && warp < 20) {
-      // keys, a page at a time: 8 rows of all chunks (D = 128), or 16 of both (D = 64), a warp and unit;
-      // lane & 7 is the row of eight, so that 8 lanes store to 8 rows
-      constexpr int U = D == 128 ? 2 : 1;
-      const int ew = warp - 16, row8 = lane & 7, chunk = D == 128 ? lane >> 3 : (lane >> 3) & 1;
-      const int row0 = D == 128 ? ew * 8 + row8 : ew * 16 + (lane >> 4) * 8 + row8;  // and + 32 in the second unit
+    if (pages > 0 && warp < 19) {
+      // keys: 8 rows of all chunks (D = 128), or 16 of both (D = 64), a unit; a page's units go to the three
+      // warps in turn, which turn with the page. lane & 7 is the row of eight, so that 8 lanes store to 8 rows.
+      constexpr int UPP = D == 128 ? 8 : 4, U = (UPP + 2) / 3, RPU = kKvPage / UPP;
+      const int row8 = lane & 7, chunk = D == 128 ? lane >> 3 : (lane >> 3) & 1;
+      const int row_in = D == 128 ? row8 : (lane >> 4) * 8 + row8;
       uint4 code[U], code_n[U];
       uint2 par[U], par_n[U];
-      const auto load = [&](int id, uint4(&cd)[U], uint2(&pr)[U]) {
+      int turn = warp - 16;  // the page's first unit of this warp
+      const auto load = [&](int id, int first, uint4(&cd)[U], uint2(&pr)[U]) {
         const uint8_t* p = block(id);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          cd[i] = __ldg(reinterpret_cast<const uint4*>(p + (row0 + 32 * i) * (D / 2) + 16 * chunk));
-          pr[i] = __ldg(reinterpret_cast<const uint2*>(p + kKvPage * D + (row0 + 32 * i) * 8));
+          const int row = min(first + 3 * i, UPP - 1) * RPU + row_in;
+          cd[i] = __ldg(reinterpret_cast<const uint4*>(p + row * (D / 2) + 16 * chunk));
+          pr[i] = __ldg(reinterpret_cast<const uint2*>(p + kKvPage * D + row * 8));
         }
       };
-      load(page_id(0), code, par);
+      load(page_id(0), turn, code, par);
       int id = page_id(1);
 #pragma unroll 1
       for (int pg = 0; pg < pages; ++pg) {
-        load(id, code_n, par_n);
+        const int turn_n = turn == 0 ? 2 : turn - 1;
+        load(id, turn_n, code_n, par_n);
         id = page_id(pg + 2);
         const int st = (pg >> 1) & 1;
-        if (pg >= 4 && !(pg & 1) && !mbar_wait_warp(&k_empty[st], (uint32_t)((pg >> 2) - 1) & 1u, &abort)) break;
+        if (pg >= 4 && !(pg & 1)) wait(&k_empty[st], (uint32_t)((pg >> 2) - 1) & 1u);
         const uint32_t dst = k_s + st * P::K_STAGE;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          const int t = 64 * (pg & 1) + kv4_rho_inv(row0 + 32 * i);
-          const uint32_t step = __byte_perm(par[i].x, 0, 0x1010);
-          uint32_t bs = __byte_perm(par[i].x, 0, 0x3232);
-          // a value vector of NaN acts through its key, so that a weight of 0 never meets a NaN
-          const uint32_t z = hsub2(par[i].y, par[i].y);
-          bs = hadd2(bs, hadd2(__byte_perm(z, 0, 0x1010), __byte_perm(z, 0, 0x3232)));
-          const uint32_t wd[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+          if (turn + 3 * i < UPP) {
+            const int t = 64 * (pg & 1) + kv4_rho_inv((turn + 3 * i) * RPU + row_in);
+            const uint32_t step = __byte_perm(par[i].x, 0, 0x1010);
+            uint32_t bs = __byte_perm(par[i].x, 0, 0x3232);
+            // a value vector of NaN acts through its key, so that a weight of 0 never meets a NaN
+            const uint32_t z = hsub2(par[i].y, par[i].y);
+            bs = hadd2(bs, hadd2(__byte_perm(z, 0, 0x1010), __byte_perm(z, 0, 0x3232)));
+            const uint32_t wd[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t up = wd[k] >> 8;
-            const int w = 4 * chunk + k;
-            sts128(dst + (w >> 3) * (TOK * 128) + sw128(t, w & 7), hfma2(codes_even(wd[k]), step, bs),
-                   hfma2(codes_odd(wd[k]), step, bs), hfma2(codes_even(up), step, bs), hfma2(codes_odd(up), step, bs));
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t up = wd[k] >> 8;
+              const int w = 4 * chunk + k;
+              sts128(dst + (w >> 3) * (TOK * 128) + sw128(t, w & 7), hfma2(codes_even(wd[k]), step, bs),
+                     hfma2(codes_odd(wd[k]), step, bs), hfma2(codes_even(up), step, bs), hfma2(codes_odd(up), step, bs));
+            }
           }
           code[i] = code_n[i];
           par[i] = par_n[i];
         }
+        turn = turn_n;
         if (pg & 1) {
           fence_proxy_async_smem();
           __syncwarp();
@@ -659,7 +701,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       }
     } else if (pages > 0) {
       // values: word w of 8 tokens a lane, 16 (D = 128) or 32 tokens a unit; the units of all pages go to
-      // the three warps in turn
+      // the four warps in turn
       constexpr int TPU = 8 * (32 / W), UPP = kKvPage / TPU;  // tokens of a unit, units of a page
       const int w = lane % W, grp = lane / W, units = UPP * pages;
       uint32_t code[8], par[8], code_n[8], par_n[8];
@@ -673,17 +715,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
           pr[k] = __ldg(reinterpret_cast<const uint32_t*>(q + kv4_rho(k) * 8));
         }
       };
-      int u = warp - 20;
+      int u = warp - 19;
       load(u, page_id(u / UPP), code, par);
-      int id = page_id((u + 3) / UPP), done = -1;  // the last step whose place was waited for
+      int id = page_id((u + 4) / UPP), done = -1;  // the last step whose place was waited for
 #pragma unroll 1
-      for (; u < units; u += 3) {
-        load(min(u + 3, units - 1), id, code_n, par_n);
-        id = page_id((u + 6) / UPP);
+      for (; u < units; u += 4) {
+        load(min(u + 4, units - 1), id, code_n, par_n);
+        id = page_id((u + 8) / UPP);
         const int j = u / (2 * UPP), st = j & 1;
         if (j != done) {
           done = j;
-          if (j >= 2 && !mbar_wait_warp(&v_empty[st], (uint32_t)(j / 2 - 1) & 1u, &abort)) break;
+          if (j >= 2) wait(&v_empty[st], (uint32_t)(j / 2 - 1) & 1u);
         }
         const uint32_t at = v_s + st * P::V_STAGE + ((u / UPP) & 1) * (D * 128);
         const int ch = ((u % UPP) * TPU >> 3) + grp;
@@ -715,7 +757,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) code[k] = code_n[k], par[k] = par_n[k];
-        if (u + 3 >= 2 * UPP * (j + 1)) {  // this warp's last unit of the step
+        if (u + 4 >= 2 * UPP * (j + 1)) {  // this warp's last unit of the step
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&v_full[st]);
@@ -756,69 +798,63 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       }
       __syncwarp();
     };
-    bool ok = mbar_wait_warp(&q_full, 0, &abort) && mbar_wait_warp(&k_full[0], 0, &abort);
-    if (ok) {
-      tc_fence_after();
-      scores(0, 0, twin);
-      if (!twin) scores(1, 0, true);
-    }
+    wait(&q_full, 0);
+    wait(&k_full[0], 0);
+    __syncwarp();
+    tc_fence_after();
+    scores(0, 0, twin);
     if (twin) {
-      if (ok && steps > 1) {
-        ok = mbar_wait_warp(&k_full[1], 0, &abort);
+      if (steps > 1) {
+        wait(&k_full[1], 0);
+        __syncwarp();
         tc_fence_after();
-        if (ok) scores(1, 1, true);
+        scores(1, 1, true);
       }
-      for (int j = 0; ok && j < steps; ++j) {  // slot j & 1, its (j / 2)-th step
+      for (int j = 0; j < steps; ++j) {  // slot j & 1, its (j / 2)-th step
         const int t = j & 1;
         const uint32_t ph = (uint32_t)(j >> 1) & 1u;
-        ok = mbar_wait_warp(&v_full[t], ph, &abort) && mbar_wait_warp(&p_full[t], ph, &abort);
-        if (!ok) break;
-        tc_fence_after();
         const bool next = j + 2 < steps;
-        if (Weights<D>::APART && next) {
-          ok = mbar_wait_warp(&k_full[t], ph ^ 1u, &abort);
-          if (!ok) break;
+        wait(&v_full[t], ph);
+        wait(&p_full[t], ph);
+        __syncwarp();
+        tc_fence_after();
+        if (!Weights<D>::APART) values(t, j, j > 1, true);
+        if (next) {
+          wait(&k_full[t], ph ^ 1u);
+          if (!Weights<D>::APART) wait(&pv_done[t], ph);
+          __syncwarp();
           tc_fence_after();
           scores(t, j + 2, true);
         }
-        values(t, j, j > 1, true);
-        if (!Weights<D>::APART && next) {
-          ok = mbar_wait_warp(&k_full[t], ph ^ 1u, &abort) && mbar_wait_warp(&pv_done[t], ph, &abort);
-          if (!ok) break;
-          tc_fence_after();
-          scores(t, j + 2, true);
-        }
+        if (Weights<D>::APART) values(t, j, j > 1, true);
       }
     } else {
-      for (int j = 0; ok && j < steps; ++j) {
-        ok = mbar_wait_warp(&v_full[j & 1], (uint32_t)(j >> 1) & 1u, &abort);
+      scores(1, 0, true);
+      for (int j = 0; j < steps; ++j) {
+        const uint32_t ph = (uint32_t)j & 1u;
+        const bool next = j + 1 < steps;
+        wait(&v_full[j & 1], (uint32_t)(j >> 1) & 1u);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          ok = ok && mbar_wait_warp(&p_full[t], (uint32_t)j & 1u, &abort);
-          if (!ok) break;
+          wait(&p_full[t], ph);
+          __syncwarp();
           tc_fence_after();
-          const bool next = j + 1 < steps;
-          if (Weights<D>::APART && next) {
-            ok = t || mbar_wait_warp(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort);
-            if (!ok) break;
+          if (!Weights<D>::APART) values(t, j, j > 0, t == 1);
+          if (next) {
+            if (t == 0) wait(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u);
+            if (!Weights<D>::APART) wait(&pv_done[t], ph);
+            __syncwarp();
             tc_fence_after();
             scores(t, j + 1, t == 1);
           }
-          values(t, j, j > 0, t == 1);
-          if (!Weights<D>::APART && next) {
-            ok = (t || mbar_wait_warp(&k_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, &abort)) &&
-                 mbar_wait_warp(&pv_done[t], (uint32_t)j & 1u, &abort);
-            if (!ok) break;
-            tc_fence_after();
-            scores(t, j + 1, t == 1);
-          }
+          if (Weights<D>::APART) values(t, j, j > 0, t == 1);
         }
       }
     }
-    if (!ok) {  // what was issued ends before the tensor memory is given back
-      bool given_up = false;
+    if (wait.gave_up()) {  // what was issued ends before the tensor memory is given back
       if (leader) mma_commit(&all_done);
-      mbar_wait(&all_done, 0, &given_up);
+      wait.polls = kMaxPolls;
+      wait(&all_done, 0);
     }
   }
   if (bad) record_device_error(kErrRange);
