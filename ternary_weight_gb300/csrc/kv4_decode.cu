@@ -1,5 +1,5 @@
 // kv4_decode.cu -- attention over the 4-bit key/value cache for a few query rows a sequence: single
-// tokens and drafted ones, n * share <= 8 NT rows (share = query heads of one key/value head).
+// tokens and drafted ones, n * share <= 32 rows (share = query heads of one key/value head).
 //
 // Bound by the bytes of the cache. Every warp is its own pipeline: it fetches whole page blocks (one
 // head's 64 tokens, one bulk copy of 64 D + 512 contiguous bytes) into a ring of its own in shared
@@ -44,13 +44,12 @@ struct Shape {
   static constexpr int W = D / 8;             // words of a vector
   static constexpr int KS = D / 16;           // k steps of the scores; m tiles of the values
   static constexpr int BLK = 64 * D + 512;    // bytes of a block
-  static constexpr int ROWS = 8 * NT;
-  static constexpr bool QS = NT > 2;          // query fragments in shared memory (registers are full)
+  static constexpr int ROWS = 8 * NT;         // rows of a unit
+  static constexpr int GROUPS = NT == 1 ? 1 : 2;  // units of a head, at most
   static constexpr int BLOCKS = NT == 1 ? 3 : 2;  // resident blocks of an SM
-  static constexpr int STAGES = BLOCKS == 3 || QS ? 2 : 3;
-  static constexpr int QBYTES = QS ? ROWS * D * 2 : 0;
+  static constexpr int STAGES = BLOCKS == 3 ? 2 : 3;
   static constexpr int PBYTES = kKvPage * 16;  // the page's parameters as fp32
-  static constexpr int WARP_BYTES = STAGES * BLK + PBYTES + QBYTES;
+  static constexpr int WARP_BYTES = STAGES * BLK + PBYTES;
   static constexpr int SMEM = WARPS * WARP_BYTES;
   static constexpr int PART = ROWS * (D + 2);  // floats of a partial: ROWS x D sums, then m, then l
 };
@@ -162,14 +161,27 @@ __device__ __forceinline__ Span span_of(const Kv4& c, const Kv4Attn& a, const Kv
 // where the runs' results go in the workspace: for each unit the first and the last run that hold a
 // part of it, then two partials for each run (a run's first and last unit may be cut)
 struct Work {
-  int2* runs;     // batch x kv_heads
+  int2* runs;     // batch x kv_heads x GROUPS
   float* parts;   // n_runs x 2 x PART
 };
 
-// A unit (sequence b, head h) and the pages [i, until) of it that a run holds; weight is what the run
+// Rows beyond a unit's make another unit of the same head and pages (17 to 32 rows: registers hold the
+// sums of 16).
+__device__ __forceinline__ int groups_of(const Kv4Seq& s, const Kv4Attn& a, int rows) {
+  return (s.n * a.share + rows - 1) / rows;
+}
+// A unit (sequence b, head h / groups, its rows from rows * (h % groups) on) and the pages [i, until) of it that a run holds; weight is what the run
 // holds beyond them.
 struct Unit {
-  int b, h, i, until, weight;
+  int b, h, i, until, weight, groups;  // groups: 1 or 2; MOST says where it is always 1
+  template <int MOST>
+  __device__ __forceinline__ int head() const {
+    return MOST == 2 && groups == 2 ? h >> 1 : h;
+  }
+  template <int MOST>
+  __device__ __forceinline__ int group() const {
+    return MOST == 2 && groups == 2 ? h & 1 : 0;
+  }
   Kv4Seq s;
   Span p;
 };
@@ -178,15 +190,17 @@ struct Unit {
 constexpr int kUnitCost = 2;
 
 // the next unit of a run; false at the run's end
-__device__ __forceinline__ bool next_unit(Unit& u, const Kv4& c, const Kv4Attn& a, int max_rows, bool* bad) {
+template <int ROWS, int GROUPS>
+__device__ __forceinline__ bool next_unit(Unit& u, const Kv4& c, const Kv4Attn& a, bool* bad) {
   if (u.until < u.p.np || u.weight <= kUnitCost) return false;
-  if (++u.h == c.kv_heads) {
+  if (++u.h == c.kv_heads * (GROUPS == 1 ? 1 : u.groups)) {
     u.h = 0;
     do {
       if (++u.b >= c.batch) return false;
       u.s = kv4_sequence(c, u.b, bad);
-      u.p = span_of(c, a, u.s, max_rows);
+      u.p = span_of(c, a, u.s, ROWS * GROUPS);
     } while (u.p.np == 0);
+    u.groups = GROUPS == 1 ? 1 : groups_of(u.s, a, ROWS);
   }
   u.weight -= kUnitCost;
   u.i = 0;
@@ -226,8 +240,8 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
     Span p{0, 0, 0};
     for (int b = b0; b < b1; ++b) {
       s = kv4_sequence(c, b, &bad);
-      p = span_of(c, a, s, S::ROWS);
-      if (p.np) mine += (int64_t)(p.np + kUnitCost) * c.kv_heads;
+      p = span_of(c, a, s, S::ROWS * S::GROUPS);
+      if (p.np) mine += (int64_t)(p.np + kUnitCost) * c.kv_heads * (S::GROUPS == 1 ? 1 : groups_of(s, a, S::ROWS));
     }
     int64_t upto = mine;
 #pragma unroll
@@ -261,14 +275,15 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       for (int b = b0; b < b1; ++b) {
         if (per > 1) {
           s = kv4_sequence(c, b, &bad);
-          p = span_of(c, a, s, S::ROWS);
+          p = span_of(c, a, s, S::ROWS * S::GROUPS);
         }
         if (p.np == 0) continue;
         const int unit = p.np + kUnitCost;
-        const int64_t here = (int64_t)unit * c.kv_heads;
+        const int groups = S::GROUPS == 1 ? 1 : groups_of(s, a, S::ROWS);
+        const int64_t here = (int64_t)unit * c.kv_heads * groups;
         if (x < at + here) {
           const int h = here <= INT32_MAX ? (uint32_t)(x - at) / (uint32_t)unit : (int)((x - at) / unit);
-          starts[i] = Unit{b, h, (int)(x - at - (int64_t)h * unit), 0, (int)(begin(run0 + i + 1) - x), s, p};
+          starts[i] = Unit{b, h, (int)(x - at - (int64_t)h * unit), 0, (int)(begin(run0 + i + 1) - x), groups, s, p};
           break;
         }
         at += here;
@@ -294,15 +309,17 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       return;
     }
   } else {
-    use.b = blockIdx.x / c.kv_heads;
-    use.h = blockIdx.x - use.b * c.kv_heads;
+    use.b = blockIdx.x / (c.kv_heads * S::GROUPS);
+    use.h = blockIdx.x - use.b * c.kv_heads * S::GROUPS;
     use.s = kv4_sequence(c, use.b, &bad);
-    use.p = span_of(c, a, use.s, S::ROWS);
-    if (use.p.np == 0) {  // nothing cached: zeros
-      if ((int64_t)use.s.n * a.share <= S::ROWS && use.s.len < 1)
-        for (int r = warp; r < use.s.n * a.share; r += WARPS)
+    use.p = span_of(c, a, use.s, S::ROWS * S::GROUPS);
+    const bool few = (int64_t)use.s.n * a.share <= S::ROWS * S::GROUPS;
+    use.groups = few ? groups_of(use.s, a, S::ROWS) : 0;
+    if (use.h >= c.kv_heads * use.groups || use.p.np == 0) {
+      if (use.h < c.kv_heads * use.groups)  // nothing cached: zeros
+        for (int r = S::ROWS * use.template group<S::GROUPS>() + warp; r < min(use.s.n * a.share, S::ROWS * (use.template group<S::GROUPS>() + 1)); r += WARPS)
           for (int d = lane; d < D; d += 32)
-            a.out[(int64_t)(use.s.q0 + r / a.share) * a.out_stride + (int64_t)(use.h * a.share + r % a.share) * D + d] = 0;
+            a.out[(int64_t)(use.s.q0 + r / a.share) * a.out_stride + (int64_t)(use.template head<S::GROUPS>() * a.share + r % a.share) * D + d] = 0;
       if (bad) record_device_error(kErrRange);
       return;
     }
@@ -311,11 +328,11 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
     use.weight = 0;
     inside = true;
   }
-  const int rows = use.s.n * a.share;  // of the first unit: the only one where they are joined here
+  // the first unit's rows: it is the only one where they are joined here
+  const int rows0 = S::ROWS * use.template group<S::GROUPS>(), rows = min(S::ROWS, use.s.n * a.share - rows0);
 
   uint8_t* const ring = smem + warp * S::WARP_BYTES;
   float4* const par = reinterpret_cast<float4*>(ring + STAGES * BLK);
-  uint8_t* const qs = ring + STAGES * BLK + S::PBYTES;
   Unit get = use;                    // the unit whose page is fetched next
   bool more = use.i < use.until;     // there is a page to fetch
   int ids = 0, ids_from = -64;       // page ids ids_from .. + 31 of the unit, one a lane
@@ -333,25 +350,25 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
     const int id = __shfl_sync(0xffffffffu, ids, get.i - ids_from);
     if (lane == 0) {
       mbar_arrive_expect_tx(&full[warp][stage], BLK);
-      bulk_copy_g2s(ring + stage * BLK, c.pages + ((int64_t)id * c.kv_heads + get.h) * BLK, BLK, &full[warp][stage]);
+      bulk_copy_g2s(ring + stage * BLK, c.pages + ((int64_t)id * c.kv_heads + get.template head<S::GROUPS>()) * BLK, BLK, &full[warp][stage]);
     }
     ++in_flight;
     if (++get.i == get.until) {
       const int b = get.b;
-      more = next_unit(get, c, a, S::ROWS, &bad);
+      more = next_unit<S::ROWS, S::GROUPS>(get, c, a, &bad);
       if (get.b != b) ids_from = -64;
       if (more) {  // its queries are wanted soon
         const int bytes = a.share * D * (a.bf16 ? 2 : 4);
         for (int i = 0; i < get.s.n; ++i) {
           const char* q = static_cast<const char*>(a.q) +
-                          ((get.s.q0 + i) * a.q_stride + (int64_t)get.h * a.share * D) * (a.bf16 ? 2 : 4);
+                          ((get.s.q0 + i) * a.q_stride + (int64_t)get.template head<S::GROUPS>() * a.share * D) * (a.bf16 ? 2 : 4);
           for (int o = 128 * lane; o < bytes; o += 128 * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + o));
         }
       }
     }
   };
 
-  uint32_t qf[S::QS ? 1 : NT][S::QS ? 1 : KS][2];
+  uint32_t qf[NT][KS][2];
   // per row (column of the fragments): u = step raw + base qs is the score up to the factor c1 >= 0,
   // m its running maximum
   float c1[NT][2], qs2[NT][2], m[NT][2], bs[NT][2];
@@ -364,14 +381,15 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
 
   while (use.i < use.until) {
     const bool begun = use.i == 0;  // this run holds the unit's first page
+    const int row0 = S::ROWS * use.template group<S::GROUPS>();
     float vref = 5.9604644775390625e-8f;  // 2^-24: no step is smaller, but 0
     {  // a new unit: its queries
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int r = 8 * nt + g, i = r / a.share;
+        const int r = row0 + 8 * nt + g, i = r / a.share;
         float x[D / 4];
         if (i < use.s.n) {
-          const int64_t at = (int64_t)(use.s.q0 + i) * a.q_stride + (int64_t)(use.h * a.share + r % a.share) * D + V * q4;
+          const int64_t at = (int64_t)(use.s.q0 + i) * a.q_stride + (int64_t)(use.template head<S::GROUPS>() * a.share + r % a.share) * D + V * q4;
 #pragma unroll
           for (int n = 0; n < 8; ++n) load_q<V>(a, at + W * n, &x[n * V]);
         } else {
@@ -406,10 +424,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           const int v = s >> 1, n = (s & 1) * 2;  // word v of the lane; nibbles n, n + 4 and n + 1, n + 5
           const uint32_t f0 = pack_half2(x[n * V + v], x[(n + 4) * V + v]);
           const uint32_t f1 = pack_half2(x[(n + 1) * V + v] * 0.0625f, x[(n + 5) * V + v] * 0.0625f);
-          if constexpr (S::QS)
-            *reinterpret_cast<uint2*>(qs + ((nt * KS + s) * 32 + lane) * 8) = make_uint2(f0, f1);
-          else
-            qf[nt][s][0] = f0, qf[nt][s][1] = f1;
+          qf[nt][s][0] = f0, qf[nt][s][1] = f1;
         }
         // c1 of 0 would make NaN of a masked score
         const float k1 = fmaxf(fabsf(a.scale) * kLog2e * down * 16777216.0f, 1.17549435e-38f);
@@ -419,7 +434,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           const int col = 2 * q4 + j;
           c1[nt][j] = __shfl_sync(0xffffffffu, k1, 4 * col);
           qs2[nt][j] = __shfl_sync(0xffffffffu, k0, 4 * col);
-          pos[nt][j] = use.s.len - use.s.n + (8 * nt + col) / a.share;
+          pos[nt][j] = use.s.len - use.s.n + (row0 + 8 * nt + col) / a.share;
           m[nt][j] = kNegInf;
           bs[nt][j] = 0.0f;
         }
@@ -506,11 +521,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           const uint32_t x = st & 1 ? k0[v] >> 8 : k0[v], y = st & 1 ? k1[v] >> 8 : k1[v];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            uint2 f;
-            if constexpr (S::QS)
-              f = lds<uint2>(qs + ((nt * KS + st) * 32 + lane) * 8);
-            else
-              f = make_uint2(qf[nt][st][0], qf[nt][st][1]);
+            const uint2 f = make_uint2(qf[nt][st][0], qf[nt][st][1]);
             if (st == 0)
               mma16816<true>(s[nt][i], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, f.x, f.y);
             else
@@ -631,8 +642,8 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
 
     {  // the unit ends, or this run's part of it
       const bool ends = use.i == use.p.np, alone = SPLIT && begun && ends;
-      const int unit_rows = use.s.n * a.share;
-      const int64_t unit = (int64_t)use.b * c.kv_heads + use.h;
+      const int unit_rows = min(S::ROWS, use.s.n * a.share - row0);
+      const int64_t unit = (int64_t)use.b * c.kv_heads * S::GROUPS + use.h;
       float* part = inside ? reinterpret_cast<float*>(ring) : ws.parts + (2 * run + (begun ? 1 : 0)) * S::PART;
       if (SPLIT && lane == 0) {
         if (begun) ws.runs[unit].x = (int)run;
@@ -653,8 +664,8 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           if (r >= unit_rows) continue;
           const float lo = vref * 16777216.0f, hi = vref * 1048576.0f;
           const float norm = alone ? (sl == 0.0f ? 0.0f : 1.0f / sl) : 1.0f;
-          uint16_t* out = a.out + (int64_t)(use.s.q0 + r / a.share) * a.out_stride +
-                          (int64_t)(use.h * a.share + r % a.share) * D;
+          uint16_t* out = a.out + (int64_t)(use.s.q0 + (row0 + r) / a.share) * a.out_stride +
+                          (int64_t)(use.template head<S::GROUPS>() * a.share + (row0 + r) % a.share) * D;
 #pragma unroll
           for (int n = 0; n < 8; ++n) {  // nibble n: dimension W n + word
             float y[W / 8];
@@ -680,7 +691,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           }
         }
     }
-    if (!next_unit(use, c, a, S::ROWS, &bad)) break;
+    if (!next_unit<S::ROWS, S::GROUPS>(use, c, a, &bad)) break;
   }
   if (abort && lane == 0) {  // copies in flight land before the block ends
     bool given_up = false;
@@ -709,8 +720,8 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           sl = fmaf(parts(i)[S::ROWS * (D + 1) + r], f[i], sl);
         }
       const float norm = sl == 0.0f ? 0.0f : 1.0f / sl;
-      uint16_t* out = a.out + (int64_t)(use.s.q0 + r / a.share) * a.out_stride +
-                      (int64_t)(use.h * a.share + r % a.share) * D;
+      uint16_t* out = a.out + (int64_t)(use.s.q0 + (rows0 + r) / a.share) * a.out_stride +
+                      (int64_t)(use.template head<S::GROUPS>() * a.share + (rows0 + r) % a.share) * D;
 #pragma unroll
       for (int d = 0; d < D; d += 32) {
         float o = 0.0f;
@@ -734,24 +745,25 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
 // Joins the partials of one row of a unit, in the order of the runs; zeros for a row of a sequence
 // that has nothing cached. A unit finished by one run is left alone.
 constexpr int JOIN_WARPS = 8;
-template <int D, int ROWS>
+template <int D, int ROWS, int GROUPS>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Attn a, Work ws) {
   constexpr int PART = ROWS * (D + 2), E = D / 32;
   __shared__ float part_m[JOIN_WARPS], part_l[JOIN_WARPS], part_o[JOIN_WARPS][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x, r = blockIdx.y, b = unit / c.kv_heads, h = unit % c.kv_heads;
+  const int b = blockIdx.x / c.kv_heads, h = blockIdx.x - b * c.kv_heads, gr = blockIdx.y;  // row of the head
   bool bad = false;
   const Kv4Seq s = kv4_sequence(c, b, &bad);
   pdl_wait();
   const int64_t rows = (int64_t)s.n * a.share;
-  if (rows > ROWS || r >= rows) return;
-  uint16_t* out = a.out + (int64_t)(s.q0 + r / a.share) * a.out_stride + (int64_t)(h * a.share + r % a.share) * D;
+  if (rows > ROWS * GROUPS || gr >= rows) return;
+  uint16_t* out = a.out + (int64_t)(s.q0 + gr / a.share) * a.out_stride + (int64_t)(h * a.share + gr % a.share) * D;
   if (s.len < 1) {
     for (int d = threadIdx.x; d < D; d += 32 * JOIN_WARPS) out[d] = 0;
     if (bad && threadIdx.x == 0) record_device_error(kErrRange);
     return;
   }
-  const int2 runs = ws.runs[unit];
+  const int r = gr % ROWS, groups = groups_of(s, a, ROWS);
+  const int2 runs = ws.runs[(int64_t)b * c.kv_heads * GROUPS + h * groups + gr / ROWS];
   if (runs.x == runs.y) return;
   float m = kNegInf, l = 0.0f, o[E];
 #pragma unroll
@@ -795,14 +807,16 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Att
   }
 }
 
-// the most pages that a sequence can show the rows of a call
+// the most pages that a sequence can show the rows of a call, and units of a call
 int64_t most_pages(const Kv4& c) { return ((int64_t)c.max_kv + kKvPage - 1) / kKvPage; }
+int64_t units_of(const Kv4& c, int rows) { return (int64_t)c.batch * c.kv_heads * (rows > 16 ? 2 : 1); }
 // runs of a call: a warp each of `resident` blocks, fewer where there are not as many pages to see
-int64_t runs_of(const Kv4& c, int resident) {
-  const int64_t weight = (int64_t)c.batch * c.kv_heads * (most_pages(c) + kUnitCost);
+int64_t runs_of(const Kv4& c, int rows, int resident) {
+  const int64_t weight = units_of(c, rows) * (most_pages(c) + kUnitCost);
   const int64_t blocks = (weight + WARPS - 1) / WARPS;
   return WARPS * (blocks < 1 ? 1 : blocks < resident ? blocks : resident);
 }
+int64_t runs_bytes(const Kv4& c, int rows) { return (units_of(c, rows) * (int64_t)sizeof(int2) + 255) / 256 * 256; }
 // Whether units are cut. A block for each unit needs no search for the runs and no second kernel, but
 // lasts as long as the longest: measured, cut and uncut, us (20 and 5 heads x 128, one query a
 // sequence): 1 x 512 tokens 9.0, 6.4; 1 x 1024 9.3, 8.4; 1 x 4096 10.4, 23.3; 64 x 1024 21.4, 16.8;
@@ -812,27 +826,28 @@ bool cuts(const Kv4& c) {
   return most_pages(c) > (uncut < 64 ? uncut : 64);
 }
 
+// rows: 8, 16, or 32 (two units of 16 a head where a sequence has more than 16)
 template <int D, int NT>
-cudaError_t launch(const Kv4& c, const Kv4Attn& a, void* workspace, int num_sms, cudaStream_t st) {
+cudaError_t launch(const Kv4& c, const Kv4Attn& a, int rows, void* workspace, int num_sms, cudaStream_t st) {
   using S = Shape<D, NT>;
   Work ws{};
   cudaError_t e;
   if (!cuts(c)) {
     e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
-    kv4_decode_kernel<D, NT, false><<<(unsigned)(c.batch * c.kv_heads), 32 * WARPS, S::SMEM, st>>>(c, a, ws);
+    kv4_decode_kernel<D, NT, false><<<(unsigned)(c.batch * c.kv_heads * S::GROUPS), 32 * WARPS, S::SMEM, st>>>(c, a, ws);
     return cudaGetLastError();
   }
   ws.runs = static_cast<int2*>(workspace);
-  ws.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                      ((int64_t)c.batch * c.kv_heads * 8 + 255) / 256 * 256);
+  ws.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + runs_bytes(c, S::ROWS * S::GROUPS));
   e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
-  kv4_decode_kernel<D, NT, true><<<(unsigned)(runs_of(c, S::BLOCKS * num_sms) / WARPS), 32 * WARPS, S::SMEM, st>>>(c, a, ws);
+  kv4_decode_kernel<D, NT, true><<<(unsigned)(runs_of(c, rows, S::BLOCKS * num_sms) / WARPS), 32 * WARPS, S::SMEM, st>>>(
+      c, a, ws);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  const int64_t rows = (int64_t)c.max_q * a.share;
-  cfg.gridDim = dim3((unsigned)(c.batch * c.kv_heads), (unsigned)(rows < S::ROWS ? rows : S::ROWS));
+  const int64_t all = (int64_t)c.max_q * a.share;
+  cfg.gridDim = dim3((unsigned)(c.batch * c.kv_heads), (unsigned)(all < rows ? all : rows));
   cfg.blockDim = dim3(32 * JOIN_WARPS);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -840,13 +855,11 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, void* workspace, int num_sms,
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, S::ROWS>, c, a, ws);
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, S::ROWS, S::GROUPS>, c, a, ws);
 }
 template <int D>
 cudaError_t launch_rows(const Kv4& c, const Kv4Attn& a, int rows, void* ws, int num_sms, cudaStream_t st) {
-  if (rows <= 8) return launch<D, 1>(c, a, ws, num_sms, st);
-  if (rows <= 16) return launch<D, 2>(c, a, ws, num_sms, st);
-  return launch<D, 4>(c, a, ws, num_sms, st);
+  return rows <= 8 ? launch<D, 1>(c, a, rows, ws, num_sms, st) : launch<D, 2>(c, a, rows, ws, num_sms, st);
 }
 
 }  // namespace
@@ -854,7 +867,8 @@ cudaError_t launch_rows(const Kv4& c, const Kv4Attn& a, int rows, void* ws, int 
 int64_t kv4_decode_ws_bytes(const Kv4& c, int dim, int rows) {
   if (!cuts(c)) return 0;
   // as for the largest GPU of this kind (160 SMs), so that the size does not depend on the device
-  return ((int64_t)c.batch * c.kv_heads * 8 + 255) / 256 * 256 + runs_of(c, 3 * 160) * 2 * rows * (dim + 2) * 4;
+  const int unit_rows = rows <= 8 ? 8 : 16;
+  return runs_bytes(c, rows <= 8 ? 8 : 32) + runs_of(c, rows, 3 * 160) * 2 * unit_rows * (dim + 2) * 4;
 }
 
 cudaError_t launch_kv4_decode(const Kv4& c, int dim, const Kv4Attn& a, int rows, void* ws, int num_sms,
