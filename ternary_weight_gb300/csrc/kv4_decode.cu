@@ -744,12 +744,12 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
 
 // Joins the partials of one row of a unit, in the order of the runs; zeros for a row of a sequence
 // that has nothing cached. A unit finished by one run is left alone.
-constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_WARPS = 16;  // at most
 template <int D, int ROWS, int GROUPS>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Attn a, Work ws) {
   constexpr int PART = ROWS * (D + 2), E = D / 32;
   __shared__ float part_m[JOIN_WARPS], part_l[JOIN_WARPS], part_o[JOIN_WARPS][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int b = blockIdx.x / c.kv_heads, h = blockIdx.x - b * c.kv_heads, gr = blockIdx.y;  // row of the head
   bool bad = false;
   const Kv4Seq s = kv4_sequence(c, b, &bad);
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Att
   if (rows > ROWS * GROUPS || gr >= rows) return;
   uint16_t* out = a.out + (int64_t)(s.q0 + gr / a.share) * a.out_stride + (int64_t)(h * a.share + gr % a.share) * D;
   if (s.len < 1) {
-    for (int d = threadIdx.x; d < D; d += 32 * JOIN_WARPS) out[d] = 0;
+    for (int d = threadIdx.x; d < D; d += blockDim.x) out[d] = 0;
     if (bad && threadIdx.x == 0) record_device_error(kErrRange);
     return;
   }
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Att
   const int head = in0 - runs.x, blocks = in0 < in1 ? (in1 - in0) / WARPS : 0;
   const int count = in0 < in1 ? head + blocks + runs.y - in1 + 1 : runs.y - runs.x + 1;
 #pragma unroll 4
-  for (int k = warp; k < count; k += JOIN_WARPS) {
+  for (int k = warp; k < count; k += warps) {
     const int i = k < head || blocks == 0 ? runs.x + k
                   : k < head + blocks     ? in0 + (k - head) * WARPS
                                           : in1 + (k - head - blocks);
@@ -795,10 +795,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Att
   __syncthreads();
   if (threadIdx.x < D) {
     float mx = kNegInf;
-    for (int i = 0; i < JOIN_WARPS; ++i) mx = fmaxf(mx, part_m[i]);
+    for (int i = 0; i < warps; ++i) mx = fmaxf(mx, part_m[i]);
     if (mx == kNegInf) mx = 0.0f;
     float sl = 0.0f, so = 0.0f;
-    for (int i = 0; i < JOIN_WARPS; ++i) {
+    for (int i = 0; i < warps; ++i) {
       const float f = exp2_approx(part_m[i] - mx);
       sl = fmaf(part_l[i], f, sl);
       so = fmaf(part_o[i][threadIdx.x], f, so);
@@ -817,13 +817,23 @@ int64_t runs_of(const Kv4& c, int rows, int resident) {
   return WARPS * (blocks < 1 ? 1 : blocks < resident ? blocks : resident);
 }
 int64_t runs_bytes(const Kv4& c, int rows) { return (units_of(c, rows) * (int64_t)sizeof(int2) + 255) / 256 * 256; }
+// Warps that join a row: 16 where a unit has many partials, or few rows would wait on long chains (1 x
+// 131072 tokens 28.8 us, with 8 31.4; 1 x 4096 10.4, 11.0), 8 where many rows share the SMs (64 ragged
+// up to 8192 42.1, with 16 44.6; 16 x 3 to 7 drafted tokens 40.1, with 16 43.8).
+unsigned join_warps(const Kv4& c, int rows, int resident) {
+  return runs_of(c, rows, resident) > 64 * units_of(c, rows) ? JOIN_WARPS : 8;
+}
 // Whether units are cut. A block for each unit needs no search for the runs and no second kernel, but
 // lasts as long as the longest: measured, cut and uncut, us (20 and 5 heads x 128, one query a
 // sequence): 1 x 512 tokens 9.0, 6.4; 1 x 1024 9.3, 8.4; 1 x 4096 10.4, 23.3; 64 x 1024 21.4, 16.8;
-// 64 x 2048 29.2, 26.8; 64 x 4096 42.2, 45.5; 256 x 2048 78.4, 68.6.
-bool cuts(const Kv4& c) {
-  const int64_t uncut = 16 + (int64_t)c.batch * c.kv_heads / 20;
-  return most_pages(c) > (uncut < 64 ? uncut : 64);
+// 64 x 2048 29.2, 26.8; 64 x 4096 42.2, 45.5; 256 x 2048 78.4, 68.6. A window bounds the pages too (for
+// the workspace, whose size does not depend on it, it is taken for none).
+bool cuts(const Kv4& c, int window, int sinks) {
+  int64_t pages = most_pages(c);
+  const int64_t seen = ((int64_t)window + c.max_q + 2 * kKvPage - 3) / kKvPage + ((int64_t)sinks + kKvPage - 1) / kKvPage;
+  if (window != INT32_MAX && seen < pages) pages = seen;
+  const int64_t uncut = 16 + (int64_t)c.batch * c.kv_heads / 10;
+  return pages > (uncut < 64 ? uncut : 64);
 }
 
 // rows: 8, 16, or 32 (two units of 16 a head where a sequence has more than 16)
@@ -832,7 +842,7 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, int rows, void* workspace, in
   using S = Shape<D, NT>;
   Work ws{};
   cudaError_t e;
-  if (!cuts(c)) {
+  if (!cuts(c, a.window, a.sinks)) {
     e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     kv4_decode_kernel<D, NT, false><<<(unsigned)(c.batch * c.kv_heads * S::GROUPS), 32 * WARPS, S::SMEM, st>>>(c, a, ws);
@@ -848,7 +858,7 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, int rows, void* workspace, in
   cudaLaunchConfig_t cfg{};
   const int64_t all = (int64_t)c.max_q * a.share;
   cfg.gridDim = dim3((unsigned)(c.batch * c.kv_heads), (unsigned)(all < rows ? all : rows));
-  cfg.blockDim = dim3(32 * JOIN_WARPS);
+  cfg.blockDim = dim3(32 * join_warps(c, rows, S::BLOCKS * num_sms));
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -865,7 +875,7 @@ cudaError_t launch_rows(const Kv4& c, const Kv4Attn& a, int rows, void* ws, int 
 }  // namespace
 
 int64_t kv4_decode_ws_bytes(const Kv4& c, int dim, int rows) {
-  if (!cuts(c)) return 0;
+  if (!cuts(c, INT32_MAX, 0)) return 0;
   // as for the largest GPU of this kind (160 SMs), so that the size does not depend on the device
   const int unit_rows = rows <= 8 ? 8 : 16;
   return runs_bytes(c, rows <= 8 ? 8 : 32) + runs_of(c, rows, 3 * 160) * 2 * unit_rows * (dim + 2) * 4;
