@@ -9,6 +9,9 @@ launch per group -- in a fixed order. The whole sequence is captured once into a
 launch. Activations enter through one contiguous input buffer and results leave through
 one contiguous output buffer, so a host round trip is one copy each way.
 
+``AttentionBlock`` runs the attention of a layer: its ternary projections, the 4-bit key/value
+cache and the attention over it.
+
 Everything the step computes runs in the library's kernels; torch only owns the buffers,
 the stream and the graph.
 """
@@ -153,3 +156,50 @@ class TernaryStack:
         if self.graph is None:
             self.capture()
         self.graph.replay()
+
+
+class AttentionBlock:
+    """The attention block of one layer: ternary q, k, v and o projections around the 4-bit cache.
+
+    ``run`` takes the rows of the new tokens of a batch of sequences (``binding.KV4Batch``): it projects
+    them to queries, keys and values, appends the keys and values to the cache, attends over what the
+    sequences then have cached, and projects the result: prompts, single tokens and both together alike.
+    Every call is asynchronous and reads the batch's lengths on the device, so a decode step can be
+    captured once and replayed as the sequences grow (``python -m ternary_weight_gb300.generate`` does).
+    Each layer has a cache of its own; the layers of a model share the batch."""
+
+    def __init__(self, q: PackedLinear, k: PackedLinear, v: PackedLinear, o: PackedLinear, cache: "binding.KV4Cache",
+                 scale: float | None = None, window: int = 0, sinks: int = 0):
+        dim = cache.head_dim
+        if q.N % dim or k.N != cache.kv_heads * dim or v.N != k.N or q.N % k.N or o.K != q.N or not q.K == k.K == v.K:
+            raise ValueError("the projections' sizes do not fit the cache's heads")
+        self.qkv, self.o, self.cache = [q, k, v], o, cache
+        self.heads = [l.N // dim for l in self.qkv]
+        self.scale = dim ** -0.5 if scale is None else scale
+        self.window, self.sinks = window, sinks
+
+    def _project(self, x, linears):
+        xq = s = rs = None
+        if x.shape[0] > 1:
+            xq = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+            s = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+            rs = torch.empty(x.shape[0], dtype=torch.int32, device=x.device)
+        return binding.linear_group(x, [l.wp for l in linears], [l.w_scale for l in linears], xq=xq, scale=s, rowsum=rs)
+
+    def run(self, x, batch, rotate=None, stream=None):
+        """x: total_q x K rows (fp32 or bf16), sequence after sequence. ``rotate(q, k)``, if given, puts
+        the positions into the queries and keys (total_q x heads x dim fp32) in place before they are
+        cached. Returns total_q x N fp32."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.run(x, batch, rotate)
+        if x.shape[0] != batch.total_q:
+            raise ValueError("x must have a row for each of the batch's new tokens")
+        if x.shape[0] == 0:
+            return torch.empty((0, self.o.N), dtype=torch.float32, device=x.device)
+        q, k, v = (t.view(-1, h, self.cache.head_dim) for t, h in zip(self._project(x, self.qkv), self.heads))
+        if rotate is not None:
+            rotate(q, k)
+        binding.kv4_append(self.cache, batch, k, v)
+        y = binding.kv4_attention(self.cache, batch, q, self.scale, window=self.window, sinks=self.sinks)
+        return self._project(y.view(x.shape[0], -1), [self.o])[0]

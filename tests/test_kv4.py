@@ -426,3 +426,56 @@ def test_batches_that_break_their_bounds_are_reported(new, breaks):
     if breaks != "page":
         assert binding.last_device_error() == binding.BITNET_ERANGE
     assert binding.last_device_error() == 0
+
+
+# ------------------------------------------------------------------- wider shapes
+@pytest.mark.parametrize("heads,share,dim", [(70, 1, 64), (66, 2, 128), (1, 128, 64), (2, 100, 128), (3, 33, 64), (1, 17, 128)])
+@pytest.mark.parametrize("new,kv", [([1, 1], [129, 64]), ([2, 1], [70, 3]), ([40], [100])])
+def test_many_heads_and_wide_groups(heads, share, dim, new, kv):
+    attend(World(new, kv, heads, dim, seed=heads + share).fill(), share)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new,kv,share", [([1, 600, 1, 5, 33, 0], [5000, 900, 1, 2000, 33, 700], 4),  # all kinds in one call
+                                          ([8, 9, 8, 2], [4000, 4100, 10, 300], 4),                   # 32 and 36 rows a head
+                                          ([16, 17, 1], [3000, 3000, 40], 1),                         # 16 and 17
+                                          ([128, 1], [6000, 6000], 1), ([32, 20], [9000, 65], 4)])     # long caches, few rows
+def test_unlike_sequences_in_one_call(dim, new, kv, share):
+    attend(World(new, kv, 2, dim, seed=sum(new)).fill(), share)
+
+
+@pytest.mark.parametrize("window,sinks", [(300, 0), (1000, 4), (3000, 130), (65, 1)])
+@pytest.mark.parametrize("new", [[1] * 4, [4, 1, 7, 2], [30, 12, 1, 3]])
+def test_windows_far_into_long_caches(new, window, sinks):
+    """Few and many pages inside the window, in caches that are far longer."""
+    attend(World(new, [9000, 4097, 8000, 2500], 2, 128, seed=window).fill(), 4, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_ragged_batches(seed):
+    rng = np.random.default_rng(100 + seed)
+    n = int(rng.integers(2, 20))
+    top = int(rng.choice([1, 8, 60, 300]))
+    new = rng.integers(0, top + 1, n).tolist()
+    kv = [a + int(c) for a, c in zip(new, rng.integers(0, 1500, n))]
+    dim, heads, share = int(rng.choice([64, 128])), int(rng.integers(1, 4)), int(rng.integers(1, 9))
+    window, sinks = (int(rng.integers(1, 600)), int(rng.integers(0, 80))) if seed % 2 else (0, 0)
+    w = World(new, kv, heads, dim, "f32" if seed % 3 == 0 else "bf16", seed=seed).fill()
+    if sum(new):
+        attend(w, share, window=window, sinks=sinks)
+
+
+def test_calls_on_several_streams_at_once():
+    """Each with an output and a workspace of its own."""
+    kinds = [([1] * 5, [3000] * 5), ([300], [2000]), ([6], [4000]), ([1], [40])]
+    worlds = [World(new, kv, 2, 128, seed=i).fill() for i, (new, kv) in enumerate(kinds)]
+    qs = [torch.randn(sum(w.new), 8, 128, dtype=torch.bfloat16, device="cuda") for w in worlds]
+    batches = [w.batch(w.new, w.kv) for w in worlds]
+    want = [binding.kv4_attention(w.cache, b, q, 0.09) for w, b, q in zip(worlds, batches, qs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in worlds]
+    got = [[binding.kv4_attention(w.cache, b, q, 0.09, stream=s) for w, b, q, s in zip(worlds, batches, qs, streams)]
+           for _ in range(10)]
+    torch.cuda.synchronize()
+    for outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
