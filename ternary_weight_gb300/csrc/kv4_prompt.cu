@@ -233,6 +233,86 @@ struct Parts {
   int splits;
 };
 
+// The queries of a warp's 16 rows of the item, scaled and in the operand's order: W lanes a row, 8 dimensions
+// a lane (8 w .. 8 w + 7: nibble n = w / (W / 8) of words 8 w % W ..). q' = q 2^(13 - e), 2^e <= max |q| <
+// 2^(e + 1), e not below -100, and 13 where there are infinities or NaN; 2^(e - 13) goes to row_f. The loads of
+// all rows (bf16; fp32: of 4) are in flight together, and a pair of rows shares its exchanges: this stands
+// at the head of every block, before the first product can begin.
+template <int D, bool BF16>
+__device__ __forceinline__ void store_queries(const Kv4Attn& a, const Item& it, uint32_t share_m, int warp, int lane,
+                                              uint32_t q_s, float* row_f) {
+  constexpr int W = D / 8, RPI = 32 / W, ALL = 16 / RPI, BATCH = BF16 ? ALL : 4, U = BF16 ? 4 : 8;
+  static_assert(ALL % BATCH == 0 && (ALL == BATCH || BATCH * RPI % 8 == 0), "a batch begins at a row of eight");
+  const int w = lane % W, n = w / (W / 8), sub = lane / W;
+  const bool high = n >= 4;
+  const uint32_t neg = a.scale < 0.0f ? 0x80008000u : 0u;
+  // of row r, token t: base + t hop + r D
+  const int64_t hop = a.q_stride - (int64_t)a.share * D;
+  const int64_t base = (int64_t)(it.s.q0 + it.tok0) * a.q_stride + (int64_t)(it.h * a.share + it.head0) * D + 8 * w;
+  uint32_t dst = q_s + (warp >> 3) * Prompt<D>::Q_TILE + (8 * w % W >> 3) * (128 * 128) +
+                 ((warp & 7) * 16 + sub) * 128 + 4 * (n & 3);
+  const uint32_t turn = ((high ? 4u : 0u) ^ (uint32_t)sub) << 4;
+#pragma unroll 1
+  for (int i0 = 0; i0 < ALL; i0 += BATCH, dst += BATCH * RPI * 128) {
+    const int r0 = warp * 16 + i0 * RPI + sub;
+    uint32_t u[BATCH][U];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {  // rows past the end read the last one
+      const int r = min(r0 + i * RPI, it.rows - 1);
+      const int64_t at = base + small_div(it.head0 + r, share_m) * hop + r * D;
+      const uint4* src = BF16 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at)
+                              : reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at);
+#pragma unroll
+      for (int k = 0; k < U / 4; ++k) {
+        const uint4 x = __ldg(src + k);
+        u[i][4 * k] = x.x, u[i][4 * k + 1] = x.y, u[i][4 * k + 2] = x.z, u[i][4 * k + 3] = x.w;
+      }
+    }
+    // the upper 16 bits of the largest magnitudes of two rows: their exponents are all that counts
+    uint32_t top[BATCH / 2];
+#pragma unroll
+    for (int i = 0; i < BATCH; i += 2) {
+      uint32_t m[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        m[s] = 0;
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          m[s] = BF16 ? __vmaxu2(m[s], u[i + s][k] & 0x7fff7fffu) : max(m[s], u[i + s][k] & 0x7fffffffu);
+      }
+      const uint32_t hi = __byte_perm(m[0], m[1], 0x7632);
+      top[i / 2] = BF16 ? __vmaxu2(hi, __byte_perm(m[0], m[1], 0x5410)) : hi;
+    }
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < BATCH / 2; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      uint32_t e = (top[i / 2] >> (i & 1 ? 23 : 7)) & 255u;  // e + 127
+      e = e == 255u ? 140u : max(e, 27u);
+      const float up = __uint_as_float((267u - e) << 23);
+      if (w == 0) row_f[r0 + i * RPI] = __uint_as_float((e - 13u) << 23);
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = __uint_as_float(BF16 ? u[i][k % U] << 16 : u[i][2 * k % U]);
+        const float y = __uint_as_float(BF16 ? u[i][k % U] & 0xffff0000u : u[i][(2 * k + 1) % U]);
+        h[k] = pack_half2(x * up, y * up) ^ neg;
+      }
+      // nibbles n and n + 4 of a word lie side by side: half of the lane's numbers go to the lane that has the
+      // other nibble, half of that one's come here
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? h[k] : h[2 + k], W / 2), own = high ? h[2 + k] : h[k];
+        const uint32_t lo = high ? got : own, up2 = high ? own : got;
+        st_shared_u32(dst + i * RPI * 128 + (turn ^ (((2 * k) ^ (i * RPI & 7)) << 4)), __byte_perm(lo, up2, 0x5410));
+        st_shared_u32(dst + i * RPI * 128 + (turn ^ (((2 * k + 1) ^ (i * RPI & 7)) << 4)), __byte_perm(lo, up2, 0x7632));
+      }
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a, int done_rows, uint32_t share_m, Parts parts) {
   using P = Prompt<D>;
@@ -261,7 +341,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       return r <= done_rows ? 0 : (int)((r + ROWS - 1) / ROWS);
     };
     int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(kv4_sequence(c, b, &bad));
+    Kv4Seq s{};
+    for (int b = b0; b < b1; ++b) mine += tiles_of(s = kv4_sequence(c, b, &bad));
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -269,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       if (lane >= o) upto += v;
     }
     if (lane == 31) warp_sum[warp] = upto;
-    if (threadIdx.x == 0) {
+    if (warp == 22 && lane == 0) {
       item_s.rows = 0;
       for (int i = 0; i < 2; ++i) {
         mbar_init(&k_full[i], 3);
@@ -284,12 +365,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
       mbar_init(&all_done, 1);
       fence_mbar_init();
     }
+    if (warp == 23) {
+      tmem_alloc(&tmem_slot, 512);
+      tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
-    int at = upto - mine;
-    for (int i = 0; i < warp; ++i) at += warp_sum[i];
+    tc_fence_after();
+    const int at0 = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0);
+    int at = at0 + upto - mine;
     if (x >= at && x < at + mine) {
       for (int b = b0; b < b1; ++b) {
-        const Kv4Seq s = kv4_sequence(c, b, &bad);
+        if (per > 1) s = kv4_sequence(c, b, &bad);
         const int t = tiles_of(s);
         if (x < at + t) {
           Item it;
@@ -319,15 +406,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     parts.info[item_no] = make_int4(it.s.q0, it.row0, it.rows, it.h);
   if (it.rows == 0) {  // fewer items than the grid was made for
     if (bad) record_device_error(kErrRange);
+    if (warp == 23) tmem_dealloc(tmem_slot, 512);
     return;
   }
-  if (warp == 23) {
-    tmem_alloc(&tmem_slot, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const int all = (it.np + 1) / 2;  // steps of the item, then of this part of it
   const int j0 = (int)((int64_t)all * split / parts.splits), j1 = (int)((int64_t)all * (split + 1) / parts.splits);
@@ -340,87 +421,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     const int tile = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
     // token (from the item's first) and head of a row of the item
     const auto token_of = [&](int r) { return small_div(it.head0 + r, share_m); };
-    {  // the queries of both tiles, 16 rows a warp: W lanes a row, 8 dimensions a lane
-      constexpr int RPI = 32 / W, BATCH = 4;  // rows at a time; of loads in flight
-      const int w = lane % W;      // dimensions 8 w .. 8 w + 7: nibble n = w / (W / 8) of words 8 w % W ..
-      const int n = w / (W / 8), word0 = 8 * w % W;
-      const bool high = n >= 4;
-#pragma unroll 1
-      for (int i0 = 0; i0 < 16; i0 += BATCH * RPI) {
-        const int r0 = warp * 16 + i0 + lane / W;
-        float q[BATCH][8], mx[BATCH], up[BATCH];
-        int64_t at[BATCH];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {  // rows past the end read the last one
-          const int r = min(r0 + i * RPI, it.rows - 1), t = token_of(r);
-          at[i] = (int64_t)(it.s.q0 + it.tok0 + t) * a.q_stride + (int64_t)(it.h * a.share + it.head0 + r - t * a.share) * D + 8 * w;
-        }
-        if (a.bf16) {
-          uint4 u[BATCH];
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at[i]));
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) q[i][2 * k] = __uint_as_float(x[k] << 16), q[i][2 * k + 1] = __uint_as_float(x[k] & 0xffff0000u);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at[i]);
-            const float4 x = __ldg(p), y = __ldg(p + 1);
-            q[i][0] = x.x, q[i][1] = x.y, q[i][2] = x.z, q[i][3] = x.w;
-            q[i][4] = y.x, q[i][5] = y.y, q[i][6] = y.z, q[i][7] = y.w;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          mx[i] = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mx[i] = fmaxf(mx[i], fabsf(q[i][k]));
-        }
-#pragma unroll
-        for (int o = W / 2; o; o >>= 1)
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          // q' = q 2^(13 - e), 2^e <= max |q| < 2^(e + 1); not below e = -100, and not for infinities
-          int e = (int)(__float_as_uint(mx[i]) >> 23) - 127;
-          e = e == 128 ? 13 : max(e, -100);
-          up[i] = __int_as_float((13 - e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
-          // a factor of 0 would make NaN of a masked score
-          if (w == 0)
-            row_c1[r0 + i * RPI] = fmaxf(fabsf(a.scale) * kLog2e * __int_as_float((e - 13 + 127) << 23), 1.17549435e-38f);
-        }
-        // nibbles n and n + 4 of a word lie side by side: half of the lane's numbers go to the lane that
-        // has the other nibble, half of that one's come here
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int word = word0 + k + (high ? 4 : 0);
-          float got[BATCH];
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) got[i] = __shfl_xor_sync(0xffffffffu, high ? q[i][k] : q[i][4 + k], W / 2);
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const float mine = high ? q[i][4 + k] : q[i][k];
-            const int r = r0 + i * RPI;
-            st_shared_u32(q_s + (r >> 7) * P::Q_TILE + (word >> 3) * (128 * 128) + sw128(r & 127, word & 7) + 4 * (n & 3),
-                          pack_half2((high ? got[i] : mine) * up[i], (high ? mine : got[i]) * up[i]));
-          }
-        }
-      }
+    if (!twin || tile == 0) {
+      if (a.bf16) store_queries<D, true>(a, it, share_m, warp, lane, q_s, row_c1);
+      else store_queries<D, false>(a, it, share_m, warp, lane, q_s, row_c1);
       fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full);
-      wait(&q_full, 0);
-      __syncwarp();
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full);
+    wait(&q_full, 0);
+    __syncwarp();
     const int w0 = (twin ? 0 : tile * 128) + quarter * 32, r = w0 + lane;  // the warp's first row, the thread's row
     const int mine = twin ? (steps + 1 - tile) / 2 : steps;                // steps of this slot
     const bool there = r < it.rows;
-    const float c1 = row_c1[r];
+    // a factor of 0 would make NaN of a masked score
+    const float c1 = fmaxf(fabsf(a.scale) * kLog2e * row_c1[r], 1.17549435e-38f);
     const int pos0 = it.s.len - it.s.n + it.tok0;
     const int pos = there ? pos0 + token_of(r) : -1;
     // of the warp's rows: the first position, and the last window's beginning (rows past the end follow the last)
@@ -447,12 +461,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
 #pragma unroll 1
         for (int ch = 0; ch < 2; ++ch) {
           const int h = hi - 32 * ch, b = max(lo, INT32_MIN + 64) - 32 * ch, k0 = sk - 32 * ch;
+          const auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };  // bits 0 .. n - 1
+          const uint32_t vis = below(h >= 31 ? 32 : h + 1) & (~below(b) | below(k0));
           uint32_t v[32];
           tmem_ld_32x32b_x32(ts + 32 * ch, v);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (k > h || (k < b && k >= k0)) v[k] = __float_as_uint(kNegInf);
+            if (!((vis >> k) & 1u)) v[k] = __float_as_uint(kNegInf);
           tmem_st_x32(ts + 32 * ch, v);
         }
         tmem_st_wait();
@@ -661,13 +677,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
           pr[i] = __ldg(reinterpret_cast<const uint2*>(p + kKvPage * D + row * 8));
         }
       };
-      load(page_id(0), turn, code, par);
-      int id = page_id(1);
+      const int id0 = page_id(0);
+      int id = page_id(1), id_n = page_id(2);  // together: each would cost the block a memory latency
+      load(id0, turn, code, par);
 #pragma unroll 1
       for (int pg = 0; pg < pages; ++pg) {
         const int turn_n = turn == 0 ? 2 : turn - 1;
         load(id, turn_n, code_n, par_n);
-        id = page_id(pg + 2);
+        id = id_n;
+        id_n = page_id(pg + 3);
         const int st = (pg >> 1) & 1;
         if (pg >= 4 && !(pg & 1)) wait(&k_empty[st], (uint32_t)((pg >> 2) - 1) & 1u);
         const uint32_t dst = k_s + st * P::K_STAGE;
@@ -716,12 +734,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         }
       };
       int u = warp - 19;
-      load(u, page_id(u / UPP), code, par);
-      int id = page_id((u + 4) / UPP), done = -1;  // the last step whose place was waited for
+      const int id0 = page_id(u / UPP);
+      int id = page_id((u + 4) / UPP), id_n = page_id((u + 8) / UPP);
+      load(u, id0, code, par);
+      int done = -1;  // the last step whose place was waited for
 #pragma unroll 1
       for (; u < units; u += 4) {
         load(min(u + 4, units - 1), id, code_n, par_n);
-        id = page_id((u + 8) / UPP);
+        id = id_n;
+        id_n = page_id((u + 12) / UPP);
         const int j = u / (2 * UPP), st = j & 1;
         if (j != done) {
           done = j;
