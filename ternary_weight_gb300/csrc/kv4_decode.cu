@@ -793,17 +793,17 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Att
 #pragma unroll
   for (int e = 0; e < E; ++e) part_o[warp][E * lane + e] = o[e];
   __syncthreads();
-  if (threadIdx.x < D) {
-    float mx = kNegInf;
-    for (int i = 0; i < warps; ++i) mx = fmaxf(mx, part_m[i]);
-    if (mx == kNegInf) mx = 0.0f;
+  float mx = kNegInf;
+  for (int i = 0; i < warps; ++i) mx = fmaxf(mx, part_m[i]);
+  if (mx == kNegInf) mx = 0.0f;
+  for (int d = threadIdx.x; d < D; d += blockDim.x) {
     float sl = 0.0f, so = 0.0f;
     for (int i = 0; i < warps; ++i) {
       const float f = exp2_approx(part_m[i] - mx);
       sl = fmaf(part_l[i], f, sl);
-      so = fmaf(part_o[i][threadIdx.x], f, so);
+      so = fmaf(part_o[i][d], f, so);
     }
-    reinterpret_cast<__nv_bfloat16*>(out)[threadIdx.x] = __float2bfloat16_rn(sl == 0.0f ? 0.0f : so / sl);
+    reinterpret_cast<__nv_bfloat16*>(out)[d] = __float2bfloat16_rn(sl == 0.0f ? 0.0f : so / sl);
   }
 }
 
@@ -817,11 +817,12 @@ int64_t runs_of(const Kv4& c, int rows, int resident) {
   return WARPS * (blocks < 1 ? 1 : blocks < resident ? blocks : resident);
 }
 int64_t runs_bytes(const Kv4& c, int rows) { return (units_of(c, rows) * (int64_t)sizeof(int2) + 255) / 256 * 256; }
-// Warps that join a row: 16 where a unit has many partials, or few rows would wait on long chains (1 x
-// 131072 tokens 28.8 us, with 8 31.4; 1 x 4096 10.4, 11.0), 8 where many rows share the SMs (64 ragged
-// up to 8192 42.1, with 16 44.6; 16 x 3 to 7 drafted tokens 40.1, with 16 43.8).
+// Warps that join a row: as many as its partials keep busy. Measured, us, with 16, 8 and 2 (20 and 5 heads x
+// 128): 1 x 131072 tokens (365 runs a unit) 28.8, 31.4, -; 16 x 4096 (23) 20.9, 21.1, 21.7; 8 x 65536 (46)
+// 66.6, 66.9, 69.7; 64 x 4096 (6) 45.4, 43.1, 42.0; 256 x 8192 (1) -, 236, 230.
 unsigned join_warps(const Kv4& c, int rows, int resident) {
-  return runs_of(c, rows, resident) > 64 * units_of(c, rows) ? JOIN_WARPS : 8;
+  const int64_t runs = runs_of(c, rows, resident), units = units_of(c, rows);
+  return runs > 64 * units ? JOIN_WARPS : runs > 8 * units ? 8 : 2;
 }
 // Whether units are cut. A block for each unit needs no search for the runs and no second kernel, but
 // lasts as long as the longest: measured, cut and uncut, us (20 and 5 heads x 128, one query a
