@@ -409,8 +409,8 @@ typedef struct bitnet_kv4_cache {
  * ones of a sequence with kv_len cached tokens (the new ones among them) has position
  * kv_len - n + i. Position j of sequence b lies in page page_table[b][j / 64], place j % 64. The
  * arrays are read on the device; the sizes below bound them (and total_q * kv_heads is at most
- * 2^33, batch * kv_heads * max_kv / 64 at most 2^40). A sequence whose entries break a
- * bound (cu_q outside 0..total_q or falling, more than max_q tokens, kv_len outside 0..max_kv, a
+ * 2^33, batch * kv_heads * max_kv / 64 at most 2^40). A sequence with tokens in the batch whose entries
+ * break a bound (cu_q outside 0..total_q or falling, more than max_q tokens, kv_len outside 0..max_kv, a
  * page id outside 0..n_pages - 1) makes the call record BITNET_ERANGE in the device error word;
  * nothing outside the arrays is read or written, and that sequence's results are not valid.
  */

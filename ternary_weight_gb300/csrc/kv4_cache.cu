@@ -1,6 +1,14 @@
 // kv4_cache.cu -- writing the 4-bit key/value cache and reading it back.
 //
-// Both kernels move each vector once and are bound by bytes.
+// Both kernels move each vector once, and nothing else: bound by bytes, with issue slots next (2.5 of 4 an
+// SM and cycle). Why this layout: W lanes share the key and the value of a token and head, so that each
+// lane's loads and stores of numbers are 16 bytes and its codes one word after an exchange of nibbles;
+// a ninth warp hides the look-up of the places (three dependent loads a row) behind the last chunk's
+// work; four blocks an SM cover the latency of the rest. Measured (5 heads x 128, bf16): 73 000 tokens of 6 sequences
+// read back in 46.8 us (237 MB, 5.1 TB/s of the measured 6.7; with two blocks an SM 50 us, with a look-up
+// by every worker 62 us); 23 165 tokens of 5 prompts written in 32.6 us (75 MB, 2.3 TB/s: the quantisation
+// takes the issue slots) and read back in 19.3; one token, or 96, written in 5 us and read in 3.6, the time
+// of a launch and a chain of loads.
 //
 // Quantisation is exact: the code is the correctly rounded quotient (x - base) / step although only
 // fp32 is used. An approximate quotient decides unless it lies near a half integer (within several times
