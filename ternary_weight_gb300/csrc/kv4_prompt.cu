@@ -445,7 +445,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     // a factor of 0 would make NaN of a masked score
     const float c1 = fmaxf(fabsf(a.scale) * kLog2e * row_c1[r], 1.17549435e-38f);
     const int pos0 = it.s.len - it.s.n + it.tok0;
-    const int pos = there ? pos0 + token_of(r) : -1;
+    // before position 0 nothing is seen, however far before: -1 keeps the mask's differences in 32 bits
+    const int pos = there ? max(pos0 + token_of(r), -1) : -1;
     // of the warp's rows: the first position, and the last window's beginning (rows past the end follow the last)
     const int pos_first = pos0 + token_of(w0);
     const int64_t low_last = (int64_t)pos0 + token_of(max(min(it.rows, w0 + 32) - 1, 0)) - a.window + 1;
