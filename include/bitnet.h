@@ -380,7 +380,7 @@ BITNET_API int bitnet_sweep_plan_destroy(bitnet_sweep_plan plan);
  *
  * A vector (the key or the value of one token and one key/value head, D = head_dim numbers) is
  * held as D codes, a step and a base, and stands for step * code + base:
- *   lo, hi = min and max of the x, each clamped to [-61440, 61440]
+ *   x is clamped to [-61440, 61440] first; lo, hi = min and max
  *   base = fp16(lo), step = fp16((hi - lo) / 15)   (fp32 subtract and divide, one rounding each)
  *   code = clamp(rne((x - base) / step), 0, 15)    (the exact quotient rounded once, ties to even)
  * with code 0 where step is 0. A vector with a NaN is held as NaN (it reads back as NaN, and

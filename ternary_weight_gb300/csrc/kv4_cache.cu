@@ -209,15 +209,18 @@ __device__ __forceinline__ uint2* params(uint8_t* blk, int t) {
   return reinterpret_cast<uint2*>(blk + kKvPage * D) + kv4_rho(t);
 }
 
-// The codes one by one, with every care: the clamp, and the borders.
+// The codes one by one, with every care: the clamps, and the borders. The numbers are clamped as lo and hi
+// are: where lo lies just below 61440, base = fp16(lo) may be 61440 itself, and a number beyond it would
+// take a code above the clamped number's.
 __device__ __noinline__ uint32_t careful_codes(const float (&x)[8], float base, float step) {
   const float inv = __frcp_rn(step);
   uint32_t word = 0;
 #pragma unroll 1
   for (int n = 7; n >= 0; --n) {
-    const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[n], base), inv), 0.0f), 15.0f);
+    const float y = fminf(fmaxf(x[n], -kKvMax), kKvMax);
+    const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(y, base), inv), 0.0f), 15.0f);
     float r = __fsub_rn(__fadd_rn(t, kMagic), kMagic);
-    if (fabsf(t - r) > kNear) r = border_code(x[n], base, step, floorf(t));
+    if (fabsf(t - r) > kNear) r = border_code(y, base, step, floorf(t));
     word = word << 4 | (uint32_t)r;
   }
   return word;
@@ -233,7 +236,6 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* par)
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
-  // (a number beyond +-61440 needs no clamp of its own: its code is clamped)
   const float range = __fsub_rn(max_nan(min_nan(hi, kKvMax), -kKvMax), max_nan(min_nan(lo, kKvMax), -kKvMax));
   // range / 15, correctly rounded: one correction by the exact remainder (Markstein)
   float q = __fmul_rn(range, 1.0f / 15.0f);

@@ -1,4 +1,5 @@
 """Edges of the 4-bit cache and its attention, against plain 64-bit numpy (tests/kv4_reference.py)."""
+import numpy as np
 import pytest
 import torch
 
@@ -27,3 +28,23 @@ def test_rows_far_before_the_first_position_are_zero(dim, new, kv, window, sinks
     w = World([new], [kv], 2, dim, seed=new + kv).fill()
     q, out = attend(w, 1, window=window, sinks=sinks)
     assert not out[:new - kv].any()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_numbers_beyond_the_clamp_take_its_code(dim):
+    """Vectors that begin just below 61440 and end beyond it: it is the clamped number that is rounded."""
+    rows = []
+    for low in (61425.0, 61430.0, 61439.99, 61440.0, 61408.0, 61000.0):
+        for high in (61440.0, 61441.0, 65000.0, 1e30, np.inf):
+            x = np.full(dim, low, np.float32)
+            x[dim // 2:] = high
+            x[1] = (low + min(high, 61440.0)) / 2
+            rows += [x, -x, np.roll(x, 5)]
+    x = np.stack(rows)[:, None]
+    w = World([len(x)], [len(x)], 1, dim, "f32", seed=1)
+    w.k, w.v = [x], [x[::-1].copy()]
+    w.fill()
+    assert np.array_equal(w.cache.pages.cpu().numpy().reshape(w.n_pages, 1, -1), w.expected_pages())
+    k, v = binding.kv4_read(w.cache, w.batch(w.kv, w.kv), torch.float32)
+    for got, parts in ((k, w.k), (v, w.v)):
+        assert np.array_equal(got.cpu().numpy(), w.values(parts)[0].astype(np.float32))
