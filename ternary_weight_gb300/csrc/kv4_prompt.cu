@@ -522,9 +522,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
           }
         }
       }
-      if (WT::APART && j > 0) {  // its weights are read
+      if (WT::APART && j > 0) {  // its weights are read: the next ones may be stored over them
         wait(&pv_done[tile], (uint32_t)(j - 1) & 1u);
         __syncwarp();
+        tc_fence_after();
       }
       const float off = m == kNegInf ? 0.0f : -c1 * m;
       const uint64_t c2 = f2pack(c1, c1), off2 = f2pack(off, off);
