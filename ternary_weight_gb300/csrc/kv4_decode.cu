@@ -37,6 +37,7 @@
 // of m16n8k32 (72.9 against 48.9), weights as two fp16 parts (83.7 against 74.3 for the drafted tokens), 32
 // rows in one unit (68 against 39.8).
 #include "kv4.cuh"
+#include "kv4_join.h"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -173,6 +174,7 @@ __device__ __forceinline__ Span span_of(const Kv4& c, const Kv4Attn& a, const Kv
 struct Work {
   int2* runs;     // batch x kv_heads x GROUPS
   float* parts;   // n_runs x 2 x PART
+  int n_runs;     // of the grid: as many as are made, or more
 };
 
 // Rows beyond a unit's make another unit of the same head and pages (17 to 32 rows: registers hold the
@@ -774,19 +776,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(Kv4 c, Kv4Att
   }
   const int r = gr % ROWS, groups = groups_of(s, a, ROWS);
   const int2 runs = ws.runs[(int64_t)b * c.kv_heads * GROUPS + h * groups + gr / ROWS];
-  if (runs.x == runs.y) return;
+  const Kv4Join join = kv4_join(runs.x, runs.y, ws.n_runs, WARPS);
+  if (join.count == 0) return;
   float m = kNegInf, l = 0.0f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  // runs of the blocks that lie inside the unit left one partial a block, with their first run
-  const int in0 = runs.x / WARPS * WARPS + WARPS, in1 = runs.y / WARPS * WARPS;
-  const int head = in0 - runs.x, blocks = in0 < in1 ? (in1 - in0) / WARPS : 0;
-  const int count = in0 < in1 ? head + blocks + runs.y - in1 + 1 : runs.y - runs.x + 1;
 #pragma unroll 4
-  for (int k = warp; k < count; k += warps) {
-    const int i = k < head || blocks == 0 ? runs.x + k
-                  : k < head + blocks     ? in0 + (k - head) * WARPS
-                                          : in1 + (k - head - blocks);
+  for (int k = warp; k < join.count; k += warps) {
+    const int i = join.run(k);
     const float* part = ws.parts + (2 * (int64_t)i + (i == runs.x ? 1 : 0)) * PART;
     const float pm = part[ROWS * D + r], pl = part[ROWS * (D + 1) + r];
     float po[E];
@@ -863,8 +860,8 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, int rows, void* workspace, in
   ws.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + runs_bytes(c, S::ROWS * S::GROUPS));
   e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
-  kv4_decode_kernel<D, NT, true><<<(unsigned)(runs_of(c, rows, S::BLOCKS * num_sms) / WARPS), 32 * WARPS, S::SMEM, st>>>(
-      c, a, ws);
+  ws.n_runs = (int)runs_of(c, rows, S::BLOCKS * num_sms);
+  kv4_decode_kernel<D, NT, true><<<(unsigned)(ws.n_runs / WARPS), 32 * WARPS, S::SMEM, st>>>(c, a, ws);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const int64_t all = (int64_t)c.max_q * a.share;
