@@ -467,7 +467,7 @@ class KV4Cache:
             raise ValueError("pages must be %d bytes of uint8" % need)
         _require_cuda(pages)
         self.pages, self.n_pages, self.kv_heads, self.head_dim = pages, n_pages, kv_heads, head_dim
-        self.device = pages.device
+        self.device, self.index = pages.device, pages.get_device()
         self._desc = _KV4CacheDesc(pages.data_ptr(), n_pages, kv_heads, head_dim)
         self._ref = ctypes.c_void_p(ctypes.addressof(self._desc))
 
@@ -487,6 +487,9 @@ class KV4Batch:
         if cu_q.shape != (n + 1,) or kv_len.shape != (n,) or page_table.dim() != 2 or page_table.shape[0] != n:
             raise ValueError("cu_q must have batch + 1 entries, kv_len batch, and page_table batch rows")
         _require_cuda(cu_q, kv_len, page_table)
+        self.index = cu_q.get_device()
+        if kv_len.get_device() != self.index or page_table.get_device() != self.index:
+            raise ValueError("cu_q, kv_len and page_table must be on one device")
         if max_kv is None:
             max_kv = page_table.shape[1] * KV4_PAGE
         self.cu_q, self.kv_len, self.page_table = cu_q, kv_len, page_table
@@ -499,7 +502,7 @@ class KV4Batch:
 
 # A decode step makes these calls for every layer, and their kernels take a few microseconds: the helpers
 # below look everything up once and touch each tensor's properties once.
-_kv4_torch = None  # (torch, its dtypes -> BITNET dtypes, torch.bfloat16, raw current stream by device index)
+_kv4_torch = None  # (torch, its dtypes -> BITNET dtypes, torch.bfloat16, stream handle by device index and stream)
 
 
 def _kv4_setup():
@@ -510,16 +513,30 @@ def _kv4_setup():
     if raw is None:
         def raw(index):
             return torch.cuda.current_stream(index).cuda_stream
-    _kv4_torch = torch, {torch.float32: BITNET_F32, torch.bfloat16: BITNET_BF16}, torch.bfloat16, raw
+    current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+    def handle(cache, batch, stream):
+        """The stream's handle, where the call can run on it: kernels run on the calling thread's current device,
+        and would take pointers to another one as they are."""
+        index = cache.index
+        if batch.index != index:
+            raise ValueError("the batch must be on the cache's device")
+        if current() != index:
+            raise ValueError("the cache's device must be the current one")
+        return raw(index) if stream is None else stream.cuda_stream
+
+    _kv4_torch = torch, {torch.float32: BITNET_F32, torch.bfloat16: BITNET_BF16}, torch.bfloat16, handle
     return _kv4_torch
 
 
-def _kv4_rows(t, rows, heads, dim):
-    """Checks a rows x heads x dim tensor whose heads lie one after another; its row stride."""
+def _kv4_rows(t, rows, heads, dim, index):
+    """Checks a rows x heads x dim tensor on device `index` whose heads lie one after another; its row stride."""
     if t.shape != (rows, heads, dim):
         raise ValueError("expected a %d x %d x %d tensor" % (rows, heads, dim))
     s = t.stride()
-    if not t.is_cuda or (rows and (s[2] != 1 or (heads > 1 and s[1] != dim))):
+    if t.get_device() != index:
+        raise ValueError("rows must be CUDA tensors on the cache's device")
+    if rows and (s[2] != 1 or (heads > 1 and s[1] != dim)):
         raise ValueError("rows must be CUDA tensors whose heads lie one after another")
     return s[0] if rows > 1 else heads * dim
 
@@ -535,15 +552,15 @@ def _kv4_empty(torch, shape, dtype, device, stream):
 def kv4_append(cache, batch, k, v, stream=None):
     """Quantise the batch's keys and values (total_q x kv_heads x head_dim, fp32 or bf16 CUDA; rows may
     be strided, e.g. slices of a fused q/k/v row) to 4 bits and write them to their places."""
-    _, dtypes, _, raw = _kv4_torch or _kv4_setup()
+    _, dtypes, _, handle = _kv4_torch or _kv4_setup()
     dt = dtypes.get(k.dtype)
     if dt is None or v.dtype != k.dtype:
         raise ValueError("k and v must both be float32 or bfloat16")
     rows, heads, dim = batch.total_q, cache.kv_heads, cache.head_dim
-    ks, vs = _kv4_rows(k, rows, heads, dim), _kv4_rows(v, rows, heads, dim)
+    ks, vs = _kv4_rows(k, rows, heads, dim, cache.index), _kv4_rows(v, rows, heads, dim, cache.index)
+    on = handle(cache, batch, stream)
     if rows:
-        st = lib().bitnet_kv4_append(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs,
-                                     raw(k.get_device()) if stream is None else stream.cuda_stream)
+        st = lib().bitnet_kv4_append(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs, on)
         if st:
             raise BitnetError(st, "bitnet_kv4_append")
 
@@ -551,8 +568,9 @@ def kv4_append(cache, batch, k, v, stream=None):
 def kv4_read(cache, batch, dtype=None, k=None, v=None, stream=None):
     """Read the batch's tokens back from the cache as (k, v), each total_q x kv_heads x head_dim of
     ``dtype`` (fp32 or bf16, default bf16; or that of the given k and v, which are written)."""
-    torch, dtypes, bf16, raw = _kv4_torch or _kv4_setup()
+    torch, dtypes, bf16, handle = _kv4_torch or _kv4_setup()
     rows, heads, dim = batch.total_q, cache.kv_heads, cache.head_dim
+    on = handle(cache, batch, stream)
     ks = vs = heads * dim
     if k is None or v is None:
         given = k if k is not None else v
@@ -561,17 +579,16 @@ def kv4_read(cache, batch, dtype=None, k=None, v=None, stream=None):
     if k is None:
         k = _kv4_empty(torch, (rows, heads, dim), dtype, cache.device, stream)
     else:
-        ks = _kv4_rows(k, rows, heads, dim)
+        ks = _kv4_rows(k, rows, heads, dim, cache.index)
     if v is None:
         v = _kv4_empty(torch, (rows, heads, dim), dtype, cache.device, stream)
     else:
-        vs = _kv4_rows(v, rows, heads, dim)
+        vs = _kv4_rows(v, rows, heads, dim, cache.index)
     dt = dtypes.get(k.dtype)
     if dt is None or v.dtype != k.dtype or (dtype is not None and dtype != k.dtype):
         raise ValueError("k and v must both be float32 or bfloat16, as asked for")
     if rows:
-        st = lib().bitnet_kv4_read(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs,
-                                   raw(cache.device.index) if stream is None else stream.cuda_stream)
+        st = lib().bitnet_kv4_read(cache._ref, batch._ref, k.data_ptr(), v.data_ptr(), dt, ks, vs, on)
         if st:
             raise BitnetError(st, "bitnet_kv4_read")
     return k, v
@@ -590,12 +607,13 @@ def kv4_attention(cache, batch, q, scale, window=0, sinks=0, out=None, workspace
     or j > p - window or j < sinks). Returns total_q x q_heads x head_dim bf16 (``out`` if given).
     ``workspace``: a uint8 CUDA tensor of at least kv4_attention_workspace_size bytes, allocated
     here if not given."""
-    torch, dtypes, bf16, raw = _kv4_torch or _kv4_setup()
+    torch, dtypes, bf16, handle = _kv4_torch or _kv4_setup()
     dt = dtypes.get(q.dtype)
     if dt is None or q.dim() != 3:
         raise ValueError("q must be total_q x q_heads x head_dim, float32 or bfloat16")
     rows, heads, dim = batch.total_q, q.shape[1], cache.head_dim
-    qs = _kv4_rows(q, rows, heads, dim)
+    qs = _kv4_rows(q, rows, heads, dim, cache.index)
+    on = handle(cache, batch, stream)
     key = (heads, cache.kv_heads, dim)
     need = batch._ws.get(key)
     if need is None:
@@ -605,18 +623,19 @@ def kv4_attention(cache, batch, q, scale, window=0, sinks=0, out=None, workspace
     elif out.dtype != bf16:
         raise ValueError("out must be bfloat16")
     else:
-        os_ = _kv4_rows(out, rows, heads, dim)
+        os_ = _kv4_rows(out, rows, heads, dim, cache.index)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         _require_cuda(workspace)
+        if workspace.get_device() != cache.index:
+            raise ValueError("the workspace must be on the cache's device")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif need:
         workspace, ws_bytes = _kv4_empty(torch, need, torch.uint8, cache.device, stream), need
         ws_ptr = workspace.data_ptr()
     if rows:
         st = lib().bitnet_kv4_attention(cache._ref, batch._ref, q.data_ptr(), dt, heads, qs, scale, window, sinks,
-                                        out.data_ptr(), os_, ws_ptr, ws_bytes,
-                                        raw(q.get_device()) if stream is None else stream.cuda_stream)
+                                        out.data_ptr(), os_, ws_ptr, ws_bytes, on)
         if st:
             raise BitnetError(st, "bitnet_kv4_attention")
     return out

@@ -3,10 +3,12 @@ import os
 import re
 import shutil
 import subprocess
+from types import SimpleNamespace
 
 import pytest
+import torch
 
-from ternary_weight_gb300 import _build
+from ternary_weight_gb300 import _build, binding
 
 
 def source(name):
@@ -77,3 +79,91 @@ def test_a_join_stays_inside_the_workspace(tmp_path):
     # and the kernel takes its places from there alone
     kernel = re.search(r"kv4_join_kernel\(.*?\n}\n", source("kv4_decode.cu"), re.S).group(0)
     assert "kv4_join(runs.x, runs.y, ws.n_runs, WARPS)" in kernel and kernel.count("runs.y") == 1
+
+
+class OnDevice:
+    """What the binding asks of a CUDA tensor, without a GPU."""
+
+    def __init__(self, index, *shape, dtype=torch.bfloat16):
+        self.index, self.shape, self.dtype, self.is_cuda = index, torch.Size(shape), dtype, True
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.shape.numel()
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return torch.empty(self.shape, device="meta").stride()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+@pytest.fixture
+def devices(monkeypatch):
+    """Two devices of which device 0 is the current one, and a library that notes the calls it gets."""
+    _build.build()
+    need = binding.kv4_cache_bytes(2, 2, 64)
+    calls = []
+    note = lambda name: lambda *a: calls.append(name) or 0  # noqa: E731
+    fake = SimpleNamespace(bitnet_kv4_cache_bytes=lambda *a: need, bitnet_kv4_attention_workspace_size=lambda *a: 256,
+                           **{n: note(n) for n in ("bitnet_kv4_append", "bitnet_kv4_read", "bitnet_kv4_attention")})
+    monkeypatch.setattr(binding, "lib", lambda: fake)
+    monkeypatch.setattr(binding, "_kv4_torch", None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
+    yield calls, need
+    binding._kv4_torch = None
+
+
+def ints(index, *shape):
+    return OnDevice(index, *shape, dtype=torch.int32)
+
+
+def call(name, cache, batch, rows, **kw):
+    if name == "bitnet_kv4_append":
+        return binding.kv4_append(cache, batch, rows[0], rows[1])
+    if name == "bitnet_kv4_read":
+        return binding.kv4_read(cache, batch, k=rows[0], v=rows[1])
+    return binding.kv4_attention(cache, batch, rows[0], 0.1, out=rows[1], **{"workspace": OnDevice(0, 256, dtype=torch.uint8), **kw})
+
+
+@pytest.mark.parametrize("name", ["bitnet_kv4_append", "bitnet_kv4_read", "bitnet_kv4_attention"])
+@pytest.mark.parametrize("pages,lengths,first,second", [(0, 0, 1, 0), (0, 0, 0, 1), (0, 1, 0, 0), (1, 0, 0, 0), (1, 1, 1, 1)])
+def test_tensors_of_another_device_are_refused(devices, name, pages, lengths, first, second):
+    """Kernels run on the current device and take every pointer as it is."""
+    calls, need = devices
+    for p, n, a, b, refused in ((0, 0, 0, 0, False), (pages, lengths, first, second, True)):
+        cache = binding.KV4Cache(2, 2, 64, pages=OnDevice(p, need, dtype=torch.uint8))
+        batch = binding.KV4Batch(ints(n, 2), ints(n, 1), ints(n, 1, 2), 3, 3)
+        rows = OnDevice(a, 3, 2, 64), OnDevice(b, 3, 2, 64)
+        if refused:
+            with pytest.raises(ValueError):
+                call(name, cache, batch, rows)
+        else:
+            call(name, cache, batch, rows)
+        assert calls == [name]
+
+
+def test_workspaces_and_lengths_of_another_device_are_refused(devices):
+    calls, need = devices
+    cache = binding.KV4Cache(2, 2, 64, pages=OnDevice(0, need, dtype=torch.uint8))
+    batch = binding.KV4Batch(ints(0, 2), ints(0, 1), ints(0, 1, 2), 3, 3)
+    with pytest.raises(ValueError):
+        call("bitnet_kv4_attention", cache, batch, (OnDevice(0, 3, 2, 64), OnDevice(0, 3, 2, 64)),
+             workspace=OnDevice(1, 256, dtype=torch.uint8))
+    for odd in range(3):
+        with pytest.raises(ValueError):
+            binding.KV4Batch(*(ints(int(i == odd), *s) for i, s in enumerate(((2,), (1,), (1, 2)))), 3, 3)
+    assert calls == []
