@@ -101,7 +101,8 @@ int64_t kv4_attention_ws_bytes(const Kv4& c, int dim, int q_heads);
 cudaError_t launch_kv4_attention(const Kv4& c, int dim, const Kv4Attn& a, void* workspace, int num_sms,
                                  cudaStream_t stream);
 
-// A few rows a sequence (kv4_decode.cu): sequences with n * share <= rows, rows = 8, 16 or 32.
+// A few rows a sequence (kv4_decode.cu): sequences with n * share <= rows, rows = 8, 16 or 32. (With 16 it would
+// take up to 32: 16 is for batches without longer sequences.)
 constexpr int kKvDecodeRows = 32;
 int64_t kv4_decode_ws_bytes(const Kv4& c, int dim, int rows);
 cudaError_t launch_kv4_decode(const Kv4& c, int dim, const Kv4Attn& a, int rows, void* ws, int num_sms,

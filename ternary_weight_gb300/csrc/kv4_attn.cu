@@ -12,12 +12,15 @@ namespace bitnet {
 namespace {
 
 // The rows of a sequence that the few-row kernel takes, 0 if it is not needed: a batch of equal, longer
-// sequences has none for it. Beside longer sequences it takes the single tokens.
+// sequences has none for it. Beside longer sequences it takes the single tokens, which make up most of such
+// batches, with the instance for 8 rows (three blocks an SM) where they have no more; drafted tokens of more
+// rows then go with the prompts (which of the two serves them better there was not measured). The instance for 16
+// rows takes up to 32 as two units, so beside longer sequences 32 is the bound that both kernels are told.
 int decode_rows(const Kv4& c, int share) {
   const int64_t all = (int64_t)c.max_q * share;
   if (all > kKvDecodeRows && (c.batch == 1 || (int64_t)c.batch * c.max_q == c.total_q)) return 0;
-  const int64_t rows = all <= kKvDecodeRows ? all : share;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kKvDecodeRows ? kKvDecodeRows : 0;
+  if (all > kKvDecodeRows) return share <= 8 ? 8 : share <= kKvDecodeRows ? kKvDecodeRows : 0;
+  return all <= 8 ? 8 : all <= 16 ? 16 : kKvDecodeRows;
 }
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 

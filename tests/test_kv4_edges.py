@@ -48,3 +48,15 @@ def test_numbers_beyond_the_clamp_take_its_code(dim):
     k, v = binding.kv4_read(w.cache, w.batch(w.kv, w.kv), torch.float32)
     for got, parts in ((k, w.k), (v, w.v)):
         assert np.array_equal(got.cpu().numpy(), w.values(parts)[0].astype(np.float32))
+
+
+@pytest.mark.parametrize("share,new", [(16, 2), (10, 2), (10, 3), (9, 3)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_few_rows_go_one_way_whatever_stands_beside_them(share, new, dim):
+    """A sequence of 17 to 32 rows a head, alone and beside a prompt: the same kernel, so the same bits."""
+    w = World([new, 150], [300, 150], 2, dim, seed=share).fill()
+    q = torch.randn(new + 150, 2 * share, dim, dtype=torch.bfloat16, device="cuda")
+    both = binding.kv4_attention(w.cache, w.batch(w.new, w.kv), q, dim ** -0.5)
+    w.check_attention(q, both, share, dim ** -0.5)
+    alone = binding.kv4_attention(w.cache, w.batch([new, 0], w.kv), q[:new], dim ** -0.5)
+    assert torch.equal(both[:new], alone)
