@@ -81,6 +81,24 @@ __device__ __forceinline__ uint8_t* kv4_block(const Kv4& c, int b, int page, int
   return c.pages + ((int64_t)id * c.kv_heads + h) * block_bytes;
 }
 
+// Softmax weights 2^(c u + off) = 2^(c1 (u - m)) of scores c1 u, m their maximum, in one multiply-add. Its
+// rounding, and that of off, is one of 2^-24 of |c1 m|: a common factor of a row's weights while that is small, but one
+// that takes them all out of range where |c1 m| passes 2^28. Beyond 2^top c is a power of two below
+// c1 with |c m| in [2^(top - 1), 2^top), for which off is exact: scores that far from 0 are apart by units where they
+// differ in fp32 at all, and what little they are brought closer is within the error of their sums.
+struct Kv4Weight {
+  float c, off;
+};
+__device__ __forceinline__ Kv4Weight kv4_weight(float c1, float m, int top) {
+  if (m == -__builtin_huge_valf()) return {c1, 0.0f};
+  Kv4Weight w{c1, -c1 * m};
+  if (fabsf(w.off) > __int_as_float((127 + top) << 23)) {
+    w.c = __int_as_float((253 + top - (int)((__float_as_uint(m) >> 23) & 255u)) << 23);
+    w.off = -w.c * m;
+  }
+  return w;
+}
+
 cudaError_t launch_kv4_append(const Kv4& c, int dim, const void* k, const void* v, bool bf16, int64_t k_stride,
                               int64_t v_stride, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4& c, int dim, void* k, void* v, bool bf16, int64_t k_stride, int64_t v_stride,

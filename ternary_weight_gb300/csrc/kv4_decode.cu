@@ -49,6 +49,7 @@ constexpr int WARPS = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBigStep = 0.015625f;  // 2^-6
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kMostC1 = 1.2676506002282294e30f;  // 2^100
 
 template <int D, int NT>
 struct Shape {
@@ -438,8 +439,9 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           const uint32_t f1 = pack_half2(x[(n + 1) * V + v] * 0.0625f, x[(n + 5) * V + v] * 0.0625f);
           qf[nt][s][0] = f0, qf[nt][s][1] = f1;
         }
-        // c1 of 0 would make NaN of a masked score
-        const float k1 = fmaxf(fabsf(a.scale) * kLog2e * down * 16777216.0f, 1.17549435e-38f);
+        // c1 of 0 would make NaN of a masked score, and c1 of 2^100 already sets unlike scores (2^-72 apart at
+        // least, 2^14 at most) infinitely far apart: from there on it would overflow
+        const float k1 = fminf(fmaxf(fabsf(a.scale) * kLog2e * down * 16777216.0f, 1.17549435e-38f), kMostC1);
         const float k0 = sum * 5.9604644775390625e-8f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -601,8 +603,9 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       uint64_t c1p[NT], off[NT];  // weight = 2^(c1 u + off)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        c1p[nt] = f2pack(c1[nt][0], c1[nt][1]);
-        off[nt] = f2pack(m[nt][0] == kNegInf ? 0.0f : -c1[nt][0] * m[nt][0], m[nt][1] == kNegInf ? 0.0f : -c1[nt][1] * m[nt][1]);
+        const Kv4Weight w0 = kv4_weight(c1[nt][0], m[nt][0], 26), w1 = kv4_weight(c1[nt][1], m[nt][1], 26);
+        c1p[nt] = f2pack(w0.c, w1.c);
+        off[nt] = f2pack(w0.off, w1.off);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

@@ -49,6 +49,7 @@ constexpr int ROWS = 256;   // query rows of a block
 constexpr int TOK = 128;    // cache tokens of a step
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kMostC1 = 1.2089258196146292e24f;  // 2^80
 constexpr float kSlack = 8.0f;  // log2 of how far a weight may exceed 1 before the maximum moves
 
 template <int D>
@@ -442,14 +443,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
     const int w0 = (twin ? 0 : tile * 128) + quarter * 32, r = w0 + lane;  // the warp's first row, the thread's row
     const int mine = twin ? (steps + 1 - tile) / 2 : steps;                // steps of this slot
     const bool there = r < it.rows;
-    // a factor of 0 would make NaN of a masked score
-    const float c1 = fmaxf(fabsf(a.scale) * kLog2e * row_c1[r], 1.17549435e-38f);
+    // a factor of 0 would make NaN of a masked score, and one of 2^80 already sets unlike scores (2^-48 apart at
+    // least, 2^37 at most) infinitely far apart: from there on it would overflow
+    const float c1 = fminf(fmaxf(fabsf(a.scale) * kLog2e * row_c1[r], 1.17549435e-38f), kMostC1);
     const int pos0 = it.s.len - it.s.n + it.tok0;
     // before position 0 nothing is seen, however far before: -1 keeps the mask's differences in 32 bits
     const int pos = there ? max(pos0 + token_of(r), -1) : -1;
     // of the warp's rows: the first position, and the last window's beginning (rows past the end follow the last)
     const int pos_first = pos0 + token_of(w0);
-    const int64_t low_last = (int64_t)pos0 + token_of(max(min(it.rows, w0 + 32) - 1, 0)) - a.window + 1;
+    const int low_last =
+        (int)max((int64_t)0, (int64_t)pos0 + token_of(max(min(it.rows, w0 + 32) - 1, 0)) - a.window + 1);
     const uint32_t lane0 = (uint32_t)(quarter * 32) << 16;
     // this page's scores and weights
     using WT = Weights<D>;
@@ -527,8 +530,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         __syncwarp();
         tc_fence_after();
       }
-      const float off = m == kNegInf ? 0.0f : -c1 * m;
-      const uint64_t c2 = f2pack(c1, c1), off2 = f2pack(off, off);
+      const Kv4Weight wt = kv4_weight(c1, m, 22);
+      const uint64_t c2 = f2pack(wt.c, wt.c), off2 = f2pack(wt.off, wt.off);
       uint64_t l2[2] = {0, 0};
 #pragma unroll
       for (int ch = 0; ch < 4; ++ch) {

@@ -50,6 +50,27 @@ def test_numbers_beyond_the_clamp_take_its_code(dim):
         assert np.array_equal(got.cpu().numpy(), w.values(parts)[0].astype(np.float32))
 
 
+@pytest.mark.parametrize("dim,new,share,kv", [(64, 1, 4, 200), (128, 1, 4, 200), (128, 1, 2, 5000), (128, 5, 4, 700), (64, 130, 2, 700), (128, 300, 1, 700)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("log2", [16, 22, 26, 30, 34, 40, 60, 100, 115, 120, 126])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_large_scores_choose_their_token(dim, new, share, kv, dtype, log2, sign):
+    """Scores from thousands to the largest of fp32, all of either sign, with one token far above the others:
+    its value is the result, to the roundings of values (fp16) and of the result (bf16)."""
+    w = World([new], [kv], 2, dim, "f32" if dtype == torch.float32 else "bf16", seed=log2)
+    at = (kv - new) // 2
+    r = w.rng.choice([-1.0, 1.0], size=(2, dim))
+    q = torch.tensor(np.repeat(r, share, 0)[None].repeat(new, 0) * 2.0 ** log2).to(dtype).cuda()
+    size = 1.0 + w.rng.random((kv, 2, 1)) if sign > 0 else 3.0 + w.rng.random((kv, 2, 1))
+    size[at] = 3.0 if sign > 0 else 1.0
+    w.k[0] = torch.tensor(r[None] * size * (1 + 0.05 * w.rng.random((kv, 2, dim)))).to(w.dtype).float().numpy()
+    w.fill()
+    got = binding.kv4_attention(w.cache, w.batch([new], [kv]), q, sign * dim ** -0.5).float().cpu().numpy()
+    want = np.repeat(w.values(w.v)[0][at], share, 0)[None]
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want) * 1.01 + 2.0 ** -10 * np.abs(want).max(-1, keepdims=True)).all()
+
+
 @pytest.mark.parametrize("share,new", [(16, 2), (10, 2), (10, 3), (9, 3)])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_few_rows_go_one_way_whatever_stands_beside_them(share, new, dim):
