@@ -9,15 +9,18 @@
 //   raw[t][r] = sum_d code_k[t][d] q'[r][d]     tokens x rows, m16n8k16 with the codes as the A operand
 //   s = scale (step_k raw + base_k sum(q))      the raw dot and its correction, fp32
 //   p = 2^(s log2 e - m), l = sum p             running maximum m and sum l, fp32
-//   O[d][r] += sum_t code_v[t][d] w[t][r]       dims x rows, w = p step_v / vref as fp16
-//   bsum[r] += p base_v                         out = (vref O + bsum) / l
+//   w[t][r] = up p step_v                       the weights of the codes, as fp16
+//   O[d][r] += sum_t code_v[t][d] w[t][r]       dims x rows
+//   bsum[r] += w base_v / step_v                out = (O + bsum) / (up l)
 // A code enters as the fp16 subnormal c * 2^-24 (its nibble masked out of the word) or c * 2^-20 (the
 // nibble above, not shifted): products and fp32 sums of subnormals are exact in the matrix unit, and
 // the factors go into q' (whose dims of odd nibbles are scaled by 2^-4) and into the last scaling of
 // O. So a word of 8 codes costs 5 instructions for keys; for values, pairs of tokens are joined byte
 // by byte first (0.75 instructions a code). q' is q at a power-of-two scale of its own row, as fp16.
-// w is fp16: vref, a power of two above every step_v met so far by the warp, keeps it below 1, so
-// the rounding is 2^-11 of a weight and at most 2^-25 of the largest for the small ones.
+// up, a power of two of each row, puts the largest p step_v that the warp has met near 2^8 (and up to 2^15 before it
+// is moved), whatever steps tokens without weight have: so a w is rounded by 2^-11 of itself, and the small ones by
+// 2^-32 of the row's largest at most. The rounded w also takes the base, so that the two terms of a value
+// do not part; where the base is more than 64 steps the unrounded one does, since the code's term is the small one.
 // The scores' fragment (tokens x rows) becomes the second product's B fragment by an 8 x 8 transpose
 // in registers.
 //
@@ -47,9 +50,12 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kBigStep = 0.015625f;  // 2^-6
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kMostC1 = 1.2676506002282294e30f;  // 2^100
+// operands of the values' product: where the largest of a row is put, how far one may grow before that is done
+// again, the least that counts for it, and the base, in steps, up to which the rounded one also takes the base
+constexpr float kFull = 256.0f, kTop = 32768.0f, kLeast = 7.888609052210118e-31f, kFar = 64.0f;
+constexpr float kFirstUp = kFull / kLeast;
 
 template <int D, int NT>
 struct Shape {
@@ -97,6 +103,9 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// the least power of two that is not below x (x > 0), and the inverse of a power of two
+__device__ __forceinline__ float power_from(float x) { return __uint_as_float((__float_as_uint(x) + 0x007fffffu) & 0x7f800000u); }
+__device__ __forceinline__ float inverse(float power) { return __uint_as_float(0x7f000000u - __float_as_uint(power)); }
 // two fp32 lanes an instruction
 __device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
   uint64_t r;
@@ -383,8 +392,8 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
 
   uint32_t qf[NT][KS][2];
   // per row (column of the fragments): u = step raw + base qs is the score up to the factor c1 >= 0,
-  // m its running maximum
-  float c1[NT][2], qs2[NT][2], m[NT][2], bs[NT][2];
+  // m its running maximum; O and bs are sums of weights times steps, times up, a power of two
+  float c1[NT][2], qs2[NT][2], m[NT][2], up[NT][2], bs[NT][2];
   uint64_t l[NT];
   int pos[NT][2];
   float O[NT][KS][4];
@@ -395,7 +404,6 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
   while (use.i < use.until) {
     const bool begun = use.i == 0;  // this run holds the unit's first page
     const int row0 = S::ROWS * use.template group<S::GROUPS>();
-    float vref = 5.9604644775390625e-8f;  // 2^-24: no step is smaller, but 0
     {  // a new unit: its queries
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -423,11 +431,11 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
         // number, also where it is scaled by 2^-4. Not below e = -100, and not for infinities.
         int e = (int)(__float_as_uint(mx) >> 23) - 127;
         e = e == 128 ? 13 : max(e, -100);
-        const float up = __int_as_float((13 - e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f), down = __int_as_float((e - 13 + 127) << 23);
+        const float grow = __int_as_float((13 - e + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f), down = __int_as_float((e - 13 + 127) << 23);
         float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < D / 4; ++k) {
-          x[k] = __half2float(__float2half_rn(x[k] * up));
+          x[k] = __half2float(__float2half_rn(x[k] * grow));
           sum += x[k];
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -450,6 +458,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           qs2[nt][j] = __shfl_sync(0xffffffffu, k0, 4 * col);
           pos[nt][j] = use.s.len - use.s.n + (row0 + 8 * nt + col) / a.share;
           m[nt][j] = kNegInf;
+          up[nt][j] = kFirstUp;
           bs[nt][j] = 0.0f;
         }
         l[nt] = 0;
@@ -473,10 +482,9 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       const bool whole = first + kKvPage <= use.s.len - use.s.n + 1 &&
                          (first >= last_low || first + kKvPage <= a.sinks);
 
-      // the parameters of two tokens a lane, as fp32: key step and base, value step and base
-      float vmax = 0.0f;
-      float4 two[2];
+      // the parameters of two tokens a lane, as fp32: key step and base, value step and base over step
       {
+        float4 two[2];
         const uint4 u = lds<uint4>(blk + kKvPage * D + lane * 16);
         const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -490,25 +498,9 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
             const int j = first + kv4_rho_inv(2 * lane + e);
             none |= j >= use.s.len || (j < first_low && j >= a.sinks);
           }
-          two[e] = make_float4(pk.x, pk.y + z, none ? 0.0f : pv.x, none ? 0.0f : pv.y);
-          vmax = fmaxf(vmax, two[e].z);
-        }
-        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
-        if (vmax >= vref) {
-          const float now = __uint_as_float((__float_as_uint(vmax) & 0x7f800000u) + 0x00800000u), f = vref / now;
-          vref = now;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) O[nt][k][j] *= f;
-        }
-        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(vref));  // 1 / vref, a power of two
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          two[e].z *= inv;
-          if (two[e].z >= kBigStep) two[e].w = __fdividef(two[e].w, two[e].z);
+          // codes of a step of 0 are 0: any other step stands for the same value
+          const float step = pv.x > 0.0f ? pv.x : fabsf(pv.y);
+          two[e] = make_float4(pk.x, pk.y + z, none ? 0.0f : step, none || step == 0.0f ? 0.0f : __fdividef(pv.y, step));
           par[2 * lane + e] = two[e];
         }
         __syncwarp();
@@ -568,8 +560,8 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           }
       }
       // running maxima
-      float mn[NT][2];
-      bool grows = false;
+      float mn[NT][2], al[NT][2];  // al: what is left of the old weights
+      bool moves = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -581,47 +573,79 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
           mn[nt][j] = v;
-          grows |= v > m[nt][j];
+          al[nt][j] = 1.0f;
+          moves |= v > m[nt][j];
         }
-      if (__any_sync(0xffffffffu, grows)) {
+      moves = __any_sync(0xffffffffu, moves);
+      if (moves) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float al[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            al[j] = mn[nt][j] == kNegInf ? 1.0f : exp2_approx(c1[nt][j] * (m[nt][j] - mn[nt][j]));
+            al[nt][j] = mn[nt][j] == kNegInf ? 1.0f : exp2_approx(c1[nt][j] * (m[nt][j] - mn[nt][j]));
             m[nt][j] = mn[nt][j];
-            bs[nt][j] *= al[j];
           }
-          l[nt] = fma2(l[nt], f2pack(al[0], al[1]), 0);
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) O[nt][k][j] *= al[j & 1];
+          l[nt] = fma2(l[nt], f2pack(al[nt][0], al[nt][1]), 0);
         }
       }
-      uint64_t c1p[NT], off[NT];  // weight = 2^(c1 u + off)
+      // weights, times steps: what a code adds to its row
+      float most[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const Kv4Weight w0 = kv4_weight(c1[nt][0], m[nt][0], 26), w1 = kv4_weight(c1[nt][1], m[nt][1], 26);
-        c1p[nt] = f2pack(w0.c, w1.c);
-        off[nt] = f2pack(w0.off, w1.off);
+        const uint64_t c1p = f2pack(w0.c, w1.c), off = f2pack(w0.off, w1.off);
+        most[nt][0] = most[nt][1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float step = par[16 * i + 8 * e + g].z;
+            const float2 t = f2unpack(fma2(f2pack(s[nt][i][2 * e], s[nt][i][2 * e + 1]), c1p, off));
+            const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
+            l[nt] = add2(l[nt], f2pack(p0, p1));
+            s[nt][i][2 * e] = p0 * step, s[nt][i][2 * e + 1] = p1 * step;
+            most[nt][0] = fmaxf(most[nt][0], s[nt][i][2 * e]);
+            most[nt][1] = fmaxf(most[nt][1], s[nt][i][2 * e + 1]);
+          }
+        moves |= fmaxf(most[nt][0] * up[nt][0], most[nt][1] * up[nt][1]) > kTop;
+      }
+      // their scale follows the largest of them
+      if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float f[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float v = most[nt][j];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            const float old = inverse(up[nt][j]);
+            v = fmaxf(fmaxf(v, al[nt][j] * (kFull * old)), kLeast);
+            up[nt][j] = kFull * inverse(power_from(v));
+            f[j] = al[nt][j] * (up[nt][j] * old);
+            bs[nt][j] *= f[j];
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) O[nt][k][j] *= f[j & 1];
+        }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t wf[NT][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float2 v = reinterpret_cast<const float2*>(&par[16 * i + 8 * e + g])[1];
+          const float ratio = par[16 * i + 8 * e + g].w;
+          const bool shared = fabsf(ratio) <= kFar;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float2 t = f2unpack(fma2(f2pack(s[nt][i][2 * e], s[nt][i][2 * e + 1]), c1p[nt], off[nt]));
-            const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
-            l[nt] = add2(l[nt], f2pack(p0, p1));
-            const uint32_t w = pack_half2(p0 * v.x, p1 * v.x);
+            const float y0 = s[nt][i][2 * e] * up[nt][0], y1 = s[nt][i][2 * e + 1] * up[nt][1];
+            const uint32_t w = pack_half2(y0, y1);
             const float2 wr = __half22float2(*reinterpret_cast<const __half2*>(&w));
-            bs[nt][0] = fmaf(v.x >= kBigStep ? wr.x : p0, v.y, bs[nt][0]);
-            bs[nt][1] = fmaf(v.x >= kBigStep ? wr.y : p1, v.y, bs[nt][1]);
+            bs[nt][0] = fmaf(shared ? wr.x : y0, ratio, bs[nt][0]);
+            bs[nt][1] = fmaf(shared ? wr.y : y1, ratio, bs[nt][1]);
             wf[nt][e] = transpose8x8(w);
           }
         }
@@ -677,8 +701,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           }
           const int r = 8 * nt + 2 * q4 + j;
           if (r >= unit_rows) continue;
-          const float lo = vref * 16777216.0f, hi = vref * 1048576.0f;
-          const float norm = alone ? (sl == 0.0f ? 0.0f : 1.0f / sl) : 1.0f;
+          const float norm = inverse(up[nt][j]) * (alone ? (sl == 0.0f ? 0.0f : 1.0f / sl) : 1.0f);
           uint16_t* out = a.out + (int64_t)(use.s.q0 + (row0 + r) / a.share) * a.out_stride +
                           (int64_t)(use.template head<S::GROUPS>() * a.share + (row0 + r) % a.share) * D;
 #pragma unroll
@@ -686,7 +709,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
             float y[W / 8];
 #pragma unroll
             for (int x = 0; x < W / 8; ++x)
-              y[x] = fmaf(O[nt][4 * x + (n >> 1)][(n & 1) * 2 + j], n & 1 ? hi : lo, sb) * norm;
+              y[x] = fmaf(O[nt][4 * x + (n >> 1)][(n & 1) * 2 + j], n & 1 ? 1048576.0f : 16777216.0f, sb) * norm;
             const int d = W * n + (W / 8) * g;
             if constexpr (D == 128) {
               if (alone)

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import kv4_reference as ref
 from test_kv4 import World, attend
 from ternary_weight_gb300 import _build, binding
 
@@ -48,6 +49,46 @@ def test_numbers_beyond_the_clamp_take_its_code(dim):
     k, v = binding.kv4_read(w.cache, w.batch(w.kv, w.kv), torch.float32)
     for got, parts in ((k, w.k), (v, w.v)):
         assert np.array_equal(got.cpu().numpy(), w.values(parts)[0].astype(np.float32))
+
+
+def directed(new, kv, dim, share, at, nats, rng, dtype, spread=0.1):
+    """Queries near one direction for each key/value head, and keys among which token `at` stands `nats`
+    above (below, if negative) the others, whose scores are small. Returns q (new, heads * share, dim) and k."""
+    heads = 2
+    r = rng.normal(size=(heads, dim))
+    q = np.repeat(r, share, 0)[None] * (1 + 0.02 * rng.random((new, heads * share, 1)))
+    k = rng.normal(size=(kv, heads, dim)) * spread
+    k[at] = r * nats / ((r * r).sum(-1, keepdims=True) * dim ** -0.5)
+    return torch.tensor(q).to(dtype).cuda(), torch.tensor(k).to(dtype).float().numpy()
+
+
+SHAPES = [(64, 1, 4, 64), (128, 1, 4, 64), (128, 1, 4, 700), (64, 1, 8, 6000), (128, 5, 4, 700), (128, 3, 4, 6000), (64, 100, 4, 700)]
+
+
+@pytest.mark.parametrize("dim,new,share,kv", SHAPES)
+@pytest.mark.parametrize("ratio", [2.0 ** 14, 2.0 ** 17, 2.0 ** 20])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+def test_a_value_without_weight_costs_the_others_nothing(dim, new, share, kv, ratio, where):
+    """One token with a weight of e^-60 and values many times the others': the result is that of the others, to
+    the roundings of weights and values (fp16), queries and keys (fp16: 2^-10 of what they add to a score, fp32
+    sums within 2^-16), and the result (bf16). A weight times its step is off by 2^-32 of a row's largest at
+    least, a code or (where base and code go together) a number of up to 79 steps."""
+    w = World([new], [kv], 2, dim, "f32", seed=kv)
+    at = {"first": 0, "middle": (kv - new) // 2, "last": kv - new}[where]
+    q, w.k[0] = directed(new, kv, dim, share, at, -60.0, w.rng, torch.float32)
+    v = w.rng.normal(size=(kv, 2, dim)) + w.rng.normal(size=(1, 2, dim))
+    v *= 2.0 ** -8
+    v[at] *= ratio
+    w.v[0] = v.astype(np.float32)
+    w.fill()
+    got = binding.kv4_attention(w.cache, w.batch([new], [kv]), q, dim ** -0.5).float().cpu().numpy()
+    kk, vv = (np.delete(w.values(x)[0], at, 0) for x in (w.k, w.v))
+    o, av, size = ref.attention(q.cpu().numpy(), kk, vv, np.arange(kv - new, kv) - 1, dim ** -0.5, 0, 0)
+    d = dim ** -0.5 * size * (2.0 ** -10 + 2.0 ** -16)
+    low = 2.0 ** -32 * 79 / 15 * kv * 2 * np.abs(vv).max()
+    bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + np.expm1(2 * d)[..., None]) * av * 1.01 + low
+    err = np.abs(got - o)
+    assert (err <= bound).all(), "worst %.3g times the bound" % (err / bound).max()
 
 
 @pytest.mark.parametrize("dim,new,share,kv", [(64, 1, 4, 200), (128, 1, 4, 200), (128, 1, 2, 5000), (128, 5, 4, 700), (64, 130, 2, 700), (128, 300, 1, 700)])
