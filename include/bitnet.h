@@ -458,8 +458,12 @@ BITNET_API int bitnet_kv4_read(const bitnet_kv4_cache *cache, const bitnet_kv4_b
  *            at q + r * q_stride (elements). A query is used as fp16 at a power-of-two scale of its
  *            own: bf16 values keep their bits (those below 2^-28 of the row's largest may not),
  *            fp32 values round to 11 bits.
- *   out    : total_q rows of q_heads x head_dim, bf16 (device, written), row stride out_stride. The
- *            sums are held in fp32; softmax weights enter the product with the values as fp16.
+ *   out    : total_q rows of q_heads x head_dim, bf16 (device, written), row stride out_stride. Scores
+ *            and all sums are held in fp32. Softmax weights enter the product with the values as
+ *            fp16, rounded by 2^-11 of themselves, the small ones by 2^-32 of the row's largest (for few
+ *            rows, of its largest weight times step). Keys and values enter as codes with fp32 steps and
+ *            bases for few rows (tokens x q_heads / kv_heads of a sequence, 32 at most), else they
+ *            are rounded to fp16 (2^-11 of each number).
  *   q_heads: a multiple of kv_heads, at most 128 * kv_heads, and total_q * q_heads / kv_heads < 2^31 - 4096
  *   window : 0 for all positions, else 1 .. 2^31 - 1; sinks: 0 .. 2^31 - 1 (unused with window 0)
  *   workspace : device, 256-byte aligned, at least bitnet_kv4_attention_workspace_size bytes (for

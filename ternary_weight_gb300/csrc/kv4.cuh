@@ -85,16 +85,17 @@ __device__ __forceinline__ uint8_t* kv4_block(const Kv4& c, int b, int page, int
 // rounding, and that of off, is one of 2^-24 of |c1 m|: a common factor of a row's weights while that is small, but one
 // that takes them all out of range where |c1 m| passes 2^28. Beyond 2^top c is a power of two below
 // c1 with |c m| in [2^(top - 1), 2^top), for which off is exact: scores that far from 0 are apart by units where they
-// differ in fp32 at all, and what little they are brought closer is within the error of their sums.
+// differ in fp32 at all, and what little they are brought closer is within the error of their sums. The weights are
+// 2^lift (a whole number) times what they stand for.
 struct Kv4Weight {
   float c, off;
 };
-__device__ __forceinline__ Kv4Weight kv4_weight(float c1, float m, int top) {
+__device__ __forceinline__ Kv4Weight kv4_weight(float c1, float m, int top, float lift = 0.0f) {
   if (m == -__builtin_huge_valf()) return {c1, 0.0f};
-  Kv4Weight w{c1, -c1 * m};
+  Kv4Weight w{c1, fmaf(-c1, m, lift)};
   if (fabsf(w.off) > __int_as_float((127 + top) << 23)) {
     w.c = __int_as_float((253 + top - (int)((__float_as_uint(m) >> 23) & 255u)) << 23);
-    w.off = -w.c * m;
+    w.off = fmaf(-w.c, m, lift);
   }
   return w;
 }

@@ -5,7 +5,7 @@
 // heads that share keys and values share their expansion too) as two tiles of 128, and walks over the
 // cache 128 tokens (two pages) at a time:
 //   S_t = Q_t K^T     128 x 128, K = D: both operands in shared memory (128-byte swizzle, K-major)
-//   P_t = 2^(c1 S - c1 m)  in registers, written over S_t in tensor memory as fp16
+//   P_t = 2^(c1 S - c1 m + 7)  in registers, written over S_t in tensor memory as fp16
 //   O_t += P_t V      128 x D, K = 128: P from tensor memory, V^T in shared memory
 // What bounds it: 4096 tokens (20 and 5 heads x 128) take 95.3 us, 902 TFLOP/s of the measured 1902, with the
 // tensor cores 44% busy and 2.7 of 4 issue slots used; 4 chunks with a window of 1024 (32 and 8 heads x 64)
@@ -17,7 +17,8 @@
 // the last product and the rows' way out.
 //
 // Operands are fp16 and sums fp32: q at a power-of-two scale of its row, k and v as step * code + base
-// rounded to fp16 (2^-11 of the number itself, less than the 4-bit step by far), p up to 2^8.
+// rounded to fp16 (2^-11 of the number itself, less than the 4-bit step by far), p up to 2^15,
+// a scale of 2^7 among that.
 // The codes are expanded once for both tiles: a code masked into the mantissa of 1024.0 (or 16 of it)
 // becomes an exact fp16 by one multiply-add, the number by another. Word w of a key goes to columns
 // 8 w .. 8 w + 7 in nibble order 0 4 1 5 2 6 3 7; the queries are stored in the same order. Values are
@@ -50,7 +51,10 @@ constexpr int TOK = 128;    // cache tokens of a step
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kMostC1 = 1.2089258196146292e24f;  // 2^80
-constexpr float kSlack = 8.0f;  // log2 of how far a weight may exceed 1 before the maximum moves
+constexpr float kSlack = 8.0f;  // log2 of how far a weight may exceed that of the maximum in use before it is moved
+// log2 of what all weights are scaled by (their sums too): up to 2^15 as fp16, so the small ones are rounded by 2^-32
+// of the row's largest at most, where a first token takes most of the weight and the others' values are what counts
+constexpr float kLift = 7.0f;
 
 template <int D>
 struct Prompt {
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         __syncwarp();
         tc_fence_after();
       }
-      const Kv4Weight wt = kv4_weight(c1, m, 22);
+      const Kv4Weight wt = kv4_weight(c1, m, 22, kLift);
       const uint64_t c2 = f2pack(wt.c, wt.c), off2 = f2pack(wt.off, wt.off);
       uint64_t l2[2] = {0, 0};
 #pragma unroll

@@ -91,6 +91,32 @@ def test_a_value_without_weight_costs_the_others_nothing(dim, new, share, kv, ra
     assert (err <= bound).all(), "worst %.3g times the bound" % (err / bound).max()
 
 
+@pytest.mark.parametrize("dim,new,share,kv", SHAPES)
+@pytest.mark.parametrize("nats", [9.0, 13.0, 16.0])
+@pytest.mark.parametrize("first", ["zero", "constant", "small"])
+def test_small_weights_beside_a_large_one(dim, new, share, kv, nats, first):
+    """The first token takes nearly all of the weight and has values of nothing, or next to it: what the others
+    give, each e^-nats of it, has to come out. The bound is that of the roundings: weights enter the
+    product with 11 bits and, relative to the row's largest, 2^-32 at least; values as fp16, keys as
+    fp16 (2^-11 of what they add to a score); fp32 sums within 2^-16 of them; the result as bf16."""
+    w = World([new], [kv], 2, dim, "bf16", seed=kv)
+    q, w.k[0] = directed(new, kv, dim, share, 0, nats, w.rng, torch.bfloat16)
+    v = 1 + w.rng.normal(size=(kv, 2, dim))
+    v[0] = {"zero": 0 * v[0], "constant": 0 * v[0] + 1e-6, "small": v[0] * 1e-6}[first]
+    w.v[0] = torch.tensor(v).bfloat16().float().numpy()
+    w.fill()
+    got = binding.kv4_attention(w.cache, w.batch([new], [kv]), q, dim ** -0.5).float().cpu().numpy()
+    kk, vv = w.values(w.k)[0], w.values(w.v)[0]
+    pos = np.arange(kv - new, kv)
+    o, av, size = ref.attention(q.float().cpu().numpy(), kk, vv, pos, dim ** -0.5, 0, 0)
+    d = dim ** -0.5 * size * (2.0 ** -11 + 2.0 ** -16)
+    # sum |v| over the sum of weights relative to the largest (at least 1)
+    low = 2.0 ** -32 * np.repeat(np.abs(vv).sum(0), share, 0)[None]
+    bound = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + np.expm1(2 * d)[..., None]) * av * 1.01 + low
+    err = np.abs(got - o)
+    assert (err <= bound).all(), "worst %.3g times the bound" % (err / bound).max()
+
+
 @pytest.mark.parametrize("dim,new,share,kv", [(64, 1, 4, 200), (128, 1, 4, 200), (128, 1, 2, 5000), (128, 5, 4, 700), (64, 130, 2, 700), (128, 300, 1, 700)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("log2", [16, 22, 26, 30, 34, 40, 60, 100, 115, 120, 126])
