@@ -220,7 +220,6 @@ struct Waits {
       polls = 1;
     }
   }
-  __device__ __forceinline__ bool gave_up() const { return polls == 1; }
 };
 
 // x / d for x < 512, 1 <= d <= 128, with m = ceil(65536 / d)
@@ -890,11 +889,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(Kv4 c, Kv4Attn a
         }
       }
     }
-    if (wait.gave_up()) {  // what was issued ends before the tensor memory is given back
-      if (leader) mma_commit(&all_done);
-      wait.polls = kMaxPolls;
-      wait(&all_done, 0);
-    }
+    // what was issued ends before the tensor memory is given back, whichever warp's wait gave up before
+    if (leader) mma_commit(&all_done);
+    __syncwarp();
+    wait.polls = kMaxPolls;
+    wait(&all_done, 0);
   }
   if (bad) record_device_error(kErrRange);
   __syncwarp();

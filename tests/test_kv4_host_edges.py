@@ -26,6 +26,18 @@ def test_softmax_warps_fence_behind_every_wait_for_a_product():
     assert all(w.startswith("tc_fence_after();") for w in waits), waits
 
 
+def test_products_end_before_tensor_memory_is_given_back():
+    """The issuing warp waits for the last of its products whatever happened before: a softmax warp whose own wait
+    gave up goes on, so that warps' waits alone do not keep the tensor memory until then."""
+    issue = re.search(r"= MMA issue =.*?tmem_dealloc", source("kv4_prompt.cu"), re.S).group(0)
+    lines = [x.strip() for x in issue.splitlines()]
+    at = lines.index("if (leader) mma_commit(&all_done);")
+    assert lines[at + 1:at + 4] == ["__syncwarp();", "wait.polls = kMaxPolls;", "wait(&all_done, 0);"]
+    assert lines[at + 4] == "}" and "if (bad)" in lines[at + 5]  # the end of the role
+    depth = sum(x.count("{") - x.count("}") for x in lines[:at])
+    assert depth == 0  # of the role's own block: not under a condition
+
+
 JOIN = r"""
 #include "kv4_join.h"
 #include <cstdio>
