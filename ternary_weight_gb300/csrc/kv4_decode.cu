@@ -53,8 +53,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kMostC1 = 1.2676506002282294e30f;  // 2^100
 // operands of the values' product: where the largest of a row is put, how far one may grow before that is done
-// again, the least that counts for it, and the base, in steps, up to which the rounded one also takes the base
-constexpr float kFull = 256.0f, kTop = 32768.0f, kLeast = 7.888609052210118e-31f, kFar = 64.0f;
+// again, the least that counts for it (2^-80), and the base, in steps, up to which the rounded one also takes the base
+constexpr float kFull = 256.0f, kTop = 32768.0f, kLeast = 8.271806125530277e-25f, kFar = 64.0f;
 constexpr float kFirstUp = kFull / kLeast;
 
 template <int D, int NT>
@@ -103,9 +103,10 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// the least power of two that is not below x (x > 0), and the inverse of a power of two
+// the least power of two that is not below x (x > 0); the inverse of a power of two, and its exponent
 __device__ __forceinline__ float power_from(float x) { return __uint_as_float((__float_as_uint(x) + 0x007fffffu) & 0x7f800000u); }
 __device__ __forceinline__ float inverse(float power) { return __uint_as_float(0x7f000000u - __float_as_uint(power)); }
+__device__ __forceinline__ float exponent(float power) { return (float)((int)(__float_as_uint(power) >> 23) - 127); }
 // two fp32 lanes an instruction
 __device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
   uint64_t r;
@@ -125,6 +126,16 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // plain shared-memory loads: the compiler may move them past one another, not past the barriers
@@ -392,9 +403,9 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
 
   uint32_t qf[NT][KS][2];
   // per row (column of the fragments): u = step raw + base qs is the score up to the factor c1 >= 0,
-  // m its running maximum; O and bs are sums of weights times steps, times up, a power of two
-  float c1[NT][2], qs2[NT][2], m[NT][2], up[NT][2], bs[NT][2];
-  uint64_t l[NT];
+  // m its running maximum; weights, and so l, O and bs, are up times what they stand for, a power of two
+  float c1[NT][2], qs2[NT][2], m[NT][2], up[NT][2];
+  uint64_t l[NT], bs[NT];
   int pos[NT][2];
   float O[NT][KS][4];
   int stage = 0;
@@ -459,9 +470,8 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           pos[nt][j] = use.s.len - use.s.n + (row0 + 8 * nt + col) / a.share;
           m[nt][j] = kNegInf;
           up[nt][j] = kFirstUp;
-          bs[nt][j] = 0.0f;
         }
-        l[nt] = 0;
+        l[nt] = bs[nt] = 0;
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -483,6 +493,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
                          (first >= last_low || first + kKvPage <= a.sinks);
 
       // the parameters of two tokens a lane, as fp32: key step and base, value step and base over step
+      bool far = false;  // a base of many steps
       {
         float4 two[2];
         const uint4 u = lds<uint4>(blk + kKvPage * D + lane * 16);
@@ -502,7 +513,9 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           const float step = pv.x > 0.0f ? pv.x : fabsf(pv.y);
           two[e] = make_float4(pk.x, pk.y + z, none ? 0.0f : step, none || step == 0.0f ? 0.0f : __fdividef(pv.y, step));
           par[2 * lane + e] = two[e];
+          far |= fabsf(two[e].w) > kFar;
         }
+        far = __any_sync(0xffffffffu, far);
         __syncwarp();
       }
 
@@ -588,32 +601,34 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           l[nt] = fma2(l[nt], f2pack(al[nt][0], al[nt][1]), 0);
         }
       }
-      // weights, times steps: what a code adds to its row
+      // weights times up in l; times steps, what a code adds to its row, in s
       float most[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const Kv4Weight w0 = kv4_weight(c1[nt][0], m[nt][0], 26), w1 = kv4_weight(c1[nt][1], m[nt][1], 26);
-        const uint64_t c1p = f2pack(w0.c, w1.c), off = f2pack(w0.off, w1.off);
+        const Kv4Weight w0 = kv4_weight(c1[nt][0], m[nt][0], 22), w1 = kv4_weight(c1[nt][1], m[nt][1], 22);
+        const uint64_t c1p = f2pack(w0.c, w1.c), off = f2pack(w0.off + exponent(up[nt][0]), w1.off + exponent(up[nt][1]));
         most[nt][0] = most[nt][1] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float step = par[16 * i + 8 * e + g].z;
             const float2 t = f2unpack(fma2(f2pack(s[nt][i][2 * e], s[nt][i][2 * e + 1]), c1p, off));
-            const float p0 = exp2_approx(t.x), p1 = exp2_approx(t.y);
-            l[nt] = add2(l[nt], f2pack(p0, p1));
-            s[nt][i][2 * e] = p0 * step, s[nt][i][2 * e + 1] = p1 * step;
-            most[nt][0] = fmaxf(most[nt][0], s[nt][i][2 * e]);
-            most[nt][1] = fmaxf(most[nt][1], s[nt][i][2 * e + 1]);
+            const uint64_t p = f2pack(exp2_approx(t.x), exp2_approx(t.y));
+            l[nt] = add2(l[nt], p);
+            const float2 y = f2unpack(mul2(p, f2pack(step, step)));
+            s[nt][i][2 * e] = y.x, s[nt][i][2 * e + 1] = y.y;
           }
-        moves |= fmaxf(most[nt][0] * up[nt][0], most[nt][1] * up[nt][1]) > kTop;
+          most[nt][0] = max3(most[nt][0], s[nt][i][0], s[nt][i][2]);
+          most[nt][1] = max3(most[nt][1], s[nt][i][1], s[nt][i][3]);
+        }
+        moves |= fmaxf(most[nt][0], most[nt][1]) > kTop;
       }
       // their scale follows the largest of them
       if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float f[2];
+          float f[2], more[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float v = most[nt][j];
@@ -621,11 +636,15 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             const float old = inverse(up[nt][j]);
-            v = fmaxf(fmaxf(v, al[nt][j] * (kFull * old)), kLeast);
+            v = fmaxf(fmaxf(v, al[nt][j] * kFull) * old, kLeast);
             up[nt][j] = kFull * inverse(power_from(v));
-            f[j] = al[nt][j] * (up[nt][j] * old);
-            bs[nt][j] *= f[j];
+            more[j] = up[nt][j] * old;
+            f[j] = al[nt][j] * more[j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[nt][i][j] *= more[j], s[nt][i][2 + j] *= more[j];
           }
+          l[nt] = mul2(l[nt], f2pack(more[0], more[1]));
+          bs[nt] = mul2(bs[nt], f2pack(f[0], f[1]));
 #pragma unroll
           for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -638,14 +657,11 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float ratio = par[16 * i + 8 * e + g].w;
-          const bool shared = fabsf(ratio) <= kFar;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float y0 = s[nt][i][2 * e] * up[nt][0], y1 = s[nt][i][2 * e + 1] * up[nt][1];
-            const uint32_t w = pack_half2(y0, y1);
+            const uint32_t w = pack_half2(s[nt][i][2 * e], s[nt][i][2 * e + 1]);
             const float2 wr = __half22float2(*reinterpret_cast<const __half2*>(&w));
-            bs[nt][0] = fmaf(shared ? wr.x : y0, ratio, bs[nt][0]);
-            bs[nt][1] = fmaf(shared ? wr.y : y1, ratio, bs[nt][1]);
+            bs[nt] = fma2(f2pack(wr.x, wr.y), f2pack(ratio, ratio), bs[nt]);
             wf[nt][e] = transpose8x8(w);
           }
         }
@@ -672,6 +688,21 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
                             wf[nt][0], wf[nt][1]);
         }
       }
+      if (far) {  // a base of many steps takes what the rounding took
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float ratio = par[16 * i + 8 * e + g].w;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float y0 = s[nt][i][2 * e], y1 = s[nt][i][2 * e + 1];
+              const float r = fabsf(ratio) > kFar ? ratio : 0.0f;
+              const float d0 = y0 - __half2float(__float2half_rn(y0)), d1 = y1 - __half2float(__float2half_rn(y1));
+              bs[nt] = fma2(f2pack(d0, d1), f2pack(r, r), bs[nt]);
+            }
+          }
+      }
       __syncwarp();  // every lane has read the block: its place may be written again
       --in_flight;
       fetch(stage);
@@ -692,8 +723,8 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float2 ls = f2unpack(l[nt]);
-          float sl = j ? ls.y : ls.x, sb = bs[nt][j];
+          const float2 ls = f2unpack(l[nt]), bsum = f2unpack(bs[nt]);
+          float sl = j ? ls.y : ls.x, sb = j ? bsum.y : bsum.x;
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             sl += __shfl_xor_sync(0xffffffffu, sl, o);
@@ -701,7 +732,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           }
           const int r = 8 * nt + 2 * q4 + j;
           if (r >= unit_rows) continue;
-          const float norm = inverse(up[nt][j]) * (alone ? (sl == 0.0f ? 0.0f : 1.0f / sl) : 1.0f);
+          const float norm = alone ? (sl == 0.0f ? 0.0f : 1.0f / sl) : inverse(up[nt][j]);
           uint16_t* out = a.out + (int64_t)(use.s.q0 + (row0 + r) / a.share) * a.out_stride +
                           (int64_t)(use.template head<S::GROUPS>() * a.share + (row0 + r) % a.share) * D;
 #pragma unroll
@@ -725,7 +756,7 @@ __global__ void __launch_bounds__(32 * WARPS, Shape<D, NT>::BLOCKS) kv4_decode_k
           }
           if (!alone && g == 0) {
             part[S::ROWS * D + r] = m[nt][j] * c1[nt][j];
-            part[S::ROWS * (D + 1) + r] = sl;
+            part[S::ROWS * (D + 1) + r] = sl * norm;
           }
         }
     }

@@ -117,6 +117,20 @@ def test_small_weights_beside_a_large_one(dim, new, share, kv, nats, first):
     assert (err <= bound).all(), "worst %.3g times the bound" % (err / bound).max()
 
 
+@pytest.mark.parametrize("dim,new,share,kv", SHAPES)
+@pytest.mark.parametrize("kind", ["zeros", "constants", "offset"])
+def test_values_without_spread(dim, new, share, kv, kind):
+    """Value vectors of one number each (their step is 0), all zeros, and numbers that stand thousands of steps
+    from 0: held to the roundings of the weights and of the result."""
+    w = World([new], [kv], 2, dim, "f32", seed=kv)
+    shape = (kv, 2, 1 if kind == "constants" else dim)
+    v = {"zeros": np.zeros(shape), "constants": w.rng.normal(size=shape), "offset": 1000 + 0.01 * w.rng.normal(size=shape)}[kind]
+    w.v[0] = np.broadcast_to(v, (kv, 2, dim)).astype(np.float32)
+    w.fill()
+    q, out = attend(w, share)
+    assert bool(out.any()) == (kind != "zeros")
+
+
 @pytest.mark.parametrize("dim,new,share,kv", [(64, 1, 4, 200), (128, 1, 4, 200), (128, 1, 2, 5000), (128, 5, 4, 700), (64, 130, 2, 700), (128, 300, 1, 700)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("log2", [16, 22, 26, 30, 34, 40, 60, 100, 115, 120, 126])
