@@ -4,8 +4,8 @@
 // bytes and go to kv4_decode.cu, longer ones by the products and go to kv4_prompt.cu. The lengths are
 // on the device, so the host goes by the batch's bounds and launches the kernels that may be needed;
 // each takes its own sequences and leaves the others. Measured, us, few-row and prompt kernel, at 4000 cached
-// tokens a sequence: 16 x 16 rows of 5 heads x 128 28.8, 63.1; 16 x 32 rows 38.7, 64.3; 64 x 32 rows 106, 174;
-// 1 x 32 rows 15.1, 18.6; 64 x 24 rows of 8 heads x 64 116, 183.
+// tokens a sequence: 16 x 16 rows of 5 heads x 128 30.1, 63.4; 16 x 32 rows 39.8, 64.4; 64 x 32 rows 110, 175;
+// 1 x 32 rows 14.6, 18.6; 64 x 24 rows of 8 heads x 64 128, 184.
 #include "kv4.cuh"
 
 namespace bitnet {

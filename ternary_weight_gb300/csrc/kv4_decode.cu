@@ -30,15 +30,18 @@
 // that is cut leaves a partial (m, l, unscaled sum) for each run, and a second kernel joins them in
 // order, so results do not depend on timing. Short caches are not cut (see cuts()).
 //
-// Measured (20 and 5 heads x 128, one query a sequence): 8 x 65536 tokens 66.7 us (357 MB, 5.3 TB/s of the
-// measured 6.7), 1 x 131072 28.8 us, 64 of 87 to 8086 42.1 us (175 MB), 1 x 76 5.0 us. What is
-// added by more pages comes at 6.5 TB/s; about 11 us of a cut call is fixed: launch, the search for the
+// Measured (20 and 5 heads x 128, one query a sequence): 8 x 65536 tokens 68.2 us (357 MB, 5.2 TB/s of the
+// measured 6.7), 1 x 131072 29.9 us, 64 of 87 to 8086 43.2 us (175 MB), 1 x 76 5.5 us. What is
+// added by more pages comes at 6.5 TB/s; 13 to 16 us of a cut call are fixed: launch, the search for the
 // runs (3 loads, one after another), the first pages' way, the last partials, the join. With 12 to 28
-// rows (16 sequences of 1221 to 9955 tokens, 3 to 7 drafted ones each, 39.8 us) the products bind: two
+// rows (16 sequences of 1221 to 9955 tokens, 3 to 7 drafted ones each, 41.0 us) the products bind: two
 // units read the same pages, and registers leave two blocks an SM.
 // Tried and slower: 8 warps an SM for 12 (66 us for the 64 ragged ones against 51 at the time), e4m3 operands
 // of m16n8k32 (72.9 against 48.9), weights as two fp16 parts (83.7 against 74.3 for the drafted tokens), 32
-// rows in one unit (68 against 39.8).
+// rows in one unit (68 against 39.8). The scale of the weights costs 1 to 4%: the scale by the largest step met, which
+// loses weights to steps without weight, took 41.8 us for the 64 and 40.2 for the drafted tokens; up as a factor
+// of its own in place of the exponent 43.2 and 42.3; up moved by the exponents of the maxima alone, with an
+// exact pass where a step is large, 45.7 and 42.8.
 #include "kv4.cuh"
 #include "kv4_join.h"
 
@@ -882,16 +885,17 @@ int64_t runs_of(const Kv4& c, int rows, int resident) {
 }
 int64_t runs_bytes(const Kv4& c, int rows) { return (units_of(c, rows) * (int64_t)sizeof(int2) + 255) / 256 * 256; }
 // Warps that join a row: as many as its partials keep busy. Measured, us, with 16, 8 and 2 (20 and 5 heads x
-// 128): 1 x 131072 tokens (365 runs a unit) 28.8, 31.4, -; 16 x 4096 (23) 20.9, 21.1, 21.7; 8 x 65536 (46)
-// 66.6, 66.9, 69.7; 64 x 4096 (6) 45.4, 43.1, 42.0; 256 x 8192 (1) -, 236, 230.
+// 128): 1 x 131072 tokens (365 runs a unit) 29.9, 32.5, 48.6; 16 x 4096 (23) 22.0, 21.9, 22.1; 8 x 65536 (46)
+// 68.1, 68.3, 71.2; 64 x 4096 (6) 47.3, 44.2, 43.2; 256 x 8192 (1) 253, 240, 233.
 unsigned join_warps(const Kv4& c, int rows, int resident) {
   const int64_t runs = runs_of(c, rows, resident), units = units_of(c, rows);
   return runs > 64 * units ? JOIN_WARPS : runs > 8 * units ? 8 : 2;
 }
 // Whether units are cut. A block for each unit needs no search for the runs and no second kernel, but
 // lasts as long as the longest: measured, cut and uncut, us (20 and 5 heads x 128, one query a
-// sequence): 1 x 512 tokens 9.0, 6.4; 1 x 1024 9.3, 8.4; 1 x 4096 10.4, 23.3; 64 x 1024 21.4, 16.8;
-// 64 x 2048 29.2, 26.8; 64 x 4096 42.2, 45.5; 256 x 2048 78.4, 68.6. A window bounds the pages too (for
+// sequence): 1 x 512 tokens 9.7, 6.6; 1 x 1024 10.4, 9.4; 1 x 4096 10.9, 24.7; 64 x 1024 22.5, 17.4;
+// 64 x 2048 29.7, 27.2; 64 x 4096 43.2, 46.0; 256 x 2048 76.0, 70.0. (Heads of 64 go by the same rule; their
+// lengths were not swept.) A window bounds the pages too (for
 // the workspace, whose size does not depend on it, it is taken for none).
 bool cuts(const Kv4& c, int window, int sinks) {
   int64_t pages = most_pages(c);

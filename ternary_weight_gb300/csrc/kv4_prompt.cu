@@ -7,9 +7,9 @@
 //   S_t = Q_t K^T     128 x 128, K = D: both operands in shared memory (128-byte swizzle, K-major)
 //   P_t = 2^(c1 S - c1 m + 7)  in registers, written over S_t in tensor memory as fp16
 //   O_t += P_t V      128 x D, K = 128: P from tensor memory, V^T in shared memory
-// What bounds it: 4096 tokens (20 and 5 heads x 128) take 95.3 us, 902 TFLOP/s of the measured 1902, with the
-// tensor cores 44% busy and 2.7 of 4 issue slots used; 4 chunks with a window of 1024 (32 and 8 heads x 64)
-// 78.1 us, 371 TFLOP/s. A step of 2 x 128 x 128 scores takes 1.98 us (D = 128) or 1.53 us (D = 64): at D =
+// What bounds it: 4096 tokens (20 and 5 heads x 128) take 97.2 us, 884 TFLOP/s of the measured 1902, with the
+// tensor cores 43% busy and 2.6 of 4 issue slots used; 4 chunks with a window of 1024 (32 and 8 heads x 64)
+// 79.3 us, 365 TFLOP/s. A step of 2 x 128 x 128 scores takes 1.98 us (D = 128) or 1.53 us (D = 64): at D =
 // 128 the products need 1.1 us of it, the exponentials 0.53, issue slots 1.3; the rest is the chain scores ->
 // weights -> product -> scores of a tile, whose weights lie over its scores. A block has about 10 us besides
 // its steps: 1.1 until it starts, 1.3 the search for its item, 4 to 5 queries and first codes (all blocks

@@ -166,6 +166,8 @@ class AttentionBlock:
     sequences then have cached, and projects the result: prompts, single tokens and both together alike.
     Every call is asynchronous and reads the batch's lengths on the device, so a decode step can be
     captured once and replayed as the sequences grow (``python -m ternary_weight_gb300.generate`` does).
+    Nothing stands between the attention and the o projection: a layer that normalises there (the 2B-4T layer does)
+    makes the calls of ``run`` itself, with its norm before the last one.
     Each layer has a cache of its own; the layers of a model share the batch."""
 
     def __init__(self, q: PackedLinear, k: PackedLinear, v: PackedLinear, o: PackedLinear, cache: "binding.KV4Cache",
