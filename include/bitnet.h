@@ -481,10 +481,105 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache *cache, const bitnet_
                                     int64_t workspace_bytes, void *stream);
 
 /*
+ * Rotary positions -- what stands between the q/k projections and the cache ("bitnet.rs" "Forward Pass",
+ * RoPE on queries and keys). The first `dims` numbers of a head are pairs: (i, i + dims / 2) in the half
+ * layout, (2 i, 2 i + 1) in the interleaved one. Pair i of a row at position p is turned by p f_i and
+ * multiplied by the magnitude:
+ *   (a, b) -> magnitude (a cos - b sin, b cos + a sin)
+ * The head's other numbers stay. Negative positions turn back (which is also the gradient's turn).
+ */
+#define BITNET_ROPE_HALF 0
+#define BITNET_ROPE_INTERLEAVED 1
+
+/* Frequencies f_i = base^(-2 i / dims), scaled for contexts longer than those trained on: */
+#define BITNET_ROPE_NONE 0          /* f_i                                                               */
+#define BITNET_ROPE_LINEAR 1        /* f_i / factor                                                      */
+#define BITNET_ROPE_NTK 2           /* base * factor^(dims / (dims - 2)) in place of base (dims > 2)     */
+#define BITNET_ROPE_BY_PARTS 3      /* f_i (1 - r) + f_i / factor r, r = clamp((i - a) / max(b - a, 0.001), 0, 1),
+                                       a = max(floor(d(high)), 0), b = min(ceil(d(low)), dims - 1), d(n) =
+                                       dims / 2 ln(original / (2 pi n)) / ln(base); magnitude 0.1 ln(factor) + 1 */
+#define BITNET_ROPE_BY_WAVELENGTH 4 /* f_i (t + (1 - t) / factor),
+                                       t = clamp((original f_i / (2 pi) - low) / (high - low), 0, 1)     */
+
+/*
+ * bitnet_rope_turns -- the table of a model's frequencies, on the HOST (no device is touched): turns[i]
+ * is the part of a turn that one position adds to pair i, f_i / (2 pi) modulo 1, times 2^64 (computed in
+ * fp64). The caller copies it to the device.
+ *   dims     : even, 2 .. 1024
+ *   base     : finite, > 1
+ *   factor   : finite, >= 1 (ignored with BITNET_ROPE_NONE)
+ *   original, low, high : finite; original > 0 and 0 < low < high with BY_PARTS and BY_WAVELENGTH
+ *              (rotations over `original` positions; usual: 1 and 32, 1 and 4), else ignored
+ *   turns    : dims / 2 (HOST, written), magnitude: 1 (HOST, written; 1 but for BY_PARTS)
+ */
+BITNET_API int bitnet_rope_turns(int64_t dims, double base, int scaling, double factor, double original, double low,
+                                 double high, uint64_t *turns, float *magnitude);
+
+typedef struct bitnet_rope_table {
+  const uint64_t *turns; /* dims / 2 (device), 8-byte aligned                                     */
+  int32_t dims;          /* a multiple of 8, 8 .. head_dim                                        */
+  int32_t layout;        /* BITNET_ROPE_HALF or BITNET_ROPE_INTERLEAVED                           */
+  float magnitude;       /* finite                                                                */
+} bitnet_rope_table;
+
+/*
+ * bitnet_rope -- turn the queries and keys of a call's rows, in one launch.
+ *   positions : `rows` positions (device, read)
+ *   q, k      : rows of q_heads x head_dim and kv_heads x head_dim, fp32 or bf16 (dtype) (device,
+ *               read); row r begins at q + r * q_stride (elements), its heads lie one after another.
+ *               kv_heads may be 0 (k and k_out are then ignored)
+ *   q_out, k_out : the same, written. Each is either its input (the same pointer and stride) or memory
+ *               that overlaps neither input nor the other output
+ *   head_dim  : a multiple of 8, 8 .. 1024; rows 0 .. 2^31 - 1; q_heads 1 .. 2^17, kv_heads 0 .. 2^17
+ *   All 16-byte aligned (positions 4), strides >= heads * head_dim, at most 2^26, multiples of 16 bytes.
+ * Angles are exact to 2^-24 half turns at any position; the turn is computed in fp32 (each product and
+ * sum one rounding) and rounded once to dtype. Infinities and NaN spread to the pair that they are in.
+ */
+BITNET_API int bitnet_rope(const bitnet_rope_table *table, const int32_t *positions, int64_t rows, const void *q,
+                           int64_t q_heads, int64_t q_stride, void *q_out, int64_t q_out_stride, const void *k,
+                           int64_t kv_heads, int64_t k_stride, void *k_out, int64_t k_out_stride, int64_t head_dim,
+                           int dtype, void *stream);
+
+/*
+ * 4-bit weights with group scales -- for the matrices of a model that are not ternary, the output head
+ * above all ("bitnet.rs" "Forward Pass", logits). The format is this library's own. A row of K weights is
+ * K codes 0..15 (code k in byte k / 2, even k in bits 3:0) with an fp16 scale and a zero point for each
+ * `group` (32, 64 or 128) of consecutive ones:  w = scale (code - zero), zero = 8 where no zero points
+ * are given.
+ *   codes  : N x K / 2 bytes (device), scales: N x K / group fp16 (device), zeros: N x K / group
+ *            bytes 0..15 (device) or NULL; all 16-byte aligned
+ *   N 1 .. 2^31 - 1; K a positive multiple of 128, at most 32768
+ *
+ * bitnet_w4_quant_weight -- w (N x K fp32 or bf16 (dtype), 16-byte aligned) to codes, for each group with
+ * lo = min(0, min w), hi = max(0, max w):
+ *   without zeros: scale = fp16(max(hi, -lo) / 7), code = clamp(rne(w / scale) + 8, 0, 15)
+ *   with zeros:    scale = fp16((hi - lo) / 15), zero = clamp(rne(-lo / scale), 0, 15),
+ *                  code = clamp(rne(w / scale) + zero, 0, 15)
+ * (fp32 subtractions and divisions, each rounded once; where scale is 0 the codes are the zero point, 8 or
+ * 0). Weights that are not finite or whose scale is not record BITNET_ERANGE in the device error word;
+ * their group's codes are not valid.
+ */
+BITNET_API int bitnet_w4_quant_weight(const void *w, int dtype, int64_t N, int64_t K, int64_t group, uint8_t *codes,
+                                      uint16_t *scales, uint8_t *zeros, void *stream);
+
+/*
+ * bitnet_w4_matmul -- out = x w^T: M x K rows x (fp32 or bf16 (dtype), 16-byte aligned, device) times 4-bit
+ * weights, M x N fp32 (device, written). M 1 .. 2^31 - 1; made for a few rows (the tokens of a decode step): more
+ * are taken in runs of at most 64 (fp32: 32), fewer where K is large, each of which reads the weights.
+ *   A row is used as fp16 at a power-of-two scale of its own: bf16 numbers keep their bits (those below
+ *   2^-31 of the row's largest may not), fp32 numbers enter as two such parts, 22 bits. Products
+ *   and sums are fp32. A row with an infinity or a NaN gives no finite number that is valid.
+ * The results of a call are the same bits each time it is made with the same arguments.
+ */
+BITNET_API int bitnet_w4_matmul(const void *x, int dtype, int64_t M, int64_t K, const uint8_t *codes,
+                                const uint16_t *scales, const uint8_t *zeros, int64_t N, int64_t group, float *out,
+                                void *stream);
+
+/*
  * bitnet_last_device_error -- read and clear the device-side error word of the current
  * device. Kernels that wait on an mbarrier give up after a bounded number of polls and
- * record BITNET_ETIMEOUT there instead of hanging; bitnet_quant_weight records BITNET_ERANGE
- * for weights outside its range, the bitnet_kv4 calls for batches that break their bounds.
+ * record BITNET_ETIMEOUT there instead of hanging; bitnet_quant_weight and
+ * bitnet_w4_quant_weight record BITNET_ERANGE for weights outside their range, the bitnet_kv4 calls for batches that break their bounds.
  * Synchronises the device.
  * Returns BITNET_OK, BITNET_ETIMEOUT, BITNET_ERANGE or BITNET_ECUDA.
  */

@@ -62,6 +62,13 @@ SIGNATURES = {
     "bitnet_kv4_attention_workspace_size": ([_P, _P, _I64], _I64),
     "bitnet_kv4_attention": (
         [_P, _P, _P, ctypes.c_int, _I64, _I64, ctypes.c_float, _I64, _I64, _P, _I64, _P, _I64, _P], ctypes.c_int),
+    "bitnet_rope_turns": (
+        [_I64, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, _P, _P],
+        ctypes.c_int),
+    "bitnet_rope": (
+        [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, ctypes.c_int, _P], ctypes.c_int),
+    "bitnet_w4_quant_weight": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P, _P], ctypes.c_int),
+    "bitnet_w4_matmul": ([_P, ctypes.c_int, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P], ctypes.c_int),
     "bitnet_w2a8_ffn": (
         [_P, ctypes.c_int, _I64, _I64, _I64, _P, ctypes.c_float, _P, ctypes.c_float, _P, ctypes.c_float, _P,
          ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _I64, _P], ctypes.c_int),
@@ -638,4 +645,144 @@ def kv4_attention(cache, batch, q, scale, window=0, sinks=0, out=None, workspace
                                         out.data_ptr(), os_, ws_ptr, ws_bytes, on)
         if st:
             raise BitnetError(st, "bitnet_kv4_attention")
+    return out
+
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "by_wavelength": 4}
+_ROPE_ENDS = {"by_parts": (1.0, 32.0), "by_wavelength": (1.0, 4.0)}
+
+
+class _RopeDesc(ctypes.Structure):
+    """ctypes mirror of bitnet_rope_table (include/bitnet.h)."""
+    _fields_ = [("turns", ctypes.c_void_p), ("dims", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
+
+def rope_turns(dims, base=10000.0, scaling="none", factor=1.0, original=0, low=None, high=None):
+    """The frequencies of rotary positions as 64-bit fractions of a turn a position (a list of dims / 2
+    integers), and the magnitude. ``scaling``: "none", "linear", "ntk", "by_parts" or "by_wavelength", by
+    ``factor``; the last two also take the ``original`` context length and the rotations over it, ``low``
+    and ``high``, between which they pass over (1 and 32, 1 and 4 if not given)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    ends = _ROPE_ENDS.get(scaling, (0.0, 0.0))
+    turns, magnitude = (ctypes.c_uint64 * max(1, int(dims) // 2))(), ctypes.c_float()
+    _check(lib().bitnet_rope_turns(int(dims), float(base), ROPE_SCALINGS[scaling], float(factor), float(original),
+                                   float(ends[0] if low is None else low), float(ends[1] if high is None else high),
+                                   ctypes.cast(turns, ctypes.c_void_p), ctypes.byref(magnitude)), "bitnet_rope_turns")
+    return list(turns), magnitude.value
+
+
+class Rope:
+    """A model's rotary positions: the frequencies (see ``rope_turns``) on the device, and the layout of
+    the pairs, "half" or "interleaved". ``dims`` (a multiple of 8) is the part of each head that is turned."""
+
+    def __init__(self, dims, base=10000.0, layout="half", scaling="none", factor=1.0, original=0, low=None, high=None,
+                 device="cuda"):
+        import torch
+
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError("layout must be one of %s" % ", ".join(ROPE_LAYOUTS))
+        if dims < 8 or dims % 8:
+            raise ValueError("dims must be a multiple of 8")
+        turns, self.magnitude = rope_turns(dims, base, scaling, factor, original, low, high)
+        self.turns = torch.tensor(turns, dtype=torch.int64, device=device)  # all below 2^62
+        self.dims, self.layout, self.index = dims, layout, self.turns.get_device()
+        self._desc = _RopeDesc(self.turns.data_ptr(), dims, ROPE_LAYOUTS[layout], self.magnitude)
+        self._ref = ctypes.c_void_p(ctypes.addressof(self._desc))
+
+
+def _rope_rows(t, out, rows, dim, index, torch, stream):
+    """An operand's checks: its heads and strides, and its output (allocated if not given)."""
+    heads = t.shape[1]
+    ins = _kv4_rows(t, rows, heads, dim, index)
+    if out is None:
+        return heads, ins, _kv4_empty(torch, (rows, heads, dim), t.dtype, t.device, stream), heads * dim
+    if out.dtype != t.dtype:
+        raise ValueError("an output must have its input's dtype")
+    return heads, ins, out, _kv4_rows(out, rows, heads, dim, index)
+
+
+def rope(table, positions, q, k=None, q_out=None, k_out=None, stream=None):
+    """Turn queries (rows x q_heads x head_dim, fp32 or bf16 CUDA, rows may be strided) and, if given,
+    keys (rows x kv_heads x head_dim) by the positions (rows, int32) of their rows, in one launch. Returns
+    the turned q, or (q, k): new tensors, or ``q_out`` and ``k_out``, which may be the inputs themselves."""
+    import torch
+
+    dt = BITNET_F32 if q.dtype == torch.float32 else BITNET_BF16 if q.dtype == torch.bfloat16 else None
+    if dt is None or (k is not None and k.dtype != q.dtype):
+        raise ValueError("q and k must both be float32 or bfloat16")
+    if q.dim() != 3 or (k is not None and k.dim() != 3) or (k is None and k_out is not None):
+        raise ValueError("q and k must be rows x heads x head_dim")
+    rows, dim, index = q.shape[0], q.shape[2], table.index
+    if positions.dtype != torch.int32 or positions.shape != (rows,) or positions.get_device() != index or \
+            not positions.is_contiguous():
+        raise ValueError("positions must be an int32 for each row, contiguous, on the table's device")
+    if torch.cuda.current_device() != index:
+        raise ValueError("the table's device must be the current one")
+    qh, qs, q_out, qos = _rope_rows(q, q_out, rows, dim, index, torch, stream)
+    kh = ks = kos = 0
+    if k is not None:
+        kh, ks, k_out, kos = _rope_rows(k, k_out, rows, dim, index, torch, stream)
+    if rows:
+        _check(lib().bitnet_rope(table._ref, positions.data_ptr(), rows, q.data_ptr(), qh, qs, q_out.data_ptr(), qos,
+                                 _ptr(k), kh, ks, _ptr(k_out), kos, dim, dt, _stream(stream)), "bitnet_rope")
+    return q_out if k is None else (q_out, k_out)
+
+
+def w4_quant_weight(w, group=128, with_zeros=False, codes=None, scales=None, zeros=None, stream=None):
+    """fp32 or bf16 weights (N x K, CUDA) to 4 bits with an fp16 scale, and with ``with_zeros`` a zero point, for
+    each ``group`` (32, 64 or 128) along K. Returns (codes uint8 N x K/2, scales fp16 N x K/group, zeros
+    uint8 N x K/group or None)."""
+    import torch
+
+    dt = _act_dtype(w)
+    N, K = w.shape
+    if group not in (32, 64, 128) or K % 128:
+        raise ValueError("group must be 32, 64 or 128, and K a multiple of 128")
+    with_zeros = with_zeros or zeros is not None
+    groups = (N, K // group)
+    codes = _kv4_empty(torch, (N, K // 2), torch.uint8, w.device, stream) if codes is None else codes
+    scales = _kv4_empty(torch, groups, torch.float16, w.device, stream) if scales is None else scales
+    if with_zeros and zeros is None:
+        zeros = _kv4_empty(torch, groups, torch.uint8, w.device, stream)
+    _w4_check(torch, w, codes, scales, zeros, None)
+    _check(lib().bitnet_w4_quant_weight(_ptr(w), dt, N, K, group, _ptr(codes), _ptr(scales), _ptr(zeros), _stream(stream)),
+           "bitnet_w4_quant_weight")
+    return codes, scales, zeros
+
+
+def _w4_check(torch, x, codes, scales, zeros, out):
+    """Checks of what both calls have; the group."""
+    N, K = codes.shape[0], codes.shape[1] * 2
+    if codes.dtype != torch.uint8 or scales.dtype != torch.float16 or scales.dim() != 2 or scales.shape[0] != N or \
+            scales.shape[1] == 0 or K % scales.shape[1]:
+        raise ValueError("codes must be N x K/2 uint8 and scales N x K/group float16")
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
+        raise ValueError("zeros must be uint8 of the scales' shape")
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError("expected rows of %d numbers" % K)
+    if out is not None and (out.dtype != torch.float32 or out.shape != (x.shape[0], N)):
+        raise ValueError("out must be M x N float32")
+    _require_cuda(x, codes, scales, zeros, out)
+    index = x.get_device()
+    if any(t is not None and t.get_device() != index for t in (codes, scales, zeros, out)):
+        raise ValueError("tensors must be on one device")
+    if torch.cuda.current_device() != index:
+        raise ValueError("the tensors' device must be the current one")
+    return K // scales.shape[1]
+
+
+def w4_matmul(x, codes, scales, zeros=None, out=None, stream=None):
+    """x (M x K fp32 or bf16 CUDA) times 4-bit weights with group scales (see ``w4_quant_weight``): M x N fp32."""
+    import torch
+
+    dt = _act_dtype(x)
+    group = _w4_check(torch, x, codes, scales, zeros, out)
+    M, N = x.shape[0], codes.shape[0]
+    out = _kv4_empty(torch, (M, N), torch.float32, x.device, stream) if out is None else out
+    if M:
+        _check(lib().bitnet_w4_matmul(_ptr(x), dt, M, x.shape[1], _ptr(codes), _ptr(scales), _ptr(zeros), N, group,
+                                      _ptr(out), _stream(stream)), "bitnet_w4_matmul")
     return out

@@ -10,6 +10,8 @@
 #include "bitnet_dev.cuh"
 #include "gemm_pair.h"
 #include "kv4.cuh"
+#include "rope.h"
+#include "w4.h"
 
 #include <cmath>
 #include <new>
@@ -562,6 +564,117 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache* cache, const bitnet_
                                         static_cast<cudaStream_t>(stream)));
 }
 
+// ---- rotary positions ----
+namespace {
+constexpr int64_t kRopeMaxDim = 1024, kRopeMaxHeads = 1 << 17;
+constexpr double kTwoPi = 6.283185307179586476925;
+
+// one operand's checks; `out` is its input or apart from it
+int check_rope_rows(const void* in, int64_t in_stride, const void* out, int64_t out_stride, int64_t least, int64_t eb) {
+  if (!in || !out) return BITNET_EINVAL;
+  if (int st = check_stride(in_stride, least, eb)) return st;
+  if (int st = check_stride(out_stride, least, eb)) return st;
+  if (in == out && in_stride != out_stride) return BITNET_EINVAL;
+  return aligned(in, 16) && aligned(out, 16) ? BITNET_OK : BITNET_EALIGN;
+}
+}  // namespace
+
+BITNET_API int bitnet_rope_turns(int64_t dims, double base, int scaling, double factor, double original, double low,
+                                 double high, uint64_t* turns, float* magnitude) {
+  if (!turns || !magnitude || dims < 2 || dims > kRopeMaxDim || dims % 2) return BITNET_EINVAL;
+  if (scaling < BITNET_ROPE_NONE || scaling > BITNET_ROPE_BY_WAVELENGTH) return BITNET_EINVAL;
+  if (!std::isfinite(base) || !(base > 1.0)) return BITNET_EINVAL;
+  if (scaling != BITNET_ROPE_NONE && (!std::isfinite(factor) || !(factor >= 1.0))) return BITNET_EINVAL;
+  const bool ends = scaling == BITNET_ROPE_BY_PARTS || scaling == BITNET_ROPE_BY_WAVELENGTH;
+  if (ends && (!std::isfinite(original) || !std::isfinite(low) || !std::isfinite(high) || !(original > 0.0) ||
+               !(low > 0.0) || !(high > low)))
+    return BITNET_EINVAL;
+  if (scaling == BITNET_ROPE_NTK) {
+    if (dims == 2) return BITNET_EINVAL;
+    base *= std::pow(factor, (double)dims / (double)(dims - 2));
+    if (!std::isfinite(base)) return BITNET_EINVAL;
+  }
+  const auto at = [&](double n) { return dims / 2 * std::log(original / (kTwoPi * n)) / std::log(base); };
+  double a = 0.0, b = 0.0;
+  if (scaling == BITNET_ROPE_BY_PARTS) {
+    a = std::fmax(std::floor(at(high)), 0.0);
+    b = std::fmin(std::ceil(at(low)), (double)(dims - 1));
+  }
+  for (int64_t i = 0; i < dims / 2; ++i) {
+    double f = std::pow(base, -2.0 * (double)i / (double)dims);
+    if (scaling == BITNET_ROPE_LINEAR) f /= factor;
+    if (scaling == BITNET_ROPE_BY_PARTS) {
+      const double r = std::fmin(std::fmax(((double)i - a) / std::fmax(b - a, 0.001), 0.0), 1.0);
+      f = f * (1.0 - r) + f / factor * r;
+    }
+    if (scaling == BITNET_ROPE_BY_WAVELENGTH) {
+      const double t = std::fmin(std::fmax((original * f / kTwoPi - low) / (high - low), 0.0), 1.0);
+      f *= t + (1.0 - t) / factor;
+    }
+    // f <= 1: less than a turn, and the product below 2^62
+    turns[i] = (uint64_t)std::llrint(f / kTwoPi * 18446744073709551616.0);
+  }
+  *magnitude = scaling == BITNET_ROPE_BY_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return BITNET_OK;
+}
+
+BITNET_API int bitnet_rope(const bitnet_rope_table* table, const int32_t* positions, int64_t rows, const void* q,
+                           int64_t q_heads, int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                           int64_t kv_heads, int64_t k_stride, void* k_out, int64_t k_out_stride, int64_t head_dim,
+                           int dtype, void* stream) {
+  if (!table || !table->turns || !positions || rows < 0 || rows > INT32_MAX) return BITNET_EINVAL;
+  if (dtype != BITNET_F32 && dtype != BITNET_BF16) return BITNET_EINVAL;
+  if (head_dim < 8 || head_dim > kRopeMaxDim || head_dim % 8) return BITNET_EINVAL;
+  if (table->dims < 8 || table->dims > head_dim || table->dims % 8 || !std::isfinite(table->magnitude))
+    return BITNET_EINVAL;
+  if (table->layout != BITNET_ROPE_HALF && table->layout != BITNET_ROPE_INTERLEAVED) return BITNET_EINVAL;
+  if (q_heads < 1 || q_heads > kRopeMaxHeads || kv_heads < 0 || kv_heads > kRopeMaxHeads) return BITNET_EINVAL;
+  const int64_t eb = dtype == BITNET_BF16 ? 2 : 4;
+  if (int st = check_rope_rows(q, q_stride, q_out, q_out_stride, q_heads * head_dim, eb)) return st;
+  if (kv_heads)
+    if (int st = check_rope_rows(k, k_stride, k_out, k_out_stride, kv_heads * head_dim, eb)) return st;
+  if (!aligned(table->turns, 8) || !aligned(positions, 4)) return BITNET_EALIGN;
+  if (rows == 0) return BITNET_OK;
+  int sms = 0;
+  if (int st = check_device(&sms)) return st;
+  const Rope r{table->turns, positions, {q, q_out, q_stride, q_out_stride, (int)q_heads},
+               {k, k_out, k_stride, k_out_stride, (int)kv_heads}, rows, (int)head_dim, table->dims, table->magnitude,
+               table->layout == BITNET_ROPE_INTERLEAVED};
+  return status_of(launch_rope(r, dtype == BITNET_BF16, sms, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- 4-bit weights ----
+namespace {
+int check_w4(const void* rows, int dtype, int64_t N, int64_t K, int64_t group, const uint8_t* codes,
+             const uint16_t* scales, const uint8_t* zeros) {
+  if (!rows || !codes || !scales || (dtype != BITNET_F32 && dtype != BITNET_BF16)) return BITNET_EINVAL;
+  if (N < 1 || N > INT32_MAX || !valid_k(K) || K > kW4MaxK) return BITNET_EINVAL;
+  if (group != 32 && group != 64 && group != 128) return BITNET_EINVAL;
+  return aligned(rows, 16) && aligned(codes, 16) && aligned(scales, 16) && aligned(zeros, 16) ? BITNET_OK : BITNET_EALIGN;
+}
+}  // namespace
+
+BITNET_API int bitnet_w4_quant_weight(const void* w, int dtype, int64_t N, int64_t K, int64_t group, uint8_t* codes,
+                                      uint16_t* scales, uint8_t* zeros, void* stream) {
+  if (int st = check_w4(w, dtype, N, K, group, codes, scales, zeros)) return st;
+  int sms = 0;
+  if (int st = check_device(&sms)) return st;
+  return status_of(launch_w4_quant(w, dtype == BITNET_BF16, N, K, (int)group, codes, scales, zeros,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+BITNET_API int bitnet_w4_matmul(const void* x, int dtype, int64_t M, int64_t K, const uint8_t* codes,
+                                const uint16_t* scales, const uint8_t* zeros, int64_t N, int64_t group, float* out,
+                                void* stream) {
+  if (!out || M < 1 || M > INT32_MAX) return BITNET_EINVAL;
+  if (int st = check_w4(x, dtype, N, K, group, codes, scales, zeros)) return st;
+  if (!aligned(out, 4)) return BITNET_EALIGN;
+  int sms = 0;
+  if (int st = check_device(&sms)) return st;
+  const W4 w4{codes, scales, zeros, (int)N, (int)K, (int)group};
+  return status_of(launch_w4_matmul(w4, x, dtype == BITNET_BF16, M, out, sms, static_cast<cudaStream_t>(stream)));
+}
+
 BITNET_API int bitnet_selftest_wait_timeout(const void* src, int64_t bytes, int32_t max_polls, uint32_t* report,
                                             void* stream) {
   if (!src || !report || !selftest_bytes_ok(bytes) || max_polls < 1 || max_polls > (1 << 20)) return BITNET_EINVAL;
@@ -583,7 +696,7 @@ BITNET_API int bitnet_last_device_error(void) {
                                     read_clear_device_error_gemv_ring, read_clear_device_error_selftest,
                                     read_clear_device_error_prefill, read_clear_device_error_pair,
                                     read_clear_device_error_kv4_cache, read_clear_device_error_kv4_decode,
-                                    read_clear_device_error_kv4_prompt};
+                                    read_clear_device_error_kv4_prompt, read_clear_device_error_w4_quant};
   for (auto rd : readers) {
     int v = 0;
     if (rd(&v) != cudaSuccess) return BITNET_ECUDA;
