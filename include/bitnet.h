@@ -481,6 +481,62 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache *cache, const bitnet_
                                     int64_t workspace_bytes, void *stream);
 
 /*
+ * The attention weight that cached tokens gather, and eviction by it -- for contexts longer than the
+ * memory. Beside a cache lies one fp32 number for each page, key/value head and place ("mass"):
+ * n_pages x kv_heads x 64 floats (device), the token in place t of its page in entry t.
+ *
+ * bitnet_kv4_attention_mass -- add up the softmax weights that the batch's queries give to the cached tokens.
+ *   Of each sequence's new tokens the last `voters` vote (0: all). A query at position p with the scores
+ *   scale * q . k_j over the positions it sees (as bitnet_kv4_attention says) gives position j the weight
+ *   softmax_j; the weights of all voting rows and of the query heads that share a key/value head are added up:
+ *     older than the call (j < kv_len - n):  mass_out = decay * mass + votes
+ *     the call's own tokens:                 mass_out = votes (whatever the page held before)
+ *   Only the places of the cached tokens of sequences with new tokens are written. A query that sees nothing votes
+ *   for nothing. Keys enter as codes with fp32 steps and bases; bf16 queries keep their bits (those below 2^-28 of
+ *   the row's largest may not), fp32 ones enter as two fp16 parts (22 bits); scores, maxima and sums are fp32. A NaN
+ *   or an infinity in a query or key makes the votes of the rows that meet it NaN.
+ *   mass, mass_out : the same array, or two that do not overlap; 16-byte aligned
+ *   decay  : finite; voters 0 .. 2^31 - 1
+ *   q, dtype, q_heads, q_stride, scale, window, sinks : as in bitnet_kv4_attention
+ *   workspace : device, 256-byte aligned, at least bitnet_kv4_attention_mass_workspace_size bytes (for the same
+ *            cache, batch sizes, q_heads and voters). Needs no initialisation; calls that may run at the same
+ *            time need one each.
+ * Pages that two sequences of the batch share gather the votes of one of them. The results of a call are the same
+ * bits each time it is made with the same arguments.
+ *
+ * bitnet_kv4_evict -- sequences of more than `limit` cached tokens keep `budget` of them in each key/value
+ *   head: the first `sinks`, the last `recent`, and of the others those of the greatest mass (a NaN is
+ *   above all; of equal ones the earlier), in their order. They become the tokens 0 .. budget - 1: codes and
+ *   parameters as they are, with their mass. Shorter sequences keep all their tokens.
+ *   batch  : kv_len, page_table, batch, max_pages and max_kv; cu_q, total_q and max_q are not used (cu_q not read)
+ *   into   : batch x into_pages page ids (device): the kept tokens, also those of shorter sequences, are written there.
+ *            No page may be a page of the sequences' own, nor stand there twice. 64 * into_pages >= budget; a shorter
+ *            sequence that does not fit there is not moved, and BITNET_ERANGE is recorded.
+ *            NULL: in place, to the sequence's first pages (then no two sequences may share pages)
+ *   new_len: batch (device, written) or NULL: the tokens that each sequence keeps. It may be the batch's kv_len
+ *            itself; the layers of a model that share it pass NULL but for the last
+ *   1 <= budget <= limit < 2^31, sinks >= 0, recent >= 0, sinks + recent <= budget
+ *   mass   : 16-byte aligned; into, new_len 4
+ *   workspace : device, 256-byte aligned, at least bitnet_kv4_evict_workspace_size bytes
+ * A kv_len outside 0 .. max_kv or a page id outside the pool records BITNET_ERANGE; nothing outside the arrays is read
+ * or written, such a sequence's results are not valid (a bad kv_len is kept). Positions of a window count slots:
+ * they are those of the kept tokens afterwards.
+ */
+BITNET_API int64_t bitnet_kv4_mass_bytes(int64_t n_pages, int64_t kv_heads);
+BITNET_API int64_t bitnet_kv4_attention_mass_workspace_size(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch,
+                                                            int64_t q_heads, int64_t voters);
+BITNET_API int bitnet_kv4_attention_mass(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch, const void *q,
+                                         int dtype, int64_t q_heads, int64_t q_stride, float scale, int64_t window,
+                                         int64_t sinks, int64_t voters, float decay, const float *mass,
+                                         float *mass_out, void *workspace, int64_t workspace_bytes, void *stream);
+BITNET_API int64_t bitnet_kv4_evict_workspace_size(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch,
+                                                   int64_t budget);
+BITNET_API int bitnet_kv4_evict(const bitnet_kv4_cache *cache, const bitnet_kv4_batch *batch, float *mass,
+                                int64_t budget, int64_t limit, int64_t sinks, int64_t recent, const int32_t *into,
+                                int64_t into_pages, int32_t *new_len, void *workspace, int64_t workspace_bytes,
+                                void *stream);
+
+/*
  * Rotary positions -- what stands between the q/k projections and the cache ("bitnet.rs" "Forward Pass",
  * RoPE on queries and keys). The first `dims` numbers of a head are pairs: (i, i + dims / 2) in the half
  * layout, (2 i, 2 i + 1) in the interleaved one. Pair i of a row at position p is turned by p f_i and

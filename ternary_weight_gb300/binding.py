@@ -62,6 +62,13 @@ SIGNATURES = {
     "bitnet_kv4_attention_workspace_size": ([_P, _P, _I64], _I64),
     "bitnet_kv4_attention": (
         [_P, _P, _P, ctypes.c_int, _I64, _I64, ctypes.c_float, _I64, _I64, _P, _I64, _P, _I64, _P], ctypes.c_int),
+    "bitnet_kv4_mass_bytes": ([_I64, _I64], _I64),
+    "bitnet_kv4_attention_mass_workspace_size": ([_P, _P, _I64, _I64], _I64),
+    "bitnet_kv4_attention_mass": (
+        [_P, _P, _P, ctypes.c_int, _I64, _I64, ctypes.c_float, _I64, _I64, _I64, ctypes.c_float, _P, _P, _P, _I64, _P],
+        ctypes.c_int),
+    "bitnet_kv4_evict_workspace_size": ([_P, _P, _I64], _I64),
+    "bitnet_kv4_evict": ([_P, _P, _P, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P], ctypes.c_int),
     "bitnet_rope_turns": (
         [_I64, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, _P, _P],
         ctypes.c_int),
@@ -646,6 +653,105 @@ def kv4_attention(cache, batch, q, scale, window=0, sinks=0, out=None, workspace
         if st:
             raise BitnetError(st, "bitnet_kv4_attention")
     return out
+
+
+def kv4_mass(cache):
+    """Room for the attention weight that a cache's tokens gather: fp32, n_pages x kv_heads x 64, zeros."""
+    import torch
+
+    return torch.zeros((cache.n_pages, cache.kv_heads, KV4_PAGE), dtype=torch.float32, device=cache.device)
+
+
+def _kv4_mass_rows(cache, mass):
+    if mass.shape != (cache.n_pages, cache.kv_heads, KV4_PAGE) or str(mass.dtype) != "torch.float32":
+        raise ValueError("mass must be n_pages x kv_heads x %d float32" % KV4_PAGE)
+    if mass.get_device() != cache.index or not mass.is_contiguous():
+        raise ValueError("mass must be contiguous, on the cache's device")
+
+
+def _kv4_workspace(torch, cache, workspace, need, stream):
+    """A call's workspace: the given one (checked), or one allocated for the call's stream. (tensor, pointer, bytes)"""
+    if workspace is None:
+        workspace = _kv4_empty(torch, need, torch.uint8, cache.device, stream) if need else None
+        return workspace, workspace.data_ptr() if need else None, need
+    _require_cuda(workspace)
+    if workspace.get_device() != cache.index:
+        raise ValueError("the workspace must be on the cache's device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def kv4_attention_mass_workspace_size(cache, batch, q_heads, voters=0) -> int:
+    n = lib().bitnet_kv4_attention_mass_workspace_size(cache._ref, batch._ref, q_heads, voters)
+    if n < 0:
+        raise BitnetError(int(n), "bitnet_kv4_attention_mass_workspace_size")
+    return int(n)
+
+
+def kv4_attention_mass(cache, batch, q, scale, mass, decay=1.0, window=0, sinks=0, voters=0, out=None, workspace=None,
+                       stream=None):
+    """Add the softmax weights of the batch's queries (as in ``kv4_attention``) to the mass of the cached
+    tokens that they see: decay * mass + votes for tokens older than the call, the votes alone for the call's
+    own. The last ``voters`` rows of each sequence vote (0: all). ``mass`` (see ``kv4_mass``) is updated in
+    place, or ``out`` (which keeps what the call does not write) is; returns it. ``workspace``: a uint8 CUDA
+    tensor of at least kv4_attention_mass_workspace_size bytes, allocated here if not given."""
+    torch, dtypes, _, handle = _kv4_torch or _kv4_setup()
+    dt = dtypes.get(q.dtype)
+    if dt is None or q.dim() != 3:
+        raise ValueError("q must be total_q x q_heads x head_dim, float32 or bfloat16")
+    rows, heads = batch.total_q, q.shape[1]
+    qs = _kv4_rows(q, rows, heads, cache.head_dim, cache.index)
+    on = handle(cache, batch, stream)
+    _kv4_mass_rows(cache, mass)
+    if out is None:
+        out = mass
+    else:
+        _kv4_mass_rows(cache, out)
+    key = (heads, cache.kv_heads, cache.head_dim, voters)
+    need = batch._ws.get(key)
+    if need is None:
+        need = batch._ws[key] = kv4_attention_mass_workspace_size(cache, batch, heads, voters)
+    if rows:
+        keep, ws, ws_bytes = _kv4_workspace(torch, cache, workspace, need, stream)
+        st = lib().bitnet_kv4_attention_mass(cache._ref, batch._ref, q.data_ptr(), dt, heads, qs, scale, window, sinks, voters,
+                                             decay, mass.data_ptr(), out.data_ptr(), ws, ws_bytes, on)
+        if st:
+            raise BitnetError(st, "bitnet_kv4_attention_mass")
+    return out
+
+
+def kv4_evict_workspace_size(cache, batch, budget) -> int:
+    n = lib().bitnet_kv4_evict_workspace_size(cache._ref, batch._ref, budget)
+    if n < 0:
+        raise BitnetError(int(n), "bitnet_kv4_evict_workspace_size")
+    return int(n)
+
+
+def kv4_evict(cache, batch, mass, budget, limit=None, sinks=0, recent=0, into=None, new_len=None, workspace=None,
+              stream=None):
+    """Cut the batch's sequences of more than ``limit`` cached tokens (default: budget) to ``budget`` in each
+    head: the first ``sinks``, the last ``recent``, and the others of the greatest mass. In place, or into the
+    pages of the table ``into`` (int32, batch x pages; then all kept tokens are written there, also those of shorter
+    sequences). Returns the new lengths, int32: a new tensor, or ``new_len``, which may be the batch's
+    kv_len itself. The batch's cu_q and sizes of new tokens are not used."""
+    torch, _, _, handle = _kv4_torch or _kv4_setup()
+    limit = budget if limit is None else limit
+    n = batch.kv_len.numel()
+    on = handle(cache, batch, stream)
+    _kv4_mass_rows(cache, mass)
+    for t, shape in ((into, (n, into.shape[-1]) if into is not None else None), (new_len, (n,))):
+        if t is not None and (t.dtype != torch.int32 or t.shape != shape or t.get_device() != cache.index or
+                              not t.is_contiguous()):
+            raise ValueError("into (batch x pages) and new_len (batch) must be contiguous int32 on the cache's device")
+    if new_len is None:
+        new_len = _kv4_empty(torch, (n,), torch.int32, cache.device, stream)
+    need = kv4_evict_workspace_size(cache, batch, budget)
+    keep, ws, ws_bytes = _kv4_workspace(torch, cache, workspace, need, stream)
+    st = lib().bitnet_kv4_evict(cache._ref, batch._ref, mass.data_ptr(), budget, limit, sinks, recent,
+                                into.data_ptr() if into is not None else None, into.shape[1] if into is not None else 0,
+                                new_len.data_ptr(), ws, ws_bytes, on)
+    if st:
+        raise BitnetError(st, "bitnet_kv4_evict")
+    return new_len
 
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}

@@ -564,6 +564,81 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache* cache, const bitnet_
                                         static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+// what attention and the weights that it gathers have in common; fills *out
+int check_kv4_queries(const Kv4& c, int dim, const void* q, int dtype, int64_t q_heads, int64_t q_stride, float scale,
+                      int64_t window, int64_t sinks, Kv4Attn* out) {
+  if (!q || (dtype != BITNET_F32 && dtype != BITNET_BF16)) return BITNET_EINVAL;
+  if (!valid_q_heads(q_heads, c.kv_heads) || !std::isfinite(scale)) return BITNET_EINVAL;
+  if (window < 0 || window > INT32_MAX || sinks < 0 || sinks > INT32_MAX) return BITNET_EINVAL;
+  if (int st = check_stride(q_stride, q_heads * dim, dtype == BITNET_BF16 ? 2 : 4)) return st;
+  if (!valid_q_rows(c, q_heads)) return BITNET_EINVAL;
+  *out = Kv4Attn{q, nullptr, q_stride, 0, (int)q_heads, (int)(q_heads / c.kv_heads), scale,
+                 window ? (int)window : INT32_MAX, window ? (int)sinks : 0, dtype == BITNET_BF16};
+  return aligned(q, 16) ? BITNET_OK : BITNET_EALIGN;
+}
+int voters_of(int64_t voters) { return voters ? (int)voters : INT32_MAX; }
+}  // namespace
+
+BITNET_API int64_t bitnet_kv4_mass_bytes(int64_t n_pages, int64_t kv_heads) {
+  if (!valid_kv4_sizes(n_pages, kv_heads, 64)) return BITNET_EINVAL;
+  return n_pages * kv_heads * kKvPage * 4;
+}
+
+BITNET_API int64_t bitnet_kv4_attention_mass_workspace_size(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* batch,
+                                                            int64_t q_heads, int64_t voters) {
+  Kv4 c{};
+  if (int st = check_kv4(cache, batch, &c)) return st;
+  if (!valid_q_heads(q_heads, c.kv_heads) || !valid_q_rows(c, q_heads)) return BITNET_EINVAL;
+  if (voters < 0 || voters > INT32_MAX) return BITNET_EINVAL;
+  return kv4_mass_ws_bytes(c, cache->head_dim, (int)q_heads, voters_of(voters));
+}
+
+BITNET_API int bitnet_kv4_attention_mass(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* batch, const void* q,
+                                         int dtype, int64_t q_heads, int64_t q_stride, float scale, int64_t window,
+                                         int64_t sinks, int64_t voters, float decay, const float* mass,
+                                         float* mass_out, void* workspace, int64_t workspace_bytes, void* stream) {
+  Kv4 c{};
+  Kv4Attn a{};
+  if (int st = check_kv4(cache, batch, &c)) return st;
+  if (!mass || !mass_out || !std::isfinite(decay) || voters < 0 || voters > INT32_MAX) return BITNET_EINVAL;
+  if (int st = check_kv4_queries(c, cache->head_dim, q, dtype, q_heads, q_stride, scale, window, sinks, &a)) return st;
+  const int64_t need = kv4_mass_ws_bytes(c, cache->head_dim, (int)q_heads, voters_of(voters));
+  if (need > 0 && (!workspace || workspace_bytes < need)) return BITNET_EINVAL;
+  if (!aligned(mass, 16) || !aligned(mass_out, 16) || (workspace && !aligned(workspace, 256))) return BITNET_EALIGN;
+  if (c.total_q == 0) return BITNET_OK;
+  int sms = 0;
+  if (int st = check_device(&sms)) return st;
+  return status_of(launch_kv4_mass(c, cache->head_dim, a, Kv4Mass{mass, mass_out, decay, voters_of(voters)}, workspace,
+                                   sms, static_cast<cudaStream_t>(stream)));
+}
+
+BITNET_API int64_t bitnet_kv4_evict_workspace_size(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* batch,
+                                                   int64_t budget) {
+  Kv4 c{};
+  if (int st = check_kv4(cache, batch, &c)) return st;
+  if (budget < 1 || budget > INT32_MAX) return BITNET_EINVAL;
+  return kv4_evict_ws_bytes(c, (int)budget);
+}
+
+BITNET_API int bitnet_kv4_evict(const bitnet_kv4_cache* cache, const bitnet_kv4_batch* batch, float* mass,
+                                int64_t budget, int64_t limit, int64_t sinks, int64_t recent, const int32_t* into,
+                                int64_t into_pages, int32_t* new_len, void* workspace, int64_t workspace_bytes,
+                                void* stream) {
+  Kv4 c{};
+  if (int st = check_kv4(cache, batch, &c)) return st;
+  if (!mass || budget < 1 || limit < budget || limit > INT32_MAX) return BITNET_EINVAL;
+  if (sinks < 0 || sinks > budget || recent < 0 || recent > budget - sinks) return BITNET_EINVAL;
+  if (into && (into_pages < 1 || into_pages > kKvMaxPages || into_pages * kKvPage < budget)) return BITNET_EINVAL;
+  const int64_t need = kv4_evict_ws_bytes(c, (int)budget);
+  if (!workspace || workspace_bytes < need) return BITNET_EINVAL;
+  if (!aligned(mass, 16) || !aligned(workspace, 256) || !aligned(into, 4) || !aligned(new_len, 4)) return BITNET_EALIGN;
+  int sms = 0;
+  if (int st = check_device(&sms)) return st;
+  const Kv4Evict e{mass, into, into_pages, new_len, (int)budget, (int)limit, (int)sinks, (int)recent};
+  return status_of(launch_kv4_evict(c, cache->head_dim, e, workspace, sms, static_cast<cudaStream_t>(stream)));
+}
+
 // ---- rotary positions ----
 namespace {
 constexpr int64_t kRopeMaxDim = 1024, kRopeMaxHeads = 1 << 17;
@@ -696,7 +771,8 @@ BITNET_API int bitnet_last_device_error(void) {
                                     read_clear_device_error_gemv_ring, read_clear_device_error_selftest,
                                     read_clear_device_error_prefill, read_clear_device_error_pair,
                                     read_clear_device_error_kv4_cache, read_clear_device_error_kv4_decode,
-                                    read_clear_device_error_kv4_prompt, read_clear_device_error_w4_quant};
+                                    read_clear_device_error_kv4_prompt, read_clear_device_error_w4_quant,
+                                    read_clear_device_error_kv4_mass, read_clear_device_error_kv4_evict};
   for (auto rd : readers) {
     int v = 0;
     if (rd(&v) != cudaSuccess) return BITNET_ECUDA;

@@ -132,4 +132,27 @@ int64_t kv4_prompt_ws_bytes(const Kv4& c, int dim, int share);
 cudaError_t launch_kv4_prompt(const Kv4& c, int dim, const Kv4Attn& a, int done_rows, void* ws, cudaStream_t stream);
 cudaError_t read_clear_device_error_kv4_prompt(int* value);
 
+// Attention weight that cached tokens gather (kv4_mass.cu): one fp32 number for each page, head and place.
+struct Kv4Mass {
+  const float* in;  // n_pages x kv_heads x 64
+  float* out;       // the same memory, or apart
+  float decay;
+  int voters;       // the last rows of a sequence that vote
+};
+int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters);
+cudaError_t launch_kv4_mass(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, void* ws, int num_sms, cudaStream_t stream);
+cudaError_t read_clear_device_error_kv4_mass(int* value);
+
+// Eviction (kv4_evict.cu).
+struct Kv4Evict {
+  float* mass;
+  const int32_t* into;  // batch x into_pages, or null: in place
+  int64_t into_pages;
+  int32_t* new_len;     // batch, or null
+  int budget, limit, sinks, recent;
+};
+int64_t kv4_evict_ws_bytes(const Kv4& c, int budget);
+cudaError_t launch_kv4_evict(const Kv4& c, int dim, const Kv4Evict& e, void* ws, int num_sms, cudaStream_t stream);
+cudaError_t read_clear_device_error_kv4_evict(int* value);
+
 }  // namespace bitnet
