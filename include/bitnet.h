@@ -496,7 +496,7 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache *cache, const bitnet_
  *   the row's largest may not), fp32 ones enter as two fp16 parts (22 bits); scores, maxima and sums are fp32. A NaN
  *   or an infinity in a query or key makes the votes of the rows that meet it NaN.
  *   mass, mass_out : the same array, or two that do not overlap; 16-byte aligned
- *   decay  : finite; voters 0 .. 2^31 - 1
+ *   decay  : finite; voters 0 .. 2^31 - 1; total_q * q_heads / kv_heads < 2^30 - 64
  *   q, dtype, q_heads, q_stride, scale, window, sinks : as in bitnet_kv4_attention
  *   workspace : device, 256-byte aligned, at least bitnet_kv4_attention_mass_workspace_size bytes (for the same
  *            cache, batch sizes, q_heads and voters). Needs no initialisation; calls that may run at the same

@@ -577,6 +577,8 @@ int check_kv4_queries(const Kv4& c, int dim, const void* q, int dtype, int64_t q
                  window ? (int)window : INT32_MAX, window ? (int)sinks : 0, dtype == BITNET_BF16};
   return aligned(q, 16) ? BITNET_OK : BITNET_EALIGN;
 }
+// columns (two a row of fp32) are counted in 32 bits
+bool valid_mass_rows(const Kv4& c, int64_t q_heads) { return (int64_t)c.total_q * (q_heads / c.kv_heads) <= (1 << 30) - 64; }
 int voters_of(int64_t voters) { return voters ? (int)voters : INT32_MAX; }
 }  // namespace
 
@@ -589,7 +591,7 @@ BITNET_API int64_t bitnet_kv4_attention_mass_workspace_size(const bitnet_kv4_cac
                                                             int64_t q_heads, int64_t voters) {
   Kv4 c{};
   if (int st = check_kv4(cache, batch, &c)) return st;
-  if (!valid_q_heads(q_heads, c.kv_heads) || !valid_q_rows(c, q_heads)) return BITNET_EINVAL;
+  if (!valid_q_heads(q_heads, c.kv_heads) || !valid_mass_rows(c, q_heads)) return BITNET_EINVAL;
   if (voters < 0 || voters > INT32_MAX) return BITNET_EINVAL;
   return kv4_mass_ws_bytes(c, cache->head_dim, (int)q_heads, voters_of(voters));
 }
@@ -603,6 +605,7 @@ BITNET_API int bitnet_kv4_attention_mass(const bitnet_kv4_cache* cache, const bi
   if (int st = check_kv4(cache, batch, &c)) return st;
   if (!mass || !mass_out || !std::isfinite(decay) || voters < 0 || voters > INT32_MAX) return BITNET_EINVAL;
   if (int st = check_kv4_queries(c, cache->head_dim, q, dtype, q_heads, q_stride, scale, window, sinks, &a)) return st;
+  if (!valid_mass_rows(c, q_heads)) return BITNET_EINVAL;
   const int64_t need = kv4_mass_ws_bytes(c, cache->head_dim, (int)q_heads, voters_of(voters));
   if (need > 0 && (!workspace || workspace_bytes < need)) return BITNET_EINVAL;
   if (!aligned(mass, 16) || !aligned(mass_out, 16) || (workspace && !aligned(workspace, 256))) return BITNET_EALIGN;

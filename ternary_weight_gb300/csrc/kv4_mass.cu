@@ -1,7 +1,22 @@
 // kv4_mass.cu -- the attention weight that cached tokens gather from a call's queries.
 //
-// Simple form: a warp for each voting row and head finds the maximum and the sum of its softmax; then a
-// block for each page and head adds up its tokens' weights. fp32 throughout.
+// A sequence's voting rows times the query heads that share a key/value head are its columns (fp32
+// queries: two columns each, the parts of their 22 bits). A tile is 32 tokens of one head; a block of columns
+// against a tile is m16n8k16 with the codes as the A operand:
+//   raw[t][r] = sum_d code[t][d] q'[r][d],   x = scale log2 e (step raw / up + base sum(q))
+// The weight of a token needs its row's maximum M and sum L over all tokens first, so the keys are read twice: the
+// first kernel finds (M, L) of each column over each chunk of tiles, the second joins them and adds up
+//   votes[t] = sum_r 2^(x - M) / L
+// The scores of both come from the same instructions, so that each row's votes add up to 1 however large they are.
+// There are no atomics: results do not depend on timing.
+//
+// A code enters as the fp16 subnormal c 2^-24 (its nibble masked out of the word) or c 2^-20 (the nibble above, not
+// shifted; q' carries the 2^-4): 5 instructions for a word of 8 codes, sums exact in fp32. Lane t of four takes 16
+// bytes of a key row (8 with D = 64), so a warp's loads of a tile are contiguous, straight from the cache.
+//
+// Few columns (64 at most): both kernels are bound by the keys' bytes, the second kernel's mostly from L2. Many: by
+// the products; then the second kernel's blocks keep their tiles' codes and go through a share of the columns, and a third
+// kernel adds up the shares.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -10,118 +25,521 @@
 namespace bitnet {
 namespace {
 
+constexpr int WARPS = 8, THREADS = WARPS * 32;
+constexpr int TILE = 32;  // tokens of a tile: half a page
+constexpr int MAX_CHUNK = 32 * WARPS;  // tiles of a chunk: a warp keeps the page ids of its own, one a lane
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
-__device__ __forceinline__ float q_number(const Kv4Attn& a, int64_t row, int head, int dim, int d) {
-  const int64_t at = row * a.q_stride + (int64_t)head * dim + d;
-  return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]) : static_cast<const float*>(a.q)[at];
+struct Plan {
+  int parts;    // columns of a row: 1, or 2 for fp32 queries
+  int votes;    // rows of a sequence that vote, at most
+  int nt;       // eights of columns of a block
+  int blocks;   // blocks of columns of a unit (a sequence's head), at most
+  int tiles;    // tiles of a unit, at most
+  int chunk;    // of them in a chunk
+  int chunks;
+  int shares;   // of the columns, in the second kernel; 0: few columns
+  int groups;   // runs of WARPS tiles (many columns)
+};
+struct Stats {
+  float2* part;  // unit, block, chunk, column: (M, L)
+  float* votes;  // unit, group, share, WARPS x TILE
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ bool visible(const Kv4Attn& a, int p, int j) {
-  return j <= p && ((int64_t)j > (int64_t)p - a.window || j < a.sinks);
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// scale log2 e (q . k) of the token in place t of a block
-template <int D>
-__device__ __forceinline__ float score(const uint8_t* blk, int t, const float* q, float qsum, float scale) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(blk) + kv4_rho(t) * (D / 8);
-  const __half2 sb = *reinterpret_cast<const __half2*>(blk + kKvPage * D + kv4_rho(t) * 8);
-  float s = 0.0f;
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int n = 0; n < 8; ++n) s = fmaf((float)((w[i] >> (4 * n)) & 15u), q[i + D / 8 * n], s);
-  // no multiply-add with what follows: both kernels get the same bits
-  return __fmul_rn(__fmul_rn(scale, kLog2e), __fmaf_rn(__low2float(sb), s, __fmul_rn(__high2float(sb), qsum)));
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
+// A unit's rows: which vote, and where they stand.
+struct Rows {
+  int b, h;
+  Kv4Seq s;
+  int votes;
+  __device__ __forceinline__ int position(int i) const { return s.len - votes + i; }  // of voting row i
+};
+__device__ __forceinline__ Rows rows_of(const Kv4& c, int unit, int voters, bool* bad) {
+  Rows r;
+  r.b = unit / c.kv_heads;
+  r.h = unit - r.b * c.kv_heads;
+  bool wrong = false;
+  r.s = kv4_sequence(c, r.b, &wrong);
+  if (wrong && c.cu_q[r.b] != c.cu_q[r.b + 1]) *bad = true;
+  r.votes = min(r.s.n, voters);
+  return r;
+}
+
+// What a column needs besides its fragments.
+struct Column {
+  float a, b;  // x = step (a raw) + base b
+  int p;       // the row's position
+  float m, l;  // the row's maximum and the inverse of its sum (second kernel)
+};
+template <int D, int NT>
+struct __align__(16) Shared {
+  uint4 frag[NT][D / 32][32];  // eight, word, lane: its column's numbers for that word's codes
+  Column col[NT * 8];
+  float2 part[WARPS][NT * 8];
+};
+
+// The fragments and constants of columns [col0, col0 + 8 NT): D / 8 lanes a row, 8 numbers each.
+template <int D, int NT, bool F32>
+__device__ __forceinline__ void load_columns(const Kv4Attn& a, const Rows& r, int col0, Shared<D, NT>& sh) {
+  constexpr int W = D / 8, PARTS = F32 ? 2 : 1, ROWS = NT * 8 / PARTS, PER = THREADS / W;
+  const int w = threadIdx.x % W, rows = r.votes * a.share;
+  for (int k = threadIdx.x / W; k < ROWS; k += PER) {
+    const int row = col0 / PARTS + k, i = row / a.share;
+    const bool there = row < rows;
+    float x[8];  // number n: dimension w + W n, the nibbles of word w
+    float sum = 0.0f;
+    uint32_t top = 0;
+    const int64_t at = there ? (int64_t)(r.s.q0 + r.s.n - r.votes + i) * a.q_stride + (int64_t)(r.h * a.share + row - i * a.share) * D : 0;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      x[n] = 0.0f;
+      if (there)
+        x[n] = F32 ? static_cast<const float*>(a.q)[at + w + W * n]
+                   : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + w + W * n]);
+      sum += x[n];
+      top = max(top, __float_as_uint(x[n]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int o = W / 2; o >= 1; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    // the row's power of two: its largest number comes to [2^14, 2^15)
+    int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);
+    e = e > 127 ? 127 : e < -113 ? -113 : e;
+    const float up = __int_as_float((e + 127) << 23);
+    // words of lane quad t: W / 4 of them
+    constexpr int WORDS = W / 4;
+    const int t = w / WORDS, word = w % WORDS;
+    float hi[8], lo[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      hi[n] = x[n] * up * (n & 1 ? 0.0625f : 1.0f);
+      lo[n] = hi[n] - __half2float(__float2half_rn(hi[n]));
+    }
+    const int col = k * PARTS;
+    sh.frag[col >> 3][word][(col & 7) * 4 + t] =
+        make_uint4(pack_half2(hi[0], hi[4]), pack_half2(hi[1], hi[5]), pack_half2(hi[2], hi[6]), pack_half2(hi[3], hi[7]));
+    if (F32)
+      sh.frag[col >> 3][word][((col & 7) + 1) * 4 + t] =
+          make_uint4(pack_half2(lo[0], lo[4]), pack_half2(lo[1], lo[5]), pack_half2(lo[2], lo[6]), pack_half2(lo[3], lo[7]));
+    if (w == 0) {
+      const float c1 = __fmul_rn(a.scale, kLog2e);
+      // c1 2^(24 - e) in two steps: the power may pass fp32's range
+      const int f = 24 - e, half = f / 2;
+      Column c;
+      c.a = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
+      c.b = __fmul_rn(c1, sum);
+      c.p = there ? r.position(i) : -1;
+      c.m = c.l = 0.0f;
+      sh.col[col] = c;
+      if (F32) sh.col[col + 1] = c;
+    }
+  }
+}
+
+// A tile's codes and parameters as they lie in the cache: rows mt * 16 + g and + 8.
 template <int D>
-__global__ void __launch_bounds__(32) kv4_mass_rows(Kv4 c, Kv4Attn a, int voters, float2* stats) {
-  __shared__ float q[D];
-  const int row = blockIdx.x, head = blockIdx.y, lane = threadIdx.x;
-  const int b = kv4_find(c, row);
-  if (b < 0) return;
+struct Codes {
+  static constexpr int WORDS = D / 32;  // words of a lane and row
+  uint32_t w[2][2][WORDS];
+  uint32_t par[2][2];
+  __device__ __forceinline__ void load(const uint8_t* blk, int tile, int g, int t) {
+    const int row0 = (tile & 1) * TILE;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = row0 + mt * 16 + h * 8 + g;
+        const uint8_t* p = blk + row * (D / 2) + t * (WORDS * 4);
+        if (D == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p);
+          w[mt][h][0] = v.x, w[mt][h][1] = v.y, w[mt][h][2 % WORDS] = v.z, w[mt][h][3 % WORDS] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          w[mt][h][0] = v.x, w[mt][h][1] = v.y;
+        }
+        par[mt][h] = *reinterpret_cast<const uint32_t*>(blk + kKvPage * D + row * 8);
+      }
+  }
+};
+// the token (of its page half) in row `row` of a tile
+__device__ __forceinline__ int token_of(int row) { return kv4_rho_inv(row); }
+
+// Scores of one m16 x n8: the lane has rows g and g + 8, columns 2 t and 2 t + 1 (fp32 queries: one row's parts).
+template <int D, int NT>
+__device__ __forceinline__ void products(const Codes<D>& k, int mt, const Shared<D, NT>& sh, int n, int lane, float (&d)[4]) {
+  d[0] = d[1] = d[2] = d[3] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < Codes<D>::WORDS; ++i) {
+    const uint4 f = sh.frag[n][i][lane];
+    const uint32_t a = k.w[mt][0][i], b = k.w[mt][1][i], a8 = a >> 8, b8 = b >> 8;
+    mma16816(d, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, f.x, f.y);
+    mma16816(d, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, f.z, f.w);
+  }
+}
+__device__ __forceinline__ float score(float raw, const Column& c, float2 par) {
+  return __fmaf_rn(par.x, __fmul_rn(c.a, raw), __fmul_rn(par.y, c.b));
+}
+__device__ __forceinline__ float2 params(uint32_t p) { return __half22float2(*reinterpret_cast<const __half2*>(&p)); }
+
+__device__ __forceinline__ bool visible(const Kv4Attn& a, int p, int j) {
+  return j <= p && (j > (int64_t)p - a.window || j < a.sinks);
+}
+// what rows at positions first .. last see of tokens [j0, j0 + n): 0 nothing, 1 some, 2 all
+__device__ __forceinline__ int seen(const Kv4Attn& a, int first, int last, int j0, int n) {
+  if (j0 > last || ((int64_t)j0 + n - 1 <= (int64_t)first - a.window && j0 >= a.sinks)) return 0;
+  return j0 + n - 1 <= first && (j0 > (int64_t)last - a.window || j0 + n - 1 < a.sinks) ? 2 : 1;
+}
+
+// joins (m, l) with (m2, l2); a NaN is no maximum, but stays in the sum
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2), from = top == kNegInf ? 0.0f : top;
+  l = l * exp2_approx(m - from) + l2 * exp2_approx(m2 - from);
+  m = top;
+}
+
+// ------------------------------------------------------------- first kernel: maxima and sums
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c, Kv4Attn a, int voters, Plan pl, Stats st) {
+  __shared__ Shared<D, NT> sh;
+  constexpr int COLS = NT * 8, PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   bool bad = false;
-  const Kv4Seq s = kv4_sequence(c, b, &bad);
-  const int i = row - s.q0, p = s.len - s.n + i;
-  if (i >= s.n || i < s.n - voters) return;
-  float sum = 0.0f;
-  for (int d = lane; d < D; d += 32) sum += q[d] = q_number(a, row, head, D, d);
-  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  __syncwarp();
-  float m = kNegInf, l = 0.0f;
-  for (int j = lane; j <= p; j += 32) {
-    if (!visible(a, p, j)) continue;
-    const uint8_t* blk = kv4_block(c, b, j / kKvPage, head / a.share, kv4_block_bytes(D), &bad);
-    const float x = score<D>(blk, j % kKvPage, q, sum, a.scale);
-    const float top = fmaxf(m, x), from = top == kNegInf ? 0.0f : top;  // a NaN is no maximum, but stays in the sum
-    l = l * exp2f(m - from) + exp2f(x - from);
-    m = top;
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks * pl.chunks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t rest = item / pl.chunks;
+    const int chunk = (int)(item - rest * pl.chunks), unit = (int)(rest / pl.blocks), block = (int)(rest - (int64_t)unit * pl.blocks);
+    const Rows r = rows_of(c, unit, voters, &bad);
+    const int rows = r.votes * a.share, col0 = block * COLS;
+    if (col0 >= rows * PARTS) continue;
+    const int tile0 = chunk * pl.chunk, tile1 = min(tile0 + pl.chunk, (r.s.len + TILE - 1) / TILE);
+    const int first = r.position(col0 / PARTS / a.share), last = r.position((min((col0 + COLS) / PARTS, rows) - 1) / a.share);
+    float2* out = st.part + item * COLS;
+    if (tile0 >= tile1 || seen(a, first, last, tile0 * TILE, (tile1 - tile0) * TILE) == 0) {
+      for (int i = threadIdx.x; i < COLS; i += THREADS) out[i] = make_float2(kNegInf, 0.0f);
+      continue;
+    }
+    // the page ids of this warp's tiles, one a lane
+    int id = 0;
+    const int mine = tile0 + warp + lane * WARPS;
+    if (mine < tile1) {
+      id = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
+      if (id < 0 || id >= c.n_pages) bad = true, id = 0;
+    }
+    load_columns<D, NT, F32>(a, r, col0, sh);
+    __syncthreads();
+    const int eights = min(NT, (rows * PARTS - col0 + 7) / 8);
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf, l[n][0] = l[n][1] = 0.0f;
+    Codes<D> cur;
+    const auto load = [&](int k) {
+      const int from = __shfl_sync(0xffffffffu, id, k);
+      const int tile = tile0 + warp + k * WARPS;
+      if (tile < tile1) cur.load(c.pages + ((int64_t)from * c.kv_heads + r.h) * BLK, tile, g, t);
+    };
+    load(0);
+    for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
+      const Codes<D> now = cur;
+      if (k < 31) load(k + 1);
+      const int j0 = tile * TILE, sees = seen(a, first, last, j0, TILE);
+      if (sees == 0) continue;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n >= eights) break;
+        float d[2][4];
+        products<D, NT>(now, 0, sh, n, lane, d[0]);
+        products<D, NT>(now, 1, sh, n, lane, d[1]);
+#pragma unroll
+        for (int e = 0; e < (F32 ? 1 : 2); ++e) {
+          const Column& col = sh.col[n * 8 + 2 * t + e];
+          float x[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int mt = v >> 1, h = v & 1;
+            const float raw = F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e];
+            x[v] = score(raw, col, params(now.par[mt][h]));
+            if (sees == 1 && !visible(a, col.p, j0 + token_of(mt * 16 + h * 8 + g))) x[v] = kNegInf;
+          }
+          const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m[n][e]), from = top == kNegInf ? 0.0f : top;
+          l[n][e] = l[n][e] * exp2_approx(m[n][e] - from) + ((exp2_approx(x[0] - from) + exp2_approx(x[1] - from)) + (exp2_approx(x[2] - from) + exp2_approx(x[3] - from)));
+          m[n][e] = top;
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1)
+          join(m[n][e], l[n][e], __shfl_xor_sync(0xffffffffu, m[n][e], o), __shfl_xor_sync(0xffffffffu, l[n][e], o));
+        if (g == 0) sh.part[warp][n * 8 + 2 * t + e] = make_float2(m[n][e], l[n][e]);
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < COLS; i += THREADS) {
+      float2 v = sh.part[0][i];
+      for (int w = 1; w < WARPS; ++w) join(v.x, v.y, sh.part[w][i].x, sh.part[w][i].y);
+      out[i] = v;
+    }
+    __syncthreads();  // the next item's columns
   }
-  for (int o = 16; o >= 1; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-    const float top = fmaxf(m, m2), from = top == kNegInf ? 0.0f : top;
-    l = l * exp2f(m - from) + l2 * exp2f(m2 - from);
-    m = top;
-  }
-  if (lane == 0) stats[(int64_t)row * a.q_heads + head] = make_float2(m, l);
   if (bad) record_device_error(kErrRange);
 }
 
-template <int D>
-__global__ void __launch_bounds__(64) kv4_mass_pages(Kv4 c, Kv4Attn a, Kv4Mass m, const float2* stats) {
-  __shared__ float q[D];
-  const int page = blockIdx.x, h = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
-  bool bad = false;
-  const Kv4Seq s = kv4_sequence(c, b, &bad);
-  bad = bad && c.cu_q[b] != c.cu_q[b + 1];
-  if (s.n == 0 || page * kKvPage >= s.len) {
-    if (bad && page == 0 && h == 0 && t == 0) record_device_error(kErrRange);
-    return;
-  }
-  bool wrong = false;
-  const uint8_t* blk = kv4_block(c, b, page, h, kv4_block_bytes(D), &wrong);
-  const int j = page * kKvPage + t;
-  float votes = 0.0f;
-  for (int i = max(0, s.n - m.voters); i < s.n; ++i) {
-    const int p = s.len - s.n + i;
-    for (int head = h * a.share; head < (h + 1) * a.share; ++head) {
-      __syncthreads();
-      for (int d = t; d < D; d += 64) q[d] = q_number(a, s.q0 + i, head, D, d);
-      __syncthreads();
-      if (j >= s.len || !visible(a, p, j)) continue;
-      float lanes[32] = {};  // as the first kernel adds them up
-      for (int d = 0; d < D; ++d) lanes[d % 32] += q[d];
-      for (int o = 16; o >= 1; o >>= 1)
-        for (int l = 0; l < o; ++l) lanes[l] += lanes[l + o];
-      const float sum = lanes[0];
-      const float2 st = stats[(int64_t)(s.q0 + i) * a.q_heads + head];
-      votes += exp2f(score<D>(blk, t, q, sum, a.scale) - st.x) / st.y;
+// The joined (M, 1 / L) of a block's columns, a warp each.
+template <int D, int NT, bool F32>
+__device__ __forceinline__ void load_sums(const Plan& pl, const Stats& st, int unit, int block, int chunks, Shared<D, NT>& sh) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const float2* part = st.part + ((int64_t)unit * pl.blocks + block) * pl.chunks * (NT * 8);
+  for (int i = warp; i < NT * 8; i += WARPS) {
+    if (F32 && (i & 1)) continue;
+    float m = kNegInf, l = 0.0f;
+    for (int k = lane; k < chunks; k += 32) {
+      const float2 v = part[(int64_t)k * (NT * 8) + i];
+      join(m, l, v.x, v.y);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+    if (lane == 0) {
+      sh.col[i].m = m == kNegInf ? 0.0f : m;
+      sh.col[i].l = l == 0.0f ? 0.0f : __frcp_rn(l);
     }
   }
-  if (j < s.len && !wrong) {
-    const int64_t at = ((int64_t)c.page_table[(int64_t)b * c.max_pages + page] * c.kv_heads + h) * kKvPage + t;
-    m.out[at] = j < s.len - s.n ? fmaf(m.decay, m.in[at], votes) : votes;
-  }
-  if (bad || wrong) record_device_error(kErrRange);
 }
 
-template <int D>
-cudaError_t launch(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, void* ws, cudaStream_t st) {
-  float2* stats = static_cast<float2*>(ws);
-  kv4_mass_rows<D><<<dim3(c.total_q, a.q_heads), 32, 0, st>>>(c, a, m.voters, stats);
+// votes of the lane's four tokens from a block of columns
+template <int D, int NT, bool F32>
+__device__ __forceinline__ void add_votes(const Kv4Attn& a, const Codes<D>& k, const Shared<D, NT>& sh, int eights, int j0, int sees,
+                                          float (&votes)[4]) {
+  const int lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (n >= eights) break;
+    float d[2][4];
+    products<D, NT>(k, 0, sh, n, lane, d[0]);
+    products<D, NT>(k, 1, sh, n, lane, d[1]);
+#pragma unroll
+    for (int e = 0; e < (F32 ? 1 : 2); ++e) {
+      const Column& col = sh.col[n * 8 + 2 * t + e];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int mt = v >> 1, h = v & 1;
+        const float raw = F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e];
+        float w = exp2_approx(score(raw, col, params(k.par[mt][h])) - col.m);
+        if (sees == 1 && !visible(a, col.p, j0 + token_of(mt * 16 + h * 8 + g))) continue;
+        if (col.p >= 0) votes[v] = fmaf(w, col.l, votes[v]);
+      }
+    }
+  }
+}
+// the sum over the four lanes that share tokens; lane t gets token (row) t / 2 * 16 + t % 2 * 8 + g
+__device__ __forceinline__ float gather_votes(const float (&votes)[4], int t) {
+  float s[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    s[v] = votes[v] + __shfl_xor_sync(0xffffffffu, votes[v], 1);
+    s[v] += __shfl_xor_sync(0xffffffffu, s[v], 2);
+  }
+  return t == 0 ? s[0] : t == 1 ? s[1] : t == 2 ? s[2] : s[3];
+}
+
+// ------------------------------------------------------------- second kernel, few columns
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_votes(Kv4 c, Kv4Attn a, Kv4Mass ms, Plan pl, Stats st) {
+  __shared__ Shared<D, NT> sh;
+  constexpr int PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+  bool bad = false;
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.chunks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int unit = (int)(item / pl.chunks), chunk = (int)(item - (int64_t)unit * pl.chunks);
+    const Rows r = rows_of(c, unit, ms.voters, &bad);
+    const int rows = r.votes * a.share, all = (r.s.len + TILE - 1) / TILE;
+    const int tile0 = chunk * pl.chunk, tile1 = min(tile0 + pl.chunk, all);
+    if (rows == 0 || tile0 >= tile1) continue;
+    int id = -1;
+    const int mine = tile0 + warp + lane * WARPS;
+    if (mine < tile1) {
+      id = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
+      if (id < 0 || id >= c.n_pages) bad = true, id = -1;
+    }
+    load_columns<D, NT, F32>(a, r, 0, sh);
+    __syncthreads();
+    load_sums<D, NT, F32>(pl, st, unit, 0, (all + pl.chunk - 1) / pl.chunk, sh);
+    __syncthreads();
+    const int eights = min(NT, (rows * PARTS + 7) / 8), first = r.position(0), last = r.position(r.votes - 1), old = r.s.len - r.s.n;
+    Codes<D> cur;
+    const auto load = [&](int k) {
+      const int from = __shfl_sync(0xffffffffu, id, k);
+      const int tile = tile0 + warp + k * WARPS;
+      if (tile < tile1 && from >= 0) cur.load(c.pages + ((int64_t)from * c.kv_heads + r.h) * BLK, tile, g, t);
+    };
+    load(0);
+    for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
+      const Codes<D> now = cur;
+      const int from = __shfl_sync(0xffffffffu, id, k);
+      if (k < 31) load(k + 1);
+      const int j0 = tile * TILE, sees = seen(a, first, last, j0, TILE);
+      if (from < 0) continue;
+      if (sees == 0 && ms.decay == 1.0f && ms.in == ms.out && j0 + TILE <= old) continue;  // nothing changes
+      const int row = (t >> 1) * 16 + (t & 1) * 8 + g, j = j0 + token_of(row);
+      const int64_t at = ((int64_t)from * c.kv_heads + r.h) * kKvPage + (tile & 1) * TILE + token_of(row);
+      const float before = j < old ? ms.in[at] : 0.0f;
+      float votes[4] = {};
+      if (sees) add_votes<D, NT, F32>(a, now, sh, eights, j0, sees, votes);
+      const float got = gather_votes(votes, t);
+      if (j < r.s.len) ms.out[at] = j < old ? fmaf(ms.decay, before, got) : got;
+    }
+    __syncthreads();
+  }
+  if (bad) record_device_error(kErrRange);
+}
+
+// ------------------------------------------------------------- second and third kernel, many columns
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, Kv4Mass ms, Plan pl, Stats st) {
+  __shared__ Shared<D, NT> sh;
+  constexpr int COLS = NT * 8, PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+  bool bad = false;
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.groups * pl.shares;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t rest = item / pl.shares;
+    const int share = (int)(item - rest * pl.shares), unit = (int)(rest / pl.groups), group = (int)(rest - (int64_t)unit * pl.groups);
+    const Rows r = rows_of(c, unit, ms.voters, &bad);
+    const int rows = r.votes * a.share, all = (r.s.len + TILE - 1) / TILE, tile = group * WARPS + warp;
+    if (rows == 0 || group * WARPS >= all) continue;
+    Codes<D> k;
+    bool there = tile < all;
+    if (there) {
+      const int id = c.page_table[(int64_t)r.b * c.max_pages + tile / 2];
+      if (id < 0 || id >= c.n_pages) bad = true, there = false;
+      else k.load(c.pages + ((int64_t)id * c.kv_heads + r.h) * BLK, tile, g, t);
+    }
+    float votes[4] = {};
+    const int chunks = (all + pl.chunk - 1) / pl.chunk;
+    for (int block = share; block * COLS < rows * PARTS; block += pl.shares) {
+      const int col0 = block * COLS, first = r.position(col0 / PARTS / a.share);
+      const int last = r.position((min((col0 + COLS) / PARTS, rows) - 1) / a.share);
+      if (seen(a, first, last, group * WARPS * TILE, WARPS * TILE) == 0) continue;
+      load_columns<D, NT, F32>(a, r, col0, sh);
+      __syncthreads();
+      load_sums<D, NT, F32>(pl, st, unit, block, chunks, sh);
+      __syncthreads();
+      const int sees = there ? seen(a, first, last, tile * TILE, TILE) : 0;
+      if (sees) add_votes<D, NT, F32>(a, k, sh, min(NT, (rows * PARTS - col0 + 7) / 8), tile * TILE, sees, votes);
+      __syncthreads();
+    }
+    const float got = gather_votes(votes, t);
+    const int row = (t >> 1) * 16 + (t & 1) * 8 + g;
+    st.votes[(item * WARPS + warp) * TILE + token_of(row)] = got;
+  }
+  if (bad) record_device_error(kErrRange);
+}
+
+__global__ void __launch_bounds__(THREADS) kv4_mass_join(Kv4 c, Kv4Mass ms, Plan pl, Stats st) {
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.groups;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int unit = (int)(item / pl.groups), group = (int)(item - (int64_t)unit * pl.groups);
+    bool bad = false;
+    const Rows r = rows_of(c, unit, ms.voters, &bad);
+    const int j = group * (WARPS * TILE) + threadIdx.x;
+    if (r.votes == 0 || j >= r.s.len) continue;
+    const int id = c.page_table[(int64_t)r.b * c.max_pages + j / kKvPage];
+    if (id < 0 || id >= c.n_pages) continue;
+    float got = 0.0f;
+    for (int s = 0; s < pl.shares; ++s) got += st.votes[(item * pl.shares + s) * (WARPS * TILE) + threadIdx.x];
+    const int64_t at = ((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage;
+    ms.out[at] = j < r.s.len - r.s.n ? fmaf(ms.decay, ms.in[at], got) : got;
+  }
+}
+
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+unsigned grid_of(int64_t items) { return (unsigned)(items < (1 << 20) ? items : (1 << 20)); }
+
+Plan plan_of(const Kv4& c, int share, int voters, bool f32, int num_sms) {
+  Plan p{};
+  p.parts = f32 ? 2 : 1;
+  p.votes = voters < c.max_q ? voters : c.max_q;
+  p.votes = p.votes < c.total_q ? p.votes : c.total_q;
+  const int64_t cols = (int64_t)p.votes * share * p.parts, units = (int64_t)c.batch * c.kv_heads;
+  p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 8;
+  p.blocks = (int)((cols + p.nt * 8 - 1) / (p.nt * 8));
+  p.tiles = (c.max_kv + TILE - 1) / TILE;
+  // a chunk: as many tiles as leave each SM several blocks
+  int64_t per = (units * p.blocks * p.tiles + (int64_t)num_sms * 4 * WARPS - 1) / ((int64_t)num_sms * 4 * WARPS);
+  per = per < 1 ? 1 : per > MAX_CHUNK / WARPS ? MAX_CHUNK / WARPS : per;
+  p.chunk = (int)per * WARPS;
+  p.chunks = (p.tiles + p.chunk - 1) / p.chunk;
+  if (p.blocks > 1) {
+    p.groups = (p.tiles + WARPS - 1) / WARPS;
+    int64_t s = ((int64_t)num_sms * 4 + units * p.groups - 1) / (units * p.groups);
+    p.shares = (int)(s < 1 ? 1 : s > p.blocks ? p.blocks : s);
+  }
+  return p;
+}
+int64_t part_bytes(const Kv4& c, const Plan& p) { return align256((int64_t)c.batch * c.kv_heads * p.blocks * p.chunks * p.nt * 8 * 8); }
+int64_t votes_bytes(const Kv4& c, const Plan& p) {
+  return p.shares ? align256((int64_t)c.batch * c.kv_heads * p.groups * p.shares * WARPS * TILE * 4) : 0;
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
+  const int64_t units = (int64_t)c.batch * c.kv_heads;
+  if (p.tiles == 0) return cudaSuccess;
+  kv4_mass_rows<D, NT, F32><<<grid_of(units * p.blocks * p.chunks), THREADS, 0, st>>>(c, a, m.voters, p, s);
   if (cudaError_t e = cudaGetLastError()) return e;
-  const unsigned pages = (unsigned)((c.max_kv + kKvPage - 1) / kKvPage);
-  if (pages == 0) return cudaSuccess;
-  kv4_mass_pages<D><<<dim3(pages, c.kv_heads, c.batch), 64, 0, st>>>(c, a, m, stats);
+  if (p.shares == 0) {
+    kv4_mass_votes<D, NT, F32><<<grid_of(units * p.chunks), THREADS, 0, st>>>(c, a, m, p, s);
+    return cudaGetLastError();
+  }
+  kv4_mass_shares<D, NT, F32><<<grid_of(units * p.groups * p.shares), THREADS, 0, st>>>(c, a, m, p, s);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  kv4_mass_join<<<grid_of(units * p.groups), THREADS, 0, st>>>(c, m, p, s);
   return cudaGetLastError();
+}
+template <int D, bool F32>
+cudaError_t by_columns(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
+  if (p.nt == 1) return launch<D, 1, F32>(c, a, m, p, s, st);
+  if (p.nt == 2) return launch<D, 2, F32>(c, a, m, p, s, st);
+  return launch<D, 8, F32>(c, a, m, p, s, st);
 }
 
 }  // namespace
 
 int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters) {
-  return ((int64_t)c.total_q * q_heads * 8 + 255) / 256 * 256;
+  int64_t most = 0;  // whatever the queries' type
+  for (int f32 = 0; f32 < 2; ++f32) {
+    const Plan p = plan_of(c, q_heads / c.kv_heads, voters, f32, 152);
+    const int64_t n = part_bytes(c, p) + votes_bytes(c, p);
+    most = n > most ? n : most;
+  }
+  return most;
 }
 cudaError_t launch_kv4_mass(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, void* ws, int num_sms, cudaStream_t st) {
-  return dim == 128 ? launch<128>(c, a, m, ws, st) : launch<64>(c, a, m, ws, st);
+  const Plan p = plan_of(c, a.share, m.voters, !a.bf16, 152);
+  const Stats s{static_cast<float2*>(ws), reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + part_bytes(c, p))};
+  if (dim == 128) return a.bf16 ? by_columns<128, false>(c, a, m, p, s, st) : by_columns<128, true>(c, a, m, p, s, st);
+  return a.bf16 ? by_columns<64, false>(c, a, m, p, s, st) : by_columns<64, true>(c, a, m, p, s, st);
 }
 
 cudaError_t read_clear_device_error_kv4_mass(int* value) {

@@ -67,6 +67,9 @@ def test_bad_caches_and_batches_are_refused(lib, c, b, want):
 def test_sizes(lib):
     assert lib.bitnet_kv4_mass_bytes(3, 5) == 3 * 5 * 256 and lib.bitnet_kv4_mass_bytes(0, 5) == -1 and lib.bitnet_kv4_mass_bytes(1, 1025) == -1
     size = lambda heads, voters: lib.bitnet_kv4_attention_mass_workspace_size(ctypes.byref(cache()), ctypes.byref(batch(total_q=3)), heads, voters)  # noqa: E731
+    large = batch(total_q=(1 << 30) - 64, max_q=(1 << 30) - 64)
+    assert lib.bitnet_kv4_attention_mass_workspace_size(ctypes.byref(cache()), ctypes.byref(large), 4, 1) == -1
+    assert call(lib, b=large, heads=4) == -1
     assert size(8, 0) >= 0 and size(8, 5) >= 0 and size(7, 0) == -1 and size(8, -1) == -1
 
 
