@@ -10,9 +10,10 @@
 // zero point's share of the sum taken off behind it, cost 5, but sums of codes that are not centred cancel:
 // 3e-6 of the result where one number of the row is great.)
 //
-// A warp takes 16 weight rows and a part of K, and streams 16 x 128 codes at a time through a ring of
-// its own in shared memory (cp.async), the next tile's behind this one's. The block keeps the rows x'
-// in shared memory in the order of the B fragments. Where tiles are few, several warps share one along K and their sums are added in a fixed order.
+// A block keeps the rows x' in shared memory in the order of the B fragments, and takes a run of tiles of 16
+// weight rows; its warps cut the run's 16 x 128-code pieces into equal parts. A warp loads its pieces straight into the
+// registers that the A fragments are made from, AHEAD pieces before they are used, and writes the tiles that it has whole; the
+// tiles that it shares are added up at the end, in order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -22,37 +23,30 @@
 namespace bitnet {
 namespace {
 
-constexpr int ROWS = 16;               // weight rows of a tile
-constexpr int STAGE = ROWS * 64 + ROWS * 8 + ROWS * 4;  // codes, scales, zero points of 16 x 128 weights
+constexpr int ROWS = 16;  // weight rows of a tile
 constexpr int MAX_SMEM = 227 * 1024;
 
 struct Call {
   W4 w;
   const void* x;
   float* out;
-  int m;        // rows of this launch
-  int cols;     // m, or 2 m where fp32 rows enter as two parts
-  int splits;   // warps that share a tile
-  int stages;
+  int m;     // rows of this launch
+  int cols;  // m, or 2 m where fp32 rows enter as two parts
   bool bf16;
 };
 
+// ZERO: the sum begins at 0 (d is not read)
+template <bool ZERO>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  if constexpr (ZERO)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
@@ -62,35 +56,35 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t as_bits(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
-// The pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word's codes less their zero point, as fp16; z: 1024 + zero, twice.
-__device__ __forceinline__ void centred(uint32_t w, uint32_t z, uint32_t (&p)[4]) {
+// (w & mask) | magic in one instruction: magic is in a register
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
+  return r;
+}
+// The pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word's codes less their zero point, as fp16; z: 1024 + zero, twice;
+// magic: 1024, twice.
+__device__ __forceinline__ void centred(uint32_t w, uint32_t z, uint32_t magic, uint32_t (&p)[4]) {
   const uint32_t w8 = w >> 8, one16 = 0x2c002c00u;  // 1/16, twice
   // 64 + zero: 1024 + zero has steps of 1, 64 + zero of 1/16
   const uint32_t z64 = 0xd400d400u | (z & 0x000f000fu) << 4;  // negative
-  p[0] = as_bits(__hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), as_half2(z)));
-  p[1] = as_bits(__hfma2(as_half2((w & 0x00f000f0u) | 0x64006400u), as_half2(one16), as_half2(z64)));
-  p[2] = as_bits(__hsub2(as_half2((w8 & 0x000f000fu) | 0x64006400u), as_half2(z)));
-  p[3] = as_bits(__hfma2(as_half2((w8 & 0x00f000f0u) | 0x64006400u), as_half2(one16), as_half2(z64)));
+  p[0] = as_bits(__hsub2(as_half2(and_or<0x000f000fu>(w, magic)), as_half2(z)));
+  p[1] = as_bits(__hfma2(as_half2(and_or<0x00f000f0u>(w, magic)), as_half2(one16), as_half2(z64)));
+  p[2] = as_bits(__hsub2(as_half2(and_or<0x000f000fu>(w8, magic)), as_half2(z)));
+  p[3] = as_bits(__hfma2(as_half2(and_or<0x00f000f0u>(w8, magic)), as_half2(one16), as_half2(z64)));
 }
 
-// Shared memory: row factors (2 floats a row), fragments, then the warps' rings.
+// Shared memory: row factors (2 floats a row), fragments, then the warps' shares of tiles.
 __host__ __device__ __forceinline__ int frag_bytes(int K, int cols) { return K * cols * 2; }
 __host__ __device__ __forceinline__ int align16(int x) { return (x + 15) & ~15; }
 __host__ __device__ __forceinline__ int rows_bytes(int K, int m, int cols) { return align16(m * 8) + frag_bytes(K, cols); }
-
-// where word i of lane quad t of a 128-block begins in K: a lane's words of one matrix step stay in one group
-template <int G>
-__device__ __forceinline__ int word_k(int i, int t) {
-  return G == 128 ? t * 32 + i * 8 : G == 64 ? (i >> 1) * 64 + t * 16 + (i & 1) * 8 : i * 32 + t * 8;
-}
-// pieces of 16 bytes of row r of a stage are exchanged so that reads of 4 and 8 bytes a lane meet no bank twice
-__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 1) * 2 + ((r >> 2) & 1); }
 
 // The rows as fragments. xf[(block * 4 + word) * cols + col][t]: the 8 numbers that word meets, as
 // (0, 4), (1, 5), (2, 6), (3, 7).
 template <int G>
 __device__ __forceinline__ void load_rows(const Call& c, uint8_t* smem) {
-  const int K = c.w.K, tid = threadIdx.x, threads = blockDim.x, lane = tid % 32, warp = tid / 32, warps = threads / 32;
+  const int K = c.w.K, tid = threadIdx.x, threads = blockDim.x, lane = tid % 32;
   float2* factor = reinterpret_cast<float2*>(smem);
   uint4* xf = reinterpret_cast<uint4*>(smem + align16(c.m * 8));
   const int parts = c.bf16 ? 1 : 2;
@@ -106,25 +100,34 @@ __device__ __forceinline__ void load_rows(const Call& c, uint8_t* smem) {
       x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
   };
-  // a row's power of two: its largest number comes to [2^14, 2^15)
-  for (int m = warp; m < c.m; m += warps) {
+  // a row's power of two: its largest number comes to [2^14, 2^15). All threads look for it: 16 lanes have
+  // numbers of the same row
+  const int octets = K / 8;
+  uint32_t* tops = reinterpret_cast<uint32_t*>(xf);
+  for (int m = tid; m < c.m; m += threads) tops[m] = 0;
+  __syncthreads();
+  for (int i = tid; i - lane < c.m * octets; i += threads) {
+    const int m = i / octets, k = (i - m * octets) * 8;
     uint32_t top = 0;
-    for (int k = lane * 8; k < K; k += 256) {
+    if (m < c.m) {
       float x[8];
       eight(m, k, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) {
-      int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);  // up = 2^e
-      e = e > 127 ? 127 : e < -113 ? -113 : e;
-      const int half = -e / 2;  // 2^-e in two factors: it may pass the range of one
-      factor[m] = make_float2(__int_as_float((half + 127) << 23), __int_as_float((-e - half + 127) << 23));
-    }
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane % 16 == 0 && m < c.m) atomicMax(&tops[m], top);
   }
   __syncthreads();
-  const int octets = K / 8;
+  for (int m = tid; m < c.m; m += threads) {
+    const uint32_t top = tops[m];
+    int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);  // up = 2^e
+    e = e > 127 ? 127 : e < -113 ? -113 : e;
+    const int half = -e / 2;  // 2^-e in two factors: it may pass the range of one
+    factor[m] = make_float2(__int_as_float((half + 127) << 23), __int_as_float((-e - half + 127) << 23));
+  }
+  __syncthreads();
   for (int i = tid; i < c.m * octets; i += threads) {
     const int m = i / octets, o = i - m * octets, k = o * 8;
     float x[8];
@@ -150,209 +153,224 @@ __device__ __forceinline__ void load_rows(const Call& c, uint8_t* smem) {
   __syncthreads();
 }
 
+// A piece of weights as a lane loads it: 32 codes of rows g and g + 8, with their scales and zero points. A lane's
+// words of one matrix step stay in one group: with groups of 128 a lane takes 16 bytes of each row, with
+// 64 twice 8, with 32 four times 4.
+template <int G, bool ZEROS>
+struct Piece {
+  static constexpr int PER = 128 / G;  // groups
+  uint32_t w[2][4];
+  uint32_t s[2][PER == 4 ? 2 : 1];  // fp16 scales
+  uint32_t z[2];
+  // codes, scales, zeros: of this lane's row and quad place, at the piece
+  __device__ __forceinline__ void load(int h, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros) {
+    if (G == 128) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(codes));
+      w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
+      s[h][0] = __ldg(scales);
+      if (ZEROS) z[h] = __ldg(zeros);
+    } else if (G == 64) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(codes + p * 32));
+        w[h][2 * p] = v.x, w[h][2 * p + 1] = v.y;
+      }
+      s[h][0] = __ldg(reinterpret_cast<const uint32_t*>(scales));
+      if (ZEROS) z[h] = __ldg(reinterpret_cast<const uint16_t*>(zeros));
+    } else {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) w[h][p] = __ldg(reinterpret_cast<const uint32_t*>(codes + p * 16));
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(scales));
+      s[h][0] = v.x, s[h][PER == 4 ? 1 : 0] = v.y;
+      if (ZEROS) z[h] = __ldg(reinterpret_cast<const uint32_t*>(zeros));
+    }
+  }
+  __device__ __forceinline__ float scale(int h, int p) const {
+    const float2 f = __half22float2(as_half2(s[h][PER == 4 ? p >> 1 : 0]));
+    return p & 1 ? f.y : f.x;
+  }
+  // 1024 + zero as two fp16
+  __device__ __forceinline__ uint32_t zero(int h, int p) const {
+    return ZEROS ? __byte_perm(z[h], 0x64646464u, 0x4040 | p | p << 8) : 0x64086408u;
+  }
+};
+
 // NT: eights of columns
+template <int NT>
+struct Shape {
+  static constexpr int WARPS = NT == 1 ? 8 : 16, THREADS = WARPS * 32;
+  static constexpr int BLOCKS = NT == 1 ? 2 : 1;     // resident blocks of an SM
+  static constexpr int AHEAD = NT == 1 ? 4 : NT == 2 ? 3 : 2;      // pieces on their way
+  static constexpr int SHARE = 32 * NT * 16;         // bytes of a warp's share of a tile
+};
+
 template <int G, bool ZEROS, int NT>
-__global__ void __launch_bounds__(NT <= 2 ? 256 : 512) w4_matmul_kernel(Call c) {
+__global__ void __launch_bounds__(Shape<NT>::THREADS, Shape<NT>::BLOCKS) w4_matmul_kernel(Call c) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int PER = 128 / G;  // groups of a 128-block
-  const int K = c.w.K, N = c.w.N, lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-  const int g = lane >> 2, t = lane & 3;
+  constexpr int PER = 128 / G, WARPS = Shape<NT>::WARPS, AHEAD = Shape<NT>::AHEAD, BYTES = G == 128 ? 16 : G == 64 ? 8 : 4;
+  const int K = c.w.K, N = c.w.N, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // known to be the same for all lanes
+  const int tiles = (N + ROWS - 1) / ROWS, blocks = K / 128, groups = K / G;
+  const int tile0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), tile1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+  const int64_t all = (int64_t)(tile1 - tile0) * blocks;
+  const int64_t p0 = all * warp / WARPS, p1 = all * (warp + 1) / WARPS;  // this warp's pieces
+
+  // where the next piece to load lies: its tile's places (the same for the warp) and the lane's in a tile
+  int in_tile = tile0 + (int)(p0 / blocks), in_block = (int)(p0 % blocks), left_in = (int)(p1 - p0);
+  const uint8_t *codes, *zeros;
+  const uint16_t* scales;
+  int code_at[2], scale_at[2];
+  const auto place = [&]() {
+    const int64_t row = (int64_t)in_tile * ROWS;
+    codes = c.w.codes + row * (K / 2) + in_block * 64;
+    scales = c.w.scales + row * groups + in_block * PER;
+    if (ZEROS) zeros = c.w.zeros + row * groups + in_block * PER;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int in = min(g + 8 * h, N - 1 - in_tile * ROWS);  // rows beyond the last: the last
+      code_at[h] = in * (K / 2) + t * BYTES;
+      scale_at[h] = in * groups;
+    }
+  };
+  const auto load = [&](Piece<G, ZEROS>& p) {
+    if (left_in <= 0) return;
+    --left_in;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) p.load(h, codes + code_at[h], scales + scale_at[h], ZEROS ? zeros + scale_at[h] : nullptr);
+    if (++in_block == blocks) {
+      in_block = 0, ++in_tile;
+      if (left_in > 0) place();
+    } else {
+      codes += 64, scales += PER;
+      if (ZEROS) zeros += PER;
+    }
+  };
+  Piece<G, ZEROS> ring[AHEAD];
+  if (left_in > 0) place();
+#pragma unroll
+  for (int u = 0; u < AHEAD; ++u) load(ring[u]);  // on their way while the rows are made ready
+
   load_rows<G>(c, smem);
   const float2* factor = reinterpret_cast<const float2*>(smem);
   const uint4* xf = reinterpret_cast<const uint4*>(smem + align16(c.m * 8));
-  uint8_t* ring = smem + rows_bytes(K, c.m, c.cols) + warp * c.stages * STAGE;
-  float* share = reinterpret_cast<float*>(smem + rows_bytes(K, c.m, c.cols) + warps * c.stages * STAGE);
+  float* share = reinterpret_cast<float*>(smem + rows_bytes(K, c.m, c.cols));
+  __shared__ int share_tile[WARPS];
+  if (lane == 0) share_tile[warp] = -1;
 
-  const int tiles = (N + ROWS - 1) / ROWS, per_pass = warps / c.splits, split = warp % c.splits;
-  const int blocks = K / 128, kb0 = blocks * split / c.splits, kb1 = blocks * (split + 1) / c.splits;
-  const int64_t groups = K / G, last_group = (int64_t)N * groups;
-  const int first = (int)blockIdx.x * per_pass + warp / c.splits, stride = (int)gridDim.x * per_pass;
-
-  // asks for the block (tile, kb) of weights
-  const auto ask = [&](int tile, int kb, int stage) {
-    const uint32_t to = smem_u32(ring + stage * STAGE);
-    if (tile < tiles) {
+  const auto write = [&](int tile, const float (&tot)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = g + 8 * h, row = min(tile * ROWS + r, N - 1);
-        cp_async_16(to + r * 64 + (t ^ swizzle(r)) * 16, c.w.codes + (int64_t)row * (K / 2) + kb * 64 + t * 16, 16);
-      }
-      const int r = lane & 15, row = min(tile * ROWS + r, N - 1);
-      const int64_t at = row * groups + (int64_t)kb * PER;  // the row's first group in this block
-      if (lane < 16) {
-        if (PER == 4) {
-          cp_async_8(to + 1024 + r * 8, c.w.scales + at);
-        } else {  // the aligned word that holds it
-          const int64_t even = at & ~1;
-          cp_async_4(to + 1024 + r * 8, c.w.scales + even, even + 1 < last_group ? 4 : 2);
-        }
-      } else if (ZEROS) {
-        const int64_t four = at & ~3;
-        cp_async_4(to + 1152 + r * 4, c.w.zeros + four, (uint32_t)min((int64_t)4, last_group - four));
-      }
-    }
-    cp_async_commit();
-  };
-
-  int ask_tile = first, ask_kb = kb0, ask_stage = 0;
-  const auto ask_next = [&]() {
-    ask(ask_tile, ask_kb, ask_stage);
-    if (++ask_kb >= kb1) ask_kb = kb0, ask_tile += stride;
-    if (++ask_stage == c.stages) ask_stage = 0;
-  };
-  if (kb0 < kb1)
-    for (int i = 0; i < c.stages - 1; ++i) ask_next();
-
-  int stage = 0;
-  // every warp of the block makes the same number of passes
-  for (int tile = first; tile - warp / c.splits < tiles; tile += stride) {
-    float tot[NT][4] = {};
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (c.stages == 8) cp_async_wait<6>();
-      else if (c.stages == 6) cp_async_wait<4>();
-      else cp_async_wait<2>();
-      __syncwarp();  // the other lanes' copies are in, and they have read the stage that is asked for next
-      ask_next();
-      const uint8_t* st = ring + stage * STAGE;
-      if (++stage == c.stages) stage = 0;
-      float scale[2][PER];
-      uint32_t zero[2][PER];  // 1024 + zero as two fp16
+        const int row = tile * ROWS + g + 8 * h;
+        if (row >= N) continue;
+        if (c.bf16) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = g + 8 * h, row = min(tile * ROWS + r, N - 1);
-        const int64_t at = row * groups + (int64_t)kb * PER;
-        const uint32_t* sp = reinterpret_cast<const uint32_t*>(st + 1024 + r * 8);
-        if (PER == 4) {
-          const uint2 v = *reinterpret_cast<const uint2*>(sp);
-          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-          scale[h][0] = a.x, scale[h][1 % PER] = a.y, scale[h][2 % PER] = b.x, scale[h][3 % PER] = b.y;
-        } else {
-          const uint32_t v = *sp;
-          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v));
-          if (PER == 2) scale[h][0] = a.x, scale[h][1 % PER] = a.y;
-          else scale[h][0] = at & 1 ? a.y : a.x;
-        }
-        if (ZEROS) {
-          const uint32_t v = *reinterpret_cast<const uint32_t*>(st + 1152 + r * 4) >> (8 * (int)(at & 3));
-#pragma unroll
-          for (int p = 0; p < PER; ++p) zero[h][p] = __byte_perm(v, 0x64646464u, 0x4040 | p | p << 8);
-        }
-      }
-      uint32_t wa[4], wb[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = g + 8 * h, sw = swizzle(r);
-        uint32_t(&w)[4] = h ? wb : wa;
-        const uint8_t* row = st + r * 64;
-        if (G == 128) {
-          const uint4 v = *reinterpret_cast<const uint4*>(row + (t ^ sw) * 16);
-          w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else if (G == 64) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint2 v = *reinterpret_cast<const uint2*>(row + ((2 * p + (t >> 1)) ^ sw) * 16 + (t & 1) * 8);
-            w[2 * p] = v.x, w[2 * p + 1] = v.y;
+          for (int j = 0; j < 2; ++j) {
+            const int m = n * 8 + 2 * t + j;
+            if (m < c.m) c.out[(int64_t)m * N + row] = tot[n][2 * h + j] * factor[m].x * factor[m].y;
           }
         } else {
-#pragma unroll
-          for (int p = 0; p < 4; ++p) w[p] = *reinterpret_cast<const uint32_t*>(row + (p ^ sw) * 16 + t * 4);
+          const int m = n * 4 + t;
+          if (m < c.m) c.out[(int64_t)m * N + row] = (tot[n][2 * h] + tot[n][2 * h + 1]) * factor[m].x * factor[m].y;
         }
       }
+    }
+  };
+
+  int tile = tile0 + (int)(p0 / blocks), block = (int)(p0 % blocks), left = (int)(p1 - p0);
+  bool begun = block == 0;  // this warp has the tile from its first piece
+  float tot[NT][4] = {};
+  uint32_t magic;
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));  // kept in a register
+  const uint4* f = xf + block * 16 * c.cols + t;
+  int col[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) col[n] = (n * 8 + g < c.cols ? n * 8 + g : 0) * 4;
+  while (left > 0) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (left <= 0) break;
+      --left;
+      const Piece<G, ZEROS>& p = ring[u];
       float acc[NT][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         constexpr int STEP = 4 / PER;  // words of a group
-        if (i % STEP == 0) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-        }
-        const uint32_t z0 = ZEROS ? zero[0][i / STEP] : 0x64086408u, z1 = ZEROS ? zero[1][i / STEP] : 0x64086408u;
         uint32_t a[4], b[4];
-        centred(wa[i], z0, a);
-        centred(wb[i], z1, b);
-        const uint4* f = xf + (kb * 4 + i) * c.cols * 4 + t;
+        centred(p.w[0][i], p.zero(0, i / STEP), magic, a);
+        centred(p.w[1][i], p.zero(1, i / STEP), magic, b);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const int col = n * 8 + g;
-          const uint4 v = f[(col < c.cols ? col : 0) * 4];
-          mma16816(acc[n], a[0], b[0], a[1], b[1], v.x, v.y);
-          mma16816(acc[n], a[2], b[2], a[3], b[3], v.z, v.w);
+          const uint4 v = f[i * 4 * c.cols + col[n]];
+          if (i % STEP == 0) mma16816<true>(acc[n], a[0], b[0], a[1], b[1], v.x, v.y);
+          else mma16816<false>(acc[n], a[0], b[0], a[1], b[1], v.x, v.y);
+          mma16816<false>(acc[n], a[2], b[2], a[3], b[3], v.z, v.w);
         }
         if (i % STEP == STEP - 1) {
-          const int p = i / STEP;
+          const float s0 = p.scale(0, i / STEP), s1 = p.scale(1, i / STEP);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            tot[n][0] = fmaf(scale[0][p], acc[n][0], tot[n][0]);
-            tot[n][1] = fmaf(scale[0][p], acc[n][1], tot[n][1]);
-            tot[n][2] = fmaf(scale[1][p], acc[n][2], tot[n][2]);
-            tot[n][3] = fmaf(scale[1][p], acc[n][3], tot[n][3]);
+            tot[n][0] = fmaf(s0, acc[n][0], tot[n][0]);
+            tot[n][1] = fmaf(s0, acc[n][1], tot[n][1]);
+            tot[n][2] = fmaf(s1, acc[n][2], tot[n][2]);
+            tot[n][3] = fmaf(s1, acc[n][3], tot[n][3]);
           }
         }
       }
-    }
-    if (c.splits > 1) {  // the first warp of a tile adds the others' sums, in order
-      float* mine = share + (warp * 32 + lane) * (NT * 4);
-      if (split) {
+      load(ring[u]);
+      f += 16 * c.cols;
+      if (++block == blocks) {
+        if (begun) {
+          write(tile, tot);
+        } else {  // its first pieces are another warp's
+          float* mine = share + (warp * 32 + lane) * (NT * 4);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(mine + 4 * n) = make_float4(tot[n][0], tot[n][1], tot[n][2], tot[n][3]);
-      }
-      __syncthreads();
-      if (split == 0) {
-        for (int s = 1; s < c.splits; ++s) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float4 v = *reinterpret_cast<const float4*>(mine + s * 32 * (NT * 4) + 4 * n);
-            tot[n][0] += v.x, tot[n][1] += v.y, tot[n][2] += v.z, tot[n][3] += v.w;
-          }
+          for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(mine + 4 * n) = make_float4(tot[n][0], tot[n][1], tot[n][2], tot[n][3]);
+          if (lane == 0) share_tile[warp] = tile;
         }
+        block = 0, ++tile, begun = true, f = xf + t;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.0f;
       }
-      __syncthreads();
     }
-    if (split == 0 && tile < tiles) {
+  }
+  // the last tile, where it is not whole: its first warp adds the others' shares
+  const bool open = block != 0 && p1 > p0;
+  if (open && !begun) {
+    float* mine = share + (warp * 32 + lane) * (NT * 4);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) *reinterpret_cast<float4*>(mine + 4 * n) = make_float4(tot[n][0], tot[n][1], tot[n][2], tot[n][3]);
+    if (lane == 0) share_tile[warp] = tile;
+  }
+  __syncthreads();
+  if (open && begun) {
+    for (int w = warp + 1; w < WARPS; ++w) {
+      if (share_tile[w] != tile) continue;
+      const float* other = share + (w * 32 + lane) * (NT * 4);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = tile * ROWS + g + 8 * h;
-          if (row >= N) continue;
-          if (c.bf16) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int m = n * 8 + 2 * t + j;
-              if (m < c.m) c.out[(int64_t)m * N + row] = tot[n][2 * h + j] * factor[m].x * factor[m].y;
-            }
-          } else {
-            const int m = n * 4 + t;
-            if (m < c.m) c.out[(int64_t)m * N + row] = (tot[n][2 * h] + tot[n][2 * h + 1]) * factor[m].x * factor[m].y;
-          }
-        }
+        const float4 v = *reinterpret_cast<const float4*>(other + 4 * n);
+        tot[n][0] += v.x, tot[n][1] += v.y, tot[n][2] += v.z, tot[n][3] += v.w;
       }
     }
+    write(tile, tot);
   }
 }
 
+template <int NT>
+int smem_of(int K, int m, int cols) {
+  return rows_bytes(K, m, cols) + Shape<NT>::WARPS * Shape<NT>::SHARE;
+}
+
 template <int G, bool ZEROS, int NT>
-cudaError_t launch(Call c, int num_sms, cudaStream_t st) {
-  const int threads = NT <= 2 ? 256 : 512, warps = threads / 32;
-  const int rows = rows_bytes(c.w.K, c.m, c.cols);
-  c.stages = 8;
-  int smem = 0;
-  const auto total = [&]() { return rows + warps * c.stages * STAGE + (c.splits > 1 ? warps * 32 * NT * 16 : 0); };
-  const int tiles = (c.w.N + ROWS - 1) / ROWS, blocks = c.w.K / 128;
-  // warps along K: where tiles would not occupy 16 warps an SM
-  c.splits = 1;
-  while (c.splits < 8 && (int64_t)tiles * c.splits < (int64_t)num_sms * 16 && blocks >= 2 * c.splits) c.splits *= 2;
-  for (c.stages = 8; c.stages > 4 && total() > MAX_SMEM; c.stages -= 2) {
-  }
-  smem = total();
-  if (smem > MAX_SMEM) return cudaErrorInvalidValue;
+cudaError_t launch(const Call& c, int num_sms, cudaStream_t st) {
+  const int smem = smem_of<NT>(c.w.K, c.m, c.cols);
   auto kernel = w4_matmul_kernel<G, ZEROS, NT>;
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-  int per_sm = 0;
-  if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem)) return e;
-  const int passes = (tiles + warps / c.splits - 1) / (warps / c.splits);
-  const int grid = passes < num_sms * per_sm ? passes : num_sms * per_sm;
-  kernel<<<grid, threads, smem, st>>>(c);
+  const int per_sm = min(Shape<NT>::BLOCKS, max(1, 228 * 1024 / (smem + 1024 + 64)));
+  const int tiles = (c.w.N + ROWS - 1) / ROWS;
+  kernel<<<min(tiles, num_sms * per_sm), Shape<NT>::THREADS, smem, st>>>(c);
   return cudaGetLastError();
 }
 
@@ -375,13 +393,14 @@ cudaError_t launch_w4_matmul(const W4& w, const void* x, bool bf16, int64_t M, f
   // rows of a launch: at most 64 columns, and what leaves the rings their place beside the fragments
   int most = 64 / parts;
   const auto fits = [&](int m) {
-    const int cols = m * parts, nt = cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8, warps = nt <= 2 ? 8 : 16;
-    return rows_bytes(w.K, m, cols) + warps * 4 * STAGE + warps * 32 * nt * 16 <= MAX_SMEM;
+    const int cols = m * parts;
+    return (cols <= 8 ? smem_of<1>(w.K, m, cols) : cols <= 16 ? smem_of<2>(w.K, m, cols)
+            : cols <= 32 ? smem_of<4>(w.K, m, cols) : smem_of<8>(w.K, m, cols)) <= MAX_SMEM - 1024;
   };
   while (most > 1 && !fits(most)) --most;
   for (int64_t m0 = 0; m0 < M; m0 += most) {
     const int m = (int)(M - m0 < most ? M - m0 : most);
-    Call c{w, nullptr, out + m0 * w.N, m, m * parts, 1, 8, bf16};
+    Call c{w, nullptr, out + m0 * w.N, m, m * parts, bf16};
     c.x = bf16 ? static_cast<const void*>(static_cast<const __nv_bfloat16*>(x) + m0 * w.K)
                : static_cast<const void*>(static_cast<const float*>(x) + m0 * w.K);
     const cudaError_t e = w.group == 128 ? by_zeros<128>(c, num_sms, st)
