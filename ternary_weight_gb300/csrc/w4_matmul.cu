@@ -100,24 +100,31 @@ __device__ __forceinline__ void load_rows(const Call& c, uint8_t* smem) {
       x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
   };
-  // a row's power of two: its largest number comes to [2^14, 2^15). All threads look for it: 16 lanes have
-  // numbers of the same row
-  const int octets = K / 8;
+  // A row's power of two: its largest number comes to [2^14, 2^15). Warps share rows where there are more of them; the
+  // loads of a step do not wait for each other.
+  constexpr int STEP = 4;
+  const int octets = K / 8, warp = tid / 32, warps = threads / 32;
+  int per_row = 1;
+  while (per_row * 2 * c.m <= warps) per_row *= 2;
+  const int first = warp / per_row, rows_a_step = warps / per_row, o0 = (warp % per_row) * 32 + lane, stride = per_row * 32;
   uint32_t* tops = reinterpret_cast<uint32_t*>(xf);
   for (int m = tid; m < c.m; m += threads) tops[m] = 0;
   __syncthreads();
-  for (int i = tid; i - lane < c.m * octets; i += threads) {
-    const int m = i / octets, k = (i - m * octets) * 8;
+  for (int m = first; m < c.m; m += rows_a_step) {
     uint32_t top = 0;
-    if (m < c.m) {
-      float x[8];
-      eight(m, k, x);
+    for (int o = o0; o - lane < octets; o += STEP * stride) {
+      float x[STEP][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+      for (int i = 0; i < STEP; ++i)
+        if (o + i * stride < octets) eight(m, (o + i * stride) * 8, x[i]);
+#pragma unroll
+      for (int i = 0; i < STEP; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (o + i * stride < octets) top = max(top, __float_as_uint(x[i][j]) & 0x7fffffffu);
     }
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane % 16 == 0 && m < c.m) atomicMax(&tops[m], top);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) atomicMax(&tops[m], top);
   }
   __syncthreads();
   for (int m = tid; m < c.m; m += threads) {
@@ -128,27 +135,34 @@ __device__ __forceinline__ void load_rows(const Call& c, uint8_t* smem) {
     factor[m] = make_float2(__int_as_float((half + 127) << 23), __int_as_float((-e - half + 127) << 23));
   }
   __syncthreads();
-  for (int i = tid; i < c.m * octets; i += threads) {
-    const int m = i / octets, o = i - m * octets, k = o * 8;
-    float x[8];
-    eight(m, k, x);
+  for (int m = first; m < c.m; m += rows_a_step) {
     const float2 f = factor[m];
     // up = 1 / (f.x f.y): its exponent from theirs
     const int e = -((int)(__float_as_uint(f.x) >> 23) - 127) - ((int)(__float_as_uint(f.y) >> 23) - 127);
     const float up = __int_as_float((e + 127) << 23);
-    const int block = k >> 7, in = k & 127;
-    const int t = G == 128 ? in >> 5 : G == 64 ? (in >> 4) & 3 : (in >> 3) & 3;
-    const int word = G == 128 ? (in >> 3) & 3 : G == 64 ? (in >> 6) * 2 + ((in >> 3) & 1) : in >> 5;
-    float hi[8], lo[8];
+    for (int o = o0; o < octets; o += STEP * stride) {
+      float x[STEP][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      hi[j] = x[j] * up;
-      lo[j] = hi[j] - __half2float(__float2half_rn(hi[j]));
+      for (int i = 0; i < STEP; ++i)
+        if (o + i * stride < octets) eight(m, (o + i * stride) * 8, x[i]);
+#pragma unroll
+      for (int i = 0; i < STEP; ++i) {
+        if (o + i * stride >= octets) break;
+        const int k = (o + i * stride) * 8, block = k >> 7, in = k & 127;
+        const int t = G == 128 ? in >> 5 : G == 64 ? (in >> 4) & 3 : (in >> 3) & 3;
+        const int word = G == 128 ? (in >> 3) & 3 : G == 64 ? (in >> 6) * 2 + ((in >> 3) & 1) : in >> 5;
+        float hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          hi[j] = x[i][j] * up;
+          lo[j] = hi[j] - __half2float(__float2half_rn(hi[j]));
+        }
+        uint4* to = xf + ((block * 4 + word) * c.cols + m * parts) * 4 + t;
+        *to = make_uint4(pack_half2(hi[0], hi[4]), pack_half2(hi[1], hi[5]), pack_half2(hi[2], hi[6]), pack_half2(hi[3], hi[7]));
+        if (parts == 2)
+          to[4] = make_uint4(pack_half2(lo[0], lo[4]), pack_half2(lo[1], lo[5]), pack_half2(lo[2], lo[6]), pack_half2(lo[3], lo[7]));
+      }
     }
-    uint4* to = xf + ((block * 4 + word) * c.cols + m * parts) * 4 + t;
-    *to = make_uint4(pack_half2(hi[0], hi[4]), pack_half2(hi[1], hi[5]), pack_half2(hi[2], hi[6]), pack_half2(hi[3], hi[7]));
-    if (parts == 2)
-      to[4] = make_uint4(pack_half2(lo[0], lo[4]), pack_half2(lo[1], lo[5]), pack_half2(lo[2], lo[6]), pack_half2(lo[3], lo[7]));
   }
   __syncthreads();
 }
@@ -198,14 +212,14 @@ struct Piece {
 // NT: eights of columns
 template <int NT>
 struct Shape {
-  static constexpr int WARPS = NT == 1 ? 8 : 16, THREADS = WARPS * 32;
-  static constexpr int BLOCKS = NT == 1 ? 2 : 1;     // resident blocks of an SM
-  static constexpr int AHEAD = NT == 1 ? 4 : NT == 2 ? 3 : 2;      // pieces on their way
-  static constexpr int SHARE = 32 * NT * 16;         // bytes of a warp's share of a tile
+  static constexpr int WARPS = 16, THREADS = WARPS * 32;  // one block an SM
+  static constexpr int AHEAD = NT == 1 ? 6 : NT == 2 ? 4 : 2;  // pieces on their way
+  static constexpr int EARLY = NT == 1 ? 3 : AHEAD;            // of them asked for before the rows are made ready
+  static constexpr int SHARE = 32 * NT * 16;                   // bytes of a warp's share of a tile
 };
 
 template <int G, bool ZEROS, int NT>
-__global__ void __launch_bounds__(Shape<NT>::THREADS, Shape<NT>::BLOCKS) w4_matmul_kernel(Call c) {
+__global__ void __launch_bounds__(Shape<NT>::THREADS, 1) w4_matmul_kernel(Call c) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int PER = 128 / G, WARPS = Shape<NT>::WARPS, AHEAD = Shape<NT>::AHEAD, BYTES = G == 128 ? 16 : G == 64 ? 8 : 4;
   const int K = c.w.K, N = c.w.N, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
@@ -248,9 +262,11 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, Shape<NT>::BLOCKS) w4_matm
   Piece<G, ZEROS> ring[AHEAD];
   if (left_in > 0) place();
 #pragma unroll
-  for (int u = 0; u < AHEAD; ++u) load(ring[u]);  // on their way while the rows are made ready
+  for (int u = 0; u < Shape<NT>::EARLY; ++u) load(ring[u]);  // on their way while the rows are made ready
 
   load_rows<G>(c, smem);
+#pragma unroll
+  for (int u = Shape<NT>::EARLY; u < AHEAD; ++u) load(ring[u]);
   const float2* factor = reinterpret_cast<const float2*>(smem);
   const uint4* xf = reinterpret_cast<const uint4*>(smem + align16(c.m * 8));
   float* share = reinterpret_cast<float*>(smem + rows_bytes(K, c.m, c.cols));
@@ -368,9 +384,8 @@ cudaError_t launch(const Call& c, int num_sms, cudaStream_t st) {
   const int smem = smem_of<NT>(c.w.K, c.m, c.cols);
   auto kernel = w4_matmul_kernel<G, ZEROS, NT>;
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-  const int per_sm = min(Shape<NT>::BLOCKS, max(1, 228 * 1024 / (smem + 1024 + 64)));
   const int tiles = (c.w.N + ROWS - 1) / ROWS;
-  kernel<<<min(tiles, num_sms * per_sm), Shape<NT>::THREADS, smem, st>>>(c);
+  kernel<<<min(tiles, num_sms), Shape<NT>::THREADS, smem, st>>>(c);
   return cudaGetLastError();
 }
 
@@ -398,6 +413,10 @@ cudaError_t launch_w4_matmul(const W4& w, const void* x, bool bf16, int64_t M, f
             : cols <= 32 ? smem_of<4>(w.K, m, cols) : smem_of<8>(w.K, m, cols)) <= MAX_SMEM - 1024;
   };
   while (most > 1 && !fits(most)) --most;
+  if (M > most) {  // launches of like size: fewer columns each cost less
+    const int64_t launches = (M + most - 1) / most;
+    most = (int)((M + launches - 1) / launches);
+  }
   for (int64_t m0 = 0; m0 < M; m0 += most) {
     const int m = (int)(M - m0 < most ? M - m0 : most);
     Call c{w, nullptr, out + m0 * w.N, m, m * parts, bf16};
