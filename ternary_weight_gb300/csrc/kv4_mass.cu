@@ -14,9 +14,9 @@
 // shifted; q' carries the 2^-4): 5 instructions for a word of 8 codes, sums exact in fp32. Lane t of four takes 16
 // bytes of a key row (8 with D = 64), so a warp's loads of a tile are contiguous, straight from the cache.
 //
-// Few columns (64 at most): both kernels are bound by the keys' bytes, the second kernel's mostly from L2. Many: by
-// the products; then the second kernel's blocks keep their tiles' codes and go through a share of the columns, and a third
-// kernel adds up the shares.
+// Few columns (16 at most): both kernels are bound by the keys' bytes, the second kernel's mostly from L2. Many: by
+// the products and exponentials; columns go in blocks of 64 whose fragments the first kernel leaves in the workspace, the second
+// kernel's blocks keep their tiles' codes and go through a share of the columns, and a third one adds up the shares.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -45,6 +45,7 @@ struct Plan {
 struct Stats {
   float2* part;  // unit, block, chunk, column: (M, L)
   float* votes;  // unit, group, share, WARPS x TILE
+  uint8_t* slabs;  // unit, block
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -414,44 +415,362 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_votes(Kv4 c
   if (bad) record_device_error(kErrRange);
 }
 
-// ------------------------------------------------------------- second and third kernel, many columns
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, Kv4Mass ms, Plan pl, Stats st) {
-  __shared__ Shared<D, NT> sh;
-  constexpr int COLS = NT * 8, PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
+// ------------------------------------------------------------- many columns
+// A block of 64 columns as the first kernel leaves it for the second: fragments and constants, copied as they are.
+constexpr int COLS = 64, EIGHTS = COLS / 8;
+template <int D>
+struct __align__(16) Slab {
+  uint4 frag[EIGHTS][D / 32][32];
+  float a[COLS], b[COLS];  // x = step (a raw) + base b
+  int p[COLS];             // the row's position
+  float m[COLS], l[COLS];  // its maximum, and the inverse of its sum
+};
+// A tile's codes as A fragments: word, then the four registers of its two products.
+template <int D>
+struct Unpacked {
+  uint32_t u[2][D / 32][8];
+  float2 par[2][2];
+  __device__ __forceinline__ explicit Unpacked(const Codes<D>& k) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t a = k.w[mt][0][i], b = k.w[mt][1][i], a8 = a >> 8, b8 = b >> 8;
+        uint32_t(&v)[8] = u[mt][i];
+        v[0] = a & 0x000f000fu, v[1] = b & 0x000f000fu, v[2] = a & 0x00f000f0u, v[3] = b & 0x00f000f0u;
+        v[4] = a8 & 0x000f000fu, v[5] = b8 & 0x000f000fu, v[6] = a8 & 0x00f000f0u, v[7] = b8 & 0x00f000f0u;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) par[mt][h] = params(k.par[mt][h]);
+    }
+  }
+};
+
+__device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Scores of an eight of columns against a tile: x[v][e] of the lane's tokens v (mt * 2 + h) and columns 2 t + e (fp32
+// queries: e = 0 alone).
+template <int D, bool F32>
+__device__ __forceinline__ void scores(const Unpacked<D>& k, const Slab<D>& sl, int n, int lane, float (&x)[4][2]) {
+  float d[2][4] = {};
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint4 f = sl.frag[n][i][lane];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) mma16816(d[mt], k.u[mt][i][0], k.u[mt][i][1], k.u[mt][i][2], k.u[mt][i][3], f.x, f.y);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) mma16816(d[mt], k.u[mt][i][4], k.u[mt][i][5], k.u[mt][i][6], k.u[mt][i][7], f.z, f.w);
+  }
+  const int col = n * 8 + 2 * (lane & 3);
+  const float2 a = *reinterpret_cast<const float2*>(&sl.a[col]), b = *reinterpret_cast<const float2*>(&sl.b[col]);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int mt = v >> 1, h = v & 1;
+    const float2 par = k.par[mt][h];
+    if (F32) {
+      x[v][0] = __fmaf_rn(par.x, __fmul_rn(a.x, d[mt][2 * h] + d[mt][2 * h + 1]), __fmul_rn(par.y, b.x));
+    } else {
+      const uint64_t y = fma2(f2pack(par.x, par.x), mul2(f2pack(a.x, a.y), f2pack(d[mt][2 * h], d[mt][2 * h + 1])),
+                              mul2(f2pack(par.y, par.y), f2pack(b.x, b.y)));
+      const float2 z = f2unpack(y);
+      x[v][0] = z.x, x[v][1] = z.y;
+    }
+  }
+}
+
+// The fragments and constants of columns [col0, col0 + 64): D / 8 lanes a row, 8 numbers each, all loads first.
+template <int D, bool F32>
+__device__ __forceinline__ void load_slab(const Kv4Attn& a, const Rows& r, int64_t col0, Slab<D>& sl) {
+  constexpr int W = D / 8, PARTS = F32 ? 2 : 1, ROWS = COLS / PARTS, PER = THREADS / W, TIMES = ROWS / PER;
+  static_assert(ROWS % PER == 0, "every thread takes as many rows");
+  const int w = threadIdx.x % W, k0 = threadIdx.x / W, rows = r.votes * a.share, row0 = (int)(col0 / PARTS);
+  float x[TIMES][8];
+#pragma unroll
+  for (int k = 0; k < TIMES; ++k) {
+    const int row = row0 + k0 + k * PER, i = row / a.share;
+    const bool there = row < rows;
+    const int64_t at = there ? (int64_t)(r.s.q0 + r.s.n - r.votes + i) * a.q_stride + (int64_t)(r.h * a.share + row - i * a.share) * D + w : 0;
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+      x[k][n] = !there ? 0.0f
+                : F32  ? static_cast<const float*>(a.q)[at + W * n]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + W * n]);
+  }
+#pragma unroll
+  for (int k = 0; k < TIMES; ++k) {
+    const int row = row0 + k0 + k * PER;
+    float sum = 0.0f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) sum += x[k][n], top = max(top, __float_as_uint(x[k][n]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = W / 2; o >= 1; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);
+    e = e > 127 ? 127 : e < -113 ? -113 : e;
+    const float up = __int_as_float((e + 127) << 23);
+    constexpr int WORDS = W / 4;
+    const int t = w / WORDS, word = w % WORDS, col = (k0 + k * PER) * PARTS;
+    float hi[8], lo[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      hi[n] = x[k][n] * up * (n & 1 ? 0.0625f : 1.0f);
+      lo[n] = hi[n] - __half2float(__float2half_rn(hi[n]));
+    }
+    sl.frag[col >> 3][word][(col & 7) * 4 + t] =
+        make_uint4(pack_half2(hi[0], hi[4]), pack_half2(hi[1], hi[5]), pack_half2(hi[2], hi[6]), pack_half2(hi[3], hi[7]));
+    if (F32)
+      sl.frag[col >> 3][word][((col & 7) + 1) * 4 + t] =
+          make_uint4(pack_half2(lo[0], lo[4]), pack_half2(lo[1], lo[5]), pack_half2(lo[2], lo[6]), pack_half2(lo[3], lo[7]));
+    if (w == 0) {
+      const float c1 = __fmul_rn(a.scale, kLog2e);
+      const int f = 24 - e, half = f / 2;
+      const float ca = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) {
+        sl.a[col + j] = ca, sl.b[col + j] = __fmul_rn(c1, sum);
+        sl.p[col + j] = row < rows ? r.position(row / a.share) : -1;
+        sl.m[col + j] = sl.l[col + j] = 0.0f;
+      }
+    }
+  }
+}
+
+// First kernel: each column's maximum and sum over a chunk of tiles. A warp's running ones lie in shared memory.
+template <int D>
+struct __align__(16) RowsShared {
+  Slab<D> sl;
+  float4 run[WARPS][EIGHTS][32];
+  float2 part[WARPS][COLS];
+};
+template <int D, bool F32>
+__global__ void __launch_bounds__(THREADS, 2) kv4_mass_rows_many(Kv4 c, Kv4Attn a, int voters, Plan pl, Stats st) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  RowsShared<D>& sh = *reinterpret_cast<RowsShared<D>*>(smem);
+  constexpr int PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   bool bad = false;
-  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.groups * pl.shares;
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks * pl.chunks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t rest = item / pl.chunks;
+    const int chunk = (int)(item - rest * pl.chunks), unit = (int)(rest / pl.blocks), block = (int)(rest - (int64_t)unit * pl.blocks);
+    const Rows r = rows_of(c, unit, voters, &bad);
+    const int64_t rows = (int64_t)r.votes * a.share, col0 = (int64_t)block * COLS;
+    if (col0 >= rows * PARTS) continue;
+    const int tile0 = chunk * pl.chunk, tile1 = min(tile0 + pl.chunk, (r.s.len + TILE - 1) / TILE);
+    const int first = r.position((int)(col0 / PARTS) / a.share), last = r.position((int)((min((col0 + COLS) / PARTS, rows) - 1) / a.share));
+    const bool some = tile0 < tile1 && seen(a, first, last, tile0 * TILE, (tile1 - tile0) * TILE) != 0;
+    if (!some && chunk) {
+      for (int i = threadIdx.x; i < COLS; i += THREADS) st.part[item * COLS + i] = make_float2(kNegInf, 0.0f);
+      continue;
+    }
+    int id = 0;
+    const int mine = tile0 + warp + lane * WARPS;
+    if (mine < tile1) {
+      id = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
+      if (id < 0 || id >= c.n_pages) bad = true, id = 0;
+    }
+    Codes<D> cur;
+    const auto load = [&](int k) {
+      const int from = __shfl_sync(0xffffffffu, id, k);
+      const int tile = tile0 + warp + k * WARPS;
+      if (tile < tile1) cur.load(c.pages + ((int64_t)from * c.kv_heads + r.h) * BLK, tile, g, t);
+    };
+    load(0);
+    load_slab<D, F32>(a, r, col0, sh.sl);
+#pragma unroll
+    for (int n = 0; n < EIGHTS; ++n) sh.run[warp][n][lane] = make_float4(kNegInf, 0.0f, kNegInf, 0.0f);
+    __syncthreads();
+    const int eights = (int)min((int64_t)EIGHTS, (rows * PARTS - col0 + 7) / 8);
+    for (int k = 0, tile = tile0 + warp; some && tile < tile1; ++k, tile += WARPS) {
+      const Unpacked<D> now(cur);
+      if (k < 31) load(k + 1);
+      const int j0 = tile * TILE, sees = seen(a, first, last, j0, TILE);
+      if (sees == 0) continue;
+#pragma unroll 1
+      for (int n = 0; n < eights; ++n) {
+        float x[4][2];
+        scores<D, F32>(now, sh.sl, n, lane, x);
+        float4 run = sh.run[warp][n][lane];
+#pragma unroll
+        for (int e = 0; e < (F32 ? 1 : 2); ++e) {
+          if (sees == 1) {
+            const int p = sh.sl.p[n * 8 + 2 * t + e];
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (!visible(a, p, j0 + token_of((v >> 1) * 16 + (v & 1) * 8 + g))) x[v][e] = kNegInf;
+          }
+          float &m = e ? run.z : run.x, &l = e ? run.w : run.y;
+          const float top = fmaxf(fmaxf(fmaxf(x[0][e], x[1][e]), fmaxf(x[2][e], x[3][e])), m), from = top == kNegInf ? 0.0f : top;
+          l = fmaf(l, exp2_approx(m - from), (exp2_approx(x[0][e] - from) + exp2_approx(x[1][e] - from)) + (exp2_approx(x[2][e] - from) + exp2_approx(x[3][e] - from)));
+          m = top;
+        }
+        sh.run[warp][n][lane] = run;
+      }
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int n = 0; n < EIGHTS; ++n) {
+      const float4 run = sh.run[warp][n][lane];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = e ? run.z : run.x, l = e ? run.w : run.y;
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+        if (g == 0) sh.part[warp][n * 8 + 2 * t + e] = make_float2(m, l);
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < COLS; i += THREADS) {
+      float2 v = sh.part[0][i];
+      for (int w = 1; w < WARPS; ++w) join(v.x, v.y, sh.part[w][i].x, sh.part[w][i].y);
+      st.part[item * COLS + i] = v;
+      sh.sl.m[i] = v.x == kNegInf ? 0.0f : v.x;  // what the second kernel needs where there is one chunk
+      sh.sl.l[i] = v.y == 0.0f ? 0.0f : __frcp_rn(v.y);
+    }
+    __syncthreads();
+    if (chunk == 0) {
+      uint4* to = reinterpret_cast<uint4*>(st.slabs + rest * (int64_t)sizeof(Slab<D>));
+      for (int i = threadIdx.x; i < (int)(sizeof(Slab<D>) / 16); i += THREADS) to[i] = reinterpret_cast<const uint4*>(&sh.sl)[i];
+    }
+    __syncthreads();  // the next item's columns
+  }
+  if (bad) record_device_error(kErrRange);
+}
+
+// Joins the chunks' maxima and sums of each block of columns (more than one chunk).
+template <int D>
+__global__ void __launch_bounds__(COLS) kv4_mass_sums(Kv4 c, Kv4Attn a, int voters, Plan pl, Stats st) {
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int unit = (int)(item / pl.blocks), block = (int)(item - (int64_t)unit * pl.blocks);
+    bool bad = false;
+    const Rows r = rows_of(c, unit, voters, &bad);
+    if ((int64_t)block * COLS >= (int64_t)r.votes * a.share * pl.parts) continue;
+    const int chunks = ((r.s.len + TILE - 1) / TILE + pl.chunk - 1) / pl.chunk;
+    float m = kNegInf, l = 0.0f;
+    for (int k = 0; k < chunks; ++k) {
+      const float2 v = st.part[(item * pl.chunks + k) * COLS + threadIdx.x];
+      join(m, l, v.x, v.y);
+    }
+    Slab<D>& sl = *reinterpret_cast<Slab<D>*>(st.slabs + item * (int64_t)sizeof(Slab<D>));
+    sl.m[threadIdx.x] = m == kNegInf ? 0.0f : m;
+    sl.l[threadIdx.x] = l == 0.0f ? 0.0f : __frcp_rn(l);
+  }
+}
+
+// Second kernel: a warp keeps its tile's codes and goes through a share of the blocks of columns, the next one's copy under
+// way while it computes.
+template <int D, bool F32>
+__global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, Kv4Mass ms, Plan pl, Stats st) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Slab<D>* const slabs = reinterpret_cast<Slab<D>*>(smem);
+  constexpr int PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D), PIECES = (int)(sizeof(Slab<D>) / 16);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+  bool bad = false;
+  // the groups of tiles outermost: with a causal mask the first ones have most to do
+  const int units = c.batch * c.kv_heads;
+  const int64_t items = (int64_t)units * pl.groups * pl.shares;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t rest = item / pl.shares;
-    const int share = (int)(item - rest * pl.shares), unit = (int)(rest / pl.groups), group = (int)(rest - (int64_t)unit * pl.groups);
+    const int share = (int)(item - rest * pl.shares), group = (int)(rest / units), unit = (int)(rest - (int64_t)group * units);
     const Rows r = rows_of(c, unit, ms.voters, &bad);
-    const int rows = r.votes * a.share, all = (r.s.len + TILE - 1) / TILE, tile = group * WARPS + warp;
+    const int64_t rows = (int64_t)r.votes * a.share;
+    const int all = (r.s.len + TILE - 1) / TILE, tile = group * WARPS + warp;
     if (rows == 0 || group * WARPS >= all) continue;
-    Codes<D> k;
+    const int blocks = (int)((rows * PARTS + COLS - 1) / COLS);
+    const auto ends = [&](int block, int* first, int* last) {
+      const int64_t col0 = (int64_t)block * COLS;
+      *first = r.position((int)(col0 / PARTS) / a.share);
+      *last = r.position((int)((min((col0 + COLS) / PARTS, rows) - 1) / a.share));
+    };
+    // the next block of this share from `block` on that sees any of the tiles
+    const auto next = [&](int block) {
+      for (; block < blocks; block += pl.shares) {
+        int first, last;
+        ends(block, &first, &last);
+        if (seen(a, first, last, group * WARPS * TILE, WARPS * TILE)) break;
+      }
+      return block;
+    };
+    const auto copy = [&](int block, int buf) {
+      if (block < blocks) {
+        const uint8_t* from = st.slabs + ((int64_t)unit * pl.blocks + block) * (int64_t)sizeof(Slab<D>);
+        const uint32_t to = smem_u32(&slabs[buf]);
+        for (int i = threadIdx.x; i < PIECES; i += THREADS) cp_async_16(to + i * 16, from + i * 16, 16);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int block = next(share), buf = 0;
+    copy(block, 0);
+    Codes<D> k{};
     bool there = tile < all;
     if (there) {
       const int id = c.page_table[(int64_t)r.b * c.max_pages + tile / 2];
       if (id < 0 || id >= c.n_pages) bad = true, there = false;
       else k.load(c.pages + ((int64_t)id * c.kv_heads + r.h) * BLK, tile, g, t);
     }
+    const Unpacked<D> now(k);
     float votes[4] = {};
-    const int chunks = (all + pl.chunk - 1) / pl.chunk;
-    for (int block = share; block * COLS < rows * PARTS; block += pl.shares) {
-      const int col0 = block * COLS, first = r.position(col0 / PARTS / a.share);
-      const int last = r.position((min((col0 + COLS) / PARTS, rows) - 1) / a.share);
-      if (seen(a, first, last, group * WARPS * TILE, WARPS * TILE) == 0) continue;
-      load_columns<D, NT, F32>(a, r, col0, sh);
+    while (block < blocks) {
+      const int then = next(block + pl.shares);
+      copy(then, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
-      load_sums<D, NT, F32>(pl, st, unit, block, chunks, sh);
-      __syncthreads();
-      const int sees = there ? seen(a, first, last, tile * TILE, TILE) : 0;
-      if (sees) add_votes<D, NT, F32>(a, k, sh, min(NT, (rows * PARTS - col0 + 7) / 8), tile * TILE, sees, votes);
-      __syncthreads();
+      int first, last;
+      ends(block, &first, &last);
+      const int j0 = tile * TILE, sees = there ? seen(a, first, last, j0, TILE) : 0;
+      const Slab<D>& sl = slabs[buf];
+      const int eights = (int)min((int64_t)EIGHTS, (rows * PARTS - (int64_t)block * COLS + 7) / 8);
+      if (sees) {
+#pragma unroll 1
+        for (int n = 0; n < eights; ++n) {
+          float x[4][2];
+          scores<D, F32>(now, sl, n, lane, x);
+          const int col = n * 8 + 2 * t;
+          const float2 m = *reinterpret_cast<const float2*>(&sl.m[col]), l = *reinterpret_cast<const float2*>(&sl.l[col]);
+          const int2 p = *reinterpret_cast<const int2*>(&sl.p[col]);
+#pragma unroll
+          for (int e = 0; e < (F32 ? 1 : 2); ++e) {
+            if ((e ? p.y : p.x) < 0) continue;  // no row, or one that sees nothing
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float w = exp2_approx(x[v][e] - (e ? m.y : m.x));
+              if (sees == 2 || visible(a, e ? p.y : p.x, j0 + token_of((v >> 1) * 16 + (v & 1) * 8 + g)))
+                votes[v] = fmaf(w, e ? l.y : l.x, votes[v]);
+            }
+          }
+        }
+      }
+      __syncthreads();  // the buffer is copied into again
+      block = then, buf ^= 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     const float got = gather_votes(votes, t);
     const int row = (t >> 1) * 16 + (t & 1) * 8 + g;
-    st.votes[(item * WARPS + warp) * TILE + token_of(row)] = got;
+    st.votes[((((int64_t)unit * pl.groups + group) * pl.shares + share) * WARPS + warp) * TILE + token_of(row)] = got;
+    __syncthreads();
   }
   if (bad) record_device_error(kErrRange);
 }
@@ -482,7 +801,7 @@ Plan plan_of(const Kv4& c, int share, int voters, bool f32, int num_sms) {
   p.votes = voters < c.max_q ? voters : c.max_q;
   p.votes = p.votes < c.total_q ? p.votes : c.total_q;
   const int64_t cols = (int64_t)p.votes * share * p.parts, units = (int64_t)c.batch * c.kv_heads;
-  p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 8;
+  p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : EIGHTS;
   p.blocks = (int)((cols + p.nt * 8 - 1) / (p.nt * 8));
   p.tiles = (c.max_kv + TILE - 1) / TILE;
   // a chunk: as many tiles as leave each SM several blocks
@@ -490,9 +809,10 @@ Plan plan_of(const Kv4& c, int share, int voters, bool f32, int num_sms) {
   per = per < 1 ? 1 : per > MAX_CHUNK / WARPS ? MAX_CHUNK / WARPS : per;
   p.chunk = (int)per * WARPS;
   p.chunks = (p.tiles + p.chunk - 1) / p.chunk;
-  if (p.blocks > 1) {
+  if (p.nt == EIGHTS) {
     p.groups = (p.tiles + WARPS - 1) / WARPS;
-    int64_t s = ((int64_t)num_sms * 4 + units * p.groups - 1) / (units * p.groups);
+    const int64_t all = units * (p.groups > 0 ? p.groups : 1);
+    const int64_t s = ((int64_t)num_sms * 4 + all - 1) / all;
     p.shares = (int)(s < 1 ? 1 : s > p.blocks ? p.blocks : s);
   }
   return p;
@@ -501,27 +821,41 @@ int64_t part_bytes(const Kv4& c, const Plan& p) { return align256((int64_t)c.bat
 int64_t votes_bytes(const Kv4& c, const Plan& p) {
   return p.shares ? align256((int64_t)c.batch * c.kv_heads * p.groups * p.shares * WARPS * TILE * 4) : 0;
 }
+int64_t slabs_bytes(const Kv4& c, const Plan& p, int dim) {
+  return p.shares ? align256((int64_t)c.batch * c.kv_heads * p.blocks * (int64_t)(dim == 128 ? sizeof(Slab<128>) : sizeof(Slab<64>))) : 0;
+}
 
 template <int D, int NT, bool F32>
-cudaError_t launch(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
+cudaError_t launch_few(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
   const int64_t units = (int64_t)c.batch * c.kv_heads;
-  if (p.tiles == 0) return cudaSuccess;
-  kv4_mass_rows<D, NT, F32><<<grid_of(units * p.blocks * p.chunks), THREADS, 0, st>>>(c, a, m.voters, p, s);
+  kv4_mass_rows<D, NT, F32><<<grid_of(units * p.chunks), THREADS, 0, st>>>(c, a, m.voters, p, s);
   if (cudaError_t e = cudaGetLastError()) return e;
-  if (p.shares == 0) {
-    kv4_mass_votes<D, NT, F32><<<grid_of(units * p.chunks), THREADS, 0, st>>>(c, a, m, p, s);
-    return cudaGetLastError();
+  kv4_mass_votes<D, NT, F32><<<grid_of(units * p.chunks), THREADS, 0, st>>>(c, a, m, p, s);
+  return cudaGetLastError();
+}
+template <int D, bool F32>
+cudaError_t launch_many(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
+  const int64_t units = (int64_t)c.batch * c.kv_heads;
+  const int rows_smem = (int)sizeof(RowsShared<D>), shares_smem = 2 * (int)sizeof(Slab<D>);
+  if (cudaError_t e = cudaFuncSetAttribute(kv4_mass_rows_many<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem)) return e;
+  if (cudaError_t e = cudaFuncSetAttribute(kv4_mass_shares<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, shares_smem)) return e;
+  kv4_mass_rows_many<D, F32><<<grid_of(units * p.blocks * p.chunks), THREADS, rows_smem, st>>>(c, a, m.voters, p, s);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  if (p.chunks > 1) {
+    kv4_mass_sums<D><<<grid_of(units * p.blocks), COLS, 0, st>>>(c, a, m.voters, p, s);
+    if (cudaError_t e = cudaGetLastError()) return e;
   }
-  kv4_mass_shares<D, NT, F32><<<grid_of(units * p.groups * p.shares), THREADS, 0, st>>>(c, a, m, p, s);
+  kv4_mass_shares<D, F32><<<grid_of(units * p.groups * p.shares), THREADS, shares_smem, st>>>(c, a, m, p, s);
   if (cudaError_t e = cudaGetLastError()) return e;
   kv4_mass_join<<<grid_of(units * p.groups), THREADS, 0, st>>>(c, m, p, s);
   return cudaGetLastError();
 }
 template <int D, bool F32>
 cudaError_t by_columns(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
-  if (p.nt == 1) return launch<D, 1, F32>(c, a, m, p, s, st);
-  if (p.nt == 2) return launch<D, 2, F32>(c, a, m, p, s, st);
-  return launch<D, 8, F32>(c, a, m, p, s, st);
+  if (p.tiles == 0) return cudaSuccess;
+  if (p.nt == 1) return launch_few<D, 1, F32>(c, a, m, p, s, st);
+  if (p.nt == 2) return launch_few<D, 2, F32>(c, a, m, p, s, st);
+  return launch_many<D, F32>(c, a, m, p, s, st);
 }
 
 }  // namespace
@@ -530,14 +864,15 @@ int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters) {
   int64_t most = 0;  // whatever the queries' type
   for (int f32 = 0; f32 < 2; ++f32) {
     const Plan p = plan_of(c, q_heads / c.kv_heads, voters, f32, 152);
-    const int64_t n = part_bytes(c, p) + votes_bytes(c, p);
+    const int64_t n = part_bytes(c, p) + votes_bytes(c, p) + slabs_bytes(c, p, dim);
     most = n > most ? n : most;
   }
   return most;
 }
 cudaError_t launch_kv4_mass(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, void* ws, int num_sms, cudaStream_t st) {
   const Plan p = plan_of(c, a.share, m.voters, !a.bf16, 152);
-  const Stats s{static_cast<float2*>(ws), reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + part_bytes(c, p))};
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  const Stats s{reinterpret_cast<float2*>(at), reinterpret_cast<float*>(at + part_bytes(c, p)), at + part_bytes(c, p) + votes_bytes(c, p)};
   if (dim == 128) return a.bf16 ? by_columns<128, false>(c, a, m, p, s, st) : by_columns<128, true>(c, a, m, p, s, st);
   return a.bf16 ? by_columns<64, false>(c, a, m, p, s, st) : by_columns<64, true>(c, a, m, p, s, st);
 }
