@@ -416,36 +416,54 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_votes(Kv4 c
 }
 
 // ------------------------------------------------------------- many columns
+constexpr float kLeastA = 7.888609052210118e-31f, kMostA = 3.4028234663852886e38f;  // 2^-100, the greatest
+// what the second kernel needs of a row: -M (0 where it sees nothing) and 1 / L, twice
+__device__ __forceinline__ float4 finished(float m, float l) {
+  const float minus = m == kNegInf ? 0.0f : -m, inv = l == 0.0f ? 0.0f : __frcp_rn(l);
+  return make_float4(minus, minus, inv, inv);
+}
+// the first of a chain of products: the sum begins at 0
+__device__ __forceinline__ void mma_first(float (&d)[4], uint4 a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// Here the columns are the rows of m16n8k16 and the tokens its columns: a lane's accumulators are pairs of tokens of one
+// column (paired fp32 operations), and four chains of products run side by side. Scores stay in units of their
+// column: x = a u, u = step raw + base b, so that max and difference are those of u; a is positive (a negative scale turns the
+// query's sign), and large or tiny enough ones are clamped, where every weight is 0 or 1 anyway.
+//
 // A block of 64 columns as the first kernel leaves it for the second: fragments and constants, copied as they are.
-constexpr int COLS = 64, EIGHTS = COLS / 8;
+constexpr int COLS = 64, SIXTEENS = COLS / 16;
 template <int D>
 struct __align__(16) Slab {
-  uint4 frag[EIGHTS][D / 32][32];
-  float a[COLS], b[COLS];  // x = step (a raw) + base b
-  int p[COLS];             // the row's position
-  float m[COLS], l[COLS];  // its maximum, and the inverse of its sum
+  uint4 frag[SIXTEENS][D / 16][32];  // columns g and g + 8 (fp32 queries: the parts of row g), by k step
+  float4 ab[COLS];                   // a, a, b, b
+  float4 ml[COLS];                   // -M, -M, 1 / L, 1 / L
+  int p[COLS];                       // the row's position
 };
-// A tile's codes as A fragments: word, then the four registers of its two products.
+// A tile's codes as B fragments of four eights of tokens, and its parameters: rows 2 t and 2 t + 1 of each.
 template <int D>
-struct Unpacked {
-  uint32_t u[2][D / 32][8];
-  float2 par[2][2];
-  __device__ __forceinline__ explicit Unpacked(const Codes<D>& k) {
+struct Tile {
+  uint32_t w[4][D / 32];
+  uint4 par[4];
+  __device__ __forceinline__ void load(const uint8_t* blk, int tile, int g, int t) {
+    constexpr int WORDS = D / 32;
+    const int row0 = (tile & 1) * TILE;
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint32_t a = k.w[mt][0][i], b = k.w[mt][1][i], a8 = a >> 8, b8 = b >> 8;
-        uint32_t(&v)[8] = u[mt][i];
-        v[0] = a & 0x000f000fu, v[1] = b & 0x000f000fu, v[2] = a & 0x00f000f0u, v[3] = b & 0x00f000f0u;
-        v[4] = a8 & 0x000f000fu, v[5] = b8 & 0x000f000fu, v[6] = a8 & 0x00f000f0u, v[7] = b8 & 0x00f000f0u;
+    for (int e = 0; e < 4; ++e) {
+      const uint8_t* p = blk + (row0 + e * 8 + g) * (D / 2) + t * (WORDS * 4);
+      if (D == 128) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[e][0] = v.x, w[e][1] = v.y, w[e][2 % WORDS] = v.z, w[e][3 % WORDS] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[e][0] = v.x, w[e][1] = v.y;
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) par[mt][h] = params(k.par[mt][h]);
+      par[e] = *reinterpret_cast<const uint4*>(blk + kKvPage * D + (row0 + e * 8 + 2 * t) * 8);
     }
   }
 };
-
 __device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -461,38 +479,64 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+template <int D>
+struct Unpacked {
+  uint32_t u[4][D / 32][4];   // word: the two registers of each of its two products
+  uint64_t step[4], base[4];  // of tokens 2 t and 2 t + 1
+  __device__ __forceinline__ explicit Unpacked(const Tile<D>& k) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t a = k.w[e][i], a8 = a >> 8;
+        u[e][i][0] = a & 0x000f000fu, u[e][i][1] = a & 0x00f000f0u, u[e][i][2] = a8 & 0x000f000fu, u[e][i][3] = a8 & 0x00f000f0u;
+      }
+      const float2 even = params(k.par[e].x), odd = params(k.par[e].z);
+      step[e] = f2pack(even.x, odd.x), base[e] = f2pack(even.y, odd.y);
+    }
+  }
+};
+// the token (of its tile) of the lane's place j (0, 1) in eight e
+__device__ __forceinline__ int token_at(int e, int t, int j) { return kv4_rho_inv(e * 8 + 2 * t + j); }
 
-// Scores of an eight of columns against a tile: x[v][e] of the lane's tokens v (mt * 2 + h) and columns 2 t + e (fp32
-// queries: e = 0 alone).
+// u of sixteen columns against a tile: u[h][e] has column g + 8 h (fp32 queries: row g, h = 0 alone), tokens 2 t and 2 t + 1 of eight e.
 template <int D, bool F32>
-__device__ __forceinline__ void scores(const Unpacked<D>& k, const Slab<D>& sl, int n, int lane, float (&x)[4][2]) {
-  float d[2][4] = {};
+__device__ __forceinline__ void scores(const Unpacked<D>& k, const Slab<D>& sl, int j, int lane, const float4 (&ab)[2], uint64_t (&u)[2][4]) {
+  float d[4][4];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    const uint4 f = sl.frag[n][i][lane];
+    const uint4 f = sl.frag[j][2 * i][lane], f2 = sl.frag[j][2 * i + 1][lane];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) mma16816(d[mt], k.u[mt][i][0], k.u[mt][i][1], k.u[mt][i][2], k.u[mt][i][3], f.x, f.y);
+    for (int e = 0; e < 4; ++e) {
+      if (i == 0) mma_first(d[e], f, k.u[e][0][0], k.u[e][0][1]);
+      else mma16816(d[e], f.x, f.y, f.z, f.w, k.u[e][i][0], k.u[e][i][1]);
+    }
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) mma16816(d[mt], k.u[mt][i][4], k.u[mt][i][5], k.u[mt][i][6], k.u[mt][i][7], f.z, f.w);
+    for (int e = 0; e < 4; ++e) mma16816(d[e], f2.x, f2.y, f2.z, f2.w, k.u[e][i][2], k.u[e][i][3]);
   }
-  const int col = n * 8 + 2 * (lane & 3);
-  const float2 a = *reinterpret_cast<const float2*>(&sl.a[col]), b = *reinterpret_cast<const float2*>(&sl.b[col]);
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int mt = v >> 1, h = v & 1;
-    const float2 par = k.par[mt][h];
+  for (int e = 0; e < 4; ++e) {
     if (F32) {
-      x[v][0] = __fmaf_rn(par.x, __fmul_rn(a.x, d[mt][2 * h] + d[mt][2 * h + 1]), __fmul_rn(par.y, b.x));
+      u[0][e] = fma2(k.step[e], add2(f2pack(d[e][0], d[e][1]), f2pack(d[e][2], d[e][3])), mul2(k.base[e], f2pack(ab[0].z, ab[0].w)));
     } else {
-      const uint64_t y = fma2(f2pack(par.x, par.x), mul2(f2pack(a.x, a.y), f2pack(d[mt][2 * h], d[mt][2 * h + 1])),
-                              mul2(f2pack(par.y, par.y), f2pack(b.x, b.y)));
-      const float2 z = f2unpack(y);
-      x[v][0] = z.x, x[v][1] = z.y;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        u[h][e] = fma2(k.step[e], f2pack(d[e][2 * h], d[e][2 * h + 1]), mul2(k.base[e], f2pack(ab[h].z, ab[h].w)));
     }
   }
 }
@@ -529,46 +573,54 @@ __device__ __forceinline__ void load_slab(const Kv4Attn& a, const Rows& r, int64
     }
     int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);
     e = e > 127 ? 127 : e < -113 ? -113 : e;
-    const float up = __int_as_float((e + 127) << 23);
+    const float up = copysignf(__int_as_float((e + 127) << 23), a.scale);
     constexpr int WORDS = W / 4;
-    const int t = w / WORDS, word = w % WORDS, col = (k0 + k * PER) * PARTS;
+    // where the row's numbers stand: fp32 queries have 8 rows in sixteen columns, their parts 8 apart
+    const int t = w / WORDS, word = w % WORDS, at = k0 + k * PER, j = at / (16 / PARTS), in = at % (16 / PARTS);
+    const int col = j * 16 + in;
     float hi[8], lo[8];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       hi[n] = x[k][n] * up * (n & 1 ? 0.0625f : 1.0f);
       lo[n] = hi[n] - __half2float(__float2half_rn(hi[n]));
     }
-    sl.frag[col >> 3][word][(col & 7) * 4 + t] =
-        make_uint4(pack_half2(hi[0], hi[4]), pack_half2(hi[1], hi[5]), pack_half2(hi[2], hi[6]), pack_half2(hi[3], hi[7]));
-    if (F32)
-      sl.frag[col >> 3][word][((col & 7) + 1) * 4 + t] =
-          make_uint4(pack_half2(lo[0], lo[4]), pack_half2(lo[1], lo[5]), pack_half2(lo[2], lo[6]), pack_half2(lo[3], lo[7]));
+    uint32_t* to = reinterpret_cast<uint32_t*>(&sl.frag[j][2 * word][(in & 7) * 4 + t]) + (F32 ? 0 : in >> 3);
+    constexpr int NEXT = 32 * 4;  // words to the next k step
+    to[0] = pack_half2(hi[0], hi[4]), to[2] = pack_half2(hi[1], hi[5]);
+    to[NEXT] = pack_half2(hi[2], hi[6]), to[NEXT + 2] = pack_half2(hi[3], hi[7]);
+    if (F32) {
+      to[1] = pack_half2(lo[0], lo[4]), to[3] = pack_half2(lo[1], lo[5]);
+      to[NEXT + 1] = pack_half2(lo[2], lo[6]), to[NEXT + 3] = pack_half2(lo[3], lo[7]);
+    }
     if (w == 0) {
-      const float c1 = __fmul_rn(a.scale, kLog2e);
+      const float c1 = __fmul_rn(fabsf(a.scale), kLog2e);
       const int f = 24 - e, half = f / 2;
       const float ca = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
-#pragma unroll
-      for (int j = 0; j < PARTS; ++j) {
-        sl.a[col + j] = ca, sl.b[col + j] = __fmul_rn(c1, sum);
-        sl.p[col + j] = row < rows ? r.position(row / a.share) : -1;
-        sl.m[col + j] = sl.l[col + j] = 0.0f;
-      }
+      const float aa = fminf(fmaxf(ca, kLeastA), kMostA), bb = __fmul_rn(__fmul_rn(sum, up), 5.9604644775390625e-8f);  // 2^-24
+      sl.ab[col] = make_float4(aa, aa, bb, bb);
+      sl.p[col] = row < rows ? r.position(row / a.share) : -1;
     }
   }
+}
+// joins (m, l) with (m2, l2), maxima of u
+__device__ __forceinline__ void join_u(float a, float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2), from = top == kNegInf ? 0.0f : top;
+  l = fmaf(l, exp2_approx(a * (m - from)), l2 * exp2_approx(a * (m2 - from)));
+  m = top;
 }
 
 // First kernel: each column's maximum and sum over a chunk of tiles. A warp's running ones lie in shared memory.
 template <int D>
 struct __align__(16) RowsShared {
   Slab<D> sl;
-  float4 run[WARPS][EIGHTS][32];
+  float4 run[WARPS][SIXTEENS][32];
   float2 part[WARPS][COLS];
 };
 template <int D, bool F32>
 __global__ void __launch_bounds__(THREADS, 2) kv4_mass_rows_many(Kv4 c, Kv4Attn a, int voters, Plan pl, Stats st) {
   extern __shared__ __align__(16) uint8_t smem[];
   RowsShared<D>& sh = *reinterpret_cast<RowsShared<D>*>(smem);
-  constexpr int PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
+  constexpr int PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D), HALVES = F32 ? 1 : 2;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   bool bad = false;
   const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks * pl.chunks;
@@ -591,63 +643,77 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_rows_many(Kv4 c, Kv4Attn 
       id = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
       if (id < 0 || id >= c.n_pages) bad = true, id = 0;
     }
-    Codes<D> cur;
+    Tile<D> cur;
     const auto load = [&](int k) {
       const int from = __shfl_sync(0xffffffffu, id, k);
       const int tile = tile0 + warp + k * WARPS;
       if (tile < tile1) cur.load(c.pages + ((int64_t)from * c.kv_heads + r.h) * BLK, tile, g, t);
     };
-    load(0);
     load_slab<D, F32>(a, r, col0, sh.sl);
+    load(0);
 #pragma unroll
-    for (int n = 0; n < EIGHTS; ++n) sh.run[warp][n][lane] = make_float4(kNegInf, 0.0f, kNegInf, 0.0f);
+    for (int j = 0; j < SIXTEENS; ++j) sh.run[warp][j][lane] = make_float4(kNegInf, 0.0f, kNegInf, 0.0f);
     __syncthreads();
-    const int eights = (int)min((int64_t)EIGHTS, (rows * PARTS - col0 + 7) / 8);
+    const int sixteens = (int)min((int64_t)SIXTEENS, (rows * PARTS - col0 + 15) / 16);
     for (int k = 0, tile = tile0 + warp; some && tile < tile1; ++k, tile += WARPS) {
       const Unpacked<D> now(cur);
       if (k < 31) load(k + 1);
       const int j0 = tile * TILE, sees = seen(a, first, last, j0, TILE);
       if (sees == 0) continue;
 #pragma unroll 1
-      for (int n = 0; n < eights; ++n) {
-        float x[4][2];
-        scores<D, F32>(now, sh.sl, n, lane, x);
-        float4 run = sh.run[warp][n][lane];
+      for (int j = 0; j < sixteens; ++j) {
+        uint64_t u[2][4];
+        const float4 ab[2] = {sh.sl.ab[j * 16 + g], sh.sl.ab[j * 16 + g + 8]};
+        scores<D, F32>(now, sh.sl, j, lane, ab, u);
+        float4 run = sh.run[warp][j][lane];
 #pragma unroll
-        for (int e = 0; e < (F32 ? 1 : 2); ++e) {
+        for (int h = 0; h < HALVES; ++h) {
+          float2 x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = f2unpack(u[h][e]);
           if (sees == 1) {
-            const int p = sh.sl.p[n * 8 + 2 * t + e];
+            const int p = sh.sl.p[j * 16 + g + 8 * h];
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (!visible(a, p, j0 + token_of((v >> 1) * 16 + (v & 1) * 8 + g))) x[v][e] = kNegInf;
+            for (int e = 0; e < 4; ++e) {
+              if (!visible(a, p, j0 + token_at(e, t, 0))) x[e].x = kNegInf;
+              if (!visible(a, p, j0 + token_at(e, t, 1))) x[e].y = kNegInf;
+            }
           }
-          float &m = e ? run.z : run.x, &l = e ? run.w : run.y;
-          const float top = fmaxf(fmaxf(fmaxf(x[0][e], x[1][e]), fmaxf(x[2][e], x[3][e])), m), from = top == kNegInf ? 0.0f : top;
-          l = fmaf(l, exp2_approx(m - from), (exp2_approx(x[0][e] - from) + exp2_approx(x[1][e] - from)) + (exp2_approx(x[2][e] - from) + exp2_approx(x[3][e] - from)));
+          float &m = h ? run.z : run.x, &l = h ? run.w : run.y;
+          const float top = max3(max3(max3(x[0].x, x[0].y, x[1].x), x[1].y, x[2].x), max3(x[2].y, x[3].x, x[3].y), m);
+          const float from = top == kNegInf ? 0.0f : top, aa = ab[h].x;
+          const uint64_t a2 = f2pack(aa, aa), minus = f2pack(-from, -from);
+          float s[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = f2unpack(mul2(a2, add2(f2pack(x[e].x, x[e].y), minus)));
+            s[e] = exp2_approx(y.x) + exp2_approx(y.y);
+          }
+          l = fmaf(l, exp2_approx(aa * (m - from)), (s[0] + s[1]) + (s[2] + s[3]));
           m = top;
         }
-        sh.run[warp][n][lane] = run;
+        sh.run[warp][j][lane] = run;
       }
     }
-    __syncwarp();
 #pragma unroll 1
-    for (int n = 0; n < EIGHTS; ++n) {
-      const float4 run = sh.run[warp][n][lane];
+    for (int j = 0; j < SIXTEENS; ++j) {
+      const float4 run = sh.run[warp][j][lane];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float m = e ? run.z : run.x, l = e ? run.w : run.y;
+      for (int h = 0; h < HALVES; ++h) {
+        float m = h ? run.z : run.x, l = h ? run.w : run.y;
+        const float aa = sh.sl.ab[j * 16 + g + 8 * h].x;
 #pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
-        if (g == 0) sh.part[warp][n * 8 + 2 * t + e] = make_float2(m, l);
+        for (int o = 1; o <= 2; o <<= 1) join_u(aa, m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+        if (t == 0) sh.part[warp][j * 16 + g + 8 * h] = make_float2(m, l);
       }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < COLS; i += THREADS) {
+      if (F32 && (i & 8)) continue;
       float2 v = sh.part[0][i];
-      for (int w = 1; w < WARPS; ++w) join(v.x, v.y, sh.part[w][i].x, sh.part[w][i].y);
+      for (int w = 1; w < WARPS; ++w) join_u(sh.sl.ab[i].x, v.x, v.y, sh.part[w][i].x, sh.part[w][i].y);
       st.part[item * COLS + i] = v;
-      sh.sl.m[i] = v.x == kNegInf ? 0.0f : v.x;  // what the second kernel needs where there is one chunk
-      sh.sl.l[i] = v.y == 0.0f ? 0.0f : __frcp_rn(v.y);
+      sh.sl.ml[i] = finished(v.x, v.y);  // what the second kernel needs where there is one chunk
     }
     __syncthreads();
     if (chunk == 0) {
@@ -667,16 +733,16 @@ __global__ void __launch_bounds__(COLS) kv4_mass_sums(Kv4 c, Kv4Attn a, int vote
     const int unit = (int)(item / pl.blocks), block = (int)(item - (int64_t)unit * pl.blocks);
     bool bad = false;
     const Rows r = rows_of(c, unit, voters, &bad);
-    if ((int64_t)block * COLS >= (int64_t)r.votes * a.share * pl.parts) continue;
+    if ((int64_t)block * COLS >= (int64_t)r.votes * a.share * pl.parts || (pl.parts == 2 && (threadIdx.x & 8))) continue;
+    Slab<D>& sl = *reinterpret_cast<Slab<D>*>(st.slabs + item * (int64_t)sizeof(Slab<D>));
     const int chunks = ((r.s.len + TILE - 1) / TILE + pl.chunk - 1) / pl.chunk;
+    const float aa = sl.ab[threadIdx.x].x;
     float m = kNegInf, l = 0.0f;
     for (int k = 0; k < chunks; ++k) {
       const float2 v = st.part[(item * pl.chunks + k) * COLS + threadIdx.x];
-      join(m, l, v.x, v.y);
+      join_u(aa, m, l, v.x, v.y);
     }
-    Slab<D>& sl = *reinterpret_cast<Slab<D>*>(st.slabs + item * (int64_t)sizeof(Slab<D>));
-    sl.m[threadIdx.x] = m == kNegInf ? 0.0f : m;
-    sl.l[threadIdx.x] = l == 0.0f ? 0.0f : __frcp_rn(l);
+    sl.ml[threadIdx.x] = finished(m, l);
   }
 }
 
@@ -724,7 +790,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
     };
     int block = next(share), buf = 0;
     copy(block, 0);
-    Codes<D> k{};
+    Tile<D> k{};
     bool there = tile < all;
     if (there) {
       const int id = c.page_table[(int64_t)r.b * c.max_pages + tile / 2];
@@ -732,7 +798,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
       else k.load(c.pages + ((int64_t)id * c.kv_heads + r.h) * BLK, tile, g, t);
     }
     const Unpacked<D> now(k);
-    float votes[4] = {};
+    uint64_t votes[4] = {0, 0, 0, 0};  // of tokens 2 t and 2 t + 1 of the eights
     while (block < blocks) {
       const int then = next(block + pl.shares);
       copy(then, buf ^ 1);
@@ -742,23 +808,29 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
       ends(block, &first, &last);
       const int j0 = tile * TILE, sees = there ? seen(a, first, last, j0, TILE) : 0;
       const Slab<D>& sl = slabs[buf];
-      const int eights = (int)min((int64_t)EIGHTS, (rows * PARTS - (int64_t)block * COLS + 7) / 8);
+      const int sixteens = (int)min((int64_t)SIXTEENS, (rows * PARTS - (int64_t)block * COLS + 15) / 16);
       if (sees) {
 #pragma unroll 1
-        for (int n = 0; n < eights; ++n) {
-          float x[4][2];
-          scores<D, F32>(now, sl, n, lane, x);
-          const int col = n * 8 + 2 * t;
-          const float2 m = *reinterpret_cast<const float2*>(&sl.m[col]), l = *reinterpret_cast<const float2*>(&sl.l[col]);
-          const int2 p = *reinterpret_cast<const int2*>(&sl.p[col]);
+        for (int j = 0; j < sixteens; ++j) {
+          uint64_t u[2][4];
+          const float4 ab[2] = {sl.ab[j * 16 + g], sl.ab[j * 16 + g + 8]};
+          scores<D, F32>(now, sl, j, lane, ab, u);
 #pragma unroll
-          for (int e = 0; e < (F32 ? 1 : 2); ++e) {
-            if ((e ? p.y : p.x) < 0) continue;  // no row, or one that sees nothing
+          for (int h = 0; h < (F32 ? 1 : 2); ++h) {
+            const int p = sl.p[j * 16 + g + 8 * h];
+            float4 ml = sl.ml[j * 16 + g + 8 * h];
+            if (p < 0) ml.z = ml.w = 0.0f;  // no row, or one that sees nothing
+            const uint64_t a2 = f2pack(ab[h].x, ab[h].y), minus = f2pack(ml.x, ml.y), inv = f2pack(ml.z, ml.w);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const float w = exp2_approx(x[v][e] - (e ? m.y : m.x));
-              if (sees == 2 || visible(a, e ? p.y : p.x, j0 + token_of((v >> 1) * 16 + (v & 1) * 8 + g)))
-                votes[v] = fmaf(w, e ? l.y : l.x, votes[v]);
+            for (int e = 0; e < 4; ++e) {
+              const float2 y = f2unpack(mul2(a2, add2(u[h][e], minus)));
+              const uint64_t more = fma2(f2pack(exp2_approx(y.x), exp2_approx(y.y)), inv, votes[e]);
+              if (sees == 2) {
+                votes[e] = more;
+              } else {
+                const float2 v = f2unpack(votes[e]), w = f2unpack(more);
+                votes[e] = f2pack(visible(a, p, j0 + token_at(e, t, 0)) ? w.x : v.x, visible(a, p, j0 + token_at(e, t, 1)) ? w.y : v.y);
+              }
             }
           }
         }
@@ -767,9 +839,16 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
       block = then, buf ^= 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    const float got = gather_votes(votes, t);
-    const int row = (t >> 1) * 16 + (t & 1) * 8 + g;
-    st.votes[((((int64_t)unit * pl.groups + group) * pl.shares + share) * WARPS + warp) * TILE + token_of(row)] = got;
+    // over the eight lanes that share tokens; lane g = 2 e + j writes place j of eight e
+    float mine = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float2 v = f2unpack(votes[e]);
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) v.x += __shfl_xor_sync(0xffffffffu, v.x, o), v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      if (g >> 1 == e) mine = g & 1 ? v.y : v.x;
+    }
+    st.votes[((((int64_t)unit * pl.groups + group) * pl.shares + share) * WARPS + warp) * TILE + token_at(g >> 1, t, g & 1)] = mine;
     __syncthreads();
   }
   if (bad) record_device_error(kErrRange);
@@ -801,7 +880,7 @@ Plan plan_of(const Kv4& c, int share, int voters, bool f32, int num_sms) {
   p.votes = voters < c.max_q ? voters : c.max_q;
   p.votes = p.votes < c.total_q ? p.votes : c.total_q;
   const int64_t cols = (int64_t)p.votes * share * p.parts, units = (int64_t)c.batch * c.kv_heads;
-  p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : EIGHTS;
+  p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : COLS / 8;
   p.blocks = (int)((cols + p.nt * 8 - 1) / (p.nt * 8));
   p.tiles = (c.max_kv + TILE - 1) / TILE;
   // a chunk: as many tiles as leave each SM several blocks
@@ -809,7 +888,7 @@ Plan plan_of(const Kv4& c, int share, int voters, bool f32, int num_sms) {
   per = per < 1 ? 1 : per > MAX_CHUNK / WARPS ? MAX_CHUNK / WARPS : per;
   p.chunk = (int)per * WARPS;
   p.chunks = (p.tiles + p.chunk - 1) / p.chunk;
-  if (p.nt == EIGHTS) {
+  if (p.nt == COLS / 8) {
     p.groups = (p.tiles + WARPS - 1) / WARPS;
     const int64_t all = units * (p.groups > 0 ? p.groups : 1);
     const int64_t s = ((int64_t)num_sms * 4 + all - 1) / all;
