@@ -1,17 +1,24 @@
 // kv4_evict.cu -- eviction: long sequences keep the tokens that gathered most attention weight.
 //
-// Two kernels, a block for each sequence and head in both. The first finds the least mass that is kept, by
-// three passes over the masses that count their digits (11, 11 and 10 bits, from the top), and lists the
-// kept tokens in order. The second moves them: their codes, parameters and mass, as they are. In
-// place a token only moves to an earlier slot, and a chunk of tokens is read whole before any of it
-// is written, so that nothing is overwritten before it has been read.
+// One kernel; a cluster of one to eight blocks for each sequence and head. Its blocks take a run of tokens each and keep
+// the ranks of their masses (whole numbers in the masses' order) in shared memory. The least rank that is kept is found by
+// three passes that count digits (11, 11 and 10 bits, from the top), added up over the cluster through distributed
+// shared memory; then every warp counts and lists the kept tokens of its run, in order, and the cluster moves them: codes,
+// parameters and mass, as they are. In place a token only moves to an earlier slot, and a chunk of tokens is read
+// whole, by all blocks of the cluster, before any of it is written, so that nothing is overwritten before it has been read.
+// New lengths that replace the old ones (which all clusters of a sequence read) are written by a second kernel.
+//
+// Bound by latency where sequences are few: loads that depend on each other (length, page, mass; kept token, page, data) and
+// the cluster's barriers; by the moved bytes where they are many.
 #include "kv4.cuh"
 
 namespace bitnet {
 namespace {
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = 2048;
+constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_RANKS = 20480;  // that a block keeps (80 KB, two blocks an SM); longer runs are read again each time
 
 // Masses as whole numbers in the same order; a NaN above all, both zeros alike.
 __device__ __forceinline__ uint32_t rank_of(float x) {
@@ -35,153 +42,197 @@ __device__ __forceinline__ float* mass_of(const Kv4& c, const Kv4Evict& e, int b
   return e.mass + ((int64_t)id * c.kv_heads + h) * kKvPage + j % kKvPage;
 }
 
-__global__ void __launch_bounds__(THREADS) kv4_select_kernel(Kv4 c, Kv4Evict e, int32_t* lens, int32_t* kept, int cap) {
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// A token's data: lanes take 16 bytes of its key or value row each, the first its parameters, the second its mass.
+template <int D>
+__global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e, int32_t* kept, int cap, int cluster, int ranks_kept,
+                                                               bool write_len) {
+  extern __shared__ uint32_t ranks[];
   __shared__ uint32_t bins[BINS];
   __shared__ uint32_t warp_sum[WARPS];
-  __shared__ int2 warp_count[WARPS];
+  __shared__ int2 warp_count[WARPS], block_count;
   __shared__ uint32_t found[2];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  constexpr int BLK = (int)kv4_block_bytes(D);
+  const int unit = blockIdx.x / cluster, me = cluster > 1 ? (int)cluster_ctarank() : 0, b = unit / c.kv_heads, h = unit - b * c.kv_heads;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const auto sync_all = [&]() {
+    if (cluster > 1) cluster_sync_all();
+    else __syncthreads();
+  };
   const Sizes s = sizes_of(c, e, b);
-  if (h == 0 && tid == 0) lens[b] = s.len;
-  if (s.len < 0) {
+  if (h == 0 && me == 0 && tid == 0 && write_len) e.new_len[b] = s.len < 0 ? c.kv_len[b] : s.keeps;
+  const bool cut = s.len > e.limit;
+  if (s.len < 0 || (e.into && s.keeps > e.into_pages * kKvPage)) {  // the second: not one that is cut
     if (tid == 0) record_device_error(kErrRange);
     return;
   }
-  if (s.len <= e.limit) return;
-  bool bad = false;
-  const int lo = e.sinks, hi = s.len - e.recent;  // the tokens that are chosen from
-  uint32_t want = (uint32_t)(e.budget - e.sinks - e.recent);  // how many of them
-  uint32_t least = 0, mask = 0;  // the digits found so far
-  if (want == 0) least = 0xffffffffu, mask = 0xffffffffu;
-  for (int pass = 0; want > 0 && pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-    for (int i = tid; i < BINS; i += THREADS) bins[i] = 0;
-    __syncthreads();
-    for (int j = lo + tid; j < hi; j += THREADS) {
-      const uint32_t r = rank_of(*mass_of(c, e, b, h, j, &bad));
-      if ((r & mask) == least) atomicAdd(&bins[(r >> shift) & ((1u << width) - 1)], 1u);
-    }
-    __syncthreads();
-    // the digit from which on `want` tokens are counted, from above: threads take two bins each, the highest first
-    const uint32_t b1 = bins[BINS - 1 - 2 * tid], b0 = bins[BINS - 2 - 2 * tid];
-    uint32_t sum = b1 + b0;
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += x;
-    }
-    if (lane == 31) warp_sum[warp] = sum;
-    __syncthreads();
-    uint32_t before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    const uint32_t above = before + sum - b1 - b0;  // tokens of higher digits than this thread's
-    if (above < want && want <= above + b1) found[0] = BINS - 1 - 2 * tid, found[1] = want - above;
-    if (above + b1 < want && want <= above + b1 + b0) found[0] = BINS - 2 - 2 * tid, found[1] = want - above - b1;
-    __syncthreads();
-    least |= found[0] << shift;
-    mask |= ((1u << width) - 1) << shift;
-    want = found[1];
-    __syncthreads();
-  }
-  // `want` is now how many of the tokens at `least` are kept. Each warp takes a run of tokens: it counts, then lists.
-  const int per = ((s.len + WARPS - 1) / WARPS + 31) / 32 * 32, j0 = min(warp * per, s.len), j1 = min(j0 + per, s.len);
-  const bool none = e.budget == e.sinks + e.recent;
-  const auto kind = [&](int j, bool* sure, bool* level) {
-    const uint32_t r = j < j1 && j >= lo && j < hi && !none ? rank_of(*mass_of(c, e, b, h, j, &bad)) : 0;
-    const bool middle = j >= lo && j < hi;
-    *sure = j < j1 && (!middle || (!none && r > least));
-    *level = j < j1 && middle && !none && r == least;
-  };
-  int sures = 0, levels = 0;
-  for (int j = j0 + lane; j - lane < j1; j += 32) {
-    bool sure, level;
-    kind(j, &sure, &level);
-    sures += __popc(__ballot_sync(0xffffffffu, sure));
-    levels += __popc(__ballot_sync(0xffffffffu, level));
-  }
-  if (lane == 0) warp_count[warp] = make_int2(sures, levels);
-  __syncthreads();
-  sures = levels = 0;
-  for (int w = 0; w < warp; ++w) sures += warp_count[w].x, levels += warp_count[w].y;
-  int32_t* list = kept + ((int64_t)b * c.kv_heads + h) * cap;
-  for (int j = j0 + lane; j - lane < j1; j += 32) {
-    bool sure, level;
-    kind(j, &sure, &level);
-    const uint32_t sm = __ballot_sync(0xffffffffu, sure), lm = __ballot_sync(0xffffffffu, level), below = (1u << lane) - 1;
-    const int ls = levels + __popc(lm & below), at = sures + __popc(sm & below) + min(ls, (int)want);
-    if ((sure || (level && ls < (int)want)) && at < cap) list[at] = j;
-    sures += __popc(sm);
-    levels += __popc(lm);
-  }
-  if (bad) record_device_error(kErrRange);
-}
-
-// A token's data: lanes take 16 bytes of its key or value row each, the first its parameters and mass too.
-template <int D>
-__global__ void __launch_bounds__(THREADS) kv4_move_kernel(Kv4 c, Kv4Evict e, const int32_t* lens, const int32_t* kept, int cap) {
-  constexpr int BLK = (int)kv4_block_bytes(D), LANES = D / 16, PIECES = LANES / 2, TOKENS = THREADS / LANES, BATCH = 4;
-  const int h = blockIdx.x, b = blockIdx.y, part = threadIdx.x % LANES, worker = threadIdx.x / LANES;
-  const int len = lens[b];
-  if (len < 0) {
-    if (h == 0 && threadIdx.x == 0 && e.new_len) e.new_len[b] = c.kv_len[b];
-    return;
-  }
-  const bool cut = len > e.limit;
-  const int keeps = cut ? e.budget : len;
-  if (h == 0 && threadIdx.x == 0 && e.new_len) e.new_len[b] = keeps;
   if (!cut && !e.into) return;
-  if (e.into && keeps > e.into_pages * kKvPage) {  // not one that is cut
-    if (threadIdx.x == 0) record_device_error(kErrRange);
-    return;
+  bool bad = false;
+  int32_t* list = kept + (int64_t)unit * cap;
+  if (cut) {
+    const int lo = e.sinks, hi = s.len - e.recent;  // the tokens that are chosen from
+    uint32_t want = (uint32_t)(e.budget - e.sinks - e.recent);  // how many of them
+    // this block's run of tokens, and its warps'
+    const int per = ((s.len + cluster * WARPS - 1) / (cluster * WARPS) + 31) / 32 * 32;
+    const int run0 = (int)min((int64_t)me * WARPS * per, (int64_t)s.len), j0 = (int)min(run0 + (int64_t)warp * per, (int64_t)s.len), j1 = (int)min(j0 + (int64_t)per, (int64_t)s.len);
+    const bool keep = WARPS * per <= ranks_kept;
+    const auto read = [&](int j) { return rank_of(*mass_of(c, e, b, h, j, &bad)); };
+    if (keep && want) {
+      for (int i0 = j0 + lane; i0 - lane < j1; i0 += 8 * 32) {
+        uint32_t r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = i0 + 32 * i < j1 ? read(i0 + 32 * i) : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + 32 * i < j1) ranks[i0 + 32 * i - run0] = r[i];
+      }
+      __syncwarp();
+    }
+    const auto rank = [&](int j) { return keep ? ranks[j - run0] : read(j); };
+    uint32_t least = 0, mask = 0;  // the digits found so far
+    const bool none = want == 0;
+    for (int pass = 0; !none && pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+      for (int i = tid; i < BINS; i += THREADS) bins[i] = 0;
+      __syncthreads();
+      for (int j = max(j0, lo) + lane; j < min(j1, hi); j += 32) {
+        const uint32_t r = rank(j);
+        if ((r & mask) == least) atomicAdd(&bins[(r >> shift) & ((1u << width) - 1)], 1u);
+      }
+      sync_all();
+      // four bins a thread, the highest first, over all blocks
+      uint32_t n[4] = {0, 0, 0, 0}, sum = 0;
+      const uint32_t at = smem_u32(&bins[BINS - 4 - 4 * tid]);
+      for (int k = 0; k < cluster; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n[i] += cluster > 1 ? ld_cluster_u32(map_to_rank(at, k) + 4 * (3 - i)) : bins[BINS - 1 - 4 * tid - i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += n[i];
+      const uint32_t own = sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      if (lane == 31) warp_sum[warp] = sum;
+      __syncthreads();
+      uint32_t above = sum - own;  // tokens of higher digits than this thread's
+      for (int w = 0; w < warp; ++w) above += warp_sum[w];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (above < want && want <= above + n[i]) found[0] = BINS - 1 - 4 * tid - i, found[1] = want - above;
+        above += n[i];
+      }
+      sync_all();  // `found` is written, and no block reads another's bins any more
+      least |= found[0] << shift;
+      mask |= ((1u << width) - 1) << shift;
+      want = found[1];
+    }
+    // `want` is now how many of the tokens at `least` are kept. Each warp counts those of its run, then lists them.
+    const auto kind = [&](int j, bool* sure, bool* level) {
+      const bool middle = j >= lo && j < hi;
+      const uint32_t r = j < j1 && middle && !none ? rank(j) : 0;
+      *sure = j < j1 && (!middle || (!none && r > least));
+      *level = j < j1 && middle && !none && r == least;
+    };
+    int sures = 0, levels = 0;
+    for (int j = j0 + lane; j - lane < j1; j += 32) {
+      bool sure, level;
+      kind(j, &sure, &level);
+      sures += __popc(__ballot_sync(0xffffffffu, sure));
+      levels += __popc(__ballot_sync(0xffffffffu, level));
+    }
+    if (lane == 0) warp_count[warp] = make_int2(sures, levels);
+    __syncthreads();
+    sures = levels = 0;
+    for (int w = 0; w < warp; ++w) sures += warp_count[w].x, levels += warp_count[w].y;
+    if (tid == THREADS - 1) block_count = make_int2(sures + warp_count[warp].x, levels + warp_count[warp].y);
+    sync_all();
+    const uint32_t count_at = smem_u32(&block_count);
+    for (int k = 0; k < me; ++k) {
+      sures += (int)ld_cluster_u32(map_to_rank(count_at, k));
+      levels += (int)ld_cluster_u32(map_to_rank(count_at, k) + 4);
+    }
+    for (int j = j0 + lane; j - lane < j1; j += 32) {
+      bool sure, level;
+      kind(j, &sure, &level);
+      const uint32_t sm = __ballot_sync(0xffffffffu, sure), lm = __ballot_sync(0xffffffffu, level), below = (1u << lane) - 1;
+      const int ls = levels + __popc(lm & below), at = sures + __popc(sm & below) + min(ls, (int)want);
+      if ((sure || (level && ls < (int)want)) && at < cap) list[at] = j;
+      sures += __popc(sm);
+      levels += __popc(lm);
+    }
+    sync_all();  // the list is written, and no block reads another's counts any more
   }
-  const int32_t* list = kept + ((int64_t)b * c.kv_heads + h) * cap;
+
+  // ---- the kept tokens move
+  constexpr int LANES = D / 16, PIECES = LANES / 2, TOKENS = THREADS / LANES, BATCH = 4;
+  const int part = tid % LANES, worker = tid / LANES;
   const int32_t* from = c.page_table + (int64_t)b * c.max_pages;
   const int32_t* to = e.into ? e.into + (int64_t)b * e.into_pages : from;
-  bool bad = false;
-  for (int r0 = 0; r0 < keeps; r0 += TOKENS * BATCH) {
+  const int row_of_part = part < PIECES ? 0 : kKvPage;
+  for (int64_t first = 0; first < s.keeps; first += (int64_t)cluster * TOKENS * BATCH) {
+    const int64_t r0 = first + me * TOKENS * BATCH + worker;
     uint4 data[BATCH];
     uint2 par[BATCH];
     float mass[BATCH];
-    int src[BATCH];
+    int src[BATCH], id[BATCH];
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      const int r = r0 + i * TOKENS + worker;
+      const int64_t r = r0 + i * TOKENS;
       src[i] = -1;
-      if (r >= keeps) continue;
-      const int j = cut ? list[r] : r;
-      if (!e.into && j == r) continue;
-      const int id = from[j / kKvPage], t = j % kKvPage;
-      if (id < 0 || id >= c.n_pages) {
-        bad = true;
-        continue;
-      }
-      src[i] = j;
-      const uint8_t* blk = c.pages + ((int64_t)id * c.kv_heads + h) * BLK;
-      const int row = part < PIECES ? kv4_rho(t) : kKvPage + t;
+      if (r < s.keeps) src[i] = cut ? list[r] : (int)r;
+      if (!e.into && src[i] == r) src[i] = -1;  // it stays
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      id[i] = src[i] >= 0 ? from[src[i] / kKvPage] : 0;
+      if (id[i] < 0 || id[i] >= c.n_pages) bad = true, src[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (src[i] < 0) continue;
+      const int t = src[i] % kKvPage;
+      const uint8_t* blk = c.pages + ((int64_t)id[i] * c.kv_heads + h) * BLK;
+      const int row = part < PIECES ? kv4_rho(t) : row_of_part + t;
       data[i] = *reinterpret_cast<const uint4*>(blk + row * (D / 2) + part % PIECES * 16);
       if (part == 0) par[i] = *reinterpret_cast<const uint2*>(blk + kKvPage * D + kv4_rho(t) * 8);
-      if (part == 1) mass[i] = e.mass[((int64_t)id * c.kv_heads + h) * kKvPage + t];
+      if (part == 1) mass[i] = e.mass[((int64_t)id[i] * c.kv_heads + h) * kKvPage + t];
     }
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      const int r = r0 + i * TOKENS + worker;
+      id[i] = src[i] >= 0 ? to[(r0 + i * TOKENS) / kKvPage] : 0;
+      if (id[i] < 0 || id[i] >= c.n_pages) bad = true, src[i] = -1;
+    }
+    if (!e.into) sync_all();
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
       if (src[i] < 0) continue;
-      const int id = to[r / kKvPage], t = r % kKvPage;
-      if (id < 0 || id >= c.n_pages) {
-        bad = true;
-        continue;
-      }
-      uint8_t* blk = c.pages + ((int64_t)id * c.kv_heads + h) * BLK;
-      const int row = part < PIECES ? kv4_rho(t) : kKvPage + t;
+      const int r = (int)(r0 + i * TOKENS), t = r % kKvPage;
+      uint8_t* blk = c.pages + ((int64_t)id[i] * c.kv_heads + h) * BLK;
+      const int row = part < PIECES ? kv4_rho(t) : row_of_part + t;
       int piece = part % PIECES;
       if (D == 128 && part >= PIECES && ((src[i] ^ r) & 2)) piece ^= 2;  // the halves of a wide value row
       *reinterpret_cast<uint4*>(blk + row * (D / 2) + piece * 16) = data[i];
       if (part == 0) *reinterpret_cast<uint2*>(blk + kKvPage * D + kv4_rho(t) * 8) = par[i];
-      if (part == 1) e.mass[((int64_t)id * c.kv_heads + h) * kKvPage + t] = mass[i];
+      if (part == 1) e.mass[((int64_t)id[i] * c.kv_heads + h) * kKvPage + t] = mass[i];
     }
-    __syncthreads();
+    if (!e.into) sync_all();
   }
   if (bad) record_device_error(kErrRange);
+}
+
+// New lengths over the old ones, once no cluster reads them any more.
+__global__ void kv4_evict_lengths(Kv4 c, Kv4Evict e) {
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b >= c.batch) return;
+  const Sizes s = sizes_of(c, e, b);
+  e.new_len[b] = s.len < 0 ? c.kv_len[b] : s.keeps;
 }
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
@@ -189,19 +240,30 @@ int cap_of(const Kv4& c, int budget) { return budget < c.max_kv ? budget : c.max
 
 }  // namespace
 
-int64_t kv4_evict_ws_bytes(const Kv4& c, int budget) {
-  return align256((int64_t)c.batch * 4) + align256((int64_t)c.batch * c.kv_heads * cap_of(c, budget) * 4);
-}
+int64_t kv4_evict_ws_bytes(const Kv4& c, int budget) { return align256((int64_t)c.batch * c.kv_heads * cap_of(c, budget) * 4); }
 cudaError_t launch_kv4_evict(const Kv4& c, int dim, const Kv4Evict& e, void* ws, int num_sms, cudaStream_t st) {
-  int32_t* lens = static_cast<int32_t*>(ws);
-  int32_t* kept = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + align256((int64_t)c.batch * 4));
-  const dim3 grid(c.kv_heads, c.batch);
-  kv4_select_kernel<<<grid, THREADS, 0, st>>>(c, e, lens, kept, cap_of(c, e.budget));
-  if (cudaError_t err = cudaGetLastError()) return err;
-  if (dim == 128)
-    kv4_move_kernel<128><<<grid, THREADS, 0, st>>>(c, e, lens, kept, cap_of(c, e.budget));
-  else
-    kv4_move_kernel<64><<<grid, THREADS, 0, st>>>(c, e, lens, kept, cap_of(c, e.budget));
+  const int64_t units = (int64_t)c.batch * c.kv_heads;
+  // blocks of a cluster: as many as there is room for (four an SM), each with some thousand tokens
+  int cluster = 1;
+  while (cluster < MAX_CLUSTER && units * cluster * 2 <= num_sms * 4 && c.max_kv > cluster * 1024) cluster *= 2;
+  int64_t per = ((c.max_kv + cluster * WARPS - 1) / (cluster * WARPS) + 31) / 32 * 32;
+  const int ranks = (int)(per * WARPS < MAX_RANKS ? per * WARPS : MAX_RANKS);
+  const bool over = e.new_len == c.kv_len;
+  auto kernel = dim == 128 ? kv4_evict_kernel<128> : kv4_evict_kernel<64>;
+  if (cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_RANKS * 4)) return err;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(units * cluster));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = ranks * 4;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, c, e, static_cast<int32_t*>(ws), cap_of(c, e.budget), cluster, ranks, e.new_len && !over)) return err;
+  if (!over) return cudaSuccess;
+  kv4_evict_lengths<<<(c.batch + 127) / 128, 128, 0, st>>>(c, e);
   return cudaGetLastError();
 }
 
