@@ -48,12 +48,18 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint4 ld_cluster_u32x4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // A token's data: lanes take 16 bytes of its key or value row each, the first its parameters, the second its mass.
 template <int D>
 __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e, int32_t* kept, int cap, int cluster, int ranks_kept,
                                                                bool write_len) {
   extern __shared__ uint32_t ranks[];
-  __shared__ uint32_t bins[BINS];
+  __shared__ __align__(16) uint32_t bins[BINS];
   __shared__ uint32_t warp_sum[WARPS];
   __shared__ int2 warp_count[WARPS], block_count;
   __shared__ uint32_t found[2];
@@ -108,9 +114,17 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       // four bins a thread, the highest first, over all blocks
       uint32_t n[4] = {0, 0, 0, 0}, sum = 0;
       const uint32_t at = smem_u32(&bins[BINS - 4 - 4 * tid]);
-      for (int k = 0; k < cluster; ++k) {
+      if (cluster > 1) {
+        uint4 v[MAX_CLUSTER];  // all on their way at once
 #pragma unroll
-        for (int i = 0; i < 4; ++i) n[i] += cluster > 1 ? ld_cluster_u32(map_to_rank(at, k) + 4 * (3 - i)) : bins[BINS - 1 - 4 * tid - i];
+        for (int k = 0; k < MAX_CLUSTER; ++k)
+          if (k < cluster) v[k] = ld_cluster_u32x4(map_to_rank(at, k));
+#pragma unroll
+        for (int k = 0; k < MAX_CLUSTER; ++k)
+          if (k < cluster) n[0] += v[k].w, n[1] += v[k].z, n[2] += v[k].y, n[3] += v[k].x;
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(&bins[BINS - 4 - 4 * tid]);
+        n[0] = v.w, n[1] = v.z, n[2] = v.y, n[3] = v.x;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum += n[i];
