@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
   __shared__ __align__(16) uint32_t bins[BINS];
   __shared__ uint32_t warp_sum[WARPS];
   __shared__ int2 warp_count[WARPS], block_count;
-  __shared__ uint32_t found[2];
+  __shared__ uint32_t found[2], totals[MAX_CLUSTER];
   constexpr int BLK = (int)kv4_block_bytes(D);
   const int unit = blockIdx.x / cluster, me = cluster > 1 ? (int)cluster_ctarank() : 0, b = unit / c.kv_heads, h = unit - b * c.kv_heads;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -89,13 +89,26 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     const bool keep = WARPS * per <= ranks_kept;
     const auto read = [&](int j) { return rank_of(*mass_of(c, e, b, h, j, &bad)); };
     if (keep && want) {
-      for (int i0 = j0 + lane; i0 - lane < j1; i0 += 8 * 32) {
-        uint32_t r[8];
+      // the page ids of the next 32 pages, one a lane, then the masses of 16 x 32 tokens at a time
+      for (int p0 = j0 / kKvPage; p0 * kKvPage < j1; p0 += 32) {
+        int id = 0;
+        if ((int64_t)(p0 + lane) * kKvPage < j1) {
+          id = c.page_table[(int64_t)b * c.max_pages + p0 + lane];
+          if (id < 0 || id >= c.n_pages) bad = true, id = 0;
+        }
+        for (int q = 0; q < 32 && (p0 + q) * kKvPage < j1; q += 8) {
+          float m[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = i0 + 32 * i < j1 ? read(i0 + 32 * i) : 0;
+          for (int i = 0; i < 16; ++i) {
+            const int from = __shfl_sync(0xffffffffu, id, q + (i >> 1)), j = (p0 + q) * kKvPage + i * 32 + lane;
+            if (j >= j0 && j < j1) m[i] = e.mass[((int64_t)from * c.kv_heads + h) * kKvPage + j % kKvPage];
+          }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + 32 * i < j1) ranks[i0 + 32 * i - run0] = r[i];
+          for (int i = 0; i < 16; ++i) {
+            const int j = (p0 + q) * kKvPage + i * 32 + lane;
+            if (j >= j0 && j < j1) ranks[j - run0] = rank_of(m[i]);
+          }
+        }
       }
       __syncwarp();
     }
@@ -106,28 +119,39 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
       for (int i = tid; i < BINS; i += THREADS) bins[i] = 0;
       __syncthreads();
-      for (int j = max(j0, lo) + lane; j < min(j1, hi); j += 32) {
-        const uint32_t r = rank(j);
-        if ((r & mask) == least) atomicAdd(&bins[(r >> shift) & ((1u << width) - 1)], 1u);
+      // tokens without any mass may be many: a warp's are counted together, not one after another in one bin
+      const uint32_t digits = (1u << width) - 1, zero = 0x80000000u;
+      uint32_t zeros = 0;
+      const int k0 = max(j0, lo), k1 = min(j1, hi);
+      for (int j = k0 + lane; j - lane < k1; j += 8 * 32) {
+        uint32_t r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = j + 32 * i < k1 ? rank(j + 32 * i) : ~least;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool in = j + 32 * i < k1 && (r[i] & mask) == least;
+          if (in && r[i] != zero) atomicAdd(&bins[(r[i] >> shift) & digits], 1u);
+          zeros += in && r[i] == zero;
+        }
       }
+      zeros = __reduce_add_sync(0xffffffffu, zeros);
+      if (lane == 0 && zeros) atomicAdd(&bins[(zero >> shift) & digits], zeros);
       sync_all();
-      // four bins a thread, the highest first, over all blocks
+      // The digit from which on `want` tokens are counted, from above. Each block adds up its slice of the bins over the
+      // cluster, a slice's total goes to all blocks, and the block whose slice has the digit tells it.
+      const int slice = BINS / cluster, mine = BINS - slice * (me + 1);  // the first block has the highest bins
       uint32_t n[4] = {0, 0, 0, 0}, sum = 0;
-      const uint32_t at = smem_u32(&bins[BINS - 4 - 4 * tid]);
-      if (cluster > 1) {
+      if (4 * tid < slice) {
+        const uint32_t at = smem_u32(&bins[mine + slice - 4 - 4 * tid]);
         uint4 v[MAX_CLUSTER];  // all on their way at once
 #pragma unroll
         for (int k = 0; k < MAX_CLUSTER; ++k)
-          if (k < cluster) v[k] = ld_cluster_u32x4(map_to_rank(at, k));
+          if (k < cluster) v[k] = cluster > 1 ? ld_cluster_u32x4(map_to_rank(at, k)) : lds128(at);
 #pragma unroll
         for (int k = 0; k < MAX_CLUSTER; ++k)
           if (k < cluster) n[0] += v[k].w, n[1] += v[k].z, n[2] += v[k].y, n[3] += v[k].x;
-      } else {
-        const uint4 v = *reinterpret_cast<const uint4*>(&bins[BINS - 4 - 4 * tid]);
-        n[0] = v.w, n[1] = v.z, n[2] = v.y, n[3] = v.x;
+        sum = n[0] + n[1] + n[2] + n[3];
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum += n[i];
       const uint32_t own = sum;
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
@@ -135,11 +159,29 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       }
       if (lane == 31) warp_sum[warp] = sum;
       __syncthreads();
-      uint32_t above = sum - own;  // tokens of higher digits than this thread's
-      for (int w = 0; w < warp; ++w) above += warp_sum[w];
+      uint32_t above = sum - own, total = 0;  // tokens of higher digits than this thread's in the slice; of the slice
+      for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) above += warp_sum[w];
+        total += warp_sum[w];
+      }
+      if (cluster > 1) {
+        if (tid < cluster) st_cluster_u32(map_to_rank(smem_u32(&totals[me]), tid), total);
+        cluster_sync_all();
+        for (int k = 0; k < me; ++k) above += totals[k];
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (above < want && want <= above + n[i]) found[0] = BINS - 1 - 4 * tid - i, found[1] = want - above;
+        if (4 * tid < slice && above < want && want <= above + n[i]) {
+          const uint32_t digit = mine + slice - 1 - 4 * tid - i, rest = want - above;
+          for (int k = 0; k < cluster; ++k) {
+            if (cluster > 1) {
+              st_cluster_u32(map_to_rank(smem_u32(&found[0]), k), digit);
+              st_cluster_u32(map_to_rank(smem_u32(&found[1]), k), rest);
+            } else {
+              found[0] = digit, found[1] = rest;
+            }
+          }
+        }
         above += n[i];
       }
       sync_all();  // `found` is written, and no block reads another's bins any more
@@ -154,12 +196,21 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       *sure = j < j1 && (!middle || (!none && r > least));
       *level = j < j1 && middle && !none && r == least;
     };
+    // (their ballots stay in the bins' place, where they fit)
+    const bool fits = WARPS * per <= BINS / 2 * 32;
+    uint2* masks = reinterpret_cast<uint2*>(bins) + warp * (per / 32);
     int sures = 0, levels = 0;
-    for (int j = j0 + lane; j - lane < j1; j += 32) {
-      bool sure, level;
-      kind(j, &sure, &level);
-      sures += __popc(__ballot_sync(0xffffffffu, sure));
-      levels += __popc(__ballot_sync(0xffffffffu, level));
+    for (int j = j0 + lane; j - lane < j1; j += 4 * 32) {
+      bool sure[4], level[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kind(j + 32 * i, &sure[i], &level[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t sm = __ballot_sync(0xffffffffu, sure[i]), lm = __ballot_sync(0xffffffffu, level[i]);
+        sures += __popc(sm);
+        levels += __popc(lm);
+        if (fits && lane == 0 && j + 32 * i < j1) masks[(j - j0) / 32 + i] = make_uint2(sm, lm);
+      }
     }
     if (lane == 0) warp_count[warp] = make_int2(sures, levels);
     __syncthreads();
@@ -173,13 +224,20 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       levels += (int)ld_cluster_u32(map_to_rank(count_at, k) + 4);
     }
     for (int j = j0 + lane; j - lane < j1; j += 32) {
-      bool sure, level;
-      kind(j, &sure, &level);
-      const uint32_t sm = __ballot_sync(0xffffffffu, sure), lm = __ballot_sync(0xffffffffu, level), below = (1u << lane) - 1;
-      const int ls = levels + __popc(lm & below), at = sures + __popc(sm & below) + min(ls, (int)want);
+      uint2 m;
+      if (fits) {
+        m = masks[(j - j0) / 32];
+      } else {
+        bool sure, level;
+        kind(j, &sure, &level);
+        m = make_uint2(__ballot_sync(0xffffffffu, sure), __ballot_sync(0xffffffffu, level));
+      }
+      const uint32_t below = (1u << lane) - 1;
+      const int ls = levels + __popc(m.y & below), at = sures + __popc(m.x & below) + min(ls, (int)want);
+      const bool sure = m.x >> lane & 1, level = m.y >> lane & 1;
       if ((sure || (level && ls < (int)want)) && at < cap) list[at] = j;
-      sures += __popc(sm);
-      levels += __popc(lm);
+      sures += __popc(m.x);
+      levels += __popc(m.y);
     }
     sync_all();  // the list is written, and no block reads another's counts any more
   }
@@ -190,28 +248,34 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
   const int32_t* from = c.page_table + (int64_t)b * c.max_pages;
   const int32_t* to = e.into ? e.into + (int64_t)b * e.into_pages : from;
   const int row_of_part = part < PIECES ? 0 : kKvPage;
+  // the sources of the next chunk are looked up while this one's data is on its way
+  int src[BATCH];
+  const auto look = [&](int64_t first) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int64_t r = first + me * TOKENS * BATCH + worker + i * TOKENS;
+      src[i] = -1;
+      if (r < s.keeps) src[i] = cut ? list[r] : (int)r;
+      if (!e.into && src[i] == r) src[i] = -1;  // it stays
+    }
+  };
+  look(0);
   for (int64_t first = 0; first < s.keeps; first += (int64_t)cluster * TOKENS * BATCH) {
     const int64_t r0 = first + me * TOKENS * BATCH + worker;
     uint4 data[BATCH];
     uint2 par[BATCH];
     float mass[BATCH];
-    int src[BATCH], id[BATCH];
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int64_t r = r0 + i * TOKENS;
-      src[i] = -1;
-      if (r < s.keeps) src[i] = cut ? list[r] : (int)r;
-      if (!e.into && src[i] == r) src[i] = -1;  // it stays
-    }
+    int id[BATCH], low[BATCH];  // low: the source's place in its page, -1 for nothing
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       id[i] = src[i] >= 0 ? from[src[i] / kKvPage] : 0;
-      if (id[i] < 0 || id[i] >= c.n_pages) bad = true, src[i] = -1;
+      low[i] = src[i] >= 0 ? src[i] % kKvPage : -1;
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      if (src[i] < 0) continue;
-      const int t = src[i] % kKvPage;
+      if (id[i] < 0 || id[i] >= c.n_pages) bad = true, low[i] = -1;
+      if (low[i] < 0) continue;
+      const int t = low[i];
       const uint8_t* blk = c.pages + ((int64_t)id[i] * c.kv_heads + h) * BLK;
       const int row = part < PIECES ? kv4_rho(t) : row_of_part + t;
       data[i] = *reinterpret_cast<const uint4*>(blk + row * (D / 2) + part % PIECES * 16);
@@ -220,18 +284,19 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      id[i] = src[i] >= 0 ? to[(r0 + i * TOKENS) / kKvPage] : 0;
-      if (id[i] < 0 || id[i] >= c.n_pages) bad = true, src[i] = -1;
+      id[i] = low[i] >= 0 ? to[(r0 + i * TOKENS) / kKvPage] : 0;
+      if (id[i] < 0 || id[i] >= c.n_pages) bad = true, low[i] = -1;
     }
+    look(first + (int64_t)cluster * TOKENS * BATCH);
     if (!e.into) sync_all();
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      if (src[i] < 0) continue;
+      if (low[i] < 0) continue;
       const int r = (int)(r0 + i * TOKENS), t = r % kKvPage;
       uint8_t* blk = c.pages + ((int64_t)id[i] * c.kv_heads + h) * BLK;
       const int row = part < PIECES ? kv4_rho(t) : row_of_part + t;
       int piece = part % PIECES;
-      if (D == 128 && part >= PIECES && ((src[i] ^ r) & 2)) piece ^= 2;  // the halves of a wide value row
+      if (D == 128 && part >= PIECES && ((low[i] ^ r) & 2)) piece ^= 2;  // the halves of a wide value row
       *reinterpret_cast<uint4*>(blk + row * (D / 2) + piece * 16) = data[i];
       if (part == 0) *reinterpret_cast<uint2*>(blk + kKvPage * D + kv4_rho(t) * 8) = par[i];
       if (part == 1) e.mass[((int64_t)id[i] * c.kv_heads + h) * kKvPage + t] = mass[i];
@@ -259,7 +324,7 @@ cudaError_t launch_kv4_evict(const Kv4& c, int dim, const Kv4Evict& e, void* ws,
   const int64_t units = (int64_t)c.batch * c.kv_heads;
   // blocks of a cluster: as many as there is room for (four an SM), each with some thousand tokens
   int cluster = 1;
-  while (cluster < MAX_CLUSTER && units * cluster * 2 <= num_sms * 4 && c.max_kv > cluster * 1024) cluster *= 2;
+  while (cluster < MAX_CLUSTER && units * cluster * 2 <= num_sms * 2 && c.max_kv > cluster * 1024) cluster *= 2;
   int64_t per = ((c.max_kv + cluster * WARPS - 1) / (cluster * WARPS) + 31) / 32 * 32;
   const int ranks = (int)(per * WARPS < MAX_RANKS ? per * WARPS : MAX_RANKS);
   const bool over = e.new_len == c.kv_len;
