@@ -89,22 +89,23 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     const bool keep = WARPS * per <= ranks_kept;
     const auto read = [&](int j) { return rank_of(*mass_of(c, e, b, h, j, &bad)); };
     if (keep && want) {
-      // the page ids of the next 32 pages, one a lane, then the masses of 16 x 32 tokens at a time
+      // the page ids of the next 32 pages, one a lane, then the masses of 8 x 32 tokens at a time
       for (int p0 = j0 / kKvPage; p0 * kKvPage < j1; p0 += 32) {
         int id = 0;
         if ((int64_t)(p0 + lane) * kKvPage < j1) {
           id = c.page_table[(int64_t)b * c.max_pages + p0 + lane];
           if (id < 0 || id >= c.n_pages) bad = true, id = 0;
         }
-        for (int q = 0; q < 32 && (p0 + q) * kKvPage < j1; q += 8) {
-          float m[16];
+#pragma unroll 1
+        for (int q = 0; q < 32 && (p0 + q) * kKvPage < j1; q += 4) {
+          float m[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 8; ++i) {
             const int from = __shfl_sync(0xffffffffu, id, q + (i >> 1)), j = (p0 + q) * kKvPage + i * 32 + lane;
             if (j >= j0 && j < j1) m[i] = e.mass[((int64_t)from * c.kv_heads + h) * kKvPage + j % kKvPage];
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 8; ++i) {
             const int j = (p0 + q) * kKvPage + i * 32 + lane;
             if (j >= j0 && j < j1) ranks[j - run0] = rank_of(m[i]);
           }
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     const auto rank = [&](int j) { return keep ? ranks[j - run0] : read(j); };
     uint32_t least = 0, mask = 0;  // the digits found so far
     const bool none = want == 0;
+#pragma unroll 1
     for (int pass = 0; !none && pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
       for (int i = tid; i < BINS; i += THREADS) bins[i] = 0;
@@ -123,12 +125,13 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       const uint32_t digits = (1u << width) - 1, zero = 0x80000000u;
       uint32_t zeros = 0;
       const int k0 = max(j0, lo), k1 = min(j1, hi);
-      for (int j = k0 + lane; j - lane < k1; j += 8 * 32) {
-        uint32_t r[8];
+#pragma unroll 1
+      for (int j = k0 + lane; j - lane < k1; j += 4 * 32) {
+        uint32_t r[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = j + 32 * i < k1 ? rank(j + 32 * i) : ~least;
+        for (int i = 0; i < 4; ++i) r[i] = j + 32 * i < k1 ? rank(j + 32 * i) : ~least;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const bool in = j + 32 * i < k1 && (r[i] & mask) == least;
           if (in && r[i] != zero) atomicAdd(&bins[(r[i] >> shift) & digits], 1u);
           zeros += in && r[i] == zero;
@@ -143,13 +146,15 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       uint32_t n[4] = {0, 0, 0, 0}, sum = 0;
       if (4 * tid < slice) {
         const uint32_t at = smem_u32(&bins[mine + slice - 4 - 4 * tid]);
-        uint4 v[MAX_CLUSTER];  // all on their way at once
+#pragma unroll 1
+        for (int k = 0; k < cluster; k += 4) {
+          uint4 v[4] = {};
 #pragma unroll
-        for (int k = 0; k < MAX_CLUSTER; ++k)
-          if (k < cluster) v[k] = cluster > 1 ? ld_cluster_u32x4(map_to_rank(at, k)) : lds128(at);
+          for (int i = 0; i < 4; ++i)
+            if (k + i < cluster) v[i] = ld_cluster_u32x4(map_to_rank(at, k + i));
 #pragma unroll
-        for (int k = 0; k < MAX_CLUSTER; ++k)
-          if (k < cluster) n[0] += v[k].w, n[1] += v[k].z, n[2] += v[k].y, n[3] += v[k].x;
+          for (int i = 0; i < 4; ++i) n[0] += v[i].w, n[1] += v[i].z, n[2] += v[i].y, n[3] += v[i].x;
+        }
         sum = n[0] + n[1] + n[2] + n[3];
       }
       const uint32_t own = sum;
@@ -160,9 +165,10 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       if (lane == 31) warp_sum[warp] = sum;
       __syncthreads();
       uint32_t above = sum - own, total = 0;  // tokens of higher digits than this thread's in the slice; of the slice
-      for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) above += warp_sum[w];
-        total += warp_sum[w];
+      {
+        const uint32_t x = lane < WARPS ? warp_sum[lane] : 0;
+        total = __reduce_add_sync(0xffffffffu, x);
+        above += __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
       }
       if (cluster > 1) {
         if (tid < cluster) st_cluster_u32(map_to_rank(smem_u32(&totals[me]), tid), total);
@@ -173,13 +179,10 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       for (int i = 0; i < 4; ++i) {
         if (4 * tid < slice && above < want && want <= above + n[i]) {
           const uint32_t digit = mine + slice - 1 - 4 * tid - i, rest = want - above;
+#pragma unroll 1
           for (int k = 0; k < cluster; ++k) {
-            if (cluster > 1) {
-              st_cluster_u32(map_to_rank(smem_u32(&found[0]), k), digit);
-              st_cluster_u32(map_to_rank(smem_u32(&found[1]), k), rest);
-            } else {
-              found[0] = digit, found[1] = rest;
-            }
+            st_cluster_u32(map_to_rank(smem_u32(&found[0]), k), digit);
+            st_cluster_u32(map_to_rank(smem_u32(&found[1]), k), rest);
           }
         }
         above += n[i];
@@ -214,8 +217,10 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     }
     if (lane == 0) warp_count[warp] = make_int2(sures, levels);
     __syncthreads();
-    sures = levels = 0;
-    for (int w = 0; w < warp; ++w) sures += warp_count[w].x, levels += warp_count[w].y;
+    {
+      const int2 x = lane < warp ? warp_count[lane] : make_int2(0, 0);
+      sures = (int)__reduce_add_sync(0xffffffffu, (unsigned)x.x), levels = (int)__reduce_add_sync(0xffffffffu, (unsigned)x.y);
+    }
     if (tid == THREADS - 1) block_count = make_int2(sures + warp_count[warp].x, levels + warp_count[warp].y);
     sync_all();
     const uint32_t count_at = smem_u32(&block_count);
