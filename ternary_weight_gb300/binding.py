@@ -543,6 +543,29 @@ def _kv4_setup():
     return _kv4_torch
 
 
+_on_device = None  # (torch, its dtypes -> BITNET dtypes, stream handle by device index and stream)
+
+
+def _on_device_setup():
+    global _on_device
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        def raw(index):
+            return torch.cuda.current_stream(index).cuda_stream
+    current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+    def handle(index, stream):
+        """The stream's handle, where tensors on device `index` can be used on it."""
+        if current() != index:
+            raise ValueError("the tensors' device must be the current one")
+        return raw(index) if stream is None else stream.cuda_stream
+
+    _on_device = torch, {torch.float32: BITNET_F32, torch.bfloat16: BITNET_BF16}, handle
+    return _on_device
+
+
 def _kv4_rows(t, rows, heads, dim, index):
     """Checks a rows x heads x dim tensor on device `index` whose heads lie one after another; its row stride."""
     if t.shape != (rows, heads, dim):
@@ -799,41 +822,49 @@ class Rope:
         self._ref = ctypes.c_void_p(ctypes.addressof(self._desc))
 
 
-def _rope_rows(t, out, rows, dim, index, torch, stream):
-    """An operand's checks: its heads and strides, and its output (allocated if not given)."""
-    heads = t.shape[1]
-    ins = _kv4_rows(t, rows, heads, dim, index)
-    if out is None:
-        return heads, ins, _kv4_empty(torch, (rows, heads, dim), t.dtype, t.device, stream), heads * dim
-    if out.dtype != t.dtype:
-        raise ValueError("an output must have its input's dtype")
-    return heads, ins, out, _kv4_rows(out, rows, heads, dim, index)
-
-
 def rope(table, positions, q, k=None, q_out=None, k_out=None, stream=None):
     """Turn queries (rows x q_heads x head_dim, fp32 or bf16 CUDA, rows may be strided) and, if given,
     keys (rows x kv_heads x head_dim) by the positions (rows, int32) of their rows, in one launch. Returns
     the turned q, or (q, k): new tensors, or ``q_out`` and ``k_out``, which may be the inputs themselves."""
-    import torch
-
-    dt = BITNET_F32 if q.dtype == torch.float32 else BITNET_BF16 if q.dtype == torch.bfloat16 else None
-    if dt is None or (k is not None and k.dtype != q.dtype):
-        raise ValueError("q and k must both be float32 or bfloat16")
-    if q.dim() != 3 or (k is not None and k.dim() != 3) or (k is None and k_out is not None):
-        raise ValueError("q and k must be rows x heads x head_dim")
-    rows, dim, index = q.shape[0], q.shape[2], table.index
+    torch, dtypes, handle = _on_device or _on_device_setup()
+    dtype, shape, index = q.dtype, q.shape, table.index
+    dt = dtypes.get(dtype)
+    if dt is None or len(shape) != 3:
+        raise ValueError("q must be rows x q_heads x head_dim, float32 or bfloat16")
+    rows, qh, dim = shape
     if positions.dtype != torch.int32 or positions.shape != (rows,) or positions.get_device() != index or \
             not positions.is_contiguous():
         raise ValueError("positions must be an int32 for each row, contiguous, on the table's device")
-    if torch.cuda.current_device() != index:
-        raise ValueError("the table's device must be the current one")
-    qh, qs, q_out, qos = _rope_rows(q, q_out, rows, dim, index, torch, stream)
+    on = handle(index, stream)
+    qs = qos = _kv4_rows(q, rows, qh, dim, index)
+    if q_out is None:
+        q_out, qos = _kv4_empty(torch, shape, dtype, q.device, stream), qh * dim
+    elif q_out is not q:
+        if q_out.dtype != dtype:
+            raise ValueError("an output must have its input's dtype")
+        qos = _kv4_rows(q_out, rows, qh, dim, index)
     kh = ks = kos = 0
+    k_in = k_to = None
     if k is not None:
-        kh, ks, k_out, kos = _rope_rows(k, k_out, rows, dim, index, torch, stream)
+        shape = k.shape
+        if k.dtype != dtype or len(shape) != 3:
+            raise ValueError("k must be rows x kv_heads x head_dim of q's dtype")
+        kh = shape[1]
+        ks = kos = _kv4_rows(k, rows, kh, dim, index)
+        if k_out is None:
+            k_out, kos = _kv4_empty(torch, shape, dtype, k.device, stream), kh * dim
+        elif k_out is not k:
+            if k_out.dtype != dtype:
+                raise ValueError("an output must have its input's dtype")
+            kos = _kv4_rows(k_out, rows, kh, dim, index)
+        k_in, k_to = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     if rows:
-        _check(lib().bitnet_rope(table._ref, positions.data_ptr(), rows, q.data_ptr(), qh, qs, q_out.data_ptr(), qos,
-                                 _ptr(k), kh, ks, _ptr(k_out), kos, dim, dt, _stream(stream)), "bitnet_rope")
+        st = lib().bitnet_rope(table._ref, positions.data_ptr(), rows, q.data_ptr(), qh, qs, q_out.data_ptr(), qos, k_in, kh, ks, k_to,
+                               kos, dim, dt, on)
+        if st:
+            raise BitnetError(st, "bitnet_rope")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -853,42 +884,43 @@ def w4_quant_weight(w, group=128, with_zeros=False, codes=None, scales=None, zer
     scales = _kv4_empty(torch, groups, torch.float16, w.device, stream) if scales is None else scales
     if with_zeros and zeros is None:
         zeros = _kv4_empty(torch, groups, torch.uint8, w.device, stream)
-    _w4_check(torch, w, codes, scales, zeros, None)
-    _check(lib().bitnet_w4_quant_weight(_ptr(w), dt, N, K, group, _ptr(codes), _ptr(scales), _ptr(zeros), _stream(stream)),
-           "bitnet_w4_quant_weight")
+    on = (_on_device or _on_device_setup())[2](_w4_check(w, codes, scales, zeros, None)[5], stream)
+    _check(lib().bitnet_w4_quant_weight(_ptr(w), dt, N, K, group, _ptr(codes), _ptr(scales), _ptr(zeros), on), "bitnet_w4_quant_weight")
     return codes, scales, zeros
 
 
-def _w4_check(torch, x, codes, scales, zeros, out):
-    """Checks of what both calls have; the group."""
-    N, K = codes.shape[0], codes.shape[1] * 2
-    if codes.dtype != torch.uint8 or scales.dtype != torch.float16 or scales.dim() != 2 or scales.shape[0] != N or \
-            scales.shape[1] == 0 or K % scales.shape[1]:
+def _w4_check(x, codes, scales, zeros, out):
+    """Checks of what both calls have; (torch, rows, N, K, group, index)."""
+    torch = (_on_device or _on_device_setup())[0]
+    (N, half), (n, groups), (M, K) = codes.shape, scales.shape, x.shape
+    if codes.dtype != torch.uint8 or scales.dtype != torch.float16 or n != N or groups == 0 or 2 * half % groups:
         raise ValueError("codes must be N x K/2 uint8 and scales N x K/group float16")
-    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != (n, groups)):
         raise ValueError("zeros must be uint8 of the scales' shape")
-    if x.dim() != 2 or x.shape[1] != K:
-        raise ValueError("expected rows of %d numbers" % K)
-    if out is not None and (out.dtype != torch.float32 or out.shape != (x.shape[0], N)):
+    if K != 2 * half:
+        raise ValueError("expected rows of %d numbers" % (2 * half))
+    if out is not None and (out.dtype != torch.float32 or out.shape != (M, N)):
         raise ValueError("out must be M x N float32")
-    _require_cuda(x, codes, scales, zeros, out)
     index = x.get_device()
-    if any(t is not None and t.get_device() != index for t in (codes, scales, zeros, out)):
-        raise ValueError("tensors must be on one device")
-    if torch.cuda.current_device() != index:
-        raise ValueError("the tensors' device must be the current one")
-    return K // scales.shape[1]
+    for t in (x, codes, scales, zeros, out):
+        if t is not None and (t.get_device() != index or index < 0 or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous, on one CUDA device")
+    return torch, M, N, K, K // groups, index
 
 
 def w4_matmul(x, codes, scales, zeros=None, out=None, stream=None):
     """x (M x K fp32 or bf16 CUDA) times 4-bit weights with group scales (see ``w4_quant_weight``): M x N fp32."""
-    import torch
-
-    dt = _act_dtype(x)
-    group = _w4_check(torch, x, codes, scales, zeros, out)
-    M, N = x.shape[0], codes.shape[0]
-    out = _kv4_empty(torch, (M, N), torch.float32, x.device, stream) if out is None else out
+    _, dtypes, handle = _on_device or _on_device_setup()
+    dt = dtypes.get(x.dtype)
+    if dt is None or x.dim() != 2 or codes.dim() != 2 or scales.dim() != 2:
+        raise ValueError("x must be M x K float32 or bfloat16, codes N x K/2, scales N x K/group")
+    torch, M, N, K, group, index = _w4_check(x, codes, scales, zeros, out)
+    on = handle(index, stream)
+    if out is None:
+        out = _kv4_empty(torch, (M, N), torch.float32, x.device, stream)
     if M:
-        _check(lib().bitnet_w4_matmul(_ptr(x), dt, M, x.shape[1], _ptr(codes), _ptr(scales), _ptr(zeros), N, group,
-                                      _ptr(out), _stream(stream)), "bitnet_w4_matmul")
+        st = lib().bitnet_w4_matmul(x.data_ptr(), dt, M, K, codes.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None else None,
+                                    N, group, out.data_ptr(), on)
+        if st:
+            raise BitnetError(st, "bitnet_w4_matmul")
     return out

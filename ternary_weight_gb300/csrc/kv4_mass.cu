@@ -415,6 +415,129 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_votes(Kv4 c
   if (bad) record_device_error(kErrRange);
 }
 
+// ------------------------------------------------------------- few columns, short enough: one kernel
+// A cluster of one to eight blocks takes a unit; its blocks keep the scores of their tiles in shared memory, exchange
+// their (M, L) through distributed shared memory, and add up the votes from the scores: a thread a token.
+constexpr int kScoreBytes = 64 * 1024;  // of a block: three blocks an SM
+struct Cluster {
+  int blocks;   // of a cluster
+  int tiles;    // of a block, at most
+  int rows;     // of scores a token
+};
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4 c, Kv4Attn a, Kv4Mass ms, Cluster cl) {
+  extern __shared__ __align__(16) float kept[];  // token, row
+  __shared__ Shared<D, NT> sh;
+  __shared__ float2 mine[NT * 8];  // this block's (M, L) of each column
+  constexpr int COLS = NT * 8, PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+  const int unit = blockIdx.x / cl.blocks, me = cl.blocks > 1 ? (int)cluster_ctarank() : 0;
+  bool bad = false;
+  const Rows r = rows_of(c, unit, ms.voters, &bad);
+  const int rows = r.votes * a.share, all = (r.s.len + TILE - 1) / TILE, per = (all + cl.blocks - 1) / cl.blocks;
+  if (bad && threadIdx.x == 0) record_device_error(kErrRange);
+  if (rows == 0 || all == 0) return;
+  const int tile0 = min(me * per, all), tile1 = min(tile0 + per, all), first = r.position(0), last = r.position(r.votes - 1);
+  const int32_t* table = c.page_table + (int64_t)r.b * c.max_pages;
+  const auto page_of = [&](int tile) {
+    const int id = table[tile / 2];
+    if (id >= 0 && id < c.n_pages) return id;
+    record_device_error(kErrRange);
+    return -1;
+  };
+  int ahead = tile0 + warp < tile1 ? page_of(tile0 + warp) : -1;
+  load_columns<D, NT, F32>(a, r, 0, sh);
+  __syncthreads();
+  const int eights = min(NT, (rows * PARTS + 7) / 8);
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf, l[n][0] = l[n][1] = 0.0f;
+  Codes<D> cur;
+  if (ahead >= 0) cur.load(c.pages + ((int64_t)ahead * c.kv_heads + r.h) * BLK, tile0 + warp, g, t);
+#pragma unroll 1
+  for (int tile = tile0 + warp; tile < tile1; tile += WARPS) {
+    const Codes<D> now = cur;
+    const int id = ahead;
+    if (tile + WARPS < tile1) {
+      ahead = page_of(tile + WARPS);
+      if (ahead >= 0) cur.load(c.pages + ((int64_t)ahead * c.kv_heads + r.h) * BLK, tile + WARPS, g, t);
+    }
+    const int j0 = tile * TILE, sees = id < 0 ? 0 : seen(a, first, last, j0, TILE);
+    if (sees == 0) continue;
+    float* to = kept + (int64_t)(tile - tile0) * TILE * cl.rows;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (n >= eights) break;
+      float d[2][4];
+      products<D, NT>(now, 0, sh, n, lane, d[0]);
+      products<D, NT>(now, 1, sh, n, lane, d[1]);
+#pragma unroll
+      for (int e = 0; e < (F32 ? 1 : 2); ++e) {
+        const Column& col = sh.col[n * 8 + 2 * t + e];
+        const int row = (n * 8 + 2 * t + e) / PARTS;
+        float x[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int mt = v >> 1, h = v & 1, in = token_of(mt * 16 + h * 8 + g);
+          const float raw = F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e];
+          x[v] = score(raw, col, params(now.par[mt][h]));
+          if (sees == 1 && !visible(a, col.p, j0 + in)) x[v] = kNegInf;
+          if (row < cl.rows) to[in * cl.rows + row] = x[v];
+        }
+        const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m[n][e]), from = top == kNegInf ? 0.0f : top;
+        l[n][e] = fmaf(l[n][e], exp2_approx(m[n][e] - from), (exp2_approx(x[0] - from) + exp2_approx(x[1] - from)) + (exp2_approx(x[2] - from) + exp2_approx(x[3] - from)));
+        m[n][e] = top;
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1)
+        join(m[n][e], l[n][e], __shfl_xor_sync(0xffffffffu, m[n][e], o), __shfl_xor_sync(0xffffffffu, l[n][e], o));
+      if (g == 0) sh.part[warp][n * 8 + 2 * t + e] = make_float2(m[n][e], l[n][e]);
+    }
+  __syncthreads();
+  if (threadIdx.x < COLS) {
+    float2 v = sh.part[0][threadIdx.x];
+#pragma unroll 1
+    for (int w = 1; w < WARPS; ++w) join(v.x, v.y, sh.part[w][threadIdx.x].x, sh.part[w][threadIdx.x].y);
+    mine[threadIdx.x] = v;
+  }
+  if (cl.blocks > 1) cluster_sync_all();
+  else __syncthreads();
+  if (threadIdx.x < COLS) {  // all blocks' in the same order
+    float top = kNegInf, sum = 0.0f;
+    const uint32_t at = smem_u32(&mine[threadIdx.x]);
+#pragma unroll 1
+    for (int k = 0; k < cl.blocks; ++k) join(top, sum, ld_cluster_f32(map_to_rank(at, k)), ld_cluster_f32(map_to_rank(at, k) + 4));
+    sh.part[0][threadIdx.x] = make_float2(top == kNegInf ? 0.0f : top, sum == 0.0f ? 0.0f : __frcp_rn(sum));
+  }
+  if (cl.blocks > 1) cluster_sync_all();  // no block leaves while another reads its sums
+  else __syncthreads();
+  // the votes: a thread a token
+  const int old = r.s.len - r.s.n, end = min(tile1 * TILE, r.s.len);
+#pragma unroll 1
+  for (int j = tile0 * TILE + threadIdx.x; j < end; j += THREADS) {
+    const int id = page_of(j / TILE), sees = seen(a, first, last, j & ~(TILE - 1), TILE);
+    if (id < 0 || (sees == 0 && ms.decay == 1.0f && ms.in == ms.out && j < old)) continue;
+    const int64_t at = ((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage;
+    const float before = j < old ? ms.in[at] : 0.0f;
+    float votes = 0.0f;
+    if (sees) {
+      const float* x = kept + (int64_t)(j - tile0 * TILE) * cl.rows;
+      for (int row = 0; row < rows; ++row) {
+        const float2 ml = sh.part[0][row * PARTS];
+        // a masked score is -inf; it takes no part, whatever the row's sum is
+        if (x[row] != kNegInf) votes = fmaf(exp2_approx(x[row] - ml.x), ml.y, votes);
+      }
+    }
+    ms.out[at] = j < old ? fmaf(ms.decay, before, votes) : votes;
+  }
+}
+
 // ------------------------------------------------------------- many columns
 constexpr float kLeastA = 7.888609052210118e-31f, kMostA = 3.4028234663852886e38f;  // 2^-100, the greatest
 // what the second kernel needs of a row: -M (0 where it sees nothing) and 1 / L, twice
@@ -884,7 +1007,8 @@ Plan plan_of(const Kv4& c, int share, int voters, bool f32, int num_sms) {
   p.blocks = (int)((cols + p.nt * 8 - 1) / (p.nt * 8));
   p.tiles = (c.max_kv + TILE - 1) / TILE;
   // a chunk: as many tiles as leave each SM several blocks
-  int64_t per = (units * p.blocks * p.tiles + (int64_t)num_sms * 4 * WARPS - 1) / ((int64_t)num_sms * 4 * WARPS);
+  const int64_t slots = (int64_t)num_sms * (p.nt == 1 ? 3 : p.nt == 2 ? 2 : 4) * WARPS;
+  int64_t per = (units * p.blocks * p.tiles + slots - 1) / slots;
   per = per < 1 ? 1 : per > MAX_CHUNK / WARPS ? MAX_CHUNK / WARPS : per;
   p.chunk = (int)per * WARPS;
   p.chunks = (p.tiles + p.chunk - 1) / p.chunk;
@@ -904,8 +1028,36 @@ int64_t slabs_bytes(const Kv4& c, const Plan& p, int dim) {
   return p.shares ? align256((int64_t)c.batch * c.kv_heads * p.blocks * (int64_t)(dim == 128 ? sizeof(Slab<128>) : sizeof(Slab<64>))) : 0;
 }
 
+// The clusters that take the units, if their blocks' scores fit: no more blocks than that needs, but enough to fill the GPU.
+Cluster cluster_of(const Kv4& c, const Plan& p, int share, int num_sms) {
+  Cluster k{1, 0, p.votes * share};
+  const int64_t units = (int64_t)c.batch * c.kv_heads, row_bytes = (int64_t)k.rows * 4 * TILE;
+  const auto bytes = [&](int n) { return (p.tiles + n - 1) / n * row_bytes; };
+  while (k.blocks < 8 && (bytes(k.blocks) > kScoreBytes || (units * k.blocks * 2 <= num_sms * 3 && p.tiles > k.blocks * 2 * WARPS))) k.blocks *= 2;
+  k.tiles = bytes(k.blocks) > kScoreBytes ? 0 : (p.tiles + k.blocks - 1) / k.blocks;
+  return k;
+}
+template <int D, int NT, bool F32>
+cudaError_t launch_cluster(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Cluster& k, cudaStream_t st) {
+  auto kernel = kv4_mass_cluster<D, NT, F32>;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreBytes)) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = k.blocks, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(c.batch * c.kv_heads * k.blocks));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = (size_t)k.tiles * TILE * k.rows * 4;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, c, a, m, k);
+}
+
 template <int D, int NT, bool F32>
 cudaError_t launch_few(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
+  const Cluster k = cluster_of(c, p, a.share, 152);
+  if (k.tiles) return launch_cluster<D, NT, F32>(c, a, m, k, st);
   const int64_t units = (int64_t)c.batch * c.kv_heads;
   kv4_mass_rows<D, NT, F32><<<grid_of(units * p.chunks), THREADS, 0, st>>>(c, a, m.voters, p, s);
   if (cudaError_t e = cudaGetLastError()) return e;
