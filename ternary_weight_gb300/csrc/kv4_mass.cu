@@ -435,17 +435,23 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
   bool bad = false;
   const Rows r = rows_of(c, unit, ms.voters, &bad);
   const int rows = r.votes * a.share, all = (r.s.len + TILE - 1) / TILE, per = (all + cl.blocks - 1) / cl.blocks;
-  if (bad && threadIdx.x == 0) record_device_error(kErrRange);
-  if (rows == 0 || all == 0) return;
+  if (rows == 0 || all == 0) {
+    if (bad && threadIdx.x == 0) record_device_error(kErrRange);
+    return;
+  }
   const int tile0 = min(me * per, all), tile1 = min(tile0 + per, all), first = r.position(0), last = r.position(r.votes - 1);
+  // the page ids of this warp's next 32 tiles, one a lane (-1: not in the pool)
   const int32_t* table = c.page_table + (int64_t)r.b * c.max_pages;
-  const auto page_of = [&](int tile) {
-    const int id = table[tile / 2];
-    if (id >= 0 && id < c.n_pages) return id;
-    record_device_error(kErrRange);
-    return -1;
+  const auto ids_of = [&](int k) {
+    const int tile = tile0 + warp + (k + lane) * WARPS;
+    int id = -1;
+    if (tile < tile1) {
+      id = table[tile / 2];
+      if (id < 0 || id >= c.n_pages) bad = true, id = -1;
+    }
+    return id;
   };
-  int ahead = tile0 + warp < tile1 ? page_of(tile0 + warp) : -1;
+  int ids = ids_of(0);
   load_columns<D, NT, F32>(a, r, 0, sh);
   __syncthreads();
   const int eights = min(NT, (rows * PARTS + 7) / 8);
@@ -453,15 +459,18 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
 #pragma unroll
   for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf, l[n][0] = l[n][1] = 0.0f;
   Codes<D> cur;
-  if (ahead >= 0) cur.load(c.pages + ((int64_t)ahead * c.kv_heads + r.h) * BLK, tile0 + warp, g, t);
+  const auto load = [&](int k) {
+    const int id = __shfl_sync(0xffffffffu, ids, k & 31), tile = tile0 + warp + k * WARPS;
+    if (id >= 0) cur.load(c.pages + ((int64_t)id * c.kv_heads + r.h) * BLK, tile, g, t);
+    return id;
+  };
+  int ahead = load(0);
 #pragma unroll 1
-  for (int tile = tile0 + warp; tile < tile1; tile += WARPS) {
+  for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
     const Codes<D> now = cur;
     const int id = ahead;
-    if (tile + WARPS < tile1) {
-      ahead = page_of(tile + WARPS);
-      if (ahead >= 0) cur.load(c.pages + ((int64_t)ahead * c.kv_heads + r.h) * BLK, tile + WARPS, g, t);
-    }
+    if ((k & 31) == 31) ids = ids_of(k + 1);
+    ahead = load(k + 1);
     const int j0 = tile * TILE, sees = id < 0 ? 0 : seen(a, first, last, j0, TILE);
     if (sees == 0) continue;
     float* to = kept + (int64_t)(tile - tile0) * TILE * cl.rows;
@@ -517,25 +526,40 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
   }
   if (cl.blocks > 1) cluster_sync_all();  // no block leaves while another reads its sums
   else __syncthreads();
-  // the votes: a thread a token
-  const int old = r.s.len - r.s.n, end = min(tile1 * TILE, r.s.len);
+  // the votes: a lane a token of the warp's tiles, the masses of four tiles on their way at once
+  const int old = r.s.len - r.s.n;
+  ids = ids_of(0);
 #pragma unroll 1
-  for (int j = tile0 * TILE + threadIdx.x; j < end; j += THREADS) {
-    const int id = page_of(j / TILE), sees = seen(a, first, last, j & ~(TILE - 1), TILE);
-    if (id < 0 || (sees == 0 && ms.decay == 1.0f && ms.in == ms.out && j < old)) continue;
-    const int64_t at = ((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage;
-    const float before = j < old ? ms.in[at] : 0.0f;
-    float votes = 0.0f;
-    if (sees) {
-      const float* x = kept + (int64_t)(j - tile0 * TILE) * cl.rows;
-      for (int row = 0; row < rows; ++row) {
-        const float2 ml = sh.part[0][row * PARTS];
-        // a masked score is -inf; it takes no part, whatever the row's sum is
-        if (x[row] != kNegInf) votes = fmaf(exp2_approx(x[row] - ml.x), ml.y, votes);
-      }
+  for (int k = 0; tile0 + warp + k * WARPS < tile1; k += 4) {
+    if (k && (k & 31) == 0) ids = ids_of(k);
+    int64_t at[4];
+    float before[4];
+    bool writes[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int id = __shfl_sync(0xffffffffu, ids, (k + i) & 31), j = (tile0 + warp + (k + i) * WARPS) * TILE + lane;
+      const bool some = seen(a, first, last, j - lane, TILE) != 0;
+      writes[i] = id >= 0 && j < r.s.len && (some || ms.decay != 1.0f || ms.in != ms.out || j >= old);
+      at[i] = ((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage;
+      before[i] = writes[i] && j < old ? ms.in[at[i]] : 0.0f;
     }
-    ms.out[at] = j < old ? fmaf(ms.decay, before, votes) : votes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!writes[i]) continue;
+      const int tile = tile0 + warp + (k + i) * WARPS, j = tile * TILE + lane;
+      float votes = 0.0f;
+      if (seen(a, first, last, tile * TILE, TILE)) {
+        const float* x = kept + (int64_t)((tile - tile0) * TILE + lane) * cl.rows;
+        for (int row = 0; row < rows; ++row) {
+          const float2 ml = sh.part[0][row * PARTS];
+          // a masked score is -inf; it takes no part, whatever the row's sum is
+          if (x[row] != kNegInf) votes = fmaf(exp2_approx(x[row] - ml.x), ml.y, votes);
+        }
+      }
+      ms.out[at[i]] = j < old ? fmaf(ms.decay, before[i], votes) : votes;
+    }
   }
+  if (bad) record_device_error(kErrRange);
 }
 
 // ------------------------------------------------------------- many columns
