@@ -59,6 +59,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the first of a chain of products: the sum begins at 0
+__device__ __forceinline__ void mma_first(float (&d)[4], uint4 a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -184,16 +190,20 @@ struct Codes {
 // the token (of its page half) in row `row` of a tile
 __device__ __forceinline__ int token_of(int row) { return kv4_rho_inv(row); }
 
-// Scores of one m16 x n8: the lane has rows g and g + 8, columns 2 t and 2 t + 1 (fp32 queries: one row's parts).
+// Products of a tile's two m16 x n8: the lane has rows mt * 16 + g and + 8, columns 2 t and 2 t + 1 (fp32 queries: one
+// row's parts).
 template <int D, int NT>
-__device__ __forceinline__ void products(const Codes<D>& k, int mt, const Shared<D, NT>& sh, int n, int lane, float (&d)[4]) {
-  d[0] = d[1] = d[2] = d[3] = 0.0f;
+__device__ __forceinline__ void products(const Codes<D>& k, const Shared<D, NT>& sh, int n, int lane, float (&d)[2][4]) {
 #pragma unroll
   for (int i = 0; i < Codes<D>::WORDS; ++i) {
     const uint4 f = sh.frag[n][i][lane];
-    const uint32_t a = k.w[mt][0][i], b = k.w[mt][1][i], a8 = a >> 8, b8 = b >> 8;
-    mma16816(d, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, f.x, f.y);
-    mma16816(d, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, f.z, f.w);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const uint32_t a = k.w[mt][0][i], b = k.w[mt][1][i], a8 = a >> 8, b8 = b >> 8;
+      if (i == 0) mma_first(d[mt], make_uint4(a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u), f.x, f.y);
+      else mma16816(d[mt], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, f.x, f.y);
+      mma16816(d[mt], a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, f.z, f.w);
+    }
   }
 }
 __device__ __forceinline__ float score(float raw, const Column& c, float2 par) {
@@ -259,16 +269,14 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
     };
     load(0);
     for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
-      const Codes<D> now = cur;
-      if (k < 31) load(k + 1);
       const int j0 = tile * TILE, sees = seen(a, first, last, j0, TILE);
-      if (sees == 0) continue;
+      const float2 par[4] = {params(cur.par[0][0]), params(cur.par[0][1]), params(cur.par[1][0]), params(cur.par[1][1])};
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (n >= eights) break;
         float d[2][4];
-        products<D, NT>(now, 0, sh, n, lane, d[0]);
-        products<D, NT>(now, 1, sh, n, lane, d[1]);
+        if (n < eights) products<D, NT>(cur, sh, n, lane, d);
+        if (n == NT - 1 && k < 31) load(k + 1);  // the codes' registers are free
+        if (n >= eights || sees == 0) continue;
 #pragma unroll
         for (int e = 0; e < (F32 ? 1 : 2); ++e) {
           const Column& col = sh.col[n * 8 + 2 * t + e];
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
           for (int v = 0; v < 4; ++v) {
             const int mt = v >> 1, h = v & 1;
             const float raw = F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e];
-            x[v] = score(raw, col, params(now.par[mt][h]));
+            x[v] = score(raw, col, par[v]);
             if (sees == 1 && !visible(a, col.p, j0 + token_of(mt * 16 + h * 8 + g))) x[v] = kNegInf;
           }
           const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m[n][e]), from = top == kNegInf ? 0.0f : top;
@@ -336,8 +344,7 @@ __device__ __forceinline__ void add_votes(const Kv4Attn& a, const Codes<D>& k, c
   for (int n = 0; n < NT; ++n) {
     if (n >= eights) break;
     float d[2][4];
-    products<D, NT>(k, 0, sh, n, lane, d[0]);
-    products<D, NT>(k, 1, sh, n, lane, d[1]);
+    products<D, NT>(k, sh, n, lane, d);
 #pragma unroll
     for (int e = 0; e < (F32 ? 1 : 2); ++e) {
       const Column& col = sh.col[n * 8 + 2 * t + e];
@@ -460,26 +467,23 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
   for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf, l[n][0] = l[n][1] = 0.0f;
   Codes<D> cur;
   const auto load = [&](int k) {
-    const int id = __shfl_sync(0xffffffffu, ids, k & 31), tile = tile0 + warp + k * WARPS;
-    if (id >= 0) cur.load(c.pages + ((int64_t)id * c.kv_heads + r.h) * BLK, tile, g, t);
+    const int id = __shfl_sync(0xffffffffu, ids, k & 31);
+    if (id >= 0) cur.load(c.pages + ((int64_t)id * c.kv_heads + r.h) * BLK, tile0 + warp + k * WARPS, g, t);
     return id;
   };
   int ahead = load(0);
 #pragma unroll 1
   for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
-    const Codes<D> now = cur;
-    const int id = ahead;
-    if ((k & 31) == 31) ids = ids_of(k + 1);
-    ahead = load(k + 1);
-    const int j0 = tile * TILE, sees = id < 0 ? 0 : seen(a, first, last, j0, TILE);
-    if (sees == 0) continue;
+    const int id = ahead, j0 = tile * TILE, sees = id < 0 ? 0 : seen(a, first, last, j0, TILE);
     float* to = kept + (int64_t)(tile - tile0) * TILE * cl.rows;
+    const float2 par[4] = {params(cur.par[0][0]), params(cur.par[0][1]), params(cur.par[1][0]), params(cur.par[1][1])};
+    if ((k & 31) == 31) ids = ids_of(k + 1);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (n >= eights) break;
       float d[2][4];
-      products<D, NT>(now, 0, sh, n, lane, d[0]);
-      products<D, NT>(now, 1, sh, n, lane, d[1]);
+      if (n < eights) products<D, NT>(cur, sh, n, lane, d);
+      if (n == NT - 1) ahead = load(k + 1);  // the codes' registers are free
+      if (n >= eights || sees == 0) continue;
 #pragma unroll
       for (int e = 0; e < (F32 ? 1 : 2); ++e) {
         const Column& col = sh.col[n * 8 + 2 * t + e];
@@ -488,8 +492,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int mt = v >> 1, h = v & 1, in = token_of(mt * 16 + h * 8 + g);
-          const float raw = F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e];
-          x[v] = score(raw, col, params(now.par[mt][h]));
+          x[v] = score(F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e], col, par[v]);
           if (sees == 1 && !visible(a, col.p, j0 + in)) x[v] = kNegInf;
           if (row < cl.rows) to[in * cl.rows + row] = x[v];
         }
@@ -532,31 +535,30 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
 #pragma unroll 1
   for (int k = 0; tile0 + warp + k * WARPS < tile1; k += 4) {
     if (k && (k & 31) == 0) ids = ids_of(k);
-    int64_t at[4];
     float before[4];
-    bool writes[4];
+    uint32_t writes = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int id = __shfl_sync(0xffffffffu, ids, (k + i) & 31), j = (tile0 + warp + (k + i) * WARPS) * TILE + lane;
-      const bool some = seen(a, first, last, j - lane, TILE) != 0;
-      writes[i] = id >= 0 && j < r.s.len && (some || ms.decay != 1.0f || ms.in != ms.out || j >= old);
-      at[i] = ((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage;
-      before[i] = writes[i] && j < old ? ms.in[at[i]] : 0.0f;
+      const bool write = id >= 0 && j < r.s.len && (ms.decay != 1.0f || ms.in != ms.out || j >= old || seen(a, first, last, j - lane, TILE) != 0);
+      before[i] = write && j < old ? ms.in[((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage] : 0.0f;
+      writes |= write << i;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (!writes[i]) continue;
-      const int tile = tile0 + warp + (k + i) * WARPS, j = tile * TILE + lane;
+      const int id = __shfl_sync(0xffffffffu, ids, (k + i) & 31), tile = tile0 + warp + (k + i) * WARPS, j = tile * TILE + lane;
+      if (!(writes >> i & 1)) continue;
       float votes = 0.0f;
       if (seen(a, first, last, tile * TILE, TILE)) {
         const float* x = kept + (int64_t)((tile - tile0) * TILE + lane) * cl.rows;
+#pragma unroll 1
         for (int row = 0; row < rows; ++row) {
           const float2 ml = sh.part[0][row * PARTS];
           // a masked score is -inf; it takes no part, whatever the row's sum is
           if (x[row] != kNegInf) votes = fmaf(exp2_approx(x[row] - ml.x), ml.y, votes);
         }
       }
-      ms.out[at[i]] = j < old ? fmaf(ms.decay, before[i], votes) : votes;
+      ms.out[((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage] = j < old ? fmaf(ms.decay, before[i], votes) : votes;
     }
   }
   if (bad) record_device_error(kErrRange);
@@ -568,12 +570,6 @@ constexpr float kLeastA = 7.888609052210118e-31f, kMostA = 3.4028234663852886e38
 __device__ __forceinline__ float4 finished(float m, float l) {
   const float minus = m == kNegInf ? 0.0f : -m, inv = l == 0.0f ? 0.0f : __frcp_rn(l);
   return make_float4(minus, minus, inv, inv);
-}
-// the first of a chain of products: the sum begins at 0
-__device__ __forceinline__ void mma_first(float (&d)[4], uint4 a, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // Here the columns are the rows of m16n8k16 and the tokens its columns: a lane's accumulators are pairs of tokens of one
 // column (paired fp32 operations), and four chains of products run side by side. Scores stay in units of their
