@@ -20,6 +20,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kv4.cuh"
 
 namespace bitnet {
@@ -803,40 +805,46 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_rows_many(Kv4 c, Kv4Attn 
       if (k < 31) load(k + 1);
       const int j0 = tile * TILE, sees = seen(a, first, last, j0, TILE);
       if (sees == 0) continue;
+      // (masked tiles are few: their loop is apart from the other's)
+      const auto columns = [&](auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll 1
-      for (int j = 0; j < sixteens; ++j) {
-        uint64_t u[2][4];
-        const float4 ab[2] = {sh.sl.ab[j * 16 + g], sh.sl.ab[j * 16 + g + 8]};
-        scores<D, F32>(now, sh.sl, j, lane, ab, u);
-        float4 run = sh.run[warp][j][lane];
+        for (int j = 0; j < sixteens; ++j) {
+          uint64_t u[2][4];
+          const float4 ab[2] = {sh.sl.ab[j * 16 + g], sh.sl.ab[j * 16 + g + 8]};
+          scores<D, F32>(now, sh.sl, j, lane, ab, u);
+          float4 run = sh.run[warp][j][lane];
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-          float2 x[4];
+          for (int h = 0; h < HALVES; ++h) {
+            float2 x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = f2unpack(u[h][e]);
-          if (sees == 1) {
-            const int p = sh.sl.p[j * 16 + g + 8 * h];
+            for (int e = 0; e < 4; ++e) x[e] = f2unpack(u[h][e]);
+            if (MASKED) {
+              const int p = sh.sl.p[j * 16 + g + 8 * h];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (!visible(a, p, j0 + token_at(e, t, 0))) x[e].x = kNegInf;
+                if (!visible(a, p, j0 + token_at(e, t, 1))) x[e].y = kNegInf;
+              }
+            }
+            float &m = h ? run.z : run.x, &l = h ? run.w : run.y;
+            const float top = max3(max3(max3(x[0].x, x[0].y, x[1].x), x[1].y, x[2].x), max3(x[2].y, x[3].x, x[3].y), m);
+            const float from = top == kNegInf ? 0.0f : top, aa = ab[h].x;
+            const uint64_t a2 = f2pack(aa, aa), minus = f2pack(-from, -from);
+            float s[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (!visible(a, p, j0 + token_at(e, t, 0))) x[e].x = kNegInf;
-              if (!visible(a, p, j0 + token_at(e, t, 1))) x[e].y = kNegInf;
+              const float2 y = f2unpack(mul2(a2, add2(f2pack(x[e].x, x[e].y), minus)));
+              s[e] = exp2_approx(y.x) + exp2_approx(y.y);
             }
+            l = fmaf(l, exp2_approx(aa * (m - from)), (s[0] + s[1]) + (s[2] + s[3]));
+            m = top;
           }
-          float &m = h ? run.z : run.x, &l = h ? run.w : run.y;
-          const float top = max3(max3(max3(x[0].x, x[0].y, x[1].x), x[1].y, x[2].x), max3(x[2].y, x[3].x, x[3].y), m);
-          const float from = top == kNegInf ? 0.0f : top, aa = ab[h].x;
-          const uint64_t a2 = f2pack(aa, aa), minus = f2pack(-from, -from);
-          float s[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 y = f2unpack(mul2(a2, add2(f2pack(x[e].x, x[e].y), minus)));
-            s[e] = exp2_approx(y.x) + exp2_approx(y.y);
-          }
-          l = fmaf(l, exp2_approx(aa * (m - from)), (s[0] + s[1]) + (s[2] + s[3]));
-          m = top;
+          sh.run[warp][j][lane] = run;
         }
-        sh.run[warp][j][lane] = run;
-      }
+      };
+      if (sees == 2) columns(std::false_type{});
+      else columns(std::true_type{});
     }
 #pragma unroll 1
     for (int j = 0; j < SIXTEENS; ++j) {
@@ -952,7 +960,8 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
       const int j0 = tile * TILE, sees = there ? seen(a, first, last, j0, TILE) : 0;
       const Slab<D>& sl = slabs[buf];
       const int sixteens = (int)min((int64_t)SIXTEENS, (rows * PARTS - (int64_t)block * COLS + 15) / 16);
-      if (sees) {
+      const auto columns = [&](auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll 1
         for (int j = 0; j < sixteens; ++j) {
           uint64_t u[2][4];
@@ -968,16 +977,18 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
             for (int e = 0; e < 4; ++e) {
               const float2 y = f2unpack(mul2(a2, add2(u[h][e], minus)));
               const uint64_t more = fma2(f2pack(exp2_approx(y.x), exp2_approx(y.y)), inv, votes[e]);
-              if (sees == 2) {
-                votes[e] = more;
-              } else {
+              if (MASKED) {
                 const float2 v = f2unpack(votes[e]), w = f2unpack(more);
                 votes[e] = f2pack(visible(a, p, j0 + token_at(e, t, 0)) ? w.x : v.x, visible(a, p, j0 + token_at(e, t, 1)) ? w.y : v.y);
+              } else {
+                votes[e] = more;
               }
             }
           }
         }
-      }
+      };
+      if (sees == 2) columns(std::false_type{});
+      else if (sees) columns(std::true_type{});
       __syncthreads();  // the buffer is copied into again
       block = then, buf ^= 1;
     }
