@@ -775,7 +775,8 @@ BITNET_API int bitnet_last_device_error(void) {
                                     read_clear_device_error_prefill, read_clear_device_error_pair,
                                     read_clear_device_error_kv4_cache, read_clear_device_error_kv4_decode,
                                     read_clear_device_error_kv4_prompt, read_clear_device_error_w4_quant,
-                                    read_clear_device_error_kv4_mass, read_clear_device_error_kv4_evict};
+                                    read_clear_device_error_kv4_mass, read_clear_device_error_kv4_mass_tc,
+                                    read_clear_device_error_kv4_evict};
   for (auto rd : readers) {
     int v = 0;
     if (rd(&v) != cudaSuccess) return BITNET_ECUDA;

@@ -142,6 +142,7 @@ struct Kv4Mass {
 int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters);
 cudaError_t launch_kv4_mass(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, void* ws, int num_sms, cudaStream_t stream);
 cudaError_t read_clear_device_error_kv4_mass(int* value);
+cudaError_t read_clear_device_error_kv4_mass_tc(int* value);
 
 // Eviction (kv4_evict.cu).
 struct Kv4Evict {

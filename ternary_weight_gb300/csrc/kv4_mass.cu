@@ -17,12 +17,9 @@
 // Few columns (16 at most): both kernels are bound by the keys' bytes, the second kernel's mostly from L2. Many: by
 // the products and exponentials; columns go in blocks of 64 whose fragments the first kernel leaves in the workspace, the second
 // kernel's blocks keep their tiles' codes and go through a share of the columns, and a third one adds up the shares.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
-#include "kv4.cuh"
+#include "kv4_mass.cuh"
 
 namespace bitnet {
 namespace {
@@ -30,9 +27,6 @@ namespace {
 constexpr int WARPS = 8, THREADS = WARPS * 32;
 constexpr int TILE = 32;  // tokens of a tile: half a page
 constexpr int MAX_CHUNK = 32 * WARPS;  // tiles of a chunk: a warp keeps the page ids of its own, one a lane
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNegInf = -__builtin_huge_valf();
-
 struct Plan {
   int parts;    // columns of a row: 1, or 2 for fp32 queries
   int votes;    // rows of a sequence that vote, at most
@@ -50,11 +44,6 @@ struct Stats {
   uint8_t* slabs;  // unit, block
 };
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -67,30 +56,6 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint4 a, uint32_t b0, u
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.0f));
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// A unit's rows: which vote, and where they stand.
-struct Rows {
-  int b, h;
-  Kv4Seq s;
-  int votes;
-  __device__ __forceinline__ int position(int i) const { return s.len - votes + i; }  // of voting row i
-};
-__device__ __forceinline__ Rows rows_of(const Kv4& c, int unit, int voters, bool* bad) {
-  Rows r;
-  r.b = unit / c.kv_heads;
-  r.h = unit - r.b * c.kv_heads;
-  bool wrong = false;
-  r.s = kv4_sequence(c, r.b, &wrong);
-  if (wrong && c.cu_q[r.b] != c.cu_q[r.b + 1]) *bad = true;
-  r.votes = min(r.s.n, voters);
-  return r;
-}
-
 // What a column needs besides its fragments.
 struct Column {
   float a, b;  // x = step (a raw) + base b
@@ -211,17 +176,6 @@ __device__ __forceinline__ void products(const Codes<D>& k, const Shared<D, NT>&
 __device__ __forceinline__ float score(float raw, const Column& c, float2 par) {
   return __fmaf_rn(par.x, __fmul_rn(c.a, raw), __fmul_rn(par.y, c.b));
 }
-__device__ __forceinline__ float2 params(uint32_t p) { return __half22float2(*reinterpret_cast<const __half2*>(&p)); }
-
-__device__ __forceinline__ bool visible(const Kv4Attn& a, int p, int j) {
-  return j <= p && (j > (int64_t)p - a.window || j < a.sinks);
-}
-// what rows at positions first .. last see of tokens [j0, j0 + n): 0 nothing, 1 some, 2 all
-__device__ __forceinline__ int seen(const Kv4Attn& a, int first, int last, int j0, int n) {
-  if (j0 > last || ((int64_t)j0 + n - 1 <= (int64_t)first - a.window && j0 >= a.sinks)) return 0;
-  return j0 + n - 1 <= first && (j0 > (int64_t)last - a.window || j0 + n - 1 < a.sinks) ? 2 : 1;
-}
-
 // joins (m, l) with (m2, l2); a NaN is no maximum, but stays in the sum
 __device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
   const float top = fmaxf(m, m2), from = top == kNegInf ? 0.0f : top;
@@ -567,7 +521,6 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
 }
 
 // ------------------------------------------------------------- many columns
-constexpr float kLeastA = 7.888609052210118e-31f, kMostA = 3.4028234663852886e38f;  // 2^-100, the greatest
 // what the second kernel needs of a row: -M (0 where it sees nothing) and 1 / L, twice
 __device__ __forceinline__ float4 finished(float m, float l) {
   const float minus = m == kNegInf ? 0.0f : -m, inv = l == 0.0f ? 0.0f : __frcp_rn(l);
@@ -609,36 +562,6 @@ struct Tile {
     }
   }
 };
-__device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2unpack(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 template <int D>
 struct Unpacked {
   uint32_t u[4][D / 32][4];   // word: the two registers of each of its two products
@@ -747,13 +670,6 @@ __device__ __forceinline__ void load_slab(const Kv4Attn& a, const Rows& r, int64
     }
   }
 }
-// joins (m, l) with (m2, l2), maxima of u
-__device__ __forceinline__ void join_u(float a, float& m, float& l, float m2, float l2) {
-  const float top = fmaxf(m, m2), from = top == kNegInf ? 0.0f : top;
-  l = fmaf(l, exp2_approx(a * (m - from)), l2 * exp2_approx(a * (m2 - from)));
-  m = top;
-}
-
 // First kernel: each column's maximum and sum over a chunk of tiles. A warp's running ones lie in shared memory.
 template <int D>
 struct __align__(16) RowsShared {
@@ -1028,6 +944,12 @@ __global__ void __launch_bounds__(THREADS) kv4_mass_join(Kv4 c, Kv4Mass ms, Plan
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 unsigned grid_of(int64_t items) { return (unsigned)(items < (1 << 20) ? items : (1 << 20)); }
 
+// rows of a unit, at most
+int64_t rows_of_plan(const Kv4& c, int share, int voters) {
+  int votes = voters < c.max_q ? voters : c.max_q;
+  votes = votes < c.total_q ? votes : c.total_q;
+  return (int64_t)votes * share;
+}
 Plan plan_of(const Kv4& c, int share, int voters, bool f32, int num_sms) {
   Plan p{};
   p.parts = f32 ? 2 : 1;
@@ -1125,6 +1047,12 @@ cudaError_t by_columns(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const P
 int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters) {
   int64_t most = 0;  // whatever the queries' type
   for (int f32 = 0; f32 < 2; ++f32) {
+    const int64_t rows = rows_of_plan(c, q_heads / c.kv_heads, voters);
+    if (rows >= kMassTcRows) {
+      const int64_t n = kv4_mass_tc_ws_bytes(c, dim, rows, f32 != 0);
+      most = n > most ? n : most;
+      continue;
+    }
     const Plan p = plan_of(c, q_heads / c.kv_heads, voters, f32, 152);
     const int64_t n = part_bytes(c, p) + votes_bytes(c, p) + slabs_bytes(c, p, dim);
     most = n > most ? n : most;
@@ -1132,6 +1060,8 @@ int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters) {
   return most;
 }
 cudaError_t launch_kv4_mass(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, void* ws, int num_sms, cudaStream_t st) {
+  const int64_t rows = rows_of_plan(c, a.share, m.voters);
+  if (rows >= kMassTcRows) return launch_kv4_mass_tc(c, dim, a, m, rows, ws, st);
   const Plan p = plan_of(c, a.share, m.voters, !a.bf16, 152);
   uint8_t* at = static_cast<uint8_t*>(ws);
   const Stats s{reinterpret_cast<float2*>(at), reinterpret_cast<float*>(at + part_bytes(c, p)), at + part_bytes(c, p) + votes_bytes(c, p)};

@@ -1,0 +1,95 @@
+// kv4_mass.cuh -- what the kernels of the gathered attention weight share (kv4_mass.cu, kv4_mass_tc.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv4.cuh"
+
+namespace bitnet {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_huge_valf();
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// A unit's rows: which vote, and where they stand.
+struct Rows {
+  int b, h;
+  Kv4Seq s;
+  int votes;
+  __device__ __forceinline__ int position(int i) const { return s.len - votes + i; }  // of voting row i
+};
+__device__ __forceinline__ Rows rows_of(const Kv4& c, int unit, int voters, bool* bad) {
+  Rows r;
+  r.b = unit / c.kv_heads;
+  r.h = unit - r.b * c.kv_heads;
+  bool wrong = false;
+  r.s = kv4_sequence(c, r.b, &wrong);
+  if (wrong && c.cu_q[r.b] != c.cu_q[r.b + 1]) *bad = true;
+  r.votes = min(r.s.n, voters);
+  return r;
+}
+__device__ __forceinline__ float2 params(uint32_t p) { return __half22float2(*reinterpret_cast<const __half2*>(&p)); }
+__device__ __forceinline__ bool visible(const Kv4Attn& a, int p, int j) {
+  return j <= p && (j > (int64_t)p - a.window || j < a.sinks);
+}
+// what rows at positions first .. last see of tokens [j0, j0 + n): 0 nothing, 1 some, 2 all
+__device__ __forceinline__ int seen(const Kv4Attn& a, int first, int last, int j0, int n) {
+  if (j0 > last || ((int64_t)j0 + n - 1 <= (int64_t)first - a.window && j0 >= a.sinks)) return 0;
+  return j0 + n - 1 <= first && (j0 > (int64_t)last - a.window || j0 + n - 1 < a.sinks) ? 2 : 1;
+}
+constexpr float kLeastA = 7.888609052210118e-31f, kMostA = 3.4028234663852886e38f;  // 2^-100, the greatest
+__device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// joins (m, l) with (m2, l2), maxima of u
+__device__ __forceinline__ void join_u(float a, float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2), from = top == kNegInf ? 0.0f : top;
+  l = fmaf(l, exp2_approx(a * (m - from)), l2 * exp2_approx(a * (m2 - from)));
+  m = top;
+}
+
+}  // namespace
+
+// Many rows (kv4_mass_tc.cu): from this many of a unit (rows that vote x heads that share a key/value head) on.
+constexpr int kMassTcRows = 65;
+int64_t kv4_mass_tc_ws_bytes(const Kv4& c, int dim, int64_t rows, bool f32);
+cudaError_t launch_kv4_mass_tc(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, int64_t rows, void* ws, cudaStream_t stream);
+
+}  // namespace bitnet

@@ -1,0 +1,610 @@
+// kv4_mass_tc.cu -- the attention weight that cached tokens gather from many rows, on the 5th-generation tensor cores.
+//
+// A unit's rows (of a sequence: voting tokens x heads that share a key/value head) go in blocks of 128, its tokens in tiles of
+// 128 (two pages). Scores of a block and a tile are one 128 x 128 product with K = D in tensor memory, codes as exact
+// fp16 subnormals c 2^-24 (c 2^-20 for every second one; q' carries the 2^-4), fp32 queries as two parts with
+// a product each. As for few rows (kv4_mass.cu), x = a u, u = step raw + base b; the first kernel finds each row's maximum M
+// of u and its sum L, the second adds up 2^(a (u - M)) / L.
+//
+// First kernel: rows are the lanes of the accumulator, so that a thread has its row's constants, maximum and sum in registers
+// and a token's parameters come from shared memory, a pair of tokens at a time. Second kernel: tokens are the lanes, so that a
+// thread adds up its token's votes and a pair of rows' constants comes from shared memory. In both the products of one
+// tile (block) run while the last one's scores are worked off; two blocks an SM cover what is left.
+//
+// Bound by issue slots and shared-memory loads of the scores' arithmetic (about five operations a score in each kernel), then by
+// the exponentials.
+#include <type_traits>
+
+#include "kv4_mass.cuh"
+
+namespace bitnet {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int TOK = 128, ROWS = 128;
+
+struct Plan {
+  int blocks, tiles, chunk, chunks, shares;
+};
+// What the second kernel needs of a block's rows, in pairs.
+struct Constants {
+  float4 ab[ROWS / 2];  // a0, a1, b0, b1
+  float4 ml[ROWS / 2];  // -M0, -M1, 1 / L0, 1 / L1
+  int p[ROWS];
+};
+template <int D, bool F32>
+struct Shape {
+  static constexpr int PARTS = F32 ? 2 : 1;
+  static constexpr int IMAGE = 128 * D * 2;               // an operand: D / 64 atoms of 128 rows x 128 bytes
+  static constexpr int BLOCK = IMAGE * PARTS + (int)sizeof(Constants);  // as the first kernel leaves it
+  static constexpr int CON = 3072;                        // place of the constants in shared memory
+  static constexpr int ROWS_SMEM = IMAGE * PARTS + CON + 2 * IMAGE + 3 * 1024 + 1024;
+  static constexpr int VOTES_SMEM = IMAGE + 2 * IMAGE * PARTS + 3 * CON + 1024;
+  static constexpr int BLOCKS = F32 && D == 128 ? 1 : 2;  // resident on an SM
+};
+static_assert(sizeof(Constants) <= 3072 && sizeof(Constants) % 16 == 0, "");
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// byte offset of 16-byte chunk c of row r in an operand of 64-column atoms, K-major, 128-byte swizzle
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return (uint32_t)((c >> 3) * (128 * 128) + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+// the token (of its half of a tile) in row r of the half: pages keep keys in the order rho
+__device__ __forceinline__ int token_of(int r) { return kv4_rho_inv(r); }
+
+// D[tmem] = A B^T over both parts of the operand that has two (PA parts of A, PB of B), by one lane
+template <int D, int PA, int PB>
+__device__ __forceinline__ void issue(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem, uint64_t* bar) {
+  constexpr int IMAGE = 128 * D * 2;
+#pragma unroll
+  for (int p = 0; p < PA * PB; ++p) {
+    const uint64_t ad = make_sw128_kmajor_desc(a_smem + (PA > 1 ? p * IMAGE : 0)), bd = make_sw128_kmajor_desc(b_smem + (PB > 1 ? p * IMAGE : 0));
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const uint64_t o = (uint64_t)((s >> 2) * ((128 * 128) >> 4) + (s & 3) * 2);
+      mma_f16_ss(d_tmem, ad + o, bd + o, make_idesc_f16_f32(128, 128), p > 0 || s > 0);
+    }
+  }
+  mma_commit(bar);
+}
+
+// A thread's part of a tile: half a key row, as codes.
+template <int D>
+struct Half {
+  static constexpr int WORDS = D / 16;
+  uint32_t w[WORDS], par;
+  // id: of the page that has the row; -1 for none
+  __device__ __forceinline__ void load(const Kv4& c, int id, int h, int row, int half) {
+    if (id < 0) {
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) w[i] = 0;
+      par = 0;
+      return;
+    }
+    const uint8_t* blk = c.pages + ((int64_t)id * c.kv_heads + h) * kv4_block_bytes(D);
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(blk + row * (D / 2) + half * (D / 4) + i * 4);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+    par = *reinterpret_cast<const uint32_t*>(blk + kKvPage * D + row * 8);
+  }
+  __device__ __forceinline__ void store(uint32_t image, int row, int half) const {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      const uint32_t a = w[i], a8 = a >> 8;
+      sts128(image + chunk_at(row, half * WORDS + i), a & 0x000f000fu, a & 0x00f000f0u, a8 & 0x000f000fu, a8 & 0x00f000f0u);
+    }
+  }
+};
+
+// The queries of rows row0 .. row0 + 127 of a unit as an operand, and their constants: D / 8 lanes a row, 8 numbers each.
+template <int D, bool F32>
+__device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int row0, uint32_t image, Constants& con) {
+  constexpr int W = D / 8, PER = THREADS / W, BATCH = 4, IMAGE = 128 * D * 2;
+  const int w = threadIdx.x % W, rows = r.votes * a.share;
+#pragma unroll 1
+  for (int k0 = threadIdx.x / W; k0 < ROWS; k0 += PER * BATCH) {
+    float x[BATCH][8];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int row = row0 + k0 + k * PER, i = row / a.share;
+      const bool there = row < rows;
+      const int64_t at = there ? (int64_t)(r.s.q0 + r.s.n - r.votes + i) * a.q_stride + (int64_t)(r.h * a.share + row - i * a.share) * D + w : 0;
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+        x[k][n] = !there ? 0.0f
+                  : F32  ? static_cast<const float*>(a.q)[at + W * n]
+                         : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + W * n]);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int in = k0 + k * PER, row = row0 + in;
+      float sum = 0.0f;
+      uint32_t top = 0;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) sum += x[k][n], top = max(top, __float_as_uint(x[k][n]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = W / 2; o >= 1; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);
+      e = e > 127 ? 127 : e < -113 ? -113 : e;
+      const float up = copysignf(__int_as_float((e + 127) << 23), a.scale);
+      float hi[8], lo[8];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        hi[n] = x[k][n] * up * (n & 1 ? 0.0625f : 1.0f);
+        lo[n] = hi[n] - __half2float(__float2half_rn(hi[n]));
+      }
+      const uint32_t to = image + chunk_at(in, w);
+      sts128(to, pack_half2(hi[0], hi[4]), pack_half2(hi[1], hi[5]), pack_half2(hi[2], hi[6]), pack_half2(hi[3], hi[7]));
+      if (F32) sts128(to + IMAGE, pack_half2(lo[0], lo[4]), pack_half2(lo[1], lo[5]), pack_half2(lo[2], lo[6]), pack_half2(lo[3], lo[7]));
+      if (w == 0) {
+        const float c1 = __fmul_rn(fabsf(a.scale), kLog2e);
+        const int f = 24 - e, half = f / 2;
+        const float ca = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
+        float* ab = reinterpret_cast<float*>(&con.ab[in >> 1]) + (in & 1);
+        ab[0] = fminf(fmaxf(ca, kLeastA), kMostA);
+        ab[2] = __fmul_rn(__fmul_rn(sum, up), 5.9604644775390625e-8f);  // 2^-24
+        con.p[in] = row < rows ? r.position(row / a.share) : -1;
+      }
+    }
+  }
+}
+
+// The first and last position of a block's rows.
+__device__ __forceinline__ void ends_of(const Kv4Attn& a, const Rows& r, int row0, int* first, int* last) {
+  *first = r.position(row0 / a.share);
+  *last = r.position((min(row0 + ROWS, r.votes * a.share) - 1) / a.share);
+}
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_rows(Kv4 c, Kv4Attn a, int voters, Plan pl, uint8_t* blocks, float2* part) {
+  using S = Shape<D, F32>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t done[2], all_done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ float2 halves[ROWS];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  Constants& con = *reinterpret_cast<Constants*>(smem + S::IMAGE * S::PARTS);
+  constexpr int KEYS = S::IMAGE * S::PARTS + S::CON, TABLE = KEYS + 2 * S::IMAGE;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, half = warp >> 2, row = (warp & 3) * 32 + lane;
+  if (threadIdx.x == 0) {
+    mbar_init(&done[0], 1), mbar_init(&done[1], 1), mbar_init(&all_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_slot, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  bool bad = false, abort = false;
+  uint32_t issued = 0;  // products so far: buffer issued & 1
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks * pl.chunks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t rest = item / pl.chunks;
+    const int chunk = (int)(item - rest * pl.chunks), unit = (int)(rest / pl.blocks), block = (int)(rest - (int64_t)unit * pl.blocks);
+    const Rows r = rows_of(c, unit, voters, &bad);
+    const int rows = r.votes * a.share, row0 = block * ROWS;
+    if (row0 >= rows) continue;
+    const int t0 = chunk * pl.chunk, t1 = min(t0 + pl.chunk, (r.s.len + TOK - 1) / TOK), pages = (r.s.len + kKvPage - 1) / kKvPage;
+    int first, last;
+    ends_of(a, r, row0, &first, &last);
+    const auto next = [&](int t) {
+      while (t < t1 && seen(a, first, last, t * TOK, TOK) == 0) ++t;
+      return t;
+    };
+    int t = next(t0);
+    if (t >= t1 && chunk) {
+      for (int i = threadIdx.x; i < ROWS; i += THREADS) part[item * ROWS + i] = make_float2(kNegInf, 0.0f);
+      continue;
+    }
+    const int krow = threadIdx.x >> 1, khalf = threadIdx.x & 1;
+    const auto page_id = [&](int tile) {
+      const int page = tile * 2 + (krow >> 6);
+      if (tile >= t1 || page >= pages) return -1;
+      const int id = c.page_table[(int64_t)r.b * c.max_pages + page];
+      if (id >= 0 && id < c.n_pages) return id;
+      bad = true;
+      return -1;
+    };
+    Half<D> codes;
+    codes.load(c, page_id(t), r.h, krow & 63, khalf);
+    load_block<D, F32>(a, r, row0, base, con);
+    __syncthreads();
+    const float4 ab4 = con.ab[row >> 1];
+    const float aa = row & 1 ? ab4.y : ab4.x, bb = row & 1 ? ab4.w : ab4.z;
+    const uint64_t a2 = f2pack(aa, aa), b2 = f2pack(bb, bb);
+    const int p = con.p[row];
+    float m = kNegInf, l = 0.0f;
+    int before = -1;  // the tile whose scores are to be worked off
+    while (t < t1 || before >= 0) {
+      const uint32_t buf = issued & 1;
+      if (t < t1) {
+        codes.store(base + KEYS + buf * S::IMAGE, krow, khalf);
+        if (khalf == 0) {
+          const float2 sb = params(codes.par);
+          // (three tables: a warp may still read the one before the last)
+          float* tab = reinterpret_cast<float*>(smem + TABLE + (issued % 3) * 1024 + (krow >> 1) * 16) + (krow & 1);
+          tab[0] = sb.x, tab[2] = sb.y;
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      if (t < t1 && warp == 0) {
+        if (elect_one()) issue<D, S::PARTS, 1>(tmem + buf * 128, base, base + KEYS + buf * S::IMAGE, &done[buf]);
+        __syncwarp();
+      }
+      const int then = t < t1 ? next(t + 1) : t1;
+      if (then < t1) codes.load(c, page_id(then), r.h, krow & 63, khalf);
+      if (before >= 0) {
+        const uint32_t was = issued - 1, at = was & 1;
+        mbar_wait_warp(&done[at], (was >> 1) & 1, &abort);
+        tc_fence_after();
+        const int j0 = before * TOK + half * 64, sees = seen(a, first, last, before * TOK, TOK);
+        const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + at * 128 + half * 64;
+        const float4* tab = reinterpret_cast<const float4*>(smem + TABLE + (was % 3) * 1024) + half * 32;
+        const auto work = [&](auto masked) {
+          constexpr bool MASKED = decltype(masked)::value;
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) {
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(ts + k * 32, s);
+            tmem_ld_wait();
+            uint64_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float4 sb = tab[k * 16 + i];
+              u[i] = fma2(f2pack(sb.x, sb.y), f2pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2(f2pack(sb.z, sb.w), b2));
+              if (MASKED) {
+                float2 v = f2unpack(u[i]);
+                if (!visible(a, p, j0 + k * 32 + token_of(2 * i))) v.x = kNegInf;
+                if (!visible(a, p, j0 + k * 32 + token_of(2 * i + 1))) v.y = kNegInf;
+                u[i] = f2pack(v.x, v.y);
+              }
+            }
+            float top[4] = {m, m, m, m};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 v = f2unpack(u[i]);
+              top[i & 3] = max3(top[i & 3], v.x, v.y);
+            }
+            const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), from = now == kNegInf ? 0.0f : now;
+            const uint64_t minus = f2pack(-from, -from);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = f2unpack(mul2(a2, add2(u[i], minus)));
+              sum[i & 1] = add2(sum[i & 1], f2pack(exp2_approx(y.x), exp2_approx(y.y)));
+            }
+            const float2 e = f2unpack(add2(sum[0], sum[1]));
+            l = fmaf(l, exp2_approx(aa * (m - from)), e.x + e.y);
+            m = now;
+          }
+        };
+        if (sees == 2) work(std::false_type{});
+        else work(std::true_type{});
+      }
+      before = -1;
+      if (t < t1) before = t, ++issued;
+      t = then;
+    }
+    if (half) halves[row] = make_float2(m, l);
+    __syncthreads();
+    if (!half) {
+      join_u(aa, m, l, halves[row].x, halves[row].y);
+      part[item * ROWS + row] = make_float2(m, l);
+      // what the second kernel needs where there is one chunk
+      float* ml = reinterpret_cast<float*>(&con.ml[row >> 1]) + (row & 1);
+      const bool none = p < 0 || m == kNegInf;
+      ml[0] = none ? 0.0f : -m;
+      ml[2] = p < 0 || l == 0.0f ? 0.0f : __frcp_rn(l);
+    }
+    __syncthreads();
+    if (chunk == 0) {
+      uint4* to = reinterpret_cast<uint4*>(blocks + rest * (int64_t)S::BLOCK);
+      for (int i = threadIdx.x; i < S::BLOCK / 16; i += THREADS) to[i] = reinterpret_cast<const uint4*>(smem)[i];
+    }
+    __syncthreads();  // the next item's queries
+  }
+  // what was issued ends before the tensor memory is given back, whichever wait gave up
+  if (warp == 0) {
+    if (elect_one()) mma_commit(&all_done);
+    __syncwarp();
+    abort = false;
+    mbar_wait_warp(&all_done, 0, &abort);
+  }
+  if (bad) record_device_error(kErrRange);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 256);
+}
+
+// Joins the chunks' maxima and sums of each block of rows (more than one chunk).
+template <int D, bool F32>
+__global__ void __launch_bounds__(ROWS) kv4_mass_tc_sums(Kv4 c, Kv4Attn a, int voters, Plan pl, uint8_t* blocks, const float2* part) {
+  using S = Shape<D, F32>;
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int unit = (int)(item / pl.blocks), block = (int)(item - (int64_t)unit * pl.blocks), row = threadIdx.x;
+    bool bad = false;
+    const Rows r = rows_of(c, unit, voters, &bad);
+    if (block * ROWS >= r.votes * a.share) continue;
+    Constants& con = *reinterpret_cast<Constants*>(blocks + item * (int64_t)S::BLOCK + S::IMAGE * S::PARTS);
+    const int chunks = ((r.s.len + TOK - 1) / TOK + pl.chunk - 1) / pl.chunk;
+    const float aa = reinterpret_cast<const float*>(&con.ab[row >> 1])[row & 1];
+    float m = kNegInf, l = 0.0f;
+    for (int k = 0; k < chunks; ++k) {
+      const float2 v = part[(item * pl.chunks + k) * ROWS + row];
+      join_u(aa, m, l, v.x, v.y);
+    }
+    const bool none = con.p[row] < 0 || m == kNegInf;
+    float* ml = reinterpret_cast<float*>(&con.ml[row >> 1]) + (row & 1);
+    ml[0] = none ? 0.0f : -m;
+    ml[2] = con.p[row] < 0 || l == 0.0f ? 0.0f : __frcp_rn(l);
+  }
+}
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_votes(Kv4 c, Kv4Attn a, Kv4Mass ms, Plan pl, const uint8_t* blocks, float* shares) {
+  using S = Shape<D, F32>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[2], done[2], all_done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ float halves[TOK];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  constexpr int QUERIES = S::IMAGE, CONS = QUERIES + 2 * S::IMAGE * S::PARTS;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, half = warp >> 2, row = (warp & 3) * 32 + lane;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) mbar_init(&full[i], 1), mbar_init(&done[i], 1);
+    mbar_init(&all_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_slot, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  bool bad = false, abort = false;
+  uint32_t issued = 0, copied = 0;
+  // the groups of tokens outermost: with a causal mask the first ones have most to do
+  const int units = c.batch * c.kv_heads;
+  const int64_t items = (int64_t)units * pl.tiles * pl.shares;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t rest = item / pl.shares;
+    const int share = (int)(item - rest * pl.shares), tile = (int)(rest / units), unit = (int)(rest - (int64_t)tile * units);
+    const Rows r = rows_of(c, unit, ms.voters, &bad);
+    const int rows = r.votes * a.share, pages = (r.s.len + kKvPage - 1) / kKvPage;
+    if (rows == 0 || tile * TOK >= r.s.len) continue;
+    const int n_blocks = (rows + ROWS - 1) / ROWS;
+    const auto next = [&](int block) {  // of this share, from `block` on, that sees any of the tokens
+      for (; block < n_blocks; block += pl.shares) {
+        int first, last;
+        ends_of(a, r, block * ROWS, &first, &last);
+        if (seen(a, first, last, tile * TOK, TOK)) break;
+      }
+      return block;
+    };
+    // a block's copy: its queries to buffer copied & 1, its constants to place copied % 3
+    const auto copy = [&](int block) {
+      if (threadIdx.x == 0) {
+        const uint8_t* from = blocks + ((int64_t)unit * pl.blocks + block) * (int64_t)S::BLOCK;
+        uint64_t* bar = &full[copied & 1];
+        mbar_arrive_expect_tx(bar, S::BLOCK);
+        bulk_copy_g2s(smem + QUERIES + (copied & 1) * S::IMAGE * S::PARTS, from, S::IMAGE * S::PARTS, bar);
+        bulk_copy_g2s(smem + CONS + (copied % 3) * S::CON, from + S::IMAGE * S::PARTS, (uint32_t)sizeof(Constants), bar);
+      }
+      ++copied;
+    };
+    const auto page_of = [&](int in) {
+      const int page = tile * 2 + (in >> 6);
+      if (page >= pages) return -1;
+      const int id = c.page_table[(int64_t)r.b * c.max_pages + page];
+      if (id >= 0 && id < c.n_pages) return id;
+      bad = true;
+      return -1;
+    };
+    int block = next(share);
+    if (block < n_blocks) copy(block);
+    const int krow = threadIdx.x >> 1, khalf = threadIdx.x & 1;
+    Half<D> codes;
+    codes.load(c, page_of(krow), r.h, krow & 63, khalf);
+    codes.store(base, krow, khalf);
+    fence_proxy_async_smem();
+    const int mine = page_of(row);
+    float2 sb = make_float2(0.0f, 0.0f);
+    if (mine >= 0) sb = params(*reinterpret_cast<const uint32_t*>(c.pages + ((int64_t)mine * c.kv_heads + r.h) * kv4_block_bytes(D) + kKvPage * D + (row & 63) * 8));
+    const uint64_t step2 = f2pack(sb.x, sb.x), base2 = f2pack(sb.y, sb.y);
+    const int in = (row & 64) + token_of(row & 63), j = tile * TOK + in;  // this thread's token
+    uint64_t votes[2] = {0, 0};
+    int before = -1;
+    while (block < n_blocks || before >= 0) {
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      const uint32_t buf = issued & 1;
+      if (block < n_blocks) {
+        mbar_wait_warp(&full[buf], (issued >> 1) & 1, &abort);
+        if (warp == 0) {
+          if (elect_one()) issue<D, 1, S::PARTS>(tmem + buf * 128, base, base + QUERIES + buf * S::IMAGE * S::PARTS, &done[buf]);
+          __syncwarp();
+        }
+      }
+      const uint32_t was = issued - 1;
+      if (before >= 0) {
+        mbar_wait_warp(&done[was & 1], (was >> 1) & 1, &abort);
+        tc_fence_after();
+      }
+      // the buffer of the last products is free now
+      const int then = block < n_blocks ? next(block + pl.shares) : n_blocks;
+      if (then < n_blocks) copy(then);
+      if (before >= 0) {
+        int first, last;
+        ends_of(a, r, before * ROWS, &first, &last);
+        const int sees = seen(a, first, last, tile * TOK, TOK), left = rows - before * ROWS - half * 64;
+        const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (was & 1) * 128 + half * 64;
+        const Constants& con = *reinterpret_cast<const Constants*>(smem + CONS + (was % 3) * S::CON);
+        const auto work = [&](auto masked) {
+          constexpr bool MASKED = decltype(masked)::value;
+#pragma unroll 1
+          for (int k = 0; k < 2 && k * 32 < left; ++k) {
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(ts + k * 32, s);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float4 ab = con.ab[half * 32 + k * 16 + i], ml = con.ml[half * 32 + k * 16 + i];
+              const uint64_t u = fma2(step2, f2pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2(base2, f2pack(ab.z, ab.w)));
+              const float2 y = f2unpack(mul2(f2pack(ab.x, ab.y), add2(u, f2pack(ml.x, ml.y))));
+              const uint64_t more = fma2(f2pack(exp2_approx(y.x), exp2_approx(y.y)), f2pack(ml.z, ml.w), votes[i & 1]);
+              if (MASKED) {
+                const float2 v = f2unpack(votes[i & 1]), w = f2unpack(more);
+                const int2 p = *reinterpret_cast<const int2*>(&con.p[half * 64 + k * 32 + 2 * i]);
+                votes[i & 1] = f2pack(visible(a, p.x, j) ? w.x : v.x, visible(a, p.y, j) ? w.y : v.y);
+              } else {
+                votes[i & 1] = more;
+              }
+            }
+          }
+        };
+        if (sees == 2) work(std::false_type{});
+        else work(std::true_type{});
+      }
+      before = -1;
+      if (block < n_blocks) before = block, ++issued;
+      block = then;
+    }
+    const float2 v = f2unpack(add2(votes[0], votes[1]));
+    if (half) halves[row] = v.x + v.y;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (!half) {
+      const float got = (v.x + v.y) + halves[row];
+      if (pl.shares > 1) {
+        shares[(((int64_t)unit * pl.tiles + tile) * pl.shares + share) * TOK + in] = got;
+      } else if (j < r.s.len && mine >= 0) {
+        const int64_t at = ((int64_t)mine * c.kv_heads + r.h) * kKvPage + j % kKvPage;
+        ms.out[at] = j < r.s.len - r.s.n ? fmaf(ms.decay, ms.in[at], got) : got;
+      }
+    }
+    __syncthreads();  // the next item's codes
+  }
+  if (warp == 0) {
+    if (elect_one()) mma_commit(&all_done);
+    __syncwarp();
+    abort = false;
+    mbar_wait_warp(&all_done, 0, &abort);
+  }
+  if (bad) record_device_error(kErrRange);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 256);
+}
+
+// Adds up the shares' votes.
+__global__ void __launch_bounds__(TOK) kv4_mass_tc_join(Kv4 c, Kv4Mass ms, Plan pl, const float* shares) {
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.tiles;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int unit = (int)(item / pl.tiles), tile = (int)(item - (int64_t)unit * pl.tiles), j = tile * TOK + threadIdx.x;
+    bool bad = false;
+    const Rows r = rows_of(c, unit, ms.voters, &bad);
+    if (r.votes == 0 || j >= r.s.len) continue;
+    const int id = c.page_table[(int64_t)r.b * c.max_pages + j / kKvPage];
+    if (id < 0 || id >= c.n_pages) continue;
+    float got = 0.0f;
+    for (int s = 0; s < pl.shares; ++s) got += shares[(item * pl.shares + s) * TOK + threadIdx.x];
+    const int64_t at = ((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage;
+    ms.out[at] = j < r.s.len - r.s.n ? fmaf(ms.decay, ms.in[at], got) : got;
+  }
+}
+
+constexpr int kSms = 152;
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+unsigned grid_of(int64_t items, int64_t most) { return (unsigned)(items < most ? items : most); }
+
+Plan plan_of(const Kv4& c, int64_t rows) {
+  Plan p{};
+  const int64_t units = (int64_t)c.batch * c.kv_heads;
+  p.blocks = (int)((rows + ROWS - 1) / ROWS);
+  p.tiles = (c.max_kv + TOK - 1) / TOK;
+  // tiles of a chunk: four blocks an SM, but enough that a block's queries are not made ready for little
+  int64_t per = (units * p.blocks * p.tiles + kSms * 4 - 1) / (kSms * 4);
+  p.chunk = (int)(per < 8 ? 8 : per > p.tiles ? (p.tiles ? p.tiles : 1) : per);
+  p.chunks = (p.tiles + p.chunk - 1) / p.chunk;
+  const int64_t all = units * (p.tiles ? p.tiles : 1), s = (kSms * 4 + all - 1) / all;
+  p.shares = (int)(s > p.blocks ? p.blocks : s);
+  return p;
+}
+int64_t block_bytes(int dim, bool f32) { return (int64_t)128 * dim * 2 * (f32 ? 2 : 1) + (int64_t)sizeof(Constants); }
+int64_t blocks_bytes(const Kv4& c, const Plan& p, int dim, bool f32) { return align256((int64_t)c.batch * c.kv_heads * p.blocks * block_bytes(dim, f32)); }
+int64_t part_bytes(const Kv4& c, const Plan& p) { return align256((int64_t)c.batch * c.kv_heads * p.blocks * p.chunks * ROWS * 8); }
+
+template <int D, bool F32>
+cudaError_t launch(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, uint8_t* ws, cudaStream_t st) {
+  using S = Shape<D, F32>;
+  if (p.tiles == 0) return cudaSuccess;
+  uint8_t* blocks = ws;
+  float2* part = reinterpret_cast<float2*>(ws + blocks_bytes(c, p, D, F32));
+  float* shares = reinterpret_cast<float*>(ws + blocks_bytes(c, p, D, F32) + part_bytes(c, p));
+  const int64_t units = (int64_t)c.batch * c.kv_heads;
+  if (cudaError_t e = cudaFuncSetAttribute(kv4_mass_tc_rows<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ROWS_SMEM)) return e;
+  if (cudaError_t e = cudaFuncSetAttribute(kv4_mass_tc_votes<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::VOTES_SMEM)) return e;
+  kv4_mass_tc_rows<D, F32><<<grid_of(units * p.blocks * p.chunks, 1 << 20), THREADS, S::ROWS_SMEM, st>>>(c, a, m.voters, p, blocks, part);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  if (p.chunks > 1) {
+    kv4_mass_tc_sums<D, F32><<<grid_of(units * p.blocks, 1 << 20), ROWS, 0, st>>>(c, a, m.voters, p, blocks, part);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  }
+  kv4_mass_tc_votes<D, F32><<<grid_of(units * p.tiles * p.shares, 1 << 20), THREADS, S::VOTES_SMEM, st>>>(c, a, m, p, blocks, shares);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  if (p.shares > 1) kv4_mass_tc_join<<<grid_of(units * p.tiles, 1 << 20), TOK, 0, st>>>(c, m, p, shares);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t kv4_mass_tc_ws_bytes(const Kv4& c, int dim, int64_t rows, bool f32) {
+  const Plan p = plan_of(c, rows);
+  return blocks_bytes(c, p, dim, f32) + part_bytes(c, p) + align256((int64_t)c.batch * c.kv_heads * p.tiles * p.shares * TOK * 4);
+}
+cudaError_t launch_kv4_mass_tc(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, int64_t rows, void* ws, cudaStream_t st) {
+  const Plan p = plan_of(c, rows);
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  if (dim == 128) return a.bf16 ? launch<128, false>(c, a, m, p, at, st) : launch<128, true>(c, a, m, p, at, st);
+  return a.bf16 ? launch<64, false>(c, a, m, p, at, st) : launch<64, true>(c, a, m, p, at, st);
+}
+
+cudaError_t read_clear_device_error_kv4_mass_tc(int* value) {
+  int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_device_error, sizeof(int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
+}
+
+}  // namespace bitnet
