@@ -42,6 +42,9 @@ __device__ __forceinline__ float2 params(uint32_t p) { return __half22float2(*re
 __device__ __forceinline__ bool visible(const Kv4Attn& a, int p, int j) {
   return j <= p && (j > (int64_t)p - a.window || j < a.sinks);
 }
+// The same with the window's beginning worked out: a row at p sees j where j <= p and (j >= lo or j < sinks).
+__device__ __forceinline__ int window_from(const Kv4Attn& a, int p) { return (int)max((int64_t)0, (int64_t)p - a.window + 1); }
+__device__ __forceinline__ bool visible(const Kv4Attn& a, int p, int lo, int j) { return j <= p && (j >= lo || j < a.sinks); }
 // what rows at positions first .. last see of tokens [j0, j0 + n): 0 nothing, 1 some, 2 all
 __device__ __forceinline__ int seen(const Kv4Attn& a, int first, int last, int j0, int n) {
   if (j0 > last || ((int64_t)j0 + n - 1 <= (int64_t)first - a.window && j0 >= a.sinks)) return 0;

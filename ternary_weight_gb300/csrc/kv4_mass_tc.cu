@@ -30,7 +30,7 @@ struct Plan {
 struct Constants {
   float4 ab[ROWS / 2];  // a0, a1, b0, b1
   float4 ml[ROWS / 2];  // -M0, -M1, 1 / L0, 1 / L1
-  int p[ROWS];
+  int2 seen[ROWS];      // the row's position (-1: no row), and where its window begins
 };
 template <int D, bool F32>
 struct Shape {
@@ -159,7 +159,8 @@ __device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int 
         float* ab = reinterpret_cast<float*>(&con.ab[in >> 1]) + (in & 1);
         ab[0] = fminf(fmaxf(ca, kLeastA), kMostA);
         ab[2] = __fmul_rn(__fmul_rn(sum, up), 5.9604644775390625e-8f);  // 2^-24
-        con.p[in] = row < rows ? r.position(row / a.share) : -1;
+        const int p = row < rows ? r.position(row / a.share) : -1;
+        con.seen[in] = make_int2(p, window_from(a, p));
       }
     }
   }
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
     const float4 ab4 = con.ab[row >> 1];
     const float aa = row & 1 ? ab4.y : ab4.x, bb = row & 1 ? ab4.w : ab4.z;
     const uint64_t a2 = f2pack(aa, aa), b2 = f2pack(bb, bb);
-    const int p = con.p[row];
+    const int p = con.seen[row].x, lo = con.seen[row].y;
     float m = kNegInf, l = 0.0f;
     int before = -1;  // the tile whose scores are to be worked off
     while (t < t1 || before >= 0) {
@@ -277,8 +278,8 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
               u[i] = fma2(f2pack(sb.x, sb.y), f2pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2(f2pack(sb.z, sb.w), b2));
               if (MASKED) {
                 float2 v = f2unpack(u[i]);
-                if (!visible(a, p, j0 + k * 32 + token_of(2 * i))) v.x = kNegInf;
-                if (!visible(a, p, j0 + k * 32 + token_of(2 * i + 1))) v.y = kNegInf;
+                if (!visible(a, p, lo, j0 + k * 32 + token_of(2 * i))) v.x = kNegInf;
+                if (!visible(a, p, lo, j0 + k * 32 + token_of(2 * i + 1))) v.y = kNegInf;
                 u[i] = f2pack(v.x, v.y);
               }
             }
@@ -358,10 +359,10 @@ __global__ void __launch_bounds__(ROWS) kv4_mass_tc_sums(Kv4 c, Kv4Attn a, int v
       const float2 v = part[(item * pl.chunks + k) * ROWS + row];
       join_u(aa, m, l, v.x, v.y);
     }
-    const bool none = con.p[row] < 0 || m == kNegInf;
+    const bool none = con.seen[row].x < 0 || m == kNegInf;
     float* ml = reinterpret_cast<float*>(&con.ml[row >> 1]) + (row & 1);
     ml[0] = none ? 0.0f : -m;
-    ml[2] = con.p[row] < 0 || l == 0.0f ? 0.0f : __frcp_rn(l);
+    ml[2] = con.seen[row].x < 0 || l == 0.0f ? 0.0f : __frcp_rn(l);
   }
 }
 
@@ -483,8 +484,8 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
               const uint64_t more = fma2(f2pack(exp2_approx(y.x), exp2_approx(y.y)), f2pack(ml.z, ml.w), votes[i & 1]);
               if (MASKED) {
                 const float2 v = f2unpack(votes[i & 1]), w = f2unpack(more);
-                const int2 p = *reinterpret_cast<const int2*>(&con.p[half * 64 + k * 32 + 2 * i]);
-                votes[i & 1] = f2pack(visible(a, p.x, j) ? w.x : v.x, visible(a, p.y, j) ? w.y : v.y);
+                const int4 p = *reinterpret_cast<const int4*>(&con.seen[half * 64 + k * 32 + 2 * i]);
+                votes[i & 1] = f2pack(visible(a, p.x, p.y, j) ? w.x : v.x, visible(a, p.z, p.w, j) ? w.y : v.y);
               } else {
                 votes[i & 1] = more;
               }
