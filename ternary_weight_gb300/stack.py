@@ -9,8 +9,8 @@ launch per group -- in a fixed order. The whole sequence is captured once into a
 launch. Activations enter through one contiguous input buffer and results leave through
 one contiguous output buffer, so a host round trip is one copy each way.
 
-``AttentionBlock`` runs the attention of a layer: its ternary projections, the 4-bit key/value
-cache and the attention over it.
+``AttentionBlock`` runs the attention of a layer: its ternary projections, rotary positions, the 4-bit
+key/value cache and the attention over it; ``W4Linear`` is a matrix that is not ternary (an output head) in 4 bits.
 
 Everything the step computes runs in the library's kernels; torch only owns the buffers,
 the stream and the graph.
@@ -42,6 +42,29 @@ class PackedLinear:
 
     def weight_bytes(self) -> int:
         return self.N * self.K // 4
+
+
+@dataclass
+class W4Linear:
+    """One matrix in 4 bits with group scales (see ``binding.w4_quant_weight``), for what is not ternary: the output head."""
+    name: str
+    codes: torch.Tensor
+    scales: torch.Tensor
+    zeros: torch.Tensor | None
+    N: int
+    K: int
+
+    @classmethod
+    def from_weights(cls, name: str, w: torch.Tensor, group: int = 128, with_zeros: bool = False, stream=None) -> "W4Linear":
+        codes, scales, zeros = binding.w4_quant_weight(w, group, with_zeros, stream=stream)
+        return cls(name, codes, scales, zeros, *w.shape)
+
+    def weight_bytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.codes, self.scales, self.zeros) if t is not None)
+
+    def run(self, x, out=None, stream=None):
+        """x (M x K fp32 or bf16) -> M x N fp32."""
+        return binding.w4_matmul(x, self.codes, self.scales, self.zeros, out=out, stream=stream)
 
 
 @dataclass
@@ -168,17 +191,25 @@ class AttentionBlock:
     captured once and replayed as the sequences grow (``python -m ternary_weight_gb300.generate`` does).
     Nothing stands between the attention and the o projection: a layer that normalises there (the 2B-4T layer does)
     makes the calls of ``run`` itself, with its norm before the last one.
-    Each layer has a cache of its own; the layers of a model share the batch."""
+    Each layer has a cache of its own; the layers of a model share the batch.
+
+    ``rope`` (``binding.Rope``): queries and keys are turned by the positions that ``run`` is given. ``mass``
+    (``binding.kv4_mass`` of the cache): the cached tokens gather the attention weight of the last ``voters`` rows of each
+    sequence (0: all), what they had fading by ``decay`` a call; ``evict`` cuts the cache by it."""
 
     def __init__(self, q: PackedLinear, k: PackedLinear, v: PackedLinear, o: PackedLinear, cache: "binding.KV4Cache",
-                 scale: float | None = None, window: int = 0, sinks: int = 0):
+                 scale: float | None = None, window: int = 0, sinks: int = 0, rope: "binding.Rope | None" = None,
+                 mass: torch.Tensor | None = None, voters: int = 0, decay: float = 1.0):
         dim = cache.head_dim
         if q.N % dim or k.N != cache.kv_heads * dim or v.N != k.N or q.N % k.N or o.K != q.N or not q.K == k.K == v.K:
             raise ValueError("the projections' sizes do not fit the cache's heads")
         self.qkv, self.o, self.cache = [q, k, v], o, cache
         self.heads = [l.N // dim for l in self.qkv]
         self.scale = dim ** -0.5 if scale is None else scale
+        if rope is not None and rope.dims > dim:
+            raise ValueError("the rotary positions do not fit the cache's heads")
         self.window, self.sinks = window, sinks
+        self.rope, self.mass, self.voters, self.decay = rope, mass, voters, decay
 
     def _project(self, x, linears):
         xq = s = rs = None
@@ -188,13 +219,16 @@ class AttentionBlock:
             rs = torch.empty(x.shape[0], dtype=torch.int32, device=x.device)
         return binding.linear_group(x, [l.wp for l in linears], [l.w_scale for l in linears], xq=xq, scale=s, rowsum=rs)
 
-    def run(self, x, batch, rotate=None, stream=None):
+    def run(self, x, batch, rotate=None, stream=None, positions=None):
         """x: total_q x K rows (fp32 or bf16), sequence after sequence. ``rotate(q, k)``, if given, puts
         the positions into the queries and keys (total_q x heads x dim fp32) in place before they are
-        cached. Returns total_q x N fp32."""
+        cached; a block with rotary positions of its own takes ``positions`` (total_q int32) instead. They count the
+        tokens of a sequence, also those that have been evicted since. Returns total_q x N fp32."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.run(x, batch, rotate)
+                return self.run(x, batch, rotate, positions=positions)
+        if (self.rope is None) != (positions is None) or (rotate is not None and positions is not None):
+            raise ValueError("positions are for a block with rotary positions, and instead of rotate")
         if x.shape[0] != batch.total_q:
             raise ValueError("x must have a row for each of the batch's new tokens")
         if x.shape[0] == 0:
@@ -202,6 +236,20 @@ class AttentionBlock:
         q, k, v = (t.view(-1, h, self.cache.head_dim) for t, h in zip(self._project(x, self.qkv), self.heads))
         if rotate is not None:
             rotate(q, k)
+        if positions is not None:
+            binding.rope(self.rope, positions, q, k, q_out=q, k_out=k)
         binding.kv4_append(self.cache, batch, k, v)
+        if self.mass is not None:
+            binding.kv4_attention_mass(self.cache, batch, q, self.scale, self.mass, decay=self.decay, window=self.window,
+                                       sinks=self.sinks, voters=self.voters)
         y = binding.kv4_attention(self.cache, batch, q, self.scale, window=self.window, sinks=self.sinks)
         return self._project(y.view(x.shape[0], -1), [self.o])[0]
+
+    def evict(self, batch, budget, limit=None, sinks=0, recent=0, new_len=None, stream=None):
+        """Cut the batch's sequences that have more than ``limit`` tokens cached to ``budget``, in place, by the
+        weight that they gathered (see ``binding.kv4_evict``). Returns the new lengths; the last of the layers that
+        share the batch may write them over its kv_len (``new_len``)."""
+        if self.mass is None:
+            raise ValueError("the block gathers no attention weight")
+        return binding.kv4_evict(self.cache, batch, self.mass, budget, limit=limit, sinks=sinks, recent=recent, new_len=new_len,
+                                 stream=stream)
