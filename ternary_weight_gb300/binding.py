@@ -686,7 +686,7 @@ def kv4_mass(cache):
 
 
 def _kv4_mass_rows(cache, mass):
-    if mass.shape != (cache.n_pages, cache.kv_heads, KV4_PAGE) or str(mass.dtype) != "torch.float32":
+    if mass.shape != (cache.n_pages, cache.kv_heads, KV4_PAGE) or mass.dtype != _kv4_torch[0].float32:
         raise ValueError("mass must be n_pages x kv_heads x %d float32" % KV4_PAGE)
     if mass.get_device() != cache.index or not mass.is_contiguous():
         raise ValueError("mass must be contiguous, on the cache's device")
@@ -761,13 +761,17 @@ def kv4_evict(cache, batch, mass, budget, limit=None, sinks=0, recent=0, into=No
     n = batch.kv_len.numel()
     on = handle(cache, batch, stream)
     _kv4_mass_rows(cache, mass)
+    index = cache.index
     for t, shape in ((into, (n, into.shape[-1]) if into is not None else None), (new_len, (n,))):
-        if t is not None and (t.dtype != torch.int32 or t.shape != shape or t.get_device() != cache.index or
+        if t is not None and (t.dtype != torch.int32 or t.shape != shape or t.get_device() != index or
                               not t.is_contiguous()):
             raise ValueError("into (batch x pages) and new_len (batch) must be contiguous int32 on the cache's device")
     if new_len is None:
         new_len = _kv4_empty(torch, (n,), torch.int32, cache.device, stream)
-    need = kv4_evict_workspace_size(cache, batch, budget)
+    key = ("evict", cache.kv_heads, cache.head_dim, budget)
+    need = batch._ws.get(key)
+    if need is None:
+        need = batch._ws[key] = kv4_evict_workspace_size(cache, batch, budget)
     keep, ws, ws_bytes = _kv4_workspace(torch, cache, workspace, need, stream)
     st = lib().bitnet_kv4_evict(cache._ref, batch._ref, mass.data_ptr(), budget, limit, sinks, recent,
                                 into.data_ptr() if into is not None else None, into.shape[1] if into is not None else 0,

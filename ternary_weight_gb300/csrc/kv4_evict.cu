@@ -11,6 +11,7 @@
 // Bound by latency where sequences are few: loads that depend on each other (length, page, mass; kept token, page, data) and
 // the cluster's barriers; by the moved bytes where they are many.
 #include "kv4.cuh"
+#include "smem_limit.h"
 
 namespace bitnet {
 namespace {
@@ -322,6 +323,13 @@ __global__ void kv4_evict_lengths(Kv4 c, Kv4Evict e) {
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 int cap_of(const Kv4& c, int budget) { return budget < c.max_kv ? budget : c.max_kv; }
 
+template <int D>
+cudaError_t launch(const cudaLaunchConfig_t& cfg, const Kv4& c, const Kv4Evict& e, int32_t* kept, int cluster, int ranks, bool write_len) {
+  static std::atomic<uint64_t> configured{0};
+  if (cudaError_t err = allow_smem(configured, kv4_evict_kernel<D>, MAX_RANKS * 4)) return err;
+  return cudaLaunchKernelEx(&cfg, kv4_evict_kernel<D>, c, e, kept, cap_of(c, e.budget), cluster, ranks, write_len);
+}
+
 }  // namespace
 
 int64_t kv4_evict_ws_bytes(const Kv4& c, int budget) { return align256((int64_t)c.batch * c.kv_heads * cap_of(c, budget) * 4); }
@@ -333,8 +341,6 @@ cudaError_t launch_kv4_evict(const Kv4& c, int dim, const Kv4Evict& e, void* ws,
   int64_t per = ((c.max_kv + cluster * WARPS - 1) / (cluster * WARPS) + 31) / 32 * 32;
   const int ranks = (int)(per * WARPS < MAX_RANKS ? per * WARPS : MAX_RANKS);
   const bool over = e.new_len == c.kv_len;
-  auto kernel = dim == 128 ? kv4_evict_kernel<128> : kv4_evict_kernel<64>;
-  if (cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_RANKS * 4)) return err;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -345,7 +351,10 @@ cudaError_t launch_kv4_evict(const Kv4& c, int dim, const Kv4Evict& e, void* ws,
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, c, e, static_cast<int32_t*>(ws), cap_of(c, e.budget), cluster, ranks, e.new_len && !over)) return err;
+  int32_t* kept = static_cast<int32_t*>(ws);
+  if (cudaError_t err = dim == 128 ? launch<128>(cfg, c, e, kept, cluster, ranks, e.new_len && !over)
+                                   : launch<64>(cfg, c, e, kept, cluster, ranks, e.new_len && !over))
+    return err;
   if (!over) return cudaSuccess;
   kv4_evict_lengths<<<(c.batch + 127) / 128, 128, 0, st>>>(c, e);
   return cudaGetLastError();

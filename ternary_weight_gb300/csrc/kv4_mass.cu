@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "kv4_mass.cuh"
+#include "smem_limit.h"
 
 namespace bitnet {
 namespace {
@@ -993,7 +994,8 @@ Cluster cluster_of(const Kv4& c, const Plan& p, int share, int num_sms) {
 template <int D, int NT, bool F32>
 cudaError_t launch_cluster(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Cluster& k, cudaStream_t st) {
   auto kernel = kv4_mass_cluster<D, NT, F32>;
-  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreBytes)) return e;
+  static std::atomic<uint64_t> configured{0};
+  if (cudaError_t e = allow_smem(configured, kernel, kScoreBytes)) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1021,8 +1023,9 @@ template <int D, bool F32>
 cudaError_t launch_many(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
   const int64_t units = (int64_t)c.batch * c.kv_heads;
   const int rows_smem = (int)sizeof(RowsShared<D>), shares_smem = 2 * (int)sizeof(Slab<D>);
-  if (cudaError_t e = cudaFuncSetAttribute(kv4_mass_rows_many<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem)) return e;
-  if (cudaError_t e = cudaFuncSetAttribute(kv4_mass_shares<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, shares_smem)) return e;
+  static std::atomic<uint64_t> configured[2];
+  if (cudaError_t e = allow_smem(configured[0], kv4_mass_rows_many<D, F32>, rows_smem)) return e;
+  if (cudaError_t e = allow_smem(configured[1], kv4_mass_shares<D, F32>, shares_smem)) return e;
   kv4_mass_rows_many<D, F32><<<grid_of(units * p.blocks * p.chunks), THREADS, rows_smem, st>>>(c, a, m.voters, p, s);
   if (cudaError_t e = cudaGetLastError()) return e;
   if (p.chunks > 1) {
@@ -1054,6 +1057,7 @@ int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters) {
       continue;
     }
     const Plan p = plan_of(c, q_heads / c.kv_heads, voters, f32, 152);
+    if (p.tiles == 0 || (p.nt <= 2 && cluster_of(c, p, q_heads / c.kv_heads, 152).tiles)) continue;
     const int64_t n = part_bytes(c, p) + votes_bytes(c, p) + slabs_bytes(c, p, dim);
     most = n > most ? n : most;
   }

@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "kv4_mass.cuh"
+#include "smem_limit.h"
 
 namespace bitnet {
 namespace {
@@ -582,8 +583,9 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan&
   float2* part = reinterpret_cast<float2*>(ws + blocks_bytes(c, p, D, F32));
   float* shares = reinterpret_cast<float*>(ws + blocks_bytes(c, p, D, F32) + part_bytes(c, p));
   const int64_t units = (int64_t)c.batch * c.kv_heads;
-  if (cudaError_t e = cudaFuncSetAttribute(kv4_mass_tc_rows<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ROWS_SMEM)) return e;
-  if (cudaError_t e = cudaFuncSetAttribute(kv4_mass_tc_votes<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::VOTES_SMEM)) return e;
+  static std::atomic<uint64_t> configured[2];
+  if (cudaError_t e = allow_smem(configured[0], kv4_mass_tc_rows<D, F32>, S::ROWS_SMEM)) return e;
+  if (cudaError_t e = allow_smem(configured[1], kv4_mass_tc_votes<D, F32>, S::VOTES_SMEM)) return e;
   kv4_mass_tc_rows<D, F32><<<grid_of(units * p.blocks * p.chunks, 1 << 20), THREADS, S::ROWS_SMEM, st>>>(c, a, m.voters, p, blocks, part);
   if (cudaError_t e = cudaGetLastError()) return e;
   if (p.chunks > 1) {

@@ -18,6 +18,7 @@
 #include <cuda_fp16.h>
 
 #include "bitnet_dev.cuh"
+#include "smem_limit.h"
 #include "w4.h"
 
 namespace bitnet {
@@ -167,9 +168,11 @@ __device__ __forceinline__ void load_rows(const Call& c, uint8_t* smem) {
   __syncthreads();
 }
 
-// A piece of weights as a lane loads it: 32 codes of rows g and g + 8, with their scales and zero points. A lane's
-// words of one matrix step stay in one group: with groups of 128 a lane takes 16 bytes of each row, with
-// 64 twice 8, with 32 four times 4.
+// A piece of weights as a lane loads it: 16 bytes of rows g and g + 8, and their scales and zero points. The words of a
+// matrix step have to be of one group over the four lanes of a row: with groups of 128 each lane's own 16 bytes are; with
+// groups of 64 a lane loads twice 8 bytes; with 32 the row's 64 bytes are dealt out anew through shared memory, since
+// every load touches a line for each row (one row x 131072 x 2560: groups of 32 by loads of 4 bytes 59.5 us, dealt
+// out 51.6; groups of 64 by loads of 8 bytes 44.3, dealt out 45.6).
 template <int G, bool ZEROS>
 struct Piece {
   static constexpr int PER = 128 / G;  // groups
@@ -178,25 +181,41 @@ struct Piece {
   uint32_t z[2];
   // codes, scales, zeros: of this lane's row and quad place, at the piece
   __device__ __forceinline__ void load(int h, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros) {
-    if (G == 128) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(codes));
-      w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
-      s[h][0] = __ldg(scales);
-      if (ZEROS) z[h] = __ldg(zeros);
-    } else if (G == 64) {
+    if (G == 64) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const uint2 v = __ldcs(reinterpret_cast<const uint2*>(codes + p * 32));
         w[h][2 * p] = v.x, w[h][2 * p + 1] = v.y;
       }
+    } else {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(codes));
+      w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
+    }
+    if (G == 128) {
+      s[h][0] = __ldg(scales);
+      if (ZEROS) z[h] = __ldg(zeros);
+    } else if (G == 64) {
       s[h][0] = __ldg(reinterpret_cast<const uint32_t*>(scales));
       if (ZEROS) z[h] = __ldg(reinterpret_cast<const uint16_t*>(zeros));
     } else {
-#pragma unroll
-      for (int p = 0; p < 4; ++p) w[h][p] = __ldg(reinterpret_cast<const uint32_t*>(codes + p * 16));
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(scales));
-      s[h][0] = v.x, s[h][PER == 4 ? 1 : 0] = v.y;
+      const uint2 sc = __ldg(reinterpret_cast<const uint2*>(scales));
+      s[h][0] = sc.x, s[h][PER == 4 ? 1 : 0] = sc.y;
       if (ZEROS) z[h] = __ldg(reinterpret_cast<const uint32_t*>(zeros));
+    }
+  }
+  // The words in the order of the fragments. buf: 1 KB of this warp's; pieces of 16 bytes of row r are exchanged so that
+  // neither stores nor loads meet a bank twice.
+  __device__ __forceinline__ void deal(uint8_t* buf, int g, int t) {
+    if (G != 32) return;
+    const auto sw = [](int r) { return ((r >> 1) & 1) * 2 + ((r >> 2) & 1); };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(buf + (g + 8 * h) * 64 + (t ^ sw(g)) * 16) = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* row = buf + (g + 8 * h) * 64;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) w[h][p] = *reinterpret_cast<const uint32_t*>(row + (p ^ sw(g)) * 16 + t * 4);
     }
   }
   __device__ __forceinline__ float scale(int h, int p) const {
@@ -221,7 +240,7 @@ struct Shape {
 template <int G, bool ZEROS, int NT>
 __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) w4_matmul_kernel(Call c) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int PER = 128 / G, WARPS = Shape<NT>::WARPS, AHEAD = Shape<NT>::AHEAD, BYTES = G == 128 ? 16 : G == 64 ? 8 : 4;
+  constexpr int PER = 128 / G, WARPS = Shape<NT>::WARPS, AHEAD = Shape<NT>::AHEAD;
   const int K = c.w.K, N = c.w.N, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // known to be the same for all lanes
   const int tiles = (N + ROWS - 1) / ROWS, blocks = K / 128, groups = K / G;
@@ -242,7 +261,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) w4_matmul_kernel(Call c
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int in = min(g + 8 * h, N - 1 - in_tile * ROWS);  // rows beyond the last: the last
-      code_at[h] = in * (K / 2) + t * BYTES;
+      code_at[h] = in * (K / 2) + t * (G == 64 ? 8 : 16);
       scale_at[h] = in * groups;
     }
   };
@@ -270,6 +289,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) w4_matmul_kernel(Call c
   const float2* factor = reinterpret_cast<const float2*>(smem);
   const uint4* xf = reinterpret_cast<const uint4*>(smem + align16(c.m * 8));
   float* share = reinterpret_cast<float*>(smem + rows_bytes(K, c.m, c.cols));
+  uint8_t* deals = smem + rows_bytes(K, c.m, c.cols) + WARPS * Shape<NT>::SHARE + warp * 2048;
   __shared__ int share_tile[WARPS];
   if (lane == 0) share_tile[warp] = -1;
 
@@ -308,7 +328,8 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) w4_matmul_kernel(Call c
     for (int u = 0; u < AHEAD; ++u) {
       if (left <= 0) break;
       --left;
-      const Piece<G, ZEROS>& p = ring[u];
+      Piece<G, ZEROS>& p = ring[u];
+      p.deal(deals + (u & 1) * 1024, g, t);  // two places in turn: one barrier each
       float acc[NT][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -375,15 +396,16 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) w4_matmul_kernel(Call c
 }
 
 template <int NT>
-int smem_of(int K, int m, int cols) {
-  return rows_bytes(K, m, cols) + Shape<NT>::WARPS * Shape<NT>::SHARE;
+int smem_of(int group, int K, int m, int cols) {
+  return rows_bytes(K, m, cols) + Shape<NT>::WARPS * (Shape<NT>::SHARE + (group == 32 ? 2048 : 0));
 }
 
 template <int G, bool ZEROS, int NT>
 cudaError_t launch(const Call& c, int num_sms, cudaStream_t st) {
-  const int smem = smem_of<NT>(c.w.K, c.m, c.cols);
+  const int smem = smem_of<NT>(G, c.w.K, c.m, c.cols);
   auto kernel = w4_matmul_kernel<G, ZEROS, NT>;
-  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+  static std::atomic<uint64_t> configured{0};
+  if (cudaError_t e = allow_smem(configured, kernel, MAX_SMEM - 1024)) return e;
   const int tiles = (c.w.N + ROWS - 1) / ROWS;
   kernel<<<min(tiles, num_sms), Shape<NT>::THREADS, smem, st>>>(c);
   return cudaGetLastError();
@@ -409,8 +431,8 @@ cudaError_t launch_w4_matmul(const W4& w, const void* x, bool bf16, int64_t M, f
   int most = 64 / parts;
   const auto fits = [&](int m) {
     const int cols = m * parts;
-    return (cols <= 8 ? smem_of<1>(w.K, m, cols) : cols <= 16 ? smem_of<2>(w.K, m, cols)
-            : cols <= 32 ? smem_of<4>(w.K, m, cols) : smem_of<8>(w.K, m, cols)) <= MAX_SMEM - 1024;
+    return (cols <= 8 ? smem_of<1>(w.group, w.K, m, cols) : cols <= 16 ? smem_of<2>(w.group, w.K, m, cols)
+            : cols <= 32 ? smem_of<4>(w.group, w.K, m, cols) : smem_of<8>(w.group, w.K, m, cols)) <= MAX_SMEM - 1024;
   };
   while (most > 1 && !fits(most)) --most;
   if (M > most) {  // launches of like size: fewer columns each cost less

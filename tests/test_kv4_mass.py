@@ -53,7 +53,7 @@ def call(lib, c=None, b=None, **kw):
     (dict(voters=1 << 31), -1), (dict(decay=float("inf")), -1), (dict(mass=None), -1), (dict(out=None), -1), (dict(ws=None), -1), (dict(ws_bytes=0), -1),
     (dict(mass=FAKE + 4), -2), (dict(out=FAKE + 8), -2), (dict(ws=FAKE + 128), -2), (dict(q=FAKE + 8), -2)])
 def test_bad_calls_are_refused(lib, kw, want):
-    b = batch(total_q=3) if want else batch()
+    b = batch(total_q=3, max_pages=1 << 16, max_kv=1 << 22) if want else batch()  # long enough for a workspace
     assert call(lib, b=b, **kw) == want
 
 
