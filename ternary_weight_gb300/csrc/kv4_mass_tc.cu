@@ -110,49 +110,74 @@ struct Half {
   }
 };
 
-// The queries of rows row0 .. row0 + 127 of a unit as an operand, and their constants: D / 8 lanes a row, 8 numbers each.
+// The queries of rows row0 .. row0 + 127 of a unit as an operand, and their constants: W = D / 8 lanes a row. Lane w
+// loads numbers 8 w .. 8 w + 7, which are nibble n = w / (W / 8) of eight words; nibbles n and n + 4 of a word lie side by side
+// in the operand, so half of a lane's numbers go to the lane that has the other nibble, and half of that one's come here.
 template <int D, bool F32>
 __device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int row0, uint32_t image, Constants& con) {
   constexpr int W = D / 8, PER = THREADS / W, BATCH = 4, IMAGE = 128 * D * 2;
-  const int w = threadIdx.x % W, rows = r.votes * a.share;
+  const int w = threadIdx.x % W, rows = r.votes * a.share, n = w / (W / 8);
+  const bool high = n >= 4;
+  const int word0 = 8 * w % W + (high ? 4 : 0);  // of the four words that the lane stores
+  const float odd = n & 1 ? 0.0625f : 1.0f;
 #pragma unroll 1
   for (int k0 = threadIdx.x / W; k0 < ROWS; k0 += PER * BATCH) {
     float x[BATCH][8];
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const int row = row0 + k0 + k * PER, i = row / a.share;
-      const bool there = row < rows;
-      const int64_t at = there ? (int64_t)(r.s.q0 + r.s.n - r.votes + i) * a.q_stride + (int64_t)(r.h * a.share + row - i * a.share) * D + w : 0;
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
-        x[k][n] = !there ? 0.0f
-                  : F32  ? static_cast<const float*>(a.q)[at + W * n]
-                         : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + W * n]);
+      for (int j = 0; j < 8; ++j) x[k][j] = 0.0f;
+      if (row >= rows) continue;
+      const int64_t at = (int64_t)(r.s.q0 + r.s.n - r.votes + i) * a.q_stride + (int64_t)(r.h * a.share + row - i * a.share) * D + 8 * w;
+      if (F32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+        const float4 u = __ldg(p), v = __ldg(p + 1);
+        x[k][0] = u.x, x[k][1] = u.y, x[k][2] = u.z, x[k][3] = u.w, x[k][4] = v.x, x[k][5] = v.y, x[k][6] = v.z, x[k][7] = v.w;
+      } else {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[k][2 * j] = __uint_as_float(u[j] << 16), x[k][2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+      }
     }
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const int in = k0 + k * PER, row = row0 + in;
-      float sum = 0.0f;
+      float sum = ((x[k][0] + x[k][1]) + (x[k][2] + x[k][3])) + ((x[k][4] + x[k][5]) + (x[k][6] + x[k][7]));
       uint32_t top = 0;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) sum += x[k][n], top = max(top, __float_as_uint(x[k][n]) & 0x7fffffffu);
+      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[k][j]) & 0x7fffffffu);
 #pragma unroll
       for (int o = W / 2; o >= 1; o >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
+      // the row's power of two: its largest number comes to [2^14, 2^15)
       int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);
       e = e > 127 ? 127 : e < -113 ? -113 : e;
       const float up = copysignf(__int_as_float((e + 127) << 23), a.scale);
-      float hi[8], lo[8];
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        hi[n] = x[k][n] * up * (n & 1 ? 0.0625f : 1.0f);
-        lo[n] = hi[n] - __half2float(__float2half_rn(hi[n]));
+      for (int part = 0; part < (F32 ? 2 : 1); ++part) {
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float y0 = x[k][2 * j] * up * odd, y1 = x[k][2 * j + 1] * up * odd;
+          h[j] = pack_half2(y0, y1);
+          if (part) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+            h[j] = pack_half2(y0 - f.x, y1 - f.y);
+          }
+        }
+        const uint32_t to = image + part * IMAGE + 4 * (n & 3);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? h[j] : h[2 + j], W / 2), own = high ? h[2 + j] : h[j];
+          const uint32_t lo = high ? got : own, hi = high ? own : got;
+          st_shared_u32(to + chunk_at(in, word0 + 2 * j), __byte_perm(lo, hi, 0x5410));
+          st_shared_u32(to + chunk_at(in, word0 + 2 * j + 1), __byte_perm(lo, hi, 0x7632));
+        }
       }
-      const uint32_t to = image + chunk_at(in, w);
-      sts128(to, pack_half2(hi[0], hi[4]), pack_half2(hi[1], hi[5]), pack_half2(hi[2], hi[6]), pack_half2(hi[3], hi[7]));
-      if (F32) sts128(to + IMAGE, pack_half2(lo[0], lo[4]), pack_half2(lo[1], lo[5]), pack_half2(lo[2], lo[6]), pack_half2(lo[3], lo[7]));
       if (w == 0) {
         const float c1 = __fmul_rn(fabsf(a.scale), kLog2e);
         const int f = 24 - e, half = f / 2;
@@ -223,16 +248,20 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
       continue;
     }
     const int krow = threadIdx.x >> 1, khalf = threadIdx.x & 1;
+    // ids are asked for a tile before they are used, and looked at then
+    constexpr int NONE = INT32_MIN;
     const auto page_id = [&](int tile) {
       const int page = tile * 2 + (krow >> 6);
-      if (tile >= t1 || page >= pages) return -1;
-      const int id = c.page_table[(int64_t)r.b * c.max_pages + page];
+      return tile < t1 && page < pages ? c.page_table[(int64_t)r.b * c.max_pages + page] : NONE;
+    };
+    const auto checked = [&](int id) {
       if (id >= 0 && id < c.n_pages) return id;
-      bad = true;
+      bad |= id != NONE;
       return -1;
     };
     Half<D> codes;
-    codes.load(c, page_id(t), r.h, krow & 63, khalf);
+    codes.load(c, checked(page_id(t)), r.h, krow & 63, khalf);
+    int then = t < t1 ? next(t + 1) : t1, id_then = page_id(then);
     load_block<D, F32>(a, r, row0, base, con);
     __syncthreads();
     const float4 ab4 = con.ab[row >> 1];
@@ -260,8 +289,8 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
         if (elect_one()) issue<D, S::PARTS, 1>(tmem + buf * 128, base, base + KEYS + buf * S::IMAGE, &done[buf]);
         __syncwarp();
       }
-      const int then = t < t1 ? next(t + 1) : t1;
-      if (then < t1) codes.load(c, page_id(then), r.h, krow & 63, khalf);
+      if (then < t1) codes.load(c, checked(id_then), r.h, krow & 63, khalf);
+      const int after = then < t1 ? next(then + 1) : t1, id_after = page_id(after);
       if (before >= 0) {
         const uint32_t was = issued - 1, at = was & 1;
         mbar_wait_warp(&done[at], (was >> 1) & 1, &abort);
@@ -312,7 +341,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
       }
       before = -1;
       if (t < t1) before = t, ++issued;
-      t = then;
+      t = then, then = after, id_then = id_after;
     }
     if (half) halves[row] = make_float2(m, l);
     __syncthreads();
