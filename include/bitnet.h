@@ -501,8 +501,8 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache *cache, const bitnet_
  *   workspace : device, 256-byte aligned, at least bitnet_kv4_attention_mass_workspace_size bytes (for the same
  *            cache, batch sizes, q_heads and voters). Needs no initialisation; calls that may run at the same
  *            time need one each.
- * Pages that two sequences of the batch share gather the votes of one of them. The results of a call are the same
- * bits each time it is made with the same arguments.
+ * The masses of a page that two sequences of the batch share are not defined afterwards; all others are the same bits
+ * each time the call is made with the same arguments.
  *
  * bitnet_kv4_evict -- sequences of more than `limit` cached tokens keep `budget` of them in each key/value
  *   head: the first `sinks`, the last `recent`, and of the others those of the greatest mass (a NaN is

@@ -248,64 +248,70 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     sync_all();  // the list is written, and no block reads another's counts any more
   }
 
-  // ---- the kept tokens move
-  constexpr int LANES = D / 16, PIECES = LANES / 2, TOKENS = THREADS / LANES, BATCH = 4;
-  const int part = tid % LANES, worker = tid / LANES;
-  const int32_t* from = c.page_table + (int64_t)b * c.max_pages;
-  const int32_t* to = e.into ? e.into + (int64_t)b * e.into_pages : from;
-  const int row_of_part = part < PIECES ? 0 : kKvPage;
+  // ---- the kept tokens move (all unsigned 32-bit: their indexes are below 2^30)
+  constexpr uint32_t LANES = D / 16, PIECES = LANES / 2, TOKENS = THREADS / LANES, BATCH = 4, PAGE = kKvPage;
+  const uint32_t part = tid % LANES, worker = tid / LANES, keeps = s.keeps, piece = part % PIECES * 16;
+  const bool is_key = part < PIECES;
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(c.page_table + (int64_t)b * c.max_pages);
+  const uint32_t* to = e.into ? reinterpret_cast<const uint32_t*>(e.into + (int64_t)b * e.into_pages) : from;
+  const uint32_t n_pages = c.n_pages, heads = c.kv_heads;
+  // a head's block of a page, in blocks; where the lane's 16 bytes and the parameters of place t lie in it
+  const auto rho = [](uint32_t t) { return (t & ~7u) | (t & 3u) << 1 | (t >> 2 & 1u); };
+  const auto data_at = [&](uint32_t t) { return (is_key ? rho(t) : PAGE + t) * (D / 2) + piece; };
   // the sources of the next chunk are looked up while this one's data is on its way
-  int src[BATCH];
-  const auto look = [&](int64_t first) {
+  constexpr uint32_t NONE = 0xffffffffu;
+  uint32_t src[BATCH];
+  const auto look = [&](uint32_t first) {
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int64_t r = first + me * TOKENS * BATCH + worker + i * TOKENS;
-      src[i] = -1;
-      if (r < s.keeps) src[i] = cut ? list[r] : (int)r;
-      if (!e.into && src[i] == r) src[i] = -1;  // it stays
+    for (uint32_t i = 0; i < BATCH; ++i) {
+      const uint32_t r = first + i * TOKENS;
+      src[i] = r < keeps ? (cut ? (uint32_t)list[r] : r) : NONE;
+      if (!e.into && src[i] == r) src[i] = NONE;  // it stays
     }
   };
-  look(0);
-  for (int64_t first = 0; first < s.keeps; first += (int64_t)cluster * TOKENS * BATCH) {
-    const int64_t r0 = first + me * TOKENS * BATCH + worker;
+  const uint32_t chunk = cluster * TOKENS * BATCH, mine = me * TOKENS * BATCH + worker;
+  look(mine);
+#pragma unroll 1
+  for (uint32_t first = 0; first < keeps; first += chunk) {
+    const uint32_t r0 = first + mine;
     uint4 data[BATCH];
-    uint2 par[BATCH];
-    float mass[BATCH];
-    int id[BATCH], low[BATCH];  // low: the source's place in its page, -1 for nothing
+    uint2 par[BATCH];  // lane 0: the parameters; lane 1: the mass
+    uint32_t id[BATCH], low[BATCH];  // low: the source's place in its page
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      id[i] = src[i] >= 0 ? from[src[i] / kKvPage] : 0;
-      low[i] = src[i] >= 0 ? src[i] % kKvPage : -1;
+    for (uint32_t i = 0; i < BATCH; ++i) id[i] = src[i] != NONE ? from[src[i] / PAGE] : NONE - 1;
+#pragma unroll
+    for (uint32_t i = 0; i < BATCH; ++i) {
+      low[i] = src[i] != NONE ? src[i] % PAGE : NONE;
+      if (src[i] == NONE) continue;
+      if (id[i] >= n_pages) {
+        bad = true, low[i] = NONE;
+        continue;
+      }
+      const uint64_t block = (uint64_t)id[i] * heads + h;
+      const uint8_t* blk = c.pages + block * BLK;
+      data[i] = *reinterpret_cast<const uint4*>(blk + data_at(low[i]));
+      if (part == 0) par[i] = *reinterpret_cast<const uint2*>(blk + PAGE * D + rho(low[i]) * 8);
+      if (part == 1) par[i].x = __float_as_uint(e.mass[block * PAGE + low[i]]);
     }
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      if (id[i] < 0 || id[i] >= c.n_pages) bad = true, low[i] = -1;
-      if (low[i] < 0) continue;
-      const int t = low[i];
-      const uint8_t* blk = c.pages + ((int64_t)id[i] * c.kv_heads + h) * BLK;
-      const int row = part < PIECES ? kv4_rho(t) : row_of_part + t;
-      data[i] = *reinterpret_cast<const uint4*>(blk + row * (D / 2) + part % PIECES * 16);
-      if (part == 0) par[i] = *reinterpret_cast<const uint2*>(blk + kKvPage * D + kv4_rho(t) * 8);
-      if (part == 1) mass[i] = e.mass[((int64_t)id[i] * c.kv_heads + h) * kKvPage + t];
-    }
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      id[i] = low[i] >= 0 ? to[(r0 + i * TOKENS) / kKvPage] : 0;
-      if (id[i] < 0 || id[i] >= c.n_pages) bad = true, low[i] = -1;
-    }
-    look(first + (int64_t)cluster * TOKENS * BATCH);
+    for (uint32_t i = 0; i < BATCH; ++i) id[i] = low[i] != NONE ? to[(r0 + i * TOKENS) / PAGE] : NONE - 1;
+    look(r0 + chunk);
     if (!e.into) sync_all();
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      if (low[i] < 0) continue;
-      const int r = (int)(r0 + i * TOKENS), t = r % kKvPage;
-      uint8_t* blk = c.pages + ((int64_t)id[i] * c.kv_heads + h) * BLK;
-      const int row = part < PIECES ? kv4_rho(t) : row_of_part + t;
-      int piece = part % PIECES;
-      if (D == 128 && part >= PIECES && ((low[i] ^ r) & 2)) piece ^= 2;  // the halves of a wide value row
-      *reinterpret_cast<uint4*>(blk + row * (D / 2) + piece * 16) = data[i];
-      if (part == 0) *reinterpret_cast<uint2*>(blk + kKvPage * D + kv4_rho(t) * 8) = par[i];
-      if (part == 1) e.mass[((int64_t)id[i] * c.kv_heads + h) * kKvPage + t] = mass[i];
+    for (uint32_t i = 0; i < BATCH; ++i) {
+      if (low[i] == NONE) continue;
+      if (id[i] >= n_pages) {
+        bad = true;
+        continue;
+      }
+      const uint32_t r = r0 + i * TOKENS, t = r % PAGE;
+      const uint64_t block = (uint64_t)id[i] * heads + h;
+      uint8_t* blk = c.pages + block * BLK;
+      // the halves of a wide value row are exchanged where bit 1 of the place is set
+      const uint32_t turn = D == 128 && !is_key ? ((low[i] ^ r) & 2) << 4 : 0;
+      *reinterpret_cast<uint4*>(blk + (data_at(t) ^ turn)) = data[i];
+      if (part == 0) *reinterpret_cast<uint2*>(blk + PAGE * D + rho(t) * 8) = par[i];
+      if (part == 1) e.mass[block * PAGE + t] = __uint_as_float(par[i].x);
     }
     if (!e.into) sync_all();
   }
