@@ -21,9 +21,11 @@ constexpr int BINS = 2048;
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX_RANKS = 20480;  // that a block keeps (80 KB, two blocks an SM); longer runs are read again each time
 
-// Masses as whole numbers in the same order; a NaN above all, both zeros alike.
+// Masses as whole numbers in the same order; a NaN above all, both zeros alike. Tokens that are kept in any case (the
+// first and the last ones) rank above every mass.
+constexpr uint32_t SURE = 0xffffffffu;
 __device__ __forceinline__ uint32_t rank_of(float x) {
-  if (x != x) return 0xffffffffu;
+  if (x != x) return SURE - 1;
   const uint32_t u = __float_as_uint(x + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
@@ -82,14 +84,14 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
   bool bad = false;
   int32_t* list = kept + (int64_t)unit * cap;
   if (cut) {
-    const int lo = e.sinks, hi = s.len - e.recent;  // the tokens that are chosen from
-    uint32_t want = (uint32_t)(e.budget - e.sinks - e.recent);  // how many of them
+    const int lo = e.sinks, hi = s.len - e.recent;  // the tokens that masses decide over
+    uint32_t want = (uint32_t)e.budget;
     // this block's run of tokens, and its warps'
     const int per = ((s.len + cluster * WARPS - 1) / (cluster * WARPS) + 31) / 32 * 32;
     const int run0 = (int)min((int64_t)me * WARPS * per, (int64_t)s.len), j0 = (int)min(run0 + (int64_t)warp * per, (int64_t)s.len), j1 = (int)min(j0 + (int64_t)per, (int64_t)s.len);
     const bool keep = WARPS * per <= ranks_kept;
-    const auto read = [&](int j) { return rank_of(*mass_of(c, e, b, h, j, &bad)); };
-    if (keep && want) {
+    const auto ranked = [&](int j, float mass) { return j < lo || j >= hi ? SURE : rank_of(mass); };
+    if (keep) {
       // the page ids of the next 32 pages, one a lane, then the masses of 8 x 32 tokens at a time
       for (int p0 = j0 / kKvPage; p0 * kKvPage < j1; p0 += 32) {
         int id = 0;
@@ -108,38 +110,39 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int j = (p0 + q) * kKvPage + i * 32 + lane;
-            if (j >= j0 && j < j1) ranks[j - run0] = rank_of(m[i]);
+            if (j >= j0 && j < j1) ranks[j - run0] = ranked(j, m[i]);
           }
         }
       }
       __syncwarp();
     }
-    const auto rank = [&](int j) { return keep ? ranks[j - run0] : read(j); };
+    // of token j of this warp's run; 0, which is no rank, past its end
+    const auto rank = [&](int j) {
+      if (j >= j1) return 0u;
+      return keep ? ranks[j - run0] : ranked(j, *mass_of(c, e, b, h, j, &bad));
+    };
     uint32_t least = 0, mask = 0;  // the digits found so far
-    const bool none = want == 0;
 #pragma unroll 1
-    for (int pass = 0; !none && pass < 3; ++pass) {
+    for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
       for (int i = tid; i < BINS; i += THREADS) bins[i] = 0;
       __syncthreads();
       // tokens without any mass may be many: a warp's are counted together, not one after another in one bin
       const uint32_t digits = (1u << width) - 1, zero = 0x80000000u;
       uint32_t zeros = 0;
-      const int k0 = max(j0, lo), k1 = min(j1, hi);
 #pragma unroll 1
-      for (int j = k0 + lane; j - lane < k1; j += 4 * 32) {
+      for (int j = j0 + lane; j - lane < j1; j += 4 * 32) {
         uint32_t r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = j + 32 * i < k1 ? rank(j + 32 * i) : ~least;
+        for (int i = 0; i < 4; ++i) r[i] = rank(j + 32 * i);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool in = j + 32 * i < k1 && (r[i] & mask) == least;
-          if (in && r[i] != zero) atomicAdd(&bins[(r[i] >> shift) & digits], 1u);
-          zeros += in && r[i] == zero;
+          if (r[i] == zero) ++zeros;
+          else if ((r[i] & mask) == least && r[i]) atomicAdd(&bins[(r[i] >> shift) & digits], 1u);
         }
       }
       zeros = __reduce_add_sync(0xffffffffu, zeros);
-      if (lane == 0 && zeros) atomicAdd(&bins[(zero >> shift) & digits], zeros);
+      if (lane == 0 && zeros && (zero & mask) == least) atomicAdd(&bins[(zero >> shift) & digits], zeros);
       sync_all();
       // The digit from which on `want` tokens are counted, from above. Each block adds up its slice of the bins over the
       // cluster, a slice's total goes to all blocks, and the block whose slice has the digit tells it.
@@ -194,23 +197,18 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       want = found[1];
     }
     // `want` is now how many of the tokens at `least` are kept. Each warp counts those of its run, then lists them.
-    const auto kind = [&](int j, bool* sure, bool* level) {
-      const bool middle = j >= lo && j < hi;
-      const uint32_t r = j < j1 && middle && !none ? rank(j) : 0;
-      *sure = j < j1 && (!middle || (!none && r > least));
-      *level = j < j1 && middle && !none && r == least;
-    };
     // (their ballots stay in the bins' place, where they fit)
     const bool fits = WARPS * per <= BINS / 2 * 32;
     uint2* masks = reinterpret_cast<uint2*>(bins) + warp * (per / 32);
     int sures = 0, levels = 0;
+#pragma unroll 1
     for (int j = j0 + lane; j - lane < j1; j += 4 * 32) {
-      bool sure[4], level[4];
+      uint32_t r[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) kind(j + 32 * i, &sure[i], &level[i]);
+      for (int i = 0; i < 4; ++i) r[i] = rank(j + 32 * i);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t sm = __ballot_sync(0xffffffffu, sure[i]), lm = __ballot_sync(0xffffffffu, level[i]);
+        const uint32_t sm = __ballot_sync(0xffffffffu, r[i] > least), lm = __ballot_sync(0xffffffffu, r[i] == least);
         sures += __popc(sm);
         levels += __popc(lm);
         if (fits && lane == 0 && j + 32 * i < j1) masks[(j - j0) / 32 + i] = make_uint2(sm, lm);
@@ -234,9 +232,8 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       if (fits) {
         m = masks[(j - j0) / 32];
       } else {
-        bool sure, level;
-        kind(j, &sure, &level);
-        m = make_uint2(__ballot_sync(0xffffffffu, sure), __ballot_sync(0xffffffffu, level));
+        const uint32_t r = rank(j);
+        m = make_uint2(__ballot_sync(0xffffffffu, r > least), __ballot_sync(0xffffffffu, r == least));
       }
       const uint32_t below = (1u << lane) - 1;
       const int ls = levels + __popc(m.y & below), at = sures + __popc(m.x & below) + min(ls, (int)want);
