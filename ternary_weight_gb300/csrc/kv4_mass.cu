@@ -14,9 +14,15 @@
 // shifted; q' carries the 2^-4): 5 instructions for a word of 8 codes, sums exact in fp32. Lane t of four takes 16
 // bytes of a key row (8 with D = 64), so a warp's loads of a tile are contiguous, straight from the cache.
 //
-// Few columns (16 at most): both kernels are bound by the keys' bytes, the second kernel's mostly from L2. Many: by
-// the products and exponentials; columns go in blocks of 64 whose fragments the first kernel leaves in the workspace, the second
-// kernel's blocks keep their tiles' codes and go through a share of the columns, and a third one adds up the shares.
+// Few columns (16 at most): where a unit's scores fit the shared memory of a cluster of up to eight blocks, one kernel does
+// it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the two kernels, the second one's
+// keys mostly from L2. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile. Measured (20 and 5 heads x 128):
+// one query over 77 tokens 4.7 us, 64 over 87 to 8086 43.9 us (fp32 queries), one over 131007 30.6 us (two kernels).
+//
+// More columns, up to 96 rows (kv4_mass_tc.cu has the others): blocks of 64 whose fragments the first kernel leaves in the
+// workspace; the second kernel's blocks keep their tiles' codes and go through a share of the columns, and a third one adds up
+// the shares. Bound by the products' latency and issue slots (tensor pipe 38% busy): 64 rows of 5 prompts of 1000 to 9000 tokens
+// each 33.7 us.
 #include <type_traits>
 
 #include "kv4_mass.cuh"
@@ -1051,7 +1057,7 @@ int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters) {
   int64_t most = 0;  // whatever the queries' type
   for (int f32 = 0; f32 < 2; ++f32) {
     const int64_t rows = rows_of_plan(c, q_heads / c.kv_heads, voters);
-    if (rows >= kMassTcRows) {
+    if (mass_on_tc(rows, f32 != 0)) {
       const int64_t n = kv4_mass_tc_ws_bytes(c, dim, rows, f32 != 0);
       most = n > most ? n : most;
       continue;
@@ -1065,7 +1071,7 @@ int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters) {
 }
 cudaError_t launch_kv4_mass(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, void* ws, int num_sms, cudaStream_t st) {
   const int64_t rows = rows_of_plan(c, a.share, m.voters);
-  if (rows >= kMassTcRows) return launch_kv4_mass_tc(c, dim, a, m, rows, ws, st);
+  if (mass_on_tc(rows, !a.bf16)) return launch_kv4_mass_tc(c, dim, a, m, rows, ws, st);
   const Plan p = plan_of(c, a.share, m.voters, !a.bf16, 152);
   uint8_t* at = static_cast<uint8_t*>(ws);
   const Stats s{reinterpret_cast<float2*>(at), reinterpret_cast<float*>(at + part_bytes(c, p)), at + part_bytes(c, p) + votes_bytes(c, p)};

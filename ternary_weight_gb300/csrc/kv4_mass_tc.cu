@@ -11,8 +11,9 @@
 // thread adds up its token's votes and a pair of rows' constants comes from shared memory. In both the products of one
 // tile (block) run while the last one's scores are worked off; two blocks an SM cover what is left.
 //
-// Bound by issue slots and shared-memory loads of the scores' arithmetic (about five operations a score in each kernel), then by
-// the exponentials.
+// Bound by the scores' arithmetic (about five operations a score in each kernel; half of the issue slots used), then by the
+// exponentials. Measured (20 and 5 heads x 128): 2048 tokens that all vote 73 us (43 and 35 of them the two kernels; 21 GFLOP in
+// both), the last 64 of 5 prompts of 1000 to 9000 tokens 63.5 us; on m16n8k16 they took 114.5 and 91.
 #include <type_traits>
 
 #include "kv4_mass.cuh"

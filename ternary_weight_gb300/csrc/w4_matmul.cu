@@ -14,6 +14,10 @@
 // weight rows; its warps cut the run's 16 x 128-code pieces into equal parts. A warp loads its pieces straight into the
 // registers that the A fragments are made from, AHEAD pieces before they are used, and writes the tiles that it has whole; the
 // tiles that it shares are added up at the end, in order.
+//
+// Measured, 131072 x 2560: one row 39 us (groups of 128; 174 MB, 4.4 TB/s of the measured 6.8, further rows of weights at 5.4),
+// 44.4 us (groups of 64, zero points), 51.9 us (32); 9 to 16 rows 50 to 51.5 us; 32 rows (bf16) 78 us, bound by issue slots and m16n8k16.
+// 2560 x 6912, one row: 7.4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
