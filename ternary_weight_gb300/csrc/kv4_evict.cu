@@ -1,6 +1,6 @@
 // kv4_evict.cu -- eviction: long sequences keep the tokens that gathered most attention weight.
 //
-// One kernel; a cluster of one to eight blocks for each sequence and head. Its blocks take a run of tokens each and keep
+// One kernel; a cluster of one to sixteen blocks for each sequence and head. Its blocks take a run of tokens each and keep
 // the ranks of their masses (whole numbers in the masses' order) in shared memory. The least rank that is kept is found by
 // three passes that count digits (11, 11 and 10 bits, from the top), added up over the cluster through distributed
 // shared memory; then every warp counts and lists the kept tokens of its run, in order, and the cluster moves them: codes,
@@ -10,7 +10,7 @@
 //
 // Bound by latency where sequences are few: loads that depend on each other (length, page, mass; kept token, page, data) and
 // the cluster's barriers; by issue slots and the moved bytes where they are many. Measured (5 heads x 128, into other pages):
-// 131007 tokens to 4096 33.3 us, to 64 29.9; 16000 to 64 15.2; 48 sequences of 501 to 16001 to 2048 59 us (141 MB), to 64 31;
+// 131007 tokens to 4096 25.2 us, to 64 23.9; 16000 to 64 15.2; 48 sequences of 501 to 16001 to 2048 59 us (141 MB), to 64 31;
 // 300 to 200 9.5 us. Loops are kept short: unrolled ones cost the small cases half as much again, in instruction fetches.
 #include "kv4.cuh"
 #include "smem_limit.h"
@@ -20,7 +20,7 @@ namespace {
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = 2048;
-constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_CLUSTER = 16;
 constexpr int MAX_RANKS = 20480;  // that a block keeps (80 KB, two blocks an SM); longer runs are read again each time
 
 // Masses as whole numbers in the same order; a NaN above all, both zeros alike. Tokens that are kept in any case (the
@@ -331,7 +331,7 @@ int cap_of(const Kv4& c, int budget) { return budget < c.max_kv ? budget : c.max
 template <int D>
 cudaError_t launch(const cudaLaunchConfig_t& cfg, const Kv4& c, const Kv4Evict& e, int32_t* kept, int cluster, int ranks, bool write_len) {
   static std::atomic<uint64_t> configured{0};
-  if (cudaError_t err = allow_smem(configured, kv4_evict_kernel<D>, MAX_RANKS * 4)) return err;
+  if (cudaError_t err = allow_smem(configured, kv4_evict_kernel<D>, MAX_RANKS * 4, true)) return err;
   return cudaLaunchKernelEx(&cfg, kv4_evict_kernel<D>, c, e, kept, cap_of(c, e.budget), cluster, ranks, write_len);
 }
 
@@ -343,7 +343,9 @@ cudaError_t launch_kv4_evict(const Kv4& c, int dim, const Kv4Evict& e, void* ws,
   // blocks of a cluster: as many as two an SM leave room for, each with some thousand tokens (48 sequences of 501 to
   // 16001 tokens x 5 heads to 2048: a block each 59 us, two each, in two waves, 68; to 64: 31 and 39.7)
   int cluster = 1;
-  while (cluster < MAX_CLUSTER && units * cluster * 2 <= num_sms * 2 && c.max_kv > cluster * 1024) cluster *= 2;
+  while (cluster < 8 && units * cluster * 2 <= num_sms * 2 && c.max_kv > cluster * 1024) cluster *= 2;
+  // sixteen: 131007 tokens x 5 heads 25.2 us, eight 33.4; 16000 tokens 17.6 and 15.4
+  if (cluster == 8 && units * MAX_CLUSTER <= num_sms * 2 && c.max_kv > 48 * 1024) cluster = MAX_CLUSTER;
   int64_t per = ((c.max_kv + cluster * WARPS - 1) / (cluster * WARPS) + 31) / 32 * 32;
   const int ranks = (int)(per * WARPS < MAX_RANKS ? per * WARPS : MAX_RANKS);
   const bool over = e.new_len == c.kv_len;

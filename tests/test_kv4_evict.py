@@ -153,6 +153,16 @@ def test_long_sequences(cuda_lib, kind, kv, budget, sinks, recent):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["any", "few values"])
+@pytest.mark.parametrize("heads,kv,budget,sinks,recent", [(2, [50000, 49999, 7], 20000, 4, 256), (5, [60001], 1030, 0, 1000), (1, [330000], 2000, 4, 64)])
+def test_very_long_sequences(cuda_lib, kind, heads, kv, budget, sinks, recent):
+    """Clusters of sixteen blocks; at last runs too long for their blocks' shared memory."""
+    w = Evict([0] * len(kv), kv, heads, 64, seed=budget)
+    w.cache.pages.copy_(torch.tensor(w.rng.integers(0, 256, size=w.cache.pages.numel(), dtype=np.uint8)))
+    w.check(w.masses(kind), budget, budget, sinks, recent)
+
+
+@pytest.mark.gpu
 def test_lengths_in_place_for_the_last_layer(cuda_lib):
     """Layers that share their lengths: each is cut by the old ones, the last call writes the new ones over them."""
     kv, n = [300, 90, 131], 100
