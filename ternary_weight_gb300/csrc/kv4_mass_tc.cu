@@ -11,9 +11,10 @@
 // thread adds up its token's votes and a pair of rows' constants comes from shared memory. In both the products of one
 // tile (block) run while the last one's scores are worked off; two blocks an SM cover what is left.
 //
-// Bound by the scores' arithmetic (about five operations a score in each kernel; half of the issue slots used), then by the
-// exponentials. Measured (20 and 5 heads x 128): 2048 tokens that all vote 73 us (43 and 35 of them the two kernels; 21 GFLOP in
-// both), the last 64 of 5 prompts of 1000 to 9000 tokens 63.5 us; on m16n8k16 they took 114.5 and 91.
+// Bound by issue slots (some 700 instructions for a warp's 64 x 32 scores, 320 of them their arithmetic) and by the latency of a
+// tile, of which a block has up to 16 in turn. Measured (20 and 5 heads x 128): 2048 tokens that all vote 68 us (21 GFLOP in the
+// two passes), 4096 183 us, the last 64 of 5 prompts of 1000 to 9000 tokens 62.5 us; on m16n8k16 the first and last took 114.5
+// and 91.
 #include <type_traits>
 
 #include "kv4_mass.cuh"
@@ -193,6 +194,35 @@ __device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int 
   }
 }
 
+// Goes through steps (tiles, blocks) that have anything to do. What 32 of them see is found by the 32 lanes at once: asked
+// again for each step it cost 3 to 7% of the time (2048 voting tokens 72 us, 4096 201; so 69.7 and 187). All lanes hold the same.
+struct Walk {
+  int first = 0, end = 0;  // the steps that `any` and `all` tell of
+  uint32_t any = 0, all = 0;
+  // the next step from k on, `last` if there is none; sees(k): 0 nothing, 1 some, 2 all
+  template <class Sees>
+  __device__ __forceinline__ int next(int k, int last, bool* whole, Sees sees) {
+    while (k < last) {
+      if (k >= end) {
+        const int at = k + (int)(threadIdx.x % 32), v = at < last ? sees(at) : 0;
+        first = k, end = k + 32;
+        any = __ballot_sync(0xffffffffu, v > 0), all = __ballot_sync(0xffffffffu, v == 2);
+      }
+      const uint32_t left = any >> (k - first);
+      if (left) {
+        k += __ffs(left) - 1;
+        *whole = all >> (k - first) & 1;
+        return k;
+      }
+      k = end;
+    }
+    return last;
+  }
+};
+
+// The lowest n bits.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+
 // The first and last position of a block's rows.
 __device__ __forceinline__ void ends_of(const Kv4Attn& a, const Rows& r, int row0, int* first, int* last) {
   *first = r.position(row0 / a.share);
@@ -239,11 +269,10 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
     const int t0 = chunk * pl.chunk, t1 = min(t0 + pl.chunk, (r.s.len + TOK - 1) / TOK), pages = (r.s.len + kKvPage - 1) / kKvPage;
     int first, last;
     ends_of(a, r, row0, &first, &last);
-    const auto next = [&](int t) {
-      while (t < t1 && seen(a, first, last, t * TOK, TOK) == 0) ++t;
-      return t;
-    };
-    int t = next(t0);
+    Walk walk;
+    const auto next = [&](int t, bool* whole) { return walk.next(t, t1, whole, [&](int k) { return seen(a, first, last, k * TOK, TOK); }); };
+    bool t_whole = false, then_whole = false, after_whole = false, before_whole = false;
+    int t = next(t0, &t_whole);
     if (t >= t1 && chunk) {
       for (int i = threadIdx.x; i < ROWS; i += THREADS) part[item * ROWS + i] = make_float2(kNegInf, 0.0f);
       continue;
@@ -262,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
     };
     Half<D> codes;
     codes.load(c, checked(page_id(t)), r.h, krow & 63, khalf);
-    int then = t < t1 ? next(t + 1) : t1, id_then = page_id(then);
+    int then = t < t1 ? next(t + 1, &then_whole) : t1, id_then = page_id(then);
     load_block<D, F32>(a, r, row0, base, con);
     __syncthreads();
     const float4 ab4 = con.ab[row >> 1];
@@ -291,12 +320,12 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
         __syncwarp();
       }
       if (then < t1) codes.load(c, checked(id_then), r.h, krow & 63, khalf);
-      const int after = then < t1 ? next(then + 1) : t1, id_after = page_id(after);
+      const int after = then < t1 ? next(then + 1, &after_whole) : t1, id_after = page_id(after);
       if (before >= 0) {
         const uint32_t was = issued - 1, at = was & 1;
         mbar_wait_warp(&done[at], (was >> 1) & 1, &abort);
         tc_fence_after();
-        const int j0 = before * TOK + half * 64, sees = seen(a, first, last, before * TOK, TOK);
+        const int j0 = before * TOK + half * 64;
         const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + at * 128 + half * 64;
         const float4* tab = reinterpret_cast<const float4*>(smem + TABLE + (was % 3) * 1024) + half * 32;
         const auto work = [&](auto masked) {
@@ -305,6 +334,9 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
           for (int k = 0; k < 2; ++k) {
             uint32_t s[32];
             tmem_ld_32x32b_x32(ts + k * 32, s);
+            // which of the 32 tokens the row sees, in the order of their positions
+            const int j = j0 + k * 32;
+            const uint32_t sees = MASKED ? below(p + 1 - j) & (~below(lo - j) | below(a.sinks - j)) : 0;
             tmem_ld_wait();
             uint64_t u[16];
 #pragma unroll
@@ -313,8 +345,8 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
               u[i] = fma2(f2pack(sb.x, sb.y), f2pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2(f2pack(sb.z, sb.w), b2));
               if (MASKED) {
                 float2 v = f2unpack(u[i]);
-                if (!visible(a, p, lo, j0 + k * 32 + token_of(2 * i))) v.x = kNegInf;
-                if (!visible(a, p, lo, j0 + k * 32 + token_of(2 * i + 1))) v.y = kNegInf;
+                if (!(sees & 1u << token_of(2 * i))) v.x = kNegInf;
+                if (!(sees & 1u << token_of(2 * i + 1))) v.y = kNegInf;
                 u[i] = f2pack(v.x, v.y);
               }
             }
@@ -337,12 +369,12 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
             m = now;
           }
         };
-        if (sees == 2) work(std::false_type{});
+        if (before_whole) work(std::false_type{});
         else work(std::true_type{});
       }
       before = -1;
-      if (t < t1) before = t, ++issued;
-      t = then, then = after, id_then = id_after;
+      if (t < t1) before = t, before_whole = t_whole, ++issued;
+      t = then, t_whole = then_whole, then = after, then_whole = after_whole, id_then = id_after;
     }
     if (half) halves[row] = make_float2(m, l);
     __syncthreads();
@@ -437,18 +469,20 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
     const int rows = r.votes * a.share, pages = (r.s.len + kKvPage - 1) / kKvPage;
     if (rows == 0 || tile * TOK >= r.s.len) continue;
     const int n_blocks = (rows + ROWS - 1) / ROWS;
-    const auto next = [&](int block) {  // of this share, from `block` on, that sees any of the tokens
-      for (; block < n_blocks; block += pl.shares) {
+    // the share's k-th block is share + k pl.shares
+    const int steps = n_blocks > share ? (n_blocks - share + pl.shares - 1) / pl.shares : 0;
+    Walk walk;
+    const auto next = [&](int k, bool* whole) {
+      return walk.next(k, steps, whole, [&](int i) {
         int first, last;
-        ends_of(a, r, block * ROWS, &first, &last);
-        if (seen(a, first, last, tile * TOK, TOK)) break;
-      }
-      return block;
+        ends_of(a, r, (share + i * pl.shares) * ROWS, &first, &last);
+        return seen(a, first, last, tile * TOK, TOK);
+      });
     };
     // a block's copy: its queries to buffer copied & 1, its constants to place copied % 3
-    const auto copy = [&](int block) {
+    const auto copy = [&](int k) {
       if (threadIdx.x == 0) {
-        const uint8_t* from = blocks + ((int64_t)unit * pl.blocks + block) * (int64_t)S::BLOCK;
+        const uint8_t* from = blocks + ((int64_t)unit * pl.blocks + share + k * pl.shares) * (int64_t)S::BLOCK;
         uint64_t* bar = &full[copied & 1];
         mbar_arrive_expect_tx(bar, S::BLOCK);
         bulk_copy_g2s(smem + QUERIES + (copied & 1) * S::IMAGE * S::PARTS, from, S::IMAGE * S::PARTS, bar);
@@ -464,8 +498,9 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
       bad = true;
       return -1;
     };
-    int block = next(share);
-    if (block < n_blocks) copy(block);
+    bool k_whole = false, then_whole = false, before_whole = false;
+    int k = next(0, &k_whole);
+    if (k < steps) copy(k);
     const int krow = threadIdx.x >> 1, khalf = threadIdx.x & 1;
     Half<D> codes;
     codes.load(c, page_of(krow), r.h, krow & 63, khalf);
@@ -476,14 +511,18 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
     if (mine >= 0) sb = params(*reinterpret_cast<const uint32_t*>(c.pages + ((int64_t)mine * c.kv_heads + r.h) * kv4_block_bytes(D) + kKvPage * D + (row & 63) * 8));
     const uint64_t step2 = f2pack(sb.x, sb.x), base2 = f2pack(sb.y, sb.y);
     const int in = (row & 64) + token_of(row & 63), j = tile * TOK + in;  // this thread's token
+    // the rows that see it: from row_from on, before row_to
+    const int64_t p0 = r.position(0), last = j < a.sinks ? r.s.len : (int64_t)j + a.window;
+    const int row_from = (int)min(max(j - p0, (int64_t)0), (int64_t)r.votes) * a.share;
+    const int row_to = (int)min(max(last - p0, (int64_t)0), (int64_t)r.votes) * a.share;
     uint64_t votes[2] = {0, 0};
     int before = -1;
-    while (block < n_blocks || before >= 0) {
+    while (k < steps || before >= 0) {
       tc_fence_before();
       __syncthreads();
       tc_fence_after();
       const uint32_t buf = issued & 1;
-      if (block < n_blocks) {
+      if (k < steps) {
         mbar_wait_warp(&full[buf], (issued >> 1) & 1, &abort);
         if (warp == 0) {
           if (elect_one()) issue<D, 1, S::PARTS>(tmem + buf * 128, base, base + QUERIES + buf * S::IMAGE * S::PARTS, &done[buf]);
@@ -496,43 +535,41 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
         tc_fence_after();
       }
       // the buffer of the last products is free now
-      const int then = block < n_blocks ? next(block + pl.shares) : n_blocks;
-      if (then < n_blocks) copy(then);
+      const int then = k < steps ? next(k + 1, &then_whole) : steps;
+      if (then < steps) copy(then);
       if (before >= 0) {
-        int first, last;
-        ends_of(a, r, before * ROWS, &first, &last);
-        const int sees = seen(a, first, last, tile * TOK, TOK), left = rows - before * ROWS - half * 64;
+        const int row0 = (share + before * pl.shares) * ROWS + half * 64, left = rows - row0;
         const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (was & 1) * 128 + half * 64;
         const Constants& con = *reinterpret_cast<const Constants*>(smem + CONS + (was % 3) * S::CON);
         const auto work = [&](auto masked) {
           constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll 1
-          for (int k = 0; k < 2 && k * 32 < left; ++k) {
+          for (int q = 0; q < 2 && q * 32 < left; ++q) {
             uint32_t s[32];
-            tmem_ld_32x32b_x32(ts + k * 32, s);
+            tmem_ld_32x32b_x32(ts + q * 32, s);
+            const uint32_t sees = MASKED ? below(row_to - row0 - q * 32) & ~below(row_from - row0 - q * 32) : 0;
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float4 ab = con.ab[half * 32 + k * 16 + i], ml = con.ml[half * 32 + k * 16 + i];
+              const float4 ab = con.ab[half * 32 + q * 16 + i], ml = con.ml[half * 32 + q * 16 + i];
               const uint64_t u = fma2(step2, f2pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2(base2, f2pack(ab.z, ab.w)));
               const float2 y = f2unpack(mul2(f2pack(ab.x, ab.y), add2(u, f2pack(ml.x, ml.y))));
               const uint64_t more = fma2(f2pack(exp2_approx(y.x), exp2_approx(y.y)), f2pack(ml.z, ml.w), votes[i & 1]);
               if (MASKED) {
                 const float2 v = f2unpack(votes[i & 1]), w = f2unpack(more);
-                const int4 p = *reinterpret_cast<const int4*>(&con.seen[half * 64 + k * 32 + 2 * i]);
-                votes[i & 1] = f2pack(visible(a, p.x, p.y, j) ? w.x : v.x, visible(a, p.z, p.w, j) ? w.y : v.y);
+                votes[i & 1] = f2pack(sees & 1u << 2 * i ? w.x : v.x, sees & 2u << 2 * i ? w.y : v.y);
               } else {
                 votes[i & 1] = more;
               }
             }
           }
         };
-        if (sees == 2) work(std::false_type{});
+        if (before_whole) work(std::false_type{});
         else work(std::true_type{});
       }
       before = -1;
-      if (block < n_blocks) before = block, ++issued;
-      block = then;
+      if (k < steps) before = k, before_whole = k_whole, ++issued;
+      k = then, k_whole = then_whole;
     }
     const float2 v = f2unpack(add2(votes[0], votes[1]));
     if (half) halves[row] = v.x + v.y;
