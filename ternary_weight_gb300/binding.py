@@ -888,6 +888,8 @@ def w4_quant_weight(w, group=128, with_zeros=False, codes=None, scales=None, zer
     scales = _kv4_empty(torch, groups, torch.float16, w.device, stream) if scales is None else scales
     if with_zeros and zeros is None:
         zeros = _kv4_empty(torch, groups, torch.uint8, w.device, stream)
+    if tuple(scales.shape) != groups:
+        raise ValueError("scales must be N x K/group float16")
     on = (_on_device or _on_device_setup())[2](_w4_check(w, codes, scales, zeros, None)[5], stream)
     _check(lib().bitnet_w4_quant_weight(_ptr(w), dt, N, K, group, _ptr(codes), _ptr(scales), _ptr(zeros), on), "bitnet_w4_quant_weight")
     return codes, scales, zeros
