@@ -589,7 +589,7 @@ typedef struct bitnet_rope_table {
  *   head_dim  : a multiple of 8, 8 .. 1024; rows 0 .. 2^31 - 1; q_heads 1 .. 2^17, kv_heads 0 .. 2^17
  *   All 16-byte aligned (positions 4), strides >= heads * head_dim, at most 2^26, multiples of 16 bytes.
  * Angles are exact to 2^-24 half turns at any position; the turn is computed in fp32 (each product and
- * sum one rounding) and rounded once to dtype. Infinities and NaN spread to the pair that they are in.
+ * sum rounded once at most) and rounded once to dtype. Infinities and NaN spread to the pair that they are in.
  */
 BITNET_API int bitnet_rope(const bitnet_rope_table *table, const int32_t *positions, int64_t rows, const void *q,
                            int64_t q_heads, int64_t q_stride, void *q_out, int64_t q_out_stride, const void *k,

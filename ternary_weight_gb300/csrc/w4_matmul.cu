@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) w4_matmul_kernel(Call c
   constexpr int PER = 128 / G, WARPS = Shape<NT>::WARPS, AHEAD = Shape<NT>::AHEAD;
   const int K = c.w.K, N = c.w.N, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // known to be the same for all lanes
-  const int tiles = (N + ROWS - 1) / ROWS, blocks = K / 128, groups = K / G;
+  const int tiles = (N - 1) / ROWS + 1, blocks = K / 128, groups = K / G;
   const int tile0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), tile1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
   const int64_t all = (int64_t)(tile1 - tile0) * blocks;
   const int64_t p0 = all * warp / WARPS, p1 = all * (warp + 1) / WARPS;  // this warp's pieces
@@ -410,7 +410,7 @@ cudaError_t launch(const Call& c, int num_sms, cudaStream_t st) {
   auto kernel = w4_matmul_kernel<G, ZEROS, NT>;
   static std::atomic<uint64_t> configured{0};
   if (cudaError_t e = allow_smem(configured, kernel, MAX_SMEM - 1024)) return e;
-  const int tiles = (c.w.N + ROWS - 1) / ROWS;
+  const int tiles = (c.w.N - 1) / ROWS + 1;
   kernel<<<min(tiles, num_sms), Shape<NT>::THREADS, smem, st>>>(c);
   return cudaGetLastError();
 }

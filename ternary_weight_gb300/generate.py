@@ -46,8 +46,8 @@ class Decoder:
     """Layers of attention blocks over one batch of sequences that may grow to `longest` tokens each.
 
     ``rope`` (``binding.Rope``): rotary positions. ``budget``: a sequence that has more than budget + budget / 8 tokens
-    cached is cut back to budget, by the attention weight that its tokens gathered (the last 64 of a prompt vote); its first
-    4 and last budget / 4 tokens stay, and pages are held for that many tokens only (or the prompt's, if it is longer).
+    cached is cut back to budget, by the attention weight that its tokens gathered (the last 64 of a prompt vote); its last
+    budget / 4 tokens and first 4 stay, and pages are held for that many tokens only (or the prompt's, if it is longer).
     ``vocab``: a 4-bit head of that many rows; `logits` and `tokens` hold what the last step gave."""
 
     VOTERS = 64
@@ -88,7 +88,7 @@ class Decoder:
             x = block.run(x, batch, positions=positions if self.rope is not None else None)
         if self.budget:  # the layers share their lengths: the last one writes the new ones
             for block in self.blocks:
-                block.evict(batch, self.budget, self.limit, sinks=min(4, self.budget), recent=self.budget // 4,
+                block.evict(batch, self.budget, self.limit, sinks=min(4, self.budget - self.budget // 4), recent=self.budget // 4,
                             new_len=self.kv_len if block is self.blocks[-1] else None)
         return x
 

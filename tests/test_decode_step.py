@@ -100,6 +100,15 @@ def test_captured_steps_are_the_eager_ones(cuda_lib, prompts, budget, steps):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("budget", [1, 2, 3, 4, 5, 7, 8])
+def test_small_budgets(cuda_lib, budget):
+    d = generate.Decoder(1, 256, 4, 2, 64, [9, 1], 20, seed=4, budget=budget)
+    d.prompt(torch.from_numpy(workloads.activations_f32(10, 256, seed=3)).cuda())
+    for _ in range(11):
+        assert bool(d.step().isfinite().all()) and all(n <= budget + budget // 8 for n in d.kv_len.tolist())
+
+
+@pytest.mark.gpu
 def test_without_eviction_the_weight_changes_nothing(cuda_lib):
     """A budget that is never reached: the same steps as without."""
     x = torch.from_numpy(workloads.activations_f32(70, 256, seed=3)).cuda()
