@@ -608,6 +608,9 @@ BITNET_API int bitnet_kv4_attention_mass(const bitnet_kv4_cache* cache, const bi
   if (!valid_mass_rows(c, q_heads)) return BITNET_EINVAL;
   const int64_t need = kv4_mass_ws_bytes(c, cache->head_dim, (int)q_heads, voters_of(voters));
   if (need > 0 && (!workspace || workspace_bytes < need)) return BITNET_EINVAL;
+  const uintptr_t from = reinterpret_cast<uintptr_t>(mass), to = reinterpret_cast<uintptr_t>(mass_out);
+  const uintptr_t bytes = (uintptr_t)bitnet_kv4_mass_bytes(c.n_pages, c.kv_heads);
+  if (from != to && from < to + bytes && to < from + bytes) return BITNET_EINVAL;  // they overlap
   if (!aligned(mass, 16) || !aligned(mass_out, 16) || (workspace && !aligned(workspace, 256))) return BITNET_EALIGN;
   if (c.total_q == 0) return BITNET_OK;
   int sms = 0;
