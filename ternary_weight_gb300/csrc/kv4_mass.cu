@@ -17,7 +17,8 @@
 // Few columns (16 at most): where a unit's scores fit the shared memory of a cluster of up to eight blocks, one kernel does
 // it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the two kernels, the second one's
 // keys mostly from L2. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile. Measured (20 and 5 heads x 128):
-// one query over 77 tokens 4.7 us, 64 over 87 to 8086 43.9 us (fp32 queries), one over 131007 30.6 us (two kernels).
+// one query over 77 tokens 4.7 us, 64 over 87 to 8086 43.9 us (fp32 queries), one over 131007 27.9 us (two kernels; 30.5 where the second one
+// is not launched until the first has ended).
 //
 // More columns, up to 96 rows (kv4_mass_tc.cu has the others): blocks of 64 whose fragments the first kernel leaves in the
 // workspace; the second kernel's blocks keep their tiles' codes and go through a share of the columns, and a third one adds up
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
   constexpr int COLS = NT * 8, PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   bool bad = false;
+  pdl_launch_dependents();
   const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks * pl.chunks;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t rest = item / pl.chunks;
@@ -353,11 +355,6 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_votes(Kv4 c
       id = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
       if (id < 0 || id >= c.n_pages) bad = true, id = -1;
     }
-    load_columns<D, NT, F32>(a, r, 0, sh);
-    __syncthreads();
-    load_sums<D, NT, F32>(pl, st, unit, 0, (all + pl.chunk - 1) / pl.chunk, sh);
-    __syncthreads();
-    const int eights = min(NT, (rows * PARTS + 7) / 8), first = r.position(0), last = r.position(r.votes - 1), old = r.s.len - r.s.n;
     Codes<D> cur;
     const auto load = [&](int k) {
       const int from = __shfl_sync(0xffffffffu, id, k);
@@ -365,6 +362,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_votes(Kv4 c
       if (tile < tile1 && from >= 0) cur.load(c.pages + ((int64_t)from * c.kv_heads + r.h) * BLK, tile, g, t);
     };
     load(0);
+    load_columns<D, NT, F32>(a, r, 0, sh);
+    __syncthreads();
+    pdl_wait();
+    load_sums<D, NT, F32>(pl, st, unit, 0, (all + pl.chunk - 1) / pl.chunk, sh);
+    __syncthreads();
+    const int eights = min(NT, (rows * PARTS + 7) / 8), first = r.position(0), last = r.position(r.votes - 1), old = r.s.len - r.s.n;
     for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
       const Codes<D> now = cur;
       const int from = __shfl_sync(0xffffffffu, id, k);
@@ -382,6 +385,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_votes(Kv4 c
     }
     __syncthreads();
   }
+  pdl_wait();
   if (bad) record_device_error(kErrRange);
 }
 
@@ -691,6 +695,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_rows_many(Kv4 c, Kv4Attn 
   constexpr int PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D), HALVES = F32 ? 1 : 2;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   bool bad = false;
+  pdl_launch_dependents();
   const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks * pl.chunks;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t rest = item / pl.chunks;
@@ -803,6 +808,8 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_rows_many(Kv4 c, Kv4Attn 
 template <int D>
 __global__ void __launch_bounds__(COLS) kv4_mass_sums(Kv4 c, Kv4Attn a, int voters, Plan pl, Stats st) {
   const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks;
+  pdl_launch_dependents();
+  pdl_wait();
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int unit = (int)(item / pl.blocks), block = (int)(item - (int64_t)unit * pl.blocks);
     bool bad = false;
@@ -829,6 +836,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
   constexpr int PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D), PIECES = (int)(sizeof(Slab<D>) / 16);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   bool bad = false;
+  pdl_launch_dependents();
   // the groups of tiles outermost: with a causal mask the first ones have most to do
   const int units = c.batch * c.kv_heads;
   const int64_t items = (int64_t)units * pl.groups * pl.shares;
@@ -863,7 +871,6 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int block = next(share), buf = 0;
-    copy(block, 0);
     Tile<D> k{};
     bool there = tile < all;
     if (there) {
@@ -871,6 +878,8 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
       if (id < 0 || id >= c.n_pages) bad = true, there = false;
       else k.load(c.pages + ((int64_t)id * c.kv_heads + r.h) * BLK, tile, g, t);
     }
+    pdl_wait();
+    copy(block, 0);
     const Unpacked<D> now(k);
     uint64_t votes[4] = {0, 0, 0, 0};  // of tokens 2 t and 2 t + 1 of the eights
     while (block < blocks) {
@@ -928,11 +937,13 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
     st.votes[((((int64_t)unit * pl.groups + group) * pl.shares + share) * WARPS + warp) * TILE + token_at(g >> 1, t, g & 1)] = mine;
     __syncthreads();
   }
+  pdl_wait();
   if (bad) record_device_error(kErrRange);
 }
 
 __global__ void __launch_bounds__(THREADS) kv4_mass_join(Kv4 c, Kv4Mass ms, Plan pl, Stats st) {
   const int64_t items = (int64_t)c.batch * c.kv_heads * pl.groups;
+  pdl_wait();
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int unit = (int)(item / pl.groups), group = (int)(item - (int64_t)unit * pl.groups);
     bool bad = false;
@@ -1022,8 +1033,7 @@ cudaError_t launch_few(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const P
   const int64_t units = (int64_t)c.batch * c.kv_heads;
   kv4_mass_rows<D, NT, F32><<<grid_of(units * p.chunks), THREADS, 0, st>>>(c, a, m.voters, p, s);
   if (cudaError_t e = cudaGetLastError()) return e;
-  kv4_mass_votes<D, NT, F32><<<grid_of(units * p.chunks), THREADS, 0, st>>>(c, a, m, p, s);
-  return cudaGetLastError();
+  return launch_behind(kv4_mass_votes<D, NT, F32>, grid_of(units * p.chunks), THREADS, 0, st, c, a, m, p, s);
 }
 template <int D, bool F32>
 cudaError_t launch_many(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
@@ -1034,14 +1044,10 @@ cudaError_t launch_many(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const 
   if (cudaError_t e = allow_smem(configured[1], kv4_mass_shares<D, F32>, shares_smem)) return e;
   kv4_mass_rows_many<D, F32><<<grid_of(units * p.blocks * p.chunks), THREADS, rows_smem, st>>>(c, a, m.voters, p, s);
   if (cudaError_t e = cudaGetLastError()) return e;
-  if (p.chunks > 1) {
-    kv4_mass_sums<D><<<grid_of(units * p.blocks), COLS, 0, st>>>(c, a, m.voters, p, s);
-    if (cudaError_t e = cudaGetLastError()) return e;
-  }
-  kv4_mass_shares<D, F32><<<grid_of(units * p.groups * p.shares), THREADS, shares_smem, st>>>(c, a, m, p, s);
-  if (cudaError_t e = cudaGetLastError()) return e;
-  kv4_mass_join<<<grid_of(units * p.groups), THREADS, 0, st>>>(c, m, p, s);
-  return cudaGetLastError();
+  if (p.chunks > 1)
+    if (cudaError_t e = launch_behind(kv4_mass_sums<D>, grid_of(units * p.blocks), COLS, 0, st, c, a, m.voters, p, s)) return e;
+  if (cudaError_t e = launch_behind(kv4_mass_shares<D, F32>, grid_of(units * p.groups * p.shares), THREADS, shares_smem, st, c, a, m, p, s)) return e;
+  return launch_behind(kv4_mass_join, grid_of(units * p.groups), THREADS, 0, st, c, m, p, s);
 }
 template <int D, bool F32>
 cudaError_t by_columns(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {

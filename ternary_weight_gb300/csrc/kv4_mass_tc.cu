@@ -12,8 +12,8 @@
 // tile (block) run while the last one's scores are worked off; two blocks an SM cover what is left.
 //
 // Bound by issue slots (some 700 instructions for a warp's 64 x 32 scores, 320 of them their arithmetic) and by the latency of a
-// tile, of which a block has up to 16 in turn. Measured (20 and 5 heads x 128): 2048 tokens that all vote 68 us (21 GFLOP in the
-// two passes), 4096 183 us, the last 64 of 5 prompts of 1000 to 9000 tokens 62.5 us; on m16n8k16 the first and last took 114.5
+// tile, of which a block has up to 16 in turn. Measured (20 and 5 heads x 128): 2048 tokens that all vote 66.2 us (21 GFLOP in the
+// two passes), 4096 180 us, the last 64 of 5 prompts of 1000 to 9000 tokens 60.8 us; on m16n8k16 the first and last took 114.5
 // and 91.
 #include <type_traits>
 
@@ -122,16 +122,19 @@ __device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int 
   const bool high = n >= 4;
   const int word0 = 8 * w % W + (high ? 4 : 0);  // of the four words that the lane stores
   const float odd = n & 1 ? 0.0625f : 1.0f;
+  // voting row and head of row row0 + k: x / share for x < 256 and share <= 128 by a product
+  const int first = row0 / a.share, rest = row0 - first * a.share, by = 65536 / a.share + 1;
+  const int64_t from = (int64_t)(r.s.q0 + r.s.n - r.votes + first) * a.q_stride + (int64_t)r.h * a.share * D + 8 * w;
 #pragma unroll 1
   for (int k0 = threadIdx.x / W; k0 < ROWS; k0 += PER * BATCH) {
     float x[BATCH][8];
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
-      const int row = row0 + k0 + k * PER, i = row / a.share;
+      const int in = k0 + k * PER, i = (rest + in) * by >> 16;
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[k][j] = 0.0f;
-      if (row >= rows) continue;
-      const int64_t at = (int64_t)(r.s.q0 + r.s.n - r.votes + i) * a.q_stride + (int64_t)(r.h * a.share + row - i * a.share) * D + 8 * w;
+      if (row0 + in >= rows) continue;
+      const int64_t at = from + i * a.q_stride + (rest + in - i * a.share) * D;
       if (F32) {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
         const float4 u = __ldg(p), v = __ldg(p + 1);
@@ -145,7 +148,7 @@ __device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int 
     }
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
-      const int in = k0 + k * PER, row = row0 + in;
+      const int in = k0 + k * PER;
       float sum = ((x[k][0] + x[k][1]) + (x[k][2] + x[k][3])) + ((x[k][4] + x[k][5]) + (x[k][6] + x[k][7]));
       uint32_t top = 0;
 #pragma unroll
@@ -180,17 +183,24 @@ __device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int 
           st_shared_u32(to + chunk_at(in, word0 + 2 * j + 1), __byte_perm(lo, hi, 0x7632));
         }
       }
-      if (w == 0) {
-        const float c1 = __fmul_rn(fabsf(a.scale), kLog2e);
-        const int f = 24 - e, half = f / 2;
-        const float ca = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
+      if (w == 0) {  // the row's constants begin with these
         float* ab = reinterpret_cast<float*>(&con.ab[in >> 1]) + (in & 1);
-        ab[0] = fminf(fmaxf(ca, kLeastA), kMostA);
-        ab[2] = __fmul_rn(__fmul_rn(sum, up), 5.9604644775390625e-8f);  // 2^-24
-        const int p = row < rows ? r.position(row / a.share) : -1;
-        con.seen[in] = make_int2(p, window_from(a, p));
+        ab[0] = __int_as_float(e);
+        ab[2] = __fmul_rn(sum, up);
       }
     }
+  }
+  __syncthreads();
+  if (threadIdx.x < ROWS) {
+    const int in = threadIdx.x;
+    float* ab = reinterpret_cast<float*>(&con.ab[in >> 1]) + (in & 1);
+    const float c1 = __fmul_rn(fabsf(a.scale), kLog2e);
+    const int f = 24 - __float_as_int(ab[0]), half = f / 2;
+    const float ca = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
+    ab[0] = fminf(fmaxf(ca, kLeastA), kMostA);
+    ab[2] = __fmul_rn(ab[2], 5.9604644775390625e-8f);  // 2^-24
+    const int p = row0 + in < rows ? r.position(first + ((rest + in) * by >> 16)) : -1;
+    con.seen[in] = make_int2(p, window_from(a, p));
   }
 }
 
@@ -253,6 +263,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  pdl_launch_dependents();  // not before: the next kernel's blocks take tensor memory and then wait for all of these
   bool bad = false, abort = false;
   uint32_t issued = 0;  // products so far: buffer issued & 1
   // the last blocks of rows outermost: with a causal mask they have most to do
@@ -413,6 +424,8 @@ template <int D, bool F32>
 __global__ void __launch_bounds__(ROWS) kv4_mass_tc_sums(Kv4 c, Kv4Attn a, int voters, Plan pl, uint8_t* blocks, const float2* part) {
   using S = Shape<D, F32>;
   const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks;
+  pdl_launch_dependents();
+  pdl_wait();
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int unit = (int)(item / pl.blocks), block = (int)(item - (int64_t)unit * pl.blocks), row = threadIdx.x;
     bool bad = false;
@@ -444,6 +457,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
   uint8_t* const smem = smem_raw + (base - raw);
   constexpr int QUERIES = S::IMAGE, CONS = QUERIES + 2 * S::IMAGE * S::PARTS;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, half = warp >> 2, row = (warp & 3) * 32 + lane;
+  if (pl.shares > 1) pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) mbar_init(&full[i], 1), mbar_init(&done[i], 1);
     mbar_init(&all_done, 1);
@@ -500,10 +514,11 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
     };
     bool k_whole = false, then_whole = false, before_whole = false;
     int k = next(0, &k_whole);
-    if (k < steps) copy(k);
     const int krow = threadIdx.x >> 1, khalf = threadIdx.x & 1;
     Half<D> codes;
     codes.load(c, page_of(krow), r.h, krow & 63, khalf);
+    pdl_wait();
+    if (k < steps) copy(k);
     codes.store(base, krow, khalf);
     fence_proxy_async_smem();
     const int mine = page_of(row);
@@ -587,6 +602,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
     }
     __syncthreads();  // the next item's codes
   }
+  pdl_wait();
   if (warp == 0) {
     if (elect_one()) mma_commit(&all_done);
     __syncwarp();
@@ -602,6 +618,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
 
 // Adds up the shares' votes.
 __global__ void __launch_bounds__(TOK) kv4_mass_tc_join(Kv4 c, Kv4Mass ms, Plan pl, const float* shares) {
+  pdl_wait();
   const int64_t items = (int64_t)c.batch * c.kv_heads * pl.tiles;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int unit = (int)(item / pl.tiles), tile = (int)(item - (int64_t)unit * pl.tiles), j = tile * TOK + threadIdx.x;
@@ -655,14 +672,12 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan&
   if (cudaError_t e = allow_smem(configured[1], kv4_mass_tc_votes<D, F32>, S::VOTES_SMEM)) return e;
   kv4_mass_tc_rows<D, F32><<<grid_of(units * p.blocks * p.chunks, 1 << 20), THREADS, S::ROWS_SMEM, st>>>(c, a, m.voters, p, blocks, part);
   if (cudaError_t e = cudaGetLastError()) return e;
-  if (p.chunks > 1) {
-    kv4_mass_tc_sums<D, F32><<<grid_of(units * p.blocks, 1 << 20), ROWS, 0, st>>>(c, a, m.voters, p, blocks, part);
-    if (cudaError_t e = cudaGetLastError()) return e;
-  }
-  kv4_mass_tc_votes<D, F32><<<grid_of(units * p.tiles * p.shares, 1 << 20), THREADS, S::VOTES_SMEM, st>>>(c, a, m, p, blocks, shares);
-  if (cudaError_t e = cudaGetLastError()) return e;
-  if (p.shares > 1) kv4_mass_tc_join<<<grid_of(units * p.tiles, 1 << 20), TOK, 0, st>>>(c, m, p, shares);
-  return cudaGetLastError();
+  if (p.chunks > 1)
+    if (cudaError_t e = launch_behind(kv4_mass_tc_sums<D, F32>, grid_of(units * p.blocks, 1 << 20), ROWS, 0, st, c, a, m.voters, p, blocks, part)) return e;
+  if (cudaError_t e = launch_behind(kv4_mass_tc_votes<D, F32>, grid_of(units * p.tiles * p.shares, 1 << 20), THREADS, S::VOTES_SMEM, st, c, a, m, p, blocks,
+                                    shares))
+    return e;
+  return p.shares > 1 ? launch_behind(kv4_mass_tc_join, grid_of(units * p.tiles, 1 << 20), TOK, 0, st, c, m, p, shares) : cudaSuccess;
 }
 
 }  // namespace
