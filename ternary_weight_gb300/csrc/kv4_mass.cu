@@ -4,10 +4,11 @@
 // queries: two columns each, the parts of their 22 bits). A tile is 32 tokens of one head; a block of columns
 // against a tile is m16n8k16 with the codes as the A operand:
 //   raw[t][r] = sum_d code[t][d] q'[r][d],   x = scale log2 e (step raw / up + base sum(q))
-// The weight of a token needs its row's maximum M and sum L over all tokens first, so the keys are read twice: the
-// first kernel finds (M, L) of each column over each chunk of tiles, the second joins them and adds up
+// The weight of a token needs its row's maximum M and sum L over all tokens first: the first kernel finds (M, L) of
+// each column over each chunk of tiles, the second joins them and adds up
 //   votes[t] = sum_r 2^(x - M) / L
-// The scores of both come from the same instructions, so that each row's votes add up to 1 however large they are.
+// The scores of both are the same bits (kept, or made by the same instructions), so that each row's votes add up to 1 however
+// large they are.
 // There are no atomics: results do not depend on timing.
 //
 // A code enters as the fp16 subnormal c 2^-24 (its nibble masked out of the word) or c 2^-20 (the nibble above, not
@@ -15,10 +16,10 @@
 // bytes of a key row (8 with D = 64), so a warp's loads of a tile are contiguous, straight from the cache.
 //
 // Few columns (16 at most): where a unit's scores fit the shared memory of a cluster of up to eight blocks, one kernel does
-// it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the two kernels, the second one's
-// keys mostly from L2. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile. Measured (20 and 5 heads x 128):
-// one query over 77 tokens 4.7 us, 64 over 87 to 8086 43.9 us (fp32 queries), one over 131007 27.9 us (two kernels; 30.5 where the second one
-// is not launched until the first has ended).
+// it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the first kernel leaves the scores
+// in the workspace and the second starts behind it. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile.
+// Measured (20 and 5 heads x 128): one query over 77 tokens 4.7 us, 64 over 87 to 8086 43.9 us (fp32 queries), one over 131007
+// 19.9 us (27.9 where the second kernel reads the keys again).
 //
 // More columns, up to 96 rows (kv4_mass_tc.cu has the others): blocks of 64 whose fragments the first kernel leaves in the
 // workspace; the second kernel's blocks keep their tiles' codes and go through a share of the columns, and a third one adds up
@@ -50,6 +51,7 @@ struct Stats {
   float2* part;  // unit, block, chunk, column: (M, L)
   float* votes;  // unit, group, share, WARPS x TILE
   uint8_t* slabs;  // unit, block
+  float* scores;   // few columns: unit, row, token
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -68,7 +70,6 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint4 a, uint32_t b0, u
 struct Column {
   float a, b;  // x = step (a raw) + base b
   int p;       // the row's position
-  float m, l;  // the row's maximum and the inverse of its sum (second kernel)
 };
 template <int D, int NT>
 struct __align__(16) Shared {
@@ -130,7 +131,6 @@ __device__ __forceinline__ void load_columns(const Kv4Attn& a, const Rows& r, in
       c.a = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
       c.b = __fmul_rn(c1, sum);
       c.p = there ? r.position(i) : -1;
-      c.m = c.l = 0.0f;
       sh.col[col] = c;
       if (F32) sh.col[col + 1] = c;
     }
@@ -199,15 +199,14 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   bool bad = false;
   pdl_launch_dependents();
-  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.blocks * pl.chunks;
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.chunks;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t rest = item / pl.chunks;
-    const int chunk = (int)(item - rest * pl.chunks), unit = (int)(rest / pl.blocks), block = (int)(rest - (int64_t)unit * pl.blocks);
+    const int unit = (int)(item / pl.chunks), chunk = (int)(item - (int64_t)unit * pl.chunks);
     const Rows r = rows_of(c, unit, voters, &bad);
-    const int rows = r.votes * a.share, col0 = block * COLS;
-    if (col0 >= rows * PARTS) continue;
+    const int rows = r.votes * a.share;
+    if (rows == 0) continue;
     const int tile0 = chunk * pl.chunk, tile1 = min(tile0 + pl.chunk, (r.s.len + TILE - 1) / TILE);
-    const int first = r.position(col0 / PARTS / a.share), last = r.position((min((col0 + COLS) / PARTS, rows) - 1) / a.share);
+    const int first = r.position(0), last = r.position(r.votes - 1);
     float2* out = st.part + item * COLS;
     if (tile0 >= tile1 || seen(a, first, last, tile0 * TILE, (tile1 - tile0) * TILE) == 0) {
       for (int i = threadIdx.x; i < COLS; i += THREADS) out[i] = make_float2(kNegInf, 0.0f);
@@ -220,9 +219,9 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
       id = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
       if (id < 0 || id >= c.n_pages) bad = true, id = 0;
     }
-    load_columns<D, NT, F32>(a, r, col0, sh);
+    load_columns<D, NT, F32>(a, r, 0, sh);
     __syncthreads();
-    const int eights = min(NT, (rows * PARTS - col0 + 7) / 8);
+    const int eights = min(NT, (rows * PARTS + 7) / 8);
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf, l[n][0] = l[n][1] = 0.0f;
@@ -235,6 +234,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
     load(0);
     for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
       const int j0 = tile * TILE, sees = seen(a, first, last, j0, TILE);
+      float* to = st.scores + ((int64_t)unit * pl.votes * a.share * pl.tiles + tile) * TILE;
       const float2 par[4] = {params(cur.par[0][0]), params(cur.par[0][1]), params(cur.par[1][0]), params(cur.par[1][1])};
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -245,13 +245,14 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
 #pragma unroll
         for (int e = 0; e < (F32 ? 1 : 2); ++e) {
           const Column& col = sh.col[n * 8 + 2 * t + e];
+          const int row = (n * 8 + 2 * t + e) / PARTS;
           float x[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const int mt = v >> 1, h = v & 1;
-            const float raw = F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e];
-            x[v] = score(raw, col, par[v]);
-            if (sees == 1 && !visible(a, col.p, j0 + token_of(mt * 16 + h * 8 + g))) x[v] = kNegInf;
+            const int mt = v >> 1, h = v & 1, in = token_of(mt * 16 + h * 8 + g);
+            x[v] = score(F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e], col, par[v]);
+            if (sees == 1 && !visible(a, col.p, j0 + in)) x[v] = kNegInf;
+            if (row < rows) to[(int64_t)row * pl.tiles * TILE + in] = x[v];
           }
           const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m[n][e]), from = top == kNegInf ? 0.0f : top;
           l[n][e] = l[n][e] * exp2_approx(m[n][e] - from) + ((exp2_approx(x[0] - from) + exp2_approx(x[1] - from)) + (exp2_approx(x[2] - from) + exp2_approx(x[3] - from)));
@@ -279,68 +280,13 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
   if (bad) record_device_error(kErrRange);
 }
 
-// The joined (M, 1 / L) of a block's columns, a warp each.
-template <int D, int NT, bool F32>
-__device__ __forceinline__ void load_sums(const Plan& pl, const Stats& st, int unit, int block, int chunks, Shared<D, NT>& sh) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const float2* part = st.part + ((int64_t)unit * pl.blocks + block) * pl.chunks * (NT * 8);
-  for (int i = warp; i < NT * 8; i += WARPS) {
-    if (F32 && (i & 1)) continue;
-    float m = kNegInf, l = 0.0f;
-    for (int k = lane; k < chunks; k += 32) {
-      const float2 v = part[(int64_t)k * (NT * 8) + i];
-      join(m, l, v.x, v.y);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
-    if (lane == 0) {
-      sh.col[i].m = m == kNegInf ? 0.0f : m;
-      sh.col[i].l = l == 0.0f ? 0.0f : __frcp_rn(l);
-    }
-  }
-}
-
-// votes of the lane's four tokens from a block of columns
-template <int D, int NT, bool F32>
-__device__ __forceinline__ void add_votes(const Kv4Attn& a, const Codes<D>& k, const Shared<D, NT>& sh, int eights, int j0, int sees,
-                                          float (&votes)[4]) {
-  const int lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    if (n >= eights) break;
-    float d[2][4];
-    products<D, NT>(k, sh, n, lane, d);
-#pragma unroll
-    for (int e = 0; e < (F32 ? 1 : 2); ++e) {
-      const Column& col = sh.col[n * 8 + 2 * t + e];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int mt = v >> 1, h = v & 1;
-        const float raw = F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e];
-        float w = exp2_approx(score(raw, col, params(k.par[mt][h])) - col.m);
-        if (sees == 1 && !visible(a, col.p, j0 + token_of(mt * 16 + h * 8 + g))) continue;
-        if (col.p >= 0) votes[v] = fmaf(w, col.l, votes[v]);
-      }
-    }
-  }
-}
-// the sum over the four lanes that share tokens; lane t gets token (row) t / 2 * 16 + t % 2 * 8 + g
-__device__ __forceinline__ float gather_votes(const float (&votes)[4], int t) {
-  float s[4];
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    s[v] = votes[v] + __shfl_xor_sync(0xffffffffu, votes[v], 1);
-    s[v] += __shfl_xor_sync(0xffffffffu, s[v], 2);
-  }
-  return t == 0 ? s[0] : t == 1 ? s[1] : t == 2 ? s[2] : s[3];
-}
-
 // ------------------------------------------------------------- second kernel, few columns
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_votes(Kv4 c, Kv4Attn a, Kv4Mass ms, Plan pl, Stats st) {
-  __shared__ Shared<D, NT> sh;
-  constexpr int PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+// A thread a token; the scores are the first kernel's.
+template <int NT, bool F32>
+__global__ void __launch_bounds__(THREADS) kv4_mass_votes(Kv4 c, Kv4Attn a, Kv4Mass ms, Plan pl, Stats st) {
+  __shared__ float2 ml[NT * 8];  // of the rows: M and 1 / L
+  constexpr int PARTS = F32 ? 2 : 1, AHEAD = 4, QUAD = 4;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   bool bad = false;
   const int64_t items = (int64_t)c.batch * c.kv_heads * pl.chunks;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -349,39 +295,68 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_votes(Kv4 c
     const int rows = r.votes * a.share, all = (r.s.len + TILE - 1) / TILE;
     const int tile0 = chunk * pl.chunk, tile1 = min(tile0 + pl.chunk, all);
     if (rows == 0 || tile0 >= tile1) continue;
-    int id = -1;
-    const int mine = tile0 + warp + lane * WARPS;
-    if (mine < tile1) {
-      id = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
-      if (id < 0 || id >= c.n_pages) bad = true, id = -1;
-    }
-    Codes<D> cur;
-    const auto load = [&](int k) {
-      const int from = __shfl_sync(0xffffffffu, id, k);
-      const int tile = tile0 + warp + k * WARPS;
-      if (tile < tile1 && from >= 0) cur.load(c.pages + ((int64_t)from * c.kv_heads + r.h) * BLK, tile, g, t);
+    const int first = r.position(0), last = r.position(r.votes - 1), old = r.s.len - r.s.n, chunks = (all + pl.chunk - 1) / pl.chunk;
+    const int32_t* table = c.page_table + (int64_t)r.b * c.max_pages;
+    const float* scores = st.scores + (int64_t)unit * pl.votes * a.share * pl.tiles * TILE + lane;
+    // four tiles of the warp at a time: their tokens' places and old masses, which wait for nothing, then four rows' scores
+    float before[AHEAD], votes[AHEAD], x[QUAD][AHEAD];
+    int64_t at[AHEAD];
+    bool write[AHEAD], any[AHEAD];
+    const auto places = [&](int tile) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int now = tile + i * WARPS, j = now * TILE + lane;
+        any[i] = now < tile1 && seen(a, first, last, now * TILE, TILE) != 0;
+        write[i] = now < tile1 && j < r.s.len && (ms.decay != 1.0f || ms.in != ms.out || j >= old || any[i]);
+        int id = 0;
+        if (write[i]) id = table[now / 2];
+        if (id < 0 || id >= c.n_pages) bad = true, write[i] = false, id = 0;
+        at[i] = ((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage;
+        before[i] = write[i] && j < old ? ms.in[at[i]] : 0.0f;
+        votes[i] = 0.0f;
+      }
     };
-    load(0);
-    load_columns<D, NT, F32>(a, r, 0, sh);
-    __syncthreads();
+    const auto load = [&](int tile, int row0) {
+#pragma unroll
+      for (int q = 0; q < QUAD; ++q)
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          x[q][i] = any[i] && row0 + q < rows ? scores[((int64_t)(row0 + q) * pl.tiles + tile + i * WARPS) * TILE] : kNegInf;
+    };
+    places(tile0 + warp);
     pdl_wait();
-    load_sums<D, NT, F32>(pl, st, unit, 0, (all + pl.chunk - 1) / pl.chunk, sh);
+    load(tile0 + warp, 0);
+    // the rows' (M, L) from those of the chunks, a warp each
+    for (int row = warp; row < rows; row += WARPS) {
+      float m = kNegInf, l = 0.0f;
+      for (int k = lane; k < chunks; k += 32) {
+        const float2 v = st.part[((int64_t)unit * pl.chunks + k) * (NT * 8) + row * PARTS];
+        join(m, l, v.x, v.y);
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+      if (lane == 0) ml[row] = make_float2(m == kNegInf ? 0.0f : m, l == 0.0f ? 0.0f : __frcp_rn(l));
+    }
     __syncthreads();
-    const int eights = min(NT, (rows * PARTS + 7) / 8), first = r.position(0), last = r.position(r.votes - 1), old = r.s.len - r.s.n;
-    for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
-      const Codes<D> now = cur;
-      const int from = __shfl_sync(0xffffffffu, id, k);
-      if (k < 31) load(k + 1);
-      const int j0 = tile * TILE, sees = seen(a, first, last, j0, TILE);
-      if (from < 0) continue;
-      if (sees == 0 && ms.decay == 1.0f && ms.in == ms.out && j0 + TILE <= old) continue;  // nothing changes
-      const int row = (t >> 1) * 16 + (t & 1) * 8 + g, j = j0 + token_of(row);
-      const int64_t at = ((int64_t)from * c.kv_heads + r.h) * kKvPage + (tile & 1) * TILE + token_of(row);
-      const float before = j < old ? ms.in[at] : 0.0f;
-      float votes[4] = {};
-      if (sees) add_votes<D, NT, F32>(a, now, sh, eights, j0, sees, votes);
-      const float got = gather_votes(votes, t);
-      if (j < r.s.len) ms.out[at] = j < old ? fmaf(ms.decay, before, got) : got;
+#pragma unroll 1
+    for (int tile = tile0 + warp; tile < tile1;) {
+#pragma unroll 1
+      for (int row0 = 0; row0 < rows; row0 += QUAD) {
+        if (row0) load(tile, row0);
+        // a masked score is -inf; it takes no part, whatever the row's sum is
+#pragma unroll
+        for (int q = 0; q < QUAD; ++q) {
+          const float2 v = ml[min(row0 + q, rows - 1)];
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i)
+            if (x[q][i] != kNegInf) votes[i] = fmaf(exp2_approx(x[q][i] - v.x), v.y, votes[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (write[i]) ms.out[at[i]] = (tile + i * WARPS) * TILE + lane < old ? fmaf(ms.decay, before[i], votes[i]) : votes[i];
+      tile += AHEAD * WARPS;
+      if (tile < tile1) places(tile), load(tile, 0);
     }
     __syncthreads();
   }
@@ -995,6 +970,9 @@ int64_t part_bytes(const Kv4& c, const Plan& p) { return align256((int64_t)c.bat
 int64_t votes_bytes(const Kv4& c, const Plan& p) {
   return p.shares ? align256((int64_t)c.batch * c.kv_heads * p.groups * p.shares * WARPS * TILE * 4) : 0;
 }
+int64_t scores_bytes(const Kv4& c, const Plan& p, int share) {
+  return p.shares ? 0 : align256((int64_t)c.batch * c.kv_heads * p.votes * share * p.tiles * TILE * 4);
+}
 int64_t slabs_bytes(const Kv4& c, const Plan& p, int dim) {
   return p.shares ? align256((int64_t)c.batch * c.kv_heads * p.blocks * (int64_t)(dim == 128 ? sizeof(Slab<128>) : sizeof(Slab<64>))) : 0;
 }
@@ -1033,7 +1011,7 @@ cudaError_t launch_few(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const P
   const int64_t units = (int64_t)c.batch * c.kv_heads;
   kv4_mass_rows<D, NT, F32><<<grid_of(units * p.chunks), THREADS, 0, st>>>(c, a, m.voters, p, s);
   if (cudaError_t e = cudaGetLastError()) return e;
-  return launch_behind(kv4_mass_votes<D, NT, F32>, grid_of(units * p.chunks), THREADS, 0, st, c, a, m, p, s);
+  return launch_behind(kv4_mass_votes<NT, F32>, grid_of(units * p.chunks), THREADS, 0, st, c, a, m, p, s);
 }
 template <int D, bool F32>
 cudaError_t launch_many(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
@@ -1070,7 +1048,7 @@ int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters) {
     }
     const Plan p = plan_of(c, q_heads / c.kv_heads, voters, f32, 152);
     if (p.tiles == 0 || (p.nt <= 2 && cluster_of(c, p, q_heads / c.kv_heads, 152).tiles)) continue;
-    const int64_t n = part_bytes(c, p) + votes_bytes(c, p) + slabs_bytes(c, p, dim);
+    const int64_t n = part_bytes(c, p) + votes_bytes(c, p) + slabs_bytes(c, p, dim) + scores_bytes(c, p, q_heads / c.kv_heads);
     most = n > most ? n : most;
   }
   return most;
@@ -1080,7 +1058,8 @@ cudaError_t launch_kv4_mass(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Ma
   if (mass_on_tc(rows, !a.bf16)) return launch_kv4_mass_tc(c, dim, a, m, rows, ws, st);
   const Plan p = plan_of(c, a.share, m.voters, !a.bf16, 152);
   uint8_t* at = static_cast<uint8_t*>(ws);
-  const Stats s{reinterpret_cast<float2*>(at), reinterpret_cast<float*>(at + part_bytes(c, p)), at + part_bytes(c, p) + votes_bytes(c, p)};
+  const Stats s{reinterpret_cast<float2*>(at), reinterpret_cast<float*>(at + part_bytes(c, p)), at + part_bytes(c, p) + votes_bytes(c, p),
+                reinterpret_cast<float*>(at + part_bytes(c, p))};
   if (dim == 128) return a.bf16 ? by_columns<128, false>(c, a, m, p, s, st) : by_columns<128, true>(c, a, m, p, s, st);
   return a.bf16 ? by_columns<64, false>(c, a, m, p, s, st) : by_columns<64, true>(c, a, m, p, s, st);
 }
