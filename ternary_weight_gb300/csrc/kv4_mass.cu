@@ -15,8 +15,8 @@
 // shifted; q' carries the 2^-4): 5 instructions for a word of 8 codes, sums exact in fp32. Lane t of four takes 16
 // bytes of a key row (8 with D = 64), so a warp's loads of a tile are contiguous, straight from the cache.
 //
-// Few columns (16 at most): where a unit's scores fit the shared memory of a cluster of up to eight blocks, one kernel does
-// it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the first kernel leaves the scores
+// Few columns (16 at most): of short sequences, and of many whose scores fit the shared memory of a cluster of up to eight
+// blocks, one kernel does it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the first kernel leaves the scores
 // in the workspace and the second starts behind it. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile.
 // Measured (20 and 5 heads x 128): one query over 77 tokens 4.7 us, 64 over 87 to 8086 43.9 us (fp32 queries), one over 131007
 // 19.9 us (27.9 where the second kernel reads the keys again).
@@ -977,12 +977,16 @@ int64_t slabs_bytes(const Kv4& c, const Plan& p, int dim) {
   return p.shares ? align256((int64_t)c.batch * c.kv_heads * p.blocks * (int64_t)(dim == 128 ? sizeof(Slab<128>) : sizeof(Slab<64>))) : 0;
 }
 
-// The clusters that take the units, if their blocks' scores fit: no more blocks than that needs, but enough to fill the GPU.
+// The clusters that take the units, if their blocks' scores fit: no more blocks than that needs. For sequences of up to 256
+// tokens, and where the units fill the GPU by themselves; else two kernels. Measured, us (5 heads x 128, one token of each sequence),
+// one kernel (there with clusters that fill the GPU) and two: 250 tokens 5.1, 5.6; 300 6.1, 5.5; 25000 21.3, 8.2; 32 sequences of
+// 1000 9.8, 8.9; 48 of 1000 10.5, 13.4; 64 of 17 to 8175 45.7, 53.5.
 Cluster cluster_of(const Kv4& c, const Plan& p, int share, int num_sms) {
   Cluster k{1, 0, p.votes * share};
   const int64_t units = (int64_t)c.batch * c.kv_heads, row_bytes = (int64_t)k.rows * 4 * TILE;
+  if (p.tiles > WARPS && units * 2 <= num_sms * 3) return k;
   const auto bytes = [&](int n) { return (p.tiles + n - 1) / n * row_bytes; };
-  while (k.blocks < 8 && (bytes(k.blocks) > kScoreBytes || (units * k.blocks * 2 <= num_sms * 3 && p.tiles > k.blocks * 2 * WARPS))) k.blocks *= 2;
+  while (k.blocks < 8 && bytes(k.blocks) > kScoreBytes) k.blocks *= 2;
   k.tiles = bytes(k.blocks) > kScoreBytes ? 0 : (p.tiles + k.blocks - 1) / k.blocks;
   return k;
 }

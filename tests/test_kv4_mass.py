@@ -192,6 +192,16 @@ def test_batches_made_for_far_more(cuda_lib, dim, dtype, share, n, kv, most_q, m
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim,dtype,share,longest", [(64, "bf16", 16, 1100), (64, "f32", 8, 9000), (128, "bf16", 16, 4500), (128, "bf16", 4, 300)])
+def test_many_sequences(cuda_lib, dim, dtype, share, longest):
+    """More units than fill the GPU, some of them long: clusters of one to eight blocks."""
+    kv = [longest, 0, 1] + [1 + 37 * i % 200 for i in range(117)]
+    w = Mass([int(n > 0) for n in kv], kv, 2, dim, dtype, seed=longest).fill()
+    mass, q = w.start(), w.queries(share)
+    w.check(gather(w, q, mass, decay=0.3), q, share, dim ** -0.5, 0.3)
+
+
+@pytest.mark.gpu
 def test_two_calls_at_once(cuda_lib):
     """Calls on two streams, and graphs of theirs replayed side by side: nothing of the calls is shared."""
     worlds = [Mass([n] * 3, [kv, 70, kv // 2], 2, 64, "bf16", seed=n).fill() for n, kv in ((1, 5000), (60, 3000), (1, 300), (9, 900))]
