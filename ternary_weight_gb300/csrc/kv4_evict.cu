@@ -10,8 +10,8 @@
 //
 // Bound by latency where sequences are few: loads that depend on each other (length, page, mass; kept token, page, data) and
 // the cluster's barriers; by issue slots and the moved bytes where they are many. Measured (5 heads x 128, into other pages):
-// 131007 tokens to 4096 25.2 us, to 64 23.9; 16000 to 64 15.2; 48 sequences of 501 to 16001 to 2048 59 us (141 MB), to 64 31;
-// 300 to 200 9.5 us. Loops are kept short: unrolled ones cost the small cases half as much again, in instruction fetches.
+// 131007 tokens to 4096 24.9 us, to 64 23.9; 16000 to 64 15.4; 48 sequences of 501 to 16001 to 2048 52 us (141 MB), to 64 31;
+// 300 to 200 8.8 us. Loops are kept short: unrolled ones cost the small cases half as much again, in instruction fetches.
 #include "kv4.cuh"
 #include "smem_limit.h"
 
@@ -59,7 +59,6 @@ __device__ __forceinline__ uint4 ld_cluster_u32x4(uint32_t addr) {
   return v;
 }
 
-// A token's data: lanes take 16 bytes of its key or value row each, the first its parameters, the second its mass.
 template <int D>
 __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e, int32_t* kept, int cap, int cluster, int ranks_kept,
                                                                bool write_len) {
@@ -247,70 +246,62 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     sync_all();  // the list is written, and no block reads another's counts any more
   }
 
-  // ---- the kept tokens move (all unsigned 32-bit: their indexes are below 2^30)
-  constexpr uint32_t LANES = D / 16, PIECES = LANES / 2, TOKENS = THREADS / LANES, BATCH = 4, PAGE = kKvPage;
-  const uint32_t part = tid % LANES, worker = tid / LANES, keeps = s.keeps, piece = part % PIECES * 16;
+  // ---- the kept tokens move (all unsigned 32-bit: their indexes are below 2^30, and so are a pool's blocks)
+  // A warp takes RUN tokens at a time. Lane l finds where token l comes from and goes to, and moves its parameters and mass; the
+  // lanes move the rows in 16-byte pieces, LANES a token, by what that lane hands them.
+  constexpr uint32_t LANES = D / 16, PIECES = LANES / 2, EACH = 32 / LANES, BATCH = 4, RUN = EACH * BATCH, PAGE = kKvPage;
+  const uint32_t part = lane % LANES, keeps = s.keeps, piece = part % PIECES * 16;
   const bool is_key = part < PIECES;
   const uint32_t* from = reinterpret_cast<const uint32_t*>(c.page_table + (int64_t)b * c.max_pages);
   const uint32_t* to = e.into ? reinterpret_cast<const uint32_t*>(e.into + (int64_t)b * e.into_pages) : from;
   const uint32_t n_pages = c.n_pages, heads = c.kv_heads;
-  // a head's block of a page, in blocks; where the lane's 16 bytes and the parameters of place t lie in it
+  // where the lane's 16 bytes and the parameters of place t lie in a head's block of a page
   const auto rho = [](uint32_t t) { return (t & ~7u) | (t & 3u) << 1 | (t >> 2 & 1u); };
   const auto data_at = [&](uint32_t t) { return (is_key ? rho(t) : PAGE + t) * (D / 2) + piece; };
-  // the sources of the next chunk are looked up while this one's data is on its way
   constexpr uint32_t NONE = 0xffffffffu;
-  uint32_t src[BATCH];
+  uint32_t from_blk = 0, to_blk = 0, places = NONE;  // the token's places in its pages, the old one and the new one << 8; NONE: it stays
   const auto look = [&](uint32_t first) {
-#pragma unroll
-    for (uint32_t i = 0; i < BATCH; ++i) {
-      const uint32_t r = first + i * TOKENS;
-      src[i] = r < keeps ? (cut ? (uint32_t)list[r] : r) : NONE;
-      if (!e.into && src[i] == r) src[i] = NONE;  // it stays
+    const uint32_t r = first + lane;
+    places = NONE;
+    if (lane >= RUN || r >= keeps) return;
+    const uint32_t j = cut ? (uint32_t)list[r] : r;
+    if (!e.into && j == r) return;
+    const uint32_t x = from[j / PAGE], y = to[r / PAGE];
+    if (x >= n_pages || y >= n_pages) {
+      bad = true;
+      return;
     }
+    from_blk = x * heads + h, to_blk = y * heads + h, places = j % PAGE | (r % PAGE) << 8;
   };
-  const uint32_t chunk = cluster * TOKENS * BATCH, mine = me * TOKENS * BATCH + worker;
+  const uint32_t chunk = cluster * WARPS * RUN, mine = (me * WARPS + warp) * RUN;
   look(mine);
 #pragma unroll 1
   for (uint32_t first = 0; first < keeps; first += chunk) {
-    const uint32_t r0 = first + mine;
     uint4 data[BATCH];
-    uint2 par[BATCH];  // lane 0: the parameters; lane 1: the mass
-    uint32_t id[BATCH], low[BATCH];  // low: the source's place in its page
-#pragma unroll
-    for (uint32_t i = 0; i < BATCH; ++i) id[i] = src[i] != NONE ? from[src[i] / PAGE] : NONE - 1;
-#pragma unroll
-    for (uint32_t i = 0; i < BATCH; ++i) {
-      low[i] = src[i] != NONE ? src[i] % PAGE : NONE;
-      if (src[i] == NONE) continue;
-      if (id[i] >= n_pages) {
-        bad = true, low[i] = NONE;
-        continue;
-      }
-      const uint64_t block = (uint64_t)id[i] * heads + h;
-      const uint8_t* blk = c.pages + block * BLK;
-      data[i] = *reinterpret_cast<const uint4*>(blk + data_at(low[i]));
-      if (part == 0) par[i] = *reinterpret_cast<const uint2*>(blk + PAGE * D + rho(low[i]) * 8);
-      if (part == 1) par[i].x = __float_as_uint(e.mass[block * PAGE + low[i]]);
+    uint2 par = make_uint2(0, 0);
+    float mass = 0.0f;
+    const uint32_t low = places & 63, high = places >> 8 & 63, blk = to_blk, both = places;
+    if (both != NONE) {
+      par = *reinterpret_cast<const uint2*>(c.pages + (uint64_t)from_blk * BLK + PAGE * D + rho(low) * 8);
+      mass = e.mass[(uint64_t)from_blk * PAGE + low];
     }
 #pragma unroll
-    for (uint32_t i = 0; i < BATCH; ++i) id[i] = low[i] != NONE ? to[(r0 + i * TOKENS) / PAGE] : NONE - 1;
-    look(r0 + chunk);
+    for (uint32_t i = 0; i < BATCH; ++i) {
+      const uint32_t x = __shfl_sync(0xffffffffu, from_blk, i * EACH + lane / LANES), p = __shfl_sync(0xffffffffu, both, i * EACH + lane / LANES);
+      if (p != NONE) data[i] = *reinterpret_cast<const uint4*>(c.pages + (uint64_t)x * BLK + data_at(p & 63));
+    }
+    look(first + chunk + mine);  // the next ones' places while these are on their way
     if (!e.into) sync_all();
 #pragma unroll
     for (uint32_t i = 0; i < BATCH; ++i) {
-      if (low[i] == NONE) continue;
-      if (id[i] >= n_pages) {
-        bad = true;
-        continue;
-      }
-      const uint32_t r = r0 + i * TOKENS, t = r % PAGE;
-      const uint64_t block = (uint64_t)id[i] * heads + h;
-      uint8_t* blk = c.pages + block * BLK;
+      const uint32_t y = __shfl_sync(0xffffffffu, blk, i * EACH + lane / LANES), p = __shfl_sync(0xffffffffu, both, i * EACH + lane / LANES);
       // the halves of a wide value row are exchanged where bit 1 of the place is set
-      const uint32_t turn = D == 128 && !is_key ? ((low[i] ^ r) & 2) << 4 : 0;
-      *reinterpret_cast<uint4*>(blk + (data_at(t) ^ turn)) = data[i];
-      if (part == 0) *reinterpret_cast<uint2*>(blk + PAGE * D + rho(t) * 8) = par[i];
-      if (part == 1) e.mass[block * PAGE + t] = __uint_as_float(par[i].x);
+      const uint32_t turn = D == 128 && !is_key ? ((p ^ p >> 8) & 2) << 4 : 0;
+      if (p != NONE) *reinterpret_cast<uint4*>(c.pages + (uint64_t)y * BLK + (data_at(p >> 8 & 63) ^ turn)) = data[i];
+    }
+    if (both != NONE) {
+      *reinterpret_cast<uint2*>(c.pages + (uint64_t)blk * BLK + PAGE * D + rho(high) * 8) = par;
+      e.mass[(uint64_t)blk * PAGE + high] = mass;
     }
     if (!e.into) sync_all();
   }
