@@ -2,7 +2,7 @@
 //
 // One kernel; a cluster of one to sixteen blocks for each sequence and head. Its blocks take a run of tokens each and keep
 // the ranks of their masses (whole numbers in the masses' order) in shared memory. The least rank that is kept is found by
-// three passes that count digits (11, 11 and 10 bits, from the top), added up over the cluster through distributed
+// three passes that count digits (11, 11 and 10 bits, from the top; the first while the masses are read), added up over the cluster through distributed
 // shared memory; then every warp counts and lists the kept tokens of its run, in order, and the cluster moves them: codes,
 // parameters and mass, as they are. In place a token only moves to an earlier slot, and a chunk of tokens is read
 // whole, by all blocks of the cluster, before any of it is written, so that nothing is overwritten before it has been read.
@@ -10,8 +10,8 @@
 //
 // Bound by latency where sequences are few: loads that depend on each other (length, page, mass; kept token, page, data) and
 // the cluster's barriers; by issue slots and the moved bytes where they are many. Measured (5 heads x 128, into other pages):
-// 131007 tokens to 4096 24.9 us, to 64 23.9; 16000 to 64 15.4; 48 sequences of 501 to 16001 to 2048 52 us (141 MB), to 64 31;
-// 300 to 200 8.8 us. Loops are kept short: unrolled ones cost the small cases half as much again, in instruction fetches.
+// 131007 tokens to 4096 24.1 us, to 64 23; 16000 to 64 15.3; 48 sequences of 501 to 16001 to 2048 52 us (141 MB), to 64 28.5;
+// 300 to 200 8.7 us. Loops are kept short: unrolled ones cost the small cases half as much again, in instruction fetches.
 #include "kv4.cuh"
 #include "smem_limit.h"
 
@@ -92,7 +92,12 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     const int run0 = (int)min((int64_t)me * WARPS * per, (int64_t)s.len), j0 = (int)min(run0 + (int64_t)warp * per, (int64_t)s.len), j1 = (int)min(j0 + (int64_t)per, (int64_t)s.len);
     const bool keep = WARPS * per <= ranks_kept;
     const auto ranked = [&](int j, float mass) { return j < lo || j >= hi ? SURE : rank_of(mass); };
+    // tokens without any mass may be many: a warp's are counted together, not one after another in one bin
+    const uint32_t zero = 0x80000000u;
+    uint32_t zeros = 0;
     if (keep) {
+      for (int i = tid; i < BINS; i += THREADS) bins[i] = 0;
+      __syncthreads();
       // the page ids of the next 32 pages, one a lane, then the masses of 8 x 32 tokens at a time
       for (int p0 = j0 / kKvPage; p0 * kKvPage < j1; p0 += 32) {
         int id = 0;
@@ -106,12 +111,17 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int from = __shfl_sync(0xffffffffu, id, q + (i >> 1)), j = (p0 + q) * kKvPage + i * 32 + lane;
-            if (j >= j0 && j < j1) m[i] = e.mass[((int64_t)from * c.kv_heads + h) * kKvPage + j % kKvPage];
+            if (j >= j0 && j < j1) m[i] = e.mass[((int64_t)from * c.kv_heads + h) * kKvPage + (i & 1) * 32 + lane];
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int j = (p0 + q) * kKvPage + i * 32 + lane;
-            if (j >= j0 && j < j1) ranks[j - run0] = ranked(j, m[i]);
+            if (j < j0 || j >= j1) continue;
+            const uint32_t r = ranked(j, m[i]);
+            ranks[j - run0] = r;
+            // the first pass's count
+            if (r == zero) ++zeros;
+            else atomicAdd(&bins[r >> 21], 1u);
           }
         }
       }
@@ -126,24 +136,25 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-      for (int i = tid; i < BINS; i += THREADS) bins[i] = 0;
-      __syncthreads();
-      // tokens without any mass may be many: a warp's are counted together, not one after another in one bin
-      const uint32_t digits = (1u << width) - 1, zero = 0x80000000u;
-      uint32_t zeros = 0;
+      if (pass > 0 || !keep) {
+        zeros = 0;
+        for (int i = tid; i < BINS; i += THREADS) bins[i] = 0;
+        __syncthreads();
+        const uint32_t digits = (1u << width) - 1;
 #pragma unroll 1
-      for (int j = j0 + lane; j - lane < j1; j += 4 * 32) {
-        uint32_t r[4];
+        for (int j = j0 + lane; j - lane < j1; j += 4 * 32) {
+          uint32_t r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = rank(j + 32 * i);
+          for (int i = 0; i < 4; ++i) r[i] = rank(j + 32 * i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (r[i] == zero) ++zeros;
-          else if ((r[i] & mask) == least && r[i]) atomicAdd(&bins[(r[i] >> shift) & digits], 1u);
+          for (int i = 0; i < 4; ++i) {
+            if (r[i] == zero) ++zeros;
+            else if ((r[i] & mask) == least && r[i]) atomicAdd(&bins[(r[i] >> shift) & digits], 1u);
+          }
         }
       }
       zeros = __reduce_add_sync(0xffffffffu, zeros);
-      if (lane == 0 && zeros && (zero & mask) == least) atomicAdd(&bins[(zero >> shift) & digits], zeros);
+      if (lane == 0 && zeros && (zero & mask) == least) atomicAdd(&bins[(zero >> shift) & ((1u << width) - 1)], zeros);
       sync_all();
       // The digit from which on `want` tokens are counted, from above. Each block adds up its slice of the bins over the
       // cluster, a slice's total goes to all blocks, and the block whose slice has the digit tells it.
