@@ -18,8 +18,8 @@
 // Few columns (16 at most): of short sequences, and of many whose scores fit the shared memory of a cluster of up to eight
 // blocks, one kernel does it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the first kernel leaves the scores
 // in the workspace and the second starts behind it. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile.
-// Measured (20 and 5 heads x 128): one query over 77 tokens 4.7 us, 64 over 87 to 8086 43.9 us (fp32 queries), one over 131007
-// 19.9 us (27.9 where the second kernel reads the keys again).
+// Measured (20 and 5 heads x 128): one query over 77 tokens 4.7 us, 64 over 87 to 8086 43.3 us (fp32 queries), one over 131007
+// 19.6 us (27.6 where the second kernel reads the keys again).
 //
 // More columns, up to 96 rows (kv4_mass_tc.cu has the others): blocks of 64 whose fragments the first kernel leaves in the
 // workspace; the second kernel's blocks keep their tiles' codes and go through a share of the columns, and a third one adds up
@@ -212,12 +212,14 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
       for (int i = threadIdx.x; i < COLS; i += THREADS) out[i] = make_float2(kNegInf, 0.0f);
       continue;
     }
-    // the page ids of this warp's tiles, one a lane
-    int id = 0;
-    const int mine = tile0 + warp + lane * WARPS;
+    // the blocks of this warp's tiles, one a lane, and which tiles the rows see any and all of
+    uint32_t id = r.h;
+    const int mine = tile0 + warp + lane * WARPS, what = mine < tile1 ? seen(a, first, last, mine * TILE, TILE) : 0;
+    const uint32_t any = __ballot_sync(0xffffffffu, what > 0), whole = __ballot_sync(0xffffffffu, what == 2);
     if (mine < tile1) {
-      id = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
-      if (id < 0 || id >= c.n_pages) bad = true, id = 0;
+      const int page = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
+      if (page < 0 || page >= c.n_pages) bad = true;
+      else id = (uint32_t)page * c.kv_heads + r.h;
     }
     load_columns<D, NT, F32>(a, r, 0, sh);
     __syncthreads();
@@ -227,13 +229,14 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
     for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf, l[n][0] = l[n][1] = 0.0f;
     Codes<D> cur;
     const auto load = [&](int k) {
-      const int from = __shfl_sync(0xffffffffu, id, k);
+      const uint32_t from = __shfl_sync(0xffffffffu, id, k);
       const int tile = tile0 + warp + k * WARPS;
-      if (tile < tile1) cur.load(c.pages + ((int64_t)from * c.kv_heads + r.h) * BLK, tile, g, t);
+      if (tile < tile1) cur.load(c.pages + (uint64_t)from * BLK, tile, g, t);
     };
     load(0);
     for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
-      const int j0 = tile * TILE, sees = seen(a, first, last, j0, TILE);
+      const int j0 = tile * TILE;
+      const bool sees = any >> k & 1, masked = !(whole >> k & 1);
       float* to = st.scores + ((int64_t)unit * pl.votes * a.share * pl.tiles + tile) * TILE;
       const float2 par[4] = {params(cur.par[0][0]), params(cur.par[0][1]), params(cur.par[1][0]), params(cur.par[1][1])};
 #pragma unroll
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
         float d[2][4];
         if (n < eights) products<D, NT>(cur, sh, n, lane, d);
         if (n == NT - 1 && k < 31) load(k + 1);  // the codes' registers are free
-        if (n >= eights || sees == 0) continue;
+        if (n >= eights || !sees) continue;
 #pragma unroll
         for (int e = 0; e < (F32 ? 1 : 2); ++e) {
           const Column& col = sh.col[n * 8 + 2 * t + e];
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
           for (int v = 0; v < 4; ++v) {
             const int mt = v >> 1, h = v & 1, in = token_of(mt * 16 + h * 8 + g);
             x[v] = score(F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e], col, par[v]);
-            if (sees == 1 && !visible(a, col.p, j0 + in)) x[v] = kNegInf;
+            if (masked && !visible(a, col.p, j0 + in)) x[v] = kNegInf;
             if (row < rows) to[(int64_t)row * pl.tiles * TILE + in] = x[v];
           }
           const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m[n][e]), from = top == kNegInf ? 0.0f : top;
@@ -389,15 +392,18 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
     return;
   }
   const int tile0 = min(me * per, all), tile1 = min(tile0 + per, all), first = r.position(0), last = r.position(r.votes - 1);
-  // the page ids of this warp's next 32 tiles, one a lane (-1: not in the pool)
+  // the blocks (below 2^30) of this warp's next 32 tiles, one a lane (-1: not in the pool), and which of them the rows see any and all of
+  uint32_t any = 0, whole = 0;
   const int32_t* table = c.page_table + (int64_t)r.b * c.max_pages;
   const auto ids_of = [&](int k) {
     const int tile = tile0 + warp + (k + lane) * WARPS;
-    int id = -1;
+    int id = -1, what = 0;
     if (tile < tile1) {
-      id = table[tile / 2];
-      if (id < 0 || id >= c.n_pages) bad = true, id = -1;
+      const int page = table[tile / 2];
+      if (page < 0 || page >= c.n_pages) bad = true;
+      else id = page * c.kv_heads + r.h, what = seen(a, first, last, tile * TILE, TILE);
     }
+    any = __ballot_sync(0xffffffffu, what > 0), whole = __ballot_sync(0xffffffffu, what == 2);
     return id;
   };
   int ids = ids_of(0);
@@ -410,13 +416,13 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
   Codes<D> cur;
   const auto load = [&](int k) {
     const int id = __shfl_sync(0xffffffffu, ids, k & 31);
-    if (id >= 0) cur.load(c.pages + ((int64_t)id * c.kv_heads + r.h) * BLK, tile0 + warp + k * WARPS, g, t);
-    return id;
+    if (id >= 0) cur.load(c.pages + (int64_t)id * BLK, tile0 + warp + k * WARPS, g, t);
   };
-  int ahead = load(0);
+  load(0);
 #pragma unroll 1
   for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
-    const int id = ahead, j0 = tile * TILE, sees = id < 0 ? 0 : seen(a, first, last, j0, TILE);
+    const int j0 = tile * TILE;
+    const bool sees = any >> (k & 31) & 1, masked = !(whole >> (k & 31) & 1);
     float* to = kept + (int64_t)(tile - tile0) * TILE * cl.rows;
     const float2 par[4] = {params(cur.par[0][0]), params(cur.par[0][1]), params(cur.par[1][0]), params(cur.par[1][1])};
     if ((k & 31) == 31) ids = ids_of(k + 1);
@@ -424,8 +430,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
     for (int n = 0; n < NT; ++n) {
       float d[2][4];
       if (n < eights) products<D, NT>(cur, sh, n, lane, d);
-      if (n == NT - 1) ahead = load(k + 1);  // the codes' registers are free
-      if (n >= eights || sees == 0) continue;
+      if (n == NT - 1) load(k + 1);  // the codes' registers are free
+      if (n >= eights || !sees) continue;
 #pragma unroll
       for (int e = 0; e < (F32 ? 1 : 2); ++e) {
         const Column& col = sh.col[n * 8 + 2 * t + e];
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
         for (int v = 0; v < 4; ++v) {
           const int mt = v >> 1, h = v & 1, in = token_of(mt * 16 + h * 8 + g);
           x[v] = score(F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e], col, par[v]);
-          if (sees == 1 && !visible(a, col.p, j0 + in)) x[v] = kNegInf;
+          if (masked && !visible(a, col.p, j0 + in)) x[v] = kNegInf;
           if (row < cl.rows) to[in * cl.rows + row] = x[v];
         }
         const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m[n][e]), from = top == kNegInf ? 0.0f : top;
@@ -482,8 +488,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int id = __shfl_sync(0xffffffffu, ids, (k + i) & 31), j = (tile0 + warp + (k + i) * WARPS) * TILE + lane;
-      const bool write = id >= 0 && j < r.s.len && (ms.decay != 1.0f || ms.in != ms.out || j >= old || seen(a, first, last, j - lane, TILE) != 0);
-      before[i] = write && j < old ? ms.in[((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage] : 0.0f;
+      const bool write = id >= 0 && j < r.s.len && (ms.decay != 1.0f || ms.in != ms.out || j >= old || (any >> ((k + i) & 31) & 1));
+      before[i] = write && j < old ? ms.in[(int64_t)id * kKvPage + j % kKvPage] : 0.0f;
       writes |= write << i;
     }
 #pragma unroll
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
       const int id = __shfl_sync(0xffffffffu, ids, (k + i) & 31), tile = tile0 + warp + (k + i) * WARPS, j = tile * TILE + lane;
       if (!(writes >> i & 1)) continue;
       float votes = 0.0f;
-      if (seen(a, first, last, tile * TILE, TILE)) {
+      if (any >> ((k + i) & 31) & 1) {
         const float* x = kept + (int64_t)((tile - tile0) * TILE + lane) * cl.rows;
 #pragma unroll 1
         for (int row = 0; row < rows; ++row) {
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_cluster(Kv4
           if (x[row] != kNegInf) votes = fmaf(exp2_approx(x[row] - ml.x), ml.y, votes);
         }
       }
-      ms.out[((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage] = j < old ? fmaf(ms.decay, before[i], votes) : votes;
+      ms.out[(int64_t)id * kKvPage + j % kKvPage] = j < old ? fmaf(ms.decay, before[i], votes) : votes;
     }
   }
   if (bad) record_device_error(kErrRange);
