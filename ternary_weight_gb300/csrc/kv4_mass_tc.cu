@@ -40,12 +40,12 @@ struct Shape {
   static constexpr int PARTS = F32 ? 2 : 1;
   static constexpr int IMAGE = 128 * D * 2;               // an operand: D / 64 atoms of 128 rows x 128 bytes
   static constexpr int BLOCK = IMAGE * PARTS + (int)sizeof(Constants);  // as the first kernel leaves it
-  static constexpr int CON = 3072;                        // place of the constants in shared memory
+  static constexpr int CON = 3 * 1024;                       // place of the constants in shared memory
   static constexpr int ROWS_SMEM = IMAGE * PARTS + CON + 2 * IMAGE + 3 * 1024 + 1024;
   static constexpr int VOTES_SMEM = IMAGE + 2 * IMAGE * PARTS + 3 * CON + 1024;
   static constexpr int BLOCKS = F32 && D == 128 ? 1 : 2;  // resident on an SM
 };
-static_assert(sizeof(Constants) <= 3072 && sizeof(Constants) % 16 == 0, "");
+static_assert(sizeof(Constants) <= 3 * 1024 && sizeof(Constants) % 16 == 0, "");
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
