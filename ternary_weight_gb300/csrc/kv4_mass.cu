@@ -18,8 +18,8 @@
 // Few columns (16 at most): of short sequences, and of many whose scores fit the shared memory of a cluster of up to eight
 // blocks, one kernel does it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the first kernel leaves the scores
 // in the workspace and the second starts behind it. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile.
-// Measured (20 and 5 heads x 128): one query over 77 tokens 4.7 us, 64 over 87 to 8086 43.3 us (fp32 queries), one over 131007
-// 19.6 us (27.9 where the second kernel reads the keys again).
+// Measured (20 and 5 heads x 128): one query over 77 tokens 4.8 us, 64 over 87 to 8086 43.7 us (fp32 queries), one over 131007
+// 19.5 us (27.9 where the second kernel reads the keys again).
 //
 // More columns, up to 96 rows (kv4_mass_tc.cu has the others): blocks of 64 whose fragments the first kernel leaves in the
 // workspace; the second kernel's blocks keep their tiles' codes and go through a share of the columns, and a third one adds up

@@ -40,7 +40,7 @@ struct Shape {
   static constexpr int PARTS = F32 ? 2 : 1;
   static constexpr int IMAGE = 128 * D * 2;               // an operand: D / 64 atoms of 128 rows x 128 bytes
   static constexpr int BLOCK = IMAGE * PARTS + (int)sizeof(Constants);  // as the first kernel leaves it
-  static constexpr int CON = 3 * 1024;                       // place of the constants in shared memory
+  static constexpr int CON = 3 * 1024;                    // place of the constants in shared memory
   static constexpr int ROWS_SMEM = IMAGE * PARTS + CON + 2 * IMAGE + 3 * 1024 + 1024;
   static constexpr int VOTES_SMEM = IMAGE + 2 * IMAGE * PARTS + 3 * CON + 1024;
   static constexpr int BLOCKS = F32 && D == 128 ? 1 : 2;  // resident on an SM
