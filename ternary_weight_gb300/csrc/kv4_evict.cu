@@ -41,10 +41,15 @@ __device__ __forceinline__ Sizes sizes_of(const Kv4& c, const Kv4Evict& e, int b
   if (l < 0 || l > c.max_kv) return {-1, 0};
   return {l, l > e.limit ? e.budget : l};
 }
-__device__ __forceinline__ float* mass_of(const Kv4& c, const Kv4Evict& e, int b, int h, int j, bool* bad) {
-  int id = c.page_table[(int64_t)b * c.max_pages + j / kKvPage];
-  if (id < 0 || id >= c.n_pages) *bad = true, id = 0;
-  return e.mass + ((int64_t)id * c.kv_heads + h) * kKvPage + j % kKvPage;
+// The mass of token j. One whose page is not in the pool has none, whatever pass asks (and no other page's, which another
+// cluster may be moving): all passes have to find the same tokens.
+__device__ __forceinline__ float mass_of(const Kv4& c, const Kv4Evict& e, int b, int h, int j, bool* bad) {
+  const int id = c.page_table[(int64_t)b * c.max_pages + j / kKvPage];
+  if (id < 0 || id >= c.n_pages) {
+    *bad = true;
+    return 0.0f;
+  }
+  return e.mass[((int64_t)id * c.kv_heads + h) * kKvPage + j % kKvPage];
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -100,10 +105,10 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
       __syncthreads();
       // the page ids of the next 32 pages, one a lane, then the masses of 8 x 32 tokens at a time
       for (int p0 = j0 / kKvPage; p0 * kKvPage < j1; p0 += 32) {
-        int id = 0;
+        int id = -1;  // not in the pool: its tokens have no mass
         if ((int64_t)(p0 + lane) * kKvPage < j1) {
           id = c.page_table[(int64_t)b * c.max_pages + p0 + lane];
-          if (id < 0 || id >= c.n_pages) bad = true, id = 0;
+          if (id < 0 || id >= c.n_pages) bad = true, id = -1;
         }
 #pragma unroll 1
         for (int q = 0; q < 32 && (p0 + q) * kKvPage < j1; q += 4) {
@@ -111,7 +116,8 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int from = __shfl_sync(0xffffffffu, id, q + (i >> 1)), j = (p0 + q) * kKvPage + i * 32 + lane;
-            if (j >= j0 && j < j1) m[i] = e.mass[((int64_t)from * c.kv_heads + h) * kKvPage + (i & 1) * 32 + lane];
+            m[i] = 0.0f;
+            if (j >= j0 && j < j1 && from >= 0) m[i] = e.mass[((int64_t)from * c.kv_heads + h) * kKvPage + (i & 1) * 32 + lane];
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     // of token j of this warp's run; 0, which is no rank, past its end
     const auto rank = [&](int j) {
       if (j >= j1) return 0u;
-      return keep ? ranks[j - run0] : ranked(j, *mass_of(c, e, b, h, j, &bad));
+      return keep ? ranks[j - run0] : ranked(j, mass_of(c, e, b, h, j, &bad));
     };
     uint32_t least = 0, mask = 0;  // the digits found so far
 #pragma unroll 1
@@ -276,6 +282,12 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_evict_kernel(Kv4 c, Kv4Evict e
     places = NONE;
     if (lane >= RUN || r >= keeps) return;
     const uint32_t j = cut ? (uint32_t)list[r] : r;
+    // A list is whole where the masses stood still. Where a table names pages of a sequence that another cluster moves they may
+    // not have, and what the workspace held before is no token.
+    if (j >= (uint32_t)s.len) {
+      bad = true;
+      return;
+    }
     if (!e.into && j == r) return;
     const uint32_t x = from[j / PAGE], y = to[r / PAGE];
     if (x >= n_pages || y >= n_pages) {
