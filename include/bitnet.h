@@ -514,7 +514,7 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache *cache, const bitnet_
  *            sequence that does not fit there is not moved, and BITNET_ERANGE is recorded.
  *            NULL: in place, to the sequence's first pages (then no two sequences may share pages)
  *   new_len: batch (device, written) or NULL: the tokens that each sequence keeps. It may be the batch's kv_len
- *            itself; the layers of a model that share it pass NULL but for the last
+ *            itself (not overlap it otherwise); the layers of a model that share it pass NULL but for the last
  *   1 <= budget <= limit < 2^31, sinks >= 0, recent >= 0, sinks + recent <= budget
  *   mass   : 16-byte aligned; into, new_len 4
  *   workspace : device, 256-byte aligned, at least bitnet_kv4_evict_workspace_size bytes

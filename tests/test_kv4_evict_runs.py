@@ -1,11 +1,22 @@
 """Eviction of sequences whose runs are longer than what a block keeps in shared memory, and by clusters into other pages:
 byte for byte against plain numpy, also where a table names pages that are not in the pool."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import kv4_reference as ref
 from ternary_weight_gb300 import _build, binding
+
+
+@pytest.mark.parametrize("to,want", [(0, -2), (4 * 8, -2), (-4 * 8, -2), (4, -1), (-4, -1), (4 * 7, -1), (-4 * 7, -1)])
+def test_new_lengths_over_those_of_other_sequences_are_refused(to, want):
+    """Over the old lengths themselves, or apart from them. (Calls that pass this check are refused for their masses' alignment.)"""
+    _build.build()
+    at = 1 << 20
+    c, b = binding._KV4CacheDesc(at, 4, 2, 128), binding._KV4BatchDesc(at, at, at, 8, 2, 0, 1, 128)
+    assert binding.lib().bitnet_kv4_evict(ctypes.byref(c), ctypes.byref(b), at + 4, 50, 60, 4, 10, None, 0, at + to, at, 1 << 40, None) == want
 
 
 @pytest.fixture
