@@ -636,12 +636,13 @@ BITNET_API int bitnet_kv4_evict(const bitnet_kv4_cache* cache, const bitnet_kv4_
   if (!mass || budget < 1 || limit < budget || limit > INT32_MAX) return BITNET_EINVAL;
   if (sinks < 0 || sinks > budget || recent < 0 || recent > budget - sinks) return BITNET_EINVAL;
   if (into && (into_pages < 1 || into_pages > kKvMaxPages || into_pages * kKvPage < budget)) return BITNET_EINVAL;
+  if (!aligned(new_len, 4)) return BITNET_EALIGN;
   // lengths that are written over those of other sequences: the blocks of a cluster would read different ones
   const uintptr_t from = reinterpret_cast<uintptr_t>(c.kv_len), to = reinterpret_cast<uintptr_t>(new_len), bytes = (uintptr_t)c.batch * 4;
   if (new_len && from != to && from < to + bytes && to < from + bytes) return BITNET_EINVAL;
   const int64_t need = kv4_evict_ws_bytes(c, (int)budget);
   if (!workspace || workspace_bytes < need) return BITNET_EINVAL;
-  if (!aligned(mass, 16) || !aligned(workspace, 256) || !aligned(into, 4) || !aligned(new_len, 4)) return BITNET_EALIGN;
+  if (!aligned(mass, 16) || !aligned(workspace, 256) || !aligned(into, 4)) return BITNET_EALIGN;
   int sms = 0;
   if (int st = check_device(&sms)) return st;
   const Kv4Evict e{mass, into, into_pages, new_len, (int)budget, (int)limit, (int)sinks, (int)recent};
