@@ -494,7 +494,7 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache *cache, const bitnet_
  *   Only the places of the cached tokens of sequences with new tokens are written. A query that sees nothing votes
  *   for nothing. Keys enter as codes with fp32 steps and bases; bf16 queries keep their bits (those below 2^-28 of
  *   the row's largest may not), fp32 ones enter as two fp16 parts (22 bits); scores, maxima and sums are fp32. A NaN
- *   or an infinity in a query or key makes the votes of the rows that meet it NaN.
+ *   in a query or key, or an infinity in a query, makes the votes of the rows that meet it NaN.
  *   mass, mass_out : the same array, or two that do not overlap; 16-byte aligned
  *   decay  : finite; voters 0 .. 2^31 - 1; total_q * q_heads / kv_heads < 2^30 - 64
  *   q, dtype, q_heads, q_stride, scale, window, sinks : as in bitnet_kv4_attention

@@ -129,7 +129,7 @@ __device__ __forceinline__ void load_columns(const Kv4Attn& a, const Rows& r, in
       const int f = 24 - e, half = f / 2;
       Column c;
       c.a = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
-      c.b = __fmul_rn(c1, sum);
+      c.b = or_nan(__fmul_rn(c1, sum), top);
       c.p = there ? r.position(i) : -1;
       sh.col[col] = c;
       if (F32) sh.col[col + 1] = c;
@@ -657,7 +657,7 @@ __device__ __forceinline__ void load_slab(const Kv4Attn& a, const Rows& r, int64
       const int f = 24 - e, half = f / 2;
       const float ca = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
       const float aa = fminf(fmaxf(ca, kLeastA), kMostA), bb = __fmul_rn(__fmul_rn(sum, up), 5.9604644775390625e-8f);  // 2^-24
-      sl.ab[col] = make_float4(aa, aa, bb, bb);
+      sl.ab[col] = make_float4(aa, aa, or_nan(bb, top), or_nan(bb, top));
       sl.p[col] = row < rows ? r.position(row / a.share) : -1;
     }
   }

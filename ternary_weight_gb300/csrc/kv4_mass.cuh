@@ -50,6 +50,9 @@ __device__ __forceinline__ int seen(const Kv4Attn& a, int first, int last, int j
   if (j0 > last || ((int64_t)j0 + n - 1 <= (int64_t)first - a.window && j0 >= a.sinks)) return 0;
   return j0 + n - 1 <= first && (j0 > (int64_t)last - a.window || j0 + n - 1 < a.sinks) ? 2 : 1;
 }
+// A row's constant b, NaN where its largest magnitude (as bits) is none: an infinity's scores may all be -inf, which is what
+// tokens have that the row does not see.
+__device__ __forceinline__ float or_nan(float b, uint32_t top) { return top < 0x7f800000u ? b : __int_as_float(0x7fffffff); }
 constexpr float kLeastA = 7.888609052210118e-31f, kMostA = 3.4028234663852886e38f;  // 2^-100, the greatest
 __device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
   uint64_t r;

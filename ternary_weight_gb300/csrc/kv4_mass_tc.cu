@@ -186,7 +186,7 @@ __device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int 
       if (w == 0) {  // the row's constants begin with these
         float* ab = reinterpret_cast<float*>(&con.ab[in >> 1]) + (in & 1);
         ab[0] = __int_as_float(e);
-        ab[2] = __fmul_rn(sum, up);
+        ab[2] = or_nan(__fmul_rn(sum, up), top);
       }
     }
   }
