@@ -67,6 +67,9 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint4 a, uint32_t b0, u
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // What a column needs besides its fragments.
+// step a raw and base b stay below 2^116 in size. Where a is cut, scores that differ at all are infinitely far apart either way:
+// they are 2^-72 or more apart before the factor.
+constexpr float kMostFew = 1.2676506002282294e30f;  // 2^100
 struct Column {
   float a, b;  // x = step (a raw) + base b
   int p;       // the row's position
@@ -108,6 +111,7 @@ __device__ __forceinline__ void load_columns(const Kv4Attn& a, const Rows& r, in
     int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);
     e = e > 127 ? 127 : e < -113 ? -113 : e;
     const float up = __int_as_float((e + 127) << 23);
+    sum = row_sum<W>(x, sum, up, top);
     // words of lane quad t: W / 4 of them
     constexpr int WORDS = W / 4;
     const int t = w / WORDS, word = w % WORDS;
@@ -127,9 +131,10 @@ __device__ __forceinline__ void load_columns(const Kv4Attn& a, const Rows& r, in
       const float c1 = __fmul_rn(a.scale, kLog2e);
       // c1 2^(24 - e) in two steps: the power may pass fp32's range
       const int f = 24 - e, half = f / 2;
+      const float ca = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
       Column c;
-      c.a = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
-      c.b = or_nan(__fmul_rn(c1, sum), top);
+      c.a = copysignf(fminf(fabsf(ca), kMostFew), ca);
+      c.b = or_nan(__fmul_rn(c.a, __fmul_rn(sum, 5.9604644775390625e-8f)), top);  // 2^-24
       c.p = there ? r.position(i) : -1;
       sh.col[col] = c;
       if (F32) sh.col[col + 1] = c;
@@ -634,6 +639,7 @@ __device__ __forceinline__ void load_slab(const Kv4Attn& a, const Rows& r, int64
     int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);
     e = e > 127 ? 127 : e < -113 ? -113 : e;
     const float up = copysignf(__int_as_float((e + 127) << 23), a.scale);
+    sum = row_sum<W>(x[k], sum, up, top);
     constexpr int WORDS = W / 4;
     // where the row's numbers stand: fp32 queries have 8 rows in sixteen columns, their parts 8 apart
     const int t = w / WORDS, word = w % WORDS, at = k0 + k * PER, j = at / (16 / PARTS), in = at % (16 / PARTS);
@@ -656,7 +662,7 @@ __device__ __forceinline__ void load_slab(const Kv4Attn& a, const Rows& r, int64
       const float c1 = __fmul_rn(fabsf(a.scale), kLog2e);
       const int f = 24 - e, half = f / 2;
       const float ca = __fmul_rn(__fmul_rn(c1, __int_as_float((half + 127) << 23)), __int_as_float((f - half + 127) << 23));
-      const float aa = fminf(fmaxf(ca, kLeastA), kMostA), bb = __fmul_rn(__fmul_rn(sum, up), 5.9604644775390625e-8f);  // 2^-24
+      const float aa = fminf(fmaxf(ca, kLeastA), kMostA), bb = __fmul_rn(sum, 5.9604644775390625e-8f);  // 2^-24
       sl.ab[col] = make_float4(aa, aa, or_nan(bb, top), or_nan(bb, top));
       sl.p[col] = row < rows ? r.position(row / a.share) : -1;
     }

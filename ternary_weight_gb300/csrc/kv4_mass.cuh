@@ -50,6 +50,18 @@ __device__ __forceinline__ int seen(const Kv4Attn& a, int first, int last, int j
   if (j0 > last || ((int64_t)j0 + n - 1 <= (int64_t)first - a.window && j0 >= a.sinks)) return 0;
   return j0 + n - 1 <= first && (j0 > (int64_t)last - a.window || j0 + n - 1 < a.sinks) ? 2 : 1;
 }
+// The sum of a row's numbers at its power of two, from that of the bare ones (over the row's W lanes): where it might overflow they
+// are added up anew.
+template <int W>
+__device__ __forceinline__ float row_sum(const float (&x)[8], float sum, float up, uint32_t top) {
+  if (!__any_sync(0xffffffffu, top >= 0x7b800000u)) return sum * up;  // none of 2^120 or more
+  sum = 0.0f;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) sum += x[n] * up;
+#pragma unroll
+  for (int o = W / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
 // A row's constant b, NaN where its largest magnitude (as bits) is none: an infinity's scores may all be -inf, which is what
 // tokens have that the row does not see.
 __device__ __forceinline__ float or_nan(float b, uint32_t top) { return top < 0x7f800000u ? b : __int_as_float(0x7fffffff); }

@@ -162,6 +162,7 @@ __device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int 
       int e = top == 0 ? 0 : 14 - ((int)(top >> 23) - 127);
       e = e > 127 ? 127 : e < -113 ? -113 : e;
       const float up = copysignf(__int_as_float((e + 127) << 23), a.scale);
+      sum = row_sum<W>(x[k], sum, up, top);
 #pragma unroll
       for (int part = 0; part < (F32 ? 2 : 1); ++part) {
         uint32_t h[4];
@@ -186,7 +187,7 @@ __device__ __forceinline__ void load_block(const Kv4Attn& a, const Rows& r, int 
       if (w == 0) {  // the row's constants begin with these
         float* ab = reinterpret_cast<float*>(&con.ab[in >> 1]) + (in & 1);
         ab[0] = __int_as_float(e);
-        ab[2] = or_nan(__fmul_rn(sum, up), top);
+        ab[2] = or_nan(sum, top);
       }
     }
   }

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import kv4_reference as ref
 from test_kv4_mass import Mass, cuda_lib, gather, lib  # noqa: F401 (fixtures)
 from ternary_weight_gb300 import binding
 
@@ -40,3 +41,75 @@ def test_a_query_that_is_not_finite(cuda_lib, dim, dtype, form, what):
         if b == 1:
             want[:seen_by(w, 1, row), 1] = True
         assert np.array_equal(np.isnan(got[w.table[b][j // 64], :, j % 64]), want)
+
+
+def check_winners(w, q, share, scale, got):
+    """Scores so far apart that a row's vote goes to one token. Scores of the call are off by
+    e = scale (D + 16) 2^-23 max_j (step sum code |q| + |base| sum |q|) at most; a token whose score is 2 e + 64 below the greatest one
+    has less than exp(-64). Where only one is not, the row's whole vote is its; where more are, any of them may have it.
+    got: of a call with decay 0."""
+    got, q64, row = got.double().cpu().numpy(), q.double().cpu().numpy(), 0
+    sure_rows = 0
+    for b, n in enumerate(w.new):
+        j = np.arange(w.kv[b])
+        code, step, base = (x.astype(np.float64) for x in ref.quantise(w.k[b]))
+        step, base = step[..., None], base[..., None]
+        for h in range(w.heads):
+            least, most = np.zeros(w.kv[b]), np.zeros(w.kv[b])
+            for a in range(h * share, (h + 1) * share):
+                x = q64[row:row + n, a]
+                sees = j[None] <= np.arange(w.kv[b] - n, w.kv[b])[:, None]
+                s = np.where(sees, scale * x @ (step[:, h] * code[:, h] + base[:, h]).T, -np.inf)
+                size = (np.abs(x) @ (step[:, h] * code[:, h]).T + np.abs(x).sum(1, keepdims=True) * np.abs(base[:, h]).T) * sees
+                e = abs(scale) * (w.dim + 16) * 2.0 ** -23 * size.max(1, keepdims=True)
+                near = s >= s.max(1, keepdims=True) - 2 * e - 64
+                most += near.sum(0)
+                least += (near & (near.sum(1, keepdims=True) == 1)).sum(0)
+            have = got[w.table[b][j // 64], h, j % 64]
+            slack = n * share * ((w.kv[b] + n * share + 32) * 2.0 ** -23 + np.exp(-64.0))
+            assert (have >= least - slack).all() and (have <= most + slack).all()
+            assert abs(have.sum() - n * share) <= slack * 2  # its own sum over the tokens is off by their rounding too
+            sure_rows += least.sum()
+        row += n
+    assert sure_rows > sum(w.new) * w.heads * share / 2  # else the check says little
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (64, "f32"), (128, "bf16"), (128, "f32")])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("power,above", [(60, False), (118, False), (124, True), (125, False)])
+def test_queries_up_to_the_greatest_numbers(cuda_lib, dim, dtype, form, power, above):
+    """above: all numbers of a query above 0, so that their sum passes the range."""
+    new, kv = FORMS[form]
+    w = Mass(new, kv, 2, dim, dtype, seed=dim + power).fill()
+    mass, q = w.start(), w.queries(2, 1.0)
+    q = (q.abs() if above else q) * 2.0 ** power
+    assert bool(q.isfinite().all())
+    check_winners(w, q, 2, dim ** -0.5, gather(w, q, mass, decay=0.0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("scale,power", [(3e38, 0), (-3e38, 0), (-1e10, 3), (1e38, 30)])
+def test_the_greatest_scales(cuda_lib, dtype, form, scale, power):
+    new, kv = FORMS[form]
+    w = Mass(new, kv, 2, 64, dtype, seed=power + 5).fill()
+    mass, q = w.start(), w.queries(2, 2.0 ** power)
+    scale = float(np.float32(scale))
+    got = binding.kv4_attention_mass(w.cache, w.batch(new, kv), q, scale, mass, decay=0.0)
+    check_winners(w, q, 2, scale, got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("scale,power", [(-64 ** -0.5, 0), (0.0, 0), (-0.0, 0), (1e-38, 0), (2.0 ** 120, -122), (-2.0 ** 120, -122), (2.0 ** -122, 118), (1e-40, 0)])
+def test_scales_of_every_size_and_sign(cuda_lib, dtype, form, scale, power):
+    """With queries of such a size that many tokens have weight."""
+    new, kv = FORMS[form]
+    w = Mass(new, kv, 2, 64, dtype, seed=7).fill()
+    mass, q = w.start(), w.queries(2, 1.5 * 2.0 ** power)
+    scale = float(np.float32(scale))
+    got = binding.kv4_attention_mass(w.cache, w.batch(new, kv), q, scale, mass, decay=0.5)
+    w.check(got, q, 2, scale, 0.5)
