@@ -17,13 +17,13 @@
 //
 // Few columns (16 at most): of short sequences, and of many whose scores fit the shared memory of a cluster of up to eight
 // blocks, one kernel does it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the first kernel leaves the scores
-// in the workspace and the second starts behind it. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile.
+// in the workspace and the second starts behind it; where that would take more than 256 MB, the second makes them again. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile.
 // Measured (20 and 5 heads x 128): one query over 77 tokens 4.8 us, 64 over 87 to 8086 43.7 us (fp32 queries), one over 131007
 // 19.5 us (27.9 where the second kernel reads the keys again).
 //
 // More columns, up to 96 rows (kv4_mass_tc.cu has the others): blocks of 64 whose fragments the first kernel leaves in the
-// workspace; the second kernel's blocks keep their tiles' codes and go through a share of the columns, and a third one adds up
-// the shares. Bound by the products' latency and issue slots (tensor pipe 38% busy): 64 rows of 5 prompts of 1000 to 9000 tokens
+// workspace; the second kernel's blocks keep their tiles' codes and go through a share of the columns, and where these are more
+// than one a third adds up the shares. Bound by the products' latency and issue slots (tensor pipe 38% busy): 64 rows of 5 prompts of 1000 to 9000 tokens
 // each 33.7 us.
 #include <type_traits>
 
@@ -49,9 +49,9 @@ struct Plan {
 };
 struct Stats {
   float2* part;  // unit, block, chunk, column: (M, L)
-  float* votes;  // unit, group, share, WARPS x TILE
+  float* votes;  // unit, group, share, WARPS x TILE (more than one share)
   uint8_t* slabs;  // unit, block
-  float* scores;   // few columns: unit, row, token
+  float* scores;   // few columns: unit, row, token; null where they are not kept
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int unit = (int)(item / pl.chunks), chunk = (int)(item - (int64_t)unit * pl.chunks);
     const Rows r = rows_of(c, unit, voters, &bad);
-    const int rows = r.votes * a.share;
+    const int rows = r.votes * a.share, kept = st.scores ? rows : 0;
     if (rows == 0) continue;
     const int tile0 = chunk * pl.chunk, tile1 = min(tile0 + pl.chunk, (r.s.len + TILE - 1) / TILE);
     const int first = r.position(0), last = r.position(r.votes - 1);
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
             const int mt = v >> 1, h = v & 1, in = token_of(mt * 16 + h * 8 + g);
             x[v] = score(F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e], col, par[v]);
             if (masked && !visible(a, col.p, j0 + in)) x[v] = kNegInf;
-            if (row < rows) to[(int64_t)row * pl.tiles * TILE + in] = x[v];
+            if (row < kept) to[(int64_t)row * pl.tiles * TILE + in] = x[v];
           }
           const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m[n][e]), from = top == kNegInf ? 0.0f : top;
           l[n][e] = l[n][e] * exp2_approx(m[n][e] - from) + ((exp2_approx(x[0] - from) + exp2_approx(x[1] - from)) + (exp2_approx(x[2] - from) + exp2_approx(x[3] - from)));
@@ -289,11 +289,26 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_rows(Kv4 c,
 }
 
 // ------------------------------------------------------------- second kernel, few columns
+// The rows' M and 1 / L from the (M, L) of the chunks, a warp each.
+template <int NT, bool F32>
+__device__ __forceinline__ void join_chunks(const Plan& pl, const Stats& st, int unit, int chunks, int rows, float2* ml) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  for (int row = warp; row < rows; row += WARPS) {
+    float m = kNegInf, l = 0.0f;
+    for (int k = lane; k < chunks; k += 32) {
+      const float2 v = st.part[((int64_t)unit * pl.chunks + k) * (NT * 8) + row * (F32 ? 2 : 1)];
+      join(m, l, v.x, v.y);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+    if (lane == 0) ml[row] = make_float2(m == kNegInf ? 0.0f : m, l == 0.0f ? 0.0f : __frcp_rn(l));
+  }
+}
 // A thread a token; the scores are the first kernel's.
 template <int NT, bool F32>
 __global__ void __launch_bounds__(THREADS) kv4_mass_votes(Kv4 c, Kv4Attn a, Kv4Mass ms, Plan pl, Stats st) {
   __shared__ float2 ml[NT * 8];  // of the rows: M and 1 / L
-  constexpr int PARTS = F32 ? 2 : 1, AHEAD = 4, QUAD = 4;
+  constexpr int AHEAD = 4, QUAD = 4;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   bool bad = false;
   const int64_t items = (int64_t)c.batch * c.kv_heads * pl.chunks;
@@ -334,17 +349,7 @@ __global__ void __launch_bounds__(THREADS) kv4_mass_votes(Kv4 c, Kv4Attn a, Kv4M
     places(tile0 + warp);
     pdl_wait();
     load(tile0 + warp, 0);
-    // the rows' (M, L) from those of the chunks, a warp each
-    for (int row = warp; row < rows; row += WARPS) {
-      float m = kNegInf, l = 0.0f;
-      for (int k = lane; k < chunks; k += 32) {
-        const float2 v = st.part[((int64_t)unit * pl.chunks + k) * (NT * 8) + row * PARTS];
-        join(m, l, v.x, v.y);
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
-      if (lane == 0) ml[row] = make_float2(m == kNegInf ? 0.0f : m, l == 0.0f ? 0.0f : __frcp_rn(l));
-    }
+    join_chunks<NT, F32>(pl, st, unit, chunks, rows, ml);
     __syncthreads();
 #pragma unroll 1
     for (int tile = tile0 + warp; tile < tile1;) {
@@ -367,6 +372,84 @@ __global__ void __launch_bounds__(THREADS) kv4_mass_votes(Kv4 c, Kv4Attn a, Kv4M
       if (tile < tile1) places(tile), load(tile, 0);
     }
     __syncthreads();
+  }
+  pdl_wait();
+  if (bad) record_device_error(kErrRange);
+}
+
+// The same where the scores are not kept: made again by the first kernel's instructions, a warp a tile.
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) kv4_mass_again(Kv4 c, Kv4Attn a, Kv4Mass ms, Plan pl, Stats st) {
+  __shared__ Shared<D, NT> sh;
+  __shared__ float2 ml[NT * 8];
+  constexpr int PARTS = F32 ? 2 : 1, BLK = (int)kv4_block_bytes(D);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+  const int own = token_of((t >> 1) * 16 + (t & 1) * 8 + g);  // the token (of a tile) whose votes end up in this lane
+  bool bad = false;
+  const int64_t items = (int64_t)c.batch * c.kv_heads * pl.chunks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int unit = (int)(item / pl.chunks), chunk = (int)(item - (int64_t)unit * pl.chunks);
+    const Rows r = rows_of(c, unit, ms.voters, &bad);
+    const int rows = r.votes * a.share, all = (r.s.len + TILE - 1) / TILE;
+    const int tile0 = chunk * pl.chunk, tile1 = min(tile0 + pl.chunk, all);
+    if (rows == 0 || tile0 >= tile1) continue;
+    const int first = r.position(0), last = r.position(r.votes - 1), old = r.s.len - r.s.n;
+    // the blocks of this warp's tiles, one a lane (-1: not in the pool), and which of them the rows see any and all of
+    int id = -1, what = 0;
+    const int mine = tile0 + warp + lane * WARPS;
+    if (mine < tile1) {
+      const int page = c.page_table[(int64_t)r.b * c.max_pages + mine / 2];
+      if (page < 0 || page >= c.n_pages) bad = true;
+      else id = page * c.kv_heads + r.h, what = seen(a, first, last, mine * TILE, TILE);
+    }
+    const uint32_t any = __ballot_sync(0xffffffffu, what > 0), whole = __ballot_sync(0xffffffffu, what == 2);
+    Codes<D> cur;
+    const auto load = [&](int k) {
+      const int from = __shfl_sync(0xffffffffu, id, k);
+      if (from >= 0) cur.load(c.pages + (int64_t)from * BLK, tile0 + warp + k * WARPS, g, t);
+    };
+    load(0);
+    load_columns<D, NT, F32>(a, r, 0, sh);
+    pdl_wait();
+    join_chunks<NT, F32>(pl, st, unit, (all + pl.chunk - 1) / pl.chunk, rows, ml);
+    __syncthreads();
+    const int eights = min(NT, (rows * PARTS + 7) / 8);
+    for (int k = 0, tile = tile0 + warp; tile < tile1; ++k, tile += WARPS) {
+      const int from = __shfl_sync(0xffffffffu, id, k), j0 = tile * TILE, j = j0 + own;
+      const bool sees = any >> k & 1, masked = !(whole >> k & 1);
+      const bool write = from >= 0 && j < r.s.len && (ms.decay != 1.0f || ms.in != ms.out || j >= old || sees);
+      const int64_t at = (int64_t)from * kKvPage + j % kKvPage;
+      const float before = write && j < old ? ms.in[at] : 0.0f;
+      const float2 par[4] = {params(cur.par[0][0]), params(cur.par[0][1]), params(cur.par[1][0]), params(cur.par[1][1])};
+      float votes[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float d[2][4];
+        if (n < eights) products<D, NT>(cur, sh, n, lane, d);
+        if (n == NT - 1 && k < 31) load(k + 1);  // the codes' registers are free
+        if (n >= eights || !sees) continue;
+#pragma unroll
+        for (int e = 0; e < (F32 ? 1 : 2); ++e) {
+          const Column& col = sh.col[n * 8 + 2 * t + e];
+          if (col.p < 0) continue;  // no row, or one that sees nothing
+          const float2 of = ml[(n * 8 + 2 * t + e) / PARTS];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int mt = v >> 1, h = v & 1;
+            const float x = score(F32 ? d[mt][2 * h] + d[mt][2 * h + 1] : d[mt][2 * h + e], col, par[v]);
+            if (!masked || visible(a, col.p, j0 + token_of(mt * 16 + h * 8 + g))) votes[v] = fmaf(exp2_approx(x - of.x), of.y, votes[v]);
+          }
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        votes[v] += __shfl_xor_sync(0xffffffffu, votes[v], 1);
+        votes[v] += __shfl_xor_sync(0xffffffffu, votes[v], 2);
+      }
+      const float got = t == 0 ? votes[0] : t == 1 ? votes[1] : t == 2 ? votes[2] : votes[3];
+      if (write) ms.out[at] = j < old ? fmaf(ms.decay, before, got) : got;
+    }
+    __syncthreads();  // the next item's columns
   }
   pdl_wait();
   if (bad) record_device_error(kErrRange);
@@ -860,8 +943,9 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
     int block = next(share), buf = 0;
     Tile<D> k{};
     bool there = tile < all;
+    int id = 0;
     if (there) {
-      const int id = c.page_table[(int64_t)r.b * c.max_pages + tile / 2];
+      id = c.page_table[(int64_t)r.b * c.max_pages + tile / 2];
       if (id < 0 || id >= c.n_pages) bad = true, there = false;
       else k.load(c.pages + ((int64_t)id * c.kv_heads + r.h) * BLK, tile, g, t);
     }
@@ -921,7 +1005,13 @@ __global__ void __launch_bounds__(THREADS, 2) kv4_mass_shares(Kv4 c, Kv4Attn a, 
       for (int o = 4; o <= 16; o <<= 1) v.x += __shfl_xor_sync(0xffffffffu, v.x, o), v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
       if (g >> 1 == e) mine = g & 1 ? v.y : v.x;
     }
-    st.votes[((((int64_t)unit * pl.groups + group) * pl.shares + share) * WARPS + warp) * TILE + token_at(g >> 1, t, g & 1)] = mine;
+    const int in = token_at(g >> 1, t, g & 1), j = tile * TILE + in;
+    if (pl.shares > 1) {
+      st.votes[((((int64_t)unit * pl.groups + group) * pl.shares + share) * WARPS + warp) * TILE + in] = mine;
+    } else if (there && j < r.s.len) {
+      const int64_t at = ((int64_t)id * c.kv_heads + r.h) * kKvPage + j % kKvPage;
+      ms.out[at] = j < r.s.len - r.s.n ? fmaf(ms.decay, ms.in[at], mine) : mine;
+    }
     __syncthreads();
   }
   pdl_wait();
@@ -980,10 +1070,16 @@ Plan plan_of(const Kv4& c, int share, int voters, bool f32, int num_sms) {
 }
 int64_t part_bytes(const Kv4& c, const Plan& p) { return align256((int64_t)c.batch * c.kv_heads * p.blocks * p.chunks * p.nt * 8 * 8); }
 int64_t votes_bytes(const Kv4& c, const Plan& p) {
-  return p.shares ? align256((int64_t)c.batch * c.kv_heads * p.groups * p.shares * WARPS * TILE * 4) : 0;
+  return p.shares > 1 ? align256((int64_t)c.batch * c.kv_heads * p.groups * p.shares * WARPS * TILE * 4) : 0;
 }
+// Scores are kept while the batch's sizes leave room for no more than this: a pool of caches should not need a call's workspace of
+// its own size. Beyond it they are made again. Measured, us, kept and made again (5 heads x 128): 4 rows, 2 x 131007 tokens (21
+// MB) 33.6, 44.8; 16 x 131007 (168 MB) 218, 298; 64 x 131007 (671 MB) 810, 1087; 64 x 1000 with room for 131072 (671 MB) 32.0,
+// 38.7; 16 rows, 16 x 131007 (671 MB) 448, 536.
+constexpr int64_t kScoresMost = 256 << 20;
 int64_t scores_bytes(const Kv4& c, const Plan& p, int share) {
-  return p.shares ? 0 : align256((int64_t)c.batch * c.kv_heads * p.votes * share * p.tiles * TILE * 4);
+  const int64_t bytes = p.shares ? 0 : align256((int64_t)c.batch * c.kv_heads * p.votes * share * p.tiles * TILE * 4);
+  return bytes > kScoresMost ? 0 : bytes;
 }
 int64_t slabs_bytes(const Kv4& c, const Plan& p, int dim) {
   return p.shares ? align256((int64_t)c.batch * c.kv_heads * p.blocks * (int64_t)(dim == 128 ? sizeof(Slab<128>) : sizeof(Slab<64>))) : 0;
@@ -1027,6 +1123,7 @@ cudaError_t launch_few(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const P
   const int64_t units = (int64_t)c.batch * c.kv_heads;
   kv4_mass_rows<D, NT, F32><<<grid_of(units * p.chunks), THREADS, 0, st>>>(c, a, m.voters, p, s);
   if (cudaError_t e = cudaGetLastError()) return e;
+  if (!s.scores) return launch_behind(kv4_mass_again<D, NT, F32>, grid_of(units * p.chunks), THREADS, 0, st, c, a, m, p, s);
   return launch_behind(kv4_mass_votes<NT, F32>, grid_of(units * p.chunks), THREADS, 0, st, c, a, m, p, s);
 }
 template <int D, bool F32>
@@ -1041,7 +1138,7 @@ cudaError_t launch_many(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const 
   if (p.chunks > 1)
     if (cudaError_t e = launch_behind(kv4_mass_sums<D>, grid_of(units * p.blocks), COLS, 0, st, c, a, m.voters, p, s)) return e;
   if (cudaError_t e = launch_behind(kv4_mass_shares<D, F32>, grid_of(units * p.groups * p.shares), THREADS, shares_smem, st, c, a, m, p, s)) return e;
-  return launch_behind(kv4_mass_join, grid_of(units * p.groups), THREADS, 0, st, c, m, p, s);
+  return p.shares > 1 ? launch_behind(kv4_mass_join, grid_of(units * p.groups), THREADS, 0, st, c, m, p, s) : cudaSuccess;
 }
 template <int D, bool F32>
 cudaError_t by_columns(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, const Stats& s, cudaStream_t st) {
@@ -1075,7 +1172,7 @@ cudaError_t launch_kv4_mass(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Ma
   const Plan p = plan_of(c, a.share, m.voters, !a.bf16, 152);
   uint8_t* at = static_cast<uint8_t*>(ws);
   const Stats s{reinterpret_cast<float2*>(at), reinterpret_cast<float*>(at + part_bytes(c, p)), at + part_bytes(c, p) + votes_bytes(c, p),
-                reinterpret_cast<float*>(at + part_bytes(c, p))};
+                scores_bytes(c, p, a.share) ? reinterpret_cast<float*>(at + part_bytes(c, p)) : nullptr};
   if (dim == 128) return a.bf16 ? by_columns<128, false>(c, a, m, p, s, st) : by_columns<128, true>(c, a, m, p, s, st);
   return a.bf16 ? by_columns<64, false>(c, a, m, p, s, st) : by_columns<64, true>(c, a, m, p, s, st);
 }

@@ -1,16 +1,30 @@
 """The attention weight that cached tokens gather, at the ends of the numbers' ranges, in every form that the call takes: a
-cluster a sequence and head (up to 16 columns), two kernels (the same, longer), blocks of 64 columns (up to 96 rows), blocks of
-128 rows."""
+cluster a sequence and head (up to 16 columns), two kernels (the same, longer), two that make the scores twice (the same, of
+batches with room for very many tokens), blocks of 64 columns (up to 96 rows), blocks of 128 rows."""
 import numpy as np
 import pytest
 import torch
 
 import kv4_reference as ref
-from test_kv4_mass import Mass, cuda_lib, gather, lib  # noqa: F401 (fixtures)
+from test_kv4_mass import Mass, cuda_lib, lib  # noqa: F401 (fixtures)
 from ternary_weight_gb300 import binding
 
 # new tokens and cached ones of each sequence: query heads that share a key/value head are two
-FORMS = {"cluster": ([1, 3], [77, 130]), "two kernels": ([1, 3], [900, 1500]), "64 columns": ([20, 33], [77, 1500]), "128 rows": ([70, 130], [90, 1500])}
+ROOM = 1 << 25
+FORMS = {"cluster": ([1, 3], [77, 130]), "two kernels": ([1, 3], [900, 1500]), "scores twice": ([1, 3], [900, 1501]), "64 columns": ([20, 33], [77, 1500]), "128 rows": ([70, 130], [90, 1500])}
+
+
+def batch_of(w, form):
+    if form != "scores twice":
+        return w.batch(w.new, w.kv)
+    table = torch.full((len(w.kv), ROOM // 64), -7, dtype=torch.int32, device="cuda")
+    table[:, :w.wide] = torch.tensor(w.table)
+    b = w.batch(w.new, w.kv)
+    return binding.KV4Batch(b.cu_q, b.kv_len, table, sum(w.new), max(w.new), ROOM)
+
+
+def gather(w, form, q, mass, scale=None, **kw):
+    return binding.kv4_attention_mass(w.cache, batch_of(w, form), q, w.dim ** -0.5 if scale is None else scale, mass, **kw)
 
 
 def seen_by(w, b, row):
@@ -34,7 +48,7 @@ def test_a_query_that_is_not_finite(cuda_lib, dim, dtype, form, what):
     mass, q = w.start(), w.queries(2)
     row = new[1] - 2  # of sequence 1
     q[new[0] + row, 3, 5] = what
-    got = gather(w, q, mass).cpu().numpy()
+    got = gather(w, form, q, mass).cpu().numpy()
     for b in range(2):
         j = np.arange(kv[b])
         want = np.zeros((kv[b], 2), bool)
@@ -85,7 +99,7 @@ def test_queries_up_to_the_greatest_numbers(cuda_lib, dim, dtype, form, power, a
     mass, q = w.start(), w.queries(2, 1.0)
     q = (q.abs() if above else q) * 2.0 ** power
     assert bool(q.isfinite().all())
-    check_winners(w, q, 2, dim ** -0.5, gather(w, q, mass, decay=0.0))
+    check_winners(w, q, 2, dim ** -0.5, gather(w, form, q, mass, decay=0.0))
 
 
 @pytest.mark.gpu
@@ -97,7 +111,7 @@ def test_the_greatest_scales(cuda_lib, dtype, form, scale, power):
     w = Mass(new, kv, 2, 64, dtype, seed=power + 5).fill()
     mass, q = w.start(), w.queries(2, 2.0 ** power)
     scale = float(np.float32(scale))
-    got = binding.kv4_attention_mass(w.cache, w.batch(new, kv), q, scale, mass, decay=0.0)
+    got = gather(w, form, q, mass, scale, decay=0.0)
     check_winners(w, q, 2, scale, got)
 
 
@@ -111,5 +125,5 @@ def test_scales_of_every_size_and_sign(cuda_lib, dtype, form, scale, power):
     w = Mass(new, kv, 2, 64, dtype, seed=7).fill()
     mass, q = w.start(), w.queries(2, 1.5 * 2.0 ** power)
     scale = float(np.float32(scale))
-    got = binding.kv4_attention_mass(w.cache, w.batch(new, kv), q, scale, mass, decay=0.5)
+    got = gather(w, form, q, mass, scale, decay=0.5)
     w.check(got, q, 2, scale, 0.5)
