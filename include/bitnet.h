@@ -500,7 +500,10 @@ BITNET_API int bitnet_kv4_attention(const bitnet_kv4_cache *cache, const bitnet_
  *   q, dtype, q_heads, q_stride, scale, window, sinks : as in bitnet_kv4_attention
  *   workspace : device, 256-byte aligned, at least bitnet_kv4_attention_mass_workspace_size bytes (for the same
  *            cache, batch sizes, q_heads and voters). Needs no initialisation; calls that may run at the same
- *            time need one each.
+ *            time need one each. With up to 16 voting rows a key/value head (its query heads counted) some 256 MB
+ *            at most; with more, these rows lie there in blocks of 128 (70 KB with D = 128), one at least for each
+ *            sequence and key/value head
+ * A cu_q that falls anywhere makes no result of the call valid (the workspace's places go by it).
  * The masses of a page that two sequences of the batch share are not defined afterwards; all others are the same bits
  * each time the call is made with the same arguments.
  *

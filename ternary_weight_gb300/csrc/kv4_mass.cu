@@ -1155,7 +1155,7 @@ int64_t kv4_mass_ws_bytes(const Kv4& c, int dim, int q_heads, int voters) {
   for (int f32 = 0; f32 < 2; ++f32) {
     const int64_t rows = rows_of_plan(c, q_heads / c.kv_heads, voters);
     if (mass_on_tc(rows, f32 != 0)) {
-      const int64_t n = kv4_mass_tc_ws_bytes(c, dim, rows, f32 != 0);
+      const int64_t n = kv4_mass_tc_ws_bytes(c, dim, q_heads / c.kv_heads, rows, f32 != 0);
       most = n > most ? n : most;
       continue;
     }

@@ -127,7 +127,7 @@ __device__ __forceinline__ void join_u(float a, float& m, float& l, float m2, fl
 // tokens, 20 and 5 heads x 128, m16n8k16 and tcgen05: bf16 queries 64 rows 33.7, 50.5; 96 rows 48.5, 51.7; 128 rows 56.4, 52.9;
 // 256 rows 91, 63.8; fp32 queries 64 rows 53.0, 62.0; 68 rows 58.2, 63.1; 96 rows 67.1, 63.2; 256 rows 136, 97.9.
 inline bool mass_on_tc(int64_t rows, bool f32) { return rows > (f32 ? 80 : 96); }
-int64_t kv4_mass_tc_ws_bytes(const Kv4& c, int dim, int64_t rows, bool f32);
+int64_t kv4_mass_tc_ws_bytes(const Kv4& c, int dim, int share, int64_t rows, bool f32);
 cudaError_t launch_kv4_mass_tc(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, int64_t rows, void* ws, cudaStream_t stream);
 
 }  // namespace bitnet

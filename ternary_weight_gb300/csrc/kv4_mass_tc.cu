@@ -28,7 +28,14 @@ constexpr int TOK = 128, ROWS = 128;
 
 struct Plan {
   int blocks, tiles, chunk, chunks, shares;
+  int64_t room;  // places for a head's blocks of rows, all sequences' together; 0: a place for each unit and block
 };
+// Where a block of rows lies in the workspace. Sequences that have far fewer rows than the longest lie one behind another: those of the
+// packed rows [q0, q0 + n) take ceil(n share / ROWS) places at most, from floor(q0 share / ROWS) + b on, which is up to where the
+// next one's begin.
+__device__ __forceinline__ int64_t place_of(const Plan& pl, const Rows& r, int unit, int share, int block) {
+  return (pl.room ? r.h * pl.room + (int64_t)r.s.q0 * share / ROWS + r.b : (int64_t)unit * pl.blocks) + block;
+}
 // What the second kernel needs of a block's rows, in pairs.
 struct Constants {
   float4 ab[ROWS / 2];  // a0, a1, b0, b1
@@ -271,13 +278,13 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
   const int units = c.batch * c.kv_heads;
   const int64_t items = (int64_t)units * pl.blocks * pl.chunks;
   for (int64_t at = blockIdx.x; at < items; at += gridDim.x) {
-    const int64_t place = at / pl.chunks;
-    const int chunk = (int)(at - place * pl.chunks), behind = (int)(place / units), unit = (int)(place - (int64_t)behind * units);
+    const int64_t rest = at / pl.chunks;
+    const int chunk = (int)(at - rest * pl.chunks), behind = (int)(rest / units), unit = (int)(rest - (int64_t)behind * units);
     const int block = pl.blocks - 1 - behind;
-    const int64_t rest = (int64_t)unit * pl.blocks + block, item = rest * pl.chunks + chunk;
     const Rows r = rows_of(c, unit, voters, &bad);
     const int rows = r.votes * a.share, row0 = block * ROWS;
     if (row0 >= rows) continue;
+    const int64_t place = place_of(pl, r, unit, a.share, block), item = place * pl.chunks + chunk;
     const int t0 = chunk * pl.chunk, t1 = min(t0 + pl.chunk, (r.s.len + TOK - 1) / TOK), pages = (r.s.len + kKvPage - 1) / kKvPage;
     int first, last;
     ends_of(a, r, row0, &first, &last);
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_ro
     }
     __syncthreads();
     if (chunk == 0) {
-      uint4* to = reinterpret_cast<uint4*>(blocks + rest * (int64_t)S::BLOCK);
+      uint4* to = reinterpret_cast<uint4*>(blocks + place * (int64_t)S::BLOCK);
       for (int i = threadIdx.x; i < S::BLOCK / 16; i += THREADS) to[i] = reinterpret_cast<const uint4*>(smem)[i];
     }
     __syncthreads();  // the next item's queries
@@ -432,12 +439,13 @@ __global__ void __launch_bounds__(ROWS) kv4_mass_tc_sums(Kv4 c, Kv4Attn a, int v
     bool bad = false;
     const Rows r = rows_of(c, unit, voters, &bad);
     if (block * ROWS >= r.votes * a.share) continue;
-    Constants& con = *reinterpret_cast<Constants*>(blocks + item * (int64_t)S::BLOCK + S::IMAGE * S::PARTS);
+    const int64_t place = place_of(pl, r, unit, a.share, block);
+    Constants& con = *reinterpret_cast<Constants*>(blocks + place * (int64_t)S::BLOCK + S::IMAGE * S::PARTS);
     const int chunks = ((r.s.len + TOK - 1) / TOK + pl.chunk - 1) / pl.chunk;
     const float aa = reinterpret_cast<const float*>(&con.ab[row >> 1])[row & 1];
     float m = kNegInf, l = 0.0f;
     for (int k = 0; k < chunks; ++k) {
-      const float2 v = part[(item * pl.chunks + k) * ROWS + row];
+      const float2 v = part[(place * pl.chunks + k) * ROWS + row];
       join_u(aa, m, l, v.x, v.y);
     }
     const bool none = con.seen[row].x < 0 || m == kNegInf;
@@ -494,10 +502,11 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
         return seen(a, first, last, tile * TOK, TOK);
       });
     };
+    const int64_t place0 = place_of(pl, r, unit, a.share, share);
     // a block's copy: its queries to buffer copied & 1, its constants to place copied % 3
     const auto copy = [&](int k) {
       if (threadIdx.x == 0) {
-        const uint8_t* from = blocks + ((int64_t)unit * pl.blocks + share + k * pl.shares) * (int64_t)S::BLOCK;
+        const uint8_t* from = blocks + (place0 + k * pl.shares) * (int64_t)S::BLOCK;
         uint64_t* bar = &full[copied & 1];
         mbar_arrive_expect_tx(bar, S::BLOCK);
         bulk_copy_g2s(smem + QUERIES + (copied & 1) * S::IMAGE * S::PARTS, from, S::IMAGE * S::PARTS, bar);
@@ -639,7 +648,7 @@ constexpr int kSms = 152;
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 unsigned grid_of(int64_t items, int64_t most) { return (unsigned)(items < most ? items : most); }
 
-Plan plan_of(const Kv4& c, int64_t rows) {
+Plan plan_of(const Kv4& c, int share, int64_t rows) {
   Plan p{};
   const int64_t units = (int64_t)c.batch * c.kv_heads;
   p.blocks = (int)((rows + ROWS - 1) / ROWS);
@@ -654,11 +663,14 @@ Plan plan_of(const Kv4& c, int64_t rows) {
   p.chunks = (p.tiles + p.chunk - 1) / p.chunk;
   const int64_t all = units * (p.tiles ? p.tiles : 1), s = (kSms * 4 + all - 1) / all;
   p.shares = (int)(s > p.blocks ? p.blocks : s);
+  const int64_t room = (int64_t)c.total_q * share / ROWS + c.batch;
+  p.room = room < (int64_t)c.batch * p.blocks ? room : 0;
   return p;
 }
+int64_t places(const Kv4& c, const Plan& p) { return p.room ? c.kv_heads * p.room : (int64_t)c.batch * c.kv_heads * p.blocks; }
 int64_t block_bytes(int dim, bool f32) { return (int64_t)128 * dim * 2 * (f32 ? 2 : 1) + (int64_t)sizeof(Constants); }
-int64_t blocks_bytes(const Kv4& c, const Plan& p, int dim, bool f32) { return align256((int64_t)c.batch * c.kv_heads * p.blocks * block_bytes(dim, f32)); }
-int64_t part_bytes(const Kv4& c, const Plan& p) { return align256((int64_t)c.batch * c.kv_heads * p.blocks * p.chunks * ROWS * 8); }
+int64_t blocks_bytes(const Kv4& c, const Plan& p, int dim, bool f32) { return align256(places(c, p) * block_bytes(dim, f32)); }
+int64_t part_bytes(const Kv4& c, const Plan& p) { return align256(places(c, p) * p.chunks * ROWS * 8); }
 
 template <int D, bool F32>
 cudaError_t launch(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan& p, uint8_t* ws, cudaStream_t st) {
@@ -683,12 +695,13 @@ cudaError_t launch(const Kv4& c, const Kv4Attn& a, const Kv4Mass& m, const Plan&
 
 }  // namespace
 
-int64_t kv4_mass_tc_ws_bytes(const Kv4& c, int dim, int64_t rows, bool f32) {
-  const Plan p = plan_of(c, rows);
-  return blocks_bytes(c, p, dim, f32) + part_bytes(c, p) + align256((int64_t)c.batch * c.kv_heads * p.tiles * p.shares * TOK * 4);
+int64_t kv4_mass_tc_ws_bytes(const Kv4& c, int dim, int share, int64_t rows, bool f32) {
+  const Plan p = plan_of(c, share, rows);
+  const int64_t shares = p.shares > 1 ? align256((int64_t)c.batch * c.kv_heads * p.tiles * p.shares * TOK * 4) : 0;
+  return blocks_bytes(c, p, dim, f32) + part_bytes(c, p) + shares;
 }
 cudaError_t launch_kv4_mass_tc(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, int64_t rows, void* ws, cudaStream_t st) {
-  const Plan p = plan_of(c, rows);
+  const Plan p = plan_of(c, a.share, rows);
   uint8_t* at = static_cast<uint8_t*>(ws);
   if (dim == 128) return a.bf16 ? launch<128, false>(c, a, m, p, at, st) : launch<128, true>(c, a, m, p, at, st);
   return a.bf16 ? launch<64, false>(c, a, m, p, at, st) : launch<64, true>(c, a, m, p, at, st);

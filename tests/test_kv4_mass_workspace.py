@@ -35,6 +35,16 @@ def test_many_columns_of_long_caches(lib, n, share):  # noqa: F811
         assert 0 <= size_of(lib, sequences, n * sequences, n, 131072, share) <= 32 * MB + sequences * 5 * blocks * 32768
 
 
+@pytest.mark.parametrize("prompts,share,voters", [([2048], 4, 0), ([9000, 3], 4, 0), ([500] * 4, 8, 0), ([9000, 700], 4, 64), ([31], 4, 0)])
+@pytest.mark.parametrize("steps", [0, 63, 1000])
+def test_prompts_beside_single_tokens(lib, prompts, share, voters, steps):  # noqa: F811
+    """More than 96 rows of the longest: every sequence and head has blocks of 128 rows for its own rows, each of 67 KB (3 KB of them
+    constants) with 1 KB for each 2048 cached tokens. Votes that are shared out over blocks are few."""
+    new = prompts + [1] * steps
+    blocks = min(sum(new) * share // 128 + len(new), len(new) * -(-min(max(new), voters or max(new)) * share // 128))
+    assert 0 < size_of(lib, len(new), sum(new), max(new), 8192 if max(new) < 8192 else 9024, share, voters=voters) <= 5 * blocks * 72 * 1024 + 8 * MB
+
+
 def with_room(w, room):
     b = w.batch(w.new, w.kv)
     table = torch.full((len(w.kv), room // 64), -7, dtype=torch.int32, device="cuda")
@@ -92,3 +102,32 @@ def test_scores_made_twice_of_bad_pages(cuda_lib, entry):  # noqa: F811
     mine = torch.ones(w.n_pages, dtype=torch.bool)
     mine[own] = False
     assert torch.equal(got[mine].nan_to_num(9.0), want[mine].nan_to_num(9.0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,dtype,share", [(128, "bf16", 4), (128, "f32", 4), (64, "bf16", 3), (64, "f32", 32)])
+@pytest.mark.parametrize("new,kv,voters", [([300] + [1] * 12 + [0, 130, 7], [300] + [40 * i + 1 for i in range(12)] + [20, 2500, 600], 0),
+                                           ([1] * 9 + [700], [64 * i + 9 for i in range(9)] + [900], 0),
+                                           ([0, 1, 400, 0, 350, 1, 0, 1, 1, 1], [5, 1, 3000, 70, 350, 90, 0, 64, 65, 2], 200)])
+def test_sequences_of_unlike_rows(cuda_lib, dim, dtype, share, new, kv, voters):  # noqa: F811
+    """Their blocks lie one behind another in the workspace; what it held before is not looked at."""
+    w = Mass(new, kv, 2, dim, dtype, seed=sum(kv)).fill()
+    mass, q, b = w.start(), w.queries(share), w.batch(new, kv)
+    ws = torch.empty(binding.kv4_attention_mass_workspace_size(w.cache, b, 2 * share, voters), dtype=torch.uint8, device="cuda").fill_(255)
+    got = binding.kv4_attention_mass(w.cache, b, q, dim ** -0.5, mass, decay=0.5, window=0, voters=voters, workspace=ws)
+    w.check(got, q, share, dim ** -0.5, 0.5, voters=voters)
+
+
+@pytest.mark.gpu
+def test_a_batch_whose_rows_fall_is_reported(cuda_lib):  # noqa: F811
+    """Nothing outside the cached tokens' masses is written."""
+    w = Mass([300, 1, 1, 1, 100], [300, 60, 60, 60, 200], 2, 64, "bf16", seed=3).fill()
+    mass, q, b = w.start(), w.queries(4), w.batch(w.new, w.kv)
+    b.cu_q.copy_(torch.tensor([0, 300, 120, 500, -9, 403], dtype=torch.int32))
+    got = binding.kv4_attention_mass(w.cache, b, q, 0.125, mass.clone())
+    assert binding.last_device_error() == binding.BITNET_ERANGE
+    used = torch.zeros_like(mass, dtype=torch.bool)
+    for s, n in enumerate(w.kv):
+        j = torch.arange(n)
+        used[torch.tensor(w.table[s])[j // 64].long().cuda(), :, (j % 64).cuda()] = True
+    assert torch.equal(got[~used].nan_to_num(9.0), mass[~used].nan_to_num(9.0))
