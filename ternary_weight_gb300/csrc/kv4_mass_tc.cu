@@ -505,14 +505,14 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
     const int64_t place0 = place_of(pl, r, unit, a.share, share);
     // a block's copy: its queries to buffer copied & 1, its constants to place copied % 3
     const auto copy = [&](int k) {
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && !abort) {  // after a wait that gave up the last ones may still be under way
         const uint8_t* from = blocks + (place0 + k * pl.shares) * (int64_t)S::BLOCK;
         uint64_t* bar = &full[copied & 1];
         mbar_arrive_expect_tx(bar, S::BLOCK);
         bulk_copy_g2s(smem + QUERIES + (copied & 1) * S::IMAGE * S::PARTS, from, S::IMAGE * S::PARTS, bar);
         bulk_copy_g2s(smem + CONS + (copied % 3) * S::CON, from + S::IMAGE * S::PARTS, (uint32_t)sizeof(Constants), bar);
       }
-      ++copied;
+      copied += !abort;
     };
     const auto page_of = [&](int in) {
       const int page = tile * 2 + (in >> 6);
@@ -614,6 +614,13 @@ __global__ void __launch_bounds__(THREADS, Shape<D, F32>::BLOCKS) kv4_mass_tc_vo
   }
   pdl_wait();
   if (warp == 0) {
+    if (abort) {  // a wait gave up: the copies that it may have left under way end before the shared memory is given back
+      for (uint32_t i = 0; i < 2; ++i) {
+        const uint32_t to = (copied + 1 - i) >> 1;  // copies to buffer i
+        bool late = false;
+        if (to) mbar_wait_warp(&full[i], (to - 1) & 1, &late);
+      }
+    }
     if (elect_one()) mma_commit(&all_done);
     __syncwarp();
     abort = false;
