@@ -70,7 +70,8 @@ class Decoder:
             self.blocks.append(make_block(cache, hidden, q_heads, seed + 10 * i, window, sinks, rope=rope, mass=mass, voters=self.VOTERS))
         self.kv_len = torch.tensor(self.prompts, dtype=torch.int32, device=device)
         n = len(self.prompts)
-        self.positions = self.kv_len - 1  # of each sequence's last token
+        # of each sequence's last token, where a step needs them or its cache forgets them
+        self.positions = self.kv_len - 1 if rope is not None or budget else None
         self.head = self.logits = self.tokens = None
         if vocab:
             w = torch.randn(vocab, hidden, generator=torch.Generator().manual_seed(seed)) * hidden ** -0.5
@@ -85,7 +86,7 @@ class Decoder:
 
     def _layers(self, x, batch, positions):
         for block in self.blocks:
-            x = block.run(x, batch, positions=positions if self.rope is not None else None)
+            x = block.run(x, batch, positions=positions)
         if self.budget:  # the layers share their lengths: the last one writes the new ones
             for block in self.blocks:
                 block.evict(batch, self.budget, self.limit, sinks=min(4, self.budget - self.budget // 4), recent=self.budget // 4,
@@ -102,7 +103,9 @@ class Decoder:
         ends = torch.tensor([0] + self.prompts).cumsum(0)
         batch = binding.KV4Batch(ends.to(torch.int32).to(x.device), self.kv_len, self.table, int(ends[-1]),
                                  max(self.prompts), self.most)
-        positions = torch.cat([torch.arange(n, dtype=torch.int32) for n in self.prompts]).to(x.device)
+        positions = None
+        if self.rope is not None:
+            positions = torch.cat([torch.arange(n, dtype=torch.int32) for n in self.prompts]).to(x.device)
         y = self._layers(x, batch, positions)
         self.x.copy_(y[(ends[1:] - 1).to(x.device)])
         self._answer()
@@ -110,8 +113,9 @@ class Decoder:
 
     def _step(self):
         self.kv_len += 1
-        self.positions += 1
-        self.x.copy_(self._layers(self.x, self.one, self.positions))
+        if self.positions is not None:
+            self.positions += 1
+        self.x.copy_(self._layers(self.x, self.one, self.positions if self.rope is not None else None))
         self._answer()
 
     def step(self):
@@ -123,7 +127,8 @@ class Decoder:
             # everything has to have run once before a capture: a step whose effects are taken back (the
             # places that it writes are written again by the step after it; where steps gather weight and cut, that
             # is caches and masses whole)
-            state = [self.kv_len, self.x, self.positions] + ([b.cache.pages for b in self.blocks] + [b.mass for b in self.blocks] if self.budget else [])
+            state = [self.kv_len, self.x] + ([self.positions] if self.positions is not None else [])
+            state += [b.cache.pages for b in self.blocks] + [b.mass for b in self.blocks] if self.budget else []
             keep = [t.clone() for t in state]
             s = torch.cuda.Stream(device=self.x.device)
             s.wait_stream(torch.cuda.current_stream(self.x.device))
