@@ -588,7 +588,8 @@ typedef struct bitnet_rope_table {
  *               read); row r begins at q + r * q_stride (elements), its heads lie one after another.
  *               kv_heads may be 0 (k and k_out are then ignored)
  *   q_out, k_out : the same, written. Each is either its input (the same pointer and stride) or memory
- *               that overlaps neither input nor the other output
+ *               that overlaps neither input nor the other output. Operands of one stride may lie in slices of
+ *               the same rows; those of two strides lie apart as a whole
  *   head_dim  : a multiple of 8, 8 .. 1024; rows 0 .. 2^31 - 1; q_heads 1 .. 2^17, kv_heads 0 .. 2^17
  *   All 16-byte aligned (positions 4), strides >= heads * head_dim, at most 2^26, multiples of 16 bytes.
  * Angles are exact to 2^-24 half turns at any position; the turn is computed in fp32 (each product and

@@ -662,6 +662,16 @@ int check_rope_rows(const void* in, int64_t in_stride, const void* out, int64_t 
   if (in == out && in_stride != out_stride) return BITNET_EINVAL;
   return aligned(in, 16) && aligned(out, 16) ? BITNET_OK : BITNET_EALIGN;
 }
+// Whether two operands' rows share bytes. Rows of one stride may lie between each other's (slices of a fused row); those of two
+// strides have to lie apart as a whole.
+bool rows_overlap(const void* a, int64_t a_stride, int64_t a_bytes, const void* b, int64_t b_stride, int64_t b_bytes, int64_t rows) {
+  const int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a));
+  if (d >= (rows - 1) * a_stride + a_bytes || -d >= (rows - 1) * b_stride + b_bytes) return false;
+  if (rows == 1 || a_stride != b_stride) return true;
+  // row i of b begins d - k stride beyond row i + k of a
+  const int64_t k = d >= 0 ? d / a_stride : -((-d + a_stride - 1) / a_stride), beyond = d - k * a_stride;
+  return (k > -rows && k < rows && beyond < a_bytes) || (k + 1 > -rows && k + 1 < rows && a_stride - beyond < b_bytes);
+}
 }  // namespace
 
 BITNET_API int bitnet_rope_turns(int64_t dims, double base, int scaling, double factor, double original, double low,
@@ -718,6 +728,16 @@ BITNET_API int bitnet_rope(const bitnet_rope_table* table, const int32_t* positi
   if (int st = check_rope_rows(q, q_stride, q_out, q_out_stride, q_heads * head_dim, eb)) return st;
   if (kv_heads)
     if (int st = check_rope_rows(k, k_stride, k_out, k_out_stride, kv_heads * head_dim, eb)) return st;
+  if (rows > 0) {  // what is written over another operand, other than in place
+    const int64_t qb = q_heads * head_dim * eb, kb = kv_heads * head_dim * eb;
+    const auto over = [&](const void* a, int64_t as, int64_t ab, const void* b, int64_t bs, int64_t bb) {
+      return rows_overlap(a, as * eb, ab, b, bs * eb, bb, rows);
+    };
+    if (q_out != q && over(q_out, q_out_stride, qb, q, q_stride, qb)) return BITNET_EINVAL;
+    if (kv_heads && ((k_out != k && over(k_out, k_out_stride, kb, k, k_stride, kb)) || over(q_out, q_out_stride, qb, k, k_stride, kb) ||
+                     over(k_out, k_out_stride, kb, q, q_stride, qb) || over(q_out, q_out_stride, qb, k_out, k_out_stride, kb)))
+      return BITNET_EINVAL;
+  }
   if (!aligned(table->turns, 8) || !aligned(positions, 4)) return BITNET_EALIGN;
   if (rows == 0) return BITNET_OK;
   int sms = 0;
