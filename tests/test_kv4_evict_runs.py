@@ -114,3 +114,27 @@ def test_bad_pages_in_long_runs_stay_inside(cuda_lib):
     mine = np.zeros(w.n_pages, bool)
     mine[w.table[0]] = True
     assert got[2] == want[2] and np.array_equal(got[0][~mine], want[0][~mine]) and np.array_equal(got[1][~mine], want[1][~mine])
+
+
+def check(w, *args):
+    want = w.expect(*args)
+    got = w.call(*args)
+    assert got[2] == want[2] and np.array_equal(got[1].view(np.uint32), want[1].view(np.uint32)) and np.array_equal(got[0], want[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["any", "equal", "few values"])
+@pytest.mark.parametrize("other", [False, True])
+@pytest.mark.parametrize("budget,sinks,recent", [(300, 4, 60), (20900, 0, 20000)])
+def test_runs_longer_than_shared_memory(cuda_lib, kind, other, budget, sinks, recent):
+    w = Pool(LONG, 5, 64, seed=budget, kind=kind, spare=len(LONG) * -(-budget // 64) if other else 0)
+    check(w, budget, sinks, recent, w.into(-(-budget // 64)) if other else None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["any", "equal"])
+@pytest.mark.parametrize("dim,heads,kv,budget,sinks,recent", [(128, 2, [9000, 100], 2100, 4, 256), (64, 1, [70000], 70, 2, 5), (64, 5, [131007, 4], 4096, 4, 1024),
+                                                              (128, 1, [5000, 2600], 2500, 0, 0), (64, 1, [60001], 60000, 1, 1)])
+def test_clusters_into_other_pages(cuda_lib, kind, dim, heads, kv, budget, sinks, recent):
+    w = Pool(kv, heads, dim, seed=budget, kind=kind, spare=len(kv) * -(-budget // 64))
+    check(w, budget, sinks, recent, w.into(-(-budget // 64)))

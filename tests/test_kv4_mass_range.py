@@ -127,3 +127,20 @@ def test_scales_of_every_size_and_sign(cuda_lib, dtype, form, scale, power):
     scale = float(np.float32(scale))
     got = gather(w, form, q, mass, scale, decay=0.5)
     w.check(got, q, 2, scale, 0.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (64, "f32"), (128, "bf16"), (128, "f32")])
+@pytest.mark.parametrize("new,kv", [([140, 60], [3000, 5000]), ([400], [400]), ([49], [9001])])
+@pytest.mark.parametrize("size", [0.0, 1.5, 60.0, 4000.0, 1e6, 1e20])
+def test_many_rows_give_one_vote_each(cuda_lib, dim, dtype, new, kv, size):
+    """Blocks of 128 rows: rows are the product's rows where maxima and sums are found, and its columns where votes are added up. Both
+    have to make the same scores: a difference in the last place of great ones would show as votes lost or won. What is left are
+    the roundings of exponentials and sums."""
+    w = Mass(new, kv, 2, dim, dtype, seed=dim + int(min(size, 1e6))).fill()
+    mass, q = w.start(), w.queries(2, size)
+    got = gather(w, "128 rows", q, mass, decay=0.0).double().cpu().numpy()
+    for b, n in enumerate(new):
+        j = np.arange(kv[b])
+        votes = got[w.table[b][j // 64], :, j % 64].sum(0)
+        assert (np.abs(votes - 2 * n) <= 2 * n * (kv[b] + 2 * n + 32) * 2.0 ** -23).all()
