@@ -16,15 +16,16 @@
 // bytes of a key row (8 with D = 64), so a warp's loads of a tile are contiguous, straight from the cache.
 //
 // Few columns (16 at most): of short sequences, and of many whose scores fit the shared memory of a cluster of up to eight
-// blocks, one kernel does it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the first kernel leaves the scores
-// in the workspace and the second starts behind it; where that would take more than 256 MB, the second makes them again. Bound by issue slots: unpacking takes 80 of some 350 instructions a tile.
-// Measured (20 and 5 heads x 128): one query over 77 tokens 4.8 us, 64 over 87 to 8086 43.7 us (fp32 queries), one over 131007
-// 19.5 us (27.9 where the second kernel reads the keys again).
+// blocks, one kernel does it all: scores once, (M, L) exchanged between the blocks, votes from the kept scores. Else the first
+// kernel leaves the scores in the workspace and the second starts behind it; where that would take more than 256 MB, the second
+// makes them again. Bound by latency (chains of loads and products), at half of the issue slots: a tile takes 445 instructions in
+// the one kernel and 363 and 197 in the two, of which 80 unpack its codes. Measured (20 and 5 heads x 128): one query over 77 tokens
+// 4.9 us, 64 over 87 to 8086 43.9 us (fp32 queries), one over 131007 19.6 us (25.4 where the scores are made again).
 //
 // More columns, up to 96 rows (kv4_mass_tc.cu has the others): blocks of 64 whose fragments the first kernel leaves in the
 // workspace; the second kernel's blocks keep their tiles' codes and go through a share of the columns, and where these are more
-// than one a third adds up the shares. Bound by the products' latency and issue slots (tensor pipe 38% busy): 64 rows of 5 prompts of 1000 to 9000 tokens
-// each 33.7 us.
+// than one a third adds up the shares. Bound by the products' latency and issue slots (tensor pipe 38% busy): 64 rows of 5 prompts of
+// 1000 to 9000 tokens each 29.9 us.
 #include <type_traits>
 
 #include "kv4_mass.cuh"

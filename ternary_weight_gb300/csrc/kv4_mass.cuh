@@ -124,8 +124,9 @@ __device__ __forceinline__ void join_u(float a, float& m, float& l, float m2, fl
 }  // namespace
 
 // Many rows of a unit (that vote x heads that share a key/value head): kv4_mass_tc.cu. Measured, us, 5 prompts of 1000 to 9000
-// tokens, 20 and 5 heads x 128, m16n8k16 and tcgen05: bf16 queries 64 rows 33.7, 50.5; 96 rows 48.5, 51.7; 128 rows 56.4, 52.9;
-// 256 rows 91, 63.8; fp32 queries 64 rows 53.0, 62.0; 68 rows 58.2, 63.1; 96 rows 67.1, 63.2; 256 rows 136, 97.9.
+// tokens, 20 and 5 heads x 128, m16n8k16 and tcgen05: bf16 queries 64 rows 29.9, 49.5; 96 rows 45.4, 50.4; 128 rows 53.3, 51.6;
+// 256 rows 87.3, 61.9; fp32 queries 64 rows 49.0, 61.2; 80 rows 58.7, 62.4; 96 rows 63.2, 62.5; 256 rows 133, 94.4. (Other shapes
+// go by the same rule; it was not measured for them.)
 inline bool mass_on_tc(int64_t rows, bool f32) { return rows > (f32 ? 80 : 96); }
 int64_t kv4_mass_tc_ws_bytes(const Kv4& c, int dim, int share, int64_t rows, bool f32);
 cudaError_t launch_kv4_mass_tc(const Kv4& c, int dim, const Kv4Attn& a, const Kv4Mass& m, int64_t rows, void* ws, cudaStream_t stream);

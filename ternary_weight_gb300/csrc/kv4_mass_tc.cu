@@ -11,10 +11,10 @@
 // thread adds up its token's votes and a pair of rows' constants comes from shared memory. In both the products of one
 // tile (block) run while the last one's scores are worked off; two blocks an SM cover what is left.
 //
-// Bound by issue slots (some 700 instructions for a warp's 64 x 32 scores, 320 of them their arithmetic) and by the latency of a
-// tile, of which a block has up to 16 in turn. Measured (20 and 5 heads x 128): 2048 tokens that all vote 66.2 us (21 GFLOP in the
-// two passes), 4096 180 us, the last 64 of 5 prompts of 1000 to 9000 tokens 60.8 us; on m16n8k16 the first and last took 114.5
-// and 91.
+// Bound by the latency of a tile, of which a block has up to 16 in turn, with 41 to 46% of the issue slots used (some 720 instructions
+// for a warp's 64 x 32 scores, 320 of them their arithmetic). Measured (20 and 5 heads x 128): 2048 tokens that all vote 67.1 us (21
+// GFLOP in the two passes; fp32 queries 98.4), 4096 179 us, the last 64 of 5 prompts of 1000 to 9000 tokens 61.4 us (94.5); on
+// m16n8k16 the first and last took 114.5 and 87.
 #include <type_traits>
 
 #include "kv4_mass.cuh"
