@@ -11,7 +11,8 @@
 // Bound by latency where sequences are few: loads that depend on each other (length, page, mass; kept token, page, data) and
 // the cluster's barriers; by issue slots and the moved bytes where they are many. Measured (5 heads x 128, into other pages):
 // 131007 tokens to 4096 24.3 us (in place 24.9), to 64 23; 16000 to 64 15.3; 48 sequences of 501 to 16001 to 2048 51.4 us (141 MB;
-// in place 56.0), to 64 28.5; 300 to 200 8.7 us. Loops are kept short: unrolled ones cost the small cases half as much again, in instruction fetches.
+// in place 56.0), to 64 28.5; 300 to 200 8.7 us. Loops are kept short: unrolled ones cost the small cases half as much again, in
+// instruction fetches.
 #include "kv4.cuh"
 #include "smem_limit.h"
 
