@@ -22,11 +22,11 @@ def call(lib, rows, q, qs, q_out, qos, k, ks, k_out, kos, q_heads=4, kv_heads=2)
     (3, (AT, 512, 2 * AT, 512, 3 * AT, 256, 4 * AT, 256), -2), (3, (AT, 512, AT, 512, 2 * AT, 256, 2 * AT, 256), -2),
     (9, (AT, 1024, AT, 1024, AT + 1024, 1024, AT + 1024, 1024), -2), (9, (AT, 1536, AT + 1536, 1536, AT + 1024, 1536, AT + 2560, 1536), -2),
     # one behind the other, of unlike strides
-    (3, (AT, 512, 2 * AT, 512, AT + 3072, 256, 2 * AT + 3072, 256), -2),
+    (5, (AT, 512, 2 * AT, 512, AT + 5120, 256, 2 * AT + 5120, 256), -2),
     # moved by 16 bytes, by a row; a row before
     (3, (AT, 512, AT + 16, 512, 3 * AT, 256, 4 * AT, 256), -1), (3, (AT, 512, AT + 1024, 512, 3 * AT, 256, 4 * AT, 256), -1),
-    (3, (AT, 512, AT - 1024, 512, 3 * AT, 256, 4 * AT, 256), -1), (3, (AT, 512, AT - 3072, 512, 3 * AT, 256, 4 * AT, 256), -2),
-    (3, (AT, 512, AT + 3072, 512, 3 * AT, 256, 4 * AT, 256), -2),
+    (3, (AT, 512, AT - 1024, 512, 3 * AT, 256, 4 * AT, 256), -1), (5, (AT, 512, AT - 5120, 512, 3 * AT, 256, 4 * AT, 256), -2),
+    (5, (AT, 512, AT + 5120, 512, 3 * AT, 256, 4 * AT, 256), -2),
     # over the other operand, or its output
     (3, (AT, 512, 2 * AT, 512, 3 * AT, 256, AT, 256), -1), (3, (AT, 512, 3 * AT, 512, 3 * AT, 256, 4 * AT, 256), -1),
     (3, (AT, 512, 2 * AT, 512, 3 * AT, 256, 2 * AT, 256), -1), (3, (AT, 512, 2 * AT, 512, 3 * AT, 256, 2 * AT + 3056, 256), -1),
